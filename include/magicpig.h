@@ -76,6 +76,11 @@ extern "C" {
                                        more, a bucket run past its segment, a list entry past the
                                        capacity) and skipped that access */
 
+#define MP_STATUS_BAD_PAGE 0x20u    /* cache operators: a page number outside the pool was met (a read
+                                       took page 0 in its place, a write was skipped) */
+#define MP_STATUS_BAD_LENGTH 0x40u  /* cache operators: a sequence's rows or length were outside the
+                                       limits of the call and were cut to them */
+
 /* element types */
 #define MP_DTYPE_F32 0
 #define MP_DTYPE_BF16 1
@@ -257,6 +262,137 @@ MP_API int mp_decode_step(const mp_config* cfg, void* tables, const void* keys, 
 MP_API int mp_decode_attention_static(const mp_config* cfg, void* tables, const void* keys,
                                       const void* values, int32_t n, const void* q, float* out,
                                       void* stream);
+
+/* ---- the key/value cache: filling it, attending to all of it, cutting it ----
+ *
+ * The sampled attention above reads a cache that something has to fill, layers that are
+ * attended exactly need an attention over all of it, and a cache that grows past its
+ * budget has to be cut. These calls work on the cache of ONE layer, kept in pages:
+ *   keys, values : [n_pages][kv_heads][page_size][head_dim]   (the pool)
+ *   page_table   : int32 [batch][max_pages], the pool's pages of each sequence in order;
+ *                  NULL: page b is the whole cache of sequence b (max_pages = 1), so that
+ *                  one layer [batch][kv_heads][capacity][head_dim] of the dense layout
+ *                  is a pool of `batch` pages with page_size = capacity.
+ * Slot s of a sequence lies in page page_table[b][s / page_size], row s % page_size.
+ * Entries of the table behind a sequence's last slot are not looked at. Two sequences
+ * may share pages that both only read.
+ *
+ * New tokens are packed: sequence b's are the rows [cu_q[b], cu_q[b+1]) of q, out and the
+ * like, and kv_len[b] counts its slots with these tokens included, so that token i of m
+ * sits in slot kv_len[b] - m + i. A token at a negative slot (m > kv_len[b]) is not in the
+ * cache and sees nothing. Rows outside every sequence are left as they were.
+ * cu_q (int32 [batch + 1], from 0, not decreasing) and kv_len (int32 [batch]) are device
+ * memory, read when the kernels run: a captured call follows their current values.
+ * The host gives limits that size the launch: total_q rows in the packed tensors,
+ * max_q >= every m and max_kv >= every kv_len. What passes a limit is cut to it and
+ * sets MP_STATUS_BAD_LENGTH; a page number outside the pool sets MP_STATUS_BAD_PAGE.
+ * `status` (device uint32, may be NULL) collects these bits; the caller clears it.
+ * Query head j of a sequence reads KV head j / (q_heads / kv_heads); the softmax scale is
+ * 1/sqrt(head_dim). Workspaces belong to the caller, hold nothing between calls and need
+ * no initialisation; calls that may overlap on the device (two streams, two captured
+ * graphs) need a workspace each. */
+typedef struct mp_cache_config {
+  int32_t batch;     /* sequences */
+  int32_t kv_heads;  /* KV heads per sequence */
+  int32_t q_heads;   /* query heads per sequence, a multiple of kv_heads */
+  int32_t head_dim;  /* d: 64 or 128 */
+  int32_t page_size; /* slots per page: with a page table a multiple of 16, without one any number */
+  int32_t n_pages;   /* pages in the pool */
+  int32_t max_pages; /* columns of the page table (1 without one) */
+  int32_t dtype;     /* MP_DTYPE_BF16 or MP_DTYPE_F32: q, k, v, the cache, the norms' weights, out */
+  int32_t reserved[4]; /* must be zero */
+} mp_cache_config;
+
+/* How queries and keys are normalised and rotated by mp_cache_append. */
+typedef struct mp_rotary {
+  int32_t rot_dim;     /* first elements of each head that are rotated: even, 0..head_dim */
+  int32_t interleaved; /* 0: element i turns with i + rot_dim/2 (rot_dim a multiple of 16 in bf16
+                          and of 8 in fp32, else MP_ERR_UNSUPPORTED); 1: element 2i with 2i + 1 */
+  float eps;           /* added to the mean square of the norms, >= 0 */
+  int32_t reserved;    /* must be zero */
+} mp_rotary;
+
+/* Validate a cache configuration. MP_OK or MP_ERR_INVALID_ARG / MP_ERR_UNSUPPORTED. */
+MP_API int mp_cache_config_check(const mp_cache_config* cfg);
+
+/* Normalise and rotate the new tokens' queries and keys, and write keys and values into
+ * the cache. For every head x of q and k:
+ *   y = x / sqrt(mean(x^2) + eps) * w          (w = q_norm or k_norm; NULL: y = x)
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t)   t = positions[row] * inv_freq[i],
+ * in fp32 with the angle reduced exactly to a fraction of a turn, rounded once. Queries go
+ * to q_out, keys to their slots; values are copied to theirs unchanged.
+ *   q, k, v   : device; row r at r * stride elements (strides in elements, multiples of
+ *               16 bytes), heads of a row dense: q [total_q][q_heads][d], k and v
+ *               [total_q][kv_heads][d]. Slices of one fused projection fit.
+ *   q_norm, k_norm : device [d] in dtype, or NULL for no norm of that tensor.
+ *   inv_freq  : device double [rot_dim/2], radians per position (may be NULL when rot_dim = 0).
+ *   positions : device int32 [total_q], where each token stands in its text (its slot may
+ *               be an earlier one once slots were evicted); NULL: its slot.
+ *   q_out     : device [total_q][q_heads][d]; overlaps none of the inputs.
+ * A token whose slot is negative, behind max_pages * page_size or in a bad page writes no
+ * key and no value (its q_out row is written). Two tokens must not share a slot. */
+MP_API int mp_cache_append(const mp_cache_config* cfg, const mp_rotary* rotary, const void* q, int64_t q_stride,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const void* q_norm, const void* k_norm, const double* inv_freq,
+                           const int32_t* positions, const int32_t* cu_q, const int32_t* kv_len,
+                           int32_t total_q, void* keys, void* values, const int32_t* page_table, void* q_out,
+                           uint32_t* status, void* stream);
+
+/* Bytes of workspace of mp_chunk_attention for these limits (0 is possible). */
+MP_API int mp_chunk_workspace_bytes(const mp_cache_config* cfg, int32_t total_q, int32_t max_q, int32_t max_kv,
+                                    uint64_t* bytes);
+
+/* Exact attention of the new tokens over their sequences' slots, each token seeing the
+ * slots up to its own (a prompt's chunk, a few draft tokens, or a single token):
+ *   out = softmax(q k / sqrt(d)) v     lse = log sum exp(q k / sqrt(d))
+ *   q    : device [total_q][q_heads][d], rotated (mp_cache_append's q_out).
+ *   out  : device [total_q][q_heads][d] in dtype.
+ *   lse  : device float [total_q][q_heads], or NULL.
+ * A token that sees nothing gets out = 0 and lse = -infinity. Slots at and behind kv_len
+ * may hold anything (NaN included); the slots below it are expected to be finite: an
+ * infinity or NaN there may reach tokens of the chunk that stand before it.
+ * bf16: logits and sums are fp32, the softmax weights enter the second product as bf16. */
+MP_API int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t* cu_q, const int32_t* kv_len,
+                              int32_t total_q, int32_t max_q, int32_t max_kv, const void* keys, const void* values,
+                              const int32_t* page_table, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* Add the attention that the new tokens paid to every slot:
+ *   scores[b][h][s] += sum over the tokens i that see s and the query heads j of KV head h
+ *                      of exp(q_ij k_hs / sqrt(d) - lse[i][j])
+ *   q, lse : as mp_chunk_attention took and gave them (the same keys in the cache).
+ *   scores : device float [batch][kv_heads][max_pages * page_size]; slots [0, kv_len) are
+ *            updated. Zero it before the first call (and for slots that are used again).
+ * The order of the additions is fixed: equal inputs give equal bits. */
+MP_API int mp_cache_weights(const mp_cache_config* cfg, const void* q, const float* lse, const int32_t* cu_q,
+                            const int32_t* kv_len, int32_t total_q, int32_t max_q, int32_t max_kv,
+                            const void* keys, const int32_t* page_table, float* scores, uint32_t* status,
+                            void* stream);
+
+/* Bytes of workspace of mp_cache_evict for these limits. */
+MP_API int mp_evict_workspace_bytes(const mp_cache_config* cfg, int32_t max_kv, int32_t budget, uint64_t* bytes);
+
+/* Cut every sequence to at most `budget` slots. Per (sequence, KV head) the first n_sink
+ * and the last `window` slots stay, and of those between them the ones with the highest
+ * scores (equal scores: the lower slot; NaN counts as the lowest) until `budget` slots are
+ * kept; a sequence of at most `budget` slots stays whole. The kept slots move, in their
+ * order, to the slots from 0 on of another cache:
+ *   dst_cfg : the destination's shape; batch, heads, head_dim and dtype as in cfg.
+ *   dst_keys, dst_values, dst_page_table : the destination: pages that hold none of the
+ *             source's slots (another pool, or free pages of the same one).
+ *   scores  : device float [batch][kv_heads][max_pages * page_size].
+ *   dst_scores : device float [batch][kv_heads][dst max_pages * page_size], or NULL: the kept
+ *             slots' scores.
+ *   dst_len : device int32 [batch]: min(kv_len, budget).
+ *   kept    : device int32 [batch][kv_heads][budget], or NULL: the kept slots, ascending;
+ *             entries from dst_len on are left as they were.
+ * 1 <= budget <= dst max_pages * page_size (else MP_ERR_CAPACITY), n_sink + window <= budget.
+ * What lies behind the new lengths in the destination is left as it was. */
+MP_API int mp_cache_evict(const mp_cache_config* cfg, const mp_cache_config* dst_cfg, const void* keys,
+                          const void* values, const int32_t* page_table, const int32_t* kv_len, int32_t max_kv,
+                          const float* scores, int32_t n_sink, int32_t window, int32_t budget, void* dst_keys,
+                          void* dst_values, const int32_t* dst_page_table, float* dst_scores, int32_t* dst_len,
+                          int32_t* kept, void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
 
 /* Copy the device status word to *status (synchronises `stream`). */
 MP_API int mp_get_status(const void* tables, uint32_t* status, void* stream);

@@ -31,6 +31,8 @@ MP_STATUS_WAIT_TIMEOUT = 0x2
 MP_STATUS_APPEND_GAP = 0x4
 MP_STATUS_NOT_BUILT = 0x8
 MP_STATUS_BAD_INDEX = 0x10
+MP_STATUS_BAD_PAGE = 0x20
+MP_STATUS_BAD_LENGTH = 0x40
 
 MP_DTYPE_F32 = 0
 MP_DTYPE_BF16 = 1
@@ -67,6 +69,17 @@ class mp_decode_layout(ctypes.Structure):
         (n, ctypes.c_int32) for n in ("splits_max", "reserved")]
 
 
+class mp_cache_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "kv_heads", "q_heads", "head_dim", "page_size", "n_pages", "max_pages", "dtype")] + [
+        ("reserved", ctypes.c_int32 * 4)]
+
+
+class mp_rotary(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
 class mp_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("total_ms", ctypes.c_double)]
@@ -74,7 +87,11 @@ class mp_kernel_time(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
+_Z = ctypes.c_size_t
+_U64 = ctypes.POINTER(ctypes.c_uint64)
 _CFG = ctypes.POINTER(mp_config)
+_CCFG = ctypes.POINTER(mp_cache_config)
 _SIGS = {
     "mp_abi_version": (ctypes.c_int, []),
     "mp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -86,6 +103,15 @@ _SIGS = {
     "mp_decode_attention": (ctypes.c_int, [_CFG, _P, _P, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]),
     "mp_decode_step": (ctypes.c_int, [_CFG, _P, _P, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]),
     "mp_decode_attention_static": (ctypes.c_int, [_CFG, _P, _P, _P, _I, _P, _P, _P]),
+    "mp_cache_config_check": (ctypes.c_int, [_CCFG]),
+    "mp_cache_append": (ctypes.c_int, [_CCFG, ctypes.POINTER(mp_rotary), _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _P, _P,
+                                       _I, _P, _P, _P, _P, _P, _P]),
+    "mp_chunk_workspace_bytes": (ctypes.c_int, [_CCFG, _I, _I, _I, _U64]),
+    "mp_chunk_attention": (ctypes.c_int, [_CCFG, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _Z, _P, _P]),
+    "mp_cache_weights": (ctypes.c_int, [_CCFG, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "mp_evict_workspace_bytes": (ctypes.c_int, [_CCFG, _I, _I, _U64]),
+    "mp_cache_evict": (ctypes.c_int, [_CCFG, _CCFG, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _Z,
+                                      _P, _P]),
     "mp_get_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
     "mp_profile_enable": (ctypes.c_int, [ctypes.c_int]),
     "mp_profile_read": (ctypes.c_int, [ctypes.POINTER(mp_kernel_time), ctypes.c_int32,
@@ -205,6 +231,159 @@ def mp_decode_attention_static(cfg: mp_config, tables, keys, values, n: int, q, 
     """mp_decode_attention with the library's built-in scratch array (no caller scratch)."""
     return _check("mp_decode_attention_static", _lib.mp_decode_attention_static(
         ctypes.byref(cfg), _ptr(tables), _ptr(keys), _ptr(values), n, _ptr(q), _ptr(out), _stream(stream)))
+
+
+# ---- the key/value cache ----
+
+def make_cache_config(*, batch: int, kv_heads: int, q_heads: int, head_dim: int, page_size: int, n_pages: int,
+                      max_pages: int = 1, dtype: Union[int, str] = "bf16") -> mp_cache_config:
+    """A cache of one layer. A dense cache [batch][kv_heads][capacity][head_dim] has
+    page_size = capacity, n_pages = batch, max_pages = 1 and no page table."""
+    if isinstance(dtype, str):
+        dtype = {"bf16": MP_DTYPE_BF16, "f32": MP_DTYPE_F32}[dtype]
+    return mp_cache_config(batch, kv_heads, q_heads, head_dim, page_size, n_pages, max_pages, int(dtype))
+
+
+def make_rotary(*, rot_dim: int, interleaved: bool = False, eps: float = 1e-6) -> mp_rotary:
+    return mp_rotary(rot_dim, int(bool(interleaved)), eps, 0)
+
+
+class _Args:
+    """Device addresses of one call's tensors, each checked for its device, type, layout
+    and size: the kernels use the addresses as the configuration says."""
+
+    def __init__(self, first):
+        import torch
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError("tensor arguments must be CUDA tensors (device memory)")
+        self.device = first.device
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors are on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
+        self.i32, self.f32, self.f64, self.u8 = torch.int32, torch.float32, torch.float64, torch.uint8
+        self.types = (torch.float32, torch.bfloat16)
+        self.current_stream = torch.cuda.current_stream
+
+    def __call__(self, name, x, dtype, numel, none=False):
+        if x is None:
+            if none:
+                return None
+            raise ValueError(f"{name} is needed")
+        if x.device != self.device:
+            raise ValueError(f"{name} is on {x.device}, not on {self.device}")
+        if x.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous (dense row-major layout)")
+        if x.numel() < numel:
+            raise ValueError(f"{name} has {x.numel()} elements, the call uses {numel}")
+        return x.data_ptr()
+
+    def rows(self, name, x, dtype, rows, width):
+        """(address, row stride) of a [rows, heads, head_dim] tensor whose rows may lie apart."""
+        if x.device != self.device or x.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype} on {self.device}")
+        if x.dim() < 2 or x.shape[0] != rows or x.numel() != rows * width:
+            raise ValueError(f"{name} must have {rows} rows of {width} elements, got {tuple(x.shape)}")
+        stride = width if rows <= 1 else x.stride(0)  # one row has no stride of its own
+        inner = 1
+        for size, st in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+            if size != 1 and st != inner:
+                raise ValueError(f"{name}: the heads of a row must be dense")
+            inner *= size
+        return x.data_ptr(), stride
+
+    def stream(self, stream):
+        return self.current_stream().cuda_stream if stream is None else _stream(stream)
+
+
+def _pool_size(cfg: mp_cache_config) -> int:
+    return cfg.n_pages * cfg.kv_heads * cfg.page_size * cfg.head_dim
+
+
+def _dtype_of(a: _Args, cfg: mp_cache_config):
+    if cfg.dtype not in (MP_DTYPE_F32, MP_DTYPE_BF16):
+        raise MagicPigError("mp_cache_config_check", MP_ERR_INVALID_ARG)
+    return a.types[cfg.dtype]
+
+
+def mp_cache_config_check(cfg: mp_cache_config) -> int:
+    return _lib.mp_cache_config_check(ctypes.byref(cfg))
+
+
+def mp_cache_append(cfg: mp_cache_config, rotary: mp_rotary, q, k, v, q_norm, k_norm, inv_freq, positions, cu_q, kv_len,
+                    keys, values, page_table, q_out, status=None, stream=None) -> int:
+    """Norms, rotation and cache write of the new tokens. q, k, v: [total_q, heads, head_dim], rows may lie apart."""
+    a = _Args(q)
+    dt = _dtype_of(a, cfg)
+    rows, d = q.shape[0], cfg.head_dim
+    qp, qs = a.rows("q", q, dt, rows, cfg.q_heads * d)
+    kp, ks = a.rows("k", k, dt, rows, cfg.kv_heads * d)
+    vp, vs = a.rows("v", v, dt, rows, cfg.kv_heads * d)
+    return _check("mp_cache_append", _lib.mp_cache_append(
+        cfg, rotary, qp, qs, kp, ks, vp, vs, a("q_norm", q_norm, dt, d, True), a("k_norm", k_norm, dt, d, True),
+        a("inv_freq", inv_freq, a.f64, rotary.rot_dim // 2, rotary.rot_dim == 0),
+        a("positions", positions, a.i32, rows, True), a("cu_q", cu_q, a.i32, cfg.batch + 1),
+        a("kv_len", kv_len, a.i32, cfg.batch), rows, a("keys", keys, dt, _pool_size(cfg)),
+        a("values", values, dt, _pool_size(cfg)), a("page_table", page_table, a.i32, cfg.batch * cfg.max_pages, True),
+        a("q_out", q_out, dt, rows * cfg.q_heads * d), a("status", status, a.i32, 1, True), a.stream(stream)))
+
+
+def mp_chunk_workspace_bytes(cfg: mp_cache_config, total_q: int, max_q: int, max_kv: int) -> int:
+    n = ctypes.c_uint64(0)
+    _check("mp_chunk_workspace_bytes", _lib.mp_chunk_workspace_bytes(cfg, total_q, max_q, max_kv, ctypes.byref(n)))
+    return n.value
+
+
+def mp_chunk_attention(cfg: mp_cache_config, q, cu_q, kv_len, max_q: int, max_kv: int, keys, values, page_table, out,
+                       lse=None, workspace=None, status=None, stream=None) -> int:
+    """Exact attention of the new tokens q [total_q, q_heads, head_dim] over their sequences' slots."""
+    a = _Args(q)
+    dt = _dtype_of(a, cfg)
+    rows, width, pool = q.shape[0], cfg.q_heads * cfg.head_dim, _pool_size(cfg)
+    return _check("mp_chunk_attention", _lib.mp_chunk_attention(
+        cfg, a("q", q, dt, rows * width), a("cu_q", cu_q, a.i32, cfg.batch + 1), a("kv_len", kv_len, a.i32, cfg.batch),
+        rows, max_q, max_kv, a("keys", keys, dt, pool), a("values", values, dt, pool),
+        a("page_table", page_table, a.i32, cfg.batch * cfg.max_pages, True), a("out", out, dt, rows * width),
+        a("lse", lse, a.f32, rows * cfg.q_heads, True), a("workspace", workspace, a.u8, 0, True),
+        0 if workspace is None else workspace.numel(), a("status", status, a.i32, 1, True), a.stream(stream)))
+
+
+def mp_cache_weights(cfg: mp_cache_config, q, lse, cu_q, kv_len, max_q: int, max_kv: int, keys, page_table, scores,
+                     status=None, stream=None) -> int:
+    """Add the attention that the new tokens paid to every slot to scores [batch, kv_heads, max_pages * page_size]."""
+    a = _Args(q)
+    dt = _dtype_of(a, cfg)
+    rows = q.shape[0]
+    return _check("mp_cache_weights", _lib.mp_cache_weights(
+        cfg, a("q", q, dt, rows * cfg.q_heads * cfg.head_dim), a("lse", lse, a.f32, rows * cfg.q_heads),
+        a("cu_q", cu_q, a.i32, cfg.batch + 1), a("kv_len", kv_len, a.i32, cfg.batch), rows, max_q, max_kv,
+        a("keys", keys, dt, _pool_size(cfg)), a("page_table", page_table, a.i32, cfg.batch * cfg.max_pages, True),
+        a("scores", scores, a.f32, cfg.batch * cfg.kv_heads * cfg.max_pages * cfg.page_size),
+        a("status", status, a.i32, 1, True), a.stream(stream)))
+
+
+def mp_evict_workspace_bytes(cfg: mp_cache_config, max_kv: int, budget: int) -> int:
+    n = ctypes.c_uint64(0)
+    _check("mp_evict_workspace_bytes", _lib.mp_evict_workspace_bytes(cfg, max_kv, budget, ctypes.byref(n)))
+    return n.value
+
+
+def mp_cache_evict(cfg: mp_cache_config, dst_cfg: mp_cache_config, keys, values, page_table, kv_len, max_kv: int, scores,
+                   n_sink: int, window: int, budget: int, dst_keys, dst_values, dst_page_table, dst_scores, dst_len,
+                   kept, workspace, status=None, stream=None) -> int:
+    """Keep sinks, window and the highest-scored slots up to the budget; the kept rows move to the destination."""
+    a = _Args(keys)
+    dt = _dtype_of(a, cfg)
+    pool, dpool, units = _pool_size(cfg), _pool_size(dst_cfg), cfg.batch * cfg.kv_heads
+    return _check("mp_cache_evict", _lib.mp_cache_evict(
+        cfg, dst_cfg, a("keys", keys, dt, pool), a("values", values, dt, pool),
+        a("page_table", page_table, a.i32, cfg.batch * cfg.max_pages, True), a("kv_len", kv_len, a.i32, cfg.batch), max_kv,
+        a("scores", scores, a.f32, units * cfg.max_pages * cfg.page_size), n_sink, window, budget,
+        a("dst_keys", dst_keys, dt, dpool), a("dst_values", dst_values, dt, dpool),
+        a("dst_page_table", dst_page_table, a.i32, cfg.batch * dst_cfg.max_pages, True),
+        a("dst_scores", dst_scores, a.f32, units * dst_cfg.max_pages * dst_cfg.page_size, True),
+        a("dst_len", dst_len, a.i32, cfg.batch), a("kept", kept, a.i32, units * max(0, budget), True),
+        a("workspace", workspace, a.u8, 0), workspace.numel(), a("status", status, a.i32, 1, True), a.stream(stream)))
 
 
 def mp_get_status(tables, stream=None) -> int:

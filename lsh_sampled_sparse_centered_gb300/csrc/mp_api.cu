@@ -11,7 +11,7 @@
 
 namespace mp {
 
-static uint64_t align256(uint64_t x) { return (x + 255u) & ~uint64_t(255u); }
+uint64_t align256(uint64_t x) { return (x + 255u) & ~uint64_t(255u); }
 
 // AUTO: the mode that moves fewer bytes per query head and decode step.
 //   CSR : L buckets of ~m/2^K ids (2 B) + per 32K-token segment 4 B of offsets, per table
@@ -197,15 +197,15 @@ static DecodePtrs decode_ptrs(const Geometry& g, void* base) {
   return p;
 }
 
-// MP_FAULT_INJECT=build|append|decode|all makes the named calls fail before any
+// MP_FAULT_INJECT=build|append|decode|chunk|weights|evict|all makes the named calls fail before any
 // launch (host-side fault injection for error-path tests).
-static bool injected(const char* what) {
+bool injected(const char* what) {
   const char* e = std::getenv("MP_FAULT_INJECT");
   if (!e || !*e) return false;
   return std::strcmp(e, "all") == 0 || std::strcmp(e, what) == 0;
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int device_sm_count() {
   // per-device cache; callers on several host threads may fill it concurrently
@@ -261,15 +261,12 @@ static int choose_splits(const Geometry& g, int n) {
 }
 
 // ---- optional per-launch event timing ----
-enum KernelId {
-  K_PREPARE_W, K_CENTER, K_HASH_KEYS_SIMT, K_HASH_KEYS_TC, K_CSR_BUILD, K_HASH_APPEND, K_MARK_APPENDED,
-  K_HASH_QUERY, K_MATCH_CSR, K_ATTEND, K_PLANES_BUILD, K_PLANES_APPEND, K_SCAN, K_COMPACT, K_HASH_STEP, K_LOGU_LUT,
-  K_COUNT
-};
 static const char* kKernelNames[K_COUNT] = {"prepare_w", "center", "hash_keys_simt", "hash_keys_tc",
                                             "csr_build", "hash_append", "mark_appended", "hash_query",
                                             "match_csr", "attend", "planes_build", "planes_append",
-                                            "scan", "compact", "hash_step", "logu_lut"};
+                                            "scan", "compact", "hash_step", "logu_lut", "cache_append",
+                                            "chunk_attend", "chunk_join", "cache_weights", "evict_select",
+                                            "evict_gather"};
 struct ProfRec {
   int id;
   cudaEvent_t a, b;
@@ -290,28 +287,19 @@ static cudaEvent_t pool_event() {
   return e;
 }
 
-// Brackets one launcher call with events when profiling is on.
-class ProfScope {
- public:
-  ProfScope(cudaStream_t st, int id) : st_(st), id_(id) {
-    std::lock_guard<std::mutex> g(g_prof_mu);
-    if (!g_prof_on) return;
-    a_ = pool_event();
-    b_ = pool_event();
-    if (a_ && b_) cudaEventRecord(a_, st_);
-  }
-  ~ProfScope() {
-    std::lock_guard<std::mutex> g(g_prof_mu);
-    if (!a_ || !b_) return;
-    cudaEventRecord(b_, st_);
-    g_prof.push_back({id_, a_, b_});
-  }
-
- private:
-  cudaStream_t st_;
-  int id_;
-  cudaEvent_t a_ = nullptr, b_ = nullptr;
-};
+ProfScope::ProfScope(cudaStream_t st, int id) : st_(st), id_(id) {
+  std::lock_guard<std::mutex> g(g_prof_mu);
+  if (!g_prof_on) return;
+  a_ = pool_event();
+  b_ = pool_event();
+  if (a_ && b_) cudaEventRecord(a_, st_);
+}
+ProfScope::~ProfScope() {
+  std::lock_guard<std::mutex> g(g_prof_mu);
+  if (!a_ || !b_) return;
+  cudaEventRecord(b_, st_);
+  g_prof.push_back({id_, a_, b_});
+}
 
 }  // namespace mp
 

@@ -1,0 +1,141 @@
+// What the cache operators' kernels share: the sequences of a packed batch, cut to the
+// call's limits, and the address of a cache slot.
+#pragma once
+
+#include "mp_internal.h"
+
+namespace mp {
+
+// One layer's paged cache and the packed batch of a call (host-checked limits).
+struct CacheArgs {
+  int batch, kvh, group, d;      // group = q_heads / kv_heads
+  int page_size, n_pages, cols;  // cols: columns of the page table
+  const int32_t* table;          // nullptr: page b is sequence b's cache
+  const int32_t* cu_q;           // nullptr: no packed rows (eviction)
+  const int32_t* kv_len;
+  int total_q, max_q, max_kv;
+  uint32_t* status;              // may be nullptr
+};
+
+struct ChunkArgs {
+  CacheArgs c;
+  const void *q, *keys, *values;
+  void* out;
+  float* lse;   // may be nullptr
+  int splits;   // slices of the keys per row tile
+  float* part;  // [splits][total_q][q_heads][d]: unnormalised partial sums (splits > 1)
+  float* ml;    // [splits][total_q][q_heads][2]: their maximum (log2 units) and sum
+};
+
+struct WeightsArgs {
+  CacheArgs c;
+  const void *q, *keys;
+  const float* lse;
+  float* scores;
+};
+
+struct AppendArgs {
+  CacheArgs c;
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const void *q_norm, *k_norm;
+  const double* inv_freq;
+  const int32_t* positions;
+  int rot, interleaved;
+  float eps;
+  void *keys, *values, *q_out;
+};
+
+struct EvictArgs {
+  CacheArgs c;
+  const void *keys, *values;
+  const float* scores;
+  int n_sink, window, budget;
+  void *dst_keys, *dst_values;
+  const int32_t* dst_table;
+  int dst_page_size, dst_n_pages, dst_cols;
+  float* dst_scores;
+  int32_t* dst_len;
+  int32_t* kept;  // [batch][kv_heads][budget]
+};
+
+// Slices of the keys that a chunk attention of these limits runs with, and the rows of
+// a tile (fixed by the limits alone, so that the workspace can be sized before the call).
+int chunk_splits(const mp_cache_config* c, int total_q, int max_q, int max_kv);
+
+cudaError_t launch_cache_append(const AppendArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_chunk_attend(const ChunkArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
+cudaError_t launch_evict_gather(const EvictArgs& a, int dtype, cudaStream_t st);
+
+#ifdef __CUDACC__
+// The index arithmetic below also compiles for the host, where a test walks it over bad
+// lengths and pages.
+__host__ __device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
+  if (!status) return;
+#ifdef __CUDA_ARCH__
+  atomicOr(status, bit);
+#else
+  *status |= bit;
+#endif
+}
+
+// Sequence b's packed rows [row0, row0 + m) and its n slots, cut to the call's limits.
+struct Seq {
+  int row0, m, n;
+};
+__host__ __device__ __forceinline__ Seq seq_of(const CacheArgs& c, int b) {
+  Seq s;
+  const int64_t slots = int64_t(c.cols) * c.page_size;
+  const int n = c.kv_len[b];
+  s.n = max(0, min(n, int(min(int64_t(c.max_kv), slots))));
+  bool cut = s.n != n;
+  if (c.cu_q) {
+    const int r0 = c.cu_q[b], r1 = c.cu_q[b + 1];
+    s.row0 = max(0, min(r0, c.total_q));
+    const int e = max(s.row0, min(r1, c.total_q));
+    s.m = min(e - s.row0, c.max_q);
+    cut = cut || s.row0 != r0 || s.row0 + s.m != r1;
+  } else {
+    s.row0 = 0;
+    s.m = 0;
+  }
+  if (cut) flag(c.status, MP_STATUS_BAD_LENGTH);
+  return s;
+}
+
+// Sequence that packed row r belongs to, or -1: the last b with cu_q[b] <= r, if r is
+// one of its rows. A table that decreases somewhere gives some sequence or none, never
+// an index outside it.
+__host__ __device__ __forceinline__ int seq_at(const CacheArgs& c, int r) {
+  int lo = 0, hi = c.batch;  // cu_q[lo] <= r is kept where it holds for 0
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (c.cu_q[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  return (c.cu_q[lo] <= r && r < c.cu_q[lo + 1]) ? lo : -1;
+}
+
+// Pool page of slot s (0 <= s < cols * page_size), or -1 when the table names none.
+__host__ __device__ __forceinline__ int page_at(const int32_t* table, int cols, int n_pages, int b, int col, uint32_t* status) {
+  if (!table) return b;
+  const int p = table[int64_t(b) * cols + col];
+  if (p < 0 || p >= n_pages) {
+    flag(status, MP_STATUS_BAD_PAGE);
+    return -1;
+  }
+  return p;
+}
+
+// Element offset of slot s of KV head h for reading: a bad page reads page 0 instead.
+__host__ __device__ __forceinline__ int64_t slot_read(const CacheArgs& c, int b, int h, int s) {
+  const int col = s / c.page_size, o = s - col * c.page_size;
+  const int p = max(0, page_at(c.table, c.cols, c.n_pages, b, col, c.status));
+  return ((int64_t(p) * c.kvh + h) * c.page_size + o) * c.d;
+}
+#endif
+
+}  // namespace mp

@@ -151,6 +151,31 @@ cudaError_t launch_attend(const Geometry& g, int n, int splits, const TablesPtrs
 
 int device_sm_count();
 
+// ---- host helpers shared by the entry points (mp_api.cu) ----
+uint64_t align256(uint64_t x);
+bool aligned16(const void* p);
+// MP_FAULT_INJECT names the calls that fail before any launch
+bool injected(const char* what);
+
+// optional per-launch event timing: names in kKernelNames
+enum KernelId {
+  K_PREPARE_W, K_CENTER, K_HASH_KEYS_SIMT, K_HASH_KEYS_TC, K_CSR_BUILD, K_HASH_APPEND, K_MARK_APPENDED,
+  K_HASH_QUERY, K_MATCH_CSR, K_ATTEND, K_PLANES_BUILD, K_PLANES_APPEND, K_SCAN, K_COMPACT, K_HASH_STEP, K_LOGU_LUT,
+  K_CACHE_APPEND, K_CHUNK_ATTEND, K_CHUNK_JOIN, K_CACHE_WEIGHTS, K_EVICT_SELECT, K_EVICT_GATHER,
+  K_COUNT
+};
+// Brackets one launcher call with events when profiling is on.
+class ProfScope {
+ public:
+  ProfScope(cudaStream_t st, int id);
+  ~ProfScope();
+
+ private:
+  cudaStream_t st_;
+  int id_;
+  cudaEvent_t a_ = nullptr, b_ = nullptr;
+};
+
 // MP_CHECK=1 builds the bounds-checking library: kernels test every index that comes
 // from data (codes, bucket offsets, list entries) against its buffer before using it,
 // record a failure in the status word (MP_STATUS_BAD_INDEX) and skip that access. In
