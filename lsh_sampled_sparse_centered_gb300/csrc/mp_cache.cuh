@@ -65,6 +65,7 @@ int chunk_splits(const mp_cache_config* c, int total_q, int max_q, int max_kv);
 
 cudaError_t launch_cache_append(const AppendArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_attend(const ChunkArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_chunk_tc(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);

@@ -314,19 +314,19 @@ cudaError_t weights_simt(const WeightsArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// As many slices as fill the SMs about twice, each of at least 256 slots.
+// Slices of the keys: as many as fill the SMs about twice, each of at least 256 slots. A
+// tile has 256 rows on the tensor cores (bf16) and 64 on the CUDA cores (fp32).
 int chunk_splits(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
   (void)total_q;
-  const int64_t group = c->q_heads / c->kv_heads;
-  const int64_t ctas = (max_q * group + kBM - 1) / kBM * c->kv_heads * c->batch;
+  const int64_t group = c->q_heads / c->kv_heads, tile = c->dtype == MP_DTYPE_BF16 ? 256 : kBM;
+  const int64_t ctas = (max_q * group + tile - 1) / tile * c->kv_heads * c->batch;
   const int64_t fill = 2 * 152 / ctas, most = (int64_t(max_kv) + 255) / 256;
   const int64_t s = fill < most ? fill : most;
   return int(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
 
 cudaError_t launch_chunk_attend(const ChunkArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == MP_DTYPE_BF16)
-    return a.c.d == 128 ? chunk_simt<__nv_bfloat16, 128>(a, st) : chunk_simt<__nv_bfloat16, 64>(a, st);
+  if (dtype == MP_DTYPE_BF16) return launch_chunk_tc(a, st);
   return a.c.d == 128 ? chunk_simt<float, 128>(a, st) : chunk_simt<float, 64>(a, st);
 }
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st) {
