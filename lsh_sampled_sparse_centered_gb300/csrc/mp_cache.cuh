@@ -63,11 +63,21 @@ struct EvictArgs {
 // a tile (fixed by the limits alone, so that the workspace can be sized before the call).
 int chunk_splits(const mp_cache_config* c, int total_q, int max_q, int max_kv);
 
+// Rows of a TMA box of K or V: the most that divide a 128-key tile and never leave a page
+// (16 at least: page sizes are multiples of 16). Without a table a box may run past the
+// sequence's end into other rows of the pool, which are masked or zeroed.
+inline int box_rows(const int32_t* table, int page_size) {
+  int b = 128;
+  while (table && page_size % b) b >>= 1;
+  return b;
+}
+
 cudaError_t launch_cache_append(const AppendArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_attend(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_weights_bf16(const WeightsArgs& a, cudaStream_t st);
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_evict_gather(const EvictArgs& a, int dtype, cudaStream_t st);
 

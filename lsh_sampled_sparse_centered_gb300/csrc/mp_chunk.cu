@@ -334,8 +334,7 @@ cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st) {
   return a.c.d == 128 ? join<float, 128>(a, st) : join<float, 64>(a, st);
 }
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == MP_DTYPE_BF16)
-    return a.c.d == 128 ? weights_simt<__nv_bfloat16, 128>(a, st) : weights_simt<__nv_bfloat16, 64>(a, st);
+  if (dtype == MP_DTYPE_BF16) return launch_weights_bf16(a, st);
   return a.c.d == 128 ? weights_simt<float, 128>(a, st) : weights_simt<float, 64>(a, st);
 }
 

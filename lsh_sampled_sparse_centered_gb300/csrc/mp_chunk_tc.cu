@@ -71,24 +71,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // One piece of work: rows [r0, r0 + 256) of KV head h of sequence b against the slots
 // [k0, k1).
 struct Item {
@@ -417,17 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && S.abort) flag(c.status, MP_STATUS_WAIT_TIMEOUT);
 }
 
-int box_rows(const CacheArgs& c) {
-  if (!c.table) return kKeys;
-  int b = kKeys;
-  while (c.page_size % b) b >>= 1;  // 16 at least: page sizes are multiples of 16
-  return b;
-}
-
 template <int D>
 cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
   CUtensorMap mk, mv;
-  const int box = box_rows(a.c);
+  const int box = box_rows(a.c.table, a.c.page_size);
   const uint64_t rows = uint64_t(a.c.n_pages) * a.c.kvh * a.c.page_size;
   if (!make_map(&mk, a.keys, D, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&mv, a.values, D, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))

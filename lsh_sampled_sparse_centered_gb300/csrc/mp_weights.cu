@@ -1,0 +1,381 @@
+// The attention that a chunk's tokens paid to every cached key, bf16.
+//
+// A key's weight is the sum over query rows of 2^(x - z), x = q k log2(e) / sqrt(d) and z
+// the row's log-sum-exp in log2. Nothing but K, Q and z is read; each key's sum has one
+// owner, so the order of its additions is fixed and no atomics are needed.
+//
+// Long chunks: k_weights_tc, keys as the M dimension of tcgen05 products (128 keys of a
+// CTA against 128 query rows at a time), so that a thread owns a key and sums along its
+// own accumulator row. The exponentials (128 x 128 a step) cost about as much as the
+// product; the accumulator is double buffered so that both run at once, and two CTAs
+// share an SM. Few rows: k_weights_step, one pass over K from global memory straight
+// into the fragments of warp-level products, bound by that read.
+#include <cudaTypedefs.h>
+
+#include "mp_cache.cuh"
+#include "mp_tc.cuh"
+
+namespace mp {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kKeys = 128, kCols = 128;  // keys of a CTA, query rows of a step
+constexpr int kLseSlots = 4;
+
+template <int D>
+struct WSmem {
+  static constexpr int kSub = D / 64;
+  __nv_bfloat16 k[kSub][kKeys * 64];
+  __nv_bfloat16 q[2][kSub][kCols * 64];
+  float nz[kLseSlots][kCols];  // -z of the step's rows
+  uint64_t k_full, q_full[2], q_empty[2], s_full[2], s_empty[2], z_full[kLseSlots], z_empty[kLseSlots];
+  uint32_t tmem_base;
+  uint32_t abort;
+};
+
+// Query rows in blocks of at most 128: whole tokens of `group` rows, or, with more than
+// 128 heads in a group, runs of 128 heads of one token.
+struct Blocks {
+  int group, heads, per, runs;  // rows of a token in a block, tokens of a block, blocks of a token
+  int n;
+};
+__host__ __device__ __forceinline__ Blocks blocks_of(int group, int m) {
+  Blocks b;
+  b.group = group;
+  b.heads = group < kCols ? group : kCols;
+  b.per = kCols / b.heads;
+  b.runs = (group + kCols - 1) / kCols;
+  b.n = group <= kCols ? (m + b.per - 1) / b.per : m * b.runs;
+  return b;
+}
+struct Block {
+  int t0, h0, cols;
+};
+__device__ __forceinline__ Block block_at(const Blocks& b, int i, int m) {
+  Block x;
+  if (b.runs == 1) {
+    x.t0 = i * b.per;
+    x.h0 = 0;
+    x.cols = min(b.per, m - x.t0) * b.group;
+  } else {
+    x.t0 = i / b.runs;
+    x.h0 = (i - x.t0 * b.runs) * kCols;
+    x.cols = min(kCols, b.group - x.h0);
+  }
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(192, 2)
+    k_weights_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, const WeightsArgs a,
+                 const int box) {
+  extern __shared__ __align__(1024) unsigned char smraw[];
+  const uint32_t base = saddr(smraw);
+  WSmem<D>& S = *reinterpret_cast<WSmem<D>*>(smraw + ((1024 - (base & 1023)) & 1023));
+  constexpr int kSub = WSmem<D>::kSub;
+  const CacheArgs& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.z, h = blockIdx.y, n0 = blockIdx.x * kKeys;
+  const Seq s = seq_of(c, b);
+  if (n0 >= s.n || s.m == 0) return;
+  volatile uint32_t* abort = &S.abort;
+  const int first = s.n - s.m, qh = c.kvh * c.group;
+  const Blocks bl = blocks_of(c.group, s.m);
+  // tokens before n0 - first see none of these keys
+  const int t_start = max(0, n0 - first);
+  const int i0 = bl.runs == 1 ? t_start / bl.per : t_start * bl.runs;
+  const int steps = bl.n - i0;
+
+  // rows of a block that no load fills stay zero
+  for (int i = threadIdx.x; i < int(sizeof(S.q) / 16); i += 192)
+    reinterpret_cast<uint4*>(&S.q[0][0][0])[i] = make_uint4(0, 0, 0, 0);
+  fence_async();
+  if (threadIdx.x == 0) {
+    mbar_init(&S.k_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.q_full[i], 1);
+      mbar_init(&S.q_empty[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.s_empty[i], 4);
+    }
+    for (int i = 0; i < kLseSlots; ++i) {
+      mbar_init(&S.z_full[i], 1);
+      mbar_init(&S.z_empty[i], 4);
+    }
+    S.abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem_base)),
+                 "r"(256)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp == 4) {
+    // ---------------- the keys once, then blocks of query rows and their z ----------------
+    const int live = min(kKeys, s.n - n0), boxes = (live + box - 1) / box;
+    if (lane == 0) mbar_expect_tx(&S.k_full, uint32_t(boxes) * box * 128 * kSub);
+    __syncwarp();
+    for (int i = lane; i < boxes; i += 32) {
+      const int slot = n0 + i * box, col = slot / c.page_size;
+      const int p = max(0, page_at(c.table, c.cols, c.n_pages, b, col, c.status));
+      const int row = (p * c.kvh + h) * c.page_size + (slot - col * c.page_size);
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) tma_load_2d(&S.k[u][i * box * 64], &tmK, u * 64, row, &S.k_full);
+    }
+    auto load_z = [&](int j, float (&z)[4]) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) z[u] = INFINITY;  // columns without a row: 2^-inf
+      if (j >= steps) return;
+      const Block x = block_at(bl, i0 + j, s.m);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int col = u * 32 + lane;
+        if (col < x.cols) {
+          const int t = x.t0 + (bl.runs == 1 ? col / bl.group : 0), g = bl.runs == 1 ? col % bl.group : x.h0 + col;
+          z[u] = a.lse[int64_t(s.row0 + t) * qh + h * c.group + g];
+        }
+      }
+    };
+    float z[4];
+    load_z(0, z);
+    bool ok = true;
+    for (int j = 0; j < steps; ++j) {
+      const int st = j & 1, zs = j % kLseSlots;
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.q_empty[st], ((j >> 1) & 1) ^ 1, abort));
+      if (!ok) break;
+      if (lane == 0) {
+        const Block x = block_at(bl, i0 + j, s.m);
+        mbar_expect_tx(&S.q_full[st], uint32_t(bl.heads) * bl.per * 128 * kSub);
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+          tma_load_3d(&S.q[st][u][0], &tmQ, u * 64, h * c.group + x.h0, s.row0 + x.t0, &S.q_full[st]);
+      }
+      float next[4];
+      load_z(j + 1, next);
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.z_empty[zs], ((j / kLseSlots) & 1) ^ 1, abort));
+      if (!ok) break;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        S.nz[zs][u * 32 + lane] = -z[u] * kLog2e;
+        z[u] = next[u];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.z_full[zs]);
+    }
+  } else if (warp == 5) {
+    // ---------------- products: S[key][row] ----------------
+    if (lane == 0) {
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kCols >> 3) << 17) | (uint32_t(kKeys >> 4) << 24);
+      bool ok = mbar_wait(&S.k_full, 0, abort);
+      for (int j = 0; j < steps && ok; ++j) {
+        const int st = j & 1, ph = (j >> 1) & 1;
+        ok = mbar_wait(&S.q_full[st], ph, abort) && mbar_wait(&S.s_empty[st], ph ^ 1, abort);
+        if (!ok) break;
+        fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int u = kk >> 2, off = (kk & 3) * 32;
+          mma_bf16(tmem + uint32_t(st * kCols), sw128_desc(saddr(&S.k[u][0]) + off),
+                   sw128_desc(saddr(&S.q[st][u][0]) + off), idesc, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&S.q_empty[st]);
+        mma_commit(&S.s_full[st]);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- one thread per key ----------------
+    const int slot = n0 + warp * 32 + lane;
+    const uint32_t ts = tmem + (uint32_t(warp * 32) << 16);
+    const float scale = kLog2e * rsqrtf(float(D));
+    const uint64_t sc2 = pk2(scale, scale);
+    float sum = 0.f;
+    for (int j = 0; j < steps; ++j) {
+      const int st = j & 1, zs = j % kLseSlots;
+      bool ok = mbar_wait(&S.s_full[st], (j >> 1) & 1, abort) && mbar_wait(&S.z_full[zs], (j / kLseSlots) & 1, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      fence_after();
+      uint32_t x0[32], x1[32], x2[32], x3[32];
+      const uint32_t at = ts + uint32_t(st * kCols);
+      tmem_ld32(at, x0);
+      tmem_ld32(at + 32, x1);
+      tmem_ld32(at + 64, x2);
+      tmem_ld32(at + 96, x3);
+      tmem_wait_ld();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.s_empty[st]);
+      const Block x = block_at(bl, i0 + j, s.m);
+      // columns [low, x.cols) see this thread's key
+      const int dt = min(slot - first - x.t0, bl.per);
+      const int low = dt <= 0 ? 0 : (bl.runs == 1 ? dt * bl.group : kCols);
+      const bool last = bl.runs == 1 ? x.cols < bl.per * bl.group : x.cols < bl.heads;
+      const float* nz = S.nz[zs];
+      uint64_t l0 = 0, l1 = 0;  // a step's own sums: two levels keep long chunks' sums exact
+      if (!__any_sync(0xffffffffu, low > 0) && !last) {
+        auto weigh = [&](const uint32_t (&v)[32], int col) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 n4 = *reinterpret_cast<const float4*>(nz + col + i);
+            const uint64_t y0 = fma2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, pk2(n4.x, n4.y));
+            const uint64_t y1 = fma2(pk2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2, pk2(n4.z, n4.w));
+            l0 = add2(l0, pk2(ex2(lo2(y0)), ex2(hi2(y0))));
+            l1 = add2(l1, pk2(ex2(lo2(y1)), ex2(hi2(y1))));
+          }
+        };
+        weigh(x0, 0);
+        weigh(x1, 32);
+        weigh(x2, 64);
+        weigh(x3, 96);
+      } else {
+        // rows outside the sequence may hold anything: selected away, not multiplied
+        float l = 0.f;
+        auto weigh = [&](const uint32_t (&v)[32], int col) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float e = ex2(fmaf(__uint_as_float(v[i]), scale, nz[col + i]));
+            l += col + i >= low && col + i < x.cols ? e : 0.f;
+          }
+        };
+        weigh(x0, 0);
+        weigh(x1, 32);
+        weigh(x2, 64);
+        weigh(x3, 96);
+        l0 = pk2(l, 0.f);
+      }
+      sum += (lo2(l0) + hi2(l0)) + (lo2(l1) + hi2(l1));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.z_empty[zs]);
+    }
+    if (slot < s.n) a.scores[(int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size) + slot] += sum;
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
+  }
+  if (threadIdx.x == 0 && S.abort) flag(c.status, MP_STATUS_WAIT_TIMEOUT);
+}
+
+// ---- few query rows ----
+
+constexpr int kStepWarps = 8, kStepKeys = 64;  // keys of a warp
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 keys (M) x 8 NT query rows (N) per warp and round. The sum over d has no order to
+// keep, so lane t of a row's four takes the 16-byte chunks t, t + 4, ... and feeds their
+// halves to two products: the loads are whole vectors and need no shared memory.
+template <int D, int NT>
+__global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsArgs a) {
+  constexpr int kChunks = D / 32;  // 16-byte chunks of a row per lane
+  const CacheArgs& c = a.c;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const Seq s = seq_of(c, b);
+  const int w0 = (blockIdx.x * kStepWarps + warp) * kStepKeys;
+  if (w0 >= s.n || s.m == 0) return;
+  const int first = s.n - s.m, qh = c.kvh * c.group, rows = s.m * c.group;
+  const float scale = kLog2e * rsqrtf(float(D));
+  uint4 q[NT][kChunks];
+  float nz[NT][2];
+  int see[NT][2];  // the thread's columns see the slots below this
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int r = u * 8 + g;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                               (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D + t * 8;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+      q[u][i] = r < rows ? *reinterpret_cast<const uint4*>(src + i * 32) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int rc = u * 8 + 2 * t + i;
+      see[u][i] = rc < rows ? first + rc / c.group + 1 : 0;
+      nz[u][i] = rc < rows ? -kLog2e * a.lse[int64_t(s.row0 + rc / c.group) * qh + h * c.group + rc % c.group] : 0.f;
+    }
+  }
+  float* scores = a.scores + (int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size);
+  const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.keys);
+#pragma unroll 2
+  for (int k0 = w0; k0 < min(s.n, w0 + kStepKeys); k0 += 16) {
+    uint4 k[2][kChunks];
+    float old[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int slot = min(k0 + g + 8 * i, s.n - 1);
+      const __nv_bfloat16* src = keys + slot_read(c, b, h, slot) + t * 8;
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) k[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + j * 32));
+      old[i] = t == 0 ? scores[slot] : 0.f;
+    }
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        mma_16816(x, k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y, q[u][j].x, q[u][j].y);
+        mma_16816(x, k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w, q[u][j].z, q[u][j].w);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int slot = k0 + g + 8 * (i >> 1);
+        if (slot < see[u][i & 1]) sum[i >> 1] += ex2(fmaf(x[i], scale, nz[u][i & 1]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+      const int slot = k0 + g + 8 * i;
+      if (t == 0 && slot < s.n) scores[slot] = old[i] + sum[i];
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch(const WeightsArgs& a, cudaStream_t st) {
+  const CacheArgs& c = a.c;
+  const int64_t rows = int64_t(c.max_q) * c.group;
+  if (rows <= 32) {
+    const dim3 grid((c.max_kv + kStepWarps * kStepKeys - 1) / (kStepWarps * kStepKeys), c.kvh, c.batch);
+    if (rows <= 8) k_weights_step<D, 1><<<grid, kStepWarps * 32, 0, st>>>(a);
+    else if (rows <= 16) k_weights_step<D, 2><<<grid, kStepWarps * 32, 0, st>>>(a);
+    else k_weights_step<D, 4><<<grid, kStepWarps * 32, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  CUtensorMap mk, mq;
+  const int box = box_rows(c.table, c.page_size);
+  const Blocks bl = blocks_of(c.group, 1);
+  if (!make_map(&mk, a.keys, D, uint64_t(c.n_pages) * c.kvh * c.page_size, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map3(&mq, a.q, D, uint64_t(c.kvh) * c.group, c.total_q, 64, bl.heads, bl.per))
+    return cudaErrorInvalidValue;
+  const size_t smem = sizeof(WSmem<D>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(k_weights_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  k_weights_tc<D><<<dim3((c.max_kv + kKeys - 1) / kKeys, c.kvh, c.batch), 192, smem, st>>>(mk, mq, a, box);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_weights_bf16(const WeightsArgs& a, cudaStream_t st) {
+  return a.c.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
+}
+
+}  // namespace mp
