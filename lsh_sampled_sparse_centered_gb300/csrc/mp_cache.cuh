@@ -22,9 +22,12 @@ struct ChunkArgs {
   const void *q, *keys, *values;
   void* out;
   float* lse;   // may be nullptr
-  int splits;   // slices of the keys per row tile
-  float* part;  // [splits][total_q][q_heads][d]: unnormalised partial sums (splits > 1)
-  float* ml;    // [splits][total_q][q_heads][2]: their maximum (log2 units) and sum
+  // partial results in the workspace: fp32 slices [splits][total_q][q_heads], bf16 slots of
+  // the pieces of tiles that are shared by CTAs
+  int splits;   // slices of the keys per row tile (fp32)
+  float* part;  // [..][d]: unnormalised sums
+  float* ml;    // [..][2]: their reference (log2) and sum
+  void* cuts;   // shared tiles (bf16)
 };
 
 struct WeightsArgs {
@@ -59,9 +62,11 @@ struct EvictArgs {
   int32_t* kept;  // [batch][kv_heads][budget]
 };
 
-// Slices of the keys that a chunk attention of these limits runs with, and the rows of
-// a tile (fixed by the limits alone, so that the workspace can be sized before the call).
-int chunk_splits(const mp_cache_config* c, int total_q, int max_q, int max_kv);
+// Sizes that the limits alone fix, so that a workspace can be sized before the call: slices
+// of the keys (fp32), CTAs of the tensor-core kernel and its workspace (bf16).
+int chunk_splits(const mp_cache_config* c, int max_q, int max_kv);
+int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv);
+uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv);
 
 // Rows of a TMA box of K or V: the most that divide a 128-key tile and never leave a page
 // (16 at least: page sizes are multiples of 16). Without a table a box may run past the
@@ -73,9 +78,9 @@ inline int box_rows(const int32_t* table, int page_size) {
 }
 
 cudaError_t launch_cache_append(const AppendArgs& a, int dtype, cudaStream_t st);
-cudaError_t launch_chunk_attend(const ChunkArgs& a, int dtype, cudaStream_t st);
-cudaError_t launch_chunk_tc(const ChunkArgs& a, cudaStream_t st);
-cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st);
+cudaError_t launch_chunk_join(const ChunkArgs& a, cudaStream_t st);
+cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st);
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_weights_bf16(const WeightsArgs& a, cudaStream_t st);
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);

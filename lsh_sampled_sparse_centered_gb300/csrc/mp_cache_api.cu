@@ -59,12 +59,15 @@ static CacheArgs cache_args(const mp_cache_config* c, const int32_t* table, cons
   return a;
 }
 
-static uint64_t chunk_part_bytes(const mp_cache_config* c, int total_q, int splits) {
+static uint64_t simt_part_bytes(const mp_cache_config* c, int total_q, int splits) {
   return align256(uint64_t(splits) * total_q * c->q_heads * c->head_dim * 4);
 }
-static uint64_t chunk_bytes(const mp_cache_config* c, int total_q, int splits) {
+static uint64_t chunk_bytes(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
+  if (total_q == 0) return 0;
+  if (c->dtype == MP_DTYPE_BF16) return chunk_tc_workspace(c, std::min(max_q, total_q), max_kv);
+  const int splits = chunk_splits(c, max_q, max_kv);
   if (splits <= 1) return 0;
-  return chunk_part_bytes(c, total_q, splits) + align256(uint64_t(splits) * total_q * c->q_heads * 2 * 4);
+  return simt_part_bytes(c, total_q, splits) + align256(uint64_t(splits) * total_q * c->q_heads * 2 * 4);
 }
 
 static uint64_t evict_bytes(const mp_cache_config* c, int budget) {
@@ -141,7 +144,7 @@ int mp_chunk_workspace_bytes(const mp_cache_config* cfg, int32_t total_q, int32_
   if (rc != MP_OK) return rc;
   if ((rc = check_limits(cfg, total_q, max_q, max_kv)) != MP_OK) return rc;
   if (!bytes) return MP_ERR_INVALID_ARG;
-  *bytes = chunk_bytes(cfg, total_q, chunk_splits(cfg, total_q, max_q, max_kv));
+  *bytes = chunk_bytes(cfg, total_q, max_q, max_kv);
   return MP_OK;
 }
 
@@ -162,32 +165,40 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
                         static_cast<const void*>(page_table), static_cast<const void*>(lse),
                         static_cast<const void*>(status)})
     if (!aligned4(p)) return MP_ERR_INVALID_ARG;
-  ChunkArgs a;
-  a.splits = chunk_splits(cfg, total_q, max_q, max_kv);
-  const uint64_t need = chunk_bytes(cfg, total_q, a.splits);
+  const uint64_t need = chunk_bytes(cfg, total_q, max_q, max_kv);
   if (need > 0) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MP_ERR_INVALID_ARG;
     if (workspace_bytes < need) return MP_ERR_SCRATCH;
   }
   if (injected("chunk")) return MP_ERR_INJECTED;
-  a.c = cache_args(cfg, page_table, cu_q, kv_len, total_q, max_q, max_kv, status);
+  ChunkArgs a;
+  a.c = cache_args(cfg, page_table, cu_q, kv_len, total_q, std::min(max_q, total_q), max_kv, status);
   a.q = q;
   a.keys = keys;
   a.values = values;
   a.out = out;
   a.lse = lse;
-  a.part = need ? static_cast<float*>(workspace) : nullptr;
-  a.ml = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) + chunk_part_bytes(cfg, total_q, a.splits))
-              : nullptr;
+  a.splits = 1;
+  a.part = a.ml = nullptr;
+  a.cuts = nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
+  if (cfg->dtype == MP_DTYPE_BF16) {
+    ProfScope ps(st, K_CHUNK_ATTEND);
+    return launch_chunk_tc(a, workspace, st) == cudaSuccess ? MP_OK : MP_ERR_CUDA;
+  }
+  a.splits = chunk_splits(cfg, max_q, max_kv);
+  if (need > 0) {
+    a.part = static_cast<float*>(workspace);
+    a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + simt_part_bytes(cfg, total_q, a.splits));
+  }
   {
     ProfScope ps(st, K_CHUNK_ATTEND);
-    if (launch_chunk_attend(a, cfg->dtype, st) != cudaSuccess) return MP_ERR_CUDA;
+    if (launch_chunk_simt(a, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   if (a.splits > 1) {
     ProfScope ps(st, K_CHUNK_JOIN);
-    if (launch_chunk_join(a, cfg->dtype, st) != cudaSuccess) return MP_ERR_CUDA;
+    if (launch_chunk_join(a, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   return MP_OK;
 }

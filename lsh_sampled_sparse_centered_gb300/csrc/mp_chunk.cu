@@ -1,5 +1,5 @@
 // Exact attention of a chunk of new tokens over the paged cache, and the attention
-// weights that its keys received, on the CUDA cores.
+// weights that its keys received, on the CUDA cores: the fp32 forms.
 //
 // A tile is 64 query rows of one KV head (row = token * group + head of the group, so the
 // heads of a group share every key they load) against 64 keys at a time. The softmax is
@@ -16,31 +16,18 @@ constexpr int kBM = 64, kBN = 64, kThr = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
 
 // 64 rows into shared memory as [d][64] (row index fastest): thread t takes row t % 64 and
 // every other group of 8 elements; p(row) is the row's address or nullptr (zeros).
-template <typename T, int D, typename P>
+template <int D, typename P>
 __device__ __forceinline__ void load_transposed(float* dst, P p) {
   const int row = threadIdx.x & 63;
-  const T* src = p(row);
+  const float* src = p(row);
 #pragma unroll 4
   for (int e = (threadIdx.x >> 6) * 8; e < D; e += 16) {
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -49,11 +36,11 @@ __device__ __forceinline__ void load_transposed(float* dst, P p) {
     for (int i = 0; i < 8; ++i) dst[(e + i) * 64 + row] = x[i];
   }
 }
-template <typename T, int D, typename P>
+template <int D, typename P>
 __device__ __forceinline__ void load_rows(float* dst, P p) {
   for (int i = threadIdx.x; i < 64 * (D / 8); i += kThr) {
     const int row = i / (D / 8), e = (i % (D / 8)) * 8;
-    const T* src = p(row);
+    const float* src = p(row);
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (src) load8(src + e, x);
     *reinterpret_cast<float4*>(dst + row * D + e) = make_float4(x[0], x[1], x[2], x[3]);
@@ -81,7 +68,7 @@ __device__ __forceinline__ void dot_tile(const float* qt, const float* kt, int t
   }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
   extern __shared__ float sm[];
   float* qt = sm;               // [D][64]
@@ -101,12 +88,12 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
   // this split's keys: a run of 64-key tiles of the sequence
   const int tiles = (s.n + kBN - 1) / kBN, per = (tiles + a.splits - 1) / a.splits;
   const int k0 = split * per * kBN, k1 = min(min(s.n, last + 1), (split + 1) * per * kBN);
-  auto qrow = [&](int i) -> const T* {
+  auto qrow = [&](int i) -> const float* {
     const int r = r0 + i;
-    return r < rows ? static_cast<const T*>(a.q) + (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D
+    return r < rows ? static_cast<const float*>(a.q) + (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D
                     : nullptr;
   };
-  load_transposed<T, D>(qt, qrow);
+  load_transposed<D>(qt, qrow);
   float m[8], l[8], o[8][D / 16];
   int see[8];  // a row sees the slots below this
 #pragma unroll
@@ -120,11 +107,11 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
   const float scale = kLog2e * rsqrtf(float(D));
   for (int n0 = k0; n0 < k1; n0 += kBN) {
     __syncthreads();
-    auto slot_ptr = [&](const void* base, int i) -> const T* {
-      return n0 + i < k1 ? static_cast<const T*>(base) + slot_read(c, b, h, n0 + i) : nullptr;
+    auto slot_ptr = [&](const void* base, int i) -> const float* {
+      return n0 + i < k1 ? static_cast<const float*>(base) + slot_read(c, b, h, n0 + i) : nullptr;
     };
-    load_transposed<T, D>(kt, [&](int i) { return slot_ptr(a.keys, i); });
-    load_rows<T, D>(vs, [&](int i) { return slot_ptr(a.values, i); });
+    load_transposed<D>(kt, [&](int i) { return slot_ptr(a.keys, i); });
+    load_rows<D>(vs, [&](int i) { return slot_ptr(a.values, i); });
     __syncthreads();
     float x[8][4];
     dot_tile<D>(qt, kt, ty, tx, x);
@@ -195,15 +182,15 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
     } else {
       const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
       if (a.lse && tx == 0) a.lse[row] = sum == 0.f ? -INFINITY : m[i] * kLn2 + logf(sum);
-      T* out = static_cast<T*>(a.out) + row * D;
+      float* out = static_cast<float*>(a.out) + row * D;
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) out[(j / 4) * 64 + tx * 4 + j % 4] = T(o[i][j] * inv);
+      for (int j = 0; j < D / 16; ++j) out[(j / 4) * 64 + tx * 4 + j % 4] = o[i][j] * inv;
     }
   }
 }
 
 // One warp per query row: joins the splits' (m, l, sum), in the order of the splits.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   const CacheArgs& c = a.c;
   const int qh = c.kvh * c.group;
@@ -231,12 +218,12 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) static_cast<T*>(a.out)[row * D + j * 32 + lane] = T(o[j] * inv);
+  for (int j = 0; j < D / 32; ++j) static_cast<float*>(a.out)[row * D + j * 32 + lane] = o[j] * inv;
 }
 
 // Attention weights: one CTA owns 64 slots of one KV head and walks the chunk's query
 // rows in order, so every slot's sum has one owner and a fixed order.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
   extern __shared__ float sm[];
   float* qt = sm;            // [D][64]
@@ -248,8 +235,8 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
   if (n0 >= s.n || s.m == 0) return;
   const int rows = s.m * c.group, first = s.n - s.m, qh = c.kvh * c.group;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  load_transposed<T, D>(kt, [&](int i) -> const T* {
-    return n0 + i < s.n ? static_cast<const T*>(a.keys) + slot_read(c, b, h, n0 + i) : nullptr;
+  load_transposed<D>(kt, [&](int i) -> const float* {
+    return n0 + i < s.n ? static_cast<const float*>(a.keys) + slot_read(c, b, h, n0 + i) : nullptr;
   });
   const float scale = kLog2e * rsqrtf(float(D));
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -257,9 +244,9 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
   const int start = max(0, n0 - first) * c.group / kBM * kBM;
   for (int r0 = start; r0 < rows; r0 += kBM) {
     __syncthreads();
-    load_transposed<T, D>(qt, [&](int i) -> const T* {
+    load_transposed<D>(qt, [&](int i) -> const float* {
       const int r = r0 + i;
-      return r < rows ? static_cast<const T*>(a.q) + (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D
+      return r < rows ? static_cast<const float*>(a.q) + (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D
                       : nullptr;
     });
     __syncthreads();
@@ -288,54 +275,50 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   constexpr int smem = (3 * D * 64 + 64 * 64) * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_chunk_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(k_chunk_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t(a.c.max_q) * a.c.group + kBM - 1) / kBM;
-  k_chunk_simt<T, D><<<dim3(unsigned(tiles * a.splits), a.c.kvh, a.c.batch), kThr, smem, st>>>(a);
+  k_chunk_simt<D><<<dim3(unsigned(tiles * a.splits), a.c.kvh, a.c.batch), kThr, smem, st>>>(a);
   return cudaGetLastError();
 }
-template <typename T, int D>
+template <int D>
 cudaError_t join(const ChunkArgs& a, cudaStream_t st) {
   const int64_t rows = int64_t(a.c.total_q) * a.c.kvh * a.c.group;
-  k_chunk_join<T, D><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
+  k_chunk_join<D><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
-template <typename T, int D>
+template <int D>
 cudaError_t weights_simt(const WeightsArgs& a, cudaStream_t st) {
   constexpr int smem = (2 * D * 64 + 8 * 64) * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_weights_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(k_weights_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_weights_simt<T, D><<<dim3((a.c.max_kv + kBN - 1) / kBN, a.c.kvh, a.c.batch), kThr, smem, st>>>(a);
+  k_weights_simt<D><<<dim3((a.c.max_kv + kBN - 1) / kBN, a.c.kvh, a.c.batch), kThr, smem, st>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Slices of the keys: as many as fill the SMs about twice, each of at least 256 slots. A
-// tile has 256 rows on the tensor cores (bf16) and 64 on the CUDA cores (fp32).
-int chunk_splits(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
-  (void)total_q;
-  const int64_t group = c->q_heads / c->kv_heads, tile = c->dtype == MP_DTYPE_BF16 ? 256 : kBM;
-  const int64_t ctas = (max_q * group + tile - 1) / tile * c->kv_heads * c->batch;
-  const int64_t fill = 2 * 152 / ctas, most = (int64_t(max_kv) + 255) / 256;
+// Slices of the keys: as many as fill the SMs about twice, each of at least 256 slots.
+int chunk_splits(const mp_cache_config* c, int max_q, int max_kv) {
+  const int64_t group = c->q_heads / c->kv_heads;
+  const int64_t ctas = (max_q * group + kBM - 1) / kBM * c->kv_heads * c->batch;
+  const int64_t fill = 2 * int64_t(device_sm_count()) / ctas, most = (int64_t(max_kv) + 255) / 256;
   const int64_t s = fill < most ? fill : most;
   return int(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
 
-cudaError_t launch_chunk_attend(const ChunkArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == MP_DTYPE_BF16) return launch_chunk_tc(a, st);
-  return a.c.d == 128 ? chunk_simt<float, 128>(a, st) : chunk_simt<float, 64>(a, st);
+cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st) {
+  return a.c.d == 128 ? chunk_simt<128>(a, st) : chunk_simt<64>(a, st);
 }
-cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == MP_DTYPE_BF16) return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, st) : join<__nv_bfloat16, 64>(a, st);
-  return a.c.d == 128 ? join<float, 128>(a, st) : join<float, 64>(a, st);
+cudaError_t launch_chunk_join(const ChunkArgs& a, cudaStream_t st) {
+  return a.c.d == 128 ? join<128>(a, st) : join<64>(a, st);
 }
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st) {
   if (dtype == MP_DTYPE_BF16) return launch_weights_bf16(a, st);
-  return a.c.d == 128 ? weights_simt<float, 128>(a, st) : weights_simt<float, 64>(a, st);
+  return a.c.d == 128 ? weights_simt<128>(a, st) : weights_simt<64>(a, st);
 }
 
 }  // namespace mp

@@ -17,6 +17,8 @@
 // Tensor memory: S/P of the halves in columns 0 and 128, O in 256 and 256 + d.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "mp_cache.cuh"
 #include "mp_tc.cuh"
 
@@ -29,6 +31,16 @@ constexpr int kThreads = 384;  // 12 warps: two of softmax for each lane quarter
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;
+constexpr int kGroup = 1024;  // sequences of a launch
+constexpr int kMinRun = 2;    // units of a CTA at least: a piece costs about as much to start and to join
+
+// One piece of work: the units [u0, u1) of a tile, as every role of the CTA sees it.
+struct Piece {
+  int b, h, row0, n, lead;  // sequence, KV head, first packed row, slots, slots before the chunk
+  int r0, rows;             // the tile's first row, and the rows of the whole chunk
+  int u0, u1;               // u0 == u1: the run has ended
+  int whole, slot;          // all of its tile's units; else where its partial result goes
+};
 
 template <int D>
 struct Smem {
@@ -37,11 +49,20 @@ struct Smem {
   __nv_bfloat16 q[2][kSub][128 * 64];
   __nv_bfloat16 kv[kStages][kSub][kKeys * 64];
   uint64_t full[kStages], empty[kStages], tail;
-  uint64_t q_full, s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];
+  uint64_t piece_full[2], piece_empty[2];
+  Piece piece[2];
+  int64_t left, run;
+  int start[4];  // sequence, KV head, tile, unit
   uint32_t tmem_base;
   uint32_t abort;
 };
 
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return r;
+}
 // MN-major operand (V: rows are keys, d contiguous) in 128B-swizzled boxes of 64 elements
 // x 128 keys: 8-key groups 1024 B apart, 64-element groups 128 rows apart.
 __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr) {
@@ -71,18 +92,35 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-// One piece of work: rows [r0, r0 + 256) of KV head h of sequence b against the slots
-// [k0, k1).
-struct Item {
-  Seq s;
-  int b, h, r0, rows, first;
-  int k0, k1, split;
+// Work is counted in units: one 256-row tile of a KV head against 128 keys (a tile that
+// sees nothing counts one, so that its rows are written). The units of all tiles, in the
+// order (sequence, KV head, tile, keys), are cut into equal runs, one per CTA, whatever the
+// lengths: a CTA's run covers the end of one tile, whole tiles, and the start of another.
+// Whole tiles are written out; of a tile that is cut every piece stores its unnormalised
+// sum, and k_chunk_tc_join puts the pieces together. A CTA has two such pieces at most: the
+// one that starts its run (slot 2 cta) and the one that ends it (slot 2 cta + 1).
+__device__ __forceinline__ int tiles_of(const Seq& s, int group) {
+  return int((int64_t(s.m) * group + kRows - 1) / kRows);
+}
+// units of tile t: steps of 128 keys up to the last slot that its last token sees
+__device__ __forceinline__ int units_of(const Seq& s, int group, int t) {
+  const int64_t last = min(int64_t(t + 1) * kRows, int64_t(s.m) * group) - 1;
+  const int see = min(s.n, s.n - s.m + int(last / group) + 1);
+  return max(1, (see + kKeys - 1) / kKeys);
+}
+
+// What k_chunk_tc_join needs of a tile that CTA `cta` began and did not end.
+struct Cut {
+  int64_t row;     // packed row of the tile's first token, as a row of (token, query head)
+  int pieces;      // CTAs that share the tile (0: nothing to join)
+  int slot;        // slot of the first piece; the others are slots 2 (cta + i)
+  int r0, rows;    // the tile's first row and its rows
 };
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkArgs a,
-               const int box) {
+               const int box, const int b_begin, const int b_end, const int slot_rows) {
   extern __shared__ __align__(1024) unsigned char smraw[];
   const uint32_t base = saddr(smraw);
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(smraw + ((1024 - (base & 1023)) & 1023));
@@ -91,25 +129,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile uint32_t* abort = &S.abort;
-
-  Item it;
-  it.b = blockIdx.z;
-  it.h = blockIdx.y;
-  it.split = blockIdx.x % a.splits;
-  it.s = seq_of(c, it.b);
-  it.rows = it.s.m * c.group;
-  it.r0 = int(blockIdx.x / a.splits) * kRows;
-  if (it.r0 >= it.rows) return;
-  it.first = it.s.n - it.s.m;
-  {
-    const int last = it.first + min(it.r0 + kRows - 1, it.rows - 1) / c.group;
-    const int tiles = (it.s.n + kKeys - 1) / kKeys, per = (tiles + a.splits - 1) / a.splits;
-    it.k0 = it.split * per * kKeys;
-    it.k1 = min(min(it.s.n, last + 1), (it.split + 1) * per * kKeys);
-  }
-  const int steps = it.k1 > it.k0 ? (it.k1 - it.k0 + kKeys - 1) / kKeys : 0;
-  const int halves = it.rows - it.r0 > 128 ? 2 : 1;
   const int qh = c.kvh * c.group;
+
+  // ---- where this CTA's run starts ----
+  int64_t* units = reinterpret_cast<int64_t*>(&S.kv[0][0][0]);  // of each sequence and KV head; the ring is not yet in use
+  static_assert(kGroup * 8 <= kKeys * 128, "one tile of the ring");
+  for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
+    const Seq s = seq_of(c, b);
+    const int tiles = tiles_of(s, c.group);
+    int64_t u = 0;
+    for (int t = lane; t < tiles; t += 32) u += units_of(s, c.group, t);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    if (lane == 0) units[b - b_begin] = u;  // of one KV head
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t all = 0;
+    for (int b = lane; b < b_end - b_begin; b += 32) all += units[b] * c.kvh;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    const int64_t run = max(int64_t(kMinRun), (all + gridDim.x - 1) / int64_t(gridDim.x));
+    int64_t at = blockIdx.x * run;
+    const int64_t left = max(int64_t(0), min(run, all - at));
+    if (left > 0) {
+      // the sequence, by prefix sums of 32 at a time
+      int b = b_begin;
+      for (;; b += 32) {
+        const int64_t mine = b + lane < b_end ? units[b + lane - b_begin] * c.kvh : 0;
+        int64_t pre = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, pre > at);
+        if (past) {
+          const int i = __ffs(past) - 1;
+          at -= __shfl_sync(0xffffffffu, pre - mine, i);
+          b += i;
+          break;
+        }
+        at -= __shfl_sync(0xffffffffu, pre, 31);
+      }
+      const int64_t per = units[b - b_begin];
+      const int h = int(at / per);
+      at -= h * per;
+      const Seq s = seq_of(c, b);
+      const int tiles = tiles_of(s, c.group);
+      int t = 0;
+      for (;; t += 32) {
+        const int64_t mine = t + lane < tiles ? units_of(s, c.group, t + lane) : 0;
+        int64_t pre = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, pre > at);
+        if (past) {
+          const int i = __ffs(past) - 1;
+          at -= __shfl_sync(0xffffffffu, pre - mine, i);
+          t += i;
+          break;
+        }
+        at -= __shfl_sync(0xffffffffu, pre, 31);
+      }
+      if (lane == 0) {
+        S.start[0] = b;
+        S.start[1] = h;
+        S.start[2] = t;
+        S.start[3] = int(at);
+      }
+    }
+    if (lane == 0) {
+      S.left = left;
+      S.run = run;
+    }
+    fence_async();
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -117,10 +215,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.empty[i], 1);
     }
     mbar_init(&S.tail, 1);
-    mbar_init(&S.q_full, 8);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.q_full[i], 4);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.p_full[i][0], 4);
+      mbar_init(&S.p_full[i][1], 4);
+      mbar_init(&S.piece_full[i], 1);
+      mbar_init(&S.piece_empty[i], 10);  // the TMA warp, the product warp, eight of softmax
       mbar_init(&S.o_full[i], 1);
     }
     S.abort = 0u;
@@ -139,233 +240,349 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // registers: 8 x 208 + 4 x 80 a lane, within the 12 x 168 of the launch
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == 8) {
-    // ---------------- K and V tiles ----------------
-    uint32_t cnt = 0;  // tiles issued: K of step 0, V of step 0, K of step 1, ...
-    bool ok = true;
-    for (int j = 0; j < steps && ok; ++j) {
-      const int n0 = it.k0 + j * kKeys;
-      const int live = min(kKeys, it.s.n - n0);          // rows that hold slots of the sequence
-      const int boxes = (live + box - 1) / box;
-      for (int kv = 0; kv < 2 && ok; ++kv, ++cnt) {
-        const int st = cnt % kStages;
-        ok = mbar_wait(&S.empty[st], ((cnt / kStages) & 1) ^ 1, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        // rows of V behind the last slot are zeroed before the products see the tile: they may
-        // hold anything, and 0 * NaN is NaN (in S such columns are masked)
-        const bool patch = kv == 1 && live < kKeys;
-        uint64_t* bar = patch ? &S.tail : &S.full[st];
-        if (lane == 0) mbar_expect_tx(bar, uint32_t(boxes) * box * kRowBytes * kSub);
-        __syncwarp();
-        for (int i = lane; i < boxes; i += 32) {
-          const int slot = n0 + i * box, col = slot / c.page_size;
-          const int p = max(0, page_at(c.table, c.cols, c.n_pages, it.b, col, c.status));
-          const int row = (p * c.kvh + it.h) * c.page_size + (slot - col * c.page_size);
-#pragma unroll
-          for (int s = 0; s < kSub; ++s)
-            tma_load_2d(&S.kv[st][s][i * box * 64], kv ? &tmV : &tmK, s * 64, row, bar);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 10) {
+      // ---------------- the run's pieces, two of them ahead ----------------
+      if (lane == 0) {
+        Cut cut;
+        cut.pieces = 0;
+        int64_t left = S.left;
+        const int64_t run = S.run, end = blockIdx.x * run + left;
+        int b = S.start[0], h = S.start[1], t = S.start[2], u0 = S.start[3];
+        Seq s = {0, 0, 0};
+        int tiles = 0;
+        if (left > 0) {
+          s = seq_of(c, b);
+          tiles = tiles_of(s, c.group);
         }
-        if (patch) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&S.tail, 0, abort));
-          if (!ok) break;
-          const uint4 z = make_uint4(0, 0, 0, 0);
-          for (int s = 0; s < kSub; ++s) {
-            uint4* p = reinterpret_cast<uint4*>(&S.kv[st][s][0]);
-            for (int i = live * 8 + lane; i < kKeys * 8; i += 32) p[i] = z;
+        for (uint32_t i = 0;; ++i) {
+          const int k = i & 1;
+          if (!mbar_wait(&S.piece_empty[k], ((i >> 1) & 1) ^ 1, abort)) break;
+          Piece& p = S.piece[k];
+          if (left <= 0) {
+            p.u0 = p.u1 = 0;
+            mbar_arrive(&S.piece_full[k]);
+            break;
           }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.full[st]);
-        }
-      }
-    }
-  } else if (warp == 9) {
-    // ---------------- products ----------------
-    if (lane == 0 && steps > 0) {
-      const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kKeys >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-      const uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) |
-                            (uint32_t(128 >> 4) << 24);
-      auto product_s = [&](int half, int st) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int s = kk >> 2, off = (kk & 3) * 32;
-          mma_bf16(tmem + uint32_t(half * 128), sw128_desc(saddr(&S.q[half][s][0]) + off),
-                   sw128_desc(saddr(&S.kv[st][s][0]) + off), id_s, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&S.s_full[half]);
-      };
-      bool ok = mbar_wait(&S.q_full, 0, abort) && mbar_wait(&S.full[0], 0, abort);
-      if (ok) {
-        fence_after();
-        for (int half = 0; half < halves; ++half) product_s(half, 0);
-        mma_commit(&S.empty[0]);
-      }
-      for (int j = 0; j < steps && ok; ++j) {
-        const uint32_t cv = 2 * j + 1, ck = 2 * j + 2;
-        const int sv = cv % kStages, sk = ck % kStages;
-        ok = mbar_wait(&S.full[sv], (cv / kStages) & 1, abort);
-        for (int half = 0; half < halves && ok; ++half) {
-          ok = mbar_wait(&S.p_full[half], j & 1, abort);
-          if (!ok) break;
-          fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_bf16_ta(tmem + uint32_t(256 + half * D), tmem + uint32_t(half * 128 + kk * 8),
-                        sw128_desc_mn(saddr(&S.kv[sv][0][0]) + kk * 2048), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&S.o_full[half]);
-          if (half == halves - 1) mma_commit(&S.empty[sv]);
-          if (j + 1 < steps) {
-            if (half == 0) {
-              ok = mbar_wait(&S.full[sk], (ck / kStages) & 1, abort);
-              if (!ok) break;
-              fence_after();
+          const int units = units_of(s, c.group, t);
+          p.b = b;
+          p.h = h;
+          p.row0 = s.row0;
+          p.n = s.n;
+          p.lead = s.n - s.m;
+          p.r0 = t * kRows;
+          p.rows = s.m * c.group;
+          p.u0 = u0;
+          p.u1 = int(min(int64_t(units), u0 + left));
+          p.whole = u0 == 0 && p.u1 == units;
+          p.slot = 2 * int(blockIdx.x) + (i == 0 ? 0 : 1);
+          if (u0 == 0 && !p.whole) {
+            // this CTA begins the tile; the CTAs of the units up to the tile's last go on with it
+            cut.row = int64_t(s.row0) * qh + h * c.group;
+            cut.slot = p.slot;
+            cut.r0 = p.r0;
+            cut.rows = min(kRows, p.rows - p.r0);
+            cut.pieces = int((end - left + units - 1) / run) - int(blockIdx.x) + 1;
+          }
+          left -= p.u1 - u0;
+          mbar_arrive(&S.piece_full[k]);
+          u0 = 0;
+          if (++t < tiles) continue;
+          t = 0;
+          if (++h < c.kvh) continue;
+          h = 0;
+          do {
+            if (++b >= b_end) {
+              left = 0;
+              break;
             }
-            product_s(half, sk);
-            if (half == halves - 1) mma_commit(&S.empty[sk]);
+            s = seq_of(c, b);
+            tiles = tiles_of(s, c.group);
+          } while (tiles == 0);
+        }
+        static_cast<Cut*>(a.cuts)[blockIdx.x] = cut;
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      // ---------------- K and V tiles ----------------
+      int st = 0;
+      uint32_t ph = 0, tails = 0;  // ring phase, tail tiles so far
+      bool ok = true;
+      for (uint32_t i = 0; ok; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.piece_full[i & 1], (i >> 1) & 1, abort));
+        if (!ok) break;
+        const Piece pc = S.piece[i & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.piece_empty[i & 1]);
+        if (pc.u0 == pc.u1) break;
+        for (int u = pc.u0; u < pc.u1 && ok; ++u) {
+          const int n0 = u * kKeys;
+          const int live = max(0, min(kKeys, pc.n - n0));  // rows that hold slots of the sequence
+          const int boxes = (live + box - 1) / box;
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[st], ph ^ 1, abort));
+            if (!ok) break;
+            // rows of V behind the last slot are zeroed before the products see the tile: they may
+            // hold anything, and 0 * NaN is NaN (in S such columns are masked)
+            const bool patch = kv == 1 && live < kKeys;
+            uint64_t* bar = patch ? &S.tail : &S.full[st];
+            if (lane == 0) mbar_expect_tx(bar, uint32_t(boxes) * box * kRowBytes * kSub);
+            __syncwarp();
+            for (int j = lane; j < boxes; j += 32) {
+              const int slot = n0 + j * box, col = slot / c.page_size;
+              const int p = max(0, page_at(c.table, c.cols, c.n_pages, pc.b, col, c.status));
+              const int row = (p * c.kvh + pc.h) * c.page_size + (slot - col * c.page_size);
+#pragma unroll
+              for (int s = 0; s < kSub; ++s)
+                tma_load_2d(&S.kv[st][s][j * box * 64], kv ? &tmV : &tmK, s * 64, row, bar);
+            }
+            if (patch) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&S.tail, tails & 1, abort));
+              if (!ok) break;
+              ++tails;
+              const uint4 z = make_uint4(0, 0, 0, 0);
+              for (int s = 0; s < kSub; ++s) {
+                uint4* p = reinterpret_cast<uint4*>(&S.kv[st][s][0]);
+                for (int j = live * 8 + lane; j < kKeys * 8; j += 32) p[j] = z;
+              }
+              fence_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.full[st]);
+            }
+            if (++st == kStages) {
+              st = 0;
+              ph ^= 1;
+            }
           }
         }
       }
+    } else if (warp == 9) {
+      // ---------------- products ----------------
+      if (lane == 0) {
+        const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kKeys >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+        const uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) |
+                              (uint32_t(128 >> 4) << 24);
+        const uint64_t dq = sw128_desc(saddr(&S.q[0][0][0])), dk = sw128_desc(saddr(&S.kv[0][0][0])),
+                       dv = sw128_desc_mn(saddr(&S.kv[0][0][0]));
+        constexpr uint32_t kTile = kKeys * D * 2 / 16, kSlab = kKeys * 128 / 16;  // in descriptor units of 16 bytes
+        int st = 0;
+        uint32_t ph = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+        auto advance = [&]() {
+          if (++st == kStages) {
+            st = 0;
+            ph ^= 1;
+          }
+        };
+        auto product_s = [&](int half, int sk) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
+            mma_bf16(tmem + uint32_t(half * 128), dq + half * kTile + off, dk + sk * kTile + off, id_s, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&S.s_full[half]);
+        };
+        bool ok = true;
+        for (uint32_t i = 0; ok; ++i) {
+          ok = mbar_wait(&S.piece_full[i & 1], (i >> 1) & 1, abort);
+          if (!ok) break;
+          const int steps = S.piece[i & 1].u1 - S.piece[i & 1].u0;
+          const int halves = S.piece[i & 1].rows - S.piece[i & 1].r0 > 128 ? 2 : 1;
+          mbar_arrive(&S.piece_empty[i & 1]);
+          if (steps == 0) break;
+          ok = mbar_wait(&S.full[st], ph, abort);
+          for (int half = 0; half < halves && ok; ++half) {
+            ok = mbar_wait(&S.q_full[half], ph_q[half], abort);
+            ph_q[half] ^= 1;
+            if (!ok) break;
+            fence_after();
+            product_s(half, st);
+          }
+          if (!ok) break;
+          mma_commit(&S.empty[st]);
+          advance();
+          for (int j = 0; j < steps && ok; ++j) {
+            const int sv = st;
+            ok = mbar_wait(&S.full[sv], ph, abort);
+            advance();
+            for (int half = 0; half < halves && ok; ++half) {
+              // P arrives in two parts of 64 keys: the product starts on the first
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                ok = ok && mbar_wait(&S.p_full[half][part], ph_p[half], abort);
+                if (!ok) break;
+                fence_after();
+#pragma unroll
+                for (int kk = part * 4; kk < part * 4 + 4; ++kk)
+                  mma_bf16_ta(tmem + uint32_t(256 + half * D), tmem + uint32_t(half * 128 + kk * 8),
+                              dv + sv * kTile + kk * 128, id_o, (j > 0 || kk > 0) ? 1u : 0u);
+              }
+              ph_p[half] ^= 1;
+              if (!ok) break;
+              mma_commit(&S.o_full[half]);
+              if (half == halves - 1) mma_commit(&S.empty[sv]);
+              if (j + 1 < steps) {
+                if (half == 0) {
+                  ok = mbar_wait(&S.full[st], ph, abort);
+                  if (!ok) break;
+                  fence_after();
+                }
+                product_s(half, st);
+                if (half == halves - 1) {
+                  mma_commit(&S.empty[st]);
+                  advance();
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax: one thread per row ----------------
-    const int half = warp >> 2;
-    // this thread's half of Q into its swizzled place (16-byte chunk c of row r at c ^ (r % 8))
-    {
-      const int t = threadIdx.x & 127;
-      for (int i = t; i < 128 * (D / 8); i += 128) {
-        const int r = i / (D / 8), ch = i % (D / 8), gr = it.r0 + half * 128 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (gr < it.rows) {
-          const int64_t at = (int64_t(it.s.row0 + gr / c.group) * qh + it.h * c.group + gr % c.group) * D + ch * 8;
-          v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-        }
-        *reinterpret_cast<uint4*>(&S.q[half][ch >> 3][r * 64 + (((ch & 7) ^ (r & 7)) << 3)]) = v;
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.q_full);
-    }
-    if (half < halves) {
-      const int quarter = warp & 3;
-      const int r = it.r0 + half * 128 + quarter * 32 + lane;
-      const bool real = r < it.rows;
-      const int see = real ? min(it.k1, it.first + r / c.group + 1) : 0;  // slots below this are seen
-      // the lowest limit of this warp's rows decides whether a step needs the mask at all
-      const int see_low = __reduce_min_sync(0xffffffffu, real ? see : INT32_MAX);
-      const uint32_t ts = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * 128);
-      const uint32_t to = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(256 + half * D);
-      const float scale = kLog2e * rsqrtf(float(D));
-      float m = -INFINITY;  // the row's reference, in log2
-      uint64_t l0 = 0, l1 = 0;
-      bool ok = true;
-      for (int j = 0; j < steps; ++j) {
-        const int n0 = it.k0 + j * kKeys;
-        ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[half], j & 1, abort));
-        if (!ok) break;
-        fence_after();
-        uint32_t x0[32], x1[32], x2[32], x3[32];
-        tmem_ld32(ts, x0);
-        tmem_ld32(ts + 32, x1);
-        tmem_ld32(ts + 64, x2);
-        tmem_ld32(ts + 96, x3);
-        tmem_wait_ld();
-        if (n0 + kKeys > see_low) {
-          const int lim = see - n0;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (i >= lim) x0[i] = 0xff800000u;
-            if (i + 32 >= lim) x1[i] = 0xff800000u;
-            if (i + 64 >= lim) x2[i] = 0xff800000u;
-            if (i + 96 >= lim) x3[i] = 0xff800000u;
+    const int half = warp >> 2, quarter = warp & 3;
+    const uint32_t ts = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * 128);
+    const uint32_t to = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(256 + half * D);
+    const float scale = kLog2e * rsqrtf(float(D));
+    uint32_t ph_s = 0, ph_o = 0;  // phases of s_full, and of o_full's next completion
+    bool ok = true;
+    for (uint32_t i = 0; ok; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.piece_full[i & 1], (i >> 1) & 1, abort));
+      if (!ok) break;
+      const Piece& pc = S.piece[i & 1];
+      const int r0 = pc.r0 + half * 128, rows = pc.rows;
+      if (pc.u0 == pc.u1) break;
+      if (r0 < rows) {
+        const int64_t head = int64_t(pc.row0) * qh + pc.h * c.group;  // row of token 0's first head
+        // this half of Q into its swizzled place (16-byte chunk c of row r at c ^ (r % 8))
+        {
+          const int t = threadIdx.x & 127;
+#pragma unroll 8
+          for (int i = t; i < 128 * (D / 8); i += 128) {
+            const int r = i / (D / 8), ch = i % (D / 8), gr = r0 + r;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (gr < rows) {
+              const int64_t at = (head + int64_t(gr / c.group) * qh + gr % c.group) * D + ch * 8;
+              v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+            }
+            *reinterpret_cast<uint4*>(&S.q[half][ch >> 3][r * 64 + (((ch & 7) ^ (r & 7)) << 3)]) = v;
           }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.q_full[half]);
         }
-        float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+        const int r = r0 + quarter * 32 + lane;
+        // slots below this, counted from the piece's first, are seen
+        int see = r < rows ? min(pc.n, pc.lead + r / c.group + 1) - pc.u0 * kKeys : 0;
+        // the lowest limit of this warp's rows decides whether a step needs the mask at all
+        int see_low = __reduce_min_sync(0xffffffffu, r < rows ? see : INT32_MAX);
+        float m = -INFINITY;  // the row's reference, in log2
+        uint64_t l0 = 0, l1 = 0;
+        const int steps = pc.u1 - pc.u0;
+        for (int j = 0; j < steps; ++j) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[half], ph_s, abort));
+          ph_s ^= 1;
+          if (!ok) break;
+          fence_after();
+          uint32_t x0[32], x1[32], x2[32], x3[32];
+          tmem_ld32(ts, x0);
+          tmem_ld32(ts + 32, x1);
+          tmem_ld32(ts + 64, x2);
+          tmem_ld32(ts + 96, x3);
+          tmem_wait_ld();
+          if (see_low < kKeys) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          t0 = fmaxf(t0, __uint_as_float(x0[i]));
-          t1 = fmaxf(t1, __uint_as_float(x1[i]));
-          t2 = fmaxf(t2, __uint_as_float(x2[i]));
-          t3 = fmaxf(t3, __uint_as_float(x3[i]));
-        }
-        const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
-        const bool raise = top > m + kRaise || (m == -INFINITY && top > m);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float by = raise ? exp2f(m - top) : 1.0f;  // 0 for the first reference
-          if (raise) m = top;
-          const uint64_t by2 = pk2(by, by);
-          l0 = mul2(l0, by2);
-          l1 = mul2(l1, by2);
-          if (j > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[half], (j - 1) & 1, abort));
-            if (!ok) break;
-            fence_after();
-#pragma unroll
-            for (int g = 0; g < D / 32; ++g) {
-              uint32_t o[32];
-              tmem_ld32(to + g * 32, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-              tmem_st32(to + g * 32, o);
+            for (int i = 0; i < 32; ++i) {
+              if (i >= see) x0[i] = 0xff800000u;
+              if (i + 32 >= see) x1[i] = 0xff800000u;
+              if (i + 64 >= see) x2[i] = 0xff800000u;
+              if (i + 96 >= see) x3[i] = 0xff800000u;
             }
           }
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const uint64_t sc2 = pk2(scale, scale), ref2 = pk2(-ref, -ref);
-        uint32_t p[32];
-        auto weigh = [&](const uint32_t (&x)[32], int at) {
+          see -= kKeys;
+          see_low -= kKeys;
+          float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const uint64_t y0 = fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, ref2);
-            const uint64_t y1 = fma2(pk2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), sc2, ref2);
-            const float e0 = ex2(lo2(y0)), e1 = ex2(hi2(y0)), e2 = ex2(lo2(y1)), e3 = ex2(hi2(y1));
-            l0 = add2(l0, pk2(e0, e1));
-            l1 = add2(l1, pk2(e2, e3));
-            p[at + i / 2] = bf2(e0, e1);
-            p[at + i / 2 + 1] = bf2(e2, e3);
+          for (int i = 0; i < 32; i += 2) {
+            t0 = max3(t0, x0[i], x0[i + 1]);
+            t1 = max3(t1, x1[i], x1[i + 1]);
+            t2 = max3(t2, x2[i], x2[i + 1]);
+            t3 = max3(t3, x3[i], x3[i + 1]);
           }
-        };
-        weigh(x0, 0);
-        weigh(x1, 16);
-        tmem_st32(ts, p);
-        weigh(x2, 0);
-        weigh(x3, 16);
-        tmem_st32(ts + 32, p);
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[half]);
-      }
-      if (ok && steps > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[half], (steps - 1) & 1, abort));
+          const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
+          const bool raise = top > m + kRaise || (m == -INFINITY && top > m);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float by = raise ? exp2f(m - top) : 1.0f;  // 0 for the first reference
+            if (raise) m = top;
+            const uint64_t by2 = pk2(by, by);
+            l0 = mul2(l0, by2);
+            l1 = mul2(l1, by2);
+            if (j > 0) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[half], ph_o ^ 1, abort));
+              if (!ok) break;
+              fence_after();
+#pragma unroll
+              for (int g = 0; g < D / 32; ++g) {
+                uint32_t o[32];
+                tmem_ld32(to + g * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                tmem_st32(to + g * 32, o);
+              }
+            }
+          }
+          ph_o ^= 1;  // past this step's second product
+          const float ref = m == -INFINITY ? 0.f : m;
+          const uint64_t sc2 = pk2(scale, scale), ref2 = pk2(-ref, -ref);
+          uint32_t p[32];
+          auto weigh = [&](const uint32_t (&x)[32], int at) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const uint64_t y0 = fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, ref2);
+              const uint64_t y1 = fma2(pk2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), sc2, ref2);
+              const float e0 = ex2(lo2(y0)), e1 = ex2(hi2(y0)), e2 = ex2(lo2(y1)), e3 = ex2(hi2(y1));
+              l0 = add2(l0, pk2(e0, e1));
+              l1 = add2(l1, pk2(e2, e3));
+              p[at + i / 2] = bf2(e0, e1);
+              p[at + i / 2 + 1] = bf2(e2, e3);
+            }
+          };
+          auto hand = [&](int part) {
+            tmem_st32(ts + part * 32, p);
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_full[half][part]);
+          };
+          weigh(x0, 0);
+          weigh(x1, 16);
+          hand(0);
+          weigh(x2, 0);
+          weigh(x3, 16);
+          hand(1);
+        }
+        if (!ok) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[half], ph_o ^ 1, abort));
+        if (!ok) break;
         fence_after();
-      }
-      if (ok) {
         const float sum = lo2(l0) + hi2(l0) + lo2(l1) + hi2(l1);
-        const int64_t row = int64_t(it.s.row0 + r / c.group) * qh + it.h * c.group + r % c.group;
+        const int64_t row = head + int64_t(r / c.group) * qh + r % c.group;
         const float inv = sum > 0.f ? 1.0f / sum : sum;
-        const int64_t at = int64_t(it.split) * c.total_q * qh + row;
+        const bool real = r < rows, whole = pc.whole;
+        const int64_t at = int64_t(pc.slot) * slot_rows + (r - pc.r0);
         if (real) {
-          if (a.splits > 1) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m, sum);
+          if (!whole) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m, sum);
           else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
         }
 #pragma unroll
         for (int g = 0; g < D / 32; ++g) {
           uint32_t o[32];
-          if (steps > 0) {
-            tmem_ld32(to + g * 32, o);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0u;
-          }
+          tmem_ld32(to + g * 32, o);
+          tmem_wait_ld();
           if (!real) {
-          } else if (a.splits > 1) {
+          } else if (!whole) {
             if (sum > 0.f) {
               float4* dst = reinterpret_cast<float4*>(a.part + at * D + g * 32);
 #pragma unroll
@@ -377,16 +594,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + g * 32);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+              uint32_t v[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                w[k] = bf2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                v[k] = bf2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+              dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
             }
           }
           __syncwarp();
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.piece_empty[i & 1]);
     }
   }
   fence_before();
@@ -399,26 +618,82 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && S.abort) flag(c.status, MP_STATUS_WAIT_TIMEOUT);
 }
 
+// One warp per row of a tile that was cut: joins the pieces' (m, l, sum) in their order.
 template <int D>
-cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
+__global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const int slot_rows) {
+  const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
+  const int i = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (cut.pieces == 0 || i >= cut.rows) return;
+  const int group = a.c.group, qh = a.c.kvh * group;
+  auto at = [&](int p) { return int64_t(p == 0 ? cut.slot : 2 * (int(blockIdx.x) + p)) * slot_rows + i; };
+  float m = -INFINITY;
+  for (int p = 0; p < cut.pieces; ++p) m = fmaxf(m, a.ml[at(p) * 2]);
+  float l = 0.f, o[D / 32];
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
+  for (int p = 0; p < cut.pieces; ++p) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.ml + at(p) * 2);
+    if (ml.y == 0.f) continue;
+    const float by = exp2f(ml.x - m);
+    l = fmaf(ml.y, by, l);
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) o[j] = fmaf(a.part[at(p) * D + j * 32 + lane], by, o[j]);
+  }
+  const int r = cut.r0 + i;
+  const int64_t row = cut.row + int64_t(r / group) * qh + r % group;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+    static_cast<__nv_bfloat16*>(a.out)[row * D + j * 32 + lane] = __float2bfloat16(o[j] * inv);
+}
+
+int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
+
+template <int D>
+cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
+  const CacheArgs& c = a.c;
   CUtensorMap mk, mv;
-  const int box = box_rows(a.c.table, a.c.page_size);
-  const uint64_t rows = uint64_t(a.c.n_pages) * a.c.kvh * a.c.page_size;
+  const int box = box_rows(c.table, c.page_size);
+  const uint64_t rows = uint64_t(c.n_pages) * c.kvh * c.page_size;
   if (!make_map(&mk, a.keys, D, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&mv, a.values, D, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<D>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t(a.c.max_q) * a.c.group + kRows - 1) / kRows;
-  k_chunk_tc<D><<<dim3(unsigned(tiles * a.splits), a.c.kvh, a.c.batch), kThreads, smem, st>>>(mk, mv, a, box);
+  const int ctas = chunk_tc_ctas(c.batch, c.kvh, c.group, c.max_q, c.max_kv);
+  const int slot_rows = slot_rows_of(c.group, c.max_q);
+  char* ws = static_cast<char*>(workspace);
+  a.cuts = ws;
+  ws += align256(uint64_t(ctas) * sizeof(Cut));
+  a.ml = reinterpret_cast<float*>(ws);
+  ws += align256(uint64_t(2 * ctas) * slot_rows * 8);
+  a.part = reinterpret_cast<float*>(ws);
+  for (int b = 0; b < c.batch; b += kGroup) {
+    k_chunk_tc<D><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
+    k_chunk_tc_join<D><<<dim3(ctas, (slot_rows + 7) / 8), 256, 0, st>>>(a, slot_rows);
+  }
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_tc(const ChunkArgs& a, cudaStream_t st) {
-  return a.c.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
+// One CTA per SM, or fewer when the limits leave fewer runs of units than that.
+int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv) {
+  const int64_t tiles = (int64_t(max_q) * group + kRows - 1) / kRows;
+  const double units = double(std::min(batch, kGroup)) * kvh * double(tiles) * ((max_kv + kKeys - 1) / kKeys);
+  return int(std::max(1.0, std::min(double(device_sm_count()), units / kMinRun + 1.0)));
+}
+
+uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv) {
+  const int group = c->q_heads / c->kv_heads, ctas = chunk_tc_ctas(c->batch, c->kv_heads, group, max_q, max_kv);
+  const uint64_t rows = uint64_t(2 * ctas) * slot_rows_of(group, max_q);
+  return align256(uint64_t(ctas) * sizeof(Cut)) + align256(rows * 8) + align256(rows * c->head_dim * 4);
+}
+
+cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st) {
+  return a.c.d == 128 ? launch<128>(a, workspace, st) : launch<64>(a, workspace, st);
 }
 
 }  // namespace mp
