@@ -248,62 +248,71 @@ def make_rotary(*, rot_dim: int, interleaved: bool = False, eps: float = 1e-6) -
     return mp_rotary(rot_dim, int(bool(interleaved)), eps, 0)
 
 
-class _Args:
-    """Device addresses of one call's tensors, each checked for its device, type, layout
-    and size: the kernels use the addresses as the configuration says."""
+_torch = None  # imported by the first call below
 
-    def __init__(self, first):
+
+def _device(first) -> int:
+    """Index of the device that a call's tensors are on: the current one, or the call is refused."""
+    global _torch
+    if _torch is None:
         import torch
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("tensor arguments must be CUDA tensors (device memory)")
-        self.device = first.device
-        if self.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors are on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
-        self.i32, self.f32, self.f64, self.u8 = torch.int32, torch.float32, torch.float64, torch.uint8
-        self.types = (torch.float32, torch.bfloat16)
-        self.current_stream = torch.cuda.current_stream
+        _torch = torch
+    if not isinstance(first, _torch.Tensor) or not first.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors (device memory)")
+    dev = first.get_device()
+    if dev != _torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_torch.cuda.current_device()}")
+    return dev
 
-    def __call__(self, name, x, dtype, numel, none=False):
-        if x is None:
-            if none:
-                return None
-            raise ValueError(f"{name} is needed")
-        if x.device != self.device:
-            raise ValueError(f"{name} is on {x.device}, not on {self.device}")
-        if x.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-        if not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous (dense row-major layout)")
-        if x.numel() < numel:
-            raise ValueError(f"{name} has {x.numel()} elements, the call uses {numel}")
-        return x.data_ptr()
 
-    def rows(self, name, x, dtype, rows, width):
-        """(address, row stride) of a [rows, heads, head_dim] tensor whose rows may lie apart."""
-        if x.device != self.device or x.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype} on {self.device}")
-        if x.dim() < 2 or x.shape[0] != rows or x.numel() != rows * width:
-            raise ValueError(f"{name} must have {rows} rows of {width} elements, got {tuple(x.shape)}")
-        stride = width if rows <= 1 else x.stride(0)  # one row has no stride of its own
-        inner = 1
-        for size, st in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-            if size != 1 and st != inner:
-                raise ValueError(f"{name}: the heads of a row must be dense")
-            inner *= size
-        return x.data_ptr(), stride
+def _arg(name, x, dtype, numel, dev):
+    """Device address of a tensor that the kernels use as the configuration says: its device,
+    type, layout and size are checked (this runs for every argument of a call that may take a
+    few microseconds, so the checks are the cheap ones and the words come after)."""
+    try:
+        if x.dtype is dtype and x.get_device() == dev and x.numel() >= numel and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{name} must be a CUDA tensor") from None
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, not on cuda:{dev}")
+    if x.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (dense row-major layout)")
+    raise ValueError(f"{name} has {x.numel()} elements, the call uses {numel}")
 
-    def stream(self, stream):
-        return self.current_stream().cuda_stream if stream is None else _stream(stream)
+
+def _opt(name, x, dtype, numel, dev):
+    return None if x is None else _arg(name, x, dtype, numel, dev)
+
+
+def _rows(name, x, dtype, rows, heads, d, dev):
+    """(address, row stride) of a [rows, heads, d] tensor whose rows may lie apart."""
+    if x.dtype is not dtype or x.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} on cuda:{dev}")
+    if tuple(x.shape) != (rows, heads, d):
+        raise ValueError(f"{name} must be {(rows, heads, d)}, got {tuple(x.shape)}")
+    stride, head, one = x.stride()
+    if one != 1 or (head != d and heads != 1):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return x.data_ptr(), (stride if rows > 1 else heads * d)  # one row has no stride of its own
+
+
+def _raw_stream(stream, dev):
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _pool_size(cfg: mp_cache_config) -> int:
     return cfg.n_pages * cfg.kv_heads * cfg.page_size * cfg.head_dim
 
 
-def _dtype_of(a: _Args, cfg: mp_cache_config):
-    if cfg.dtype not in (MP_DTYPE_F32, MP_DTYPE_BF16):
-        raise MagicPigError("mp_cache_config_check", MP_ERR_INVALID_ARG)
-    return a.types[cfg.dtype]
+def _dtype_of(cfg: mp_cache_config):
+    if cfg.dtype == MP_DTYPE_BF16:
+        return _torch.bfloat16
+    if cfg.dtype == MP_DTYPE_F32:
+        return _torch.float32
+    raise MagicPigError("mp_cache_config_check", MP_ERR_INVALID_ARG)
 
 
 def mp_cache_config_check(cfg: mp_cache_config) -> int:
@@ -313,19 +322,19 @@ def mp_cache_config_check(cfg: mp_cache_config) -> int:
 def mp_cache_append(cfg: mp_cache_config, rotary: mp_rotary, q, k, v, q_norm, k_norm, inv_freq, positions, cu_q, kv_len,
                     keys, values, page_table, q_out, status=None, stream=None) -> int:
     """Norms, rotation and cache write of the new tokens. q, k, v: [total_q, heads, head_dim], rows may lie apart."""
-    a = _Args(q)
-    dt = _dtype_of(a, cfg)
-    rows, d = q.shape[0], cfg.head_dim
-    qp, qs = a.rows("q", q, dt, rows, cfg.q_heads * d)
-    kp, ks = a.rows("k", k, dt, rows, cfg.kv_heads * d)
-    vp, vs = a.rows("v", v, dt, rows, cfg.kv_heads * d)
+    dev = _device(q)
+    dt, i32 = _dtype_of(cfg), _torch.int32
+    rows, d, hq, hk, batch, pool = q.shape[0], cfg.head_dim, cfg.q_heads, cfg.kv_heads, cfg.batch, _pool_size(cfg)
+    qp, qs = _rows("q", q, dt, rows, hq, d, dev)
+    kp, ks = _rows("k", k, dt, rows, hk, d, dev)
+    vp, vs = _rows("v", v, dt, rows, hk, d, dev)
     return _check("mp_cache_append", _lib.mp_cache_append(
-        cfg, rotary, qp, qs, kp, ks, vp, vs, a("q_norm", q_norm, dt, d, True), a("k_norm", k_norm, dt, d, True),
-        a("inv_freq", inv_freq, a.f64, rotary.rot_dim // 2, rotary.rot_dim == 0),
-        a("positions", positions, a.i32, rows, True), a("cu_q", cu_q, a.i32, cfg.batch + 1),
-        a("kv_len", kv_len, a.i32, cfg.batch), rows, a("keys", keys, dt, _pool_size(cfg)),
-        a("values", values, dt, _pool_size(cfg)), a("page_table", page_table, a.i32, cfg.batch * cfg.max_pages, True),
-        a("q_out", q_out, dt, rows * cfg.q_heads * d), a("status", status, a.i32, 1, True), a.stream(stream)))
+        cfg, rotary, qp, qs, kp, ks, vp, vs, _opt("q_norm", q_norm, dt, d, dev), _opt("k_norm", k_norm, dt, d, dev),
+        _opt("inv_freq", inv_freq, _torch.float64, rotary.rot_dim // 2, dev), _opt("positions", positions, i32, rows, dev),
+        _arg("cu_q", cu_q, i32, batch + 1, dev), _arg("kv_len", kv_len, i32, batch, dev), rows,
+        _arg("keys", keys, dt, pool, dev), _arg("values", values, dt, pool, dev),
+        _opt("page_table", page_table, i32, batch * cfg.max_pages, dev), _arg("q_out", q_out, dt, rows * hq * d, dev),
+        _opt("status", status, i32, 1, dev), _raw_stream(stream, dev)))
 
 
 def mp_chunk_workspace_bytes(cfg: mp_cache_config, total_q: int, max_q: int, max_kv: int) -> int:
@@ -337,29 +346,30 @@ def mp_chunk_workspace_bytes(cfg: mp_cache_config, total_q: int, max_q: int, max
 def mp_chunk_attention(cfg: mp_cache_config, q, cu_q, kv_len, max_q: int, max_kv: int, keys, values, page_table, out,
                        lse=None, workspace=None, status=None, stream=None) -> int:
     """Exact attention of the new tokens q [total_q, q_heads, head_dim] over their sequences' slots."""
-    a = _Args(q)
-    dt = _dtype_of(a, cfg)
-    rows, width, pool = q.shape[0], cfg.q_heads * cfg.head_dim, _pool_size(cfg)
+    dev = _device(q)
+    dt, i32 = _dtype_of(cfg), _torch.int32
+    rows, hq, batch, pool = q.shape[0], cfg.q_heads, cfg.batch, _pool_size(cfg)
+    n = rows * hq * cfg.head_dim
     return _check("mp_chunk_attention", _lib.mp_chunk_attention(
-        cfg, a("q", q, dt, rows * width), a("cu_q", cu_q, a.i32, cfg.batch + 1), a("kv_len", kv_len, a.i32, cfg.batch),
-        rows, max_q, max_kv, a("keys", keys, dt, pool), a("values", values, dt, pool),
-        a("page_table", page_table, a.i32, cfg.batch * cfg.max_pages, True), a("out", out, dt, rows * width),
-        a("lse", lse, a.f32, rows * cfg.q_heads, True), a("workspace", workspace, a.u8, 0, True),
-        0 if workspace is None else workspace.numel(), a("status", status, a.i32, 1, True), a.stream(stream)))
+        cfg, _arg("q", q, dt, n, dev), _arg("cu_q", cu_q, i32, batch + 1, dev), _arg("kv_len", kv_len, i32, batch, dev), rows,
+        max_q, max_kv, _arg("keys", keys, dt, pool, dev), _arg("values", values, dt, pool, dev),
+        _opt("page_table", page_table, i32, batch * cfg.max_pages, dev), _arg("out", out, dt, n, dev),
+        _opt("lse", lse, _torch.float32, rows * hq, dev), _opt("workspace", workspace, _torch.uint8, 0, dev),
+        0 if workspace is None else workspace.numel(), _opt("status", status, i32, 1, dev), _raw_stream(stream, dev)))
 
 
 def mp_cache_weights(cfg: mp_cache_config, q, lse, cu_q, kv_len, max_q: int, max_kv: int, keys, page_table, scores,
                      status=None, stream=None) -> int:
     """Add the attention that the new tokens paid to every slot to scores [batch, kv_heads, max_pages * page_size]."""
-    a = _Args(q)
-    dt = _dtype_of(a, cfg)
-    rows = q.shape[0]
+    dev = _device(q)
+    dt, i32, f32 = _dtype_of(cfg), _torch.int32, _torch.float32
+    rows, hq, batch = q.shape[0], cfg.q_heads, cfg.batch
     return _check("mp_cache_weights", _lib.mp_cache_weights(
-        cfg, a("q", q, dt, rows * cfg.q_heads * cfg.head_dim), a("lse", lse, a.f32, rows * cfg.q_heads),
-        a("cu_q", cu_q, a.i32, cfg.batch + 1), a("kv_len", kv_len, a.i32, cfg.batch), rows, max_q, max_kv,
-        a("keys", keys, dt, _pool_size(cfg)), a("page_table", page_table, a.i32, cfg.batch * cfg.max_pages, True),
-        a("scores", scores, a.f32, cfg.batch * cfg.kv_heads * cfg.max_pages * cfg.page_size),
-        a("status", status, a.i32, 1, True), a.stream(stream)))
+        cfg, _arg("q", q, dt, rows * hq * cfg.head_dim, dev), _arg("lse", lse, f32, rows * hq, dev),
+        _arg("cu_q", cu_q, i32, batch + 1, dev), _arg("kv_len", kv_len, i32, batch, dev), rows, max_q, max_kv,
+        _arg("keys", keys, dt, _pool_size(cfg), dev), _opt("page_table", page_table, i32, batch * cfg.max_pages, dev),
+        _arg("scores", scores, f32, batch * cfg.kv_heads * cfg.max_pages * cfg.page_size, dev),
+        _opt("status", status, i32, 1, dev), _raw_stream(stream, dev)))
 
 
 def mp_evict_workspace_bytes(cfg: mp_cache_config, max_kv: int, budget: int) -> int:
@@ -372,18 +382,19 @@ def mp_cache_evict(cfg: mp_cache_config, dst_cfg: mp_cache_config, keys, values,
                    n_sink: int, window: int, budget: int, dst_keys, dst_values, dst_page_table, dst_scores, dst_len,
                    kept, workspace, status=None, stream=None) -> int:
     """Keep sinks, window and the highest-scored slots up to the budget; the kept rows move to the destination."""
-    a = _Args(keys)
-    dt = _dtype_of(a, cfg)
-    pool, dpool, units = _pool_size(cfg), _pool_size(dst_cfg), cfg.batch * cfg.kv_heads
+    dev = _device(keys)
+    dt, i32, f32 = _dtype_of(cfg), _torch.int32, _torch.float32
+    pool, dpool, batch, units = _pool_size(cfg), _pool_size(dst_cfg), cfg.batch, cfg.batch * cfg.kv_heads
     return _check("mp_cache_evict", _lib.mp_cache_evict(
-        cfg, dst_cfg, a("keys", keys, dt, pool), a("values", values, dt, pool),
-        a("page_table", page_table, a.i32, cfg.batch * cfg.max_pages, True), a("kv_len", kv_len, a.i32, cfg.batch), max_kv,
-        a("scores", scores, a.f32, units * cfg.max_pages * cfg.page_size), n_sink, window, budget,
-        a("dst_keys", dst_keys, dt, dpool), a("dst_values", dst_values, dt, dpool),
-        a("dst_page_table", dst_page_table, a.i32, cfg.batch * dst_cfg.max_pages, True),
-        a("dst_scores", dst_scores, a.f32, units * dst_cfg.max_pages * dst_cfg.page_size, True),
-        a("dst_len", dst_len, a.i32, cfg.batch), a("kept", kept, a.i32, units * max(0, budget), True),
-        a("workspace", workspace, a.u8, 0), workspace.numel(), a("status", status, a.i32, 1, True), a.stream(stream)))
+        cfg, dst_cfg, _arg("keys", keys, dt, pool, dev), _arg("values", values, dt, pool, dev),
+        _opt("page_table", page_table, i32, batch * cfg.max_pages, dev), _arg("kv_len", kv_len, i32, batch, dev), max_kv,
+        _arg("scores", scores, f32, units * cfg.max_pages * cfg.page_size, dev), n_sink, window, budget,
+        _arg("dst_keys", dst_keys, dt, dpool, dev), _arg("dst_values", dst_values, dt, dpool, dev),
+        _opt("dst_page_table", dst_page_table, i32, batch * dst_cfg.max_pages, dev),
+        _opt("dst_scores", dst_scores, f32, units * dst_cfg.max_pages * dst_cfg.page_size, dev),
+        _arg("dst_len", dst_len, i32, batch, dev), _opt("kept", kept, i32, units * max(0, budget), dev),
+        _arg("workspace", workspace, _torch.uint8, 0, dev), workspace.numel(), _opt("status", status, i32, 1, dev),
+        _raw_stream(stream, dev)))
 
 
 def mp_get_status(tables, stream=None) -> int:

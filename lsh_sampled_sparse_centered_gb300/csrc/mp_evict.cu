@@ -3,15 +3,27 @@
 //
 // Selection orders the slots between the sinks and the window by their scores as unsigned
 // keys (the order of the floats; both zeros alike, NaN lowest). The key of the want-th
-// highest score is found by radix selection, four passes of 8 bits over the scores; slots
-// above it stay, and of those equal to it the lowest ones that are still wanted.
-// The copy reads and writes the kept rows once, in 16-byte vectors.
+// highest score is found by radix selection in digits of 12, 10 and 10 bits; slots above it
+// stay, and of those equal to it the lowest ones that are still wanted. A cluster of up to
+// eight CTAs shares a head: each counts the digits of its part of the slots, all read the
+// others' counts through distributed shared memory and find the digit for themselves. The
+// first digit has 12 bits (sign, exponent, three of the mantissa) so that scores of like
+// size spread over many counters. A part of the scores is read once into shared memory
+// (parts of more than kStage slots are read again from L2 for each digit).
+// The copy reads and writes the kept rows once, in 16-byte vectors, bound by memory.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
 #include "mp_cache.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int kSel = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kSel = 1024, kWarps = kSel / 32;
+constexpr int kStage = 32768;  // slots of a CTA that shared memory holds
 
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0u;
@@ -19,22 +31,81 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);  // -inf -> 0x007fffff > 0
 }
 
+struct alignas(16) SelectSmem {
+  uint32_t hist[4096 + 1024 + 1024];  // one set of counters per digit: no pass waits to reuse another's
+  uint32_t warp_sum[kWarps];
+  int2 warp_count[kWarps];  // slots above the threshold key and slots equal to it, of each warp
+  int2 count;               // of the CTA
+  uint32_t digit;
+  int left;
+};
+
+// The digit in which the want-th highest counted key lies, and how many are still wanted
+// in it: a suffix sum over the cluster's counters, every thread with its own run of bins.
+template <int BITS>
+__device__ __forceinline__ void find_digit(SelectSmem& S, uint32_t* hist, cg::cluster_group& cluster, int want) {
+  constexpr int BINS = 1 << BITS, PER = BINS / kSel;  // bins of a thread, 4 or 1
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ranks = int(cluster.num_blocks());
+  const int first = BINS - (tid + 1) * PER;  // the highest bins belong to thread 0
+  uint32_t n[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) n[i] = 0;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    if (r >= ranks) continue;
+    const uint32_t* other = cluster.map_shared_rank(hist, r) + first;
+    if (PER == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(other);
+      n[0] += v.x;
+      n[PER > 1 ? 1 : 0] += PER > 1 ? v.y : 0;
+      n[PER > 2 ? 2 : 0] += PER > 2 ? v.z : 0;
+      n[PER > 3 ? 3 : 0] += PER > 3 ? v.w : 0;
+    } else {
+      n[0] += *other;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sum += n[i];
+  uint32_t pre = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) S.warp_sum[warp] = pre;
+  __syncthreads();
+  uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? S.warp_sum[lane] : 0u) + pre - sum;
+  // the thread whose run crosses `want` (there is one: at least `want` keys were counted)
+  if (before < uint32_t(want) && before + sum >= uint32_t(want)) {
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i) {
+      if (before < uint32_t(want) && before + n[i] >= uint32_t(want)) {
+        S.digit = uint32_t(first + i);
+        S.left = want - int(before);
+      }
+      before += n[i];
+    }
+  }
+  __syncthreads();
+}
+
 __global__ void __launch_bounds__(kSel) k_evict_select(const EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ int warp_sum[2][32];
-  __shared__ uint32_t sh_prefix;
-  __shared__ int sh_want;
+  __shared__ SelectSmem S;
+  extern __shared__ float stage[];
+  cg::cluster_group cluster = cg::this_cluster();
   const CacheArgs& c = a.c;
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  const int h = blockIdx.x / ranks, b = blockIdx.y;
   const int n = seq_of(c, b).n;
   const int64_t unit = int64_t(b) * c.kvh + h;
   const float* sc = a.scores + unit * (int64_t(c.cols) * c.page_size);
   int32_t* kept = a.kept + unit * a.budget;
   float* ds = a.dst_scores ? a.dst_scores + unit * (int64_t(a.dst_cols) * a.dst_page_size) : nullptr;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (h == 0 && tid == 0) a.dst_len[b] = min(n, a.budget);
-  if (n <= a.budget) {
-    for (int i = tid; i < n; i += kSel) {
+  if (h == 0 && rank == 0 && tid == 0) a.dst_len[b] = min(n, a.budget);
+  if (n <= a.budget) {  // the same for the whole cluster
+    for (int i = rank * kSel + tid; i < n; i += ranks * kSel) {
       kept[i] = i;
       if (ds) ds[i] = sc[i];
     }
@@ -42,104 +113,159 @@ __global__ void __launch_bounds__(kSel) k_evict_select(const EvictArgs a) {
   }
   const int lo = a.n_sink, hi = n - a.window;
   int want = a.budget - a.n_sink - a.window;  // < hi - lo
-  uint32_t prefix = 0;
+  uint32_t prefix = 0xffffffffu;              // no score has this key: nothing between lo and hi stays
+  // this CTA's slots [p0, p1), a whole number of 32 per warp
+  const int per = ((n + ranks * kWarps - 1) / (ranks * kWarps) + 31) & ~31;
+  const int p0 = min(n, rank * kWarps * per), p1 = min(n, p0 + kWarps * per);
+  const bool staged = p1 - p0 <= kStage;
+  for (int i = tid; i < 4096 + 1024 + 1024; i += kSel) S.hist[i] = 0;
+  if (staged) {
+#pragma unroll 8
+    for (int i = p0 + tid; i < p1; i += kSel) stage[i - p0] = sc[i];
+  }
+  __syncthreads();
+  const float* mine = staged ? stage : sc + p0;
   if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int i = lo + tid; i < hi; i += kSel) {
-        const uint32_t k = order_key(sc[i]);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    prefix = 0;
+    const int q0 = max(lo, p0), q1 = min(hi, p1);
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      const int bits = d == 0 ? 12 : 10, shift = d == 0 ? 20 : (d == 1 ? 10 : 0);
+      uint32_t* hist = S.hist + (d == 0 ? 0 : (d == 1 ? 4096 : 4096 + 1024));
+      const uint32_t mask = d == 0 ? 0u : 0xffffffffu << (shift + bits);
+#pragma unroll 4
+      for (int i = q0 + tid; i < q1; i += kSel) {
+        const uint32_t k = order_key(mine[i - p0]);
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
       }
-      __syncthreads();
-      if (tid == 0) {
-        int left = want;
-        int bin = 255;
-        while (bin > 0 && int(hist[bin]) < left) left -= int(hist[bin--]);
-        sh_prefix = prefix | (uint32_t(bin) << shift);
-        sh_want = left;
-      }
-      __syncthreads();
-      prefix = sh_prefix;
-      want = sh_want;
-      __syncthreads();
+      cluster.sync();
+      if (d == 0) find_digit<12>(S, hist, cluster, want);
+      else find_digit<10>(S, hist, cluster, want);
+      prefix |= S.digit << shift;
+      want = S.left;
     }
   }
-  // keep: every key above `prefix` and the first `want` keys equal to it (none at all when
-  // nothing is wanted between the sinks and the window)
-  const bool any = a.budget > a.n_sink + a.window;
-  int base = 0, ties = 0;  // kept and tied slots before this round
-  for (int i0 = 0; i0 < n; i0 += kSel) {
-    const int i = i0 + tid;
-    bool keep = false, tie = false;
-    float x = 0.f;
-    if (i < n) {
-      x = sc[i];
-      if (i < lo || i >= hi) keep = true;
-      else if (any) {
-        const uint32_t k = order_key(x);
-        keep = k > prefix;
-        tie = k == prefix;
-      }
-    }
-    const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) warp_sum[0][warp] = __popc(tb);
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < 32; ++w) {
-      before += w < warp ? warp_sum[0][w] : 0;
-      all += warp_sum[0][w];
-    }
-    if (tie && ties + before + __popc(tb & ((1u << lane) - 1u)) < want) keep = true;
-    ties += all;
-    const uint32_t kb = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) warp_sum[1][warp] = __popc(kb);
-    __syncthreads();
-    before = 0;
-    all = 0;
-    for (int w = 0; w < 32; ++w) {
-      before += w < warp ? warp_sum[1][w] : 0;
-      all += warp_sum[1][w];
-    }
-    if (keep) {
-      const int at = base + before + __popc(kb & ((1u << lane) - 1u));
-      kept[at] = i;
+  // Each warp owns a run of slots: counts first, then the places. Slots above the threshold
+  // (sinks and window among them) all stay, the first `want` of those equal to it too.
+  const int i0 = min(n, p0 + warp * per), i1 = min(n, i0 + per);
+  auto look = [&](int i, float& x, bool& above, bool& tie) {
+    above = tie = false;
+    x = 0.f;
+    if (i >= i1) return;
+    x = mine[i - p0];
+    const uint32_t k = order_key(x);
+    const bool sure = i < lo || i >= hi;
+    above = sure || k > prefix;
+    tie = !sure && k == prefix;
+  };
+  int above_n = 0, tie_n = 0;
+#pragma unroll 4
+  for (int i = i0; i < i1; i += 32) {
+    float x;
+    bool above, tie;
+    look(i + lane, x, above, tie);
+    above_n += __popc(__ballot_sync(0xffffffffu, above));
+    tie_n += __popc(__ballot_sync(0xffffffffu, tie));
+  }
+  if (lane == 0) S.warp_count[warp] = make_int2(above_n, tie_n);
+  __syncthreads();
+  if (warp == 0) {
+    const int2 v = S.warp_count[lane];
+    const int2 all = make_int2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
+    if (lane == 0) S.count = all;
+  }
+  cluster.sync();
+  // what the warps and CTAs before this one hold
+  int2 v = lane < warp ? S.warp_count[lane] : make_int2(0, 0);
+  if (lane < rank) {
+    const int2 o = *cluster.map_shared_rank(&S.count, lane);
+    v.x += o.x;
+    v.y += o.y;
+  }
+  int above_before = __reduce_add_sync(0xffffffffu, v.x), tie_before = __reduce_add_sync(0xffffffffu, v.y);
+  const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int i = i0; i < i1; i += 32) {
+    float x;
+    bool above, tie;
+    look(i + lane, x, above, tie);
+    const uint32_t tb = __ballot_sync(0xffffffffu, tie), ab = __ballot_sync(0xffffffffu, above);
+    const int t = tie_before + __popc(tb & lower);  // ties before this slot
+    if (above || (tie && t < want)) {
+      const int at = above_before + __popc(ab & lower) + min(t, want);
+      kept[at] = i + lane;
       if (ds) ds[at] = x;
     }
-    base += all;
+    above_before += __popc(ab);
+    tie_before += __popc(tb);
   }
+  cluster.sync();  // no CTA leaves while others read its counts
 }
 
-// One 16-byte vector of K and of V per thread; rows of a (sequence, KV head) in order.
-template <int ROW>  // vectors per row
+// ROW 16-byte vectors per row, one lane each, kRowsEach rows of K and V per lane so that
+// enough loads are in flight.
+constexpr int kRowsEach = 4;
+
+template <int ROW>
 __global__ void __launch_bounds__(256) k_evict_gather(const EvictArgs a) {
+  constexpr int GROUPS = 256 / ROW;
   const CacheArgs& c = a.c;
   const int h = blockIdx.y, b = blockIdx.z;
   const int m = min(seq_of(c, b).n, a.budget);
-  const int j = blockIdx.x * (256 / ROW) + threadIdx.x / ROW, e = threadIdx.x % ROW;
-  if (j >= m) return;
-  const int32_t src = a.kept[(int64_t(b) * c.kvh + h) * a.budget + j];
-  const int col = j / a.dst_page_size;
-  const int p = page_at(a.dst_table, a.dst_cols, a.dst_n_pages, b, col, c.status);
-  if (p < 0) return;
-  const int64_t from = slot_read(c, b, h, src) / c.d * ROW + e;
-  const int64_t to = ((int64_t(p) * c.kvh + h) * a.dst_page_size + (j - col * a.dst_page_size)) * ROW + e;
-  static_cast<uint4*>(a.dst_keys)[to] = static_cast<const uint4*>(a.keys)[from];
-  static_cast<uint4*>(a.dst_values)[to] = static_cast<const uint4*>(a.values)[from];
+  const int j0 = blockIdx.x * (GROUPS * kRowsEach) + threadIdx.x / ROW, e = threadIdx.x % ROW;
+  if (j0 >= m) return;
+  const int32_t* kept = a.kept + (int64_t(b) * c.kvh + h) * a.budget;
+  const uint4 *keys = static_cast<const uint4*>(a.keys), *values = static_cast<const uint4*>(a.values);
+  int64_t to[kRowsEach];
+  uint4 k[kRowsEach], v[kRowsEach];
+#pragma unroll
+  for (int i = 0; i < kRowsEach; ++i) {
+    const int j = j0 + i * GROUPS;
+    to[i] = -1;
+    if (j >= m) continue;
+    const int col = j / a.dst_page_size;
+    const int p = page_at(a.dst_table, a.dst_cols, a.dst_n_pages, b, col, c.status);
+    const int64_t from = slot_read(c, b, h, kept[j]) / c.d * ROW + e;
+    k[i] = __ldcs(keys + from);
+    v[i] = __ldcs(values + from);
+    if (p >= 0) to[i] = ((int64_t(p) * c.kvh + h) * a.dst_page_size + (j - col * a.dst_page_size)) * ROW + e;
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsEach; ++i)
+    if (to[i] >= 0) {
+      static_cast<uint4*>(a.dst_keys)[to[i]] = k[i];
+      static_cast<uint4*>(a.dst_values)[to[i]] = v[i];
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st) {
-  k_evict_select<<<dim3(a.c.kvh, a.c.batch), kSel, 0, st>>>(a);
-  return cudaGetLastError();
+  // about 4096 slots per CTA; clusters of up to eight are always schedulable
+  int ranks = 1;
+  while (ranks < 8 && int64_t(ranks) * 4096 < a.c.max_kv) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.c.kvh * ranks, a.c.batch);
+  cfg.blockDim = dim3(kSel);
+  const int64_t part = ((int64_t(a.c.max_kv) + ranks * kWarps - 1) / (ranks * kWarps) + 31) / 32 * 32 * kWarps;
+  cfg.dynamicSmemBytes = size_t(std::min<int64_t>(part, kStage)) * 4;
+  cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kStage * 4);
+  if (e != cudaSuccess) return e;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_evict_select, a);
 }
 
 cudaError_t launch_evict_gather(const EvictArgs& a, int dtype, cudaStream_t st) {
   const int row = a.c.d * (dtype == MP_DTYPE_BF16 ? 2 : 4) / 16;
   const int most = a.budget < a.c.max_kv ? a.budget : a.c.max_kv;
-  const dim3 grid((most + 256 / row - 1) / (256 / row), a.c.kvh, a.c.batch);
+  const int per = 256 / row * kRowsEach;
+  const dim3 grid((most + per - 1) / per, a.c.kvh, a.c.batch);
   if (row == 8) k_evict_gather<8><<<grid, 256, 0, st>>>(a);
   else if (row == 16) k_evict_gather<16><<<grid, 256, 0, st>>>(a);
   else k_evict_gather<32><<<grid, 256, 0, st>>>(a);

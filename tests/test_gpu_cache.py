@@ -320,6 +320,8 @@ APPEND = [
     ("f32", 4, 2, 128, 16, [1, 3, 0, 20], [1, 50, 9, 20], 128, False, True),
     ("f32", 6, 2, 64, 0, [70, 1], [70, 200], 8, False, True),
     ("f32", 7, 1, 64, 32, [33], [40], 62, True, False),
+    ("bf16", 3, 1, 64, 16, [1225, 0, 6, 3], [1300, 5, 6, 200], 64, False, True),  # enough rows for several tokens a block
+    ("f32", 1, 1, 128, 64, [1250], [1250], 128, True, True),
 ]
 
 
@@ -401,6 +403,7 @@ EVICT = [
     ("bf16", 2, 64, 32, 32, [513, 77], 1, 0, 0, "ties"),
     ("bf16", 2, 64, 16, 16, [333], 100, 0, 1, "odd"),
     ("bf16", 1, 64, 0, 0, [40000], 33000, 4, 64, "ties"),
+    ("bf16", 1, 64, 0, 0, [300001], 2000, 4, 64, "normal"),          # more scores than shared memory holds
 ]
 
 
