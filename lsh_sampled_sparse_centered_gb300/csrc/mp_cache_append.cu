@@ -6,15 +6,18 @@
 // integer position modulo 2^64 is the exact fraction of the turn that the angle leaves
 // (error 2^-53 of a turn per position), so far positions cost no more than near ones.
 //
-// Memory bound: (q_heads + 2 kv_heads) * d values in and out per token. 16-byte vectors,
-// d * size / 16 lanes per head; the sines and cosines are shared by a token's heads
-// through shared memory (computing them per head would cost more than the traffic).
+// Memory bound: (q_heads + 2 kv_heads) * d values in and out per token. A warp takes whole
+// heads of one token, d * size / 16 lanes with a 16-byte vector each per head. What it does
+// once per token (slot, angles, the factors of its elements) costs about as many
+// instructions as eight heads, so a warp takes all heads of its token where there are
+// tokens enough, and a part of them where there are few.
 #include "mp_cache.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 4;  // independent of each other
+constexpr int kBatch = 4;  // vectors of a lane in flight
 
 template <typename T>
 struct Vec {
@@ -48,147 +51,126 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
   return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
-// TOK tokens of a CTA; kBatch vectors of a lane are in flight at a time, the first of them
-// while the tokens' slots and angles are worked out.
-constexpr int kBatch = 4;
-
-template <typename T, int D, int TOK>
-__global__ void __launch_bounds__(kThreads) k_cache_append(const AppendArgs a) {
-  constexpr int V = Vec<T>::N, TPH = D / V, GROUPS = kThreads / TPH;
-  __shared__ float2 cs[TOK][D / 2];  // cosine and sine of each pair's angle
-  __shared__ int64_t dst[TOK];       // element offset of the slot's row of KV head 0, or -1
-  __shared__ int64_t pos[TOK];       // where the token stands
-  __shared__ int live[TOK];          // the row belongs to a sequence
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a, const int parts) {
+  constexpr int V = Vec<T>::N, TPH = D / V, HPW = 32 / TPH;  // heads of a warp at a time
+  __shared__ alignas(16) float cosine[kWarps][D / 2], sine[kWarps][D / 2];  // of each pair's angle
   const CacheArgs& c = a.c;
-  const int row0 = blockIdx.x * TOK, toks = min(TOK, c.total_q - row0);
+  const int warp = threadIdx.x >> 5, l32 = threadIdx.x & 31, lane = l32 % TPH, e0 = lane * V;
+  const int64_t w = int64_t(blockIdx.x) * kWarps + warp;
+  const int64_t r = w / parts;
+  const int h0 = int(w - r * parts) * HPW + l32 / TPH, step = parts * HPW;  // this lane's heads
+  if (r >= c.total_q) return;
   const int half = a.rot / 2;
-  const int lane = threadIdx.x % TPH, e0 = lane * V, group = threadIdx.x / TPH;
-  const int qh = c.kvh * c.group, heads = qh + 2 * c.kvh, items = toks * heads;
+  const int qh = c.kvh * c.group;
 
-  auto source = [&](int i) -> const uint4* {
-    const int tok = TOK == 1 ? 0 : i / heads, h = i - tok * heads;
-    const int64_t r = row0 + tok;
-    const T* p = h < qh ? static_cast<const T*>(a.q) + r * a.q_stride + int64_t(h) * D
-                        : (h < qh + c.kvh ? static_cast<const T*>(a.k) + r * a.k_stride + int64_t(h - qh) * D
-                                          : static_cast<const T*>(a.v) + r * a.v_stride + int64_t(h - qh - c.kvh) * D);
-    return reinterpret_cast<const uint4*>(p + e0);
-  };
-  uint4 u[kBatch];
-#pragma unroll
-  for (int k = 0; k < kBatch; ++k) {
-    const int i = group + k * GROUPS;
-    u[k] = i < items ? __ldcs(source(i)) : make_uint4(0, 0, 0, 0);
+  const int b = seq_at(c, int(r));
+  if (b < 0) return;  // a row outside every sequence
+  const Seq s = seq_of(c, b);
+  if (r < s.row0 || r >= s.row0 + s.m) return;
+  const int slot = s.n - s.m + int(r - s.row0);
+  int64_t dst = -1;  // element offset of the slot's row of KV head 0
+  if (slot >= 0 && slot < int64_t(c.cols) * c.page_size) {
+    const int col = slot / c.page_size;
+    const int p = page_at(c.table, c.cols, c.n_pages, b, col, c.status);
+    if (p >= 0) dst = (int64_t(p) * c.kvh * c.page_size + (slot - col * c.page_size)) * D;
+  } else if (l32 == 0) {
+    flag(c.status, MP_STATUS_BAD_LENGTH);
   }
-  uint4 gq = make_uint4(0, 0, 0, 0), gk = gq;
-  if (a.q_norm) gq = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q_norm) + e0);
-  if (a.k_norm) gk = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_norm) + e0);
-
-  if (int(threadIdx.x) < toks) {
-    const int t = threadIdx.x, r = row0 + t;
-    const int b = seq_at(c, r);
-    int64_t at = -1;
-    int slot = -1;
-    bool in = false;
-    if (b >= 0) {
-      const Seq s = seq_of(c, b);
-      in = r >= s.row0 && r < s.row0 + s.m;
-      slot = s.n - s.m + (r - s.row0);
-      if (in && slot >= 0 && slot < int64_t(c.cols) * c.page_size) {
-        const int col = slot / c.page_size;
-        const int p = page_at(c.table, c.cols, c.n_pages, b, col, c.status);
-        if (p >= 0) at = (int64_t(p) * c.kvh * c.page_size + (slot - col * c.page_size)) * D;
-      } else if (in) {
-        flag(c.status, MP_STATUS_BAD_LENGTH);
-      }
-    }
-    dst[t] = at;
-    live[t] = in;
-    pos[t] = a.positions ? a.positions[r] : slot;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < half; i += kThreads) {
+  const int64_t pos = a.positions ? a.positions[r] : slot;
+  for (int i = l32; i < half; i += 32) {
     const double turns = a.inv_freq[i] * 0.15915494309189533577;  // 1 / 2 pi
-    const uint64_t step = static_cast<uint64_t>((turns - floor(turns)) * 18446744073709551616.0);
-    for (int t = 0; t < toks; ++t) {
-      const uint64_t phase = static_cast<uint64_t>(pos[t]) * step + 0x80000000ull;
-      float sn, cn;
-      sincospif(float(int32_t(uint32_t(phase >> 32))) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31 half turns
-      cs[t][i] = make_float2(cn, sn);
-    }
+    const uint64_t per = static_cast<uint64_t>((turns - floor(turns)) * 18446744073709551616.0);
+    const uint64_t phase = static_cast<uint64_t>(pos) * per + 0x80000000ull;
+    sincospif(float(int32_t(uint32_t(phase >> 32))) * 4.656612873077393e-10f, &sine[warp][i], &cosine[warp][i]);  // 2^-31 half turns
   }
-  __syncthreads();
+  __syncwarp();
 
-  const int64_t head_stride = int64_t(c.page_size) * D;
   // the partner half of a split rotation sits half / V lanes away
   const bool first = e0 < half, turns = e0 < a.rot;
-  const int partner = (threadIdx.x & 31) + (a.interleaved || !turns ? 0 : (first ? half / V : -(half / V)));
-  for (int base = group; base - group < items; base += kBatch * GROUPS) {
-    if (base != group) {
+  const int away = a.interleaved || !turns ? 0 : (first ? half / V : -(half / V));
+  const int64_t head_stride = int64_t(c.page_size) * D;
+
+  // A lane turns the same elements of every head, so norm and rotation of its elements are
+  // one sum with the same factors for all query heads, and others for all key heads:
+  //   y_i = r (x_i own_i + x_partner other_i), r the inverse root (1 without a norm),
+  //   own_i = w_i cos, other_i = -+ w_partner sin.
+  auto turn_heads = [&](const T* src, const void* norm, int heads, T* to, int64_t to_stride) {
+    float own[V], other[V];
+    {
+      float g[V], gp[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) g[j] = gp[j] = 1.f;
+      if (norm) {
+        unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(norm) + e0), g);
+        unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(norm) + e0 + away * V), gp);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float cn = 1.f, sn = 0.f;
+        if (a.interleaved ? e0 + j < a.rot : turns) {
+          const int at = a.interleaved ? (e0 + j) / 2 : (first ? e0 + j : e0 + j - half);
+          cn = cosine[warp][at];
+          sn = (a.interleaved ? (j & 1) == 0 : first) ? -sine[warp][at] : sine[warp][at];
+        }
+        own[j] = g[j] * cn;
+        other[j] = (a.interleaved ? g[j ^ 1] : gp[j]) * sn;
+      }
+    }
+    for (int hb = h0; hb - h0 < heads; hb += kBatch * step) {
+      uint4 u[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int i = base + k * GROUPS;
-        u[k] = i < items ? __ldcs(source(i)) : make_uint4(0, 0, 0, 0);
+        const int h = hb + k * step;
+        u[k] = h < heads ? __ldcs(reinterpret_cast<const uint4*>(src + int64_t(h) * D + e0)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int h = hb + k * step;
+        if (h - h0 >= heads) break;  // the same for the whole warp
+        float x[V], y[V], z[V];
+        unpack(u[k], x);
+        if (a.interleaved) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) y[j] = x[j ^ 1];
+        } else {
+          uint4 o;
+          o.x = __shfl_sync(0xffffffffu, u[k].x, l32 + away);
+          o.y = __shfl_sync(0xffffffffu, u[k].y, l32 + away);
+          o.z = __shfl_sync(0xffffffffu, u[k].z, l32 + away);
+          o.w = __shfl_sync(0xffffffffu, u[k].w, l32 + away);
+          unpack(o, y);
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+        for (int i = TPH / 2; i > 0; i >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, i);
+        const float rs = norm ? rsqrtf(ss * (1.0f / D) + a.eps) : 1.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) z[j] = rs * fmaf(x[j], own[j], y[j] * other[j]);
+        if (h < heads) *reinterpret_cast<uint4*>(to + h * to_stride + e0) = pack(z);
       }
     }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = base + k * GROUPS;
-      const int tok = TOK == 1 ? 0 : min(i / heads, TOK - 1), h = i - tok * heads;
-      const int kind = h < qh ? 0 : (h < qh + c.kvh ? 1 : 2);  // query, key, value
-      float x[V], y[V];
-      unpack(u[k], x);
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-      for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (kind == 0 ? a.q_norm != nullptr : a.k_norm != nullptr) {
-        const float rs = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        float g[V];
-        unpack(kind == 0 ? gq : gk, g);
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = x[j] * rs * g[j];
-      }
-      if (a.interleaved) {
-#pragma unroll
-        for (int j = 0; j < V; j += 2) {
-          if (e0 + j < a.rot) {
-            const float2 t = cs[tok][(e0 + j) / 2];
-            const float x0 = x[j], x1 = x[j + 1];
-            x[j] = x0 * t.x - x1 * t.y;
-            x[j + 1] = x1 * t.x + x0 * t.y;
-          }
-        }
-      } else if (half > 0) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], partner);
-        if (turns) {
-          const float4* t4 = reinterpret_cast<const float4*>(&cs[tok][first ? e0 : e0 - half]);
-#pragma unroll
-          for (int j = 0; j < V; j += 2) {
-            const float4 t = t4[j / 2];
-            x[j] = first ? x[j] * t.x - y[j] * t.y : x[j] * t.x + y[j] * t.y;
-            x[j + 1] = first ? x[j + 1] * t.z - y[j + 1] * t.w : x[j + 1] * t.z + y[j + 1] * t.w;
-          }
-        }
-      }
-      if (i >= items || !live[tok]) continue;
-      T* to;
-      if (kind == 0) to = static_cast<T*>(a.q_out) + (int64_t(row0 + tok) * qh + h) * D;
-      else if (dst[tok] < 0) continue;
-      else to = static_cast<T*>(kind == 1 ? a.keys : a.values) + dst[tok] + (h - qh - (kind == 1 ? 0 : c.kvh)) * head_stride;
-      *reinterpret_cast<uint4*>(to + e0) = kind == 2 ? u[k] : pack(x);
-    }
-  }
+  };
+  turn_heads(static_cast<const T*>(a.q) + r * a.q_stride, a.q_norm, qh, static_cast<T*>(a.q_out) + r * qh * D, D);
+  if (dst < 0) return;  // the same for the whole warp
+  const T* v = static_cast<const T*>(a.v) + r * a.v_stride + e0;
+  for (int h = h0; h < c.kvh; h += step)
+    *reinterpret_cast<uint4*>(static_cast<T*>(a.values) + dst + h * head_stride + e0) =
+        __ldcs(reinterpret_cast<const uint4*>(v + int64_t(h) * D));
+  turn_heads(static_cast<const T*>(a.k) + r * a.k_stride, a.k_norm, c.kvh, static_cast<T*>(a.keys) + dst, head_stride);
 }
 
 template <typename T, int D>
 void launch(const AppendArgs& a, cudaStream_t st) {
-  // several tokens share a CTA once there are enough to fill the SMs with CTAs of four
-  if (a.c.total_q >= 8 * device_sm_count())
-    k_cache_append<T, D, 4><<<(a.c.total_q + 3) / 4, kThreads, 0, st>>>(a);
-  else
-    k_cache_append<T, D, 1><<<a.c.total_q, kThreads, 0, st>>>(a);
+  constexpr int HPW = 32 / (D / Vec<T>::N);
+  // as many warps per token as fill the SMs with about 32 warps each, at most one for every
+  // round of heads
+  const int64_t want = 32 * int64_t(device_sm_count()) / a.c.total_q, most = (a.c.kvh * a.c.group + HPW - 1) / HPW;
+  const int parts = int(want < 1 ? 1 : (want < most ? want : most));
+  const int64_t warps = int64_t(a.c.total_q) * parts;
+  k_cache_append<T, D><<<unsigned((warps + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(a, parts);
 }
 
 }  // namespace
