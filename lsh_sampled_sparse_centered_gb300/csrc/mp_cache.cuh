@@ -22,12 +22,12 @@ struct ChunkArgs {
   const void *q, *keys, *values;
   void* out;
   float* lse;   // may be nullptr
-  // partial results in the workspace: fp32 slices [splits][total_q][q_heads], bf16 slots of
-  // the pieces of tiles that are shared by CTAs
-  int splits;   // slices of the keys per row tile (fp32)
+  // partial results in the workspace: slices [splits][total_q][q_heads], or (tensor cores)
+  // slots of the pieces of tiles that are shared by CTAs
+  int splits;   // slices of the keys per row tile
   float* part;  // [..][d]: unnormalised sums
   float* ml;    // [..][2]: their reference (log2) and sum
-  void* cuts;   // shared tiles (bf16)
+  void* cuts;   // shared tiles (tensor cores)
 };
 
 struct WeightsArgs {
@@ -62,9 +62,11 @@ struct EvictArgs {
   int32_t* kept;  // [batch][kv_heads][budget]
 };
 
-// Sizes that the limits alone fix, so that a workspace can be sized before the call: slices
-// of the keys (fp32), CTAs of the tensor-core kernel and its workspace (bf16).
+// What the limits alone fix, so that a workspace can be sized before the call: slices of the
+// keys (fp32, and bf16 with few query rows), CTAs of the tensor-core kernel and its workspace.
 int chunk_splits(const mp_cache_config* c, int max_q, int max_kv);
+bool chunk_is_step(int group, int max_q);
+int chunk_step_splits(int batch, int kvh, int max_kv);
 int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv);
 uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv);
 
@@ -79,7 +81,8 @@ inline int box_rows(const int32_t* table, int page_size) {
 
 cudaError_t launch_cache_append(const AppendArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st);
-cudaError_t launch_chunk_join(const ChunkArgs& a, cudaStream_t st);
+cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st);
+cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st);
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_weights_bf16(const WeightsArgs& a, cudaStream_t st);

@@ -59,15 +59,22 @@ static CacheArgs cache_args(const mp_cache_config* c, const int32_t* table, cons
   return a;
 }
 
-static uint64_t simt_part_bytes(const mp_cache_config* c, int total_q, int splits) {
+static bool chunk_on_tensor_cores(const mp_cache_config* c, int max_q) {
+  return c->dtype == MP_DTYPE_BF16 && !chunk_is_step(c->q_heads / c->kv_heads, max_q);
+}
+static int slices(const mp_cache_config* c, int max_q, int max_kv) {
+  return c->dtype == MP_DTYPE_BF16 ? chunk_step_splits(c->batch, c->kv_heads, max_kv) : chunk_splits(c, max_q, max_kv);
+}
+static uint64_t part_bytes(const mp_cache_config* c, int total_q, int splits) {
   return align256(uint64_t(splits) * total_q * c->q_heads * c->head_dim * 4);
 }
 static uint64_t chunk_bytes(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
   if (total_q == 0) return 0;
-  if (c->dtype == MP_DTYPE_BF16) return chunk_tc_workspace(c, std::min(max_q, total_q), max_kv);
-  const int splits = chunk_splits(c, max_q, max_kv);
+  max_q = std::min(max_q, total_q);
+  if (chunk_on_tensor_cores(c, max_q)) return chunk_tc_workspace(c, max_q, max_kv);
+  const int splits = slices(c, max_q, max_kv);
   if (splits <= 1) return 0;
-  return simt_part_bytes(c, total_q, splits) + align256(uint64_t(splits) * total_q * c->q_heads * 2 * 4);
+  return part_bytes(c, total_q, splits) + align256(uint64_t(splits) * total_q * c->q_heads * 2 * 4);
 }
 
 static uint64_t evict_bytes(const mp_cache_config* c, int budget) {
@@ -183,22 +190,23 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
   a.cuts = nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  if (cfg->dtype == MP_DTYPE_BF16) {
+  if (chunk_on_tensor_cores(cfg, a.c.max_q)) {
     ProfScope ps(st, K_CHUNK_ATTEND);
     return launch_chunk_tc(a, workspace, st) == cudaSuccess ? MP_OK : MP_ERR_CUDA;
   }
-  a.splits = chunk_splits(cfg, max_q, max_kv);
+  a.splits = slices(cfg, a.c.max_q, max_kv);
   if (need > 0) {
     a.part = static_cast<float*>(workspace);
-    a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + simt_part_bytes(cfg, total_q, a.splits));
+    a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(cfg, total_q, a.splits));
   }
   {
     ProfScope ps(st, K_CHUNK_ATTEND);
-    if (launch_chunk_simt(a, st) != cudaSuccess) return MP_ERR_CUDA;
+    const cudaError_t e = cfg->dtype == MP_DTYPE_BF16 ? launch_chunk_step(a, st) : launch_chunk_simt(a, st);
+    if (e != cudaSuccess) return MP_ERR_CUDA;
   }
   if (a.splits > 1) {
     ProfScope ps(st, K_CHUNK_JOIN);
-    if (launch_chunk_join(a, st) != cudaSuccess) return MP_ERR_CUDA;
+    if (launch_chunk_join(a, cfg->dtype, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   return MP_OK;
 }

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
       }
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_chunk_join may be set up
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float sum = l[i];
@@ -189,36 +190,59 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
   }
 }
 
-// One warp per query row: joins the splits' (m, l, sum), in the order of the splits.
-template <int D>
+// One warp per query row: joins the splits' (m, l, sum), in the order of the splits. Started
+// while the slices still run (its launch costs as much as its work); it waits for them first.
+template <typename T, int D>
 __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
+  constexpr int PER = D / 32;
   const CacheArgs& c = a.c;
   const int qh = c.kvh * c.group;
   const int64_t rows = int64_t(c.total_q) * qh;
   const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
   const int t = int(row / qh), b = seq_at(c, t);
   if (b < 0) return;
   const Seq s = seq_of(c, b);
   if (t < s.row0 || t >= s.row0 + s.m) return;
+  const float2* ml = reinterpret_cast<const float2*>(a.ml) + row;
   float m = -INFINITY;
-  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.ml[(i * rows + row) * 2]);
-  float l = 0.f, o[D / 32];
+  for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, ml[i * rows].x);
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
-  for (int i = 0; i < a.splits; ++i) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.ml + (i * rows + row) * 2);
-    if (ml.y == 0.f) continue;
-    const float by = exp2f(ml.x - m);
-    l = fmaf(ml.y, by, l);
+  for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[PER];
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) o[j] = fmaf(a.part[(i * rows + row) * D + j * 32 + lane], by, o[j]);
+  for (int j = 0; j < PER; ++j) o[j] = 0.f;
+  for (int i0 = 0; i0 < a.splits; i0 += 32) {
+    const float2 v = i0 + lane < a.splits ? ml[(i0 + lane) * rows] : make_float2(-INFINITY, 0.f);
+    const float by = v.y == 0.f ? 0.f : exp2f(v.x - ref);
+    float sum = v.y * by;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    l += sum;
+    const int n = min(32, a.splits - i0);
+    for (int i = 0; i < n; i += 8) {
+      float x[8][PER], f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        f[k] = __shfl_sync(0xffffffffu, by, i + k);
+        const bool live = i + k < n && f[k] != 0.f;  // an empty slice has written no sum
+        const float* p = a.part + ((i0 + i + k) * rows + row) * D + lane * PER;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) x[k][j] = live ? p[j] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) o[j] = fmaf(x[k][j], f[k], o[j]);
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) static_cast<float*>(a.out)[row * D + j * 32 + lane] = o[j] * inv;
+  for (int j = 0; j < PER; ++j) static_cast<T*>(a.out)[row * D + lane * PER + j] = T(o[j] * inv);
 }
 
 // Attention weights: one CTA owns 64 slots of one KV head and walks the chunk's query
@@ -284,11 +308,19 @@ cudaError_t chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   k_chunk_simt<D><<<dim3(unsigned(tiles * a.splits), a.c.kvh, a.c.batch), kThr, smem, st>>>(a);
   return cudaGetLastError();
 }
-template <int D>
+template <typename T, int D>
 cudaError_t join(const ChunkArgs& a, cudaStream_t st) {
   const int64_t rows = int64_t(a.c.total_q) * a.c.kvh * a.c.group;
-  k_chunk_join<D><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_chunk_join<T, D>, a);
 }
 template <int D>
 cudaError_t weights_simt(const WeightsArgs& a, cudaStream_t st) {
@@ -313,8 +345,9 @@ int chunk_splits(const mp_cache_config* c, int max_q, int max_kv) {
 cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   return a.c.d == 128 ? chunk_simt<128>(a, st) : chunk_simt<64>(a, st);
 }
-cudaError_t launch_chunk_join(const ChunkArgs& a, cudaStream_t st) {
-  return a.c.d == 128 ? join<128>(a, st) : join<64>(a, st);
+cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st) {
+  if (dtype == MP_DTYPE_BF16) return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, st) : join<__nv_bfloat16, 64>(a, st);
+  return a.c.d == 128 ? join<float, 128>(a, st) : join<float, 64>(a, st);
 }
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st) {
   if (dtype == MP_DTYPE_BF16) return launch_weights_bf16(a, st);

@@ -1,0 +1,235 @@
+// Exact attention of few query rows per KV head (single tokens, a handful of draft tokens),
+// bf16: bound by one pass over K and V.
+//
+// At most 16 rows (tokens x heads of the group) per KV head. The slots are cut into slices,
+// one CTA each, 16 slots per warp and round. K and V go from global memory straight into
+// the fragments of warp-level products, so that nothing but registers holds them:
+//   S[row][key]: the sum over d has no order to keep, so lane t of a key's four takes the
+//     16-byte chunks t, t + 4, ... and feeds their halves to two products.
+//   O^T[d][row] += V^T P^T: lane (g, t) holds chunk g of V of the keys 2t, 2t + 1, 2t + 8
+//     and 2t + 9; element i of the chunks makes the 16 x 16 tile of the d that are i modulo 8.
+//     The accumulators of S are P^T's fragments as they stand.
+// Loads of the next round are issued as soon as their registers are free. The reference of
+// a row's softmax is raised only when a logit passes it by more than 8 (log2). P is bf16
+// (2^-8 relative per weight), its sum is taken before that rounding.
+#include "mp_cache.cuh"
+#include "mp_tc.cuh"
+
+namespace mp {
+namespace {
+
+constexpr int kWarps = 4, kRound = 16;  // slots of a warp and round
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRaise = 8.0f;
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
+// element e (0..7) of the 16-byte chunks a and b as one pair
+__device__ __forceinline__ uint32_t pair(const uint4& a, const uint4& b, int e) {
+  return __byte_perm(word(a, e >> 1), word(b, e >> 1), (e & 1) ? 0x7632 : 0x5410);
+}
+
+template <int D, int NT>  // NT: query rows in eights
+__global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
+  constexpr int KC = D / 32;      // chunks of a K row per lane
+  constexpr int VC = D / 64;      // chunks of a V row per lane
+  constexpr int TILES = D / 16;   // 16-row tiles of O^T
+  __shared__ float so[kWarps][NT * 8][D + 4];
+  __shared__ float sm[kWarps][NT * 8], sl[kWarps][NT * 8];
+  const CacheArgs& c = a.c;
+  const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const Seq s = seq_of(c, b);
+  const int rows = s.m * c.group, first = s.n - s.m, qh = c.kvh * c.group;
+  if (rows == 0) return;
+  // this CTA's slots, a whole number of rounds of all warps
+  const int per = ((s.n + a.splits - 1) / a.splits + kWarps * kRound - 1) / (kWarps * kRound) * (kWarps * kRound);
+  const int k0 = int(min(int64_t(s.n), int64_t(split) * per)), k1 = min(s.n, k0 + per);
+
+  // Q: row r of the tile is token r / group, head r % group; rows behind the last are zero
+  uint4 q[NT][KC];
+  int see[NT];  // the lane's row (8 u + g) sees the slots below this
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int r = u * 8 + g;
+    see[u] = r < rows ? min(s.n, first + r / c.group + 1) : 0;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                               (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D + t * 8;
+#pragma unroll
+    for (int i = 0; i < KC; ++i)
+      q[u][i] = r < rows ? *reinterpret_cast<const uint4*>(src + i * 32) : make_uint4(0, 0, 0, 0);
+  }
+  const float scale = kLog2e * rsqrtf(float(D));
+  float o[NT][TILES][4], m[NT], l[NT];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    m[u] = -INFINITY;
+    l[u] = 0.f;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[u][i][j] = 0.f;
+  }
+  const __nv_bfloat16 *keys = static_cast<const __nv_bfloat16*>(a.keys), *values = static_cast<const __nv_bfloat16*>(a.values);
+  uint4 k[2][KC], v[4][VC];
+  // slots behind the last are read as the last: their weights are zero
+  auto load_k = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __nv_bfloat16* src = keys + slot_read(c, b, h, min(n0 + g + 8 * i, s.n - 1)) + t * 8;
+#pragma unroll
+      for (int j = 0; j < KC; ++j) k[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + j * 32));
+    }
+  };
+  auto load_v = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat16* src = values + slot_read(c, b, h, min(n0 + 2 * t + (i & 1) + 8 * (i >> 1), s.n - 1)) + g * 8;
+#pragma unroll
+      for (int j = 0; j < VC; ++j) v[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + j * 64));
+    }
+  };
+  int n0 = k0 + warp * kRound;
+  if (n0 < k1) {
+    load_k(n0);
+    load_v(n0);
+  }
+  for (; n0 < k1; n0 += kWarps * kRound) {
+    const int next = n0 + kWarps * kRound;
+    // S: x[u][key half][..]: rows g (and 8 + g), keys 2t, 2t + 1 of each half
+    float x[NT][2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        mma_16816(d, q[0][j].x, NT > 1 ? q[NT - 1][j].x : 0u, q[0][j].y, NT > 1 ? q[NT - 1][j].y : 0u, k[i][j].x, k[i][j].y);
+        mma_16816(d, q[0][j].z, NT > 1 ? q[NT - 1][j].z : 0u, q[0][j].w, NT > 1 ? q[NT - 1][j].w : 0u, k[i][j].z, k[i][j].w);
+      }
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          x[u][i][j] = n0 + 8 * i + 2 * t + j < see[u] ? d[2 * u + j] * scale : -INFINITY;
+    }
+    if (next < k1) load_k(next);
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      float top = fmaxf(fmaxf(x[u][0][0], x[u][0][1]), fmaxf(x[u][1][0], x[u][1][1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const bool raise = top > m[u] + kRaise || (m[u] == -INFINITY && top > m[u]);
+      if (__any_sync(0xffffffffu, raise)) {
+        const float by = raise ? exp2f(m[u] - top) : 1.f;  // 0 for the first reference
+        if (raise) m[u] = top;
+        l[u] *= by;
+        const float b0 = __shfl_sync(0xffffffffu, by, 8 * t), b1 = __shfl_sync(0xffffffffu, by, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+          o[u][i][0] *= b0;
+          o[u][i][1] *= b1;
+          o[u][i][2] *= b0;
+          o[u][i][3] *= b1;
+        }
+      }
+      const float ref = m[u] == -INFINITY ? 0.f : m[u];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float e0 = ex2(x[u][i][0] - ref), e1 = ex2(x[u][i][1] - ref);
+        l[u] += e0 + e1;
+        p[u][i] = bf2(e0, e1);
+      }
+    }
+    // O^T: tile i holds the d that are i modulo 8 (of both 64-element halves; d = 64: i and i + 4)
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+      const int e1 = D == 128 ? i : i + 4, c1 = D == 128 ? VC - 1 : 0;
+      const uint32_t a0 = pair(v[0][0], v[1][0], i), a1 = pair(v[0][c1], v[1][c1], e1);
+      const uint32_t a2 = pair(v[2][0], v[3][0], i), a3 = pair(v[2][c1], v[3][c1], e1);
+#pragma unroll
+      for (int u = 0; u < NT; ++u) mma_16816(o[u][i], a0, a1, a2, a3, p[u][0], p[u][1]);
+    }
+    if (next < k1) load_v(next);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_chunk_join may be set up
+  // the four warps' parts, in their order
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
+    l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
+    if (t == 0) {
+      sm[warp][u * 8 + g] = m[u];
+      sl[warp][u * 8 + g] = l[u];
+    }
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+      const int d0 = 8 * g + i, d1 = D == 128 ? d0 + 64 : d0 + 4;
+      so[warp][u * 8 + 2 * t][d0] = o[u][i][0];
+      so[warp][u * 8 + 2 * t + 1][d0] = o[u][i][1];
+      so[warp][u * 8 + 2 * t][d1] = o[u][i][2];
+      so[warp][u * 8 + 2 * t + 1][d1] = o[u][i][3];
+    }
+  }
+  __syncthreads();
+  for (int r = warp; r < rows; r += kWarps) {
+    float top = sm[0][r], sum = 0.f, by[kWarps];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm[w][r]);
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      by[w] = ex2(sm[w][r] - ref);
+      sum = fmaf(sl[w][r], by[w], sum);
+    }
+    const int64_t row = int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group;
+    const int64_t at = int64_t(split) * c.total_q * qh + row;
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    if (lane == 0) {
+      if (a.splits > 1) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(top, sum);
+      else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+    }
+    for (int d = lane * 4; d < D; d += 128) {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 z = *reinterpret_cast<const float4*>(&so[w][r][d]);
+        y.x = fmaf(z.x, by[w], y.x);
+        y.y = fmaf(z.y, by[w], y.y);
+        y.z = fmaf(z.z, by[w], y.z);
+        y.w = fmaf(z.w, by[w], y.w);
+      }
+      if (a.splits > 1)
+        *reinterpret_cast<float4*>(a.part + at * D + d) = y;
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d) =
+            make_uint2(bf2(y.x * inv, y.y * inv), bf2(y.z * inv, y.w * inv));
+    }
+  }
+}
+
+template <int D>
+void launch(const ChunkArgs& a, cudaStream_t st) {
+  const dim3 grid(a.splits, a.c.kvh, a.c.batch);
+  if (int64_t(a.c.max_q) * a.c.group <= 8) k_chunk_step<D, 1><<<grid, kWarps * 32, 0, st>>>(a);
+  else k_chunk_step<D, 2><<<grid, kWarps * 32, 0, st>>>(a);
+}
+
+}  // namespace
+
+bool chunk_is_step(int group, int max_q) { return int64_t(max_q) * group <= 16; }
+
+// Slices: about two waves of three CTAs per SM, each of at least 128 slots.
+int chunk_step_splits(int batch, int kvh, int max_kv) {
+  const int64_t fill = 6 * int64_t(device_sm_count()) / (int64_t(batch) * kvh), most = (int64_t(max_kv) + 127) / 128;
+  const int64_t s = fill < most ? fill : most;
+  return int(s < 1 ? 1 : (s > 1024 ? 1024 : s));
+}
+
+cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st) {
+  if (a.c.d == 128) launch<128>(a, st);
+  else launch<64>(a, st);
+  return cudaGetLastError();
+}
+
+}  // namespace mp

@@ -270,13 +270,6 @@ __global__ void __launch_bounds__(192, 2)
 
 constexpr int kStepWarps = 8, kStepKeys = 64;  // keys of a warp
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // 16 keys (M) x 8 NT query rows (N) per warp and round. The sum over d has no order to
 // keep, so lane t of a row's four takes the 16-byte chunks t, t + 4, ... and feeds their
 // halves to two products: the loads are whole vectors and need no shared memory.
