@@ -10,6 +10,7 @@ namespace mp {
 struct CacheArgs {
   int batch, kvh, group, d;      // group = q_heads / kv_heads
   int page_size, n_pages, cols;  // cols: columns of the page table
+  int page_shift;                // log2(page_size) where it is a power of two, else -1
   const int32_t* table;          // nullptr: page b is sequence b's cache
   const int32_t* cu_q;           // nullptr: no packed rows (eviction)
   const int32_t* kv_len;
@@ -66,7 +67,7 @@ struct EvictArgs {
 // keys (fp32, and bf16 with few query rows), CTAs of the tensor-core kernel and its workspace.
 int chunk_splits(const mp_cache_config* c, int max_q, int max_kv);
 bool chunk_is_step(int group, int max_q);
-int chunk_step_splits(int batch, int kvh, int max_kv);
+int chunk_step_splits(int batch, int kvh, int group, int max_q, int max_kv);
 int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv);
 uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv);
 
@@ -149,11 +150,17 @@ __host__ __device__ __forceinline__ int page_at(const int32_t* table, int cols, 
   return p;
 }
 
-// Element offset of slot s of KV head h for reading: a bad page reads page 0 instead.
-__host__ __device__ __forceinline__ int64_t slot_read(const CacheArgs& c, int b, int h, int s) {
-  const int col = s / c.page_size, o = s - col * c.page_size;
+// Row of the pool that holds slot s of KV head h, for reading: a bad page reads page 0
+// instead. The pool's rows are 32-bit (checked by the host).
+__host__ __device__ __forceinline__ int slot_row(const CacheArgs& c, int b, int h, int s) {
+  if (!c.table) return (b * c.kvh + h) * c.page_size + s;
+  const int col = c.page_shift >= 0 ? s >> c.page_shift : s / c.page_size;
   const int p = max(0, page_at(c.table, c.cols, c.n_pages, b, col, c.status));
-  return ((int64_t(p) * c.kvh + h) * c.page_size + o) * c.d;
+  return (p * c.kvh + h) * c.page_size + (s - col * c.page_size);
+}
+// Its element offset.
+__host__ __device__ __forceinline__ int64_t slot_read(const CacheArgs& c, int b, int h, int s) {
+  return int64_t(slot_row(c, b, h, s)) * c.d;
 }
 #endif
 

@@ -49,6 +49,9 @@ static CacheArgs cache_args(const mp_cache_config* c, const int32_t* table, cons
   a.page_size = c->page_size;
   a.n_pages = c->n_pages;
   a.cols = c->max_pages;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (c->page_size == 1 << i) a.page_shift = i;
   a.table = table;
   a.cu_q = cu_q;
   a.kv_len = kv_len;
@@ -63,7 +66,8 @@ static bool chunk_on_tensor_cores(const mp_cache_config* c, int max_q) {
   return c->dtype == MP_DTYPE_BF16 && !chunk_is_step(c->q_heads / c->kv_heads, max_q);
 }
 static int slices(const mp_cache_config* c, int max_q, int max_kv) {
-  return c->dtype == MP_DTYPE_BF16 ? chunk_step_splits(c->batch, c->kv_heads, max_kv) : chunk_splits(c, max_q, max_kv);
+  if (c->dtype != MP_DTYPE_BF16) return chunk_splits(c, max_q, max_kv);
+  return chunk_step_splits(c->batch, c->kv_heads, c->q_heads / c->kv_heads, max_q, max_kv);
 }
 static uint64_t part_bytes(const mp_cache_config* c, int total_q, int splits) {
   return align256(uint64_t(splits) * total_q * c->q_heads * c->head_dim * 4);

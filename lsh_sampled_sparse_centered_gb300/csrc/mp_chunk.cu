@@ -190,16 +190,20 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
   }
 }
 
-// One warp per query row: joins the splits' (m, l, sum), in the order of the splits. Started
-// while the slices still run (its launch costs as much as its work); it waits for them first.
-template <typename T, int D>
+// Joins the splits' (m, l, sum) of a query row, in an order that is fixed by their number:
+// WARPS warps per row (8 where there are many splits, so that their loads overlap) take
+// eight splits at a time each. Started while the slices still run (its launch costs as much
+// as its work); it waits for them first.
+template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   constexpr int PER = D / 32;
+  __shared__ float so[8][D], sl[8];
   const CacheArgs& c = a.c;
   const int qh = c.kvh * c.group;
   const int64_t rows = int64_t(c.total_q) * qh;
-  const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * (8 / WARPS) + warp / WARPS;
+  const int part = warp % WARPS;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
   const int t = int(row / qh), b = seq_at(c, t);
@@ -215,28 +219,34 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   float l = 0.f, o[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) o[j] = 0.f;
-  for (int i0 = 0; i0 < a.splits; i0 += 32) {
-    const float2 v = i0 + lane < a.splits ? ml[(i0 + lane) * rows] : make_float2(-INFINITY, 0.f);
-    const float by = v.y == 0.f ? 0.f : exp2f(v.x - ref);
-    float sum = v.y * by;
+  for (int i = part * 8; i < a.splits; i += WARPS * 8) {
+    float x[8][PER], f[8];
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-    l += sum;
-    const int n = min(32, a.splits - i0);
-    for (int i = 0; i < n; i += 8) {
-      float x[8][PER], f[8];
+    for (int k = 0; k < 8; ++k) {
+      const float2 v = i + k < a.splits ? ml[(i + k) * rows] : make_float2(-INFINITY, 0.f);
+      f[k] = v.y == 0.f ? 0.f : exp2f(v.x - ref);
+      l = fmaf(v.y, f[k], l);
+      const bool live = v.y != 0.f;  // an empty slice has written no sum
+      const float* p = a.part + ((i + k) * rows + row) * D + lane * PER;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f[k] = __shfl_sync(0xffffffffu, by, i + k);
-        const bool live = i + k < n && f[k] != 0.f;  // an empty slice has written no sum
-        const float* p = a.part + ((i0 + i + k) * rows + row) * D + lane * PER;
+      for (int j = 0; j < PER; ++j) x[k][j] = live ? p[j] : 0.f;
+    }
 #pragma unroll
-        for (int j = 0; j < PER; ++j) x[k][j] = live ? p[j] : 0.f;
-      }
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int j = 0; j < PER; ++j) o[j] = fmaf(x[k][j], f[k], o[j]);
+  }
+  if (WARPS > 1) {  // one row per CTA: no warp has left
 #pragma unroll
-        for (int j = 0; j < PER; ++j) o[j] = fmaf(x[k][j], f[k], o[j]);
+    for (int j = 0; j < PER; ++j) so[warp][lane * PER + j] = o[j];
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      l += sl[w];
+#pragma unroll
+      for (int j = 0; j < PER; ++j) o[j] += so[w][lane * PER + j];
     }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
@@ -312,7 +322,8 @@ template <typename T, int D>
 cudaError_t join(const ChunkArgs& a, cudaStream_t st) {
   const int64_t rows = int64_t(a.c.total_q) * a.c.kvh * a.c.group;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((rows + 7) / 8));
+  const bool wide = a.splits > 8;
+  cfg.gridDim = dim3(unsigned(wide ? rows : (rows + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -320,7 +331,7 @@ cudaError_t join(const ChunkArgs& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_chunk_join<T, D>, a);
+  return wide ? cudaLaunchKernelEx(&cfg, k_chunk_join<T, D, 8>, a) : cudaLaunchKernelEx(&cfg, k_chunk_join<T, D, 1>, a);
 }
 template <int D>
 cudaError_t weights_simt(const WeightsArgs& a, cudaStream_t st) {

@@ -72,27 +72,41 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
   }
   const __nv_bfloat16 *keys = static_cast<const __nv_bfloat16*>(a.keys), *values = static_cast<const __nv_bfloat16*>(a.values);
   uint4 k[2][KC], v[4][VC];
-  // slots behind the last are read as the last: their weights are zero
-  auto load_k = [&](int n0) {
+  // Rows of the pool for a round's slots, looked up a round ahead of their loads. Slots behind
+  // the last are read as the last: their weights are zero.
+  int rk[2], rv[4];
+  auto find_k = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rk[i] = slot_row(c, b, h, min(n0 + g + 8 * i, s.n - 1));
+  };
+  auto find_v = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rv[i] = slot_row(c, b, h, min(n0 + 2 * t + (i & 1) + 8 * (i >> 1), s.n - 1));
+  };
+  auto load_k = [&]() {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const __nv_bfloat16* src = keys + slot_read(c, b, h, min(n0 + g + 8 * i, s.n - 1)) + t * 8;
+      const __nv_bfloat16* src = keys + int64_t(rk[i]) * D + t * 8;
 #pragma unroll
       for (int j = 0; j < KC; ++j) k[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + j * 32));
     }
   };
-  auto load_v = [&](int n0) {
+  auto load_v = [&]() {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat16* src = values + slot_read(c, b, h, min(n0 + 2 * t + (i & 1) + 8 * (i >> 1), s.n - 1)) + g * 8;
+      const __nv_bfloat16* src = values + int64_t(rv[i]) * D + g * 8;
 #pragma unroll
       for (int j = 0; j < VC; ++j) v[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + j * 64));
     }
   };
   int n0 = k0 + warp * kRound;
   if (n0 < k1) {
-    load_k(n0);
-    load_v(n0);
+    find_k(n0);
+    load_k();
+    find_v(n0);
+    load_v();
+    find_k(n0 + kWarps * kRound);
+    find_v(n0 + kWarps * kRound);
   }
   for (; n0 < k1; n0 += kWarps * kRound) {
     const int next = n0 + kWarps * kRound;
@@ -112,7 +126,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
         for (int j = 0; j < 2; ++j)
           x[u][i][j] = n0 + 8 * i + 2 * t + j < see[u] ? d[2 * u + j] * scale : -INFINITY;
     }
-    if (next < k1) load_k(next);
+    if (next < k1) {
+      load_k();
+      find_k(next + kWarps * kRound);
+    }
     uint32_t p[NT][2];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
@@ -150,7 +167,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
 #pragma unroll
       for (int u = 0; u < NT; ++u) mma_16816(o[u][i], a0, a1, a2, a3, p[u][0], p[u][1]);
     }
-    if (next < k1) load_v(next);
+    if (next < k1) {
+      load_v();
+      find_v(next + kWarps * kRound);
+    }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_chunk_join may be set up
   // the four warps' parts, in their order
@@ -219,11 +239,15 @@ void launch(const ChunkArgs& a, cudaStream_t st) {
 
 bool chunk_is_step(int group, int max_q) { return int64_t(max_q) * group <= 16; }
 
-// Slices: about two waves of three CTAs per SM, each of at least 128 slots.
-int chunk_step_splits(int batch, int kvh, int max_kv) {
-  const int64_t fill = 6 * int64_t(device_sm_count()) / (int64_t(batch) * kvh), most = (int64_t(max_kv) + 127) / 128;
-  const int64_t s = fill < most ? fill : most;
-  return int(s < 1 ? 1 : (s > 1024 ? 1024 : s));
+// Slices of at least 128 slots: one wave of the CTAs that fit (three per SM with up to eight
+// rows, two with more), or two waves where a slice then still has 2048 slots (98304 slots of
+// eight KV heads: 66.8 us in one wave, 71.0 in two; four times that: 222 and 217 us).
+int chunk_step_splits(int batch, int kvh, int group, int max_q, int max_kv) {
+  const int64_t fit = int64_t(device_sm_count()) * (int64_t(max_q) * group <= 8 ? 3 : 2), units = int64_t(batch) * kvh;
+  const int64_t wave = fit / units, most = (int64_t(max_kv) + 127) / 128;
+  const int64_t two = 2 * fit / units;
+  const int64_t fill = two * 2048 <= max_kv ? two : wave, s = fill < most ? fill : most;
+  return int(s < 1 ? 1 : s);
 }
 
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st) {

@@ -329,9 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_expect_tx(bar, uint32_t(boxes) * box * kRowBytes * kSub);
             __syncwarp();
             for (int j = lane; j < boxes; j += 32) {
-              const int slot = n0 + j * box, col = slot / c.page_size;
-              const int p = max(0, page_at(c.table, c.cols, c.n_pages, pc.b, col, c.status));
-              const int row = (p * c.kvh + pc.h) * c.page_size + (slot - col * c.page_size);
+              const int row = slot_row(c, pc.b, pc.h, n0 + j * box);
 #pragma unroll
               for (int s = 0; s < kSub; ++s)
                 tma_load_2d(&S.kv[st][s][j * box * 64], kv ? &tmV : &tmK, s * 64, row, bar);

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(256) k_evict_gather(const EvictArgs a) {
     if (j >= m) continue;
     const int col = j / a.dst_page_size;
     const int p = page_at(a.dst_table, a.dst_cols, a.dst_n_pages, b, col, c.status);
-    const int64_t from = slot_read(c, b, h, kept[j]) / c.d * ROW + e;
+    const int64_t from = int64_t(slot_row(c, b, h, kept[j])) * ROW + e;
     k[i] = __ldcs(keys + from);
     v[i] = __ldcs(values + from);
     if (p >= 0) to[i] = ((int64_t(p) * c.kvh + h) * a.dst_page_size + (j - col * a.dst_page_size)) * ROW + e;

@@ -122,9 +122,7 @@ __global__ void __launch_bounds__(192, 2)
     if (lane == 0) mbar_expect_tx(&S.k_full, uint32_t(boxes) * box * 128 * kSub);
     __syncwarp();
     for (int i = lane; i < boxes; i += 32) {
-      const int slot = n0 + i * box, col = slot / c.page_size;
-      const int p = max(0, page_at(c.table, c.cols, c.n_pages, b, col, c.status));
-      const int row = (p * c.kvh + h) * c.page_size + (slot - col * c.page_size);
+      const int row = slot_row(c, b, h, n0 + i * box);
 #pragma unroll
       for (int u = 0; u < kSub; ++u) tma_load_2d(&S.k[u][i * box * 64], &tmK, u * 64, row, &S.k_full);
     }

@@ -52,6 +52,9 @@ int main() {
     c.page_size = ps;
     c.n_pages = pages;
     c.cols = cols;
+    c.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+      if (ps == 1 << i) c.page_shift = i;
     c.table = table.data();
     c.cu_q = cu.data();
     c.kv_len = kv.data();
