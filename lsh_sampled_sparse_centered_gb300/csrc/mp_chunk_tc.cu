@@ -355,86 +355,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 9) {
-      // ---------------- products ----------------
-      if (lane == 0) {
-        const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kKeys >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-        const uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) |
-                              (uint32_t(128 >> 4) << 24);
-        const uint64_t dq = sw128_desc(saddr(&S.q[0][0][0])), dk = sw128_desc(saddr(&S.kv[0][0][0])),
-                       dv = sw128_desc_mn(saddr(&S.kv[0][0][0]));
-        constexpr uint32_t kTile = kKeys * D * 2 / 16, kSlab = kKeys * 128 / 16;  // in descriptor units of 16 bytes
-        int st = 0;
-        uint32_t ph = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
-        auto advance = [&]() {
-          if (++st == kStages) {
-            st = 0;
-            ph ^= 1;
-          }
-        };
-        auto product_s = [&](int half, int sk) {
+      // ---------------- products: the warp as one, an elected lane issues ----------------
+      const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kKeys >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+      const uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) |
+                            (uint32_t(128 >> 4) << 24);
+      const uint64_t dq = sw128_desc(saddr(&S.q[0][0][0])), dk = sw128_desc(saddr(&S.kv[0][0][0])),
+                     dv = sw128_desc_mn(saddr(&S.kv[0][0][0]));
+      constexpr uint32_t kTile = kKeys * D * 2 / 16, kSlab = kKeys * 128 / 16;  // in descriptor units of 16 bytes
+      int st = 0;
+      uint32_t ph = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+      auto advance = [&]() {
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      };
+      auto product_s = [&](int half, int sk, bool release) {
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
             mma_bf16(tmem + uint32_t(half * 128), dq + half * kTile + off, dk + sk * kTile + off, id_s, kk > 0 ? 1u : 0u);
           }
           mma_commit(&S.s_full[half]);
-        };
-        bool ok = true;
-        for (uint32_t i = 0; ok; ++i) {
-          ok = mbar_wait(&S.piece_full[i & 1], (i >> 1) & 1, abort);
-          if (!ok) break;
-          const int steps = S.piece[i & 1].u1 - S.piece[i & 1].u0;
-          const int halves = S.piece[i & 1].rows - S.piece[i & 1].r0 > 128 ? 2 : 1;
-          mbar_arrive(&S.piece_empty[i & 1]);
-          if (steps == 0) break;
-          ok = mbar_wait(&S.full[st], ph, abort);
-          for (int half = 0; half < halves && ok; ++half) {
-            ok = mbar_wait(&S.q_full[half], ph_q[half], abort);
-            ph_q[half] ^= 1;
-            if (!ok) break;
-            fence_after();
-            product_s(half, st);
-          }
-          if (!ok) break;
-          mma_commit(&S.empty[st]);
-          advance();
-          for (int j = 0; j < steps && ok; ++j) {
-            const int sv = st;
-            ok = mbar_wait(&S.full[sv], ph, abort);
-            advance();
-            for (int half = 0; half < halves && ok; ++half) {
-              // P arrives in two parts of 64 keys: the product starts on the first
+          if (release) mma_commit(&S.empty[sk]);
+        }
+        __syncwarp();
+      };
+      bool ok = true;
+      for (uint32_t i = 0; ok; ++i) {
+        ok = mbar_wait_warp(&S.piece_full[i & 1], (i >> 1) & 1, abort);
+        if (!ok) break;
+        const Piece& pc = S.piece[i & 1];
+        const int steps = __reduce_max_sync(0xffffffffu, pc.u1 - pc.u0);
+        const int halves = __reduce_max_sync(0xffffffffu, pc.rows - pc.r0) > 128 ? 2 : 1;
+        if (elect_one()) mbar_arrive(&S.piece_empty[i & 1]);
+        __syncwarp();
+        if (steps == 0) break;
+        ok = mbar_wait_warp(&S.full[st], ph, abort);
 #pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                ok = ok && mbar_wait(&S.p_full[half][part], ph_p[half], abort);
-                if (!ok) break;
-                fence_after();
+        for (int half = 0; half < 2; ++half) {
+          if (half >= halves || !ok) break;
+          ok = mbar_wait_warp(&S.q_full[half], ph_q[half], abort);
+          ph_q[half] ^= 1;
+          if (!ok) break;
+          fence_after();
+          product_s(half, st, half == halves - 1);
+        }
+        if (!ok) break;
+        advance();
+        for (int j = 0; j < steps && ok; ++j) {
+          const int sv = st;
+          ok = mbar_wait_warp(&S.full[sv], ph, abort);
+          advance();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (half >= halves || !ok) break;
+            // P arrives in two parts of 64 keys: the product starts on the first
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              ok = ok && mbar_wait_warp(&S.p_full[half][part], ph_p[half], abort);
+              if (!ok) break;
+              fence_after();
+              if (elect_one()) {
 #pragma unroll
                 for (int kk = part * 4; kk < part * 4 + 4; ++kk)
                   mma_bf16_ta(tmem + uint32_t(256 + half * D), tmem + uint32_t(half * 128 + kk * 8),
                               dv + sv * kTile + kk * 128, id_o, (j > 0 || kk > 0) ? 1u : 0u);
-              }
-              ph_p[half] ^= 1;
-              if (!ok) break;
-              mma_commit(&S.o_full[half]);
-              if (half == halves - 1) mma_commit(&S.empty[sv]);
-              if (j + 1 < steps) {
-                if (half == 0) {
-                  ok = mbar_wait(&S.full[st], ph, abort);
-                  if (!ok) break;
-                  fence_after();
-                }
-                product_s(half, st);
-                if (half == halves - 1) {
-                  mma_commit(&S.empty[st]);
-                  advance();
+                if (part == 1) {
+                  mma_commit(&S.o_full[half]);
+                  if (half == halves - 1) mma_commit(&S.empty[sv]);
                 }
               }
+              __syncwarp();
+            }
+            ph_p[half] ^= 1;
+            if (!ok) break;
+            if (j + 1 < steps) {
+              if (half == 0) {
+                ok = mbar_wait_warp(&S.full[st], ph, abort);
+                if (!ok) break;
+                fence_after();
+              }
+              product_s(half, st, half == halves - 1);
+              if (half == halves - 1) advance();
             }
           }
         }
       }
-      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
