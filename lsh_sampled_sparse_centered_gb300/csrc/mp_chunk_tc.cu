@@ -7,7 +7,8 @@
 //   O += P V    (128 x d x 128, P from tensor memory, V from shared memory)
 // While the softmax warps of one half work, the tensor cores work for the other half.
 // Warps 0-3 and 4-7 are the softmax of the halves, warp 8 streams K and V by TMA into a
-// ring of shared-memory tiles, warp 9 issues the products.
+// ring of shared-memory tiles, warps 9 and 11 issue the halves' products, warp 10 walks the
+// CTA's work.
 //
 // The reference m of a row is raised only when a logit passes it by more than 8 (in log2),
 // so that O is rescaled in few steps; P then is at most 2^8, which costs a float nothing.
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kRows = 256;   // query rows of a CTA
 constexpr int kKeys = 128;   // keys of a step
-constexpr int kThreads = 384;  // 12 warps: two of softmax for each lane quarter, TMA, products, two idle
+constexpr int kThreads = 384;  // 12 warps: two of softmax for each lane quarter, TMA, work, two of products
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&S.full[i], 1);
-      mbar_init(&S.empty[i], 1);
+      mbar_init(&S.empty[i], 2);  // both halves' products
     }
     mbar_init(&S.tail, 1);
     for (int i = 0; i < 2; ++i) {
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.p_full[i][0], 4);
       mbar_init(&S.p_full[i][1], 4);
       mbar_init(&S.piece_full[i], 1);
-      mbar_init(&S.piece_empty[i], 10);  // the TMA warp, the product warp, eight of softmax
+      mbar_init(&S.piece_empty[i], 11);  // the TMA warp, two of products, eight of softmax
       mbar_init(&S.o_full[i], 1);
     }
     S.abort = 0u;
@@ -354,33 +355,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-    } else if (warp == 9) {
-      // ---------------- products: the warp as one, an elected lane issues ----------------
+    } else {
+      // ---------------- products: warp 9 for the first half, 11 for the second ----------------
+      // Each runs as one warp and an elected lane issues. A warp's own products follow each
+      // other (P overlays S), the other's fill the tensor cores while it waits for its P.
+      const int half = warp == 9 ? 0 : 1;
       const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kKeys >> 3) << 17) | (uint32_t(128 >> 4) << 24);
       const uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) |
                             (uint32_t(128 >> 4) << 24);
-      const uint64_t dq = sw128_desc(saddr(&S.q[0][0][0])), dk = sw128_desc(saddr(&S.kv[0][0][0])),
+      const uint64_t dq = sw128_desc(saddr(&S.q[half][0][0])), dk = sw128_desc(saddr(&S.kv[0][0][0])),
                      dv = sw128_desc_mn(saddr(&S.kv[0][0][0]));
       constexpr uint32_t kTile = kKeys * D * 2 / 16, kSlab = kKeys * 128 / 16;  // in descriptor units of 16 bytes
+      const uint32_t t_s = tmem + uint32_t(half * 128), t_o = tmem + uint32_t(256 + half * D);
       int st = 0;
-      uint32_t ph = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+      uint32_t ph = 0, ph_q = 0, ph_p = 0;
       auto advance = [&]() {
         if (++st == kStages) {
           st = 0;
           ph ^= 1;
         }
       };
-      auto product_s = [&](int half, int sk, bool release) {
+      auto product_s = [&]() {
+        fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
-            mma_bf16(tmem + uint32_t(half * 128), dq + half * kTile + off, dk + sk * kTile + off, id_s, kk > 0 ? 1u : 0u);
+            mma_bf16(t_s, dq + off, dk + st * kTile + off, id_s, kk > 0 ? 1u : 0u);
           }
           mma_commit(&S.s_full[half]);
-          if (release) mma_commit(&S.empty[sk]);
+          mma_commit(&S.empty[st]);
         }
         __syncwarp();
+        advance();
       };
       bool ok = true;
       for (uint32_t i = 0; ok; ++i) {
@@ -388,58 +395,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const Piece& pc = S.piece[i & 1];
         const int steps = __reduce_max_sync(0xffffffffu, pc.u1 - pc.u0);
-        const int halves = __reduce_max_sync(0xffffffffu, pc.rows - pc.r0) > 128 ? 2 : 1;
+        const bool active = __reduce_max_sync(0xffffffffu, pc.rows - pc.r0) > half * 128;
         if (elect_one()) mbar_arrive(&S.piece_empty[i & 1]);
         __syncwarp();
         if (steps == 0) break;
-        ok = mbar_wait_warp(&S.full[st], ph, abort);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half >= halves || !ok) break;
-          ok = mbar_wait_warp(&S.q_full[half], ph_q[half], abort);
-          ph_q[half] ^= 1;
-          if (!ok) break;
-          fence_after();
-          product_s(half, st, half == halves - 1);
+        if (!active) {  // the ring's tiles pass this half by
+          for (int j = 0; j < 2 * steps && ok; ++j) {
+            ok = mbar_wait_warp(&S.full[st], ph, abort);
+            if (ok && elect_one()) mbar_arrive(&S.empty[st]);
+            __syncwarp();
+            advance();
+          }
+          continue;
         }
+        ok = mbar_wait_warp(&S.full[st], ph, abort) && mbar_wait_warp(&S.q_full[half], ph_q, abort);
+        ph_q ^= 1;
         if (!ok) break;
-        advance();
-        for (int j = 0; j < steps && ok; ++j) {
-          const int sv = st;
-          ok = mbar_wait_warp(&S.full[sv], ph, abort);
-          advance();
+        product_s();
+        for (int j = 0; j < steps; ++j) {
+          ok = mbar_wait_warp(&S.full[st], ph, abort);
+          // P arrives in two parts of 64 keys: the product starts on the first
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (half >= halves || !ok) break;
-            // P arrives in two parts of 64 keys: the product starts on the first
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              ok = ok && mbar_wait_warp(&S.p_full[half][part], ph_p[half], abort);
-              if (!ok) break;
-              fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = part * 4; kk < part * 4 + 4; ++kk)
-                  mma_bf16_ta(tmem + uint32_t(256 + half * D), tmem + uint32_t(half * 128 + kk * 8),
-                              dv + sv * kTile + kk * 128, id_o, (j > 0 || kk > 0) ? 1u : 0u);
-                if (part == 1) {
-                  mma_commit(&S.o_full[half]);
-                  if (half == halves - 1) mma_commit(&S.empty[sv]);
-                }
-              }
-              __syncwarp();
-            }
-            ph_p[half] ^= 1;
+          for (int part = 0; part < 2; ++part) {
+            ok = ok && mbar_wait_warp(&S.p_full[half][part], ph_p, abort);
             if (!ok) break;
-            if (j + 1 < steps) {
-              if (half == 0) {
-                ok = mbar_wait_warp(&S.full[st], ph, abort);
-                if (!ok) break;
-                fence_after();
+            fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = part * 4; kk < part * 4 + 4; ++kk)
+                mma_bf16_ta(t_o, t_s + uint32_t(kk * 8), dv + st * kTile + kk * 128, id_o, (j > 0 || kk > 0) ? 1u : 0u);
+              if (part == 1) {
+                mma_commit(&S.o_full[half]);
+                mma_commit(&S.empty[st]);
               }
-              product_s(half, st, half == halves - 1);
-              if (half == halves - 1) advance();
             }
+            __syncwarp();
+          }
+          if (!ok) break;
+          ph_p ^= 1;
+          advance();
+          if (j + 1 < steps) {
+            ok = mbar_wait_warp(&S.full[st], ph, abort);
+            if (!ok) break;
+            product_s();
           }
         }
       }
