@@ -33,9 +33,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;
 constexpr int kGroup = 1024;  // sequences of a launch
-constexpr int kMinRun = 2;    // units of a CTA at least: a piece costs about as much to start and to join
+constexpr int kLead = 3;      // units that starting and ending a tile costs (5.5 us, a step 1.5 to 1.8 us)
+constexpr int kMinRun = 2;    // units of a CTA at least
 
-// One piece of work: the units [u0, u1) of a tile, as every role of the CTA sees it.
+// One piece of work: the steps [u0, u1) of a tile, as every role of the CTA sees it.
 struct Piece {
   int b, h, row0, n, lead;  // sequence, KV head, first packed row, slots, slots before the chunk
   int r0, rows;             // the tile's first row, and the rows of the whole chunk
@@ -94,17 +95,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 // Work is counted in units: one 256-row tile of a KV head against 128 keys (a tile that
-// sees nothing counts one, so that its rows are written). The units of all tiles, in the
-// order (sequence, KV head, tile, keys), are cut into equal runs, one per CTA, whatever the
-// lengths: a CTA's run covers the end of one tile, whole tiles, and the start of another.
+// sees nothing counts one, so that its rows are written), and kLead more for starting a
+// tile. The units of all tiles, in the order (sequence, KV head, tile, lead, keys), are cut
+// into equal runs, one per CTA, whatever the lengths: a CTA's run covers the end of one
+// tile, whole tiles, and the start of another.
 // Whole tiles are written out; of a tile that is cut every piece stores its unnormalised
 // sum, and k_chunk_tc_join puts the pieces together. A CTA has two such pieces at most: the
 // one that starts its run (slot 2 cta) and the one that ends it (slot 2 cta + 1).
 __device__ __forceinline__ int tiles_of(const Seq& s, int group) {
   return int((int64_t(s.m) * group + kRows - 1) / kRows);
 }
-// units of tile t: steps of 128 keys up to the last slot that its last token sees
-__device__ __forceinline__ int units_of(const Seq& s, int group, int t) {
+// steps of tile t: 128 keys each, up to the last slot that its last token sees
+__device__ __forceinline__ int steps_of(const Seq& s, int group, int t) {
   const int64_t last = min(int64_t(t + 1) * kRows, int64_t(s.m) * group) - 1;
   const int see = min(s.n, s.n - s.m + int(last / group) + 1);
   return max(1, (see + kKeys - 1) / kKeys);
@@ -132,85 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort = &S.abort;
   const int qh = c.kvh * c.group;
 
-  // ---- where this CTA's run starts ----
-  int64_t* units = reinterpret_cast<int64_t*>(&S.kv[0][0][0]);  // of each sequence and KV head; the ring is not yet in use
-  static_assert(kGroup * 8 <= kKeys * 128, "one tile of the ring");
-  for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
-    const Seq s = seq_of(c, b);
-    const int tiles = tiles_of(s, c.group);
-    int64_t u = 0;
-    for (int t = lane; t < tiles; t += 32) u += units_of(s, c.group, t);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    if (lane == 0) units[b - b_begin] = u;  // of one KV head
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int64_t all = 0;
-    for (int b = lane; b < b_end - b_begin; b += 32) all += units[b] * c.kvh;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    const int64_t run = max(int64_t(kMinRun), (all + gridDim.x - 1) / int64_t(gridDim.x));
-    int64_t at = blockIdx.x * run;
-    const int64_t left = max(int64_t(0), min(run, all - at));
-    if (left > 0) {
-      // the sequence, by prefix sums of 32 at a time
-      int b = b_begin;
-      for (;; b += 32) {
-        const int64_t mine = b + lane < b_end ? units[b + lane - b_begin] * c.kvh : 0;
-        int64_t pre = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
-          if (lane >= o) pre += v;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, pre > at);
-        if (past) {
-          const int i = __ffs(past) - 1;
-          at -= __shfl_sync(0xffffffffu, pre - mine, i);
-          b += i;
-          break;
-        }
-        at -= __shfl_sync(0xffffffffu, pre, 31);
-      }
-      const int64_t per = units[b - b_begin];
-      const int h = int(at / per);
-      at -= h * per;
-      const Seq s = seq_of(c, b);
-      const int tiles = tiles_of(s, c.group);
-      int t = 0;
-      for (;; t += 32) {
-        const int64_t mine = t + lane < tiles ? units_of(s, c.group, t + lane) : 0;
-        int64_t pre = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
-          if (lane >= o) pre += v;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, pre > at);
-        if (past) {
-          const int i = __ffs(past) - 1;
-          at -= __shfl_sync(0xffffffffu, pre - mine, i);
-          t += i;
-          break;
-        }
-        at -= __shfl_sync(0xffffffffu, pre, 31);
-      }
-      if (lane == 0) {
-        S.start[0] = b;
-        S.start[1] = h;
-        S.start[2] = t;
-        S.start[3] = int(at);
-      }
-    }
-    if (lane == 0) {
-      S.left = left;
-      S.run = run;
-    }
-    fence_async();
-  }
-
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 320) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&S.full[i], 1);
       mbar_init(&S.empty[i], 2);  // both halves' products
@@ -234,6 +158,89 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // ---- where this CTA's run starts ----
+  int64_t* units = reinterpret_cast<int64_t*>(&S.kv[0][0][0]);  // of each sequence and KV head; the ring is not yet in use
+  static_assert(kGroup * 8 <= kKeys * 128, "one tile of the ring");
+  for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
+    const Seq s = seq_of(c, b);
+    const int tiles = tiles_of(s, c.group);
+    int64_t u = 0;
+    for (int t = lane; t < tiles; t += 32) u += kLead + steps_of(s, c.group, t);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    if (lane == 0) units[b - b_begin] = u;  // of one KV head
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t all = 0;
+    for (int b = lane; b < b_end - b_begin; b += 32) all += units[b] * c.kvh;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    const int64_t run = max(int64_t(kMinRun), (all + gridDim.x - 1) / int64_t(gridDim.x));
+    int64_t at = blockIdx.x * run;
+    int64_t left = max(int64_t(0), min(run, all - at));
+    if (left > 0) {
+      // the sequence, by prefix sums of 32 at a time
+      int b = b_begin;
+      bool found = false;
+      for (; b < b_end; b += 32) {
+        const int64_t mine = b + lane < b_end ? units[b + lane - b_begin] * c.kvh : 0;
+        int64_t pre = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, pre > at);
+        if (past) {
+          const int i = __ffs(past) - 1;
+          at -= __shfl_sync(0xffffffffu, pre - mine, i);
+          b += i;
+          found = true;
+          break;
+        }
+        at -= __shfl_sync(0xffffffffu, pre, 31);
+      }
+      const int64_t per = found ? units[b - b_begin] : 1;
+      const int h = int(at / per);
+      at -= h * per;
+      const Seq s = found ? seq_of(c, b) : Seq{0, 0, 0};
+      const int tiles = tiles_of(s, c.group);
+      int t = 0;
+      found = false;
+      for (; t < tiles; t += 32) {
+        const int64_t mine = t + lane < tiles ? kLead + steps_of(s, c.group, t + lane) : 0;
+        int64_t pre = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, pre > at);
+        if (past) {
+          const int i = __ffs(past) - 1;
+          at -= __shfl_sync(0xffffffffu, pre - mine, i);
+          t += i;
+          found = true;
+          break;
+        }
+        at -= __shfl_sync(0xffffffffu, pre, 31);
+      }
+      if (!found) left = 0;  // the lengths changed under the call: no work rather than wrong places
+      if (lane == 0) {
+        S.start[0] = b;
+        S.start[1] = h;
+        S.start[2] = t;
+        S.start[3] = int(at);
+      }
+    }
+    if (lane == 0) {
+      S.left = left;
+      S.run = run;
+    }
+    fence_async();
+  }
+
   fence_before();
   __syncthreads();
   fence_after();
@@ -249,14 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         cut.pieces = 0;
         int64_t left = S.left;
         const int64_t run = S.run, end = blockIdx.x * run + left;
-        int b = S.start[0], h = S.start[1], t = S.start[2], u0 = S.start[3];
+        int b = S.start[0], h = S.start[1], t = S.start[2], at = S.start[3];  // at: units into the tile
         Seq s = {0, 0, 0};
         int tiles = 0;
         if (left > 0) {
           s = seq_of(c, b);
           tiles = tiles_of(s, c.group);
         }
-        for (uint32_t i = 0;; ++i) {
+        for (uint32_t i = 0;;) {
           const int k = i & 1;
           if (!mbar_wait(&S.piece_empty[k], ((i >> 1) & 1) ^ 1, abort)) break;
           Piece& p = S.piece[k];
@@ -265,29 +272,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&S.piece_full[k]);
             break;
           }
-          const int units = units_of(s, c.group, t);
-          p.b = b;
-          p.h = h;
-          p.row0 = s.row0;
-          p.n = s.n;
-          p.lead = s.n - s.m;
-          p.r0 = t * kRows;
-          p.rows = s.m * c.group;
-          p.u0 = u0;
-          p.u1 = int(min(int64_t(units), u0 + left));
-          p.whole = u0 == 0 && p.u1 == units;
-          p.slot = 2 * int(blockIdx.x) + (i == 0 ? 0 : 1);
-          if (u0 == 0 && !p.whole) {
-            // this CTA begins the tile; the CTAs of the units up to the tile's last go on with it
-            cut.row = int64_t(s.row0) * qh + h * c.group;
-            cut.slot = p.slot;
-            cut.r0 = p.r0;
-            cut.rows = min(kRows, p.rows - p.r0);
-            cut.pieces = int((end - left + units - 1) / run) - int(blockIdx.x) + 1;
+          const int steps = steps_of(s, c.group, t);
+          const int to = int(min(int64_t(kLead + steps), at + left));
+          const int u0 = max(0, at - kLead), u1 = max(0, to - kLead);
+          if (u1 > u0) {  // a run that ends within the lead leaves the tile to the next
+            p.b = b;
+            p.h = h;
+            p.row0 = s.row0;
+            p.n = s.n;
+            p.lead = s.n - s.m;
+            p.r0 = t * kRows;
+            p.rows = s.m * c.group;
+            p.u0 = u0;
+            p.u1 = u1;
+            p.whole = u0 == 0 && u1 == steps;
+            p.slot = 2 * int(blockIdx.x) + (i == 0 ? 0 : 1);
+            if (u0 == 0 && !p.whole) {
+              // this CTA begins the tile; the CTAs of the units up to the tile's last go on with it
+              cut.row = int64_t(s.row0) * qh + h * c.group;
+              cut.slot = p.slot;
+              cut.r0 = p.r0;
+              cut.rows = min(kRows, p.rows - p.r0);
+              cut.pieces = int((end - left - at + kLead + steps - 1) / run) - int(blockIdx.x) + 1;
+            }
+            mbar_arrive(&S.piece_full[k]);
+            ++i;
           }
-          left -= p.u1 - u0;
-          mbar_arrive(&S.piece_full[k]);
-          u0 = 0;
+          left -= to - at;
+          at = 0;
           if (++t < tiles) continue;
           t = 0;
           if (++h < c.kvh) continue;
@@ -459,24 +471,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pc.u0 == pc.u1) break;
       if (r0 < rows) {
         const int64_t head = int64_t(pc.row0) * qh + pc.h * c.group;  // row of token 0's first head
-        // this half of Q into its swizzled place (16-byte chunk c of row r at c ^ (r % 8))
+        const int r = r0 + quarter * 32 + lane;
+        const int64_t row = head + int64_t(r / c.group) * qh + r % c.group;
+        // this thread's row of Q into its swizzled place (16-byte chunk i of row k at i ^ (k % 8))
         {
-          const int t = threadIdx.x & 127;
-#pragma unroll 8
-          for (int i = t; i < 128 * (D / 8); i += 128) {
-            const int r = i / (D / 8), ch = i % (D / 8), gr = r0 + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (gr < rows) {
-              const int64_t at = (head + int64_t(gr / c.group) * qh + gr % c.group) * D + ch * 8;
-              v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-            }
-            *reinterpret_cast<uint4*>(&S.q[half][ch >> 3][r * 64 + (((ch & 7) ^ (r & 7)) << 3)]) = v;
-          }
+          const int k = quarter * 32 + lane;
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D);
+          uint4 v[D / 8];
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) v[i] = r < rows ? src[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<uint4*>(&S.q[half][i >> 3][k * 64 + (((i & 7) ^ (k & 7)) << 3)]) = v[i];
           fence_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.q_full[half]);
         }
-        const int r = r0 + quarter * 32 + lane;
         // slots below this, counted from the piece's first, are seen
         int see = r < rows ? min(pc.n, pc.lead + r / c.group + 1) - pc.u0 * kKeys : 0;
         // the lowest limit of this warp's rows decides whether a step needs the mask at all
@@ -572,7 +582,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after();
         const float sum = lo2(l0) + hi2(l0) + lo2(l1) + hi2(l1);
-        const int64_t row = head + int64_t(r / c.group) * qh + r % c.group;
         const float inv = sum > 0.f ? 1.0f / sum : sum;
         const bool real = r < rows, whole = pc.whole;
         const int64_t at = int64_t(pc.slot) * slot_rows + (r - pc.r0);
@@ -612,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&S.piece_empty[i & 1]);
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -622,34 +632,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && S.abort) flag(c.status, MP_STATUS_WAIT_TIMEOUT);
 }
 
-// One warp per row of a tile that was cut: joins the pieces' (m, l, sum) in their order.
+// One warp per row of a tile that was cut: joins the pieces' (m, l, sum), eight at a time in
+// their order. Set up while k_chunk_tc still runs; it waits for it first.
 template <int D>
 __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const int slot_rows) {
+  constexpr int PER = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
   const int i = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (cut.pieces == 0 || i >= cut.rows) return;
   const int group = a.c.group, qh = a.c.kvh * group;
   auto at = [&](int p) { return int64_t(p == 0 ? cut.slot : 2 * (int(blockIdx.x) + p)) * slot_rows + i; };
+  const float2* ml = reinterpret_cast<const float2*>(a.ml);
   float m = -INFINITY;
-  for (int p = 0; p < cut.pieces; ++p) m = fmaxf(m, a.ml[at(p) * 2]);
-  float l = 0.f, o[D / 32];
+  for (int p = lane; p < cut.pieces; p += 32) m = fmaxf(m, ml[at(p)].x);
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
-  for (int p = 0; p < cut.pieces; ++p) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.ml + at(p) * 2);
-    if (ml.y == 0.f) continue;
-    const float by = exp2f(ml.x - m);
-    l = fmaf(ml.y, by, l);
+  for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[PER];
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) o[j] = fmaf(a.part[at(p) * D + j * 32 + lane], by, o[j]);
+  for (int j = 0; j < PER; ++j) o[j] = 0.f;
+  for (int p = 0; p < cut.pieces; p += 8) {
+    float x[8][PER], f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 v = p + k < cut.pieces ? ml[at(p + k)] : make_float2(-INFINITY, 0.f);
+      f[k] = v.y == 0.f ? 0.f : exp2f(v.x - ref);
+      l = fmaf(v.y, f[k], l);
+      const bool live = v.y != 0.f;  // a piece that saw nothing has written no sum
+#pragma unroll
+      for (int j = 0; j < PER; ++j) x[k][j] = live ? a.part[at(p + k) * D + lane * PER + j] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int j = 0; j < PER; ++j) o[j] = fmaf(x[k][j], f[k], o[j]);
   }
   const int r = cut.r0 + i;
   const int64_t row = cut.row + int64_t(r / group) * qh + r % group;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j)
-    static_cast<__nv_bfloat16*>(a.out)[row * D + j * 32 + lane] = __float2bfloat16(o[j] * inv);
+  for (int j = 0; j < PER; ++j)
+    static_cast<__nv_bfloat16*>(a.out)[row * D + lane * PER + j] = __float2bfloat16(o[j] * inv);
 }
 
 int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
@@ -676,7 +701,16 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
   a.part = reinterpret_cast<float*>(ws);
   for (int b = 0; b < c.batch; b += kGroup) {
     k_chunk_tc<D><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
-    k_chunk_tc_join<D><<<dim3(ctas, (slot_rows + 7) / 8), 256, 0, st>>>(a, slot_rows);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (slot_rows + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
