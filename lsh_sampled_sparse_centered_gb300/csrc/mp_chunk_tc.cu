@@ -15,7 +15,10 @@
 // P enters the second product as bf16 (2^-8 relative per weight); the sum of the weights
 // is taken before that rounding. Everything else is fp32.
 //
-// Tensor memory: S/P of the halves in columns 0 and 128, O in 256 and 256 + d.
+// Tensor memory: S of the halves in columns 0 and 128, O in 256 and 256 + d. With d = 128
+// that fills it and P overlays its S, so that the next S waits for the product with P. With
+// d = 64 P has columns of its own (384 and 448): the next S is formed while the softmax of
+// this one still runs.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -47,11 +50,12 @@ struct Piece {
 template <int D>
 struct Smem {
   static constexpr int kSub = D / 64;
+  static constexpr bool kOwnP = D == 64;  // P beside S
   static constexpr int kStages = D == 128 ? 5 : 8;
   __nv_bfloat16 q[2][kSub][128 * 64];
   __nv_bfloat16 kv[kStages][kSub][kKeys * 64];
   uint64_t full[kStages], empty[kStages], tail;
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];
+  uint64_t q_full[2], s_full[2], s_free[2], p_full[2][2], o_full[2];
   uint64_t piece_full[2], piece_empty[2];
   Piece piece[2];
   int64_t left, run;
@@ -143,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.q_full[i], 4);
       mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.s_free[i], 4);
       mbar_init(&S.p_full[i][0], 4);
       mbar_init(&S.p_full[i][1], 4);
       mbar_init(&S.piece_full[i], 1);
@@ -378,13 +383,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = sw128_desc(saddr(&S.q[half][0][0])), dk = sw128_desc(saddr(&S.kv[0][0][0])),
                      dv = sw128_desc_mn(saddr(&S.kv[0][0][0]));
       constexpr uint32_t kTile = kKeys * D * 2 / 16, kSlab = kKeys * 128 / 16;  // in descriptor units of 16 bytes
+      constexpr bool kOwnP = Smem<D>::kOwnP;
       const uint32_t t_s = tmem + uint32_t(half * 128), t_o = tmem + uint32_t(256 + half * D);
-      int st = 0;
-      uint32_t ph = 0, ph_q = 0, ph_p = 0;
-      auto advance = [&]() {
-        if (++st == kStages) {
-          st = 0;
+      const uint32_t t_p = kOwnP ? tmem + uint32_t(384 + half * 64) : t_s;
+      // The ring holds K and V tiles in turn. They are used in that order where P overlays S:
+      // one cursor (two cost 6 percent there). With P beside S a K tile is used before the V
+      // tile that precedes it: a cursor each.
+      int st = 0, v_st = 1;
+      uint32_t ph = 0, v_ph = 0, ph_q = 0, ph_p = 0, ph_f = 0;
+      auto advance = [&]() {  // st, ph: the next tile, or the next K tile
+        if ((st += kOwnP ? 2 : 1) >= kStages) {
+          st -= kStages;
           ph ^= 1;
+        }
+      };
+      auto advance_v = [&]() {
+        if (!kOwnP) return advance();
+        if ((v_st += 2) >= kStages) {
+          v_st -= kStages;
+          v_ph ^= 1;
         }
       };
       auto product_s = [&]() {
@@ -412,11 +429,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (steps == 0) break;
         if (!active) {  // the ring's tiles pass this half by
-          for (int j = 0; j < 2 * steps && ok; ++j) {
+          for (int j = 0; j < steps && ok; ++j) {
             ok = mbar_wait_warp(&S.full[st], ph, abort);
             if (ok && elect_one()) mbar_arrive(&S.empty[st]);
             __syncwarp();
             advance();
+            ok = ok && mbar_wait_warp(&S.full[kOwnP ? v_st : st], kOwnP ? v_ph : ph, abort);
+            if (ok && elect_one()) mbar_arrive(&S.empty[kOwnP ? v_st : st]);
+            __syncwarp();
+            advance_v();
           }
           continue;
         }
@@ -425,7 +446,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         product_s();
         for (int j = 0; j < steps; ++j) {
-          ok = mbar_wait_warp(&S.full[st], ph, abort);
+          if (kOwnP) {
+            // S is free once the softmax has it in registers
+            ok = mbar_wait_warp(&S.s_free[half], ph_f, abort);
+            if (!ok) break;
+            ph_f ^= 1;
+            if (j + 1 < steps) {
+              ok = mbar_wait_warp(&S.full[st], ph, abort);
+              if (!ok) break;
+              product_s();
+            }
+          }
+          ok = mbar_wait_warp(&S.full[kOwnP ? v_st : st], kOwnP ? v_ph : ph, abort);
           // P arrives in two parts of 64 keys: the product starts on the first
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
@@ -435,18 +467,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
 #pragma unroll
               for (int kk = part * 4; kk < part * 4 + 4; ++kk)
-                mma_bf16_ta(t_o, t_s + uint32_t(kk * 8), dv + st * kTile + kk * 128, id_o, (j > 0 || kk > 0) ? 1u : 0u);
+                mma_bf16_ta(t_o, t_p + uint32_t(kk * 8), dv + (kOwnP ? v_st : st) * kTile + kk * 128, id_o, (j > 0 || kk > 0) ? 1u : 0u);
               if (part == 1) {
                 mma_commit(&S.o_full[half]);
-                mma_commit(&S.empty[st]);
+                mma_commit(&S.empty[kOwnP ? v_st : st]);
               }
             }
             __syncwarp();
           }
           if (!ok) break;
           ph_p ^= 1;
-          advance();
-          if (j + 1 < steps) {
+          advance_v();
+          if (!kOwnP && j + 1 < steps) {
             ok = mbar_wait_warp(&S.full[st], ph, abort);
             if (!ok) break;
             product_s();
@@ -460,6 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2, quarter = warp & 3;
     const uint32_t ts = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * 128);
     const uint32_t to = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(256 + half * D);
+    constexpr bool kOwnP = Smem<D>::kOwnP;
+    const uint32_t tp = kOwnP ? tmem + (uint32_t(quarter * 32) << 16) + uint32_t(384 + half * 64) : ts;
     const float scale = kLog2e * rsqrtf(float(D));
     uint32_t ph_s = 0, ph_o = 0;  // phases of s_full, and of o_full's next completion
     bool ok = true;
@@ -505,6 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(ts + 64, x2);
           tmem_ld32(ts + 96, x3);
           tmem_wait_ld();
+          if (kOwnP) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.s_free[half]);
+          }
           if (see_low < kKeys) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -547,7 +586,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          ph_o ^= 1;  // past this step's second product
           const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = pk2(scale, scale), ref2 = pk2(-ref, -ref);
           uint32_t p[32];
@@ -564,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           };
           auto hand = [&](int part) {
-            tmem_st32(ts + part * 32, p);
+            tmem_st32(tp + part * 32, p);
             tmem_wait_st();
             fence_before();
             __syncwarp();
@@ -572,10 +610,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           weigh(x0, 0);
           weigh(x1, 16);
+          if (kOwnP && j > 0) {  // the last step's product has read P
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[half], ph_o ^ 1, abort));
+            if (!ok) break;
+            fence_after();
+          }
           hand(0);
           weigh(x2, 0);
           weigh(x3, 16);
           hand(1);
+          ph_o ^= 1;  // past this step's second product
         }
         if (!ok) break;
         ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[half], ph_o ^ 1, abort));
