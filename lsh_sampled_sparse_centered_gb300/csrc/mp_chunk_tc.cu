@@ -538,7 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(ts + 32, x1);
           tmem_ld32(ts + 64, x2);
           tmem_ld32(ts + 96, x3);
-          tmem_wait_ld();
+          tmem_wait_ld(x0);
+          tmem_tie(x1);
+          tmem_tie(x2);
+          tmem_tie(x3);
           if (kOwnP) {
             fence_before();
             __syncwarp();
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int g = 0; g < D / 32; ++g) {
                 uint32_t o[32];
                 tmem_ld32(to + g * 32, o);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
                 tmem_st32(to + g * 32, o);
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; g < D / 32; ++g) {
           uint32_t o[32];
           tmem_ld32(to + g * 32, o);
-          tmem_wait_ld();
+          tmem_wait_ld(o);
           if (!real) {
           } else if (!whole) {
             if (sum > 0.f) {

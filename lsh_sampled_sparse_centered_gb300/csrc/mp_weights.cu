@@ -7,10 +7,12 @@
 // Long chunks: k_weights_tc, keys as the M dimension of tcgen05 products (128 keys of a
 // CTA against 128 query rows at a time), so that a thread owns a key and sums along its
 // own accumulator row. The exponentials (128 x 128 a step) cost about as much as the
-// product; the accumulator is double buffered so that both run at once, and two CTAs
-// share an SM. Few rows: k_weights_step, one pass over K from global memory straight
+// product; two accumulators, each with a warpgroup that reads it, let both run at once,
+// and two CTAs share an SM. Few rows: k_weights_step, one pass over K from global memory straight
 // into the fragments of warp-level products, bound by that read.
 #include <cudaTypedefs.h>
+
+#include <algorithm>
 
 #include "mp_cache.cuh"
 #include "mp_tc.cuh"
@@ -21,6 +23,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKeys = 128, kCols = 128;  // keys of a CTA, query rows of a step
 constexpr int kLseSlots = 4;
+constexpr int kThreads = 320;  // two warpgroups of sums, a warp of loads, a warp of products
 
 template <int D>
 struct WSmem {
@@ -28,6 +31,7 @@ struct WSmem {
   __nv_bfloat16 k[kSub][kKeys * 64];
   __nv_bfloat16 q[2][kSub][kCols * 64];
   float nz[kLseSlots][kCols];  // -z of the step's rows
+  float sums[kKeys];           // of the second warpgroup
   uint64_t k_full, q_full[2], q_empty[2], s_full[2], s_empty[2], z_full[kLseSlots], z_empty[kLseSlots];
   uint32_t tmem_base;
   uint32_t abort;
@@ -66,7 +70,7 @@ __device__ __forceinline__ Block block_at(const Blocks& b, int i, int m) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(kThreads, 2)
     k_weights_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, const WeightsArgs a,
                  const int box) {
   extern __shared__ __align__(1024) unsigned char smraw[];
@@ -87,7 +91,7 @@ __global__ void __launch_bounds__(192, 2)
   const int steps = bl.n - i0;
 
   // rows of a block that no load fills stay zero
-  for (int i = threadIdx.x; i < int(sizeof(S.q) / 16); i += 192)
+  for (int i = threadIdx.x; i < int(sizeof(S.q) / 16); i += kThreads)
     reinterpret_cast<uint4*>(&S.q[0][0][0])[i] = make_uint4(0, 0, 0, 0);
   fence_async();
   if (threadIdx.x == 0) {
@@ -105,7 +109,7 @@ __global__ void __launch_bounds__(192, 2)
     S.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem_base)),
                  "r"(256)
                  : "memory");
@@ -115,8 +119,9 @@ __global__ void __launch_bounds__(192, 2)
   __syncthreads();
   fence_after();
   const uint32_t tmem = S.tmem_base;
+  float sum = 0.f;
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ---------------- the keys once, then blocks of query rows and their z ----------------
     const int live = min(kKeys, s.n - n0), boxes = (live + box - 1) / box;
     if (lane == 0) mbar_expect_tx(&S.k_full, uint32_t(boxes) * box * 128 * kSub);
@@ -166,59 +171,50 @@ __global__ void __launch_bounds__(192, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.z_full[zs]);
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---------------- products: S[key][row] ----------------
-    if (lane == 0) {
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kCols >> 3) << 17) | (uint32_t(kKeys >> 4) << 24);
-      bool ok = mbar_wait(&S.k_full, 0, abort);
-      for (int j = 0; j < steps && ok; ++j) {
-        const int st = j & 1, ph = (j >> 1) & 1;
-        ok = mbar_wait(&S.q_full[st], ph, abort) && mbar_wait(&S.s_empty[st], ph ^ 1, abort);
-        if (!ok) break;
-        fence_after();
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kCols >> 3) << 17) | (uint32_t(kKeys >> 4) << 24);
+    const uint64_t dk = sw128_desc(saddr(&S.k[0][0])), dq = sw128_desc(saddr(&S.q[0][0][0]));
+    constexpr uint32_t kTile = kCols * D * 2 / 16, kSlab = kKeys * 128 / 16;  // in descriptor units of 16 bytes
+    bool ok = mbar_wait_warp(&S.k_full, 0, abort);
+    for (int j = 0; j < steps && ok; ++j) {
+      const int st = j & 1, ph = (j >> 1) & 1;
+      ok = mbar_wait_warp(&S.q_full[st], ph, abort) && mbar_wait_warp(&S.s_empty[st], ph ^ 1, abort);
+      if (!ok) break;
+      fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const int u = kk >> 2, off = (kk & 3) * 32;
-          mma_bf16(tmem + uint32_t(st * kCols), sw128_desc(saddr(&S.k[u][0]) + off),
-                   sw128_desc(saddr(&S.q[st][u][0]) + off), idesc, kk > 0 ? 1u : 0u);
+          const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
+          mma_bf16(tmem + uint32_t(st * kCols), dk + off, dq + st * kTile + off, idesc, kk > 0 ? 1u : 0u);
         }
         mma_commit(&S.q_empty[st]);
         mma_commit(&S.s_full[st]);
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
-    // ---------------- one thread per key ----------------
-    const int slot = n0 + warp * 32 + lane;
-    const uint32_t ts = tmem + (uint32_t(warp * 32) << 16);
+    // ---------------- one thread per key and accumulator: blocks j = wg, wg + 2, ... ----------------
+    const int wg = warp >> 2, key = (warp & 3) * 32 + lane, slot = n0 + key;
+    const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(wg * kCols);
     const float scale = kLog2e * rsqrtf(float(D));
     const uint64_t sc2 = pk2(scale, scale);
-    float sum = 0.f;
-    for (int j = 0; j < steps; ++j) {
-      const int st = j & 1, zs = j % kLseSlots;
-      bool ok = mbar_wait(&S.s_full[st], (j >> 1) & 1, abort) && mbar_wait(&S.z_full[zs], (j / kLseSlots) & 1, abort);
+    for (int j = wg; j < steps; j += 2) {
+      const int zs = j % kLseSlots;
+      bool ok = mbar_wait(&S.z_full[zs], (j / kLseSlots) & 1, abort) && mbar_wait(&S.s_full[wg], (j >> 1) & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       fence_after();
-      uint32_t x0[32], x1[32], x2[32], x3[32];
-      const uint32_t at = ts + uint32_t(st * kCols);
-      tmem_ld32(at, x0);
-      tmem_ld32(at + 32, x1);
-      tmem_ld32(at + 64, x2);
-      tmem_ld32(at + 96, x3);
-      tmem_wait_ld();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.s_empty[st]);
       const Block x = block_at(bl, i0 + j, s.m);
       // columns [low, x.cols) see this thread's key
       const int dt = min(slot - first - x.t0, bl.per);
       const int low = dt <= 0 ? 0 : (bl.runs == 1 ? dt * bl.group : kCols);
       const bool last = bl.runs == 1 ? x.cols < bl.per * bl.group : x.cols < bl.heads;
+      const bool plain = !__any_sync(0xffffffffu, low > 0) && !last;
       const float* nz = S.nz[zs];
       uint64_t l0 = 0, l1 = 0;  // a step's own sums: two levels keep long chunks' sums exact
-      if (!__any_sync(0xffffffffu, low > 0) && !last) {
-        auto weigh = [&](const uint32_t (&v)[32], int col) {
+      auto weigh = [&](const uint32_t (&v)[32], int col) {
+        if (plain) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             const float4 n4 = *reinterpret_cast<const float4*>(nz + col + i);
@@ -227,36 +223,44 @@ __global__ void __launch_bounds__(192, 2)
             l0 = add2(l0, pk2(ex2(lo2(y0)), ex2(hi2(y0))));
             l1 = add2(l1, pk2(ex2(lo2(y1)), ex2(hi2(y1))));
           }
-        };
-        weigh(x0, 0);
-        weigh(x1, 32);
-        weigh(x2, 64);
-        weigh(x3, 96);
-      } else {
-        // rows outside the sequence may hold anything: selected away, not multiplied
-        float l = 0.f;
-        auto weigh = [&](const uint32_t (&v)[32], int col) {
+        } else {
+          // rows outside the sequence may hold anything: selected away, not multiplied
+          float l = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float e = ex2(fmaf(__uint_as_float(v[i]), scale, nz[col + i]));
             l += col + i >= low && col + i < x.cols ? e : 0.f;
           }
-        };
-        weigh(x0, 0);
-        weigh(x1, 32);
-        weigh(x2, 64);
-        weigh(x3, 96);
-        l0 = pk2(l, 0.f);
-      }
+          l0 = add2(l0, pk2(l, 0.f));
+        }
+      };
+      uint32_t v0[32], v1[32];
+      tmem_ld32(ts, v0);
+      tmem_wait_ld(v0);
+      tmem_ld32(ts + 32, v1);
+      weigh(v0, 0);
+      tmem_wait_ld(v1);
+      tmem_ld32(ts + 64, v0);
+      weigh(v1, 32);
+      tmem_wait_ld(v0);
+      tmem_ld32(ts + 96, v1);
+      weigh(v0, 64);
+      tmem_wait_ld(v1);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.s_empty[wg]);
+      weigh(v1, 96);
       sum += (lo2(l0) + hi2(l0)) + (lo2(l1) + hi2(l1));
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.z_empty[zs]);
     }
-    if (slot < s.n) a.scores[(int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size) + slot] += sum;
+    if (wg == 1) S.sums[key] = sum;
   }
   fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp < 4 && n0 + int(threadIdx.x) < s.n && !S.abort)
+    a.scores[(int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size) + n0 + threadIdx.x] += sum + S.sums[threadIdx.x];
+  if (warp == 9) {
     __syncwarp();
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
@@ -266,23 +270,51 @@ __global__ void __launch_bounds__(192, 2)
 
 // ---- few query rows ----
 
-constexpr int kStepWarps = 8, kStepKeys = 64;  // keys of a warp
+constexpr int kStepWarps = 4, kRound = 16;  // keys of a warp and round
 
 // 16 keys (M) x 8 NT query rows (N) per warp and round. The sum over d has no order to
 // keep, so lane t of a row's four takes the 16-byte chunks t, t + 4, ... and feeds their
-// halves to two products: the loads are whole vectors and need no shared memory.
+// halves to two products: the loads are whole vectors and need no shared memory. The next
+// round's keys are loaded as soon as their registers are free, their places looked up a
+// round before that.
 template <int D, int NT>
 __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsArgs a) {
-  constexpr int kChunks = D / 32;  // 16-byte chunks of a row per lane
+  constexpr int KC = D / 32;  // 16-byte chunks of a row per lane
   const CacheArgs& c = a.c;
   const int b = blockIdx.z, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Seq s = seq_of(c, b);
-  const int w0 = (blockIdx.x * kStepWarps + warp) * kStepKeys;
-  if (w0 >= s.n || s.m == 0) return;
+  constexpr int kAll = kStepWarps * kRound;
+  const int per = ((s.n + int(gridDim.x) - 1) / int(gridDim.x) + kAll - 1) / kAll * kAll;
+  const int64_t p0 = int64_t(blockIdx.x) * per;
+  if (p0 >= s.n || s.m == 0) return;
+  const int p1 = min(s.n, int(p0) + per);
   const int first = s.n - s.m, qh = c.kvh * c.group, rows = s.m * c.group;
   const float scale = kLog2e * rsqrtf(float(D));
-  uint4 q[NT][kChunks];
+  float* scores = a.scores + (int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size);
+  const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.keys);
+  uint4 k[2][KC];
+  int row[2];
+  float old[2];
+  auto find = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) row[i] = slot_row(c, b, h, min(n0 + g + 8 * i, s.n - 1));
+  };
+  auto load = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __nv_bfloat16* src = keys + int64_t(row[i]) * D + t * 8;
+#pragma unroll
+      for (int j = 0; j < KC; ++j) k[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + j * 32));
+      old[i] = t == 0 ? scores[min(n0 + g + 8 * i, s.n - 1)] : 0.f;
+    }
+  };
+  int n0 = int(p0) + warp * kRound;
+  if (n0 >= p1) return;
+  find(n0);
+  load(n0);
+  find(n0 + kAll);
+  uint4 q[NT][KC];
   float nz[NT][2];
   int see[NT][2];  // the thread's columns see the slots below this
 #pragma unroll
@@ -291,7 +323,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsA
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
                                (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D + t * 8;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
+    for (int i = 0; i < KC; ++i)
       q[u][i] = r < rows ? *reinterpret_cast<const uint4*>(src + i * 32) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -300,41 +332,36 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsA
       nz[u][i] = rc < rows ? -kLog2e * a.lse[int64_t(s.row0 + rc / c.group) * qh + h * c.group + rc % c.group] : 0.f;
     }
   }
-  float* scores = a.scores + (int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size);
-  const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.keys);
-#pragma unroll 2
-  for (int k0 = w0; k0 < min(s.n, w0 + kStepKeys); k0 += 16) {
-    uint4 k[2][kChunks];
-    float old[2];
+  for (; n0 < p1; n0 += kAll) {
+    const int next = n0 + kAll;
+    float x[NT][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int slot = min(k0 + g + 8 * i, s.n - 1);
-      const __nv_bfloat16* src = keys + slot_read(c, b, h, slot) + t * 8;
+    for (int u = 0; u < NT; ++u) {
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j) k[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + j * 32));
-      old[i] = t == 0 ? scores[slot] : 0.f;
+      for (int i = 0; i < 4; ++i) x[u][i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        mma_16816(x[u], k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y, q[u][j].x, q[u][j].y);
+        mma_16816(x[u], k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w, q[u][j].z, q[u][j].w);
+      }
+    }
+    const float was[2] = {old[0], old[1]};
+    if (next < p1) {
+      load(next);
+      find(next + kAll);
     }
     float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j) {
-        mma_16816(x, k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y, q[u][j].x, q[u][j].y);
-        mma_16816(x, k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w, q[u][j].z, q[u][j].w);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int slot = k0 + g + 8 * (i >> 1);
-        if (slot < see[u][i & 1]) sum[i >> 1] += ex2(fmaf(x[i], scale, nz[u][i & 1]));
-      }
-    }
+      for (int i = 0; i < 4; ++i)
+        if (n0 + g + 8 * (i >> 1) < see[u][i & 1]) sum[i >> 1] += ex2(fmaf(x[u][i], scale, nz[u][i & 1]));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-      const int slot = k0 + g + 8 * i;
-      if (t == 0 && slot < s.n) scores[slot] = old[i] + sum[i];
+      const int slot = n0 + g + 8 * i;
+      if (t == 0 && slot < s.n) scores[slot] = was[i] + sum[i];
     }
   }
 }
@@ -344,7 +371,10 @@ cudaError_t launch(const WeightsArgs& a, cudaStream_t st) {
   const CacheArgs& c = a.c;
   const int64_t rows = int64_t(c.max_q) * c.group;
   if (rows <= 32) {
-    const dim3 grid((c.max_kv + kStepWarps * kStepKeys - 1) / (kStepWarps * kStepKeys), c.kvh, c.batch);
+    // slices of at least four rounds, one wave of the CTAs that fit
+    const int64_t fit = int64_t(device_sm_count()) * (rows <= 16 ? 5 : 3) / (int64_t(c.kvh) * c.batch);
+    const int64_t most = (c.max_kv + 4 * kStepWarps * kRound - 1) / (4 * kStepWarps * kRound);
+    const dim3 grid(unsigned(std::max<int64_t>(1, std::min(fit, most))), c.kvh, c.batch);
     if (rows <= 8) k_weights_step<D, 1><<<grid, kStepWarps * 32, 0, st>>>(a);
     else if (rows <= 16) k_weights_step<D, 2><<<grid, kStepWarps * 32, 0, st>>>(a);
     else k_weights_step<D, 4><<<grid, kStepWarps * 32, 0, st>>>(a);
@@ -359,7 +389,7 @@ cudaError_t launch(const WeightsArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(WSmem<D>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k_weights_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  k_weights_tc<D><<<dim3((c.max_kv + kKeys - 1) / kKeys, c.kvh, c.batch), 192, smem, st>>>(mk, mq, a, box);
+  k_weights_tc<D><<<dim3((c.max_kv + kKeys - 1) / kKeys, c.kvh, c.batch), kThreads, smem, st>>>(mk, mq, a, box);
   return cudaGetLastError();
 }
 
