@@ -4,11 +4,13 @@
 // the row's log-sum-exp in log2. Nothing but K, Q and z is read; each key's sum has one
 // owner, so the order of its additions is fixed and no atomics are needed.
 //
-// Long chunks: k_weights_tc, keys as the M dimension of tcgen05 products (128 keys of a
-// CTA against 128 query rows at a time), so that a thread owns a key and sums along its
-// own accumulator row. The exponentials (128 x 128 a step) cost about as much as the
-// product; two accumulators, each with a warpgroup that reads it, let both run at once,
-// and two CTAs share an SM. Few rows: k_weights_step, one pass over K from global memory straight
+// Long chunks: k_weights_tc, keys as the M dimension of tcgen05 products (256 keys of a
+// CTA, as two halves, against 128 query rows at a time), so that a thread owns a key and
+// sums along its own accumulator row. The exponentials (256 x 128 a step) cost about as
+// much as the products; each half has two accumulators, and each of the four a warpgroup
+// that reads it, so that all run at once. Every CTA reads all query rows: with 128 keys a
+// CTA that stream (7 TB/s out of L2) was the bound (154 us for 1000 tokens of 32 heads over
+// 16384 slots). Few rows: k_weights_step, one pass over K from global memory straight
 // into the fragments of warp-level products, bound by that read.
 #include <cudaTypedefs.h>
 
@@ -21,18 +23,19 @@ namespace mp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kKeys = 128, kCols = 128;  // keys of a CTA, query rows of a step
-constexpr int kLseSlots = 4;
-constexpr int kThreads = 320;  // two warpgroups of sums, a warp of loads, a warp of products
+constexpr int kHalf = 128, kKeys = 256, kCols = 128;  // keys of a product and of a CTA, query rows of a step
+constexpr int kLseSlots = 8;
+constexpr int kThreads = 608;  // four warpgroups of sums, a warp each of loads, products and z
 
 template <int D>
 struct WSmem {
   static constexpr int kSub = D / 64;
-  __nv_bfloat16 k[kSub][kKeys * 64];
-  __nv_bfloat16 q[2][kSub][kCols * 64];
+  static constexpr int kStages = D == 128 ? 4 : 6;
+  __nv_bfloat16 k[2][kSub][kHalf * 64];
+  __nv_bfloat16 q[kStages][kSub][kCols * 64];
   float nz[kLseSlots][kCols];  // -z of the step's rows
-  float sums[kKeys];           // of the second warpgroup
-  uint64_t k_full, q_full[2], q_empty[2], s_full[2], s_empty[2], z_full[kLseSlots], z_empty[kLseSlots];
+  float sums[kKeys];           // of the second accumulators
+  uint64_t k_full, q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2], z_full[kLseSlots], z_empty[kLseSlots];
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -70,13 +73,13 @@ __device__ __forceinline__ Block block_at(const Blocks& b, int i, int m) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     k_weights_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, const WeightsArgs a,
                  const int box) {
   extern __shared__ __align__(1024) unsigned char smraw[];
   const uint32_t base = saddr(smraw);
   WSmem<D>& S = *reinterpret_cast<WSmem<D>*>(smraw + ((1024 - (base & 1023)) & 1023));
-  constexpr int kSub = WSmem<D>::kSub;
+  constexpr int kSub = WSmem<D>::kSub, kStages = WSmem<D>::kStages;
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.z, h = blockIdx.y, n0 = blockIdx.x * kKeys;
@@ -89,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int t_start = max(0, n0 - first);
   const int i0 = bl.runs == 1 ? t_start / bl.per : t_start * bl.runs;
   const int steps = bl.n - i0;
+  const int halves = s.n - n0 > kHalf ? 2 : 1;
 
   // rows of a block that no load fills stay zero
   for (int i = threadIdx.x; i < int(sizeof(S.q) / 16); i += kThreads)
@@ -96,22 +100,24 @@ __global__ void __launch_bounds__(kThreads, 2)
   fence_async();
   if (threadIdx.x == 0) {
     mbar_init(&S.k_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&S.q_full[i], 1);
       mbar_init(&S.q_empty[i], 1);
-      mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.s_empty[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&S.s_full[i >> 1][i & 1], 1);
+      mbar_init(&S.s_empty[i >> 1][i & 1], 4);
     }
     for (int i = 0; i < kLseSlots; ++i) {
       mbar_init(&S.z_full[i], 1);
-      mbar_init(&S.z_empty[i], 4);
+      mbar_init(&S.z_empty[i], 4 * halves);
     }
     S.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == 17) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem_base)),
-                 "r"(256)
+                 "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -121,36 +127,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = S.tmem_base;
   float sum = 0.f;
 
-  if (warp == 8) {
-    // ---------------- the keys once, then blocks of query rows and their z ----------------
+  if (warp == 16) {
+    // ---------------- the keys once, then blocks of query rows ----------------
     const int live = min(kKeys, s.n - n0), boxes = (live + box - 1) / box;
     if (lane == 0) mbar_expect_tx(&S.k_full, uint32_t(boxes) * box * 128 * kSub);
     __syncwarp();
     for (int i = lane; i < boxes; i += 32) {
       const int row = slot_row(c, b, h, n0 + i * box);
 #pragma unroll
-      for (int u = 0; u < kSub; ++u) tma_load_2d(&S.k[u][i * box * 64], &tmK, u * 64, row, &S.k_full);
+      for (int u = 0; u < kSub; ++u)
+        tma_load_2d(&S.k[i * box / kHalf][u][i * box % kHalf * 64], &tmK, u * 64, row, &S.k_full);
     }
-    auto load_z = [&](int j, float (&z)[4]) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) z[u] = INFINITY;  // columns without a row: 2^-inf
-      if (j >= steps) return;
-      const Block x = block_at(bl, i0 + j, s.m);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int col = u * 32 + lane;
-        if (col < x.cols) {
-          const int t = x.t0 + (bl.runs == 1 ? col / bl.group : 0), g = bl.runs == 1 ? col % bl.group : x.h0 + col;
-          z[u] = a.lse[int64_t(s.row0 + t) * qh + h * c.group + g];
-        }
-      }
-    };
-    float z[4];
-    load_z(0, z);
     bool ok = true;
+    int st = 0;
+    uint32_t ph = 1;
     for (int j = 0; j < steps; ++j) {
-      const int st = j & 1, zs = j % kLseSlots;
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.q_empty[st], ((j >> 1) & 1) ^ 1, abort));
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.q_empty[st], ph, abort));
       if (!ok) break;
       if (lane == 0) {
         const Block x = block_at(bl, i0 + j, s.m);
@@ -159,49 +151,89 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int u = 0; u < kSub; ++u)
           tma_load_3d(&S.q[st][u][0], &tmQ, u * 64, h * c.group + x.h0, s.row0 + x.t0, &S.q_full[st]);
       }
-      float next[4];
-      load_z(j + 1, next);
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.z_empty[zs], ((j / kLseSlots) & 1) ^ 1, abort));
-      if (!ok) break;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        S.nz[zs][u * 32 + lane] = -z[u] * kLog2e;
-        z[u] = next[u];
-      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.z_full[zs]);
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1;
+      }
     }
-  } else if (warp == 9) {
-    // ---------------- products: S[key][row] ----------------
-    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kCols >> 3) << 17) | (uint32_t(kKeys >> 4) << 24);
-    const uint64_t dk = sw128_desc(saddr(&S.k[0][0])), dq = sw128_desc(saddr(&S.q[0][0][0]));
-    constexpr uint32_t kTile = kCols * D * 2 / 16, kSlab = kKeys * 128 / 16;  // in descriptor units of 16 bytes
-    bool ok = mbar_wait_warp(&S.k_full, 0, abort);
-    for (int j = 0; j < steps && ok; ++j) {
-      const int st = j & 1, ph = (j >> 1) & 1;
-      ok = mbar_wait_warp(&S.q_full[st], ph, abort) && mbar_wait_warp(&S.s_empty[st], ph ^ 1, abort);
-      if (!ok) break;
-      fence_after();
-      if (elect_one()) {
+  } else if (warp == 18) {
+    // ---------------- -z of the rows, four steps' loads at a time ----------------
+    // (one step at a time, the latency of its loads was what a step took: 146 us where
+    // 16384 slots see 1000 tokens of 32 heads)
+    int tok[4], head[4];  // of this lane's columns within a block
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
-          mma_bf16(tmem + uint32_t(st * kCols), dk + off, dq + st * kTile + off, idesc, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&S.q_empty[st]);
-        mma_commit(&S.s_full[st]);
+    for (int u = 0; u < 4; ++u) {
+      const int col = u * 32 + lane;
+      tok[u] = bl.runs == 1 ? col / bl.group : 0;
+      head[u] = col - tok[u] * bl.group;
+    }
+    bool ok = true;
+    for (int j0 = 0; j0 < steps && ok; j0 += 4) {
+      float z[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const Block x = block_at(bl, i0 + min(j0 + k, steps - 1), s.m);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          z[k][u] = u * 32 + lane < x.cols
+                        ? a.lse[int64_t(s.row0 + x.t0 + tok[u]) * qh + h * c.group + x.h0 + head[u]]
+                        : INFINITY;  // columns without a row: 2^-inf
       }
-      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (j0 + k >= steps) break;
+        const int zs = (j0 + k) % kLseSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.z_empty[zs], (((j0 + k) / kLseSlots) & 1) ^ 1, abort));
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) S.nz[zs][u * 32 + lane] = -z[k][u] * kLog2e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.z_full[zs]);
+      }
+    }
+  } else if (warp == 17) {
+    // ---------------- products: S[key][row] ----------------
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kCols >> 3) << 17) | (uint32_t(kHalf >> 4) << 24);
+    const uint64_t dk = sw128_desc(saddr(&S.k[0][0][0])), dq = sw128_desc(saddr(&S.q[0][0][0]));
+    constexpr uint32_t kTile = kCols * D * 2 / 16, kSlab = kHalf * 128 / 16;  // in descriptor units of 16 bytes
+    bool ok = mbar_wait_warp(&S.k_full, 0, abort);
+    int st = 0;
+    uint32_t ph = 0;
+    for (int j = 0; j < steps && ok; ++j) {
+      ok = mbar_wait_warp(&S.q_full[st], ph, abort);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (half >= halves) break;
+        ok = ok && mbar_wait_warp(&S.s_empty[half][j & 1], ((j >> 1) & 1) ^ 1, abort);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
+            mma_bf16(tmem + uint32_t((half * 2 + (j & 1)) * kCols), dk + half * kTile + off, dq + st * kTile + off, idesc,
+                     kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&S.s_full[half][j & 1]);
+          if (half == halves - 1) mma_commit(&S.q_empty[st]);
+        }
+        __syncwarp();
+      }
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1;
+      }
     }
   } else {
-    // ---------------- one thread per key and accumulator: blocks j = wg, wg + 2, ... ----------------
-    const int wg = warp >> 2, key = (warp & 3) * 32 + lane, slot = n0 + key;
-    const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(wg * kCols);
+    // ---------------- one thread per key and accumulator: blocks j = buf, buf + 2, ... ----------------
+    const int half = warp >> 3, buf = (warp >> 2) & 1, slot = n0 + half * kHalf + (warp & 3) * 32 + lane;
+    const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t((half * 2 + buf) * kCols);
     const float scale = kLog2e * rsqrtf(float(D));
     const uint64_t sc2 = pk2(scale, scale);
-    for (int j = wg; j < steps; j += 2) {
+    for (int j = buf; half < halves && j < steps; j += 2) {
       const int zs = j % kLseSlots;
-      bool ok = mbar_wait(&S.z_full[zs], (j / kLseSlots) & 1, abort) && mbar_wait(&S.s_full[wg], (j >> 1) & 1, abort);
+      bool ok = mbar_wait(&S.z_full[zs], (j / kLseSlots) & 1, abort) && mbar_wait(&S.s_full[half][buf], (j >> 1) & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       fence_after();
@@ -248,22 +280,25 @@ __global__ void __launch_bounds__(kThreads, 2)
       tmem_wait_ld(v1);
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.s_empty[wg]);
+      if (lane == 0) mbar_arrive(&S.s_empty[half][buf]);
       weigh(v1, 96);
       sum += (lo2(l0) + hi2(l0)) + (lo2(l1) + hi2(l1));
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.z_empty[zs]);
     }
-    if (wg == 1) S.sums[key] = sum;
+    if (buf == 1) S.sums[slot - n0] = sum;
   }
   fence_before();
   __syncthreads();
-  if (warp < 4 && n0 + int(threadIdx.x) < s.n && !S.abort)
-    a.scores[(int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size) + n0 + threadIdx.x] += sum + S.sums[threadIdx.x];
-  if (warp == 9) {
+  if (warp < 16 && !(warp & 4)) {
+    const int key = (warp >> 3) * kHalf + (warp & 3) * 32 + lane;
+    if (n0 + key < s.n && !S.abort)
+      a.scores[(int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size) + n0 + key] += sum + S.sums[key];
+  }
+  if (warp == 17) {
     __syncwarp();
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
   if (threadIdx.x == 0 && S.abort) flag(c.status, MP_STATUS_WAIT_TIMEOUT);
 }
