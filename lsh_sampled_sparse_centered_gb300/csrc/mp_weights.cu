@@ -25,7 +25,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHalf = 128, kKeys = 256, kCols = 128;  // keys of a product and of a CTA, query rows of a step
 constexpr int kLseSlots = 8;
-constexpr int kThreads = 608;  // four warpgroups of sums, a warp each of loads, products and z
+constexpr int kThreads = 640;  // four warpgroups of sums, a warp each of loads and z, two of products
 
 template <int D>
 struct WSmem {
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&S.k_full, 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&S.q_full[i], 1);
-      mbar_init(&S.q_empty[i], 1);
+      mbar_init(&S.q_empty[i], halves);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&S.s_full[i >> 1][i & 1], 1);
@@ -192,34 +192,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&S.z_full[zs]);
       }
     }
-  } else if (warp == 17) {
-    // ---------------- products: S[key][row] ----------------
+  } else if (warp >= 16) {
+    // ---------------- products S[key][row]: warp 17 for the first half of the keys, 19 for the
+    // second, so that one's products run while the other waits ----------------
+    const int half = warp == 17 ? 0 : 1;
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kCols >> 3) << 17) | (uint32_t(kHalf >> 4) << 24);
-    const uint64_t dk = sw128_desc(saddr(&S.k[0][0][0])), dq = sw128_desc(saddr(&S.q[0][0][0]));
+    const uint64_t dk = sw128_desc(saddr(&S.k[half][0][0])), dq = sw128_desc(saddr(&S.q[0][0][0]));
     constexpr uint32_t kTile = kCols * D * 2 / 16, kSlab = kHalf * 128 / 16;  // in descriptor units of 16 bytes
-    bool ok = mbar_wait_warp(&S.k_full, 0, abort);
+    bool ok = half < halves && mbar_wait_warp(&S.k_full, 0, abort);
     int st = 0;
     uint32_t ph = 0;
     for (int j = 0; j < steps && ok; ++j) {
-      ok = mbar_wait_warp(&S.q_full[st], ph, abort);
+      ok = mbar_wait_warp(&S.q_full[st], ph, abort) &&
+           mbar_wait_warp(&S.s_empty[half][j & 1], ((j >> 1) & 1) ^ 1, abort);
+      if (!ok) break;
+      fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half >= halves) break;
-        ok = ok && mbar_wait_warp(&S.s_empty[half][j & 1], ((j >> 1) & 1) ^ 1, abort);
-        if (!ok) break;
-        fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
-            mma_bf16(tmem + uint32_t((half * 2 + (j & 1)) * kCols), dk + half * kTile + off, dq + st * kTile + off, idesc,
-                     kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&S.s_full[half][j & 1]);
-          if (half == halves - 1) mma_commit(&S.q_empty[st]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
+          mma_bf16(tmem + uint32_t((half * 2 + (j & 1)) * kCols), dk + off, dq + st * kTile + off, idesc, kk > 0 ? 1u : 0u);
         }
-        __syncwarp();
+        mma_commit(&S.s_full[half][j & 1]);
+        mma_commit(&S.q_empty[st]);
       }
+      __syncwarp();
       if (++st == kStages) {
         st = 0;
         ph ^= 1;
