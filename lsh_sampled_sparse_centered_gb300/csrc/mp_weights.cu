@@ -6,12 +6,19 @@
 //
 // Long chunks: k_weights_tc, keys as the M dimension of tcgen05 products (256 keys of a
 // CTA, as two halves, against 128 query rows at a time), so that a thread owns a key and
-// sums along its own accumulator row. The exponentials (256 x 128 a step) cost about as
-// much as the products; each half has two accumulators, and each of the four a warpgroup
-// that reads it, so that all run at once. Every CTA reads all query rows: with 128 keys a
-// CTA that stream (7 TB/s out of L2) was the bound (154 us for 1000 tokens of 32 heads over
-// 16384 slots). Few rows: k_weights_step, one pass over K from global memory straight
-// into the fragments of warp-level products, bound by that read.
+// sums along its accumulator row. -z enters through one more K step, after the others: a
+// column (1, 1, 1, 0, ...) of the keys times the split of -z sqrt(d) into three bf16 terms
+// (exact to fp32), so that the threads neither load nor add it. Each half has two
+// accumulators and each of the four a warpgroup that reads it, so that products and
+// exponentials of both run at once. A step costs an SM about 1024 clocks of products, 1024
+// of exponentials, and of shared memory 1152 for the products' operands and 288 for the
+// loads (with z read from shared memory by every thread 512 more: FIGZ).
+// Products of 256 columns need a quarter less of it, but leave no room for second
+// accumulators and deep enough loads (140 us where this takes FIGN: 16384 slots, 1000 tokens
+// of 32 heads).
+//
+// Few rows: k_weights_step, one pass over K from global memory straight into the fragments
+// of warp-level products, bound by that read.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -24,18 +31,18 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHalf = 128, kKeys = 256, kCols = 128;  // keys of a product and of a CTA, query rows of a step
-constexpr int kLseSlots = 8;
 constexpr int kThreads = 640;  // four warpgroups of sums, a warp each of loads and z, two of products
 
 template <int D>
 struct WSmem {
   static constexpr int kSub = D / 64;
-  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   __nv_bfloat16 k[2][kSub][kHalf * 64];
   __nv_bfloat16 q[kStages][kSub][kCols * 64];
-  float nz[kLseSlots][kCols];  // -z of the step's rows
-  float sums[kKeys];           // of the second accumulators
-  uint64_t k_full, q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2], z_full[kLseSlots], z_empty[kLseSlots];
+  __nv_bfloat16 z[kStages][kCols * 16];  // (hi, mid, lo, 0, ...) of the step's rows (32-byte swizzle)
+  __nv_bfloat16 ones[kHalf * 16];        // rows (1, 1, 1, 0, ...) (32-byte swizzle)
+  float sums[kKeys];                     // of the second accumulators
+  uint64_t k_full, q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2];
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -94,23 +101,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int steps = bl.n - i0;
   const int halves = s.n - n0 > kHalf ? 2 : 1;
 
-  // rows of a block that no load fills stay zero
-  for (int i = threadIdx.x; i < int(sizeof(S.q) / 16); i += kThreads)
-    reinterpret_cast<uint4*>(&S.q[0][0][0])[i] = make_uint4(0, 0, 0, 0);
+  // rows of a block that no load fills stay zero, and so does all but the first three elements
+  // of z and ones
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < int(sizeof(S.z) / 16); i += kThreads) reinterpret_cast<uint4*>(&S.z[0][0])[i] = zero;
+  const int filled = bl.heads * bl.per;  // rows of a full load
+  for (int i = threadIdx.x; i < (kCols - filled) * 8 * kSub * kStages; i += kThreads)
+    reinterpret_cast<uint4*>(&S.q[0][0][0])[(i / ((kCols - filled) * 8)) * (kCols * 8) + filled * 8 + i % ((kCols - filled) * 8)] = zero;
+  for (int r = threadIdx.x; r < kHalf; r += kThreads) {
+    uint4* row = reinterpret_cast<uint4*>(&S.ones[r * 16]);  // 16-byte chunk i of row r at i ^ (r / 4 % 2)
+    row[(r >> 2) & 1] = make_uint4(0x3f803f80u, 0x00003f80u, 0, 0);
+    row[1 - ((r >> 2) & 1)] = zero;
+  }
   fence_async();
   if (threadIdx.x == 0) {
     mbar_init(&S.k_full, 1);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&S.q_full[i], 1);
+      mbar_init(&S.q_full[i], 2);  // the load and z
       mbar_init(&S.q_empty[i], halves);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&S.s_full[i >> 1][i & 1], 1);
       mbar_init(&S.s_empty[i >> 1][i & 1], 4);
-    }
-    for (int i = 0; i < kLseSlots; ++i) {
-      mbar_init(&S.z_full[i], 1);
-      mbar_init(&S.z_empty[i], 4 * halves);
     }
     S.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -158,39 +170,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 18) {
-    // ---------------- -z of the rows, four steps' loads at a time ----------------
-    // (one step at a time, the latency of its loads was what a step took: 146 us where
-    // 16384 slots see 1000 tokens of 32 heads)
-    int tok[4], head[4];  // of this lane's columns within a block
+    // ---------------- -z of the rows, the next step's loads in flight ----------------
+    constexpr int kPer = kCols / 32;
+    int tok[kPer], head[kPer];  // of this lane's columns within a block
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kPer; ++u) {
       const int col = u * 32 + lane;
       tok[u] = bl.runs == 1 ? col / bl.group : 0;
       head[u] = col - tok[u] * bl.group;
     }
+    const float root = sqrtf(float(D));
+    auto load_z = [&](int j, float (&z)[kPer]) {
+      const Block x = block_at(bl, i0 + min(j, steps - 1), s.m);
+#pragma unroll
+      for (int u = 0; u < kPer; ++u)
+        z[u] = u * 32 + lane < x.cols ? a.lse[int64_t(s.row0 + x.t0 + tok[u]) * qh + h * c.group + x.h0 + head[u]]
+                                      : INFINITY;  // columns without a row: 2^-inf
+    };
     bool ok = true;
-    for (int j0 = 0; j0 < steps && ok; j0 += 4) {
-      float z[4][4];
+    int st = 0;
+    uint32_t ph = 1;
+    float z0[kPer], z1[kPer];
+    auto put = [&](const float (&z)[kPer]) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.q_empty[st], ph, abort));
+      if (!ok) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const Block x = block_at(bl, i0 + min(j0 + k, steps - 1), s.m);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          z[k][u] = u * 32 + lane < x.cols
-                        ? a.lse[int64_t(s.row0 + x.t0 + tok[u]) * qh + h * c.group + x.h0 + head[u]]
-                        : INFINITY;  // columns without a row: 2^-inf
+      for (int u = 0; u < kPer; ++u) {
+        const int r = u * 32 + lane;
+        const float v = -z[u] * root;
+        const __nv_bfloat16 hi = __float2bfloat16(v);
+        const float rest = isinf(v) ? 0.f : v - __bfloat162float(hi);
+        const __nv_bfloat16 mid = __float2bfloat16(rest);
+        const float low = rest - __bfloat162float(mid);
+        *reinterpret_cast<uint2*>(&S.z[st][r * 16 + ((r >> 2) & 1) * 8]) =
+            make_uint2(uint32_t(__bfloat16_as_ushort(hi)) | uint32_t(__bfloat16_as_ushort(mid)) << 16, bf2(low, 0.f));
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (j0 + k >= steps) break;
-        const int zs = (j0 + k) % kLseSlots;
-        ok = __all_sync(0xffffffffu, mbar_wait(&S.z_empty[zs], (((j0 + k) / kLseSlots) & 1) ^ 1, abort));
-        if (!ok) break;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) S.nz[zs][u * 32 + lane] = -z[k][u] * kLog2e;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.z_full[zs]);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.q_full[st]);
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1;
       }
+    };
+    load_z(0, z0);
+    for (int j = 0; j < steps && ok; j += 2) {
+      load_z(j + 1, z1);
+      put(z0);
+      if (j + 1 >= steps || !ok) break;
+      load_z(j + 2, z0);
+      put(z1);
     }
   } else if (warp >= 16) {
     // ---------------- products S[key][row]: warp 17 for the first half of the keys, 19 for the
@@ -198,21 +227,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp == 17 ? 0 : 1;
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kCols >> 3) << 17) | (uint32_t(kHalf >> 4) << 24);
     const uint64_t dk = sw128_desc(saddr(&S.k[half][0][0])), dq = sw128_desc(saddr(&S.q[0][0][0]));
-    constexpr uint32_t kTile = kCols * D * 2 / 16, kSlab = kHalf * 128 / 16;  // in descriptor units of 16 bytes
+    const uint64_t d1 = sw32_desc(saddr(&S.ones[0])), dz = sw32_desc(saddr(&S.z[0][0]));
+    constexpr uint32_t kTile = kCols * D * 2 / 16, kSlabK = kHalf * 128 / 16, kSlabQ = kCols * 128 / 16, kTileZ = kCols * 32 / 16;
     bool ok = half < halves && mbar_wait_warp(&S.k_full, 0, abort);
     int st = 0;
     uint32_t ph = 0;
     for (int j = 0; j < steps && ok; ++j) {
-      ok = mbar_wait_warp(&S.q_full[st], ph, abort) &&
-           mbar_wait_warp(&S.s_empty[half][j & 1], ((j >> 1) & 1) ^ 1, abort);
+      ok = mbar_wait_warp(&S.q_full[st], ph, abort) && mbar_wait_warp(&S.s_empty[half][j & 1], ((j >> 1) & 1) ^ 1, abort);
       if (!ok) break;
       fence_after();
       if (elect_one()) {
+        const uint32_t ts = tmem + uint32_t((half * 2 + (j & 1)) * kCols);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 2;
-          mma_bf16(tmem + uint32_t((half * 2 + (j & 1)) * kCols), dk + off, dq + st * kTile + off, idesc, kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16(ts, dk + (kk >> 2) * kSlabK + (kk & 3) * 2, dq + st * kTile + (kk >> 2) * kSlabQ + (kk & 3) * 2, idesc,
+                   kk > 0 ? 1u : 0u);
+        mma_bf16(ts, d1, dz + st * kTileZ, idesc, 1u);
         mma_commit(&S.s_full[half][j & 1]);
         mma_commit(&S.q_empty[st]);
       }
@@ -229,10 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = kLog2e * rsqrtf(float(D));
     const uint64_t sc2 = pk2(scale, scale);
     for (int j = buf; half < halves && j < steps; j += 2) {
-      const int zs = j % kLseSlots;
-      bool ok = mbar_wait(&S.z_full[zs], (j / kLseSlots) & 1, abort) && mbar_wait(&S.s_full[half][buf], (j >> 1) & 1, abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&S.s_full[half][buf], (j >> 1) & 1, abort))) break;
       fence_after();
       const Block x = block_at(bl, i0 + j, s.m);
       // columns [low, x.cols) see this thread's key
@@ -240,15 +267,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int low = dt <= 0 ? 0 : (bl.runs == 1 ? dt * bl.group : kCols);
       const bool last = bl.runs == 1 ? x.cols < bl.per * bl.group : x.cols < bl.heads;
       const bool plain = !__any_sync(0xffffffffu, low > 0) && !last;
-      const float* nz = S.nz[zs];
       uint64_t l0 = 0, l1 = 0;  // a step's own sums: two levels keep long chunks' sums exact
       auto weigh = [&](const uint32_t (&v)[32], int col) {
         if (plain) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            const float4 n4 = *reinterpret_cast<const float4*>(nz + col + i);
-            const uint64_t y0 = fma2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, pk2(n4.x, n4.y));
-            const uint64_t y1 = fma2(pk2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2, pk2(n4.z, n4.w));
+            const uint64_t y0 = mul2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2);
+            const uint64_t y1 = mul2(pk2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2);
             l0 = add2(l0, pk2(ex2(lo2(y0)), ex2(hi2(y0))));
             l1 = add2(l1, pk2(ex2(lo2(y1)), ex2(hi2(y1))));
           }
@@ -257,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float l = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float e = ex2(fmaf(__uint_as_float(v[i]), scale, nz[col + i]));
+            const float e = ex2(__uint_as_float(v[i]) * scale);
             l += col + i >= low && col + i < x.cols ? e : 0.f;
           }
           l0 = add2(l0, pk2(l, 0.f));
@@ -280,8 +305,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&S.s_empty[half][buf]);
       weigh(v1, 96);
       sum += (lo2(l0) + hi2(l0)) + (lo2(l1) + hi2(l1));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.z_empty[zs]);
     }
     if (buf == 1) S.sums[slot - n0] = sum;
   }

@@ -127,6 +127,7 @@ ATTEND = [
     ("bf16", 32, 8, 128, 0, [513], [2500]),
     ("bf16", 64, 1, 128, 96, [5], [900]),
     ("bf16", 136, 1, 64, 32, [3, 1], [100, 40]),                    # a group of more than 128
+    ("bf16", 300, 1, 64, 16, [2, 1], [50, 7]),                      # and of more than 256
     ("bf16", 4, 4, 64, 64, [20, 8, 32], [500, 1300, 32]),
     ("f32", 4, 2, 64, 0, [1], [1]),
     ("f32", 8, 2, 128, 16, [1, 1, 3], [17, 2000, 64]),
