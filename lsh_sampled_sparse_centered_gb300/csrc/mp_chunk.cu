@@ -36,18 +36,6 @@ __device__ __forceinline__ void load_transposed(float* dst, P p) {
     for (int i = 0; i < 8; ++i) dst[(e + i) * 64 + row] = x[i];
   }
 }
-template <int D, typename P>
-__device__ __forceinline__ void load_rows(float* dst, P p) {
-  for (int i = threadIdx.x; i < 64 * (D / 8); i += kThr) {
-    const int row = i / (D / 8), e = (i % (D / 8)) * 8;
-    const float* src = p(row);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (src) load8(src + e, x);
-    *reinterpret_cast<float4*>(dst + row * D + e) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(dst + row * D + e + 4) = make_float4(x[4], x[5], x[6], x[7]);
-  }
-}
-
 // S[8][4] of rows ty*8.. and keys tx*4.. from [d][64] tiles
 template <int D>
 __device__ __forceinline__ void dot_tile(const float* qt, const float* kt, int ty, int tx, float (&s)[8][4]) {
@@ -68,13 +56,29 @@ __device__ __forceinline__ void dot_tile(const float* qt, const float* kt, int t
   }
 }
 
+// 16 bytes of global memory into shared memory in the background, zeros where !live
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Thread (ty, tx) holds S of rows 8 ty .. + 8 and keys tx, tx + 16, ... (rows of shared memory
+// are padded by four floats, so that sixteen keys' vectors fall on all banks), and O of the
+// same rows and the columns 4 tx .. + 4 of each 64. Products run as packed pairs, over
+// pairs of d for S and of columns for O. V arrives under S and the softmax, the next K under
+// the product with V.
 template <int D>
-__global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
+__global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const ChunkArgs a) {
+  constexpr int kRow = D + 4, kPt = kBM + 4;
   extern __shared__ float sm[];
-  float* qt = sm;               // [D][64]
-  float* kt = qt + D * kBM;     // [D][64]
-  float* vs = kt + D * kBN;     // [64][D]
-  float* pt = vs + D * kBN;     // [64 keys][64 rows]
+  float* qs = sm;                // [64][kRow]
+  float* ks = qs + kBM * kRow;   // [64][kRow]
+  float* vs = ks + kBN * kRow;   // [64][kRow]
+  float* pt = vs + kBN * kRow;   // [64 keys][kPt]
   const CacheArgs& c = a.c;
   const int b = blockIdx.z, h = blockIdx.y;
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
@@ -87,41 +91,73 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   // this split's keys: a run of 64-key tiles of the sequence
   const int tiles = (s.n + kBN - 1) / kBN, per = (tiles + a.splits - 1) / a.splits;
-  const int k0 = split * per * kBN, k1 = min(min(s.n, last + 1), (split + 1) * per * kBN);
-  auto qrow = [&](int i) -> const float* {
-    const int r = r0 + i;
-    return r < rows ? static_cast<const float*>(a.q) + (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D
-                    : nullptr;
+  const int k0 = min(s.n, split * per * kBN), k1 = min(min(s.n, last + 1), (split + 1) * per * kBN);
+  constexpr int kVec = D / 4, kStep = kThr / kVec;  // vectors of a row, rows that the CTA copies at a time
+  const int cr = threadIdx.x / kVec, ce = threadIdx.x % kVec * 4;
+  auto copy_tile = [&](float* dst, const void* base, int n0) {
+#pragma unroll 4
+    for (int i = cr; i < kBN; i += kStep) {
+      const bool live = n0 + i < k1;
+      const float* src = static_cast<const float*>(base) + (live ? slot_read(c, b, h, n0 + i) + ce : 0);
+      copy16(dst + i * kRow + ce, src, live);
+    }
+    copy_commit();
   };
-  load_transposed<D>(qt, qrow);
-  float m[8], l[8], o[8][D / 16];
-  int see[8];  // a row sees the slots below this
+  for (int i = cr; i < kBM; i += kStep) {
+    const int r = r0 + i;
+    const bool live = r < rows;
+    const float* src = static_cast<const float*>(a.q);
+    if (live) src += (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D + ce;
+    copy16(qs + i * kRow + ce, src, live);
+  }
+  if (k0 < k1) {
+    copy_tile(ks, a.keys, k0);
+    copy_tile(vs, a.values, k0);
+  }
+  float m[8], l[8];
+  uint64_t o[8][D / 32];  // pairs of columns
+  int see[8];             // a row sees the slots below this
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
     see[i] = first + (r0 + ty * 8 + i) / c.group + 1;
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) o[i][j] = 0.f;
+    for (int j = 0; j < D / 32; ++j) o[i][j] = 0;
   }
   const float scale = kLog2e * rsqrtf(float(D));
   for (int n0 = k0; n0 < k1; n0 += kBN) {
+    copy_wait<1>();  // K is there, V may still come
     __syncthreads();
-    auto slot_ptr = [&](const void* base, int i) -> const float* {
-      return n0 + i < k1 ? static_cast<const float*>(base) + slot_read(c, b, h, n0 + i) : nullptr;
-    };
-    load_transposed<D>(kt, [&](int i) { return slot_ptr(a.keys, i); });
-    load_rows<D>(vs, [&](int i) { return slot_ptr(a.values, i); });
-    __syncthreads();
+    uint64_t x2[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x2[i][j] = 0;
+#pragma unroll 2
+    for (int e = 0; e < D; e += 4) {
+      uint64_t kv[4][2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(ks + (tx + 16 * j) * kRow + e);
+        kv[j][0] = v.x;
+        kv[j][1] = v.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qs + (ty * 8 + i) * kRow + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x2[i][j] = fma2(q.y, kv[j][1], fma2(q.x, kv[j][0], x2[i][j]));
+      }
+    }
     float x[8][4];
-    dot_tile<D>(qt, kt, ty, tx, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int slot = n0 + tx * 4 + j;
-        x[i][j] = slot < see[i] && slot < k1 ? x[i][j] * scale : -INFINITY;
+        const int slot = n0 + tx + 16 * j;
+        x[i][j] = slot < see[i] && slot < k1 ? (lo2(x2[i][j]) + hi2(x2[i][j])) * scale : -INFINITY;
         top = fmaxf(top, x[i][j]);
       }
 #pragma unroll
@@ -137,32 +173,44 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
         sum += x[i][j];
       }
       l[i] = l[i] * by + sum;
+      const uint64_t by2 = pk2(by, by);
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) o[i][j] *= by;
+      for (int j = 0; j < D / 32; ++j) o[i][j] = mul2(o[i][j], by2);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<float4*>(pt + (tx * 4 + j) * 64 + ty * 8) = make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
-      *reinterpret_cast<float4*>(pt + (tx * 4 + j) * 64 + ty * 8 + 4) =
-          make_float4(x[4][j], x[5][j], x[6][j], x[7][j]);
+      *reinterpret_cast<float4*>(pt + (tx + 16 * j) * kPt + ty * 8) = make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
+      *reinterpret_cast<float4*>(pt + (tx + 16 * j) * kPt + ty * 8 + 4) = make_float4(x[4][j], x[5][j], x[6][j], x[7][j]);
     }
-    __syncthreads();
-#pragma unroll 2
+    __syncthreads();  // K has been read, P is written
+    const bool more = n0 + kBN < k1;
+    if (more) {
+      copy_tile(ks, a.keys, n0 + kBN);
+      copy_wait<1>();
+    } else {
+      copy_wait<0>();
+    }
+    __syncthreads();  // V is there
+#pragma unroll 4
     for (int k = 0; k < kBN; ++k) {
-      const float4 a0 = *reinterpret_cast<const float4*>(pt + k * 64 + ty * 8);
-      const float4 a1 = *reinterpret_cast<const float4*>(pt + k * 64 + ty * 8 + 4);
+      const float4 a0 = *reinterpret_cast<const float4*>(pt + k * kPt + ty * 8);
+      const float4 a1 = *reinterpret_cast<const float4*>(pt + k * kPt + ty * 8 + 4);
       const float p[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
-        const float4 v4 = *reinterpret_cast<const float4*>(vs + k * D + g * 64 + tx * 4);
-        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(vs + k * kRow + g * 64 + tx * 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[i][g * 4 + j] = fmaf(p[i], v[j], o[i][g * 4 + j]);
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t pp = pk2(p[i], p[i]);
+          o[i][g * 2] = fma2(pp, v.x, o[i][g * 2]);
+          o[i][g * 2 + 1] = fma2(pp, v.y, o[i][g * 2 + 1]);
+        }
       }
     }
+    __syncthreads();  // V and P have been read
+    if (more) copy_tile(vs, a.values, n0 + kBN);
   }
+  copy_wait<0>();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_chunk_join may be set up
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -172,21 +220,17 @@ __global__ void __launch_bounds__(kThr) k_chunk_simt(const ChunkArgs a) {
     const int r = r0 + ty * 8 + i;
     if (r >= rows) continue;
     const int64_t row = int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group;
-    if (a.splits > 1) {
-      const int64_t at = int64_t(split) * c.total_q * qh + row;
-      if (tx == 0) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m[i], sum);
-      if (sum > 0.f)
-#pragma unroll
-        for (int g = 0; g < D / 64; ++g)
-          *reinterpret_cast<float4*>(a.part + at * D + g * 64 + tx * 4) =
-              make_float4(o[i][g * 4], o[i][g * 4 + 1], o[i][g * 4 + 2], o[i][g * 4 + 3]);
-    } else {
-      const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
-      if (a.lse && tx == 0) a.lse[row] = sum == 0.f ? -INFINITY : m[i] * kLn2 + logf(sum);
-      float* out = static_cast<float*>(a.out) + row * D;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) out[(j / 4) * 64 + tx * 4 + j % 4] = o[i][j] * inv;
+    const int64_t at = int64_t(split) * c.total_q * qh + row;
+    const float inv = a.splits > 1 ? 1.f : (sum > 0.f ? 1.0f / sum : sum);
+    if (tx == 0) {
+      if (a.splits > 1) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m[i], sum);
+      else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m[i] * kLn2 + logf(sum);
     }
+    float* out = a.splits > 1 ? a.part + at * D : static_cast<float*>(a.out) + row * D;
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g)
+      *reinterpret_cast<float4*>(out + g * 64 + tx * 4) =
+          make_float4(lo2(o[i][g * 2]) * inv, hi2(o[i][g * 2]) * inv, lo2(o[i][g * 2 + 1]) * inv, hi2(o[i][g * 2 + 1]) * inv);
   }
 }
 
@@ -311,7 +355,7 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
 
 template <int D>
 cudaError_t chunk_simt(const ChunkArgs& a, cudaStream_t st) {
-  constexpr int smem = (3 * D * 64 + 64 * 64) * 4;
+  constexpr int smem = (3 * 64 * (D + 4) + 64 * 68) * 4;
   cudaError_t e = cudaFuncSetAttribute(k_chunk_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t(a.c.max_q) * a.c.group + kBM - 1) / kBM;
@@ -344,11 +388,11 @@ cudaError_t weights_simt(const WeightsArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Slices of the keys: as many as fill the SMs about twice, each of at least 256 slots.
+// Slices of the keys: as many as the CTAs that fit leave room for, each of at least 256 slots.
 int chunk_splits(const mp_cache_config* c, int max_q, int max_kv) {
   const int64_t group = c->q_heads / c->kv_heads;
   const int64_t ctas = (max_q * group + kBM - 1) / kBM * c->kv_heads * c->batch;
-  const int64_t fill = 2 * int64_t(device_sm_count()) / ctas, most = (int64_t(max_kv) + 255) / 256;
+  const int64_t fill = (c->head_dim == 64 ? 3 : 2) * int64_t(device_sm_count()) / ctas, most = (int64_t(max_kv) + 255) / 256;
   const int64_t s = fill < most ? fill : most;
   return int(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
