@@ -69,7 +69,7 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // Thread (ty, tx) holds S of rows 8 ty .. + 8 and keys tx, tx + 16, ... (rows of shared memory
 // are padded by four floats, so that sixteen keys' vectors fall on all banks), and O of the
 // same rows and the columns 4 tx .. + 4 of each 64. Products run as packed pairs, over
-// pairs of d for S and of columns for O. V arrives under S and the softmax, the next K under
+// pairs of d for S and of rows for O. V arrives under S and the softmax, the next K under
 // the product with V.
 template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const ChunkArgs a) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
     copy_tile(vs, a.values, k0);
   }
   float m[8], l[8];
-  uint64_t o[8][D / 32];  // pairs of columns
+  uint64_t o[4][D / 16];  // rows 2 i and 2 i + 1 of a column
   int see[8];             // a row sees the slots below this
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
     l[i] = 0.f;
     see[i] = first + (r0 + ty * 8 + i) / c.group + 1;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) o[i][j] = 0;
+    for (int j = 0; j < D / 16; ++j) o[i / 2][j] = 0;
   }
   const float scale = kLog2e * rsqrtf(float(D));
   for (int n0 = k0; n0 < k1; n0 += kBN) {
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) x2[i][j] = 0;
-#pragma unroll 2
+#pragma unroll 1
     for (int e = 0; e < D; e += 4) {
       uint64_t kv[4][2];
 #pragma unroll
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
         for (int j = 0; j < 4; ++j) x2[i][j] = fma2(q.y, kv[j][1], fma2(q.x, kv[j][0], x2[i][j]));
       }
     }
-    float x[8][4];
+    float x[8][4], by[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float top = -INFINITY;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
       for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
       const float mn = fmaxf(m[i], top);
       const float ref = mn == -INFINITY ? 0.f : mn;
-      const float by = exp2f(m[i] - ref);
+      by[i] = exp2f(m[i] - ref);
       m[i] = mn;
       float sum = 0.f;
 #pragma unroll
@@ -172,11 +172,12 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
         x[i][j] = exp2f(x[i][j] - ref);
         sum += x[i][j];
       }
-      l[i] = l[i] * by + sum;
-      const uint64_t by2 = pk2(by, by);
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) o[i][j] = mul2(o[i][j], by2);
+      l[i] = l[i] * by[i] + sum;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) o[i][j] = mul2(o[i][j], pk2(by[2 * i], by[2 * i + 1]));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       *reinterpret_cast<float4*>(pt + (tx + 16 * j) * kPt + ty * 8) = make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
@@ -191,20 +192,19 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
       copy_wait<0>();
     }
     __syncthreads();  // V is there
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < kBN; ++k) {
-      const float4 a0 = *reinterpret_cast<const float4*>(pt + k * kPt + ty * 8);
-      const float4 a1 = *reinterpret_cast<const float4*>(pt + k * kPt + ty * 8 + 4);
-      const float p[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      const ulonglong2 p0 = *reinterpret_cast<const ulonglong2*>(pt + k * kPt + ty * 8);
+      const ulonglong2 p1 = *reinterpret_cast<const ulonglong2*>(pt + k * kPt + ty * 8 + 4);
+      const uint64_t p[4] = {p0.x, p0.y, p1.x, p1.y};
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(vs + k * kRow + g * 64 + tx * 4);
+        const float4 v4 = *reinterpret_cast<const float4*>(vs + k * kRow + g * 64 + tx * 4);
+        const uint64_t v[4] = {pk2(v4.x, v4.x), pk2(v4.y, v4.y), pk2(v4.z, v4.z), pk2(v4.w, v4.w)};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint64_t pp = pk2(p[i], p[i]);
-          o[i][g * 2] = fma2(pp, v.x, o[i][g * 2]);
-          o[i][g * 2 + 1] = fma2(pp, v.y, o[i][g * 2 + 1]);
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][g * 4 + j] = fma2(p[i], v[j], o[i][g * 4 + j]);
       }
     }
     __syncthreads();  // V and P have been read
@@ -228,9 +228,12 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
     }
     float* out = a.splits > 1 ? a.part + at * D : static_cast<float*>(a.out) + row * D;
 #pragma unroll
-    for (int g = 0; g < D / 64; ++g)
-      *reinterpret_cast<float4*>(out + g * 64 + tx * 4) =
-          make_float4(lo2(o[i][g * 2]) * inv, hi2(o[i][g * 2]) * inv, lo2(o[i][g * 2 + 1]) * inv, hi2(o[i][g * 2 + 1]) * inv);
+    for (int g = 0; g < D / 64; ++g) {
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = (i & 1 ? hi2(o[i / 2][g * 4 + j]) : lo2(o[i / 2][g * 4 + j])) * inv;
+      *reinterpret_cast<float4*>(out + g * 64 + tx * 4) = make_float4(y[0], y[1], y[2], y[3]);
+    }
   }
 }
 
