@@ -1,7 +1,8 @@
 """Python binding of libmagicpig (LSH-sampled sparse decode attention on one GB300).
 
 Argument marshalling only: every function forwards to the C entry point of the same
-name in ``include/magicpig.h``. Tensors are passed as device pointers; PyTorch
+name in ``include/magicpig.h`` (through ctypes, the cache operators through a compiled
+extension). Tensors are passed as device pointers; PyTorch
 supplies device memory and streams. The shared library must have been built
 (``python lsh_sampled_sparse_centered_gb300/build.py`` or ``__graft_entry__.build()``);
 importing this package without it raises ImportError, and there is no fallback.
@@ -248,71 +249,28 @@ def make_rotary(*, rot_dim: int, interleaved: bool = False, eps: float = 1e-6) -
     return mp_rotary(rot_dim, int(bool(interleaved)), eps, 0)
 
 
-_torch = None  # imported by the first call below
+_calls = None
 
 
-def _device(first) -> int:
-    """Index of the device that a call's tensors are on: the current one, or the call is refused."""
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    if not isinstance(first, _torch.Tensor) or not first.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors (device memory)")
-    dev = first.get_device()
-    if dev != _torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_torch.cuda.current_device()}")
-    return dev
+def _cache_calls():
+    """The compiled calls of the cache operators (csrc/mp_binding.cpp). They check a call's
+    tensors (device, type, layout, size: ValueError) and pass on their addresses; loaded by
+    the first call, which needs PyTorch anyway."""
+    global _calls
+    import importlib.machinery
+    import importlib.util
 
-
-def _arg(name, x, dtype, numel, dev):
-    """Device address of a tensor that the kernels use as the configuration says: its device,
-    type, layout and size are checked (this runs for every argument of a call that may take a
-    few microseconds, so the checks are the cheap ones and the words come after)."""
-    try:
-        if x.dtype is dtype and x.get_device() == dev and x.numel() >= numel and x.is_contiguous():
-            return x.data_ptr()
-    except AttributeError:
-        raise ValueError(f"{name} must be a CUDA tensor") from None
-    if x.get_device() != dev:
-        raise ValueError(f"{name} is on {x.device}, not on cuda:{dev}")
-    if x.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (dense row-major layout)")
-    raise ValueError(f"{name} has {x.numel()} elements, the call uses {numel}")
-
-
-def _opt(name, x, dtype, numel, dev):
-    return None if x is None else _arg(name, x, dtype, numel, dev)
-
-
-def _rows(name, x, dtype, rows, heads, d, dev):
-    """(address, row stride) of a [rows, heads, d] tensor whose rows may lie apart."""
-    if x.dtype is not dtype or x.get_device() != dev:
-        raise ValueError(f"{name} must be {dtype} on cuda:{dev}")
-    if tuple(x.shape) != (rows, heads, d):
-        raise ValueError(f"{name} must be {(rows, heads, d)}, got {tuple(x.shape)}")
-    stride, head, one = x.stride()
-    if one != 1 or (head != d and heads != 1):
-        raise ValueError(f"{name}: the heads of a row must be dense")
-    return x.data_ptr(), (stride if rows > 1 else heads * d)  # one row has no stride of its own
-
-
-def _raw_stream(stream, dev):
-    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-def _pool_size(cfg: mp_cache_config) -> int:
-    return cfg.n_pages * cfg.kv_heads * cfg.page_size * cfg.head_dim
-
-
-def _dtype_of(cfg: mp_cache_config):
-    if cfg.dtype == MP_DTYPE_BF16:
-        return _torch.bfloat16
-    if cfg.dtype == MP_DTYPE_F32:
-        return _torch.float32
-    raise MagicPigError("mp_cache_config_check", MP_ERR_INVALID_ARG)
+    import torch  # noqa: F401  (its libraries are the extension's)
+    path = os.path.join(_PKG, "_lib", "_mp_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_mp_calls.so is not built ({path}); run `python lsh_sampled_sparse_centered_gb300/build.py`")
+    loader = importlib.machinery.ExtensionFileLoader("_mp_calls", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mp_calls", loader))
+    loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
+        "mp_cache_append", "mp_chunk_attention", "mp_cache_weights", "mp_cache_evict")))
+    _calls = mod
+    return mod
 
 
 def mp_cache_config_check(cfg: mp_cache_config) -> int:
@@ -322,19 +280,9 @@ def mp_cache_config_check(cfg: mp_cache_config) -> int:
 def mp_cache_append(cfg: mp_cache_config, rotary: mp_rotary, q, k, v, q_norm, k_norm, inv_freq, positions, cu_q, kv_len,
                     keys, values, page_table, q_out, status=None, stream=None) -> int:
     """Norms, rotation and cache write of the new tokens. q, k, v: [total_q, heads, head_dim], rows may lie apart."""
-    dev = _device(q)
-    dt, i32 = _dtype_of(cfg), _torch.int32
-    rows, d, hq, hk, batch, pool = q.shape[0], cfg.head_dim, cfg.q_heads, cfg.kv_heads, cfg.batch, _pool_size(cfg)
-    qp, qs = _rows("q", q, dt, rows, hq, d, dev)
-    kp, ks = _rows("k", k, dt, rows, hk, d, dev)
-    vp, vs = _rows("v", v, dt, rows, hk, d, dev)
-    return _check("mp_cache_append", _lib.mp_cache_append(
-        cfg, rotary, qp, qs, kp, ks, vp, vs, _opt("q_norm", q_norm, dt, d, dev), _opt("k_norm", k_norm, dt, d, dev),
-        _opt("inv_freq", inv_freq, _torch.float64, rotary.rot_dim // 2, dev), _opt("positions", positions, i32, rows, dev),
-        _arg("cu_q", cu_q, i32, batch + 1, dev), _arg("kv_len", kv_len, i32, batch, dev), rows,
-        _arg("keys", keys, dt, pool, dev), _arg("values", values, dt, pool, dev),
-        _opt("page_table", page_table, i32, batch * cfg.max_pages, dev), _arg("q_out", q_out, dt, rows * hq * d, dev),
-        _opt("status", status, i32, 1, dev), _raw_stream(stream, dev)))
+    return _check("mp_cache_append", (_calls or _cache_calls()).append(
+        cfg, rotary, q, k, v, q_norm, k_norm, inv_freq, positions, cu_q, kv_len, keys, values, page_table, q_out, status,
+        stream if stream is None else _stream(stream)))
 
 
 def mp_chunk_workspace_bytes(cfg: mp_cache_config, total_q: int, max_q: int, max_kv: int) -> int:
@@ -346,30 +294,17 @@ def mp_chunk_workspace_bytes(cfg: mp_cache_config, total_q: int, max_q: int, max
 def mp_chunk_attention(cfg: mp_cache_config, q, cu_q, kv_len, max_q: int, max_kv: int, keys, values, page_table, out,
                        lse=None, workspace=None, status=None, stream=None) -> int:
     """Exact attention of the new tokens q [total_q, q_heads, head_dim] over their sequences' slots."""
-    dev = _device(q)
-    dt, i32 = _dtype_of(cfg), _torch.int32
-    rows, hq, batch, pool = q.shape[0], cfg.q_heads, cfg.batch, _pool_size(cfg)
-    n = rows * hq * cfg.head_dim
-    return _check("mp_chunk_attention", _lib.mp_chunk_attention(
-        cfg, _arg("q", q, dt, n, dev), _arg("cu_q", cu_q, i32, batch + 1, dev), _arg("kv_len", kv_len, i32, batch, dev), rows,
-        max_q, max_kv, _arg("keys", keys, dt, pool, dev), _arg("values", values, dt, pool, dev),
-        _opt("page_table", page_table, i32, batch * cfg.max_pages, dev), _arg("out", out, dt, n, dev),
-        _opt("lse", lse, _torch.float32, rows * hq, dev), _opt("workspace", workspace, _torch.uint8, 0, dev),
-        0 if workspace is None else workspace.numel(), _opt("status", status, i32, 1, dev), _raw_stream(stream, dev)))
+    return _check("mp_chunk_attention", (_calls or _cache_calls()).attend(
+        cfg, q, cu_q, kv_len, max_q, max_kv, keys, values, page_table, out, lse, workspace, status,
+        stream if stream is None else _stream(stream)))
 
 
 def mp_cache_weights(cfg: mp_cache_config, q, lse, cu_q, kv_len, max_q: int, max_kv: int, keys, page_table, scores,
                      status=None, stream=None) -> int:
     """Add the attention that the new tokens paid to every slot to scores [batch, kv_heads, max_pages * page_size]."""
-    dev = _device(q)
-    dt, i32, f32 = _dtype_of(cfg), _torch.int32, _torch.float32
-    rows, hq, batch = q.shape[0], cfg.q_heads, cfg.batch
-    return _check("mp_cache_weights", _lib.mp_cache_weights(
-        cfg, _arg("q", q, dt, rows * hq * cfg.head_dim, dev), _arg("lse", lse, f32, rows * hq, dev),
-        _arg("cu_q", cu_q, i32, batch + 1, dev), _arg("kv_len", kv_len, i32, batch, dev), rows, max_q, max_kv,
-        _arg("keys", keys, dt, _pool_size(cfg), dev), _opt("page_table", page_table, i32, batch * cfg.max_pages, dev),
-        _arg("scores", scores, f32, batch * cfg.kv_heads * cfg.max_pages * cfg.page_size, dev),
-        _opt("status", status, i32, 1, dev), _raw_stream(stream, dev)))
+    return _check("mp_cache_weights", (_calls or _cache_calls()).weights(
+        cfg, q, lse, cu_q, kv_len, max_q, max_kv, keys, page_table, scores, status,
+        stream if stream is None else _stream(stream)))
 
 
 def mp_evict_workspace_bytes(cfg: mp_cache_config, max_kv: int, budget: int) -> int:
@@ -382,19 +317,9 @@ def mp_cache_evict(cfg: mp_cache_config, dst_cfg: mp_cache_config, keys, values,
                    n_sink: int, window: int, budget: int, dst_keys, dst_values, dst_page_table, dst_scores, dst_len,
                    kept, workspace, status=None, stream=None) -> int:
     """Keep sinks, window and the highest-scored slots up to the budget; the kept rows move to the destination."""
-    dev = _device(keys)
-    dt, i32, f32 = _dtype_of(cfg), _torch.int32, _torch.float32
-    pool, dpool, batch, units = _pool_size(cfg), _pool_size(dst_cfg), cfg.batch, cfg.batch * cfg.kv_heads
-    return _check("mp_cache_evict", _lib.mp_cache_evict(
-        cfg, dst_cfg, _arg("keys", keys, dt, pool, dev), _arg("values", values, dt, pool, dev),
-        _opt("page_table", page_table, i32, batch * cfg.max_pages, dev), _arg("kv_len", kv_len, i32, batch, dev), max_kv,
-        _arg("scores", scores, f32, units * cfg.max_pages * cfg.page_size, dev), n_sink, window, budget,
-        _arg("dst_keys", dst_keys, dt, dpool, dev), _arg("dst_values", dst_values, dt, dpool, dev),
-        _opt("dst_page_table", dst_page_table, i32, batch * dst_cfg.max_pages, dev),
-        _opt("dst_scores", dst_scores, f32, units * dst_cfg.max_pages * dst_cfg.page_size, dev),
-        _arg("dst_len", dst_len, i32, batch, dev), _opt("kept", kept, i32, units * max(0, budget), dev),
-        _arg("workspace", workspace, _torch.uint8, 0, dev), workspace.numel(), _opt("status", status, i32, 1, dev),
-        _raw_stream(stream, dev)))
+    return _check("mp_cache_evict", (_calls or _cache_calls()).evict(
+        cfg, dst_cfg, keys, values, page_table, kv_len, max_kv, scores, n_sink, window, budget, dst_keys, dst_values,
+        dst_page_table, dst_scores, dst_len, kept, workspace, status, stream if stream is None else _stream(stream)))
 
 
 def mp_get_status(tables, stream=None) -> int:

@@ -6,15 +6,18 @@ __graft_entry__.build(). The translation units compile in parallel; the shared l
 links the CUDA runtime dynamically with an rpath to the toolkit's lib64. --check builds
 the bounds-checking library libmagicpig_check.so (MP_CHECK=1: kernels test every index
 that comes from data before using it and report failures in the status word), which the
-binding loads instead when MP_BOUNDS_CHECK=1 is set.
+binding loads instead when MP_BOUNDS_CHECK=1 is set. Beside them g++ builds _mp_calls.so,
+the binding of the cache operators, against the installed PyTorch's headers.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmagicpig.so")
 LIB_CHECK = os.path.join(OUT_DIR, "libmagicpig_check.so")
+CALLS = os.path.join(OUT_DIR, "_mp_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,9 +44,36 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def build_calls(nvcc: str, force: bool = False) -> None:
+    """Compile the Python calls of the cache operators (csrc/mp_binding.cpp)."""
+    src, header = os.path.join(CSRC, "mp_binding.cpp"), os.path.join(ROOT, "include", "magicpig.h")
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in (src, header)):
+        return
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden", src, "-o", tmp,
+           "-I" + os.path.join(ROOT, "include"), "-I" + sysconfig.get_paths()["include"],
+           "-I" + os.path.join(os.path.dirname(_cuda_lib64(nvcc)), "include"),
+           "-I" + os.path.join(torch, "include"), "-I" + os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath," + os.path.join(torch, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False, force: bool = False, check: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside the kernels
+        calls = ex.submit(build_calls, nvcc, force)
+        lib = build_library(nvcc, verbose, force, check)
+        calls.result()
+    return lib
+
+
+def build_library(nvcc: str, verbose: bool, force: bool, check: bool) -> str:
     srcs = sources()
     deps = srcs + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     deps.append(os.path.join(ROOT, "include", "magicpig.h"))
