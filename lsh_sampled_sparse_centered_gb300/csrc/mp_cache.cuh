@@ -139,6 +139,23 @@ __host__ __device__ __forceinline__ int seq_at(const CacheArgs& c, int r) {
   return (c.cu_q[lo] <= r && r < c.cu_q[lo + 1]) ? lo : -1;
 }
 
+#ifdef __CUDACC__
+// The same for a whole warp that asks for one row: 32 boundaries are looked at at a time, so
+// that up to 33 sequences take one round of loads and not five that wait for each other.
+__device__ __forceinline__ int seq_at_warp(const CacheArgs& c, int r) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = c.batch;  // cu_q[lo] <= r is kept where it holds for 0
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 32) / 33, at = lo + (lane + 1) * step;
+    const uint32_t below = __ballot_sync(0xffffffffu, at < hi && c.cu_q[min(at, hi - 1)] <= r);
+    const int k = below == 0xffffffffu ? 32 : __ffs(~below) - 1;  // the first boundaries in a row
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return (c.cu_q[lo] <= r && r < c.cu_q[lo + 1]) ? lo : -1;
+}
+#endif
+
 // Pool page of slot s (0 <= s < cols * page_size), or -1 when the table names none.
 __host__ __device__ __forceinline__ int page_at(const int32_t* table, int cols, int n_pages, int b, int col, uint32_t* status) {
   if (!table) return b;

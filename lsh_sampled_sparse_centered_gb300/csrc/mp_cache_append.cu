@@ -17,7 +17,7 @@ namespace mp {
 namespace {
 
 constexpr int kWarps = 4;  // independent of each other
-constexpr int kBatch = 4;  // vectors of a lane in flight
+constexpr int kBatch = 2;  // vectors of a lane that are worked on, as many more are on their way
 
 template <typename T>
 struct Vec {
@@ -64,7 +64,21 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a
   const int half = a.rot / 2;
   const int qh = c.kvh * c.group;
 
-  const int b = seq_at(c, int(r));
+  // what does not wait for the token's sequence is on its way before that is looked up: the
+  // first vectors of q, the frequencies and the position
+  const T* q = static_cast<const T*>(a.q) + r * a.q_stride;
+  uint4 early[kBatch];
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int h = h0 + k * step;
+    early[k] = h < qh ? __ldcs(reinterpret_cast<const uint4*>(q + int64_t(h) * D + e0)) : make_uint4(0, 0, 0, 0);
+  }
+  double freq[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) freq[i] = i * 32 + l32 < half ? a.inv_freq[i * 32 + l32] : 0.0;
+  const int64_t given = a.positions ? a.positions[r] : 0;
+
+  const int b = seq_at_warp(c, int(r));
   if (b < 0) return;  // a row outside every sequence
   const Seq s = seq_of(c, b);
   if (r < s.row0 || r >= s.row0 + s.m) return;
@@ -77,9 +91,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a
   } else if (l32 == 0) {
     flag(c.status, MP_STATUS_BAD_LENGTH);
   }
-  const int64_t pos = a.positions ? a.positions[r] : slot;
-  for (int i = l32; i < half; i += 32) {
-    const double turns = a.inv_freq[i] * 0.15915494309189533577;  // 1 / 2 pi
+  const int64_t pos = a.positions ? given : slot;
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) {
+    const int i = k * 32 + l32;
+    if (i >= half) break;
+    const double turns = freq[k] * 0.15915494309189533577;  // 1 / 2 pi
     const uint64_t per = static_cast<uint64_t>((turns - floor(turns)) * 18446744073709551616.0);
     const uint64_t phase = static_cast<uint64_t>(pos) * per + 0x80000000ull;
     sincospif(float(int32_t(uint32_t(phase >> 32))) * 4.656612873077393e-10f, &sine[warp][i], &cosine[warp][i]);  // 2^-31 half turns
@@ -95,7 +112,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a
   // one sum with the same factors for all query heads, and others for all key heads:
   //   y_i = r (x_i own_i + x_partner other_i), r the inverse root (1 without a norm),
   //   own_i = w_i cos, other_i = -+ w_partner sin.
-  auto turn_heads = [&](const T* src, const void* norm, int heads, T* to, int64_t to_stride) {
+  auto turn_heads = [&](const T* src, const void* norm, int heads, T* to, int64_t to_stride, const uint4* have) {
     float own[V], other[V];
     {
       float g[V], gp[V];
@@ -117,13 +134,24 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a
         other[j] = (a.interleaved ? g[j ^ 1] : gp[j]) * sn;
       }
     }
-    for (int hb = h0; hb - h0 < heads; hb += kBatch * step) {
-      uint4 u[kBatch];
+    uint4 u[kBatch], ahead[kBatch];  // a batch, and the next one on its way
+    auto load = [&](int hb, uint4 (&v)[kBatch]) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int h = hb + k * step;
-        u[k] = h < heads ? __ldcs(reinterpret_cast<const uint4*>(src + int64_t(h) * D + e0)) : make_uint4(0, 0, 0, 0);
+        v[k] = h < heads ? __ldcs(reinterpret_cast<const uint4*>(src + int64_t(h) * D + e0)) : make_uint4(0, 0, 0, 0);
       }
+    };
+    if (have) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) ahead[k] = have[k];
+    } else {
+      load(h0, ahead);
+    }
+    for (int hb = h0; hb - h0 < heads; hb += kBatch * step) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) u[k] = ahead[k];
+      load(hb + kBatch * step, ahead);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int h = hb + k * step;
@@ -153,13 +181,20 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a
       }
     }
   };
-  turn_heads(static_cast<const T*>(a.q) + r * a.q_stride, a.q_norm, qh, static_cast<T*>(a.q_out) + r * qh * D, D);
+  turn_heads(q, a.q_norm, qh, static_cast<T*>(a.q_out) + r * qh * D, D, early);
   if (dst < 0) return;  // the same for the whole warp
   const T* v = static_cast<const T*>(a.v) + r * a.v_stride + e0;
-  for (int h = h0; h < c.kvh; h += step)
-    *reinterpret_cast<uint4*>(static_cast<T*>(a.values) + dst + h * head_stride + e0) =
-        __ldcs(reinterpret_cast<const uint4*>(v + int64_t(h) * D));
-  turn_heads(static_cast<const T*>(a.k) + r * a.k_stride, a.k_norm, c.kvh, static_cast<T*>(a.keys) + dst, head_stride);
+  for (int hb = h0; hb < c.kvh; hb += 4 * step) {
+    uint4 u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (hb + k * step < c.kvh) u[k] = __ldcs(reinterpret_cast<const uint4*>(v + int64_t(hb + k * step) * D));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (hb + k * step < c.kvh)
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.values) + dst + (hb + k * step) * head_stride + e0) = u[k];
+  }
+  turn_heads(static_cast<const T*>(a.k) + r * a.k_stride, a.k_norm, c.kvh, static_cast<T*>(a.keys) + dst, head_stride, nullptr);
 }
 
 template <typename T, int D>

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   const int part = warp % WARPS;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
-  const int t = int(row / qh), b = seq_at(c, t);
+  const int t = int(row / qh), b = seq_at_warp(c, t);
   if (b < 0) return;
   const Seq s = seq_of(c, b);
   if (t < s.row0 || t >= s.row0 + s.m) return;
