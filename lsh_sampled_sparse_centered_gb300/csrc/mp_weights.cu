@@ -5,17 +5,15 @@
 // owner, so the order of its additions is fixed and no atomics are needed.
 //
 // Long chunks: k_weights_tc, keys as the M dimension of tcgen05 products (256 keys of a
-// CTA, as two halves, against 128 query rows at a time), so that a thread owns a key and
+// CTA, as two halves, against 96 query rows at a time), so that a thread owns a key and
 // sums along its accumulator row. -z enters through one more K step, after the others: a
 // column (1, 1, 1, 0, ...) of the keys times the split of -z sqrt(d) into three bf16 terms
-// (exact to fp32), so that the threads neither load nor add it. Each half has two
-// accumulators and each of the four a warpgroup that reads it, so that products and
-// exponentials of both run at once. A step costs an SM about 1024 clocks of products, 1024
-// of exponentials, and of shared memory 1152 for the products' operands and 288 for the
-// loads (with z read from shared memory by every thread 512 more: FIGZ).
-// Products of 256 columns need a quarter less of it, but leave no room for second
-// accumulators and deep enough loads (140 us where this takes FIGN: 16384 slots, 1000 tokens
-// of 32 heads).
+// (exact to fp32), so that the threads neither load nor add it. K is copied into tensor
+// memory first: from shared memory both operands of a 128 x 128 product need all of its
+// bandwidth (16384 slots, 1000 tokens of 32 heads: 124 us so, 117 us from tensor
+// memory). Beside it there is room for four accumulators of 96 columns, two for each half,
+// each with a warpgroup that reads it, so that products and exponentials of both halves run
+// at once. A step of 96 rows costs an SM 864 clocks of products and 768 of exponentials.
 //
 // Few rows: k_weights_step, one pass over K from global memory straight into the fragments
 // of warp-level products, bound by that read.
@@ -30,25 +28,25 @@ namespace mp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kHalf = 128, kKeys = 256, kCols = 128;  // keys of a product and of a CTA, query rows of a step
+constexpr int kHalf = 128, kKeys = 256, kCols = 96;  // keys of a product and of a CTA, query rows of a step
 constexpr int kThreads = 640;  // four warpgroups of sums, a warp each of loads and z, two of products
 
 template <int D>
 struct WSmem {
   static constexpr int kSub = D / 64;
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = D == 128 ? 5 : 8;
   __nv_bfloat16 k[2][kSub][kHalf * 64];
   __nv_bfloat16 q[kStages][kSub][kCols * 64];
   __nv_bfloat16 z[kStages][kCols * 16];  // (hi, mid, lo, 0, ...) of the step's rows (32-byte swizzle)
   __nv_bfloat16 ones[kHalf * 16];        // rows (1, 1, 1, 0, ...) (32-byte swizzle)
-  float sums[kKeys];                     // of the second accumulators
-  uint64_t k_full, q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2];
+  float sums[kKeys];                     // of the odd steps
+  uint64_t k_full, k_ready, q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2];
   uint32_t tmem_base;
   uint32_t abort;
 };
 
-// Query rows in blocks of at most 128: whole tokens of `group` rows, or, with more than
-// 128 heads in a group, runs of 128 heads of one token.
+// Query rows in blocks of at most 96: whole tokens of `group` rows, or, with more than
+// 96 heads in a group, runs of 96 heads of one token.
 struct Blocks {
   int group, heads, per, runs;  // rows of a token in a block, tokens of a block, blocks of a token
   int n;
@@ -120,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.q_full[i], 2);  // the load and z
       mbar_init(&S.q_empty[i], halves);
     }
+    mbar_init(&S.k_ready, 4 * halves);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&S.s_full[i >> 1][i & 1], 1);
       mbar_init(&S.s_empty[i >> 1][i & 1], 4);
@@ -137,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = S.tmem_base;
+  const uint32_t t_k = tmem + 4 * kCols;  // K: d / 2 columns of each half behind the accumulators
   float sum = 0.f;
 
   if (warp == 16) {
@@ -226,22 +226,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // second, so that one's products run while the other waits ----------------
     const int half = warp == 17 ? 0 : 1;
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kCols >> 3) << 17) | (uint32_t(kHalf >> 4) << 24);
-    const uint64_t dk = sw128_desc(saddr(&S.k[half][0][0])), dq = sw128_desc(saddr(&S.q[0][0][0]));
+    const uint64_t dq = sw128_desc(saddr(&S.q[0][0][0]));
     const uint64_t d1 = sw32_desc(saddr(&S.ones[0])), dz = sw32_desc(saddr(&S.z[0][0]));
-    constexpr uint32_t kTile = kCols * D * 2 / 16, kSlabK = kHalf * 128 / 16, kSlabQ = kCols * 128 / 16, kTileZ = kCols * 32 / 16;
-    bool ok = half < halves && mbar_wait_warp(&S.k_full, 0, abort);
+    constexpr uint32_t kTile = kCols * D * 2 / 16, kSlabQ = kCols * 128 / 16, kTileZ = kCols * 32 / 16;
+    bool ok = half < halves && mbar_wait_warp(&S.k_ready, 0, abort);
     int st = 0;
     uint32_t ph = 0;
     for (int j = 0; j < steps && ok; ++j) {
-      ok = mbar_wait_warp(&S.q_full[st], ph, abort) && mbar_wait_warp(&S.s_empty[half][j & 1], ((j >> 1) & 1) ^ 1, abort);
+      ok = mbar_wait_warp(&S.q_full[st], ph, abort) &&
+           mbar_wait_warp(&S.s_empty[half][j & 1], ((j >> 1) & 1) ^ 1, abort);
       if (!ok) break;
       fence_after();
       if (elect_one()) {
         const uint32_t ts = tmem + uint32_t((half * 2 + (j & 1)) * kCols);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16(ts, dk + (kk >> 2) * kSlabK + (kk & 3) * 2, dq + st * kTile + (kk >> 2) * kSlabQ + (kk & 3) * 2, idesc,
-                   kk > 0 ? 1u : 0u);
+          mma_bf16_ta(ts, t_k + uint32_t(half * (D / 2) + kk * 8), dq + st * kTile + (kk >> 2) * kSlabQ + (kk & 3) * 2, idesc,
+                      kk > 0 ? 1u : 0u);
         mma_bf16(ts, d1, dz + st * kTileZ, idesc, 1u);
         mma_commit(&S.s_full[half][j & 1]);
         mma_commit(&S.q_empty[st]);
@@ -253,13 +254,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---------------- one thread per key and accumulator: blocks j = buf, buf + 2, ... ----------------
-    const int half = warp >> 3, buf = (warp >> 2) & 1, slot = n0 + half * kHalf + (warp & 3) * 32 + lane;
-    const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t((half * 2 + buf) * kCols);
+    // ---------------- one thread per key and every other step ----------------
+    const int half = warp >> 3, odd = (warp >> 2) & 1, key = (warp & 3) * 32 + lane, slot = n0 + half * kHalf + key;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const float scale = kLog2e * rsqrtf(float(D));
     const uint64_t sc2 = pk2(scale, scale);
-    for (int j = buf; half < halves && j < steps; j += 2) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&S.s_full[half][buf], (j >> 1) & 1, abort))) break;
+    if (odd == 0 && half < halves && __all_sync(0xffffffffu, mbar_wait(&S.k_full, 0, abort))) {
+      // this thread's key into tensor memory (16-byte chunk i of row k lies at i ^ (k % 8))
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(&S.k[half][u][key * 64 + ((i ^ (key & 7)) << 3)]);
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+        tmem_st32(t_k + lanes + uint32_t(half * (D / 2) + u * 32), w);
+      }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.k_ready);
+    }
+    const uint32_t ts = tmem + lanes + uint32_t((half * 2 + odd) * kCols);
+    for (int j = odd; half < halves && j < steps; j += 2) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&S.s_full[half][odd], (j >> 1) & 1, abort))) break;
       fence_after();
       const Block x = block_at(bl, i0 + j, s.m);
       // columns [low, x.cols) see this thread's key
@@ -297,16 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(ts + 64, v0);
       weigh(v1, 32);
       tmem_wait_ld(v0);
-      tmem_ld32(ts + 96, v1);
-      weigh(v0, 64);
-      tmem_wait_ld(v1);
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.s_empty[half][buf]);
-      weigh(v1, 96);
+      if (lane == 0) mbar_arrive(&S.s_empty[half][odd]);
+      weigh(v0, 64);
       sum += (lo2(l0) + hi2(l0)) + (lo2(l1) + hi2(l1));
     }
-    if (buf == 1) S.sums[slot - n0] = sum;
+    if (odd == 1) S.sums[slot - n0] = sum;
   }
   fence_before();
   __syncthreads();
