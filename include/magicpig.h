@@ -351,7 +351,8 @@ MP_API int mp_chunk_workspace_bytes(const mp_cache_config* cfg, int32_t total_q,
  * A token that sees nothing gets out = 0 and lse = -infinity. Slots at and behind kv_len
  * may hold anything (NaN included); the slots below it are expected to be finite: an
  * infinity or NaN there may reach tokens of the chunk that stand before it.
- * bf16: logits and sums are fp32, the softmax weights enter the second product as bf16. */
+ * bf16: logits and sums are fp32; the softmax weights enter the second product as bf16, or as
+ * the sum of two bf16 where a KV head has at most 16 rows (tokens x heads of its group). */
 MP_API int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t* cu_q, const int32_t* kv_len,
                               int32_t total_q, int32_t max_q, int32_t max_kv, const void* keys, const void* values,
                               const int32_t* page_table, void* out, float* lse, void* workspace,

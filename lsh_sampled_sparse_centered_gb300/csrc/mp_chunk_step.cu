@@ -10,8 +10,9 @@
 //     and 2t + 9; element i of the chunks makes the 16 x 16 tile of the d that are i modulo 8.
 //     The accumulators of S are P^T's fragments as they stand.
 // Loads of the next round are issued as soon as their registers are free. The reference of
-// a row's softmax is raised only when a logit passes it by more than 8 (log2). P is bf16
-// (2^-8 relative per weight), its sum is taken before that rounding.
+// a row's softmax is raised only when a logit passes it by more than 8 (log2). P enters the
+// second product as the sum of two bf16 terms (2^-17 relative per weight): the products are
+// a few percent of the time, and one term would double the result's error.
 #include "mp_cache.cuh"
 #include "mp_tc.cuh"
 
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
       load_k();
       find_k(next + kWarps * kRound);
     }
-    uint32_t p[NT][2];
+    uint32_t p[NT][2], rest[NT][2];  // P and what its rounding leaves
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       float top = fmaxf(fmaxf(x[u][0][0], x[u][0][1]), fmaxf(x[u][1][0], x[u][1][1]));
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
         const float e0 = ex2(x[u][i][0] - ref), e1 = ex2(x[u][i][1] - ref);
         l[u] += e0 + e1;
         p[u][i] = bf2(e0, e1);
+        rest[u][i] = bf2(e0 - __uint_as_float(p[u][i] << 16), e1 - __uint_as_float(p[u][i] & 0xffff0000u));
       }
     }
     // O^T: tile i holds the d that are i modulo 8 (of both 64-element halves; d = 64: i and i + 4)
@@ -165,7 +167,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
       const uint32_t a0 = pair(v[0][0], v[1][0], i), a1 = pair(v[0][c1], v[1][c1], e1);
       const uint32_t a2 = pair(v[2][0], v[3][0], i), a3 = pair(v[2][c1], v[3][c1], e1);
 #pragma unroll
-      for (int u = 0; u < NT; ++u) mma_16816(o[u][i], a0, a1, a2, a3, p[u][0], p[u][1]);
+      for (int u = 0; u < NT; ++u) {
+        mma_16816(o[u][i], a0, a1, a2, a3, p[u][0], p[u][1]);
+        mma_16816(o[u][i], a0, a1, a2, a3, rest[u][0], rest[u][1]);
+      }
     }
     if (next < k1) {
       load_v();
