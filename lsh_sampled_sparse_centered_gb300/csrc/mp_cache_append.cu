@@ -82,12 +82,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a
   if (b < 0) return;  // a row outside every sequence
   const Seq s = seq_of(c, b);
   if (r < s.row0 || r >= s.row0 + s.m) return;
-  const int slot = s.n - s.m + int(r - s.row0);
+  // from the length as it is: cut to the cache it would move the tokens to other slots
+  const int64_t slot = int64_t(c.kv_len[b]) - s.m + (r - s.row0);
   int64_t dst = -1;  // element offset of the slot's row of KV head 0
   if (slot >= 0 && slot < int64_t(c.cols) * c.page_size) {
-    const int col = slot / c.page_size;
+    const int col = int(slot) / c.page_size;
     const int p = page_at(c.table, c.cols, c.n_pages, b, col, c.status);
-    if (p >= 0) dst = (int64_t(p) * c.kvh * c.page_size + (slot - col * c.page_size)) * D;
+    if (p >= 0) dst = (int64_t(p) * c.kvh * c.page_size + (slot - int64_t(col) * c.page_size)) * D;
   } else if (l32 == 0) {
     flag(c.status, MP_STATUS_BAD_LENGTH);
   }

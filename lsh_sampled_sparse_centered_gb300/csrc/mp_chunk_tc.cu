@@ -56,7 +56,7 @@ struct Smem {
   __nv_bfloat16 kv[kStages][kSub][kKeys * 64];
   uint64_t full[kStages], empty[kStages], tail;
   uint64_t q_full[2], s_full[2], s_free[2], p_full[2][2], o_full[2];
-  uint64_t piece_full[2], piece_empty[2];
+  uint64_t piece_full[2], piece_empty[2], drain[2];
   Piece piece[2];
   int64_t left, run;
   int start[4];  // sequence, KV head, tile, unit
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.piece_full[i], 1);
       mbar_init(&S.piece_empty[i], 11);  // the TMA warp, two of products, eight of softmax
       mbar_init(&S.o_full[i], 1);
+      mbar_init(&S.drain[i], 1);
     }
     S.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -354,6 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // tiles below `st` were last filled in this lap of the ring, the others in the one before
+      if (!ok && lane == 0)
+        for (int i = 0; i < kStages; ++i) mbar_drain(&S.full[i], i < st ? ph : ph ^ 1);
     } else {
       // ---------------- products: warp 9 for the first half, 11 for the second ----------------
       // Each runs as one warp and an elected lane issues. A warp's own products follow each
@@ -466,6 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             product_s();
           }
         }
+      }
+      if (!ok) {
+        if (elect_one()) mma_commit(&S.drain[half]);
+        __syncwarp();
+        if (lane == 0) mbar_drain(&S.drain[half], 0);
+        __syncwarp();
       }
     }
   } else {

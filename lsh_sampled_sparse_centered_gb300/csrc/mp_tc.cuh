@@ -56,7 +56,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
   }
 }
-// The same by a whole warp, which then goes on as one: the instructions that one elected
+// After a wait has given up: the limited wait for what the CTA itself still has in flight
+// (copies into its shared memory, products on its tensor memory).
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_ns();
+  while (!mbar_try(bar, parity) && global_ns() - t0 < kWaitLimitNs) {
+  }
+}
+// mbar_wait by a whole warp, which then goes on as one: the instructions that one elected
 // lane issues for it take their operands from uniform registers (issued from a branch that
 // only one lane enters, a tcgen05.mma took 80 clocks to set up; this way it takes a few).
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {

@@ -40,7 +40,7 @@ struct WSmem {
   __nv_bfloat16 z[kStages][kCols * 16];  // (hi, mid, lo, 0, ...) of the step's rows (32-byte swizzle)
   __nv_bfloat16 ones[kHalf * 16];        // rows (1, 1, 1, 0, ...) (32-byte swizzle)
   float sums[kKeys];                     // of the odd steps
-  uint64_t k_full, k_ready, q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2];
+  uint64_t k_full, k_ready, q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2], drain[2];
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -119,6 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.q_empty[i], halves);
     }
     mbar_init(&S.k_ready, 4 * halves);
+    mbar_init(&S.drain[0], 1);
+    mbar_init(&S.drain[1], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&S.s_full[i >> 1][i & 1], 1);
       mbar_init(&S.s_empty[i >> 1][i & 1], 4);
@@ -168,6 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         st = 0;
         ph ^= 1;
       }
+    }
+    if (!ok && lane == 0) {
+      mbar_drain(&S.k_full, 0);
+      for (int i = 0; i < kStages; ++i) mbar_drain(&S.q_full[i], i < st ? ph ^ 1 : ph);
     }
   } else if (warp == 18) {
     // ---------------- -z of the rows, the next step's loads in flight ----------------
@@ -252,6 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         st = 0;
         ph ^= 1;
       }
+    }
+    if (!ok && half < halves) {
+      if (elect_one()) mma_commit(&S.drain[half]);
+      __syncwarp();
+      if (lane == 0) mbar_drain(&S.drain[half], 0);
+      __syncwarp();
     }
   } else {
     // ---------------- one thread per key and every other step ----------------

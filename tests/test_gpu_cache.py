@@ -203,6 +203,76 @@ def test_attention_over_offsets_past_32_bits(mp):
         check_attention(c, "bf16", q, cu, out, lse)
 
 
+def test_append_weights_and_evict_over_offsets_past_32_bits(mp):
+    ps, hk, d, n = 4096, 4, 128, 5000
+    pages = 2 ** 31 // (ps * hk * d) * 2 + 3
+    cfg = mp.make_cache_config(batch=1, kv_heads=hk, q_heads=hk, head_dim=d, page_size=ps, n_pages=pages, max_pages=2, dtype="bf16")
+    keys = torch.zeros(pages, hk, ps, d, dtype=torch.bfloat16, device=DEV)
+    values = torch.zeros_like(keys)
+    assert keys.numel() > 2 ** 32
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, k, v = (torch.randn(n, hk, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(3))
+    cu, cu_t = offsets([n])
+    kv_len = torch.tensor([n], dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q_out = torch.empty_like(q)
+    mp.mp_cache_append(cfg, mp.make_rotary(rot_dim=0), q, k, v, None, None, None, None, cu_t, kv_len, keys, values, table, q_out, status)
+    for pool, x in ((keys, k), (values, v)):
+        assert torch.equal(R.gather(pool, table, 0, 3, n), x[:, 3].double())
+    assert not keys[:-2].any() and not values[:-2].any() and torch.equal(q_out, q)
+    cu, cu_t = offsets([2])
+    lse = R.attention(q[:2], cu, [n], keys, values, table, hk)[1].float()
+    scores = torch.zeros(1, hk, 2 * ps, device=DEV)
+    mp.mp_cache_weights(cfg, q[:2], lse, cu_t, kv_len, 2, n, keys, table, scores, status)
+    want = R.weights(q[:2], lse, cu, [n], keys, table, torch.zeros_like(scores))[0]
+    assert ((scores.double() - want).abs() <= 2.0 ** -14 * want + 1e-30).all()
+    dst = mp.make_cache_config(batch=1, kv_heads=hk, q_heads=hk, head_dim=d, page_size=100, n_pages=1, dtype="bf16")
+    dk, dv = (torch.zeros(1, hk, 100, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    dlen, kept = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros(1, hk, 100, dtype=torch.int32, device=DEV)
+    ws = torch.empty(mp.mp_evict_workspace_bytes(cfg, n, 100), dtype=torch.uint8, device=DEV)
+    mp.mp_cache_evict(cfg, dst, keys, values, table, kv_len, n, scores, 4, 16, 100, dk, dv, None, None, dlen, kept, ws, status)
+    for h in range(hk):
+        keep = R.keep(scores[0, h], n, 4, 16, 100)
+        assert kept[0, h].tolist() == keep
+        at = torch.tensor(keep, device=DEV)
+        assert torch.equal(dk[0, h], k[at, h]) and torch.equal(dv[0, h], v[at, h])
+    assert status.item() == 0
+
+
+def test_attention_of_more_sequences_than_one_launch_takes(mp):
+    """The tensor-core path plans 1024 sequences at a time."""
+    batch = 1100
+    kv = [(7 * b) % 40 for b in range(batch)]
+    q_lens = [min(n, 1 + b % 5) for b, n in enumerate(kv)]
+    c = Cache(mp, "bf16", 5, 1, 64, 16, kv)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1] + 1, 5, 64)
+    out, lse = attend(mp, c, q, cu_t, 5)
+    check_attention(c, "bf16", q, cu, out, lse)
+    assert c.status.item() == 0
+
+
+def test_two_calls_at_once_with_a_workspace_each(mp):
+    """Two streams, both kinds of the attention, a shared page that both sequences read."""
+    for m in (1, 50):
+        c = Cache(mp, "bf16", 8, 2, 128, 64, [3000, 2500])
+        c.table[1, 0] = c.table[0, 0]
+        cu, cu_t = offsets([m, m])
+        qs = [c.randn(2 * m, 8, 128) for _ in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        size = max(1, mp.mp_chunk_workspace_bytes(c.cfg, 2 * m, m, 3000))
+        ws = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        outs = [(torch.empty_like(q), torch.empty(2 * m, 8, device=DEV)) for q in qs]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for q, (out, lse), w, st in zip(qs, outs, ws, streams):
+                mp.mp_chunk_attention(c.cfg, q, cu_t, c.kv_len, m, 3000, c.keys, c.values, c.table, out, lse, w, c.status, stream=st)
+        torch.cuda.synchronize()
+        for q, (out, lse) in zip(qs, outs):
+            check_attention(c, "bf16", q, cu, out, lse)
+
+
 def test_bad_lengths_and_pages_set_their_bits_and_leave_the_rest(mp):
     c = Cache(mp, "bf16", 8, 2, 128, 32, [200, 100, 150])
     cu, cu_t = offsets([5, 40, 1])
@@ -368,6 +438,24 @@ def test_append(mp, dtype, hq, hk, d, page, q_lens, kv, rot, inter, norms):
             assert (pool.transpose(1, 2)[~touched] == 5.0).all()
 
 
+def test_append_past_the_end_of_the_cache(mp):
+    """Tokens behind the cache's last slot are left out, the others stand where they belong."""
+    c = Cache(mp, "bf16", 2, 1, 64, 16, [48], fill="none")
+    c.keys.fill_(5.0)
+    c.values.fill_(5.0)
+    _, cu_t = offsets([6])
+    c.kv_len[0] = 51  # three more than the table has room for: slots 45 to 50
+    q, k, v = c.randn(6, 2, 64), c.randn(6, 1, 64), c.randn(6, 1, 64)
+    q_out = torch.empty_like(q)
+    mp.mp_cache_append(c.cfg, mp.make_rotary(rot_dim=0), q, k, v, None, None, None, None, cu_t, c.kv_len, c.keys, c.values, c.table, q_out,
+                       c.status)
+    assert c.status.item() == mp.MP_STATUS_BAD_LENGTH
+    last = int(c.table[0, 2])
+    assert torch.equal(c.keys[last, 0, 13:], k[:3, 0]) and torch.equal(c.values[last, 0, 13:], v[:3, 0])
+    c.keys[last, 0, 13:] = 5.0
+    assert (c.keys == 5.0).all() and torch.equal(q_out, q)
+
+
 def test_append_far_positions_and_bad_pages(mp):
     """Angles of hundreds of millions of radians, negative positions, and a page outside the pool."""
     c = Cache(mp, "f32", 2, 1, 64, 16, [40], fill="none")
@@ -480,6 +568,64 @@ def test_evict_skips_bad_destination_pages(mp):
 
 
 # ---- together ----
+
+def test_a_captured_step_follows_the_lengths(mp):
+    """One generated token's append, attention, weights and eviction in one graph, replayed
+    while the sequence grows (what a serving loop captures once), in fp32 and bf16."""
+    for dtype in ("bf16", "f32"):
+        c = Cache(mp, dtype, 4, 2, 64, 16, [0, 0], cap=200, fill="none")
+        c.keys.zero_()
+        c.values.zero_()
+        full = torch.arange(2 * c.cols, dtype=torch.int32, device=DEV).view(2, c.cols)
+        c.table.copy_(full)
+        cu, cu_t = offsets([1, 1])
+        q, k, v = c.randn(2, 4, 64), c.randn(2, 2, 64), c.randn(2, 2, 64)
+        q_out, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(2, 4, device=DEV)
+        inv = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).to(DEV)
+        scores = torch.zeros(2, 2, c.ps * c.cols, device=DEV)
+        ws = torch.empty(max(1, mp.mp_chunk_workspace_bytes(c.cfg, 2, 1, 200)), dtype=torch.uint8, device=DEV)
+        t = Cache(mp, dtype, 4, 2, 64, 0, [20, 20], cap=20, fill="none")
+        dlen, kept = torch.zeros(2, dtype=torch.int32, device=DEV), torch.zeros(2, 2, 20, dtype=torch.int32, device=DEV)
+        ews = torch.empty(mp.mp_evict_workspace_bytes(c.cfg, 200, 20), dtype=torch.uint8, device=DEV)
+
+        def step():
+            mp.mp_cache_append(c.cfg, mp.make_rotary(rot_dim=64), q, k, v, None, None, inv, None, cu_t, c.kv_len, c.keys, c.values, c.table,
+                               q_out, c.status)
+            mp.mp_chunk_attention(c.cfg, q_out, cu_t, c.kv_len, 1, 200, c.keys, c.values, c.table, out, lse, ws, c.status)
+            mp.mp_cache_weights(c.cfg, q_out, lse, cu_t, c.kv_len, 1, 200, c.keys, c.table, scores, c.status)
+            mp.mp_cache_evict(c.cfg, t.cfg, c.keys, c.values, c.table, c.kv_len, 200, scores, 2, 4, 20, t.keys, t.values, None, None, dlen,
+                              kept, ews, c.status)
+
+        st = torch.cuda.Stream()
+        c.kv_len.fill_(1)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            step()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=st):
+                step()
+        scores.zero_()
+        want = torch.zeros(2, 2, c.ps * c.cols, dtype=torch.float64, device=DEV)
+        for n in range(1, 60):
+            c.kv = [n, max(1, n - 5)]
+            c.kv_len.copy_(torch.tensor(c.kv, dtype=torch.int32))
+            q.copy_(c.randn(2, 4, 64))
+            k.copy_(c.randn(2, 2, 64))
+            v.copy_(c.randn(2, 2, 64))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            check_attention(c, dtype, q_out, cu, out, lse)
+            want = R.weights(q_out, lse, cu, c.kv, c.keys, c.table, want)[0]
+        # each step adds one exponential's error (2^-21 and the logits'), weighted as the sum is
+        assert ((scores.double() - want).abs() <= 2.0 ** -16 * want).all()
+        assert c.status.item() == 0 and dlen.tolist() == [20, 20]
+        for b, n in enumerate(c.kv):
+            for h in range(2):
+                keep = R.keep(scores[b, h], n, 2, 4, 20)
+                assert kept[b, h].tolist() == keep
+                assert torch.equal(t.keys[b, h], pool_rows(c.keys, c, b, h, n)[torch.tensor(keep, device=DEV)])
+
 
 def test_a_prompt_in_chunks_then_eviction_then_sampled_decode(mp):
     """The operators as a serving loop uses them on one dense layer: a prompt arrives in
