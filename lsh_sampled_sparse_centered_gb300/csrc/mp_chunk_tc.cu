@@ -60,6 +60,7 @@ struct Smem {
   Piece piece[2];
   int64_t left, run;
   int start[4];  // sequence, KV head, tile, unit
+  uint8_t filled[kStages];  // phase in which each tile of the ring was last filled (1: never)
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&S.full[i], 1);
       mbar_init(&S.empty[i], 2);  // both halves' products
+      S.filled[i] = 1;
     }
     mbar_init(&S.tail, 1);
     for (int i = 0; i < 2; ++i) {
@@ -327,7 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // hold anything, and 0 * NaN is NaN (in S such columns are masked)
             const bool patch = kv == 1 && live < kKeys;
             uint64_t* bar = patch ? &S.tail : &S.full[st];
-            if (lane == 0) mbar_expect_tx(bar, uint32_t(boxes) * box * kRowBytes * kSub);
+            if (lane == 0) {
+              mbar_expect_tx(bar, uint32_t(boxes) * box * kRowBytes * kSub);
+              S.filled[st] = uint8_t(ph);
+            }
             __syncwarp();
             for (int j = lane; j < boxes; j += 32) {
               const int row = slot_row(c, pc.b, pc.h, n0 + j * box);
@@ -355,9 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // tiles below `st` were last filled in this lap of the ring, the others in the one before
-      if (!ok && lane == 0)
-        for (int i = 0; i < kStages; ++i) mbar_drain(&S.full[i], i < st ? ph : ph ^ 1);
     } else {
       // ---------------- products: warp 9 for the first half, 11 for the second ----------------
       // Each runs as one warp and an elected lane issues. A warp's own products follow each
@@ -668,7 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
-  if (threadIdx.x == 0 && S.abort) flag(c.status, MP_STATUS_WAIT_TIMEOUT);
+  if (threadIdx.x == 0 && S.abort) {
+    for (int i = 0; i < kStages; ++i) mbar_drain(&S.full[i], S.filled[i]);
+    flag(c.status, MP_STATUS_WAIT_TIMEOUT);
+  }
 }
 
 // One warp per row of a tile that was cut: joins the pieces' (m, l, sum), eight at a time in
