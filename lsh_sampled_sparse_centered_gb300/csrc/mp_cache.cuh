@@ -68,6 +68,7 @@ struct EvictArgs {
 int chunk_splits(const mp_cache_config* c, int max_q, int max_kv);
 bool chunk_is_step(int group, int max_q);
 int chunk_step_splits(int batch, int kvh, int group, int max_q, int max_kv);
+bool chunk_step_joined(int splits);  // the slices join themselves
 int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv);
 uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv);
 

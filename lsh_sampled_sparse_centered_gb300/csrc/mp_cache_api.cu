@@ -69,6 +69,9 @@ static int slices(const mp_cache_config* c, int max_q, int max_kv) {
   if (c->dtype != MP_DTYPE_BF16) return chunk_splits(c, max_q, max_kv);
   return chunk_step_splits(c->batch, c->kv_heads, c->q_heads / c->kv_heads, max_q, max_kv);
 }
+static bool needs_join(const mp_cache_config* c, int splits) {
+  return splits > 1 && !(c->dtype == MP_DTYPE_BF16 && chunk_step_joined(splits));
+}
 static uint64_t part_bytes(const mp_cache_config* c, int total_q, int splits) {
   return align256(uint64_t(splits) * total_q * c->q_heads * c->head_dim * 4);
 }
@@ -77,7 +80,7 @@ static uint64_t chunk_bytes(const mp_cache_config* c, int total_q, int max_q, in
   max_q = std::min(max_q, total_q);
   if (chunk_on_tensor_cores(c, max_q)) return chunk_tc_workspace(c, max_q, max_kv);
   const int splits = slices(c, max_q, max_kv);
-  if (splits <= 1) return 0;
+  if (!needs_join(c, splits)) return 0;
   return part_bytes(c, total_q, splits) + align256(uint64_t(splits) * total_q * c->q_heads * 2 * 4);
 }
 
@@ -208,7 +211,7 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
     const cudaError_t e = cfg->dtype == MP_DTYPE_BF16 ? launch_chunk_step(a, st) : launch_chunk_simt(a, st);
     if (e != cudaSuccess) return MP_ERR_CUDA;
   }
-  if (a.splits > 1) {
+  if (needs_join(cfg, a.splits)) {
     ProfScope ps(st, K_CHUNK_JOIN);
     if (launch_chunk_join(a, cfg->dtype, st) != cudaSuccess) return MP_ERR_CUDA;
   }

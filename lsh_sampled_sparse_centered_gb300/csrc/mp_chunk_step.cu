@@ -13,16 +13,22 @@
 // a row's softmax is raised only when a logit passes it by more than 8 (log2). P enters the
 // second product as the sum of two bf16 terms (2^-17 relative per weight): the products are
 // a few percent of the time, and one term would double the result's error.
+#include <cooperative_groups.h>
+
 #include "mp_cache.cuh"
 #include "mp_tc.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int kWarps = 4, kRound = 16;  // slots of a warp and round
+namespace cg = cooperative_groups;
+
+constexpr int kRound = 16;  // slots of a warp and round
+__host__ __device__ constexpr int warps_of(bool joined) { return joined ? 8 : 4; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;
+constexpr int kShort = 4096;
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 // element e (0..7) of the 16-byte chunks a and b as one pair
@@ -30,8 +36,11 @@ __device__ __forceinline__ uint32_t pair(const uint4& a, const uint4& b, int e) 
   return __byte_perm(word(a, e >> 1), word(b, e >> 1), (e & 1) ? 0x7632 : 0x5410);
 }
 
-template <int D, int NT>  // NT: query rows in eights
-__global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
+// NT: query rows in eights. JOINED: the slices of a KV head are a cluster and join through
+// distributed shared memory (no second kernel, no workspace).
+template <int D, int NT, bool JOINED>
+__global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const ChunkArgs a) {
+  constexpr int kWarps = warps_of(JOINED);
   constexpr int KC = D / 32;      // chunks of a K row per lane
   constexpr int VC = D / 64;      // chunks of a V row per lane
   constexpr int TILES = D / 16;   // 16-row tiles of O^T
@@ -42,7 +51,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Seq s = seq_of(c, b);
   const int rows = s.m * c.group, first = s.n - s.m, qh = c.kvh * c.group;
-  if (rows == 0) return;
+  if (rows == 0) return;  // the whole cluster
   // this CTA's slots, a whole number of rounds of all warps
   const int per = ((s.n + a.splits - 1) / a.splits + kWarps * kRound - 1) / (kWarps * kRound) * (kWarps * kRound);
   const int k0 = int(min(int64_t(s.n), int64_t(split) * per)), k1 = min(s.n, k0 + per);
@@ -177,8 +186,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
       find_v(next + kWarps * kRound);
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_chunk_join may be set up
-  // the four warps' parts, in their order
+  if (!JOINED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_chunk_join may be set up
+  // the warps' parts, in their order
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
     l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
@@ -210,7 +219,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
     const int64_t row = int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group;
     const int64_t at = int64_t(split) * c.total_q * qh + row;
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    if (lane == 0) {
+    if (lane == 0 && !JOINED) {
       if (a.splits > 1) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(top, sum);
       else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
     }
@@ -224,20 +233,80 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_step(const ChunkArgs a) {
         y.z = fmaf(z.z, by[w], y.z);
         y.w = fmaf(z.w, by[w], y.w);
       }
-      if (a.splits > 1)
+      if (JOINED)
+        *reinterpret_cast<float4*>(&so[0][r][d]) = y;  // this row's own place, read above
+      else if (a.splits > 1)
         *reinterpret_cast<float4*>(a.part + at * D + d) = y;
       else
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d) =
             make_uint2(bf2(y.x * inv, y.y * inv), bf2(y.z * inv, y.w * inv));
     }
+    if (JOINED) {
+      __syncwarp();
+      if (lane == 0) {
+        sm[0][r] = top;
+        sl[0][r] = sum;
+      }
+    }
   }
+  if (!JOINED) return;
+  // the slices' sums, in their order: CTA i of the cluster joins the rows i, i + size, ...
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  constexpr int kMost = 8;
+  for (int r = split + warp * a.splits; r < rows; r += kWarps * a.splits) {
+    float part_m[kMost], part_l[kMost], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      part_m[i] = i < a.splits ? *cluster.map_shared_rank(&sm[0][r], i) : -INFINITY;
+      part_l[i] = i < a.splits ? *cluster.map_shared_rank(&sl[0][r], i) : 0.f;
+      top = fmaxf(top, part_m[i]);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      part_m[i] = ex2(part_m[i] - ref);
+      sum = fmaf(part_l[i], part_m[i], sum);
+    }
+    const int64_t row = int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group;
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+    for (int d = lane * 4; d < D; d += 128) {
+      float4 z[kMost], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kMost; ++i)
+        z[i] = i < a.splits ? *reinterpret_cast<const float4*>(cluster.map_shared_rank(&so[0][r][d], i)) : y;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        y.x = fmaf(z[i].x, part_m[i], y.x);
+        y.y = fmaf(z[i].y, part_m[i], y.y);
+        y.z = fmaf(z[i].z, part_m[i], y.z);
+        y.w = fmaf(z[i].w, part_m[i], y.w);
+      }
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d) =
+          make_uint2(bf2(y.x * inv, y.y * inv), bf2(y.z * inv, y.w * inv));
+    }
+  }
+  cluster.sync();  // no CTA leaves while others read its sums
 }
 
 template <int D>
-void launch(const ChunkArgs& a, cudaStream_t st) {
-  const dim3 grid(a.splits, a.c.kvh, a.c.batch);
-  if (int64_t(a.c.max_q) * a.c.group <= 8) k_chunk_step<D, 1><<<grid, kWarps * 32, 0, st>>>(a);
-  else k_chunk_step<D, 2><<<grid, kWarps * 32, 0, st>>>(a);
+cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.splits, a.c.kvh, a.c.batch);
+  cfg.blockDim = dim3(warps_of(chunk_step_joined(a.splits)) * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.splits;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  const bool one = int64_t(a.c.max_q) * a.c.group <= 8;
+  if (chunk_step_joined(a.splits)) {
+    cfg.numAttrs = 1;
+    return one ? cudaLaunchKernelEx(&cfg, k_chunk_step<D, 1, true>, a) : cudaLaunchKernelEx(&cfg, k_chunk_step<D, 2, true>, a);
+  }
+  return one ? cudaLaunchKernelEx(&cfg, k_chunk_step<D, 1, false>, a) : cudaLaunchKernelEx(&cfg, k_chunk_step<D, 2, false>, a);
 }
 
 }  // namespace
@@ -246,19 +315,20 @@ bool chunk_is_step(int group, int max_q) { return int64_t(max_q) * group <= 16; 
 
 // Slices of at least 128 slots: one wave of the CTAs that fit (three per SM with up to eight
 // rows, two with more), or two waves where a slice then still has 2048 slots (98304 slots of
-// eight KV heads: 66.8 us in one wave, 71.0 in two; four times that: 222 and 217 us).
+// eight KV heads: 66.8 us in one wave, 71.0 in two; four times that: 222 and 217 us). Caches of up to kShort slots take eight, a cluster that
+// joins itself (2048 slots of eight KV heads: 8.9 us, 10.5 with 16 slices and a second kernel).
 int chunk_step_splits(int batch, int kvh, int group, int max_q, int max_kv) {
   const int64_t fit = int64_t(device_sm_count()) * (int64_t(max_q) * group <= 8 ? 3 : 2), units = int64_t(batch) * kvh;
   const int64_t wave = fit / units, most = (int64_t(max_kv) + 127) / 128;
   const int64_t two = 2 * fit / units;
   const int64_t fill = two * 2048 <= max_kv ? two : wave, s = fill < most ? fill : most;
+  if (s > 8 && max_kv <= kShort) return 8;
   return int(s < 1 ? 1 : s);
 }
+bool chunk_step_joined(int splits) { return splits == 2 || splits == 4 || splits == 8; }
 
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st) {
-  if (a.c.d == 128) launch<128>(a, st);
-  else launch<64>(a, st);
-  return cudaGetLastError();
+  return a.c.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
 
 }  // namespace mp
