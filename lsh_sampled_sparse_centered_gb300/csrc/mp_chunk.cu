@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
   load_transposed<D>(kt, [&](int i) -> const float* {
     return n0 + i < s.n ? static_cast<const float*>(a.keys) + slot_read(c, b, h, n0 + i) : nullptr;
   });
-  const float scale = kLog2e * rsqrtf(float(D));
+  const float root = rsqrtf(float(D));
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   // rows before token n0 - first see none of these slots
   const int start = max(0, n0 - first) * c.group / kBM * kBM;
@@ -338,10 +338,10 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
       const int r = r0 + ty * 8 + i;
       if (r >= rows) continue;
       const int t = r / c.group;
-      const float z = a.lse[int64_t(s.row0 + t) * qh + h * c.group + r % c.group] * kLog2e;
+      const float z = a.lse[int64_t(s.row0 + t) * qh + h * c.group + r % c.group];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (n0 + tx * 4 + j <= first + t) acc[j] += exp2f(fmaf(x[i][j], scale, -z));
+        if (n0 + tx * 4 + j <= first + t) acc[j] += exp2f(kLog2e * fmaf(x[i][j], root, -z));
     }
   }
   *reinterpret_cast<float4*>(col + ty * 64 + tx * 4) = make_float4(acc[0], acc[1], acc[2], acc[3]);

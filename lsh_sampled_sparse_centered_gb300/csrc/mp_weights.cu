@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsA
   if (p0 >= s.n || s.m == 0) return;
   const int p1 = min(s.n, int(p0) + per);
   const int first = s.n - s.m, qh = c.kvh * c.group, rows = s.m * c.group;
-  const float scale = kLog2e * rsqrtf(float(D));
+  const float root = rsqrtf(float(D));
   float* scores = a.scores + (int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size);
   const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.keys);
   uint4 k[2][KC];
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsA
     for (int i = 0; i < 2; ++i) {
       const int rc = u * 8 + 2 * t + i;
       see[u][i] = rc < rows ? first + rc / c.group + 1 : 0;
-      nz[u][i] = rc < rows ? -kLog2e * a.lse[int64_t(s.row0 + rc / c.group) * qh + h * c.group + rc % c.group] : 0.f;
+      nz[u][i] = rc < rows ? -a.lse[int64_t(s.row0 + rc / c.group) * qh + h * c.group + rc % c.group] : 0.f;
     }
   }
   for (; n0 < p1; n0 += kAll) {
@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsA
     for (int u = 0; u < NT; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (n0 + g + 8 * (i >> 1) < see[u][i & 1]) sum[i >> 1] += ex2(fmaf(x[u][i], scale, nz[u][i & 1]));
+        if (n0 + g + 8 * (i >> 1) < see[u][i & 1])  // z taken off before the change to log2: its rounding there would count
+          sum[i >> 1] += ex2(kLog2e * fmaf(x[u][i], root, nz[u][i & 1]));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
