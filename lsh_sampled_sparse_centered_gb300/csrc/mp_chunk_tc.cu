@@ -683,42 +683,44 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
   constexpr int PER = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
-  const int i = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (cut.pieces == 0 || i >= cut.rows) return;
+  const int lane = threadIdx.x & 31;
+  if (cut.pieces == 0) return;
   const int group = a.c.group, qh = a.c.kvh * group;
-  auto at = [&](int p) { return int64_t(p == 0 ? cut.slot : 2 * (int(blockIdx.x) + p)) * slot_rows + i; };
-  const float2* ml = reinterpret_cast<const float2*>(a.ml);
-  float m = -INFINITY;
-  for (int p = lane; p < cut.pieces; p += 32) m = fmaxf(m, ml[at(p)].x);
+  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < cut.rows; i += gridDim.y * 8) {
+    auto at = [&](int p) { return int64_t(p == 0 ? cut.slot : 2 * (int(blockIdx.x) + p)) * slot_rows + i; };
+    const float2* ml = reinterpret_cast<const float2*>(a.ml);
+    float m = -INFINITY;
+    for (int p = lane; p < cut.pieces; p += 32) m = fmaxf(m, ml[at(p)].x);
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[PER];
+    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[PER];
 #pragma unroll
-  for (int j = 0; j < PER; ++j) o[j] = 0.f;
-  for (int p = 0; p < cut.pieces; p += 8) {
-    float x[8][PER], f[8];
+    for (int j = 0; j < PER; ++j) o[j] = 0.f;
+    for (int p = 0; p < cut.pieces; p += 8) {
+      float x[8][PER], f[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 v = p + k < cut.pieces ? ml[at(p + k)] : make_float2(-INFINITY, 0.f);
-      f[k] = v.y == 0.f ? 0.f : exp2f(v.x - ref);
-      l = fmaf(v.y, f[k], l);
-      const bool live = v.y != 0.f;  // a piece that saw nothing has written no sum
+      for (int k = 0; k < 8; ++k) {
+        const float2 v = p + k < cut.pieces ? ml[at(p + k)] : make_float2(-INFINITY, 0.f);
+        f[k] = v.y == 0.f ? 0.f : exp2f(v.x - ref);
+        l = fmaf(v.y, f[k], l);
+        const bool live = v.y != 0.f;  // a piece that saw nothing has written no sum
 #pragma unroll
-      for (int j = 0; j < PER; ++j) x[k][j] = live ? a.part[at(p + k) * D + lane * PER + j] : 0.f;
+        for (int j = 0; j < PER; ++j) x[k][j] = live ? a.part[at(p + k) * D + lane * PER + j] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) o[j] = fmaf(x[k][j], f[k], o[j]);
     }
+    const int r = cut.r0 + i;
+    const int64_t row = cut.row + int64_t(r / group) * qh + r % group;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-#pragma unroll
-      for (int j = 0; j < PER; ++j) o[j] = fmaf(x[k][j], f[k], o[j]);
+    for (int j = 0; j < PER; ++j)
+      static_cast<__nv_bfloat16*>(a.out)[row * D + lane * PER + j] = __float2bfloat16(o[j] * inv);
   }
-  const int r = cut.r0 + i;
-  const int64_t row = cut.row + int64_t(r / group) * qh + r % group;
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-#pragma unroll
-  for (int j = 0; j < PER; ++j)
-    static_cast<__nv_bfloat16*>(a.out)[row * D + lane * PER + j] = __float2bfloat16(o[j] * inv);
 }
 
 int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
@@ -746,7 +748,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
   for (int b = 0; b < c.batch; b += kGroup) {
     k_chunk_tc<D><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, (slot_rows + 7) / 8);
+    cfg.gridDim = dim3(ctas, std::min(16, (slot_rows + 7) / 8));  // few CTAs: most runs leave nothing to join
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
