@@ -638,11 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!real) {
           } else if (!whole) {
             if (sum > 0.f) {
-              float4* dst = reinterpret_cast<float4*>(a.part + at * D + g * 32);
+              float4* dst = reinterpret_cast<float4*>(a.part) +
+                            (int64_t(pc.slot) * (D / 4) + g * 8) * slot_rows + (r - pc.r0);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                     __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                dst[i * slot_rows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
             }
           } else {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + g * 32);
@@ -676,51 +677,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// One warp per row of a tile that was cut: joins the pieces' (m, l, sum), eight at a time in
-// their order. Set up while k_chunk_tc still runs; it waits for it first.
+// Joins the pieces' (m, l, sum) of the tiles that were cut, in their order: a warp takes 32
+// rows, a lane each, and 16 columns. Partial sums lie [slot][column / 4][row][4], so that
+// the threads that own rows (in the kernel above and here) write and read whole lines. Set up
+// while k_chunk_tc still runs; it waits for it first.
 template <int D>
 __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const int slot_rows) {
-  constexpr int PER = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
-  const int lane = threadIdx.x & 31;
-  if (cut.pieces == 0) return;
-  const int group = a.c.group, qh = a.c.kvh * group;
-  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < cut.rows; i += gridDim.y * 8) {
-    auto at = [&](int p) { return int64_t(p == 0 ? cut.slot : 2 * (int(blockIdx.x) + p)) * slot_rows + i; };
-    const float2* ml = reinterpret_cast<const float2*>(a.ml);
-    float m = -INFINITY;
-    for (int p = lane; p < cut.pieces; p += 32) m = fmaxf(m, ml[at(p)].x);
+  const int task = blockIdx.y * 8 + (threadIdx.x >> 5), columns = task % (D / 16);
+  const int i = task / (D / 16) * 32 + (threadIdx.x & 31);
+  if (i >= cut.rows || cut.pieces == 0) return;
+  auto slot = [&](int p) { return int64_t(p == 0 ? cut.slot : 2 * (int(blockIdx.x) + p)); };
+  const float2* ml = reinterpret_cast<const float2*>(a.ml) + i;
+  const float4* part = reinterpret_cast<const float4*>(a.part) + int64_t(columns) * 4 * slot_rows + i;
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int p = 0; p < cut.pieces; ++p) m = fmaxf(m, ml[slot(p) * slot_rows].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o[4];
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[PER];
+  for (int j = 0; j < 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int p = 0; p < cut.pieces; ++p) {
+    const float2 v = ml[slot(p) * slot_rows];
+    const bool live = v.y != 0.f;  // a piece that saw nothing has written no sum
+    const float by = live ? exp2f(v.x - ref) : 0.f;
+    l = fmaf(v.y, by, l);
+    float4 x[4];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) o[j] = 0.f;
-    for (int p = 0; p < cut.pieces; p += 8) {
-      float x[8][PER], f[8];
+    for (int j = 0; j < 4; ++j)
+      x[j] = live ? part[(slot(p) * (D / 4) + j) * slot_rows] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 v = p + k < cut.pieces ? ml[at(p + k)] : make_float2(-INFINITY, 0.f);
-        f[k] = v.y == 0.f ? 0.f : exp2f(v.x - ref);
-        l = fmaf(v.y, f[k], l);
-        const bool live = v.y != 0.f;  // a piece that saw nothing has written no sum
-#pragma unroll
-        for (int j = 0; j < PER; ++j) x[k][j] = live ? a.part[at(p + k) * D + lane * PER + j] : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int j = 0; j < PER; ++j) o[j] = fmaf(x[k][j], f[k], o[j]);
+    for (int j = 0; j < 4; ++j) {
+      o[j].x = fmaf(x[j].x, by, o[j].x);
+      o[j].y = fmaf(x[j].y, by, o[j].y);
+      o[j].z = fmaf(x[j].z, by, o[j].z);
+      o[j].w = fmaf(x[j].w, by, o[j].w);
     }
-    const int r = cut.r0 + i;
-    const int64_t row = cut.row + int64_t(r / group) * qh + r % group;
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-      static_cast<__nv_bfloat16*>(a.out)[row * D + lane * PER + j] = __float2bfloat16(o[j] * inv);
   }
+  const int group = a.c.group, r = cut.r0 + i;
+  const int64_t row = cut.row + int64_t(r / group) * (a.c.kvh * group) + r % group;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  if (a.lse && columns == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + columns * 16);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    out[j] = make_uint4(bf2(o[2 * j].x * inv, o[2 * j].y * inv), bf2(o[2 * j].z * inv, o[2 * j].w * inv),
+                        bf2(o[2 * j + 1].x * inv, o[2 * j + 1].y * inv), bf2(o[2 * j + 1].z * inv, o[2 * j + 1].w * inv));
 }
 
 int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
@@ -748,7 +753,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
   for (int b = 0; b < c.batch; b += kGroup) {
     k_chunk_tc<D><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, std::min(16, (slot_rows + 7) / 8));  // few CTAs: most runs leave nothing to join
+    cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 16) + 7) / 8);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
