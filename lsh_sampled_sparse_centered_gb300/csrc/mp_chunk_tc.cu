@@ -635,9 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld32(to + g * 32, o);
           tmem_wait_ld(o);
-          if (!real) {
-          } else if (!whole) {
-            if (sum > 0.f) {
+          if (!whole) {
+            if (real && sum > 0.f) {
               float4* dst = reinterpret_cast<float4*>(a.part) +
                             (int64_t(pc.slot) * (D / 4) + g * 8) * slot_rows + (r - pc.r0);
 #pragma unroll
@@ -646,14 +645,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + g * 32);
+            // Four lanes swap their rows' 16-byte parts, so that each store writes 64 bytes of a row.
+            uint32_t v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              v[k] = bf2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+#pragma unroll
+            for (int bit = 1; bit <= 2; bit *= 2) {
+              const bool high = lane & bit;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                if (k & (4 * bit)) continue;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? v[k] : v[k + 4 * bit], bit);
+                if (high) v[k] = got;
+                else v[k + 4 * bit] = got;
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                v[k] = bf2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-              dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+              const int64_t to_row = __shfl_sync(0xffffffffu, row, (lane & ~3) + i);
+              if (r - (lane & 3) + i < rows)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to_row * D + g * 32 + (lane & 3) * 8) =
+                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
           __syncwarp();
