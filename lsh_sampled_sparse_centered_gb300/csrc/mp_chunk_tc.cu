@@ -19,6 +19,12 @@
 // that fills it and P overlays its S, so that the next S waits for the product with P. With
 // d = 64 P has columns of its own (384 and 448): the next S is formed while the softmax of
 // this one still runs.
+//
+// With d = 128 the halves take turns: one reads its S and weighs three quarters of it, then
+// the other may. Left alone they may fall into step, both in the softmax and then both
+// waiting for products, and stay there (2048 tokens over 32768 slots, 32/8 heads: 700 to 770
+// us by how they started, 670 us with turns; 1024 over 8192: 117 and 104 us). With d = 64,
+// where S is formed ahead, turns cost a quarter (540 against 680 us).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -38,6 +44,7 @@ constexpr float kRaise = 8.0f;
 constexpr int kGroup = 1024;  // sequences of a launch
 constexpr int kLead = 3;      // units that starting and ending a tile costs (5.5 us, a step 1.5 to 1.8 us)
 constexpr int kMinRun = 2;    // units of a CTA at least
+constexpr int kCut = 10;      // units that cutting the tiles costs: a second piece for most CTAs, and the join
 
 // One piece of work: the steps [u0, u1) of a tile, as every role of the CTA sees it.
 struct Piece {
@@ -46,6 +53,11 @@ struct Piece {
   int u0, u1;               // u0 == u1: the run has ended
   int whole, slot;          // all of its tile's units; else where its partial result goes
 };
+
+// Of numbers that are not negative; nearly always of 32 bits, where it costs a fraction.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return uint64_t(a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
 
 template <int D>
 struct Smem {
@@ -56,10 +68,12 @@ struct Smem {
   __nv_bfloat16 kv[kStages][kSub][kKeys * 64];
   uint64_t full[kStages], empty[kStages], tail;
   uint64_t q_full[2], s_full[2], s_free[2], p_full[2][2], o_full[2];
-  uint64_t piece_full[2], piece_empty[2], drain[2];
+  uint64_t piece_full[2], piece_empty[2], drain[2], turn[2];
   Piece piece[2];
   int64_t left, run;
   int start[4];  // sequence, KV head, tile, unit
+  Seq first;     // that sequence
+  int longest[12];  // units of a tile, of each warp's sequences
   uint8_t filled[kStages];  // phase in which each tile of the ring was last filled (1: never)
   uint32_t tmem_base;
   uint32_t abort;
@@ -138,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.piece_empty[i], 11);  // the TMA warp, two of products, eight of softmax
       mbar_init(&S.o_full[i], 1);
       mbar_init(&S.drain[i], 1);
+      mbar_init(&S.turn[i], 4);
     }
     S.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -150,31 +165,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // ---- where this CTA's run starts ----
   int64_t* units = reinterpret_cast<int64_t*>(&S.kv[0][0][0]);  // of each sequence and KV head; the ring is not yet in use
-  static_assert(kGroup * 8 <= kKeys * 128, "one tile of the ring");
+  int* counts = reinterpret_cast<int*>(&S.kv[1][0][0]);                  // tiles of each sequence and KV head
+  Seq* seqs = reinterpret_cast<Seq*>(&S.kv[2][0][0]);
+  static_assert(kGroup * sizeof(Seq) <= kKeys * 128, "one tile of the ring");
+  int longest = 0;  // units of a tile
   for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
     const Seq s = seq_of(c, b);
     const int tiles = tiles_of(s, c.group);
     int64_t u = 0;
-    for (int t = lane; t < tiles; t += 32) u += kLead + steps_of(s, c.group, t);
+    for (int t = lane; t < tiles; t += 32) {
+      const int mine = kLead + steps_of(s, c.group, t);
+      u += mine;
+      longest = max(longest, mine);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    if (lane == 0) units[b - b_begin] = u;  // of one KV head
+    if (lane == 0) {  // of one KV head
+      seqs[b - b_begin] = s;
+      units[b - b_begin] = u;
+      counts[b - b_begin] = tiles;
+    }
   }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) S.longest[warp] = longest;
   __syncthreads();
   if (warp == 0) {
-    int64_t all = 0;
-    for (int b = lane; b < b_end - b_begin; b += 32) all += units[b] * c.kvh;
+    int64_t all = 0, all_tiles = 0;
+    for (int b = lane; b < b_end - b_begin; b += 32) {
+      all += units[b] * c.kvh;
+      all_tiles += int64_t(counts[b]) * c.kvh;
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    const int64_t run = max(int64_t(kMinRun), (all + gridDim.x - 1) / int64_t(gridDim.x));
-    int64_t at = blockIdx.x * run;
-    int64_t left = max(int64_t(0), min(run, all - at));
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      all_tiles += __shfl_xor_sync(0xffffffffu, all_tiles, o);
+    }
+    longest = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? S.longest[lane] : 0);
+    const int64_t run = max(int64_t(kMinRun), quotient(all + gridDim.x - 1, gridDim.x));
+    // Equal runs cut tiles; where a CTA for each tile takes little longer, none is cut (1024
+    // tokens, 32/8 heads, 128 tiles: over 2048 slots 47 against 51 us; over 8192, where the rule
+    // cuts, 107 against 104).
+    const bool by_tile = all_tiles <= gridDim.x && longest <= run + kCut;
+    int64_t at = by_tile ? blockIdx.x : blockIdx.x * run;  // into the tiles, or their units
+    int64_t left = max(int64_t(0), by_tile ? min(int64_t(1), all_tiles - at) : min(run, all - at));
     if (left > 0) {
       // the sequence, by prefix sums of 32 at a time
       int b = b_begin;
       bool found = false;
       for (; b < b_end; b += 32) {
-        const int64_t mine = b + lane < b_end ? units[b + lane - b_begin] * c.kvh : 0;
+        const int64_t mine =
+            b + lane < b_end ? (by_tile ? counts[b + lane - b_begin] : units[b + lane - b_begin]) * c.kvh : 0;
         int64_t pre = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -191,14 +231,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         at -= __shfl_sync(0xffffffffu, pre, 31);
       }
-      const int64_t per = found ? units[b - b_begin] : 1;
-      const int h = int(at / per);
+      const int64_t per = !found ? 1 : by_tile ? counts[b - b_begin] : units[b - b_begin];
+      const int h = int(quotient(at, per));
       at -= h * per;
-      const Seq s = found ? seq_of(c, b) : Seq{0, 0, 0};
+      const Seq s = found ? seqs[b - b_begin] : Seq{0, 0, 0};
       const int tiles = tiles_of(s, c.group);
       int t = 0;
-      found = false;
-      for (; t < tiles; t += 32) {
+      if (by_tile) {
+        t = int(at);
+        at = 0;
+        found = t < tiles;
+        if (found) left = kLead + steps_of(s, c.group, t);
+      }
+      for (; !by_tile && t < tiles; t += 32) {
         const int64_t mine = t + lane < tiles ? kLead + steps_of(s, c.group, t + lane) : 0;
         int64_t pre = mine;
 #pragma unroll
@@ -216,12 +261,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         at -= __shfl_sync(0xffffffffu, pre, 31);
       }
-      if (!found) left = 0;  // the lengths changed under the call: no work rather than wrong places
+      if (!found) left = 0;
       if (lane == 0) {
         S.start[0] = b;
         S.start[1] = h;
         S.start[2] = t;
         S.start[3] = int(at);
+        S.first = s;
       }
     }
     if (lane == 0) {
@@ -250,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Seq s = {0, 0, 0};
         int tiles = 0;
         if (left > 0) {
-          s = seq_of(c, b);
+          s = S.first;
           tiles = tiles_of(s, c.group);
         }
         for (uint32_t i = 0;;) {
@@ -275,17 +321,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.rows = s.m * c.group;
             p.u0 = u0;
             p.u1 = u1;
-            p.whole = u0 == 0 && u1 == steps;
-            p.slot = 2 * int(blockIdx.x) + (i == 0 ? 0 : 1);
-            if (u0 == 0 && !p.whole) {
+            const bool whole = u0 == 0 && u1 == steps;
+            const int slot = 2 * int(blockIdx.x) + (i == 0 ? 0 : 1);
+            p.whole = whole;
+            p.slot = slot;
+            mbar_arrive(&S.piece_full[k]);
+            if (u0 == 0 && !whole) {
               // this CTA begins the tile; the CTAs of the units up to the tile's last go on with it
               cut.row = int64_t(s.row0) * qh + h * c.group;
-              cut.slot = p.slot;
-              cut.r0 = p.r0;
-              cut.rows = min(kRows, p.rows - p.r0);
-              cut.pieces = int((end - left - at + kLead + steps - 1) / run) - int(blockIdx.x) + 1;
+              cut.slot = slot;
+              cut.r0 = t * kRows;
+              cut.rows = min(kRows, s.m * c.group - t * kRows);
+              cut.pieces = int(quotient(end - left - at + kLead + steps - 1, run)) - int(blockIdx.x) + 1;
             }
-            mbar_arrive(&S.piece_full[k]);
             ++i;
           }
           left -= to - at;
@@ -490,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tp = kOwnP ? tmem + (uint32_t(quarter * 32) << 16) + uint32_t(384 + half * 64) : ts;
     const float scale = kLog2e * rsqrtf(float(D));
     uint32_t ph_s = 0, ph_o = 0;  // phases of s_full, and of o_full's next completion
+    uint32_t ph_t = half == 0;    // of turn; the first turn is half 0's
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
       ok = __all_sync(0xffffffffu, mbar_wait(&S.piece_full[i & 1], (i >> 1) & 1, abort));
@@ -501,16 +550,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t head = int64_t(pc.row0) * qh + pc.h * c.group;  // row of token 0's first head
         const int r = r0 + quarter * 32 + lane;
         const int64_t row = head + int64_t(r / c.group) * qh + r % c.group;
-        // this thread's row of Q into its swizzled place (16-byte chunk i of row k at i ^ (k % 8))
+        // the warp's rows of Q into their swizzled places (16-byte chunk i of row k at i ^ (k % 8)),
+        // 512 contiguous bytes a load
         {
-          const int k = quarter * 32 + lane;
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D);
-          uint4 v[D / 8];
+          constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;
+          const int i = lane % kChunks, own = lane / kChunks;
+          uint4 v[kChunks];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) v[i] = r < rows ? src[i] : make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < kChunks; ++j) {
+            const int k = j * kAtOnce + own;
+            const int64_t from = __shfl_sync(0xffffffffu, row, k);
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (r - lane + k < rows)
+              v[j] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + from * D)[i];
+          }
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<uint4*>(&S.q[half][i >> 3][k * 64 + (((i & 7) ^ (k & 7)) << 3)]) = v[i];
+          for (int j = 0; j < kChunks; ++j) {
+            const int k = quarter * 32 + j * kAtOnce + own;
+            *reinterpret_cast<uint4*>(&S.q[half][i >> 3][k * 64 + (((i & 7) ^ (k & 7)) << 3)]) = v[j];
+          }
           fence_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.q_full[half]);
@@ -522,10 +580,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY;  // the row's reference, in log2
         uint64_t l0 = 0, l1 = 0;
         const int steps = pc.u1 - pc.u0;
+        const bool turns = !kOwnP && rows - pc.r0 > 128;  // both halves have rows
         for (int j = 0; j < steps; ++j) {
           ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[half], ph_s, abort));
           ph_s ^= 1;
           if (!ok) break;
+          if (turns) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.turn[half], ph_t, abort));
+            ph_t ^= 1;
+            if (!ok) break;
+          }
           fence_after();
           uint32_t x0[32], x1[32], x2[32], x3[32];
           tmem_ld32(ts, x0);
@@ -614,6 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           hand(0);
           weigh(x2, 0);
+          if (turns) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.turn[half ^ 1]);
+          }
           weigh(x3, 16);
           hand(1);
           ph_o ^= 1;  // past this step's second product
@@ -630,11 +698,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!whole) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m, sum);
           else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
         }
+        uint32_t all[D / 32][32];
+#pragma unroll
+        for (int g = 0; g < D / 32; ++g) tmem_ld32(to + g * 32, all[g]);
+        tmem_wait_ld(all[0]);
+#pragma unroll
+        for (int g = 1; g < D / 32; ++g) tmem_tie(all[g]);
 #pragma unroll
         for (int g = 0; g < D / 32; ++g) {
-          uint32_t o[32];
-          tmem_ld32(to + g * 32, o);
-          tmem_wait_ld(o);
+          uint32_t (&o)[32] = all[g];
           if (!whole) {
             if (real && sum > 0.f) {
               float4* dst = reinterpret_cast<float4*>(a.part) +
@@ -669,7 +741,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
-          __syncwarp();
         }
       }
       __syncwarp();
