@@ -127,6 +127,11 @@ __host__ __device__ __forceinline__ Seq seq_of(const CacheArgs& c, int b) {
   return s;
 }
 
+// Of numbers that are not negative; nearly always of 32 bits, where it costs a fraction.
+__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return uint64_t(a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
+
 // Sequence that packed row r belongs to, or -1: the last b with cu_q[b] <= r, if r is
 // one of its rows. A table that decreases somewhere gives some sequence or none, never
 // an index outside it.

@@ -54,11 +54,6 @@ struct Piece {
   int whole, slot;          // all of its tile's units; else where its partial result goes
 };
 
-// Of numbers that are not negative; nearly always of 32 bits, where it costs a fraction.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return uint64_t(a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
-}
-
 template <int D>
 struct Smem {
   static constexpr int kSub = D / 64;

@@ -89,6 +89,22 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(saddr(bar))
       : "memory");
 }
+// A float and an arrival to the same places of another CTA of the cluster, and the wait there.
+__device__ __forceinline__ void put_remote(float* p, int rank, float v) {
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.f32 [a], %2;\n}" ::"r"(saddr(p)),
+               "r"(rank), "f"(v)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, int rank) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(saddr(bar)),
+      "r"(rank)
+      : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // K-major operand in 128B-swizzled rows of 64 bf16 (the TMA SWIZZLE_128B layout):
 // 8-row atoms 1024 B apart (SBO), leading offset unused, descriptor version 1.
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {

@@ -14,12 +14,19 @@
 // memory). Beside it there is room for four accumulators of 96 columns, two for each half,
 // each with a warpgroup that reads it, so that products and exponentials of both halves run
 // at once. A step of 96 rows costs an SM 864 clocks of products and 768 of exponentials.
+// A CTA stays for several blocks of keys and loads the next ones while it works. The CTAs go
+// in clusters of two that share the last block of an odd number, half of the rows each: whole
+// blocks for each CTA alone leave most SMs without work in the last round (512 blocks for 152
+// SMs, 1000 tokens over 16384 slots: 117 us so, 107 us now; over 2048 slots 33 and 25 us; where
+// a CTA has one block at most either way, the search for it costs: 300 over 4096, 19 and 21 us).
+// Q loaded once for both by multicast was slower, 35 us a round of 152 blocks against 28.
 //
 // Few rows: k_weights_step, one pass over K from global memory straight into the fragments
 // of warp-level products, bound by that read.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "mp_cache.cuh"
 #include "mp_tc.cuh"
@@ -30,6 +37,16 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHalf = 128, kKeys = 256, kCols = 96;  // keys of a product and of a CTA, query rows of a step
 constexpr int kThreads = 640;  // four warpgroups of sums, a warp each of loads and z, two of products
+constexpr int kGroup = 512;    // sequences of a launch
+
+// Keys of one KV head against the blocks of query rows that see any of them.
+struct Item {
+  Seq s;
+  int b, h, n0;   // sequence, KV head, first slot
+  int halves;     // of 128 keys
+  int i0, steps;  // first block of rows, blocks; no steps: the CTA's work has ended
+  int share;      // of an item that two CTAs share: 1 gets the other's sums, 2 gives its own
+};
 
 template <int D>
 struct WSmem {
@@ -40,7 +57,14 @@ struct WSmem {
   __nv_bfloat16 z[kStages][kCols * 16];  // (hi, mid, lo, 0, ...) of the step's rows (32-byte swizzle)
   __nv_bfloat16 ones[kHalf * 16];        // rows (1, 1, 1, 0, ...) (32-byte swizzle)
   float sums[kKeys];                     // of the odd steps
-  uint64_t k_full, k_ready, q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2], drain[2];
+  uint64_t k_full, k_ready[2], k_free[2], q_full[kStages], q_empty[kStages], s_full[2][2], s_empty[2][2], drain[2];
+  uint64_t item_full[2], item_empty[2], sums_full[2], sums_empty[2];
+  Item item[2];
+  uint64_t other_full[2];
+  float other[kKeys];    // the other CTA's sums of an item that two share
+  int64_t past[kGroup];  // key blocks of a KV head, up to and with each sequence
+  Seq seqs[kGroup];
+  uint32_t loaded[3];    // phase of the last keys; the ring's next place and its phase
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -78,49 +102,55 @@ __device__ __forceinline__ Block block_at(const Blocks& b, int i, int m) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_weights_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, const WeightsArgs a,
-                 const int box) {
+                 const int box, const int b_begin, const int b_end) {
   extern __shared__ __align__(1024) unsigned char smraw[];
   const uint32_t base = saddr(smraw);
   WSmem<D>& S = *reinterpret_cast<WSmem<D>*>(smraw + ((1024 - (base & 1023)) & 1023));
   constexpr int kSub = WSmem<D>::kSub, kStages = WSmem<D>::kStages;
   const CacheArgs& c = a.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, h = blockIdx.y, n0 = blockIdx.x * kKeys;
-  const Seq s = seq_of(c, b);
-  if (n0 >= s.n || s.m == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
   volatile uint32_t* abort = &S.abort;
-  const int first = s.n - s.m, qh = c.kvh * c.group;
-  const Blocks bl = blocks_of(c.group, s.m);
-  // tokens before n0 - first see none of these keys
-  const int t_start = max(0, n0 - first);
-  const int i0 = bl.runs == 1 ? t_start / bl.per : t_start * bl.runs;
-  const int steps = bl.n - i0;
-  const int halves = s.n - n0 > kHalf ? 2 : 1;
+  const int qh = c.kvh * c.group;
+  const Blocks bl = blocks_of(c.group, 0);  // all but n, which is a sequence's own
 
   // rows of a block that no load fills stay zero, and so does all but the first three elements
   // of z and ones
+  constexpr int kZero = kThreads / 2;  // threads that do this, the others look at the lengths
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x; i < int(sizeof(S.z) / 16); i += kThreads) reinterpret_cast<uint4*>(&S.z[0][0])[i] = zero;
+  const int z0 = int(threadIdx.x) < kZero ? int(threadIdx.x) : INT_MAX / 2;
+  for (int i = z0; i < int(sizeof(S.z) / 16); i += kZero) reinterpret_cast<uint4*>(&S.z[0][0])[i] = zero;
   const int filled = bl.heads * bl.per;  // rows of a full load
-  for (int i = threadIdx.x; i < (kCols - filled) * 8 * kSub * kStages; i += kThreads)
+  for (int i = z0; i < (kCols - filled) * 8 * kSub * kStages; i += kZero)
     reinterpret_cast<uint4*>(&S.q[0][0][0])[(i / ((kCols - filled) * 8)) * (kCols * 8) + filled * 8 + i % ((kCols - filled) * 8)] = zero;
-  for (int r = threadIdx.x; r < kHalf; r += kThreads) {
+  for (int r = z0; r < kHalf; r += kZero) {
     uint4* row = reinterpret_cast<uint4*>(&S.ones[r * 16]);  // 16-byte chunk i of row r at i ^ (r / 4 % 2)
     row[(r >> 2) & 1] = make_uint4(0x3f803f80u, 0x00003f80u, 0, 0);
     row[1 - ((r >> 2) & 1)] = zero;
   }
+  for (int i = int(threadIdx.x) - kZero; i >= 0 && i < b_end - b_begin; i += kThreads - kZero) {
+    const Seq s = seq_of(c, b_begin + i);
+    S.seqs[i] = s;
+    S.past[i] = s.m == 0 ? 0 : (s.n + kKeys - 1) / kKeys;
+  }
   fence_async();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kThreads - 32) {
     mbar_init(&S.k_full, 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&S.q_full[i], 2);  // the load and z
-      mbar_init(&S.q_empty[i], halves);
+      mbar_init(&S.q_empty[i], 2);  // both halves' products
     }
-    mbar_init(&S.k_ready, 4 * halves);
-    mbar_init(&S.drain[0], 1);
-    mbar_init(&S.drain[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_ready[i], 8);
+      mbar_init(&S.drain[i], 1);
+      mbar_init(&S.k_free[i], 1);
+      mbar_init(&S.item_full[i], 1);
+      mbar_init(&S.item_empty[i], 19);  // z, two of products, 16 of sums
+      mbar_init(&S.sums_full[i], 4);
+      mbar_init(&S.sums_empty[i], 4);
+      mbar_init(&S.other_full[i], 4);
+    }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&S.s_full[i >> 1][i & 1], 1);
       mbar_init(&S.s_empty[i >> 1][i & 1], 4);
@@ -136,44 +166,116 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before();
   __syncthreads();
+  cluster_arrive();
+  bool met = false;  // waited for the other CTA's arrival
   fence_after();
   const uint32_t tmem = S.tmem_base;
   const uint32_t t_k = tmem + 4 * kCols;  // K: d / 2 columns of each half behind the accumulators
-  float sum = 0.f;
 
   if (warp == 16) {
-    // ---------------- the keys once, then blocks of query rows ----------------
-    const int live = min(kKeys, s.n - n0), boxes = (live + box - 1) / box;
-    if (lane == 0) mbar_expect_tx(&S.k_full, uint32_t(boxes) * box * 128 * kSub);
-    __syncwarp();
-    for (int i = lane; i < boxes; i += 32) {
-      const int row = slot_row(c, b, h, n0 + i * box);
+    // ---------------- the CTA's items: the keys once, then blocks of query rows ----------------
+    int64_t all = 0;
+    for (int i0 = 0; i0 < b_end - b_begin; i0 += 32) {  // sums up to each sequence, by this warp alone
+      const int64_t mine = i0 + lane < b_end - b_begin ? S.past[i0 + lane] : 0;
+      int64_t pre = mine;
 #pragma unroll
-      for (int u = 0; u < kSub; ++u)
-        tma_load_2d(&S.k[i * box / kHalf][u][i * box % kHalf * 64], &tmK, u * 64, row, &S.k_full);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += v;
+      }
+      if (i0 + lane < b_end - b_begin) S.past[i0 + lane] = all + pre;
+      all += __shfl_sync(0xffffffffu, pre, 31);
     }
+    __syncwarp();
+    const int64_t blocks = all * c.kvh;
     bool ok = true;
     int st = 0;
-    uint32_t ph = 1;
-    for (int j = 0; j < steps; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.q_empty[st], ph, abort));
+    uint32_t ph = 1, items = 0, keys = 0;
+    // The pairs of CTAs take blocks of keys in turn and their CTAs every other one of these. Where
+    // that leaves a last one over, they share it, half of the rows each: the second CTA first
+    // of all, the first at its end, so that it finds the other's sums there.
+    const int64_t pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int64_t mine = blocks > pair ? quotient(blocks - pair + pairs - 1, pairs) : 0;  // of the pair
+    const int shared = int(mine & 1);
+    const int64_t turns = (mine >> 1) + shared;
+    for (int64_t i = 0; ok; ++i) {
+      Item it;
+      it.steps = 0;
+      it.share = shared && i == (rank ? 0 : turns - 1) ? 1 + rank : 0;
+      const int64_t block = pair + pairs * (it.share ? mine - 1 : rank ? 2 * (i - shared) + 1 : 2 * i);
+      if (i < turns) {
+        // block = (blocks of the sequences before b) * kvh + h * (blocks of b) + its own
+        int lo = 0, hi = b_end - b_begin - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (S.past[mid] * c.kvh > block) hi = mid;
+          else lo = mid + 1;
+        }
+        const int64_t before = lo > 0 ? S.past[lo - 1] : 0, per = S.past[lo] - before, in = block - before * c.kvh;
+        it.b = b_begin + lo;
+        it.h = int(quotient(in, per));
+        it.s = S.seqs[lo];
+        it.n0 = int(in - it.h * per) * kKeys;
+        const Blocks own = blocks_of(c.group, it.s.m);
+        // tokens before n0 - (n - m) see none of these keys
+        const int t_start = max(0, it.n0 - (it.s.n - it.s.m));
+        it.i0 = own.runs == 1 ? t_start / own.per : t_start * own.runs;
+        it.halves = it.s.n - it.n0 > kHalf ? 2 : 1;
+        it.steps = own.n - it.i0;  // at least one: n0 < n
+        if (it.share && it.steps == 1) {
+          if (rank) continue;  // nothing to share
+          it.share = 0;
+        }
+        if (it.share) {
+          const int first = (it.steps + 1) / 2;
+          if (rank) it.i0 += first;
+          it.steps = rank ? it.steps - first : first;
+        }
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.item_empty[items & 1], ((items >> 1) & 1) ^ 1, abort));
       if (!ok) break;
       if (lane == 0) {
-        const Block x = block_at(bl, i0 + j, s.m);
-        mbar_expect_tx(&S.q_full[st], uint32_t(bl.heads) * bl.per * 128 * kSub);
-#pragma unroll
-        for (int u = 0; u < kSub; ++u)
-          tma_load_3d(&S.q[st][u][0], &tmQ, u * 64, h * c.group + x.h0, s.row0 + x.t0, &S.q_full[st]);
+        S.item[items & 1] = it;
+        mbar_arrive(&S.item_full[items & 1]);
       }
       __syncwarp();
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1;
+      ++items;
+      if (it.steps == 0) break;
+      // the last item's keys have gone to tensor memory
+      if (items > 1) ok = __all_sync(0xffffffffu, mbar_wait(&S.k_ready[items & 1], ((items - 2) >> 1) & 1, abort));
+      if (!ok) break;
+      const int live = max(0, min(kKeys, it.s.n - it.n0)), boxes = (live + box - 1) / box;
+      if (lane == 0) mbar_expect_tx(&S.k_full, uint32_t(boxes) * box * 128 * kSub);
+      __syncwarp();
+      for (int i = lane; i < boxes; i += 32) {
+        const int row = slot_row(c, it.b, it.h, it.n0 + i * box);
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+          tma_load_2d(&S.k[i * box / kHalf][u][i * box % kHalf * 64], &tmK, u * 64, row, &S.k_full);
+      }
+      __syncwarp();
+      ++keys;
+      for (int j = 0; j < it.steps; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.q_empty[st], ph, abort));
+        if (!ok) break;
+        if (lane == 0) {
+          const Block x = block_at(bl, it.i0 + j, it.s.m);
+          mbar_expect_tx(&S.q_full[st], uint32_t(bl.heads) * bl.per * 128 * kSub);
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+            tma_load_3d(&S.q[st][u][0], &tmQ, u * 64, it.h * c.group + x.h0, it.s.row0 + x.t0, &S.q_full[st]);
+        }
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
       }
     }
-    if (!ok && lane == 0) {
-      mbar_drain(&S.k_full, 0);
-      for (int i = 0; i < kStages; ++i) mbar_drain(&S.q_full[i], i < st ? ph ^ 1 : ph);
+    if (lane == 0) {
+      S.loaded[0] = (keys & 1) ^ 1;
+      S.loaded[1] = st;
+      S.loaded[2] = ph;
     }
   } else if (warp == 18) {
     // ---------------- -z of the rows, the next step's loads in flight ----------------
@@ -186,46 +288,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       head[u] = col - tok[u] * bl.group;
     }
     const float root = sqrtf(float(D));
-    auto load_z = [&](int j, float (&z)[kPer]) {
-      const Block x = block_at(bl, i0 + min(j, steps - 1), s.m);
-#pragma unroll
-      for (int u = 0; u < kPer; ++u)
-        z[u] = u * 32 + lane < x.cols ? a.lse[int64_t(s.row0 + x.t0 + tok[u]) * qh + h * c.group + x.h0 + head[u]]
-                                      : INFINITY;  // columns without a row: 2^-inf
-    };
     bool ok = true;
     int st = 0;
     uint32_t ph = 1;
-    float z0[kPer], z1[kPer];
-    auto put = [&](const float (&z)[kPer]) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.q_empty[st], ph, abort));
-      if (!ok) return;
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int r = u * 32 + lane;
-        const float v = -z[u] * root;
-        const __nv_bfloat16 hi = __float2bfloat16(v);
-        const float rest = isinf(v) ? 0.f : v - __bfloat162float(hi);
-        const __nv_bfloat16 mid = __float2bfloat16(rest);
-        const float low = rest - __bfloat162float(mid);
-        *reinterpret_cast<uint2*>(&S.z[st][r * 16 + ((r >> 2) & 1) * 8]) =
-            make_uint2(uint32_t(__bfloat16_as_ushort(hi)) | uint32_t(__bfloat16_as_ushort(mid)) << 16, bf2(low, 0.f));
-      }
-      fence_async();
+    for (uint32_t n = 0; ok; ++n) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.item_full[n & 1], (n >> 1) & 1, abort));
+      if (!ok) break;
+      const Item it = S.item[n & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.q_full[st]);
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1;
+      if (lane == 0) mbar_arrive(&S.item_empty[n & 1]);
+      if (it.steps == 0) break;
+      auto load_z = [&](int j, float (&z)[kPer]) {
+        const Block x = block_at(bl, it.i0 + min(j, it.steps - 1), it.s.m);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u)
+          z[u] = u * 32 + lane < x.cols ? a.lse[int64_t(it.s.row0 + x.t0 + tok[u]) * qh + it.h * c.group + x.h0 + head[u]]
+                                        : INFINITY;  // columns without a row: 2^-inf
+      };
+      float z0[kPer], z1[kPer];
+      auto put = [&](const float (&z)[kPer]) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.q_empty[st], ph, abort));
+        if (!ok) return;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          const int r = u * 32 + lane;
+          const float v = -z[u] * root;
+          const __nv_bfloat16 hi = __float2bfloat16(v);
+          const float rest = isinf(v) ? 0.f : v - __bfloat162float(hi);
+          const __nv_bfloat16 mid = __float2bfloat16(rest);
+          const float low = rest - __bfloat162float(mid);
+          *reinterpret_cast<uint2*>(&S.z[st][r * 16 + ((r >> 2) & 1) * 8]) =
+              make_uint2(uint32_t(__bfloat16_as_ushort(hi)) | uint32_t(__bfloat16_as_ushort(mid)) << 16, bf2(low, 0.f));
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.q_full[st]);
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      };
+      load_z(0, z0);
+      for (int j = 0; j < it.steps && ok; j += 2) {
+        load_z(j + 1, z1);
+        put(z0);
+        if (j + 1 >= it.steps || !ok) break;
+        load_z(j + 2, z0);
+        put(z1);
       }
-    };
-    load_z(0, z0);
-    for (int j = 0; j < steps && ok; j += 2) {
-      load_z(j + 1, z1);
-      put(z0);
-      if (j + 1 >= steps || !ok) break;
-      load_z(j + 2, z0);
-      put(z1);
     }
   } else if (warp >= 16) {
     // ---------------- products S[key][row]: warp 17 for the first half of the keys, 19 for the
@@ -235,31 +345,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq = sw128_desc(saddr(&S.q[0][0][0]));
     const uint64_t d1 = sw32_desc(saddr(&S.ones[0])), dz = sw32_desc(saddr(&S.z[0][0]));
     constexpr uint32_t kTile = kCols * D * 2 / 16, kSlabQ = kCols * 128 / 16, kTileZ = kCols * 32 / 16;
-    bool ok = half < halves && mbar_wait_warp(&S.k_ready, 0, abort);
+    bool ok = true;
     int st = 0;
-    uint32_t ph = 0;
-    for (int j = 0; j < steps && ok; ++j) {
-      ok = mbar_wait_warp(&S.q_full[st], ph, abort) &&
-           mbar_wait_warp(&S.s_empty[half][j & 1], ((j >> 1) & 1) ^ 1, abort);
+    uint32_t ph = 0, g = 0;  // g: this half's steps so far
+    for (uint32_t n = 0; ok; ++n) {
+      ok = mbar_wait_warp(&S.item_full[n & 1], (n >> 1) & 1, abort);
       if (!ok) break;
-      fence_after();
-      if (elect_one()) {
-        const uint32_t ts = tmem + uint32_t((half * 2 + (j & 1)) * kCols);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_ta(ts, t_k + uint32_t(half * (D / 2) + kk * 8), dq + st * kTile + (kk >> 2) * kSlabQ + (kk & 3) * 2, idesc,
-                      kk > 0 ? 1u : 0u);
-        mma_bf16(ts, d1, dz + st * kTileZ, idesc, 1u);
-        mma_commit(&S.s_full[half][j & 1]);
-        mma_commit(&S.q_empty[st]);
-      }
+      const int steps = __reduce_max_sync(0xffffffffu, S.item[n & 1].steps);
+      const bool active = __reduce_max_sync(0xffffffffu, S.item[n & 1].halves) > half;
+      if (steps == 0) break;
+      ok = mbar_wait_warp(&S.k_ready[n & 1], (n >> 1) & 1, abort);
+      if (elect_one()) mbar_arrive(&S.item_empty[n & 1]);  // after the wait: k_ready's next phase is of item n + 2
       __syncwarp();
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1;
+      for (int j = 0; j < steps && ok; ++j) {
+        ok = mbar_wait_warp(&S.q_full[st], ph, abort);
+        if (!active) {  // the block of rows passes this half by
+          if (ok && elect_one()) mbar_arrive(&S.q_empty[st]);
+        } else {
+          ok = ok && mbar_wait_warp(&S.s_empty[half][g & 1], ((g >> 1) & 1) ^ 1, abort);
+          if (!ok) break;
+          fence_after();
+          if (elect_one()) {
+            const uint32_t ts = tmem + uint32_t((half * 2 + (g & 1)) * kCols);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ta(ts, t_k + uint32_t(half * (D / 2) + kk * 8), dq + st * kTile + (kk >> 2) * kSlabQ + (kk & 3) * 2,
+                          idesc, kk > 0 ? 1u : 0u);
+            mma_bf16(ts, d1, dz + st * kTileZ, idesc, 1u);
+            mma_commit(&S.s_full[half][g & 1]);
+            mma_commit(&S.q_empty[st]);
+            if (j == steps - 1) mma_commit(&S.k_free[half]);
+          }
+          ++g;
+        }
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
       }
+      if (ok && !active && elect_one()) mbar_arrive(&S.k_free[half]);
+      __syncwarp();
     }
-    if (!ok && half < halves) {
+    if (!ok) {
       if (elect_one()) mma_commit(&S.drain[half]);
       __syncwarp();
       if (lane == 0) mbar_drain(&S.drain[half], 0);
@@ -267,91 +395,152 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- one thread per key and every other step ----------------
-    const int half = warp >> 3, odd = (warp >> 2) & 1, key = (warp & 3) * 32 + lane, slot = n0 + half * kHalf + key;
+    const int half = warp >> 3, odd = (warp >> 2) & 1, key = (warp & 3) * 32 + lane;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const float scale = kLog2e * rsqrtf(float(D));
     const uint64_t sc2 = pk2(scale, scale);
-    if (odd == 0 && half < halves && __all_sync(0xffffffffu, mbar_wait(&S.k_full, 0, abort))) {
-      // this thread's key into tensor memory (16-byte chunk i of row k lies at i ^ (k % 8))
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(&S.k[half][u][key * 64 + ((i ^ (key & 7)) << 3)]);
-          w[4 * i] = v.x;
-          w[4 * i + 1] = v.y;
-          w[4 * i + 2] = v.z;
-          w[4 * i + 3] = v.w;
-        }
-        tmem_st32(t_k + lanes + uint32_t(half * (D / 2) + u * 32), w);
-      }
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.k_ready);
-    }
     const uint32_t ts = tmem + lanes + uint32_t((half * 2 + odd) * kCols);
-    for (int j = odd; half < halves && j < steps; j += 2) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&S.s_full[half][odd], (j >> 1) & 1, abort))) break;
-      fence_after();
-      const Block x = block_at(bl, i0 + j, s.m);
-      // columns [low, x.cols) see this thread's key
-      const int dt = min(slot - first - x.t0, bl.per);
-      const int low = dt <= 0 ? 0 : (bl.runs == 1 ? dt * bl.group : kCols);
-      const bool last = bl.runs == 1 ? x.cols < bl.per * bl.group : x.cols < bl.heads;
-      const bool plain = !__any_sync(0xffffffffu, low > 0) && !last;
-      uint64_t l0 = 0, l1 = 0;  // a step's own sums: two levels keep long chunks' sums exact
-      auto weigh = [&](const uint32_t (&v)[32], int col) {
-        if (plain) {
+    uint32_t g = 0, joined = 0;  // this half's steps and items so far
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.item_full[n & 1], (n >> 1) & 1, abort));
+      if (!ok) break;
+      const Item& it = S.item[n & 1];
+      const int steps = it.steps;
+      if (steps == 0) break;
+      const bool active = half < it.halves;
+      const int slot = it.n0 + half * kHalf + key, m = it.s.m, i0 = it.i0, first = it.s.n - m;
+      const bool mine = active && slot < it.s.n;
+      const int share = it.share;
+      float* const score = a.scores + (int64_t(it.b) * c.kvh + it.h) * (int64_t(c.cols) * c.page_size) + slot;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.item_empty[n & 1]);
+      const float old = mine && odd == 0 && share != 2 ? *score : 0.f;
+      if (odd == 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.k_full, n & 1, abort) && mbar_wait(&S.k_free[half], (n & 1) ^ 1, abort));
+        if (!ok) break;
+        if (active) {
+          fence_after();
+          // this thread's key into tensor memory (16-byte chunk i of row k lies at i ^ (k % 8))
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const uint64_t y0 = mul2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2);
-            const uint64_t y1 = mul2(pk2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2);
-            l0 = add2(l0, pk2(ex2(lo2(y0)), ex2(hi2(y0))));
-            l1 = add2(l1, pk2(ex2(lo2(y1)), ex2(hi2(y1))));
+          for (int u = 0; u < kSub; ++u) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(&S.k[half][u][key * 64 + ((i ^ (key & 7)) << 3)]);
+              w[4 * i] = v.x;
+              w[4 * i + 1] = v.y;
+              w[4 * i + 2] = v.z;
+              w[4 * i + 3] = v.w;
+            }
+            tmem_st32(t_k + lanes + uint32_t(half * (D / 2) + u * 32), w);
+          }
+          tmem_wait_st();
+          fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.k_ready[n & 1]);
+      }
+      if (!active) continue;
+      float sum = 0.f;
+      for (int j = (g ^ odd) & 1; j < steps; j += 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[half][odd], ((g + j) >> 1) & 1, abort));
+        if (!ok) break;
+        fence_after();
+        const Block x = block_at(bl, i0 + j, m);
+        // columns [low, x.cols) see this thread's key
+        const int dt = min(slot - first - x.t0, bl.per);
+        const int low = dt <= 0 ? 0 : (bl.runs == 1 ? dt * bl.group : kCols);
+        const bool last = bl.runs == 1 ? x.cols < bl.per * bl.group : x.cols < bl.heads;
+        const bool plain = !__any_sync(0xffffffffu, low > 0) && !last;
+        uint64_t l0 = 0, l1 = 0;  // a step's own sums: two levels keep long chunks' sums exact
+        auto weigh = [&](const uint32_t (&v)[32], int col) {
+          if (plain) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const uint64_t y0 = mul2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2);
+              const uint64_t y1 = mul2(pk2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2);
+              l0 = add2(l0, pk2(ex2(lo2(y0)), ex2(hi2(y0))));
+              l1 = add2(l1, pk2(ex2(lo2(y1)), ex2(hi2(y1))));
+            }
+          } else {
+            // rows outside the sequence may hold anything: selected away, not multiplied
+            float l = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float e = ex2(__uint_as_float(v[i]) * scale);
+              l += col + i >= low && col + i < x.cols ? e : 0.f;
+            }
+            l0 = add2(l0, pk2(l, 0.f));
+          }
+        };
+        uint32_t v0[32], v1[32];
+        tmem_ld32(ts, v0);
+        tmem_wait_ld(v0);
+        tmem_ld32(ts + 32, v1);
+        weigh(v0, 0);
+        tmem_wait_ld(v1);
+        tmem_ld32(ts + 64, v0);
+        weigh(v1, 32);
+        tmem_wait_ld(v0);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.s_empty[half][odd]);
+        weigh(v0, 64);
+        sum += (lo2(l0) + hi2(l0)) + (lo2(l1) + hi2(l1));
+      }
+      if (!ok) break;
+      g += uint32_t(steps);
+      // the odd steps' sums join the even ones'
+      if (odd == 1) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.sums_empty[half], (joined & 1) ^ 1, abort));
+        if (!ok) break;
+        S.sums[half * kHalf + key] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.sums_full[half]);
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.sums_full[half], joined & 1, abort));
+        if (!ok) break;
+        sum += S.sums[half * kHalf + key];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.sums_empty[half]);
+        if (share == 2) {
+          if (!met) cluster_wait();
+          met = true;
+          put_remote(&S.other[half * kHalf + key], 0, sum);
+          __syncwarp();
+          if (lane == 0) {
+            fence_cluster();
+            mbar_arrive_remote(&S.other_full[half], 0);
           }
         } else {
-          // rows outside the sequence may hold anything: selected away, not multiplied
-          float l = 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float e = ex2(__uint_as_float(v[i]) * scale);
-            l += col + i >= low && col + i < x.cols ? e : 0.f;
+          if (share == 1) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.other_full[half], 0, abort));
+            if (!ok) break;
+            fence_cluster();
+            sum += S.other[half * kHalf + key];
           }
-          l0 = add2(l0, pk2(l, 0.f));
+          if (mine) *score = old + sum;
         }
-      };
-      uint32_t v0[32], v1[32];
-      tmem_ld32(ts, v0);
-      tmem_wait_ld(v0);
-      tmem_ld32(ts + 32, v1);
-      weigh(v0, 0);
-      tmem_wait_ld(v1);
-      tmem_ld32(ts + 64, v0);
-      weigh(v1, 32);
-      tmem_wait_ld(v0);
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.s_empty[half][odd]);
-      weigh(v0, 64);
-      sum += (lo2(l0) + hi2(l0)) + (lo2(l1) + hi2(l1));
+      }
+      ++joined;
     }
-    if (odd == 1) S.sums[slot - n0] = sum;
   }
   fence_before();
   __syncthreads();
-  if (warp < 16 && !(warp & 4)) {
-    const int key = (warp >> 3) * kHalf + (warp & 3) * 32 + lane;
-    if (n0 + key < s.n && !S.abort)
-      a.scores[(int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size) + n0 + key] += sum + S.sums[key];
+  if (threadIdx.x == 0 && S.abort) {
+    mbar_drain(&S.k_full, S.loaded[0]);
+    for (int i = 0; i < kStages; ++i) mbar_drain(&S.q_full[i], i < int(S.loaded[1]) ? S.loaded[2] ^ 1 : S.loaded[2]);
+    flag(c.status, MP_STATUS_WAIT_TIMEOUT);
   }
   if (warp == 17) {
     __syncwarp();
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
-  if (threadIdx.x == 0 && S.abort) flag(c.status, MP_STATUS_WAIT_TIMEOUT);
+  if (!met) cluster_wait();
+  cluster_arrive();
+  cluster_wait();  // the other CTA's sums come here
 }
 
 // ---- few query rows ----
@@ -476,8 +665,16 @@ cudaError_t launch(const WeightsArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(WSmem<D>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k_weights_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  k_weights_tc<D><<<dim3((c.max_kv + kKeys - 1) / kKeys, c.kvh, c.batch), kThreads, smem, st>>>(mk, mq, a, box);
-  return cudaGetLastError();
+  // A pair of CTAs per pair of SMs, or fewer when the limits leave fewer blocks than pairs.
+  for (int b = 0; b < c.batch; b += kGroup) {
+    const int n = std::min(kGroup, c.batch - b);
+    const int64_t most = int64_t(n) * c.kvh * ((int64_t(c.max_kv) + kKeys - 1) / kKeys);
+    const int ctas = 2 * int(std::min<int64_t>(device_sm_count() / 2, most));
+    if (ctas == 0) continue;
+    k_weights_tc<D><<<ctas, kThreads, smem, st>>>(mk, mq, a, box, b, b + n);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
