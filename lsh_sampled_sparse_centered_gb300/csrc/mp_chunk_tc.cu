@@ -54,6 +54,8 @@ struct Piece {
   int whole, slot;          // all of its tile's units; else where its partial result goes
 };
 
+static_assert(kKeys / 16 <= 8, "boxes of 16 rows at least");
+
 template <int D>
 struct Smem {
   static constexpr int kSub = D / 64;
@@ -361,7 +363,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.piece_empty[i & 1]);
         if (pc.u0 == pc.u1) break;
+        // Where the boxes of a tile lie (eight at most), for four steps at a time and one such round
+        // ahead: a page looked up when its box is due cost every tile that wait (a ragged batch over
+        // pages of 16: 2 us a step).
+        auto look = [&](int u) {
+          const int n = u * kKeys + (lane >> 3) * kKeys + (lane & 7) * box;
+          const bool any = u + (lane >> 3) < pc.u1 && (lane & 7) * box < kKeys && n < pc.n;
+          return any ? slot_row(c, pc.b, pc.h, n) : 0;
+        };
+        int rows = 0, ahead = look(pc.u0);
         for (int u = pc.u0; u < pc.u1 && ok; ++u) {
+          if (((u - pc.u0) & 3) == 0) {
+            rows = ahead;
+            ahead = look(u + 4);
+          }
+          const int row = __shfl_sync(0xffffffffu, rows, ((u - pc.u0) & 3) * 8 + (lane & 7));
           const int n0 = u * kKeys;
           const int live = max(0, min(kKeys, pc.n - n0));  // rows that hold slots of the sequence
           const int boxes = (live + box - 1) / box;
@@ -377,11 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               S.filled[st] = uint8_t(ph);
             }
             __syncwarp();
-            for (int j = lane; j < boxes; j += 32) {
-              const int row = slot_row(c, pc.b, pc.h, n0 + j * box);
+            if (lane < boxes) {
 #pragma unroll
               for (int s = 0; s < kSub; ++s)
-                tma_load_2d(&S.kv[st][s][j * box * 64], kv ? &tmV : &tmK, s * 64, row, bar);
+                tma_load_2d(&S.kv[st][s][lane * box * 64], kv ? &tmV : &tmK, s * 64, row, bar);
             }
             if (patch) {
               ok = __all_sync(0xffffffffu, mbar_wait(&S.tail, tails & 1, abort));
