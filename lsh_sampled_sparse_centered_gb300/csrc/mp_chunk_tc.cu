@@ -785,30 +785,48 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
   auto slot = [&](int p) { return int64_t(p == 0 ? cut.slot : 2 * (int(blockIdx.x) + p)); };
   const float2* ml = reinterpret_cast<const float2*>(a.ml) + i;
   const float4* part = reinterpret_cast<const float4*>(a.part) + int64_t(columns) * 4 * slot_rows + i;
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int p = 0; p < cut.pieces; ++p) m = fmaxf(m, ml[slot(p) * slot_rows].x);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
+  float m = -INFINITY, l = 0.f;
   float4 o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int p = 0; p < cut.pieces; ++p) {
-    const float2 v = ml[slot(p) * slot_rows];
-    const bool live = v.y != 0.f;  // a piece that saw nothing has written no sum
-    const float by = live ? exp2f(v.x - ref) : 0.f;
-    l = fmaf(v.y, by, l);
-    float4 x[4];
+  constexpr int kAtOnce = 4;  // pieces whose loads are in flight together
+  for (int p0 = 0; p0 < cut.pieces; p0 += kAtOnce) {
+    float2 v[kAtOnce];
+    float4 x[kAtOnce][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      x[j] = live ? part[(slot(p) * (D / 4) + j) * slot_rows] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int64_t at = slot(min(p0 + k, cut.pieces - 1));
+      v[k] = ml[at * slot_rows];
+      if (p0 + k >= cut.pieces) v[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[k][j] = part[(at * (D / 4) + j) * slot_rows];
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, v[k].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float before = exp2f(m - ref);  // 0 while nothing was seen
+    m = top;
+    l *= before;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      o[j].x = fmaf(x[j].x, by, o[j].x);
-      o[j].y = fmaf(x[j].y, by, o[j].y);
-      o[j].z = fmaf(x[j].z, by, o[j].z);
-      o[j].w = fmaf(x[j].w, by, o[j].w);
+      o[j].x *= before;
+      o[j].y *= before;
+      o[j].z *= before;
+      o[j].w *= before;
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const bool live = v[k].y != 0.f;  // a piece that saw nothing has written no sum
+      const float by = live ? exp2f(v[k].x - ref) : 0.f;
+      l = fmaf(v[k].y, by, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[j].x = live ? fmaf(x[k][j].x, by, o[j].x) : o[j].x;
+        o[j].y = live ? fmaf(x[k][j].y, by, o[j].y) : o[j].y;
+        o[j].z = live ? fmaf(x[k][j].z, by, o[j].z) : o[j].z;
+        o[j].w = live ? fmaf(x[k][j].w, by, o[j].w) : o[j].w;
+      }
     }
   }
   const int group = a.c.group, r = cut.r0 + i;
