@@ -772,34 +772,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces' (m, l, sum) of the tiles that were cut, in their order: a warp takes 32
-// rows, a lane each, and 16 columns. Partial sums lie [slot][column / 4][row][4], so that
+// rows, a lane each, and 8 columns. Partial sums lie [slot][column / 4][row][4], so that
 // the threads that own rows (in the kernel above and here) write and read whole lines. Set up
 // while k_chunk_tc still runs; it waits for it first.
 template <int D>
 __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const int slot_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
-  const int task = blockIdx.y * 8 + (threadIdx.x >> 5), columns = task % (D / 16);
-  const int i = task / (D / 16) * 32 + (threadIdx.x & 31);
+  const int task = blockIdx.y * 8 + (threadIdx.x >> 5), columns = task % (D / 8);
+  const int i = task / (D / 8) * 32 + (threadIdx.x & 31);
   if (i >= cut.rows || cut.pieces == 0) return;
   auto slot = [&](int p) { return int64_t(p == 0 ? cut.slot : 2 * (int(blockIdx.x) + p)); };
   const float2* ml = reinterpret_cast<const float2*>(a.ml) + i;
-  const float4* part = reinterpret_cast<const float4*>(a.part) + int64_t(columns) * 4 * slot_rows + i;
+  const float4* part = reinterpret_cast<const float4*>(a.part) + int64_t(columns) * 2 * slot_rows + i;
   float m = -INFINITY, l = 0.f;
-  float4 o[4];
+  float4 o[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < 2; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kAtOnce = 4;  // pieces whose loads are in flight together
   for (int p0 = 0; p0 < cut.pieces; p0 += kAtOnce) {
     float2 v[kAtOnce];
-    float4 x[kAtOnce][4];
+    float4 x[kAtOnce][2];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int64_t at = slot(min(p0 + k, cut.pieces - 1));
-      v[k] = ml[at * slot_rows];
-      if (p0 + k >= cut.pieces) v[k] = make_float2(-INFINITY, 0.f);
+      v[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[k][j] = part[(at * (D / 4) + j) * slot_rows];
+      for (int j = 0; j < 2; ++j) x[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p0 + k >= cut.pieces) continue;
+      const int64_t at = slot(p0 + k);
+      v[k] = ml[at * slot_rows];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) x[k][j] = part[(at * (D / 4) + j) * slot_rows];
     }
     float top = m;
 #pragma unroll
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
     m = top;
     l *= before;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       o[j].x *= before;
       o[j].y *= before;
       o[j].z *= before;
@@ -821,7 +824,7 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
       const float by = live ? exp2f(v[k].x - ref) : 0.f;
       l = fmaf(v[k].y, by, l);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         o[j].x = live ? fmaf(x[k][j].x, by, o[j].x) : o[j].x;
         o[j].y = live ? fmaf(x[k][j].y, by, o[j].y) : o[j].y;
         o[j].z = live ? fmaf(x[k][j].z, by, o[j].z) : o[j].z;
@@ -833,11 +836,9 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
   const int64_t row = cut.row + int64_t(r / group) * (a.c.kvh * group) + r % group;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   if (a.lse && columns == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + columns * 16);
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    out[j] = make_uint4(bf2(o[2 * j].x * inv, o[2 * j].y * inv), bf2(o[2 * j].z * inv, o[2 * j].w * inv),
-                        bf2(o[2 * j + 1].x * inv, o[2 * j + 1].y * inv), bf2(o[2 * j + 1].z * inv, o[2 * j + 1].w * inv));
+  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + columns * 8);
+  out[0] = make_uint4(bf2(o[0].x * inv, o[0].y * inv), bf2(o[0].z * inv, o[0].w * inv),
+                        bf2(o[1].x * inv, o[1].y * inv), bf2(o[1].z * inv, o[1].w * inv));
 }
 
 int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
@@ -865,7 +866,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
   for (int b = 0; b < c.batch; b += kGroup) {
     k_chunk_tc<D><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 16) + 7) / 8);
+    cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 8) + 7) / 8);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
