@@ -42,7 +42,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;
 constexpr int kGroup = 1024;  // sequences of a launch
-constexpr int kLead = 3;      // units that starting and ending a tile costs (5.5 us, a step 1.5 to 1.8 us)
+// Units that starting and ending a tile costs: 5.5 us, a step 1.1 us with d = 64 and 1.5 with
+// d = 128, of which some runs under the neighbouring tiles. Where there are tiles for every
+// CTA, d = 128 counts more (8192 tokens over as many slots: 429 us with 3, 404 with 4, 398 with
+// 5, 394 with 6); where tiles are cut in many pieces, less (300 over 2000: 27.3 and 29.5 us).
+constexpr int kLead = 3, kLeadWhole = 5;
 constexpr int kMinRun = 2;    // units of a CTA at least
 constexpr int kCut = 10;      // units that cutting the tiles costs: a second piece for most CTAs, and the join
 
@@ -68,9 +72,10 @@ struct Smem {
   uint64_t piece_full[2], piece_empty[2], drain[2], turn[2];
   Piece piece[2];
   int64_t left, run;
+  int lead;      // units that a tile counts besides its steps
   int start[4];  // sequence, KV head, tile, unit
   Seq first;     // that sequence
-  int longest[12];  // units of a tile, of each warp's sequences
+  int longest[12];  // steps of a tile, of each warp's sequences
   uint8_t filled[kStages];  // phase in which each tile of the ring was last filled (1: never)
   uint32_t tmem_base;
   uint32_t abort;
@@ -93,7 +98,7 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr) {
   return d;
 }
 // Work is counted in units: one 256-row tile of a KV head against 128 keys (a tile that
-// sees nothing counts one, so that its rows are written), and kLead more for starting a
+// sees nothing counts one, so that its rows are written), and `lead` more for starting a
 // tile. The units of all tiles, in the order (sequence, KV head, tile, lead, keys), are cut
 // into equal runs, one per CTA, whatever the lengths: a CTA's run covers the end of one
 // tile, whole tiles, and the start of another.
@@ -165,13 +170,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* counts = reinterpret_cast<int*>(&S.kv[1][0][0]);                  // tiles of each sequence and KV head
   Seq* seqs = reinterpret_cast<Seq*>(&S.kv[2][0][0]);
   static_assert(kGroup * sizeof(Seq) <= kKeys * 128, "one tile of the ring");
-  int longest = 0;  // units of a tile
+  int longest = 0;  // steps of a tile
   for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
     const Seq s = seq_of(c, b);
     const int tiles = tiles_of(s, c.group);
     int64_t u = 0;
     for (int t = lane; t < tiles; t += 32) {
-      const int mine = kLead + steps_of(s, c.group, t);
+      const int mine = steps_of(s, c.group, t);
       u += mine;
       longest = max(longest, mine);
     }
@@ -198,6 +203,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       all_tiles += __shfl_xor_sync(0xffffffffu, all_tiles, o);
     }
     longest = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? S.longest[lane] : 0);
+    const int lead = D == 128 && all_tiles >= gridDim.x ? kLeadWhole : kLead;
+    all += lead * all_tiles;
+    longest += lead;
+    auto units_of = [&](int b) { return units[b - b_begin] + int64_t(lead) * counts[b - b_begin]; };
     const int64_t run = max(int64_t(kMinRun), quotient(all + gridDim.x - 1, gridDim.x));
     // Equal runs cut tiles; where a CTA for each tile takes little longer, none is cut (1024
     // tokens, 32/8 heads, 128 tiles: over 2048 slots 47 against 51 us; over 8192, where the rule
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool found = false;
       for (; b < b_end; b += 32) {
         const int64_t mine =
-            b + lane < b_end ? (by_tile ? counts[b + lane - b_begin] : units[b + lane - b_begin]) * c.kvh : 0;
+            b + lane < b_end ? (by_tile ? counts[b + lane - b_begin] : units_of(b + lane)) * c.kvh : 0;
         int64_t pre = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -228,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         at -= __shfl_sync(0xffffffffu, pre, 31);
       }
-      const int64_t per = !found ? 1 : by_tile ? counts[b - b_begin] : units[b - b_begin];
+      const int64_t per = !found ? 1 : by_tile ? counts[b - b_begin] : units_of(b);
       const int h = int(quotient(at, per));
       at -= h * per;
       const Seq s = found ? seqs[b - b_begin] : Seq{0, 0, 0};
@@ -238,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         t = int(at);
         at = 0;
         found = t < tiles;
-        if (found) left = kLead + steps_of(s, c.group, t);
+        if (found) left = lead + steps_of(s, c.group, t);
       }
       for (; !by_tile && t < tiles; t += 32) {
-        const int64_t mine = t + lane < tiles ? kLead + steps_of(s, c.group, t + lane) : 0;
+        const int64_t mine = t + lane < tiles ? lead + steps_of(s, c.group, t + lane) : 0;
         int64_t pre = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -270,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       S.left = left;
       S.run = run;
+      S.lead = lead;
     }
     fence_async();
   }
@@ -288,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Cut cut;
         cut.pieces = 0;
         int64_t left = S.left;
+        const int lead = S.lead;
         const int64_t run = S.run, end = blockIdx.x * run + left;
         int b = S.start[0], h = S.start[1], t = S.start[2], at = S.start[3];  // at: units into the tile
         Seq s = {0, 0, 0};
@@ -306,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const int steps = steps_of(s, c.group, t);
-          const int to = int(min(int64_t(kLead + steps), at + left));
-          const int u0 = max(0, at - kLead), u1 = max(0, to - kLead);
+          const int to = int(min(int64_t(lead + steps), at + left));
+          const int u0 = max(0, at - lead), u1 = max(0, to - lead);
           if (u1 > u0) {  // a run that ends within the lead leaves the tile to the next
             p.b = b;
             p.h = h;
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               cut.slot = slot;
               cut.r0 = t * kRows;
               cut.rows = min(kRows, s.m * c.group - t * kRows);
-              cut.pieces = int(quotient(end - left - at + kLead + steps - 1, run)) - int(blockIdx.x) + 1;
+              cut.pieces = int(quotient(end - left - at + lead + steps - 1, run)) - int(blockIdx.x) + 1;
             }
             ++i;
           }
