@@ -288,9 +288,9 @@ MP_API int mp_decode_attention_static(const mp_config* cfg, void* tables, const 
  * sets MP_STATUS_BAD_LENGTH; a page number outside the pool sets MP_STATUS_BAD_PAGE.
  * `status` (device uint32, may be NULL) collects these bits; the caller clears it.
  * Query head j of a sequence reads KV head j / (q_heads / kv_heads); the softmax scale is
- * 1/sqrt(head_dim). Workspaces belong to the caller, hold nothing between calls and need
- * no initialisation; calls that may overlap on the device (two streams, two captured
- * graphs) need a workspace each. */
+ * 1/sqrt(head_dim). Workspaces are device memory of the caller's, aligned to 256 bytes; they
+ * hold nothing between calls and need no initialisation; calls that may overlap on the
+ * device (two streams, two captured graphs) need a workspace each. */
 typedef struct mp_cache_config {
   int32_t batch;     /* sequences */
   int32_t kv_heads;  /* KV heads per sequence */

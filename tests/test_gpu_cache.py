@@ -377,6 +377,64 @@ def test_weights_sum_to_the_number_of_queries(mp):
     assert ((total - want).abs() <= 2.0 ** -14 * want).all()
 
 
+# Enough tiles of rows and blocks of keys that a CTA has several of them, shares some with
+# others, and passes from one sequence to the next.
+WIDE = [
+    ("bf16", 40, 40, 128, 64, [1000], [1100]),
+    ("bf16", 32, 8, 128, 0, [1024], [2048]),
+    ("bf16", 64, 8, 64, 16, [300, 200, 90], [2000, 900, 3000]),
+    ("bf16", 16, 16, 128, 48, [33, 40, 65], [9000, 4000, 2500]),
+    ("bf16", 17, 1, 64, 16, [1 + b % 2 for b in range(520)], [1 + (7 * b) % 40 for b in range(520)]),
+]
+
+
+@pytest.mark.parametrize("dtype,hq,hk,d,page,q_lens,kv", WIDE)
+def test_attention_of_many_tiles(mp, dtype, hq, hk, d, page, q_lens, kv):
+    test_attention(mp, dtype, hq, hk, d, page, q_lens, kv)
+
+
+@pytest.mark.parametrize("dtype,hq,hk,d,page,q_lens,kv", WIDE)
+def test_weights_of_many_blocks(mp, dtype, hq, hk, d, page, q_lens, kv):
+    test_weights(mp, dtype, hq, hk, d, page, q_lens, kv)
+
+
+def test_weights_captured_and_on_two_streams(mp):
+    """One captured call per stream, replayed at once, that follows the lengths."""
+    c = Cache(mp, "bf16", 8, 2, 128, 64, [3000, 2500])
+    cu, cu_t = offsets([50, 20])
+    parts = []
+    for _ in range(2):
+        st = torch.cuda.Stream()
+        q = c.randn(70, 8, 128)
+        lse = R.attention(q, cu, [2000, 2500], c.keys, c.values, c.table, 2)[1].float()
+        sc = torch.zeros(2, 2, c.ps * c.cols, device=DEV)
+        call = lambda: mp.mp_cache_weights(c.cfg, q, lse, cu_t, c.kv_len, 50, 3000, c.keys, c.table, sc, c.status)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            call()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=st):
+                call()
+        parts.append((g, st, q, lse, sc))
+    torch.cuda.synchronize()
+    c.kv_len.copy_(torch.tensor([2000, 2500], dtype=torch.int32))
+    for _, _, _, _, sc in parts:
+        sc.zero_()
+    torch.cuda.synchronize()
+    for g, st, *_ in parts:
+        with torch.cuda.stream(st):
+            g.replay()
+    torch.cuda.synchronize()
+    assert c.status.item() == 0
+    for _, _, q, lse, sc in parts:
+        want, slack = R.weights(q, lse, cu, [2000, 2500], c.keys, c.table, torch.zeros_like(sc))
+        for b, n in enumerate([2000, 2500]):
+            # as in test_weights
+            rel = 136 * 2.0 ** -24 * slack[b, :, :n] + 2.0 ** -21 * (1 + lse.abs().max().double()) + 202 * 2.0 ** -24
+            assert ((sc[b, :, :n].double() - want[b, :, :n]).abs() <= rel * want[b, :, :n]).all()
+            assert not sc[b, :, n:].any()
+
+
 # ---- append ----
 
 APPEND = [
