@@ -1,8 +1,8 @@
 // The attention that a chunk's tokens paid to every cached key, bf16.
 //
 // A key's weight is the sum over query rows of 2^(x - z), x = q k log2(e) / sqrt(d) and z
-// the row's log-sum-exp in log2. Nothing but K, Q and z is read; each key's sum has one
-// owner, so the order of its additions is fixed and no atomics are needed.
+// the row's log-sum-exp in log2. Nothing but K, Q and z is read; each key's sum is written by
+// one thread, its parts joined in a fixed order without atomics.
 //
 // Long chunks: k_weights_tc, keys as the M dimension of tcgen05 products (256 keys of a
 // CTA, as two halves, against 96 query rows at a time), so that a thread owns a key and
