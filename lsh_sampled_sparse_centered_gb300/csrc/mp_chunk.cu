@@ -66,15 +66,20 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Thread (ty, tx) holds S of rows 8 ty .. + 8 and keys tx, tx + 16, ... (rows of shared memory
-// are padded by four floats, so that sixteen keys' vectors fall on all banks), and O of the
-// same rows and the columns 4 tx .. + 4 of each 64. Products run as packed pairs, over
-// pairs of d for S and of rows for O. V arrives under S and the softmax, the next K under
-// the product with V.
+// Thread (ty, tx) holds S of rows 8 ty .. + 8 and keys tx, tx + 16, ..., and O of the same rows
+// and the columns 4 tx .. + 4 of each 64. The vectors that a warp reads or writes at once fall on
+// all banks of shared memory: with d = 64 by rows padded by four floats, with d = 128, where
+// padding leaves room for one CTA on an SM instead of two (512 tokens over 8192 slots, 32/8
+// heads: 2988 against 2098 us), by keeping the 16-byte chunk i of a row at i ^ x, x = key % 8 for K,
+// row / 8 % 2 for Q, key % 16 for P, 0 for V (with d = 64 3 % slower than padding).
+// Products run as packed pairs, over pairs of d for S and of rows for O. V arrives under S and
+// the softmax, the next K under the product with V.
 template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const ChunkArgs a) {
-  constexpr int kRow = D + 4, kPt = kBM + 4;
-  extern __shared__ float sm[];
+  constexpr bool kPad = D == 64;
+  constexpr int kRow = D + kPad * 4, kPt = kBM + kPad * 4;
+  auto place = [](int at, int x) { return kPad ? at : at ^ (x * 4); };  // of a chunk's first float
+  extern __shared__ __align__(16) float sm[];
   float* qs = sm;                // [64][kRow]
   float* ks = qs + kBM * kRow;   // [64][kRow]
   float* vs = ks + kBN * kRow;   // [64][kRow]
@@ -94,12 +99,12 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
   const int k0 = min(s.n, split * per * kBN), k1 = min(min(s.n, last + 1), (split + 1) * per * kBN);
   constexpr int kVec = D / 4, kStep = kThr / kVec;  // vectors of a row, rows that the CTA copies at a time
   const int cr = threadIdx.x / kVec, ce = threadIdx.x % kVec * 4;
-  auto copy_tile = [&](float* dst, const void* base, int n0) {
+  auto copy_tile = [&](float* dst, const void* base, int n0, int swizzle) {
 #pragma unroll 4
     for (int i = cr; i < kBN; i += kStep) {
       const bool live = n0 + i < k1;
       const float* src = static_cast<const float*>(base) + (live ? slot_read(c, b, h, n0 + i) + ce : 0);
-      copy16(dst + i * kRow + ce, src, live);
+      copy16(dst + i * kRow + place(ce, i & swizzle), src, live);
     }
     copy_commit();
   };
@@ -108,11 +113,11 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
     const bool live = r < rows;
     const float* src = static_cast<const float*>(a.q);
     if (live) src += (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D + ce;
-    copy16(qs + i * kRow + ce, src, live);
+    copy16(qs + i * kRow + place(ce, (i >> 3) & 1), src, live);
   }
   if (k0 < k1) {
-    copy_tile(ks, a.keys, k0);
-    copy_tile(vs, a.values, k0);
+    copy_tile(ks, a.keys, k0, 7);
+    copy_tile(vs, a.values, k0, 0);
   }
   float m[8], l[8];
   uint64_t o[4][D / 16];  // rows 2 i and 2 i + 1 of a column
@@ -134,18 +139,19 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) x2[i][j] = 0;
-#pragma unroll 1
+#pragma unroll(D == 64 ? 1 : 2)
     for (int e = 0; e < D; e += 4) {
+      const int ek = place(e, tx & 7), eq = place(e, ty & 1);
       uint64_t kv[4][2];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(ks + (tx + 16 * j) * kRow + e);
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(ks + (tx + 16 * j) * kRow + ek);
         kv[j][0] = v.x;
         kv[j][1] = v.y;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qs + (ty * 8 + i) * kRow + e);
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qs + (ty * 8 + i) * kRow + eq);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x2[i][j] = fma2(q.y, kv[j][1], fma2(q.x, kv[j][0], x2[i][j]));
       }
@@ -180,22 +186,22 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
       for (int j = 0; j < D / 16; ++j) o[i][j] = mul2(o[i][j], pk2(by[2 * i], by[2 * i + 1]));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<float4*>(pt + (tx + 16 * j) * kPt + ty * 8) = make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
-      *reinterpret_cast<float4*>(pt + (tx + 16 * j) * kPt + ty * 8 + 4) = make_float4(x[4][j], x[5][j], x[6][j], x[7][j]);
+      *reinterpret_cast<float4*>(pt + (tx + 16 * j) * kPt + place(ty * 8, tx)) = make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
+      *reinterpret_cast<float4*>(pt + (tx + 16 * j) * kPt + place(ty * 8 + 4, tx)) = make_float4(x[4][j], x[5][j], x[6][j], x[7][j]);
     }
     __syncthreads();  // K has been read, P is written
     const bool more = n0 + kBN < k1;
     if (more) {
-      copy_tile(ks, a.keys, n0 + kBN);
+      copy_tile(ks, a.keys, n0 + kBN, 7);
       copy_wait<1>();
     } else {
       copy_wait<0>();
     }
     __syncthreads();  // V is there
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < kBN; ++k) {
-      const ulonglong2 p0 = *reinterpret_cast<const ulonglong2*>(pt + k * kPt + ty * 8);
-      const ulonglong2 p1 = *reinterpret_cast<const ulonglong2*>(pt + k * kPt + ty * 8 + 4);
+      const ulonglong2 p0 = *reinterpret_cast<const ulonglong2*>(pt + k * kPt + place(ty * 8, k & 15));
+      const ulonglong2 p1 = *reinterpret_cast<const ulonglong2*>(pt + k * kPt + place(ty * 8 + 4, k & 15));
       const uint64_t p[4] = {p0.x, p0.y, p1.x, p1.y};
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
       }
     }
     __syncthreads();  // V and P have been read
-    if (more) copy_tile(vs, a.values, n0 + kBN);
+    if (more) copy_tile(vs, a.values, n0 + kBN, 0);
   }
   copy_wait<0>();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_chunk_join may be set up
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
 
 template <int D>
 cudaError_t chunk_simt(const ChunkArgs& a, cudaStream_t st) {
-  constexpr int smem = (3 * 64 * (D + 4) + 64 * 68) * 4;
+  constexpr int pad = D == 64 ? 4 : 0, smem = (3 * 64 * (D + pad) + 64 * (64 + pad)) * 4;
   cudaError_t e = cudaFuncSetAttribute(k_chunk_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t(a.c.max_q) * a.c.group + kBM - 1) / kBM;
