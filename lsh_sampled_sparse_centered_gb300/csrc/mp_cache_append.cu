@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kWarps = 4;  // independent of each other
 constexpr int kBatch = 2;  // vectors of a lane that are worked on, as many more are on their way
+constexpr int kResident = 7;  // CTAs of an SM: left alone bf16 takes 80 registers, and six fit
 
 template <typename T>
 struct Vec {
@@ -52,7 +53,7 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a, const int parts) {
+__global__ void __launch_bounds__(kWarps * 32, kResident) k_cache_append(const AppendArgs a, const int parts) {
   constexpr int V = Vec<T>::N, TPH = D / V, HPW = 32 / TPH;  // heads of a warp at a time
   __shared__ alignas(16) float cosine[kWarps][D / 2], sine[kWarps][D / 2];  // of each pair's angle
   const CacheArgs& c = a.c;
@@ -159,15 +160,18 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_append(const AppendArgs a
         if (h - h0 >= heads) break;  // the same for the whole warp
         float x[V], y[V], z[V];
         unpack(u[k], x);
+        // An element that does not turn has no partner: an infinity next to it, or its own,
+        // times the factor 0 would be NaN.
         if (a.interleaved) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) y[j] = x[j ^ 1];
+          for (int j = 0; j < V; ++j) y[j] = e0 + (j & ~1) < a.rot ? x[j ^ 1] : 0.f;
         } else {
           uint4 o;
           o.x = __shfl_sync(0xffffffffu, u[k].x, l32 + away);
           o.y = __shfl_sync(0xffffffffu, u[k].y, l32 + away);
           o.z = __shfl_sync(0xffffffffu, u[k].z, l32 + away);
           o.w = __shfl_sync(0xffffffffu, u[k].w, l32 + away);
+          if (!turns) o = make_uint4(0, 0, 0, 0);
           unpack(o, y);
         }
         float ss = 0.f;
