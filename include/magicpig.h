@@ -284,8 +284,10 @@ MP_API int mp_decode_attention_static(const mp_config* cfg, void* tables, const 
  * cu_q (int32 [batch + 1], from 0, not decreasing) and kv_len (int32 [batch]) are device
  * memory, read when the kernels run: a captured call follows their current values.
  * The host gives limits that size the launch: total_q rows in the packed tensors,
- * max_q >= every m and max_kv >= every kv_len. What passes a limit is cut to it and
- * sets MP_STATUS_BAD_LENGTH; a page number outside the pool sets MP_STATUS_BAD_PAGE.
+ * max_q >= every m and max_kv >= every kv_len (both at least 1). What passes a limit (or the
+ * table's capacity) is left out and sets MP_STATUS_BAD_LENGTH: rows behind the first max_q and
+ * slots behind max_kv; the other tokens stay in their slots. A page number outside the pool sets
+ * MP_STATUS_BAD_PAGE.
  * `status` (device uint32, may be NULL) collects these bits; the caller clears it.
  * Query head j of a sequence reads KV head j / (q_heads / kv_heads); the softmax scale is
  * 1/sqrt(head_dim). Workspaces are device memory of the caller's, aligned to 256 bytes; they

@@ -103,9 +103,13 @@ __host__ __device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
 #endif
 }
 
-// Sequence b's packed rows [row0, row0 + m) and its n slots, cut to the call's limits.
+// Sequence b's packed rows [row0, row0 + m) and its n slots, cut to the call's limits, and the
+// slot that row row0 stands in. That slot goes by the lengths as they are, so that a cut moves
+// no token: row r is in slot kv_len - cu_q[b + 1] + r. Where every slot is behind (before) the
+// cut ones, any value from n - 1 on (up to -m) says the same and `first` is that limit.
 struct Seq {
-  int row0, m, n;
+  int row0, m, n, first;
+  __host__ __device__ int seen() const { return max(0, min(n, first + m)); }  // slots that any row sees
 };
 __host__ __device__ __forceinline__ Seq seq_of(const CacheArgs& c, int b) {
   Seq s;
@@ -113,8 +117,10 @@ __host__ __device__ __forceinline__ Seq seq_of(const CacheArgs& c, int b) {
   const int n = c.kv_len[b];
   s.n = max(0, min(n, int(min(int64_t(c.max_kv), slots))));
   bool cut = s.n != n;
+  int r1 = 0;
   if (c.cu_q) {
-    const int r0 = c.cu_q[b], r1 = c.cu_q[b + 1];
+    const int r0 = c.cu_q[b];
+    r1 = c.cu_q[b + 1];
     s.row0 = max(0, min(r0, c.total_q));
     const int e = max(s.row0, min(r1, c.total_q));
     s.m = min(e - s.row0, c.max_q);
@@ -123,7 +129,11 @@ __host__ __device__ __forceinline__ Seq seq_of(const CacheArgs& c, int b) {
     s.row0 = 0;
     s.m = 0;
   }
-  if (cut) flag(c.status, MP_STATUS_BAD_LENGTH);
+  s.first = s.n - s.m;
+  if (cut) {
+    if (c.cu_q) s.first = int(max(int64_t(-s.m), min(int64_t(n) - r1 + s.row0, int64_t(s.n) - 1)));
+    flag(c.status, MP_STATUS_BAD_LENGTH);
+  }
   return s;
 }
 

@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) k_cache_append(const A
   if (b < 0) return;  // a row outside every sequence
   const Seq s = seq_of(c, b);
   if (r < s.row0 || r >= s.row0 + s.m) return;
-  // from the length as it is: cut to the cache it would move the tokens to other slots
-  const int64_t slot = int64_t(c.kv_len[b]) - s.m + (r - s.row0);
+  // from the lengths as they are: cut to the limits they would move the tokens to other slots
+  const int64_t slot = int64_t(c.kv_len[b]) - c.cu_q[b + 1] + r;
   int64_t dst = -1;  // element offset of the slot's row of KV head 0
   if (slot >= 0 && slot < int64_t(c.cols) * c.page_size) {
     const int col = int(slot) / c.page_size;

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
   const int rows = s.m * c.group, r0 = tile * kBM;
   if (r0 >= rows) return;
   const int qh = c.kvh * c.group;
-  const int first = s.n - s.m;                                       // slot of token 0
+  const int first = s.first;                                         // slot of token 0
   const int last = first + min(r0 + kBM - 1, rows - 1) / c.group;     // slot of the tile's last token
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   // this split's keys: a run of 64-key tiles of the sequence
@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
   const CacheArgs& c = a.c;
   const int b = blockIdx.z, h = blockIdx.y, n0 = blockIdx.x * kBN;
   const Seq s = seq_of(c, b);
-  if (n0 >= s.n || s.m == 0) return;
-  const int rows = s.m * c.group, first = s.n - s.m, qh = c.kvh * c.group;
+  if (n0 >= s.seen() || s.m == 0) return;
+  const int rows = s.m * c.group, first = s.first, qh = c.kvh * c.group;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   load_transposed<D>(kt, [&](int i) -> const float* {
     return n0 + i < s.n ? static_cast<const float*>(a.keys) + slot_read(c, b, h, n0 + i) : nullptr;

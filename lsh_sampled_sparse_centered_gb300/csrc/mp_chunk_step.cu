@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Seq s = seq_of(c, b);
-  const int rows = s.m * c.group, first = s.n - s.m, qh = c.kvh * c.group;
+  const int rows = s.m * c.group, first = s.first, qh = c.kvh * c.group;
   if (rows == 0) return;  // the whole cluster
   // this CTA's slots, a whole number of rounds of all warps
   const int per = ((s.n + a.splits - 1) / a.splits + kWarps * kRound - 1) / (kWarps * kRound) * (kWarps * kRound);

@@ -52,7 +52,7 @@ constexpr int kCut = 10;      // units that cutting the tiles costs: a second pi
 
 // One piece of work: the steps [u0, u1) of a tile, as every role of the CTA sees it.
 struct Piece {
-  int b, h, row0, n, lead;  // sequence, KV head, first packed row, slots, slots before the chunk
+  int b, h, row0, n, lead;  // sequence, KV head, first packed row, slots, slot of that row
   int r0, rows;             // the tile's first row, and the rows of the whole chunk
   int u0, u1;               // u0 == u1: the run has ended
   int whole, slot;          // all of its tile's units; else where its partial result goes
@@ -111,7 +111,7 @@ __device__ __forceinline__ int tiles_of(const Seq& s, int group) {
 // steps of tile t: 128 keys each, up to the last slot that its last token sees
 __device__ __forceinline__ int steps_of(const Seq& s, int group, int t) {
   const int64_t last = min(int64_t(t + 1) * kRows, int64_t(s.m) * group) - 1;
-  const int see = min(s.n, s.n - s.m + int(last / group) + 1);
+  const int see = min(s.n, s.first + int(last / group) + 1);
   return max(1, (see + kKeys - 1) / kKeys);
 }
 
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t per = !found ? 1 : by_tile ? counts[b - b_begin] : units_of(b);
       const int h = int(quotient(at, per));
       at -= h * per;
-      const Seq s = found ? seqs[b - b_begin] : Seq{0, 0, 0};
+      const Seq s = found ? seqs[b - b_begin] : Seq{0, 0, 0, 0};
       const int tiles = tiles_of(s, c.group);
       int t = 0;
       if (by_tile) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lead = S.lead;
         const int64_t run = S.run, end = blockIdx.x * run + left;
         int b = S.start[0], h = S.start[1], t = S.start[2], at = S.start[3];  // at: units into the tile
-        Seq s = {0, 0, 0};
+        Seq s = {0, 0, 0, 0};
         int tiles = 0;
         if (left > 0) {
           s = S.first;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.h = h;
             p.row0 = s.row0;
             p.n = s.n;
-            p.lead = s.n - s.m;
+            p.lead = s.first;
             p.r0 = t * kRows;
             p.rows = s.m * c.group;
             p.u0 = u0;

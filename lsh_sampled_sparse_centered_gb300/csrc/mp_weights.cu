@@ -132,7 +132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   for (int i = int(threadIdx.x) - kZero; i >= 0 && i < b_end - b_begin; i += kThreads - kZero) {
     const Seq s = seq_of(c, b_begin + i);
     S.seqs[i] = s;
-    S.past[i] = s.m == 0 ? 0 : (s.n + kKeys - 1) / kKeys;
+    S.past[i] = s.m == 0 ? 0 : (s.seen() + kKeys - 1) / kKeys;
   }
   fence_async();
   if (threadIdx.x == kThreads - 32) {
@@ -217,11 +217,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         it.s = S.seqs[lo];
         it.n0 = int(in - it.h * per) * kKeys;
         const Blocks own = blocks_of(c.group, it.s.m);
-        // tokens before n0 - (n - m) see none of these keys
-        const int t_start = max(0, it.n0 - (it.s.n - it.s.m));
+        // tokens before slot n0 see none of these keys
+        const int t_start = max(0, it.n0 - it.s.first);
         it.i0 = own.runs == 1 ? t_start / own.per : t_start * own.runs;
         it.halves = it.s.n - it.n0 > kHalf ? 2 : 1;
-        it.steps = own.n - it.i0;  // at least one: n0 < n
+        it.steps = own.n - it.i0;  // at least one: n0 < seen()
         if (it.share && it.steps == 1) {
           if (rank) continue;  // nothing to share
           it.share = 0;
@@ -409,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int steps = it.steps;
       if (steps == 0) break;
       const bool active = half < it.halves;
-      const int slot = it.n0 + half * kHalf + key, m = it.s.m, i0 = it.i0, first = it.s.n - m;
+      const int slot = it.n0 + half * kHalf + key, m = it.s.m, i0 = it.i0, first = it.s.first;
       const bool mine = active && slot < it.s.n;
       const int share = it.share;
       float* const score = a.scores + (int64_t(it.b) * c.kvh + it.h) * (int64_t(c.cols) * c.page_size) + slot;
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsA
   const int64_t p0 = int64_t(blockIdx.x) * per;
   if (p0 >= s.n || s.m == 0) return;
   const int p1 = min(s.n, int(p0) + per);
-  const int first = s.n - s.m, qh = c.kvh * c.group, rows = s.m * c.group;
+  const int first = s.first, qh = c.kvh * c.group, rows = s.m * c.group;
   const float root = rsqrtf(float(D));
   float* scores = a.scores + (int64_t(b) * c.kvh + h) * (int64_t(c.cols) * c.page_size);
   const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.keys);

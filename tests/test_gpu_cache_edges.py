@@ -62,3 +62,102 @@ def test_append_keeps_infinities_out_of_other_elements(mp, dtype, rot, inter):
         want[e] = math.nan
         assert same(q_out[r, h], want), q_out[r, h]
     assert c.status.item() == 0
+
+
+# ---- lengths that pass a limit: every token stays in its own slot ----
+
+CUT = [
+    # dtype, q heads, kv heads, d, page, slots filled, kv_len, cu_q's end, rows of q, max_q, max_kv
+    ("bf16", 4, 2, 64, 16, 48, 51, 6, 6, 6, 48),        # three tokens behind the table's last slot
+    ("bf16", 4, 1, 128, 16, 48, 50, 4, 4, 4, 48),       # (at most 16 rows per KV head)
+    ("bf16", 8, 2, 128, 16, 400, 390, 40, 40, 40, 300),  # a limit that no token's own slot is below
+    ("bf16", 8, 2, 64, 16, 400, 390, 200, 200, 200, 300),  # and one that falls inside the chunk
+    ("bf16", 8, 2, 128, 16, 400, 390, 40, 40, 30, 400),  # more tokens than max_q
+    ("bf16", 4, 2, 128, 16, 400, 390, 50, 42, 50, 400),  # more tokens than rows
+    ("bf16", 4, 2, 64, 16, 400, 390, 8, 8, 5, 400),
+    ("bf16", 4, 2, 64, 16, 300, 20, 60, 60, 50, 300),    # chunk longer than the cache, and cut: the first 40 slots are negative
+    ("bf16", 4, 2, 64, 16, 300, 2 ** 31 - 1, 60, 60, 60, 300),
+    ("f32", 4, 2, 64, 16, 48, 51, 6, 6, 6, 48),
+    ("f32", 8, 2, 128, 16, 400, 390, 200, 200, 150, 300),
+    ("f32", 4, 2, 64, 16, 300, 20, 60, 60, 50, 300),
+]
+
+
+@pytest.mark.parametrize("dtype,hq,hk,d,page,fill,kv,end,rows,max_q,max_kv", CUT)
+def test_cut_lengths_leave_tokens_in_their_slots(mp, dtype, hq, hk, d, page, fill, kv, end, rows, max_q, max_kv):
+    c = Cache(mp, dtype, hq, hk, d, page, [fill])
+    c.kv_len.fill_(kv)
+    cu_t = torch.tensor([0, end], dtype=torch.int32, device=DEV)
+    q = c.randn(rows, hq, d, by=1.5)
+    live = min(rows, end, max_q)  # rows that the call takes
+    out, lse = attend(mp, c, q, cu_t, max_q, max_kv=max_kv)
+    assert c.status.item() == mp.MP_STATUS_BAD_LENGTH
+    n = min(kv, max_kv, c.ps * c.cols)
+    x = torch.full((live, hq, n), -math.inf, dtype=torch.float64, device=DEV)
+    ab, p_v, p_av = torch.zeros_like(x), torch.zeros(live, hq, d, dtype=torch.float64, device=DEV), None
+    p_av = torch.zeros_like(p_v)
+    seen = torch.arange(n, device=DEV)[None] <= (kv - end + torch.arange(live, device=DEV))[:, None]
+    for j in range(hq):
+        k = R.gather(c.keys, c.table, 0, j // (hq // hk), n)
+        x[:, j] = (q[:live, j].double() @ k.T / math.sqrt(d)).masked_fill(~seen, -math.inf)
+        ab[:, j] = (q[:live, j].double().abs() @ k.abs().T / math.sqrt(d)).masked_fill(~seen, 0)
+    z = torch.logsumexp(x, -1)
+    p = torch.where(seen[:, None], torch.exp(x - z[..., None]), torch.zeros_like(x))
+    p = torch.where(torch.isinf(z)[..., None], torch.zeros_like(p), p)
+    for j in range(hq):
+        v = R.gather(c.values, c.table, 0, j // (hq // hk), n)
+        p_v[:, j], p_av[:, j] = p[:, j] @ v, p[:, j] @ v.abs()
+    eps_x = (d + 8) * 2.0 ** -24 * ab.amax(-1)
+    rel = 2 * eps_x + n * 2.0 ** -24 + 2.0 ** -20 + (2.0 ** -8 if dtype == "bf16" else 0.0)
+    tol = HALF[dtype] * p_v.abs() + (1 + HALF[dtype]) * rel[..., None] * p_av
+    assert ((out[:live].double() - p_v).abs() <= tol).all()
+    empty = torch.isinf(z)
+    assert torch.equal(torch.isinf(lse[:live]), empty)
+    ztol = eps_x + (n + 8) * 2.0 ** -24 + 2.0 ** -21 * (1 + z.abs())
+    assert ((lse[:live].double() - z).abs()[~empty] <= ztol[~empty]).all()
+    assert (out[live:] == 77.0).all() and (lse[live:] == 77.0).all()  # rows that the limits leave out
+    # the weights see the same slots
+    c.status.zero_()
+    given = torch.full((rows, hq), math.nan, device=DEV)
+    given[:live] = z.float()
+    sc0 = torch.rand(1, hk, c.ps * c.cols, generator=c.gen).to(DEV) * 0.01
+    sc = sc0.clone()
+    mp.mp_cache_weights(c.cfg, q, given, cu_t, c.kv_len, max_q, max_kv, c.keys, c.table, sc, c.status)
+    assert c.status.item() == mp.MP_STATUS_BAD_LENGTH
+    zz = torch.where(empty, torch.zeros_like(z), given[:live].double())
+    w = torch.where(seen[:, None] & ~empty[..., None], torch.exp(x - zz[..., None]), torch.zeros_like(x))
+    want = sc0.double()
+    want[0, :, :n] += w.unflatten(1, (hk, hq // hk)).sum((0, 2))
+    top = zz.abs().max()
+    rel = (d + 8) * 2.0 ** -24 * ab.amax() + 2.0 ** -21 * (1 + top) + (hq // hk * live + 2) * 2.0 ** -24
+    assert ((sc.double() - want).abs() <= rel * want).all()
+
+
+def test_append_and_attention_agree_where_a_cut_token_stands(mp):
+    """A token that the append has put into the last slots attends to its own key there."""
+    c = Cache(mp, "f32", 2, 1, 64, 16, [48])
+    c.keys.zero_()
+    c.values.zero_()
+    c.kv_len.fill_(51)  # three more than the table has room for: the tokens stand in slots 45 to 50
+    _, cu_t = offsets([6])
+    q, k, v = c.randn(6, 2, 64), c.randn(6, 1, 64), c.randn(6, 1, 64)
+    q_out = torch.empty_like(q)
+    mp.mp_cache_append(c.cfg, mp.make_rotary(rot_dim=0), q, k, v, None, None, None, None, cu_t, c.kv_len, c.keys, c.values, c.table, q_out,
+                       c.status)
+    out, _ = attend(mp, c, 40.0 * k.expand(6, 2, 64).contiguous(), cu_t, 6)  # queries that see little but their own key
+    assert (out[:3].double() - v[:3].double()).abs().max() <= 2.0 ** -20 * v.abs().max()
+
+
+def test_append_of_more_rows_than_the_call_has(mp):
+    """cu_q that ends behind the packed tensors: the rows that are there go where they belong."""
+    c = Cache(mp, "bf16", 2, 1, 64, 16, [48], fill="none")
+    c.keys.fill_(5.0)
+    c.values.fill_(5.0)
+    cu_t = torch.tensor([0, 9], dtype=torch.int32, device=DEV)
+    q, k, v = c.randn(6, 2, 64), c.randn(6, 1, 64), c.randn(6, 1, 64)
+    q_out = torch.empty_like(q)
+    mp.mp_cache_append(c.cfg, mp.make_rotary(rot_dim=0), q, k, v, None, None, None, None, cu_t, c.kv_len, c.keys, c.values, c.table, q_out,
+                       c.status)
+    assert c.status.item() == mp.MP_STATUS_BAD_LENGTH
+    assert torch.equal(pool_rows(c.keys, c, 0, 0, 48)[39:45], k[:, 0]) and torch.equal(pool_rows(c.values, c, 0, 0, 48)[39:45], v[:, 0])
+    assert (pool_rows(c.keys, c, 0, 0, 48)[:39] == 5.0).all() and (pool_rows(c.keys, c, 0, 0, 48)[45:] == 5.0).all()
