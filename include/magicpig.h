@@ -390,7 +390,9 @@ MP_API int mp_evict_workspace_bytes(const mp_cache_config* cfg, int32_t max_kv, 
  *   kept    : device int32 [batch][kv_heads][budget], or NULL: the kept slots, ascending;
  *             entries from dst_len on are left as they were.
  * 1 <= budget <= dst max_pages * page_size (else MP_ERR_CAPACITY), n_sink + window <= budget.
- * What lies behind the new lengths in the destination is left as it was. */
+ * What lies behind the new lengths in the destination is left as it was.
+ * dst_len may be kv_len itself; any other overlap of dst_scores, dst_len, kept or the workspace
+ * with what is read, and of two dense caches, is refused (MP_ERR_INVALID_ARG). */
 MP_API int mp_cache_evict(const mp_cache_config* cfg, const mp_cache_config* dst_cfg, const void* keys,
                           const void* values, const int32_t* page_table, const int32_t* kv_len, int32_t max_kv,
                           const float* scores, int32_t n_sink, int32_t window, int32_t budget, void* dst_keys,

@@ -84,6 +84,39 @@ static uint64_t chunk_bytes(const mp_cache_config* c, int total_q, int max_q, in
   return part_bytes(c, total_q, splits) + align256(uint64_t(splits) * total_q * c->q_heads * 2 * 4);
 }
 
+struct Range {
+  const void* p;
+  uint64_t bytes;
+};
+static bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// What the eviction writes against what it reads: its CTAs work in no order, so that a buffer that
+// is both would be read after it was overwritten. dst_len may be kv_len (mp_evict.cu). Pages
+// named by a table are the caller's business, a dense cache's are known.
+static bool evict_overlaps(const mp_cache_config* c, const mp_cache_config* d, const void* keys, const void* values,
+                           const void* table, const void* kv_len, const void* scores, int budget, const void* dst_keys,
+                           const void* dst_values, const void* dst_table, const void* dst_scores, const void* dst_len,
+                           const void* kept, const void* workspace) {
+  const uint64_t units = uint64_t(c->batch) * c->kv_heads, row = uint64_t(c->head_dim) * (c->dtype == MP_DTYPE_BF16 ? 2 : 4);
+  const uint64_t src_slots = uint64_t(c->max_pages) * c->page_size, dst_slots = uint64_t(d->max_pages) * d->page_size;
+  const Range in[] = {{scores, units * src_slots * 4}, {table, uint64_t(c->batch) * c->max_pages * 4},
+                      {dst_table, uint64_t(c->batch) * d->max_pages * 4}, {kv_len, uint64_t(c->batch) * 4}};
+  const Range out[] = {{dst_scores, units * dst_slots * 4}, {kept, units * budget * 4}, {kept ? nullptr : workspace, units * budget * 4},
+                       {dst_len, uint64_t(c->batch) * 4}};
+  for (const Range& i : in)
+    for (const Range& o : out)
+      if (overlap(i, o) && !(i.p == kv_len && o.p == dst_len && kv_len == dst_len)) return true;
+  if (table || dst_table) return false;
+  const Range from[] = {{keys, units * src_slots * row}, {values, units * src_slots * row}};
+  const Range to[] = {{dst_keys, units * dst_slots * row}, {dst_values, units * dst_slots * row}};
+  for (const Range& i : from)
+    for (const Range& o : to)
+      if (overlap(i, o)) return true;
+  return false;
+}
+
 static uint64_t evict_bytes(const mp_cache_config* c, int budget) {
   return align256(uint64_t(c->batch) * c->kv_heads * budget * 4);
 }
@@ -282,6 +315,9 @@ int mp_cache_evict(const mp_cache_config* cfg, const mp_cache_config* dst_cfg, c
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MP_ERR_INVALID_ARG;
   if (workspace_bytes < evict_bytes(cfg, budget)) return MP_ERR_SCRATCH;
   if (injected("evict")) return MP_ERR_INJECTED;
+  if (evict_overlaps(cfg, dst_cfg, keys, values, page_table, kv_len, scores, budget, dst_keys, dst_values, dst_page_table,
+                     dst_scores, dst_len, kept, workspace))
+    return MP_ERR_INVALID_ARG;
   EvictArgs a;
   a.c = cache_args(cfg, page_table, nullptr, kv_len, 0, 1, max_kv, status);
   a.keys = keys;

@@ -88,7 +88,6 @@ __global__ void __launch_bounds__(kSel, 1) k_evict_select(const EvictArgs a) {
   const float* sc = a.scores + unit * (int64_t(c.cols) * c.page_size);
   int32_t* kept = a.kept + unit * a.budget;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (h == 0 && rank == 0 && tid == 0) a.dst_len[b] = min(n, a.budget);
   if (n <= a.budget) {  // the same for the whole cluster
     for (int i = rank * kSel + tid; i < n; i += ranks * kSel) kept[i] = i;
     return;
@@ -206,6 +205,9 @@ __global__ void __launch_bounds__(256) k_evict_gather(const EvictArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // k_evict_select has written the kept slots
   const int m = min(seq_of(c, b).n, a.budget);
   const int j0 = blockIdx.x * (GROUPS * kRowsEach) + threadIdx.x / ROW, e = threadIdx.x % ROW;
+  // here and not by the selection, whose CTAs all read the old length: dst_len may be kv_len (both
+  // lengths give this kernel the same m)
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.dst_len[b] = m;
   if (j0 >= m) return;
   const int64_t unit = int64_t(b) * c.kvh + h;
   const int32_t* kept = a.kept + unit * a.budget;

@@ -161,3 +161,23 @@ def test_append_of_more_rows_than_the_call_has(mp):
     assert c.status.item() == mp.MP_STATUS_BAD_LENGTH
     assert torch.equal(pool_rows(c.keys, c, 0, 0, 48)[39:45], k[:, 0]) and torch.equal(pool_rows(c.values, c, 0, 0, 48)[39:45], v[:, 0])
     assert (pool_rows(c.keys, c, 0, 0, 48)[:39] == 5.0).all() and (pool_rows(c.keys, c, 0, 0, 48)[45:] == 5.0).all()
+
+
+# ---- eviction in place ----
+
+def test_eviction_may_write_the_new_lengths_over_the_old(mp):
+    """dst_len == kv_len: what a loop that keeps one length per sequence passes. Every head must
+    have read the old length before it changes."""
+    kv = [5000, 300, 2049, 1000, 4096, 0, 77, 3000]
+    for rep in range(3):
+        c = Cache(mp, "bf16", 8, 8, 64, 0, kv, seed=rep)
+        t = Cache(mp, "bf16", 8, 8, 64, 0, [500] * 8, cap=500, fill="none")
+        sc = make_scores("heavy", (8, 8, c.ps), c.gen)
+        ws = torch.empty(mp.mp_evict_workspace_bytes(c.cfg, 5000, 500), dtype=torch.uint8, device=DEV)
+        mp.mp_cache_evict(c.cfg, t.cfg, c.keys, c.values, None, c.kv_len, 5000, sc, 4, 16, 500, t.keys, t.values, None, None, c.kv_len, None,
+                          ws, c.status)
+        assert c.status.item() == 0 and c.kv_len.tolist() == [min(n, 500) for n in kv]
+        for b, n in enumerate(kv):
+            for h in range(8):
+                at = torch.tensor(R.keep(sc[b, h], n, 4, 16, 500), dtype=torch.int64, device=DEV)
+                assert torch.equal(t.keys[b, h, :len(at)], c.keys[b, h][at]) and torch.equal(t.values[b, h, :len(at)], c.values[b, h][at])
