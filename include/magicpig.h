@@ -282,7 +282,8 @@ MP_API int mp_decode_attention_static(const mp_config* cfg, void* tables, const 
  * sits in slot kv_len[b] - m + i. A token at a negative slot (m > kv_len[b]) is not in the
  * cache and sees nothing. Rows outside every sequence are left as they were.
  * cu_q (int32 [batch + 1], from 0, not decreasing) and kv_len (int32 [batch]) are device
- * memory, read when the kernels run: a captured call follows their current values.
+ * memory, read when the kernels run: a captured call follows their current values. Nothing may
+ * write them, the page table or the cache's pages while a call that reads them runs.
  * The host gives limits that size the launch: total_q rows in the packed tensors,
  * max_q >= every m and max_kv >= every kv_len (both at least 1). What passes a limit (or the
  * table's capacity) is left out and sets MP_STATUS_BAD_LENGTH: rows behind the first max_q and

@@ -51,10 +51,13 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Seq s = seq_of(c, b);
   const int rows = s.m * c.group, first = s.first, qh = c.kvh * c.group;
-  if (rows == 0) return;  // the whole cluster
+  // A cluster goes through its barriers without new tokens too: were the length written meanwhile
+  // (a caller that does not wait for its own copy), a CTA that had left would be read by the
+  // others, which faults.
+  if (!JOINED && rows == 0) return;
   // this CTA's slots, a whole number of rounds of all warps
   const int per = ((s.n + a.splits - 1) / a.splits + kWarps * kRound - 1) / (kWarps * kRound) * (kWarps * kRound);
-  const int k0 = int(min(int64_t(s.n), int64_t(split) * per)), k1 = min(s.n, k0 + per);
+  const int k0 = int(min(int64_t(s.n), int64_t(split) * per)), k1 = rows == 0 ? k0 : min(s.n, k0 + per);
 
   // Q: row r of the tile is token r / group, head r % group; rows behind the last are zero
   uint4 q[NT][KC];

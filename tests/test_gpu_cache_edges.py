@@ -163,6 +163,48 @@ def test_append_of_more_rows_than_the_call_has(mp):
     assert (pool_rows(c.keys, c, 0, 0, 48)[:39] == 5.0).all() and (pool_rows(c.keys, c, 0, 0, 48)[45:] == 5.0).all()
 
 
+# ---- few rows: 9 to 16 per KV head ----
+
+FEW = [
+    # q heads, kv heads, d, page, chunk lengths, cache lengths
+    (12, 1, 128, 0, [1], [2000]),                    # a short cache, one cluster of slices
+    (8, 2, 128, 64, [4, 3], [2000, 700]),
+    (16, 1, 128, 16, [1, 1, 1], [300, 5, 500]),       # four slices
+    (16, 1, 64, 0, [1], [200]),                      # two
+    (9, 1, 128, 48, [1], [250]),
+    (12, 1, 128, 64, [1], [20000]),                  # slices that a second kernel joins
+    (8, 2, 128, 0, [4], [20000]),
+    (8, 2, 64, 64, [4, 2], [20000, 13000]),
+    (12, 1, 64, 0, [1, 1], [9000, 20000]),
+    (16, 16, 128, 16, [16, 9, 1], [700, 3000, 40]),
+    (16, 16, 64, 0, [13], [1000]),
+    (24, 2, 128, 64, [1] * 40, [70 * (b + 1) for b in range(40)]),  # as many sequences as leave a slice each
+    (8, 2, 128, 16, [4, 0, 3], [600, 50, 400]),      # a sequence without new tokens
+    # and up to 8 rows
+    (8, 1, 128, 0, [1], [20000]),
+    (4, 1, 128, 64, [2, 0, 1], [600, 50, 400]),
+    (8, 8, 64, 16, [8, 5], [500, 2000]),
+    (4, 2, 64, 64, [4, 1], [9000, 200]),
+]
+
+
+@pytest.mark.parametrize("hq,hk,d,page,q_lens,kv", FEW)
+def test_few_rows_keep_their_weights_exact(mp, hq, hk, d, page, q_lens, kv):
+    assert hq // hk * max(q_lens) <= 16
+    c = Cache(mp, "bf16", hq, hk, d, page, kv)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1], hq, d, by=1.5)
+    out, lse = attend(mp, c, q, cu_t, max(q_lens))
+    assert c.status.item() == 0
+    want, z, spread, slack = R.attention(q, cu, c.kv, c.keys, c.values, c.table, hk)
+    eps_x = (d + 8) * 2.0 ** -24 * slack
+    rel = 2 * eps_x + max(kv) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -16
+    tol = HALF["bf16"] * want.abs() + (1 + HALF["bf16"]) * rel[..., None] * spread
+    assert ((out.double() - want).abs() <= tol).all()
+    ztol = eps_x + (max(kv) + 8) * 2.0 ** -24 + 2.0 ** -21 * (1 + z.abs())
+    assert ((lse.double() - z).abs() <= ztol).all()
+
+
 # ---- eviction in place ----
 
 def test_eviction_may_write_the_new_lengths_over_the_old(mp):
