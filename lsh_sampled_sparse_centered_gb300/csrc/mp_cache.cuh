@@ -26,6 +26,7 @@ struct ChunkArgs {
   // partial results in the workspace: slices [splits][total_q][q_heads], or (tensor cores)
   // slots of the pieces of tiles that are shared by CTAs
   int splits;   // slices of the keys per row tile
+  bool joined;  // the slices are a cluster that joins itself
   float* part;  // [..][d]: unnormalised sums
   float* ml;    // [..][2]: their reference (log2) and sum
   void* cuts;   // shared tiles (tensor cores)
@@ -67,8 +68,11 @@ struct EvictArgs {
 // keys (fp32, and bf16 with few query rows), CTAs of the tensor-core kernel and its workspace.
 int chunk_splits(const mp_cache_config* c, int max_q, int max_kv);
 bool chunk_is_step(int group, int max_q);
-int chunk_step_splits(int batch, int kvh, int group, int max_q, int max_kv);
-bool chunk_step_joined(int splits);  // the slices join themselves
+struct StepPlan {
+  int splits;
+  bool joined;  // the slices join themselves
+};
+StepPlan chunk_step_plan(const mp_cache_config* c, int max_q, int max_kv);
 int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv);
 uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv);
 

@@ -65,13 +65,10 @@ static CacheArgs cache_args(const mp_cache_config* c, const int32_t* table, cons
 static bool chunk_on_tensor_cores(const mp_cache_config* c, int max_q) {
   return c->dtype == MP_DTYPE_BF16 && !chunk_is_step(c->q_heads / c->kv_heads, max_q);
 }
-static int slices(const mp_cache_config* c, int max_q, int max_kv) {
-  if (c->dtype != MP_DTYPE_BF16) return chunk_splits(c, max_q, max_kv);
-  return chunk_step_splits(c->batch, c->kv_heads, c->q_heads / c->kv_heads, max_q, max_kv);
+static StepPlan slices(const mp_cache_config* c, int max_q, int max_kv) {
+  return c->dtype == MP_DTYPE_BF16 ? chunk_step_plan(c, max_q, max_kv) : StepPlan{chunk_splits(c, max_q, max_kv), false};
 }
-static bool needs_join(const mp_cache_config* c, int splits) {
-  return splits > 1 && !(c->dtype == MP_DTYPE_BF16 && chunk_step_joined(splits));
-}
+static bool needs_join(const StepPlan& p) { return p.splits > 1 && !p.joined; }
 static uint64_t part_bytes(const mp_cache_config* c, int total_q, int splits) {
   return align256(uint64_t(splits) * total_q * c->q_heads * c->head_dim * 4);
 }
@@ -79,9 +76,9 @@ static uint64_t chunk_bytes(const mp_cache_config* c, int total_q, int max_q, in
   if (total_q == 0) return 0;
   max_q = std::min(max_q, total_q);
   if (chunk_on_tensor_cores(c, max_q)) return chunk_tc_workspace(c, max_q, max_kv);
-  const int splits = slices(c, max_q, max_kv);
-  if (!needs_join(c, splits)) return 0;
-  return part_bytes(c, total_q, splits) + align256(uint64_t(splits) * total_q * c->q_heads * 2 * 4);
+  const StepPlan plan = slices(c, max_q, max_kv);
+  if (!needs_join(plan)) return 0;
+  return part_bytes(c, total_q, plan.splits) + align256(uint64_t(plan.splits) * total_q * c->q_heads * 2 * 4);
 }
 
 struct Range {
@@ -226,6 +223,7 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
   a.out = out;
   a.lse = lse;
   a.splits = 1;
+  a.joined = false;
   a.part = a.ml = nullptr;
   a.cuts = nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -234,7 +232,9 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
     ProfScope ps(st, K_CHUNK_ATTEND);
     return launch_chunk_tc(a, workspace, st) == cudaSuccess ? MP_OK : MP_ERR_CUDA;
   }
-  a.splits = slices(cfg, a.c.max_q, max_kv);
+  const StepPlan plan = slices(cfg, a.c.max_q, max_kv);
+  a.splits = plan.splits;
+  a.joined = plan.joined;
   if (need > 0) {
     a.part = static_cast<float*>(workspace);
     a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(cfg, total_q, a.splits));
@@ -244,7 +244,7 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
     const cudaError_t e = cfg->dtype == MP_DTYPE_BF16 ? launch_chunk_step(a, st) : launch_chunk_simt(a, st);
     if (e != cudaSuccess) return MP_ERR_CUDA;
   }
-  if (needs_join(cfg, a.splits)) {
+  if (needs_join(plan)) {
     ProfScope ps(st, K_CHUNK_JOIN);
     if (launch_chunk_join(a, cfg->dtype, st) != cudaSuccess) return MP_ERR_CUDA;
   }

@@ -15,6 +15,8 @@
 // a few percent of the time, and one term would double the result's error.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "mp_cache.cuh"
 #include "mp_tc.cuh"
 
@@ -28,7 +30,8 @@ __host__ __device__ constexpr int warps_of(bool joined) { return joined ? 8 : 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;
-constexpr int kShort = 4096;
+constexpr int kShort = 4096;  // slots of a cache, and of a slice, that a cluster joins itself
+constexpr int kSlice = 1024;
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 // element e (0..7) of the 16-byte chunks a and b as one pair
@@ -297,7 +300,7 @@ template <int D>
 cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.splits, a.c.kvh, a.c.batch);
-  cfg.blockDim = dim3(warps_of(chunk_step_joined(a.splits)) * 32);
+  cfg.blockDim = dim3(warps_of(a.joined) * 32);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -305,7 +308,7 @@ cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   const bool one = int64_t(a.c.max_q) * a.c.group <= 8;
-  if (chunk_step_joined(a.splits)) {
+  if (a.joined) {
     cfg.numAttrs = 1;
     return one ? cudaLaunchKernelEx(&cfg, k_chunk_step<D, 1, true>, a) : cudaLaunchKernelEx(&cfg, k_chunk_step<D, 2, true>, a);
   }
@@ -316,19 +319,64 @@ cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
 
 bool chunk_is_step(int group, int max_q) { return int64_t(max_q) * group <= 16; }
 
+// Clusters of `size` CTAs that run at once on the current device (kept per device; without one, a
+// low guess, so that sizes can be asked for).
+static int clusters_at_once(int d, bool one, int size) {
+  static std::atomic<int> cache[64][2][2][3];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 76 / size;
+  }
+  std::atomic<int>& kept = cache[dev][d == 128][one][size == 8 ? 2 : (size == 4 ? 1 : 0)];
+  int n = kept.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size, 65535);
+    cfg.blockDim = dim3(warps_of(true) * 32);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    auto ask = [&](auto kernel) { return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg); };
+    const cudaError_t e = d == 128 ? (one ? ask(k_chunk_step<128, 1, true>) : ask(k_chunk_step<128, 2, true>))
+                                   : (one ? ask(k_chunk_step<64, 1, true>) : ask(k_chunk_step<64, 2, true>));
+    if (e != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = 76 / size;
+    }
+    kept.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // Slices of at least 128 slots: one wave of the CTAs that fit (three per SM with up to eight
 // rows, two with more), or two waves where a slice then still has 2048 slots (98304 slots of
-// eight KV heads: 66.8 us in one wave, 71.0 in two; four times that: 222 and 217 us). Caches of up to kShort slots take eight, a cluster that
-// joins itself (2048 slots of eight KV heads: 8.9 us, 10.5 with 16 slices and a second kernel).
-int chunk_step_splits(int batch, int kvh, int group, int max_q, int max_kv) {
-  const int64_t fit = int64_t(device_sm_count()) * (int64_t(max_q) * group <= 8 ? 3 : 2), units = int64_t(batch) * kvh;
-  const int64_t wave = fit / units, most = (int64_t(max_kv) + 127) / 128;
-  const int64_t two = 2 * fit / units;
+// eight KV heads: 66.8 us in one wave, 71.0 in two; four times that: 222 and 217 us).
+//
+// Short caches take a cluster of slices that joins itself instead (no second kernel, no
+// workspace), the largest of 8, 4 and 2 whose clusters all run at once: its CTAs have twice the
+// warps and need an SM each (half of one with d = 64 and up to eight rows), and a second round of
+// them costs more than the join. One token, d = 128, four heads per KV head, us in one cluster of
+// 8, 4 or 2 per KV head and as separate slices:
+//   8 KV heads x 1024 slots    6.5   7.3   9.2    8.7
+//   16 (15 clusters of 8 fit) 12.2   8.0  10.2    9.4
+//   32 x 4096 slots           30.9  17.6  25.0   18.4
+//   64 x 1024                 30.4  16.4  11.7   13.8
+//   56 x 4096                 42.4  32.8  27.9   25.9
+//   8 x 8192                  15.8  24.1  41.4   14.0
+//   56 x 30000               176.8 166.3 159.1  132.2
+StepPlan chunk_step_plan(const mp_cache_config* c, int max_q, int max_kv) {
+  const int64_t rows = int64_t(max_q) * (c->q_heads / c->kv_heads), units = int64_t(c->batch) * c->kv_heads;
+  const int64_t most = (int64_t(max_kv) + 127) / 128;
+  for (int size = 8; max_kv <= kShort && size > 1; size /= 2)
+    if (size < 2 * most && max_kv <= size * kSlice && units <= clusters_at_once(c->head_dim, rows <= 8, size)) return {size, true};
+  const int64_t fit = int64_t(device_sm_count()) * (rows <= 8 ? 3 : 2), wave = fit / units, two = 2 * fit / units;
   const int64_t fill = two * 2048 <= max_kv ? two : wave, s = fill < most ? fill : most;
-  if (s > 8 && max_kv <= kShort) return 8;
-  return int(s < 1 ? 1 : s);
+  return {int(s < 1 ? 1 : s), false};
 }
-bool chunk_step_joined(int splits) { return splits == 2 || splits == 4 || splits == 8; }
 
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st) {
   return a.c.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
