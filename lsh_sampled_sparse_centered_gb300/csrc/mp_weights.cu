@@ -26,6 +26,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "mp_cache.cuh"
@@ -642,17 +643,36 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsA
   }
 }
 
+// CTAs of k_weights_step that an SM of the current device holds, for up to 8, 16 or 32 rows (kept
+// per device).
+template <int D>
+int step_ctas_per_sm(int kind) {
+  static std::atomic<int> cache[64][3];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 4;
+  n = cache[dev][kind].load(std::memory_order_relaxed);
+  if (n == 0) {
+    auto ask = [&](auto kernel) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kStepWarps * 32, 0); };
+    const cudaError_t e = kind == 0 ? ask(k_weights_step<D, 1>) : (kind == 1 ? ask(k_weights_step<D, 2>) : ask(k_weights_step<D, 4>));
+    if (e != cudaSuccess || n < 1) return 4;  // the launch will say what is wrong
+    cache[dev][kind].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 template <int D>
 cudaError_t launch(const WeightsArgs& a, cudaStream_t st) {
   const CacheArgs& c = a.c;
   const int64_t rows = int64_t(c.max_q) * c.group;
   if (rows <= 32) {
-    // slices of at least four rounds, one wave of the CTAs that fit
-    const int64_t fit = int64_t(device_sm_count()) * (rows <= 16 ? 5 : 3) / (int64_t(c.kvh) * c.batch);
+    // Slices of at least four rounds, one wave of the CTAs that fit (one more per SM than fit: 16
+    // rows, 65536 slots of 32 KV heads 106 us instead of 84; half of them: 111).
+    const int kind = rows <= 8 ? 0 : (rows <= 16 ? 1 : 2);
+    const int64_t fit = int64_t(device_sm_count()) * step_ctas_per_sm<D>(kind) / (int64_t(c.kvh) * c.batch);
     const int64_t most = (c.max_kv + 4 * kStepWarps * kRound - 1) / (4 * kStepWarps * kRound);
     const dim3 grid(unsigned(std::max<int64_t>(1, std::min(fit, most))), c.kvh, c.batch);
-    if (rows <= 8) k_weights_step<D, 1><<<grid, kStepWarps * 32, 0, st>>>(a);
-    else if (rows <= 16) k_weights_step<D, 2><<<grid, kStepWarps * 32, 0, st>>>(a);
+    if (kind == 0) k_weights_step<D, 1><<<grid, kStepWarps * 32, 0, st>>>(a);
+    else if (kind == 1) k_weights_step<D, 2><<<grid, kStepWarps * 32, 0, st>>>(a);
     else k_weights_step<D, 4><<<grid, kStepWarps * 32, 0, st>>>(a);
     return cudaGetLastError();
   }
