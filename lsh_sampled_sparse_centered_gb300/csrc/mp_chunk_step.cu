@@ -352,9 +352,33 @@ static int clusters_at_once(int d, bool one, int size) {
   return n;
 }
 
-// Slices of at least 128 slots: one wave of the CTAs that fit (three per SM with up to eight
-// rows, two with more), or two waves where a slice then still has 2048 slots (98304 slots of
-// eight KV heads: 66.8 us in one wave, 71.0 in two; four times that: 222 and 217 us).
+// CTAs of a separate slice that an SM of the current device holds (the same way).
+static int ctas_per_sm(int d, bool one) {
+  static std::atomic<int> cache[64][2][2];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return one ? 3 : 2;
+  }
+  std::atomic<int>& kept = cache[dev][d == 128][one];
+  int n = kept.load(std::memory_order_relaxed);
+  if (n == 0) {
+    auto ask = [&](auto kernel) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, warps_of(false) * 32, 0); };
+    const cudaError_t e = d == 128 ? (one ? ask(k_chunk_step<128, 1, false>) : ask(k_chunk_step<128, 2, false>))
+                                   : (one ? ask(k_chunk_step<64, 1, false>) : ask(k_chunk_step<64, 2, false>));
+    if (e != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = one ? 3 : 2;
+    }
+    kept.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Slices of at least 128 slots: one wave of the CTAs that fit (d = 128: three per SM with up to
+// eight rows, two with more; d = 64: four. One less, d = 64, 98304 slots of 32 KV heads: 143 us
+// instead of 127, one more 137), or two waves where a slice then still has 2048 slots (98304 slots
+// of eight KV heads: 66.8 us in one wave, 71.0 in two; four times that: 222 and 217 us).
 //
 // Short caches take a cluster of slices that joins itself instead (no second kernel, no
 // workspace), the largest of 8, 4 and 2 whose clusters all run at once: its CTAs have twice the
@@ -373,7 +397,7 @@ StepPlan chunk_step_plan(const mp_cache_config* c, int max_q, int max_kv) {
   const int64_t most = (int64_t(max_kv) + 127) / 128;
   for (int size = 8; max_kv <= kShort && size > 1; size /= 2)
     if (size < 2 * most && max_kv <= size * kSlice && units <= clusters_at_once(c->head_dim, rows <= 8, size)) return {size, true};
-  const int64_t fit = int64_t(device_sm_count()) * (rows <= 8 ? 3 : 2), wave = fit / units, two = 2 * fit / units;
+  const int64_t fit = int64_t(device_sm_count()) * ctas_per_sm(c->head_dim, rows <= 8), wave = fit / units, two = 2 * fit / units;
   const int64_t fill = two * 2048 <= max_kv ? two : wave, s = fill < most ? fill : most;
   return {int(s < 1 ? 1 : s), false};
 }
