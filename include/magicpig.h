@@ -341,7 +341,8 @@ MP_API int mp_cache_append(const mp_cache_config* cfg, const mp_rotary* rotary, 
                            int32_t total_q, void* keys, void* values, const int32_t* page_table, void* q_out,
                            uint32_t* status, void* stream);
 
-/* Bytes of workspace of mp_chunk_attention for these limits (0 is possible). */
+/* Bytes of workspace that serve every mp_chunk_attention whose limits are at most these (0 is
+ * possible). One call may need less, and a call with smaller limits more than one with larger. */
 MP_API int mp_chunk_workspace_bytes(const mp_cache_config* cfg, int32_t total_q, int32_t max_q, int32_t max_kv,
                                     uint64_t* bytes);
 

@@ -69,16 +69,48 @@ static StepPlan slices(const mp_cache_config* c, int max_q, int max_kv) {
   return c->dtype == MP_DTYPE_BF16 ? chunk_step_plan(c, max_q, max_kv) : StepPlan{chunk_splits(c, max_q, max_kv), false};
 }
 static bool needs_join(const StepPlan& p) { return p.splits > 1 && !p.joined; }
-static uint64_t part_bytes(const mp_cache_config* c, int total_q, int splits) {
-  return align256(uint64_t(splits) * total_q * c->q_heads * c->head_dim * 4);
+// tokens that partial results are kept for: those of the sequences, however many rows lie packed
+static int part_rows(const mp_cache_config* c, int total_q, int max_q) {
+  return int(std::min(int64_t(total_q), int64_t(c->batch) * max_q));
 }
+static uint64_t part_bytes(const mp_cache_config* c, int rows, int splits) {
+  return align256(uint64_t(splits) * rows * c->q_heads * c->head_dim * 4);
+}
+static uint64_t slices_bytes(const mp_cache_config* c, int rows, int splits) {
+  return part_bytes(c, rows, splits) + align256(uint64_t(splits) * rows * c->q_heads * 2 * 4);
+}
+// What one call takes.
 static uint64_t chunk_bytes(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
   if (total_q == 0) return 0;
   max_q = std::min(max_q, total_q);
   if (chunk_on_tensor_cores(c, max_q)) return chunk_tc_workspace(c, max_q, max_kv);
   const StepPlan plan = slices(c, max_q, max_kv);
-  if (!needs_join(plan)) return 0;
-  return part_bytes(c, total_q, plan.splits) + align256(uint64_t(plan.splits) * total_q * c->q_heads * 2 * 4);
+  return needs_join(plan) ? slices_bytes(c, part_rows(c, total_q, max_q), plan.splits) : 0;
+}
+// What the calls take whose limits are at most these. One call's need falls where more rows or a
+// shorter cache are cut into fewer slices, or into slices that join themselves, so this is the
+// largest need over the smaller max_q, with slices that only grow with max_kv.
+static uint64_t chunk_bytes_most(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
+  if (total_q == 0) return 0;
+  max_q = std::min(max_q, total_q);
+  const int group = c->q_heads / c->kv_heads;
+  uint64_t most = 0;
+  if (c->dtype == MP_DTYPE_BF16) {
+    if (chunk_on_tensor_cores(c, max_q)) most = chunk_tc_workspace(c, max_q, max_kv);  // grows with both
+    for (int q = 1; q <= max_q && chunk_is_step(group, q); ++q) {
+      const int splits = chunk_step_most(c, q, max_kv);
+      if (splits > 1) most = std::max(most, slices_bytes(c, part_rows(c, total_q, q), splits));
+    }
+    return most;
+  }
+  // the slices go by the number of row tiles: the largest max_q of each, until one slice is left
+  for (int64_t rows = (int64_t(group) + kChunkRows - 1) / kChunkRows * kChunkRows;; rows += kChunkRows) {
+    const int q = int(std::min<int64_t>(max_q, rows / group));
+    const int splits = chunk_splits(c, q, max_kv);
+    if (splits == 1) return most;
+    most = std::max(most, slices_bytes(c, part_rows(c, total_q, q), splits));
+    if (q == max_q) return most;
+  }
 }
 
 struct Range {
@@ -188,7 +220,7 @@ int mp_chunk_workspace_bytes(const mp_cache_config* cfg, int32_t total_q, int32_
   if (rc != MP_OK) return rc;
   if ((rc = check_limits(cfg, total_q, max_q, max_kv)) != MP_OK) return rc;
   if (!bytes) return MP_ERR_INVALID_ARG;
-  *bytes = chunk_bytes(cfg, total_q, max_q, max_kv);
+  *bytes = chunk_bytes_most(cfg, total_q, max_q, max_kv);
   return MP_OK;
 }
 
@@ -224,6 +256,7 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
   a.lse = lse;
   a.splits = 1;
   a.joined = false;
+  a.part_rows = part_rows(cfg, total_q, a.c.max_q);
   a.part = a.ml = nullptr;
   a.cuts = nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -237,7 +270,7 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
   a.joined = plan.joined;
   if (need > 0) {
     a.part = static_cast<float*>(workspace);
-    a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(cfg, total_q, a.splits));
+    a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(cfg, a.part_rows, a.splits));
   }
   {
     ProfScope ps(st, K_CHUNK_ATTEND);

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
       sum = fmaf(sl[w][r], by[w], sum);
     }
     const int64_t row = int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group;
-    const int64_t at = int64_t(split) * c.total_q * qh + row;
+    const int64_t at = (int64_t(split) * a.part_rows + part_row(a, s, b, r / c.group)) * qh + h * c.group + r % c.group;
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
     if (lane == 0 && !JOINED) {
       if (a.splits > 1) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(top, sum);
@@ -392,14 +392,28 @@ static int ctas_per_sm(int d, bool one) {
 //   56 x 4096                 42.4  32.8  27.9   25.9
 //   8 x 8192                  15.8  24.1  41.4   14.0
 //   56 x 30000               176.8 166.3 159.1  132.2
+static int separate_slices(const mp_cache_config* c, bool one, int max_kv) {
+  const int64_t units = int64_t(c->batch) * c->kv_heads, most = (int64_t(max_kv) + 127) / 128;
+  const int64_t fit = int64_t(device_sm_count()) * ctas_per_sm(c->head_dim, one), wave = fit / units, two = 2 * fit / units;
+  const int64_t fill = two * 2048 <= max_kv ? two : wave, s = fill < most ? fill : most;
+  return int(s < 1 ? 1 : s);
+}
 StepPlan chunk_step_plan(const mp_cache_config* c, int max_q, int max_kv) {
   const int64_t rows = int64_t(max_q) * (c->q_heads / c->kv_heads), units = int64_t(c->batch) * c->kv_heads;
   const int64_t most = (int64_t(max_kv) + 127) / 128;
   for (int size = 8; max_kv <= kShort && size > 1; size /= 2)
     if (size < 2 * most && max_kv <= size * kSlice && units <= clusters_at_once(c->head_dim, rows <= 8, size)) return {size, true};
-  const int64_t fit = int64_t(device_sm_count()) * ctas_per_sm(c->head_dim, rows <= 8), wave = fit / units, two = 2 * fit / units;
-  const int64_t fill = two * 2048 <= max_kv ? two : wave, s = fill < most ? fill : most;
-  return {int(s < 1 ? 1 : s), false};
+  return {separate_slices(c, rows <= 8, max_kv), false};
+}
+// (separate_slices only grows with max_kv; caches of up to max_kv slots all join themselves where
+// the longest of them do in fours, or up to two slices' slots in twos)
+int chunk_step_most(const mp_cache_config* c, int max_q, int max_kv) {
+  const bool one = int64_t(max_q) * (c->q_heads / c->kv_heads) <= 8;
+  const int64_t units = int64_t(c->batch) * c->kv_heads;
+  if (max_kv <= kShort && units <= clusters_at_once(c->head_dim, one, 2) &&
+      (max_kv <= 2 * kSlice || units <= clusters_at_once(c->head_dim, one, 4)))
+    return 1;
+  return separate_slices(c, one, max_kv);
 }
 
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st) {

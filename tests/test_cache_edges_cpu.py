@@ -67,3 +67,55 @@ def test_evict_refuses_to_overwrite_what_it_reads(mp):
         assert evict_at(mp, c, c, **good) == mp.MP_ERR_CUDA, good
     for good in (dict(), dict(dkeys=APART["keys"] + size), dict(dlen=APART["kv"])):
         assert evict_at(mp, d, d, **dense, **good) == mp.MP_ERR_CUDA, good
+
+
+# ---- workspaces of the attention ----
+
+def needed(mp, c, total, max_q, max_kv, size):
+    """What a call with a workspace of `size` bytes is answered, short of a launch."""
+    return attend(mp, c, table=FAKE if c.max_pages > 1 else None, total=total, max_q=max_q, max_kv=max_kv, wsn=size)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_workspace_for_the_largest_limits_serves_all_smaller_ones(mp, monkeypatch, dtype):
+    import random
+    monkeypatch.setenv("MP_FAULT_INJECT", "chunk")  # answered after the workspace has been looked at
+    rng = random.Random(7)
+    log = lambda lo, hi: min(hi, max(lo, round(lo * (hi / lo) ** rng.random())))
+    dips = 0
+    for _ in range(400):
+        hk, group = rng.choice((1, 2, 4, 8, 40)), rng.choice((1, 3, 4, 8, 12, 16, 100, 300))
+        ps = 16 * log(1, 4096)
+        c = cfg_of(mp, batch=log(1, 64), kv_heads=hk, q_heads=hk * group, head_dim=rng.choice((64, 128)), page_size=ps, n_pages=64, max_pages=8,
+                   dtype=dtype)
+        max_kv, max_q, total = log(1, 8 * ps), log(1, 3000), log(1, 5000)
+        size = mp.mp_chunk_workspace_bytes(c, total, max_q, max_kv)
+        for _ in range(30):
+            t, q, n = log(1, total), log(1, max_q), log(1, max_kv)
+            own = mp.mp_chunk_workspace_bytes(c, t, q, n)
+            assert own <= size
+            assert needed(mp, c, t, q, n, size) == mp.MP_ERR_INJECTED, (t, q, n)
+            dips += size > 0 and needed(mp, c, total, max_q, max_kv, 0) == mp.MP_ERR_INJECTED and needed(mp, c, t, q, n, 0) == mp.MP_ERR_SCRATCH
+        for t, q, n in ((total, 1, max_kv), (total, max_q, max(1, max_kv // 8)), (min(total, 3), 1, min(max_kv, 300)), (total, 1, 1)):
+            assert needed(mp, c, t, q, n, size) == mp.MP_ERR_INJECTED, (t, q, n)
+    assert dips  # calls that need a workspace below a call that needs none
+
+
+def test_a_workspace_that_is_too_small_or_astray_is_refused(mp, monkeypatch):
+    c = cfg_of(mp, page_size=4096)  # 5000 slots in 40 slices of a token each of 8 heads, for 2 tokens
+    need = 40 * 2 * 8 * 128 * 4 + 40 * 2 * 8 * 8
+    monkeypatch.setenv("MP_FAULT_INJECT", "chunk")
+    call = lambda **kw: attend(mp, c, total=2, max_q=1, max_kv=5000, **kw)
+    assert call(wsn=need) == mp.MP_ERR_INJECTED
+    assert call(wsn=need - 1) == mp.MP_ERR_SCRATCH
+    assert call(ws=None) == mp.MP_ERR_INVALID_ARG
+    assert call(ws=FAKE + 16) == mp.MP_ERR_INVALID_ARG
+    # rows of no sequence need no place, however many there are
+    assert attend(mp, c, total=2000, max_q=1, max_kv=5000, wsn=need) == mp.MP_ERR_INJECTED
+    # fp32 and the large tiles, by the size that the library names
+    for kw, limits in ((dict(dtype="f32"), (6, 4, 512)), (dict(), (60, 40, 512))):
+        d = cfg_of(mp, **kw)
+        size = mp.mp_chunk_workspace_bytes(d, *limits)
+        ask = lambda **k: attend(mp, d, total=limits[0], max_q=limits[1], max_kv=limits[2], **k)
+        assert size > 0 and ask(wsn=size) == mp.MP_ERR_INJECTED
+        assert ask(wsn=0) == mp.MP_ERR_SCRATCH and ask(ws=None) == mp.MP_ERR_INVALID_ARG and ask(ws=FAKE + 128) == mp.MP_ERR_INVALID_ARG

@@ -205,6 +205,37 @@ def test_few_rows_keep_their_weights_exact(mp, hq, hk, d, page, q_lens, kv):
     assert ((lse.double() - z).abs() <= ztol).all()
 
 
+# ---- workspaces ----
+
+@pytest.mark.parametrize("dtype,hq,hk,page,total,max_q,max_kv", [
+    ("bf16", 8, 2, 0, 90, 30, 4000), ("bf16", 8, 2, 64, 9, 3, 20000), ("f32", 8, 2, 64, 200, 70, 6000)])
+def test_a_workspace_sized_for_the_largest_call_serves_smaller_ones(mp, dtype, hq, hk, page, total, max_q, max_kv):
+    """One workspace for a serving loop's limits, and calls below them: other lengths, fewer rows,
+    rows that belong to no sequence, each followed by a guard that nothing may touch."""
+    d = 64
+    lens = [max_kv, max_kv // 3, max_kv // 7]
+    c = Cache(mp, dtype, hq, hk, d, page, lens)
+    size = mp.mp_chunk_workspace_bytes(c.cfg, total, max_q, max_kv)
+    buf = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    ws = buf[:size]
+    for m, n, rows in ((max_q, max_kv, total), (1, max_kv, 3), (1, max_kv, total), (2, max_kv // 2, 7), (1, 700, 3), (1, 300, 5), (2, 130, 6),
+                       (max_q, 1000, total), (max_q // 2 + 1, 300, total), (1, 1, 3)):
+        kv = [min(x, n) for x in lens]
+        q_lens = [min(m, x) for x in kv]
+        c.kv = kv
+        c.kv_len.copy_(torch.tensor(kv, dtype=torch.int32))
+        cu, cu_t = offsets(q_lens)
+        if cu[-1] > rows:
+            q_lens = [1, 1, 1]
+            cu, cu_t = offsets(q_lens)
+        q = c.randn(rows, hq, d, by=1.5)
+        out, lse = attend(mp, c, q, cu_t, m, max_kv=n, workspace=ws)
+        from test_gpu_cache import check_attention
+        check_attention(c, dtype, q, cu, out, lse)
+        assert (buf[size:] == 0xA5).all()
+    assert c.status.item() == 0
+
+
 # ---- eviction in place ----
 
 def test_eviction_may_write_the_new_lengths_over_the_old(mp):
