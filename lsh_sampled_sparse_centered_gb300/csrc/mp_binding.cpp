@@ -90,6 +90,18 @@ class Args {
     }
     return t.data_ptr();
   }
+  // the same of a tensor whose first dimension counts `rows` rows of `width` elements: with more
+  // elements (a leading dimension of one, say) the rows behind would be left out unnoticed
+  void* rows_of(const char* name, at::ScalarType type, int64_t rows, int64_t width) {
+    void* p = dense(name, type, rows * width);
+    const at::Tensor& t = THPVariable_Unpack(a_[i_ - 1]);
+    if (t.numel() != rows * width) {
+      PyErr_Format(PyExc_ValueError, "%s has %lld elements, %lld rows of the call take %lld", name, (long long)t.numel(), (long long)rows,
+                   (long long)(rows * width));
+      throw Refused();
+    }
+    return p;
+  }
   // address and row stride of a [rows, heads, d] tensor whose rows may lie apart
   void* rows(const char* name, at::ScalarType type, int64_t rows, int64_t heads, int64_t d, int64_t* stride) {
     const at::Tensor& t = checked(a_[i_++], name, type);
@@ -178,7 +190,7 @@ int attend(Args a) {
   const auto cfg = a.structure<mp_cache_config>("config");
   const auto t = type_of(cfg);
   const int64_t rows = a.first("q").dim() ? a.first("q").size(0) : 0, width = int64_t(cfg.q_heads) * cfg.head_dim;
-  const void* q = a.dense("q", t, rows * width);
+  const void* q = a.rows_of("q", t, rows, width);
   const void* cu_q = a.dense("cu_q", at::kInt, int64_t(cfg.batch) + 1);
   const void* kv_len = a.dense("kv_len", at::kInt, cfg.batch);
   const int32_t max_q = a.number("max_q"), max_kv = a.number("max_kv");
@@ -199,7 +211,7 @@ int weights(Args a) {
   const auto cfg = a.structure<mp_cache_config>("config");
   const auto t = type_of(cfg);
   const int64_t rows = a.first("q").dim() ? a.first("q").size(0) : 0;
-  const void* q = a.dense("q", t, rows * cfg.q_heads * cfg.head_dim);
+  const void* q = a.rows_of("q", t, rows, int64_t(cfg.q_heads) * cfg.head_dim);
   const void* lse = a.dense("lse", at::kFloat, rows * cfg.q_heads);
   const void* cu_q = a.dense("cu_q", at::kInt, int64_t(cfg.batch) + 1);
   const void* kv_len = a.dense("kv_len", at::kInt, cfg.batch);

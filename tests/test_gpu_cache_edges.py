@@ -163,6 +163,28 @@ def test_append_of_more_rows_than_the_call_has(mp):
     assert (pool_rows(c.keys, c, 0, 0, 48)[:39] == 5.0).all() and (pool_rows(c.keys, c, 0, 0, 48)[45:] == 5.0).all()
 
 
+# ---- the binding: tensors that are not what the call takes ----
+
+def test_queries_of_another_shape_are_refused(mp):
+    """A leading dimension of one would pass for one row: the other tokens would be left out."""
+    c = Cache(mp, "bf16", 8, 2, 128, 64, [300])
+    _, cu_t = offsets([20])
+    q = c.randn(20, 8, 128)
+    out, lse = torch.full_like(q, 77.0), torch.zeros(20, 8, device=DEV)
+    ws = torch.empty(max(1, mp.mp_chunk_workspace_bytes(c.cfg, 20, 20, 300)), dtype=torch.uint8, device=DEV)
+    sc = torch.zeros(1, 2, c.ps * c.cols, device=DEV)
+    for bad in (q[None], q.view(4, 5, 8, 128), q.view(2, 10 * 8, 128), q.flatten()):
+        with pytest.raises(ValueError):
+            mp.mp_chunk_attention(c.cfg, bad, cu_t, c.kv_len, 20, 300, c.keys, c.values, c.table, out, lse, ws, c.status)
+        with pytest.raises(ValueError):
+            mp.mp_cache_weights(c.cfg, bad, lse, cu_t, c.kv_len, 20, 300, c.keys, c.table, sc, c.status)
+    assert (out == 77.0).all() and not sc.any()
+    a, _ = attend(mp, c, q, cu_t, 20)
+    b = torch.empty_like(q)
+    mp.mp_chunk_attention(c.cfg, q.flatten(1), cu_t, c.kv_len, 20, 300, c.keys, c.values, c.table, b, None, ws, c.status)
+    assert torch.equal(a, b)
+
+
 # ---- few rows: 9 to 16 per KV head ----
 
 FEW = [
