@@ -160,6 +160,17 @@ at::ScalarType type_of(const mp_cache_config& c) {
 }
 int64_t pool_of(const mp_cache_config& c) { return int64_t(c.n_pages) * c.kv_heads * c.page_size * c.head_dim; }
 
+// The library call lets other threads have the interpreter: a launch waits where the device's queue
+// is full. (The caller's references hold the tensors meanwhile.)
+template <typename F>
+int unlocked(F f) {
+  struct Release {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Release() { PyEval_RestoreThread(state); }
+  } release;
+  return f();
+}
+
 int append(Args a) {
   const auto cfg = a.structure<mp_cache_config>("config");
   const auto rotary = a.structure<mp_rotary>("rotary");
@@ -180,10 +191,13 @@ int append(Args a) {
   const void* table = a.dense("page_table", at::kInt, int64_t(cfg.batch) * cfg.max_pages, true);
   void* q_out = a.dense("q_out", t, rows * cfg.q_heads * d);
   void* status = a.dense("status", at::kInt, 1, true);
-  return g_append(&cfg, &rotary, q, qs, k, ks, v, vs, q_norm, k_norm, static_cast<const double*>(inv_freq),
-                  static_cast<const int32_t*>(positions), static_cast<const int32_t*>(cu_q),
-                  static_cast<const int32_t*>(kv_len), int32_t(rows), keys, values, static_cast<const int32_t*>(table), q_out,
-                  static_cast<uint32_t*>(status), a.stream());
+  void* stream = a.stream();
+  return unlocked([&] {
+    return g_append(&cfg, &rotary, q, qs, k, ks, v, vs, q_norm, k_norm, static_cast<const double*>(inv_freq),
+                    static_cast<const int32_t*>(positions), static_cast<const int32_t*>(cu_q),
+                    static_cast<const int32_t*>(kv_len), int32_t(rows), keys, values, static_cast<const int32_t*>(table), q_out,
+                    static_cast<uint32_t*>(status), stream);
+  });
 }
 
 int attend(Args a) {
@@ -202,9 +216,12 @@ int attend(Args a) {
   void* workspace = a.dense("workspace", at::kByte, 0, true);
   const size_t bytes = a.bytes_of_last();
   void* status = a.dense("status", at::kInt, 1, true);
-  return g_attend(&cfg, q, static_cast<const int32_t*>(cu_q), static_cast<const int32_t*>(kv_len), int32_t(rows), max_q, max_kv,
-                  keys, values, static_cast<const int32_t*>(table), out, static_cast<float*>(lse), workspace, bytes,
-                  static_cast<uint32_t*>(status), a.stream());
+  void* stream = a.stream();
+  return unlocked([&] {
+    return g_attend(&cfg, q, static_cast<const int32_t*>(cu_q), static_cast<const int32_t*>(kv_len), int32_t(rows), max_q, max_kv,
+                    keys, values, static_cast<const int32_t*>(table), out, static_cast<float*>(lse), workspace, bytes,
+                    static_cast<uint32_t*>(status), stream);
+  });
 }
 
 int weights(Args a) {
@@ -220,9 +237,12 @@ int weights(Args a) {
   const void* table = a.dense("page_table", at::kInt, int64_t(cfg.batch) * cfg.max_pages, true);
   void* scores = a.dense("scores", at::kFloat, int64_t(cfg.batch) * cfg.kv_heads * cfg.max_pages * cfg.page_size);
   void* status = a.dense("status", at::kInt, 1, true);
-  return g_weights(&cfg, q, static_cast<const float*>(lse), static_cast<const int32_t*>(cu_q),
-                   static_cast<const int32_t*>(kv_len), int32_t(rows), max_q, max_kv, keys, static_cast<const int32_t*>(table),
-                   static_cast<float*>(scores), static_cast<uint32_t*>(status), a.stream());
+  void* stream = a.stream();
+  return unlocked([&] {
+    return g_weights(&cfg, q, static_cast<const float*>(lse), static_cast<const int32_t*>(cu_q),
+                     static_cast<const int32_t*>(kv_len), int32_t(rows), max_q, max_kv, keys, static_cast<const int32_t*>(table),
+                     static_cast<float*>(scores), static_cast<uint32_t*>(status), stream);
+  });
 }
 
 int evict(Args a) {
@@ -246,10 +266,13 @@ int evict(Args a) {
   void* workspace = a.dense("workspace", at::kByte, 0);
   const size_t bytes = a.bytes_of_last();
   void* status = a.dense("status", at::kInt, 1, true);
-  return g_evict(&cfg, &dst, keys, values, static_cast<const int32_t*>(table), static_cast<const int32_t*>(kv_len), max_kv,
-                 static_cast<const float*>(scores), n_sink, window, budget, dst_keys, dst_values,
-                 static_cast<const int32_t*>(dst_table), static_cast<float*>(dst_scores), static_cast<int32_t*>(dst_len),
-                 static_cast<int32_t*>(kept), workspace, bytes, static_cast<uint32_t*>(status), a.stream());
+  void* stream = a.stream();
+  return unlocked([&] {
+    return g_evict(&cfg, &dst, keys, values, static_cast<const int32_t*>(table), static_cast<const int32_t*>(kv_len), max_kv,
+                   static_cast<const float*>(scores), n_sink, window, budget, dst_keys, dst_values,
+                   static_cast<const int32_t*>(dst_table), static_cast<float*>(dst_scores), static_cast<int32_t*>(dst_len),
+                   static_cast<int32_t*>(kept), workspace, bytes, static_cast<uint32_t*>(status), stream);
+  });
 }
 
 // METH_FASTCALL entry: the library's return code, or a Python exception

@@ -25,6 +25,8 @@
 // All waits are bounded: on expiry the kernel records MP_STATUS_WAIT_TIMEOUT and stops.
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "mp_tc.cuh"
 
 namespace mp {
@@ -530,14 +532,15 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
 }  // namespace
 
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> kept{nullptr};  // host threads may ask at once
+  PFN_cuTensorMapEncodeTiled_v12000 fn = kept.load(std::memory_order_relaxed);
   if (!fn) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
             cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+      kept.store(fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p), std::memory_order_relaxed);
   }
   return fn;
 }

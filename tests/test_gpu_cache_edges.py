@@ -276,3 +276,55 @@ def test_eviction_may_write_the_new_lengths_over_the_old(mp):
             for h in range(8):
                 at = torch.tensor(R.keep(sc[b, h], n, 4, 16, 500), dtype=torch.int64, device=DEV)
                 assert torch.equal(t.keys[b, h, :len(at)], c.keys[b, h][at]) and torch.equal(t.values[b, h, :len(at)], c.values[b, h][at])
+
+
+# ---- other threads run while a call is in the library ----
+
+def test_calls_leave_the_interpreter_to_other_threads(mp, tmp_path):
+    """A launch can wait for room in the device's queue. Stood in for by a library call that
+    sleeps: Python code of another thread has to go on meanwhile."""
+    import ctypes
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src, lib = tmp_path / "slow.c", str(tmp_path / "slow.so")
+    src.write_text("#define _GNU_SOURCE\n#include <unistd.h>\nint slow(void) { usleep(400000); return 0; }\n")
+    subprocess.run([cc, "-shared", "-fPIC", str(src), "-o", lib], check=True)
+    slow = ctypes.cast(ctypes.CDLL(lib).slow, ctypes.c_void_p).value
+    calls = mp._cache_calls()
+    real = [ctypes.cast(getattr(mp._lib, f), ctypes.c_void_p).value
+            for f in ("mp_cache_append", "mp_chunk_attention", "mp_cache_weights", "mp_cache_evict")]
+    c = Cache(mp, "bf16", 2, 1, 64, 16, [20])
+    _, cu_t = offsets([1])
+    q, k = c.randn(1, 2, 64), c.randn(1, 1, 64)
+    lse, sc = torch.zeros(1, 2, device=DEV), torch.zeros(1, 1, c.ps * c.cols, device=DEV)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=DEV)
+    dlen = torch.zeros(1, dtype=torch.int32, device=DEV)
+    four = [
+        lambda: mp.mp_cache_append(c.cfg, mp.make_rotary(rot_dim=0), q, k, k, None, None, None, None, cu_t, c.kv_len, c.keys, c.values, c.table,
+                                   q.clone(), c.status),
+        lambda: mp.mp_chunk_attention(c.cfg, q, cu_t, c.kv_len, 1, 20, c.keys, c.values, c.table, q.clone(), lse, ws, c.status),
+        lambda: mp.mp_cache_weights(c.cfg, q, lse, cu_t, c.kv_len, 1, 20, c.keys, c.table, sc, c.status),
+        lambda: mp.mp_cache_evict(c.cfg, c.cfg, c.keys, c.values, c.table, c.kv_len, 20, sc, 0, 0, 4, c.keys, c.values, c.table, None, dlen, None,
+                                  ws, c.status)]
+    calls.bind(*[slow] * 4)
+    try:
+        for call in four:
+            ticks, stop = [], threading.Event()
+
+            def tick():
+                while not stop.is_set():
+                    ticks.append(time.perf_counter())
+                    time.sleep(0.005)
+
+            th = threading.Thread(target=tick)
+            th.start()
+            t0 = time.perf_counter()
+            call()
+            t1 = time.perf_counter()
+            stop.set()
+            th.join()
+            assert t1 - t0 >= 0.35
+            assert sum(t0 + 0.05 < t < t1 - 0.05 for t in ticks) >= 5
+    finally:
+        calls.bind(*real)
