@@ -260,10 +260,13 @@ def _cache_calls():
     import importlib.machinery
     import importlib.util
 
-    import torch  # noqa: F401  (its libraries are the extension's)
-    path = os.path.join(_PKG, "_lib", "_mp_calls.so")
+    import torch  # its libraries are the extension's, and its version names it
+
+    from .build import calls_path
+    path = calls_path(str(torch.__version__))
     if not os.path.exists(path):
-        raise ImportError(f"_mp_calls.so is not built ({path}); run `python lsh_sampled_sparse_centered_gb300/build.py`")
+        raise ImportError(f"the cache operators' calls are not built for this PyTorch ({path}); "
+                          "run `python lsh_sampled_sparse_centered_gb300/build.py`")
     loader = importlib.machinery.ExtensionFileLoader("_mp_calls", path)
     mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mp_calls", loader))
     loader.exec_module(mod)

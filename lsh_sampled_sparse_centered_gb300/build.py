@@ -6,14 +6,16 @@ __graft_entry__.build(). The translation units compile in parallel; the shared l
 links the CUDA runtime dynamically with an rpath to the toolkit's lib64. --check builds
 the bounds-checking library libmagicpig_check.so (MP_CHECK=1: kernels test every index
 that comes from data before using it and report failures in the status word), which the
-binding loads instead when MP_BOUNDS_CHECK=1 is set. Beside them g++ builds _mp_calls.so,
-the binding of the cache operators, against the installed PyTorch's headers.
+binding loads instead when MP_BOUNDS_CHECK=1 is set. Beside them g++ builds the binding of the
+cache operators (_mp_calls-*.so, one per interpreter and PyTorch version) against the installed
+PyTorch's headers, where there is one.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -25,7 +27,6 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmagicpig.so")
 LIB_CHECK = os.path.join(OUT_DIR, "libmagicpig_check.so")
-CALLS = os.path.join(OUT_DIR, "_mp_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,13 +45,41 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def calls_path(torch_version: str) -> str:
+    """The Python calls' extension for this interpreter and that PyTorch. It uses PyTorch's inline
+    C++, so one that was built for another version would misread tensors: the name tells them apart."""
+    return os.path.join(OUT_DIR, f"_mp_calls-{sysconfig.get_config_var('SOABI')}-torch{torch_version}.so")
+
+
+def installed_torch() -> tuple[str, str] | None:
+    """Folder and version of a PyTorch with CUDA, without importing it; None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    root = spec.submodule_search_locations[0]
+    try:
+        with open(os.path.join(root, "version.py")) as f:
+            version = re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M)
+    except OSError:
+        return None
+    if version is None or not os.path.exists(os.path.join(root, "lib", "libc10_cuda.so")):
+        return None
+    return root, version.group(1)
+
+
 def build_calls(nvcc: str, force: bool = False) -> None:
-    """Compile the Python calls of the cache operators (csrc/mp_binding.cpp)."""
-    src, header = os.path.join(CSRC, "mp_binding.cpp"), os.path.join(ROOT, "include", "magicpig.h")
-    if not force and os.path.exists(CALLS) and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in (src, header)):
+    """Compile the Python calls of the cache operators (csrc/mp_binding.cpp). The C library stands
+    without them, and without PyTorch there is nobody to make them."""
+    found = installed_torch()
+    if found is None:
+        sys.stderr.write("no PyTorch with CUDA found: libmagicpig.so is built without the Python calls of the cache operators\n")
         return
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
-    tmp = CALLS + ".tmp"
+    torch, version = found
+    src, header, out = os.path.join(CSRC, "mp_binding.cpp"), os.path.join(ROOT, "include", "magicpig.h"), calls_path(version)
+    deps = (src, header, os.path.abspath(__file__))
+    if not force and os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps):
+        return
+    tmp = out + ".tmp"
     cmd = ["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden", src, "-o", tmp,
            "-I" + os.path.join(ROOT, "include"), "-I" + sysconfig.get_paths()["include"],
            "-I" + os.path.join(os.path.dirname(_cuda_lib64(nvcc)), "include"),
@@ -60,7 +89,7 @@ def build_calls(nvcc: str, force: bool = False) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    os.replace(tmp, out)
 
 
 def build(verbose: bool = False, force: bool = False, check: bool = False) -> str:

@@ -119,3 +119,51 @@ def test_a_workspace_that_is_too_small_or_astray_is_refused(mp, monkeypatch):
         ask = lambda **k: attend(mp, d, total=limits[0], max_q=limits[1], max_kv=limits[2], **k)
         assert size > 0 and ask(wsn=size) == mp.MP_ERR_INJECTED
         assert ask(wsn=0) == mp.MP_ERR_SCRATCH and ask(ws=None) == mp.MP_ERR_INVALID_ARG and ask(ws=FAKE + 128) == mp.MP_ERR_INVALID_ARG
+
+
+# ---- the binding's build ----
+
+def test_the_python_calls_are_of_one_interpreter_and_pytorch(mp, monkeypatch):
+    """The extension uses PyTorch's inline C++: one of another version must not be loaded."""
+    import torch
+    import __graft_entry__
+    b = __graft_entry__._builder()
+    root, version = b.installed_torch()
+    assert version == str(torch.__version__) and os.path.samefile(root, os.path.dirname(torch.__file__))
+    assert os.path.exists(b.calls_path(version)) and mp._cache_calls() is not None
+    monkeypatch.setattr(torch, "__version__", "1.0.0+other")
+    with pytest.raises(ImportError, match="1.0.0"):
+        mp._cache_calls()
+    monkeypatch.undo()
+    import sysconfig
+    real = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-99-none" if n == "SOABI" else real(n))
+    with pytest.raises(ImportError, match="cpython-99-none"):
+        mp._cache_calls()
+
+
+def test_the_library_builds_without_pytorch(mp, monkeypatch, capfd):
+    """A user of the C library alone needs no PyTorch."""
+    import importlib.util
+    import __graft_entry__
+    b = __graft_entry__._builder()
+    real = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else real(name, *a))
+    assert b.build() == mp.LIB_PATH
+    assert "without the Python calls" in capfd.readouterr().err
+
+
+def test_a_change_of_the_build_or_the_header_rebuilds_the_python_calls(mp, monkeypatch, tmp_path):
+    import __graft_entry__
+    b = __graft_entry__._builder()
+    out = b.calls_path(b.installed_torch()[1])
+    ran = []
+    monkeypatch.setattr(b.subprocess, "run", lambda cmd, **kw: ran.append(cmd) or subprocess.CompletedProcess(cmd, 1, "", "stopped"))
+    b.build_calls(b._nvcc())
+    assert not ran
+    real = os.path.getmtime
+    for changed in ("build.py", "magicpig.h", "mp_binding.cpp"):
+        monkeypatch.setattr(os.path, "getmtime", lambda p: real(out) + 1 if os.path.basename(p) == changed else real(p))
+        with pytest.raises(RuntimeError, match="stopped"):
+            b.build_calls(b._nvcc())
+    assert len(ran) == 3
