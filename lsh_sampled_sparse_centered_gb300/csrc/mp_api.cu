@@ -198,7 +198,9 @@ static DecodePtrs decode_ptrs(const Geometry& g, void* base) {
 }
 
 // MP_FAULT_INJECT=build|append|decode|chunk|weights|evict|all makes the named calls fail before any
-// launch (host-side fault injection for error-path tests).
+// launch (host-side fault injection for error-path tests). In the bounds-checking build
+// chunk_wait|weights_wait stop one CTA of the tensor-core kernels, so that the others' bounded
+// waits run out.
 bool injected(const char* what) {
   const char* e = std::getenv("MP_FAULT_INJECT");
   if (!e || !*e) return false;

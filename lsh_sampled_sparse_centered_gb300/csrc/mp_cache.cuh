@@ -31,6 +31,9 @@ struct ChunkArgs {
   float* part;  // [..][d]: unnormalised sums
   float* ml;    // [..][2]: their reference (log2) and sum
   void* cuts;   // shared tiles (tensor cores)
+#if MP_CHECK
+  bool stall;  // one CTA stops half way, so that the others' waits run out
+#endif
 };
 
 struct WeightsArgs {
@@ -38,6 +41,9 @@ struct WeightsArgs {
   const void *q, *keys;
   const float* lse;
   float* scores;
+#if MP_CHECK
+  bool stall;
+#endif
 };
 
 struct AppendArgs {

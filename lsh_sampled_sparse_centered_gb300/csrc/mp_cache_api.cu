@@ -258,6 +258,9 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
   a.joined = false;
   a.part_rows = part_rows(cfg, total_q, a.c.max_q);
   a.part = a.ml = nullptr;
+#if MP_CHECK
+  a.stall = injected("chunk_wait");
+#endif
   a.cuts = nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
@@ -306,6 +309,9 @@ int mp_cache_weights(const mp_cache_config* cfg, const void* q, const float* lse
   a.keys = keys;
   a.lse = lse;
   a.scores = scores;
+#if MP_CHECK
+  a.stall = injected("weights_wait");
+#endif
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
   ProfScope ps(st, K_CACHE_WEIGHTS);

@@ -77,6 +77,7 @@ struct Smem {
   Seq first;     // that sequence
   int longest[12];  // steps of a tile, of each warp's sequences
   uint8_t filled[kStages];  // phase in which each tile of the ring was last filled (1: never)
+                            // by a copy whose barrier is full, or patched
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -131,6 +132,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = saddr(smraw);
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(smraw + ((1024 - (base & 1023)) & 1023));
   constexpr int kSub = Smem<D>::kSub, kStages = Smem<D>::kStages;
+  // 128-byte swizzle: copies and products take the tiles from 1024-byte boundaries (members in
+  // front of them would move them off, and the copies then fault)
+  static_assert(offsetof(Smem<D>, q) % 1024 == 0 && offsetof(Smem<D>, kv) % 1024 == 0 && sizeof(S.q[0][0]) % 1024 == 0 &&
+                sizeof(S.kv[0][0]) % 1024 == 0);
   constexpr uint32_t kRowBytes = 128;
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t* bar = patch ? &S.tail : &S.full[st];
             if (lane == 0) {
               mbar_expect_tx(bar, uint32_t(boxes) * box * kRowBytes * kSub);
-              S.filled[st] = uint8_t(ph);
+              if (!patch) S.filled[st] = uint8_t(ph);
             }
             __syncwarp();
             if (lane < boxes) {
@@ -411,7 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (patch) {
               ok = __all_sync(0xffffffffu, mbar_wait(&S.tail, tails & 1, abort));
-              if (!ok) break;
+              if (!ok) {
+                if (lane == 0) mbar_drain(&S.tail, tails & 1);  // this copy is nobody else's to wait for
+                break;
+              }
               ++tails;
               const uint4 z = make_uint4(0, 0, 0, 0);
               for (int s = 0; s < kSub; ++s) {
@@ -420,7 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               fence_async();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&S.full[st]);
+              if (lane == 0) {
+                S.filled[st] = uint8_t(ph);
+                mbar_arrive(&S.full[st]);
+              }
             }
             if (++st == kStages) {
               st = 0;
@@ -688,6 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             fence_before();
             __syncwarp();
+#if MP_CHECK
+            if (a.stall && blockIdx.x == 0 && half == 0 && j == 1) return;  // never handed over: the waits run out
+#endif
             if (lane == 0) mbar_arrive(&S.p_full[half][part]);
           };
           weigh(x0, 0);

@@ -66,6 +66,7 @@ struct WSmem {
   int64_t past[kGroup];  // key blocks of a KV head, up to and with each sequence
   Seq seqs[kGroup];
   uint32_t loaded[3];    // phase of the last keys; the ring's next place and its phase
+  uint32_t steps[2];     // of the ring: loads issued, z given
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -110,6 +111,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t base = saddr(smraw);
   WSmem<D>& S = *reinterpret_cast<WSmem<D>*>(smraw + ((1024 - (base & 1023)) & 1023));
   constexpr int kSub = WSmem<D>::kSub, kStages = WSmem<D>::kStages;
+  // 128-byte swizzle: tiles from 1024-byte boundaries, 32-byte swizzle: from 256-byte ones
+  static_assert(offsetof(WSmem<D>, k) % 1024 == 0 && offsetof(WSmem<D>, q) % 1024 == 0 && sizeof(S.k[0][0]) % 1024 == 0 &&
+                sizeof(S.q[0][0]) % 1024 == 0 && offsetof(WSmem<D>, z) % 256 == 0 && offsetof(WSmem<D>, ones) % 256 == 0 &&
+                sizeof(S.z[0]) % 256 == 0);
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
   volatile uint32_t* abort = &S.abort;
@@ -191,7 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int64_t blocks = all * c.kvh;
     bool ok = true;
     int st = 0;
-    uint32_t ph = 1, items = 0, keys = 0;
+    uint32_t ph = 1, items = 0, keys = 0, issued = 0;
     // The pairs of CTAs take blocks of keys in turn and their CTAs every other one of these. Where
     // that leaves a last one over, they share it, half of the rows each: the second CTA first
     // of all, the first at its end, so that it finds the other's sums there.
@@ -267,6 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_load_3d(&S.q[st][u][0], &tmQ, u * 64, it.h * c.group + x.h0, it.s.row0 + x.t0, &S.q_full[st]);
         }
         __syncwarp();
+        ++issued;
         if (++st == kStages) {
           st = 0;
           ph ^= 1;
@@ -277,6 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       S.loaded[0] = (keys & 1) ^ 1;
       S.loaded[1] = st;
       S.loaded[2] = ph;
+      S.steps[0] = issued;
     }
   } else if (warp == 18) {
     // ---------------- -z of the rows, the next step's loads in flight ----------------
@@ -291,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const float root = sqrtf(float(D));
     bool ok = true;
     int st = 0;
-    uint32_t ph = 1;
+    uint32_t ph = 1, given = 0;
     for (uint32_t n = 0; ok; ++n) {
       ok = __all_sync(0xffffffffu, mbar_wait(&S.item_full[n & 1], (n >> 1) & 1, abort));
       if (!ok) break;
@@ -324,6 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.q_full[st]);
+        ++given;
         if (++st == kStages) {
           st = 0;
           ph ^= 1;
@@ -331,6 +339,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       load_z(0, z0);
       for (int j = 0; j < it.steps && ok; j += 2) {
+#if MP_CHECK
+        if (a.stall && blockIdx.x == 0 && given == 2) {  // z is given no more: the waits run out
+          ok = false;
+          break;
+        }
+#endif
         load_z(j + 1, z1);
         put(z0);
         if (j + 1 >= it.steps || !ok) break;
@@ -338,6 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         put(z1);
       }
     }
+    if (lane == 0) S.steps[1] = given;
   } else if (warp >= 16) {
     // ---------------- products S[key][row]: warp 17 for the first half of the keys, 19 for the
     // second, so that one's products run while the other waits ----------------
@@ -531,6 +546,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0 && S.abort) {
     mbar_drain(&S.k_full, S.loaded[0]);
+    // a load whose z was not given completes its barrier with this
+    for (uint32_t i = S.steps[1]; i < S.steps[0]; ++i) mbar_arrive(&S.q_full[i % kStages]);
     for (int i = 0; i < kStages; ++i) mbar_drain(&S.q_full[i], i < int(S.loaded[1]) ? S.loaded[2] ^ 1 : S.loaded[2]);
     flag(c.status, MP_STATUS_WAIT_TIMEOUT);
   }
