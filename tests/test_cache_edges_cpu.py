@@ -4,7 +4,6 @@ import ctypes
 import os
 import shutil
 import subprocess
-import sys
 
 import pytest
 
@@ -167,3 +166,24 @@ def test_a_change_of_the_build_or_the_header_rebuilds_the_python_calls(mp, monke
         with pytest.raises(RuntimeError, match="stopped"):
             b.build_calls(b._nvcc())
     assert len(ran) == 3
+
+
+def test_a_c_caller_of_the_cache_operators(mp, tmp_path):
+    """The header's structures, codes and sizes are those of the binding, compiled as C99 without a warning."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    libdir, exe = os.path.dirname(mp.LIB_PATH), str(tmp_path / "cache_abi_from_c")
+    subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"),
+                    os.path.join(ROOT, "tests", "cache_abi_from_c.c"), "-L", libdir, "-lmagicpig", "-Wl,-rpath," + libdir, "-o", exe], check=True)
+    env = {k: v for k, v in os.environ.items() if k != "MP_FAULT_INJECT"}
+    out = subprocess.run([exe], check=True, capture_output=True, text=True, env=env).stdout
+    got = dict(line.split(" ", 1) for line in out.strip().splitlines())
+    c = cfg_of(mp, page_size=4096)
+    want = dict(sizeof_cache_config=ctypes.sizeof(mp.mp_cache_config), offset_dtype=mp.mp_cache_config.dtype.offset,
+                sizeof_rotary=ctypes.sizeof(mp.mp_rotary), offset_eps=mp.mp_rotary.eps.offset, check_ok=mp.MP_OK,
+                check_null=mp.MP_ERR_INVALID_ARG, chunk_bytes_rc=mp.MP_OK, chunk_bytes=mp.mp_chunk_workspace_bytes(c, 2, 1, 5000),
+                evict_bytes_rc=mp.MP_OK, evict_bytes=mp.mp_evict_workspace_bytes(c, 5000, 100), append_rotary=mp.MP_ERR_INVALID_ARG,
+                append_empty=mp.MP_OK, attention_scratch=mp.MP_ERR_SCRATCH, weights_capacity=mp.MP_ERR_CAPACITY,
+                evict_budget=mp.MP_ERR_INVALID_ARG, bits=f"{mp.MP_STATUS_BAD_PAGE} {mp.MP_STATUS_BAD_LENGTH}")
+    assert got == {k: str(v) for k, v in want.items()}
