@@ -328,3 +328,64 @@ def test_calls_leave_the_interpreter_to_other_threads(mp, tmp_path):
             assert sum(t0 + 0.05 < t < t1 - 0.05 for t in ticks) >= 5
     finally:
         calls.bind(*real)
+
+
+# ---- a process whose first call is a captured one ----
+
+FIRST = '''
+import sys
+import torch
+sys.path.insert(0, {root!r})
+import lsh_sampled_sparse_centered_gb300 as mp
+dev, d, hk, hq, n = "cuda:0", {d}, 2, 8, 3000
+dt = {{"bf16": torch.bfloat16, "f32": torch.float32}}[{dtype!r}]
+g = torch.Generator(device=dev).manual_seed(1)
+rnd = lambda *s: torch.randn(*s, generator=g, device=dev).to(dt)
+cfg = mp.make_cache_config(batch=1, kv_heads=hk, q_heads=hq, head_dim=d, page_size={cap}, n_pages=1, dtype={dtype!r})
+dst = mp.make_cache_config(batch=1, kv_heads=hk, q_heads=hq, head_dim=d, page_size=100, n_pages=1, dtype={dtype!r})
+m = {m}
+keys, values = rnd(1, hk, {cap}, d), rnd(1, hk, {cap}, d)
+q, k, v = rnd(m, hq, d), rnd(m, hk, d), rnd(m, hk, d)
+cu = torch.tensor([0, m], dtype=torch.int32, device=dev)
+kv = torch.tensor([{n}], dtype=torch.int32, device=dev)
+inv = torch.ones(d // 2, dtype=torch.float64, device=dev)
+ws = torch.empty(1 << 25, dtype=torch.uint8, device=dev)
+status = torch.zeros(1, dtype=torch.int32, device=dev)
+q_out, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(m, hq, device=dev)
+sc = torch.zeros(1, hk, {cap}, device=dev)
+dk, dv = torch.zeros(1, hk, 100, d, dtype=dt, device=dev), torch.zeros(1, hk, 100, d, dtype=dt, device=dev)
+dlen, kept = torch.zeros(1, dtype=torch.int32, device=dev), torch.zeros(1, hk, 100, dtype=torch.int32, device=dev)
+def step():
+    mp.mp_cache_append(cfg, mp.make_rotary(rot_dim=d), q, k, v, None, None, inv, None, cu, kv, keys, values, None, q_out, status)
+    mp.mp_chunk_attention(cfg, q_out, cu, kv, m, {n}, keys, values, None, out, lse, ws, status)
+    mp.mp_cache_weights(cfg, q_out, lse, cu, kv, m, {n}, keys, None, sc, status)
+    mp.mp_cache_evict(cfg, dst, keys, values, None, kv, {n}, sc, 4, 16, 100, dk, dv, None, None, dlen, kept, ws, status)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (q_out, out, lse, sc, dk, dv, dlen, kept)]
+sc.zero_()
+step()
+torch.cuda.synchronize()
+assert status.item() == 0
+assert all(torch.equal(a, b) for a, b in zip(got, (q_out, out, lse, sc, dk, dv, dlen, kept)))
+print("same")
+'''
+
+
+@pytest.mark.parametrize("dtype,d,m,cap,n", [("bf16", 128, 1, 3000, 2000), ("bf16", 64, 3, 9000, 8000), ("bf16", 128, 50, 3000, 2500),
+                                             ("f32", 64, 5, 3000, 2900)])
+def test_a_first_call_may_be_captured(dtype, d, m, cap, n):
+    """Kernels are loaded and occupancies asked for under the capture; equal bits afterwards."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sys
+    import __graft_entry__
+    __graft_entry__.build()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, dtype=dtype, d=d, m=m, cap=cap, n=n)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), (r.stdout[-500:], r.stderr[-2000:])
