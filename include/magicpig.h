@@ -267,7 +267,10 @@ MP_API int mp_decode_attention_static(const mp_config* cfg, void* tables, const 
  *
  * The sampled attention above reads a cache that something has to fill, layers that are
  * attended exactly need an attention over all of it, and a cache that grows past its
- * budget has to be cut. These calls work on the cache of ONE layer, kept in pages:
+ * budget has to be cut. (mp_build_tables and mp_decode_step take a dense cache whose sequences
+ * have one length: a paged or ragged cache reaches them through mp_cache_evict into a dense
+ * destination, with a budget that no sequence is below.) These calls work on the cache of ONE
+ * layer, kept in pages:
  *   keys, values : [n_pages][kv_heads][page_size][head_dim]   (the pool)
  *   page_table   : int32 [batch][max_pages], the pool's pages of each sequence in order;
  *                  NULL: page b is the whole cache of sequence b (max_pages = 1), so that
@@ -289,7 +292,9 @@ MP_API int mp_decode_attention_static(const mp_config* cfg, void* tables, const 
  * table's capacity) is left out and sets MP_STATUS_BAD_LENGTH: rows behind the first max_q and
  * slots behind max_kv; the other tokens stay in their slots. A page number outside the pool sets
  * MP_STATUS_BAD_PAGE.
- * `status` (device uint32, may be NULL) collects these bits; the caller clears it.
+ * `status` (device uint32, may be NULL) collects these bits; the caller clears it. The waits of
+ * the tensor-core kernels are limited to 2 s (MP_STATUS_WAIT_TIMEOUT: the outputs do not hold);
+ * only a tile of rows that sees more than 10^8 slots works that long.
  * Query head j of a sequence reads KV head j / (q_heads / kv_heads); the softmax scale is
  * 1/sqrt(head_dim). Workspaces are device memory of the caller's, aligned to 256 bytes; they
  * hold nothing between calls and need no initialisation; calls that may overlap on the
@@ -322,8 +327,10 @@ MP_API int mp_cache_config_check(const mp_cache_config* cfg);
  * the cache. For every head x of q and k:
  *   y = x / sqrt(mean(x^2) + eps) * w          (w = q_norm or k_norm; NULL: y = x)
  *   (a, b) -> (a cos t - b sin t, b cos t + a sin t)   t = positions[row] * inv_freq[i],
- * in fp32 with the angle reduced exactly to a fraction of a turn, rounded once. Queries go
- * to q_out, keys to their slots; values are copied to theirs unchanged.
+ * in fp32, rounded once. The angle is reduced to a fraction of a turn in 64-bit fixed point, so
+ * that far positions cost no accuracy beyond inv_freq's own: inv_freq / 2 pi is rounded to a
+ * double (2^-53 of a turn per position), the fraction to 2^-32 of a turn and then to a float.
+ * Queries go to q_out, keys to their slots; values are copied to theirs unchanged.
  *   q, k, v   : device; row r at r * stride elements (strides in elements, multiples of
  *               16 bytes), heads of a row dense: q [total_q][q_heads][d], k and v
  *               [total_q][kv_heads][d]. Slices of one fused projection fit.

@@ -1,10 +1,11 @@
 // Norms and rotation of the new tokens' queries and keys, and the cache write.
 //
 // Per head x of d elements: y = x * rsqrt(mean(x^2) + eps) * w, then the pairs of the
-// first rot elements turn by the angle position * inv_freq. The angle is reduced without
-// rounding: inv_freq / 2 pi is held as a 64-bit fraction of a turn, its product with the
-// integer position modulo 2^64 is the exact fraction of the turn that the angle leaves
-// (error 2^-53 of a turn per position), so far positions cost no more than near ones.
+// first rot elements turn by the angle position * inv_freq. inv_freq / 2 pi, rounded to a double
+// (2^-53 of a turn per position), is held as a 64-bit fraction of a turn; its product with the
+// integer position modulo 2^64 is the fraction of the turn that the angle leaves, without a
+// rounding of its own, so far positions cost no more than near ones. sincospif takes its
+// upper 32 bits as a float.
 //
 // Memory bound: (q_heads + 2 kv_heads) * d values in and out per token. A warp takes whole
 // heads of one token, d * size / 16 lanes with a 16-byte vector each per head. What it does

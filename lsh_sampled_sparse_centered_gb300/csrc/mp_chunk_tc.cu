@@ -22,9 +22,10 @@
 //
 // With d = 128 the halves take turns: one reads its S and weighs three quarters of it, then
 // the other may. Left alone they may fall into step, both in the softmax and then both
-// waiting for products, and stay there (2048 tokens over 32768 slots, 32/8 heads: 700 to 770
-// us by how they started, 670 us with turns; 1024 over 8192: 117 and 104 us). With d = 64,
-// where S is formed ahead, turns cost a quarter (540 against 680 us).
+// waiting for products, and stay there (2048 tokens over 32768 slots, 32/8 heads, short runs: 700
+// to 770 us by how they started, 670 us with turns, 750 in long runs under the power cap; 1024 over
+// 8192: 117 and 104 us). With d = 64, where S is formed ahead, turns cost a quarter (540 against
+// 680 us).
 #include <cudaTypedefs.h>
 
 #include <algorithm>

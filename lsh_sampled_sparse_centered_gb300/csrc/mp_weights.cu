@@ -17,8 +17,9 @@
 // A CTA stays for several blocks of keys and loads the next ones while it works. The CTAs go
 // in clusters of two that share the last block of an odd number, half of the rows each: whole
 // blocks for each CTA alone leave most SMs without work in the last round (512 blocks for 152
-// SMs, 1000 tokens over 16384 slots: 117 us so, 107 us now; over 2048 slots 33 and 25 us; where
-// a CTA has one block at most either way, the search for it costs: 300 over 4096, 19 and 21 us).
+// SMs, 1000 tokens over 16384 slots: 117 us so, 107 us now, 111 among other calls; over 2048 slots
+// 33 and 25 us; where a CTA has one block at most either way, the search for it costs: 300 over
+// 4096, 19 and 21 us).
 // Q loaded once for both by multicast was slower, 35 us a round of 152 blocks against 28.
 //
 // Few rows: k_weights_step, one pass over K from global memory straight into the fragments
