@@ -357,7 +357,7 @@ MP_API int mp_chunk_workspace_bytes(const mp_cache_config* cfg, int32_t total_q,
  * slots up to its own (a prompt's chunk, a few draft tokens, or a single token):
  *   out = softmax(q k / sqrt(d)) v     lse = log sum exp(q k / sqrt(d))
  *   q    : device [total_q][q_heads][d], rotated (mp_cache_append's q_out).
- *   out  : device [total_q][q_heads][d] in dtype.
+ *   out  : device [total_q][q_heads][d] in dtype; overlaps none of the inputs.
  *   lse  : device float [total_q][q_heads], or NULL.
  * A token that sees nothing gets out = 0 and lse = -infinity. Slots at and behind kv_len
  * may hold anything (NaN included); the slots below it are expected to be finite: an

@@ -30,8 +30,8 @@ __host__ __device__ constexpr int warps_of(bool joined) { return joined ? 8 : 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;
-constexpr int kShort = 4096;  // slots of a cache, and of a slice, that a cluster joins itself
-constexpr int kSlice = 1024;
+// Slots of a cache, and of a slice, up to which the slices may be a cluster that joins itself
+constexpr int kShort = 4096, kSlice = 1024;
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 // element e (0..7) of the 16-byte chunks a and b as one pair
@@ -379,7 +379,13 @@ static int ctas_per_sm(int d, bool one) {
 // eight rows, two with more; d = 64: four. One less, d = 64, 98304 slots of 32 KV heads: 143 us
 // instead of 127, one more 137), or two waves where a slice then still has 2048 slots (98304 slots
 // of eight KV heads: 66.8 us in one wave, 71.0 in two; four times that: 222 and 217 us).
-//
+static int separate_slices(const mp_cache_config* c, bool one, int max_kv) {
+  const int64_t units = int64_t(c->batch) * c->kv_heads, most = (int64_t(max_kv) + 127) / 128;
+  const int64_t fit = int64_t(device_sm_count()) * ctas_per_sm(c->head_dim, one), wave = fit / units, two = 2 * fit / units;
+  const int64_t fill = two * 2048 <= max_kv ? two : wave, s = fill < most ? fill : most;
+  return int(s < 1 ? 1 : s);
+}
+
 // Short caches take a cluster of slices that joins itself instead (no second kernel, no
 // workspace), the largest of 8, 4 and 2 whose clusters all run at once: its CTAs have twice the
 // warps and need an SM each (half of one with d = 64 and up to eight rows), and a second round of
@@ -392,12 +398,6 @@ static int ctas_per_sm(int d, bool one) {
 //   56 x 4096                 42.4  32.8  27.9   25.9
 //   8 x 8192                  15.8  24.1  41.4   14.0
 //   56 x 30000               176.8 166.3 159.1  132.2
-static int separate_slices(const mp_cache_config* c, bool one, int max_kv) {
-  const int64_t units = int64_t(c->batch) * c->kv_heads, most = (int64_t(max_kv) + 127) / 128;
-  const int64_t fit = int64_t(device_sm_count()) * ctas_per_sm(c->head_dim, one), wave = fit / units, two = 2 * fit / units;
-  const int64_t fill = two * 2048 <= max_kv ? two : wave, s = fill < most ? fill : most;
-  return int(s < 1 ? 1 : s);
-}
 StepPlan chunk_step_plan(const mp_cache_config* c, int max_q, int max_kv) {
   const int64_t rows = int64_t(max_q) * (c->q_heads / c->kv_heads), units = int64_t(c->batch) * c->kv_heads;
   const int64_t most = (int64_t(max_kv) + 127) / 128;

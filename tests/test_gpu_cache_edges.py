@@ -17,7 +17,7 @@ import pytest
 import torch
 
 import cache_reference as R
-from test_gpu_cache import DEV, DT, HALF, Cache, attend, make_scores, offsets, pool_rows
+from test_gpu_cache import DEV, HALF, Cache, attend, check_attention, make_scores, offsets, pool_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -252,7 +252,6 @@ def test_a_workspace_sized_for_the_largest_call_serves_smaller_ones(mp, dtype, h
             cu, cu_t = offsets(q_lens)
         q = c.randn(rows, hq, d, by=1.5)
         out, lse = attend(mp, c, q, cu_t, m, max_kv=n, workspace=ws)
-        from test_gpu_cache import check_attention
         check_attention(c, dtype, q, cu, out, lse)
         assert (buf[size:] == 0xA5).all()
     assert c.status.item() == 0
