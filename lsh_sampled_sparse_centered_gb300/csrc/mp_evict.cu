@@ -195,18 +195,18 @@ __global__ void __launch_bounds__(kSel, 1) k_evict_select(const EvictArgs a) {
 
 // ROW 16-byte vectors per row, one lane each, kRowsEach rows of K and V per lane so that
 // enough loads are in flight.
-constexpr int kRowsEach = 2;
+constexpr int kRowsEach = 2, kResident = 8;  // CTAs of an SM: 32 registers
 
 template <int ROW>
-__global__ void __launch_bounds__(256) k_evict_gather(const EvictArgs a) {
+__global__ void __launch_bounds__(256, kResident) k_evict_gather(const EvictArgs a) {
   constexpr int GROUPS = 256 / ROW;
   const CacheArgs& c = a.c;
   const int h = blockIdx.y, b = blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // k_evict_select has written the kept slots
   const int m = min(seq_of(c, b).n, a.budget);
   const int j0 = blockIdx.x * (GROUPS * kRowsEach) + threadIdx.x / ROW, e = threadIdx.x % ROW;
-  // here and not by the selection, whose CTAs all read the old length: dst_len may be kv_len (both
-  // lengths give this kernel the same m)
+  // Here and not by the selection, whose CTAs all read the old length: dst_len may be kv_len (both
+  // lengths give this kernel the same m).
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.dst_len[b] = m;
   if (j0 >= m) return;
   const int64_t unit = int64_t(b) * c.kvh + h;
