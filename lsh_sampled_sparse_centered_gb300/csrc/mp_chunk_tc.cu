@@ -78,7 +78,6 @@ struct Smem {
   Seq first;     // that sequence
   int longest[12];  // steps of a tile, of each warp's sequences
   uint8_t filled[kStages];  // phase in which each tile of the ring was last filled (1: never)
-                            // by a copy whose barrier is full, or patched
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -407,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t* bar = patch ? &S.tail : &S.full[st];
             if (lane == 0) {
               mbar_expect_tx(bar, uint32_t(boxes) * box * kRowBytes * kSub);
-              if (!patch) S.filled[st] = uint8_t(ph);
+              S.filled[st] = uint8_t(ph);
             }
             __syncwarp();
             if (lane < boxes) {
@@ -418,7 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (patch) {
               ok = __all_sync(0xffffffffu, mbar_wait(&S.tail, tails & 1, abort));
               if (!ok) {
-                if (lane == 0) mbar_drain(&S.tail, tails & 1);  // this copy is nobody else's to wait for
+                if (lane == 0) {  // this copy is nobody else's to wait for
+                  mbar_drain(&S.tail, tails & 1);
+                  S.filled[st] = uint8_t(ph ^ 1);
+                }
                 break;
               }
               ++tails;
@@ -429,10 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               fence_async();
               __syncwarp();
-              if (lane == 0) {
-                S.filled[st] = uint8_t(ph);
-                mbar_arrive(&S.full[st]);
-              }
+              if (lane == 0) mbar_arrive(&S.full[st]);
             }
             if (++st == kStages) {
               st = 0;
