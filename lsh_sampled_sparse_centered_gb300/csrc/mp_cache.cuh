@@ -23,11 +23,10 @@ struct ChunkArgs {
   const void *q, *keys, *values;
   void* out;
   float* lse;   // may be nullptr
-  // partial results in the workspace: slices [splits][part_rows][q_heads], or (tensor cores)
+  // partial results in the workspace: slices [splits][total_q][q_heads], or (tensor cores)
   // slots of the pieces of tiles that are shared by CTAs
   int splits;   // slices of the keys per row tile
   bool joined;  // the slices are a cluster that joins itself
-  int part_rows;  // tokens of a slice: total_q, or batch * max_q where that is less
   float* part;  // [..][d]: unnormalised sums
   float* ml;    // [..][2]: their reference (log2) and sum
   void* cuts;   // shared tiles (tensor cores)
@@ -149,12 +148,6 @@ __host__ __device__ __forceinline__ Seq seq_of(const CacheArgs& c, int b) {
     flag(c.status, MP_STATUS_BAD_LENGTH);
   }
   return s;
-}
-
-// Place among a slice's partial results of row i of a sequence's own: the packed row, or where
-// the packed tensors have more rows than the sequences may have, max_q places per sequence.
-__host__ __device__ __forceinline__ int part_row(const ChunkArgs& a, const Seq& s, int b, int i) {
-  return a.part_rows == a.c.total_q ? s.row0 + i : b * a.c.max_q + i;
 }
 
 // Of numbers that are not negative; nearly always of 32 bits, where it costs a fraction.

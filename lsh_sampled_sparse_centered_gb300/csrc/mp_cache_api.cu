@@ -65,18 +65,22 @@ static CacheArgs cache_args(const mp_cache_config* c, const int32_t* table, cons
 static bool chunk_on_tensor_cores(const mp_cache_config* c, int max_q) {
   return c->dtype == MP_DTYPE_BF16 && !chunk_is_step(c->q_heads / c->kv_heads, max_q);
 }
-static StepPlan slices(const mp_cache_config* c, int max_q, int max_kv) {
-  return c->dtype == MP_DTYPE_BF16 ? chunk_step_plan(c, max_q, max_kv) : StepPlan{chunk_splits(c, max_q, max_kv), false};
+// Packed rows that partial results have to have a place for: all of them, unless most belong to no
+// sequence. (A place for those alone cost the fp32 kernel, whose registers are full, 3 %.)
+static int64_t part_rows(const mp_cache_config* c, int total_q, int max_q) {
+  return std::min(int64_t(total_q), 4 * int64_t(c->batch) * max_q);
+}
+static StepPlan slices(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
+  StepPlan p = c->dtype == MP_DTYPE_BF16 ? chunk_step_plan(c, max_q, max_kv) : StepPlan{chunk_splits(c, max_q, max_kv), false};
+  // with more rows than that, as many fewer slices
+  if (!p.joined) p.splits = std::max(1, int(p.splits * part_rows(c, total_q, max_q) / total_q));
+  return p;
 }
 static bool needs_join(const StepPlan& p) { return p.splits > 1 && !p.joined; }
-// tokens that partial results are kept for: those of the sequences, however many rows lie packed
-static int part_rows(const mp_cache_config* c, int total_q, int max_q) {
-  return int(std::min(int64_t(total_q), int64_t(c->batch) * max_q));
-}
-static uint64_t part_bytes(const mp_cache_config* c, int rows, int splits) {
+static uint64_t part_bytes(const mp_cache_config* c, uint64_t rows, int splits) {
   return align256(uint64_t(splits) * rows * c->q_heads * c->head_dim * 4);
 }
-static uint64_t slices_bytes(const mp_cache_config* c, int rows, int splits) {
+static uint64_t slices_bytes(const mp_cache_config* c, uint64_t rows, int splits) {
   return part_bytes(c, rows, splits) + align256(uint64_t(splits) * rows * c->q_heads * 2 * 4);
 }
 // What one call takes.
@@ -84,8 +88,8 @@ static uint64_t chunk_bytes(const mp_cache_config* c, int total_q, int max_q, in
   if (total_q == 0) return 0;
   max_q = std::min(max_q, total_q);
   if (chunk_on_tensor_cores(c, max_q)) return chunk_tc_workspace(c, max_q, max_kv);
-  const StepPlan plan = slices(c, max_q, max_kv);
-  return needs_join(plan) ? slices_bytes(c, part_rows(c, total_q, max_q), plan.splits) : 0;
+  const StepPlan plan = slices(c, total_q, max_q, max_kv);
+  return needs_join(plan) ? slices_bytes(c, total_q, plan.splits) : 0;
 }
 // What the calls take whose limits are at most these. One call's need falls where more rows or a
 // shorter cache are cut into fewer slices, or into slices that join themselves, so this is the
@@ -256,7 +260,6 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
   a.lse = lse;
   a.splits = 1;
   a.joined = false;
-  a.part_rows = part_rows(cfg, total_q, a.c.max_q);
   a.part = a.ml = nullptr;
 #if MP_CHECK
   a.stall = injected("chunk_wait");
@@ -268,12 +271,12 @@ int mp_chunk_attention(const mp_cache_config* cfg, const void* q, const int32_t*
     ProfScope ps(st, K_CHUNK_ATTEND);
     return launch_chunk_tc(a, workspace, st) == cudaSuccess ? MP_OK : MP_ERR_CUDA;
   }
-  const StepPlan plan = slices(cfg, a.c.max_q, max_kv);
+  const StepPlan plan = slices(cfg, total_q, a.c.max_q, max_kv);
   a.splits = plan.splits;
   a.joined = plan.joined;
   if (need > 0) {
     a.part = static_cast<float*>(workspace);
-    a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(cfg, a.part_rows, a.splits));
+    a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(cfg, total_q, a.splits));
   }
   {
     ProfScope ps(st, K_CHUNK_ATTEND);

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
     const int r = r0 + ty * 8 + i;
     if (r >= rows) continue;
     const int64_t row = int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group;
-    const int64_t at = (int64_t(split) * a.part_rows + part_row(a, s, b, r / c.group)) * qh + h * c.group + r % c.group;
+    const int64_t at = int64_t(split) * c.total_q * qh + row;
     const float inv = a.splits > 1 ? 1.f : (sum > 0.f ? 1.0f / sum : sum);
     if (tx == 0) {
       if (a.splits > 1) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m[i], sum);
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   __shared__ float so[8][D], sl[8];
   const CacheArgs& c = a.c;
   const int qh = c.kvh * c.group;
-  const int64_t rows = int64_t(c.total_q) * qh, stride = int64_t(a.part_rows) * qh;  // of a slice
+  const int64_t rows = int64_t(c.total_q) * qh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * (8 / WARPS) + warp / WARPS;
   const int part = warp % WARPS;
@@ -263,10 +263,9 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   if (b < 0) return;
   const Seq s = seq_of(c, b);
   if (t < s.row0 || t >= s.row0 + s.m) return;
-  const int64_t at = int64_t(part_row(a, s, b, t - s.row0)) * qh + (row - int64_t(t) * qh);
-  const float2* ml = reinterpret_cast<const float2*>(a.ml) + at;
+  const float2* ml = reinterpret_cast<const float2*>(a.ml) + row;
   float m = -INFINITY;
-  for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, ml[i * stride].x);
+  for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, ml[i * rows].x);
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
   const float ref = m == -INFINITY ? 0.f : m;
@@ -277,11 +276,11 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
     float x[8][PER], f[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float2 v = i + k < a.splits ? ml[(i + k) * stride] : make_float2(-INFINITY, 0.f);
+      const float2 v = i + k < a.splits ? ml[(i + k) * rows] : make_float2(-INFINITY, 0.f);
       f[k] = v.y == 0.f ? 0.f : exp2f(v.x - ref);
       l = fmaf(v.y, f[k], l);
       const bool live = v.y != 0.f;  // an empty slice has written no sum
-      const float* p = a.part + ((i + k) * stride + at) * D + lane * PER;
+      const float* p = a.part + ((i + k) * rows + row) * D + lane * PER;
 #pragma unroll
       for (int j = 0; j < PER; ++j) x[k][j] = live ? p[j] : 0.f;
     }

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
       sum = fmaf(sl[w][r], by[w], sum);
     }
     const int64_t row = int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group;
-    const int64_t at = (int64_t(split) * a.part_rows + part_row(a, s, b, r / c.group)) * qh + h * c.group + r % c.group;
+    const int64_t at = int64_t(split) * c.total_q * qh + row;
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
     if (lane == 0 && !JOINED) {
       if (a.splits > 1) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(top, sum);
