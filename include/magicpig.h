@@ -80,6 +80,8 @@ extern "C" {
                                        took page 0 in its place, a write was skipped) */
 #define MP_STATUS_BAD_LENGTH 0x40u  /* cache operators: a sequence's rows or length were outside the
                                        limits of the call and were cut to them */
+#define MP_STATUS_NO_ROOM 0x80u     /* mp_cache_plan: pages or packed rows ran out, and some sequences
+                                       got none of their new tokens */
 
 /* element types */
 #define MP_DTYPE_F32 0
@@ -407,6 +409,105 @@ MP_API int mp_cache_evict(const mp_cache_config* cfg, const mp_cache_config* dst
                           const float* scores, int32_t n_sink, int32_t window, int32_t budget, void* dst_keys,
                           void* dst_values, const int32_t* dst_page_table, float* dst_scores, int32_t* dst_len,
                           int32_t* kept, void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* ---- planning a step, attending to shared prefixes, moving keys ---- */
+
+/* Sequences that mp_cache_plan takes at most. */
+#define MP_PLAN_SEQUENCES 8192
+
+/* One step's lengths, pages and packed rows, from how each sequence changes. With n = kv_len[b],
+ * x = change[b] and pages(n) = ceil(n / page_size):
+ *   x > 0: the sequence grows by x tokens, whose rows are packed behind those of the sequences before
+ *          it, and takes pages(n + x) - pages(n) pages;
+ *   x < 0: its last -x slots are dropped (all of them where it has fewer: a rejected draft, a sequence
+ *          that has ended), and the pages behind its new end become free;
+ *   x = 0: nothing changes.
+ * Pages given back go to the end of the list of free pages, sequences in order, a sequence's pages in
+ * order; after all of them, pages are taken from the list's end, the last one first, in the same order.
+ * The sequences that grow are served in order until one needs more pages than are left or more rows
+ * than max_rows leaves: that one and all behind it get none of their tokens in this step (their length
+ * and pages stay) and MP_STATUS_NO_ROOM is set. A sequence that would outgrow max_pages * page_size
+ * gets none either, without holding up the others (MP_STATUS_BAD_LENGTH).
+ *   change     : device int32 [batch].
+ *   base       : device int32 [batch], the text position of each sequence's slot 0 (a shared prefix in
+ *                front of it, say), or NULL for 0.
+ *   kv_len     : device int32 [batch], the slots before the step.
+ *   n_free     : device int32 [1], entries of free_pages that are free before the step.
+ *   page_table : device int32 [batch][max_pages]: entries of taken pages are written. NULL: a dense cache
+ *                (page b is sequence b's), where no pages move and n_free, free_pages and new_free
+ *                are not looked at.
+ *   free_pages : device int32 [n_pages]: the free pages are its first n_free entries; the entries from
+ *                n_free to new_free are written.
+ *   new_len    : device int32 [batch], the slots after the step; may be kv_len itself.
+ *   new_free   : device int32 [1]; may be n_free itself.
+ *   cu_q       : device int32 [batch + 1], the first packed row of each sequence, and their number.
+ * For the packed rows [0, cu_q[batch]), each of the three device int32 [max_rows] or NULL:
+ *   positions  : base[b] + slot, what mp_cache_append takes.
+ *   slots      : page * page_size + row in the page (-1 in a page outside the pool).
+ *   row_seq    : b.
+ * Rows and entries that are not named here are left as they were. new_len, cu_q and positions are what
+ * mp_cache_append, the attentions and mp_cache_weights take as kv_len, cu_q and positions.
+ * batch is at most MP_PLAN_SEQUENCES, max_rows at most 2^30 (else MP_ERR_UNSUPPORTED); heads, head_dim and
+ * dtype of the configuration are not used. No two of the arrays overlap, but for the two pairs named
+ * (MP_ERR_INVALID_ARG). Page numbers outside the pool are moved as they are and set MP_STATUS_BAD_PAGE;
+ * lengths outside the table, and n_free outside the list, are cut and set MP_STATUS_BAD_LENGTH; pages
+ * given back beyond n_pages free ones (a page in two tables) are lost and set it too. */
+MP_API int mp_cache_plan(const mp_cache_config* cfg, const int32_t* change, const int32_t* base, const int32_t* kv_len,
+                         const int32_t* n_free, int32_t max_rows, int32_t* page_table, int32_t* free_pages,
+                         int32_t* new_len, int32_t* new_free, int32_t* cu_q, int32_t* positions, int32_t* slots,
+                         int32_t* row_seq, uint32_t* status, void* stream);
+
+/* Bytes of workspace that serve every mp_prefix_attention whose limits are at most these. */
+MP_API int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_config* prefix_cfg, int32_t total_q,
+                                     int32_t max_q, int32_t max_kv, int32_t max_group_q, int32_t max_prefix,
+                                     uint64_t* bytes);
+
+/* Exact attention of a batch whose sequences share prefixes, each of which is read once for all of
+ * its sequences: mp_chunk_attention over the whole prefix of the sequence's group and then its own slots.
+ *   out = softmax(q k / sqrt(d)) v     lse = log sum exp(q k / sqrt(d))     over both
+ * Group g are the sequences [cu_group[g], cu_group[g + 1]); those outside every group have no prefix.
+ * Tokens see the whole prefix and their own slots up to their own; one at a negative slot sees the
+ * prefix alone.
+ *   cfg, q, cu_q, kv_len, total_q, max_q, max_kv, keys, values, page_table, out, lse : as
+ *              mp_chunk_attention takes them, of the sequences' own slots.
+ *   prefix_cfg : the prefixes' cache: batch = groups; heads, head_dim and dtype as in cfg.
+ *   cu_group   : device int32 [groups + 1], not decreasing, from 0 to at most cfg.batch.
+ *   prefix_len : device int32 [groups], the slots of each prefix (0 is allowed).
+ *   max_group_q, max_prefix : limits as max_q and max_kv: packed rows of any group, slots of any
+ *              prefix. Rows of a group behind the first max_group_q do not see the prefix
+ *              (MP_STATUS_BAD_LENGTH).
+ *   prefix_keys, prefix_values, prefix_table : the prefixes' pages, which may be pages of the same pool.
+ * A row that sees nothing gets out = 0 and lse = -infinity. mp_cache_weights takes q and this lse for
+ * the sequences' own slots. The accuracy is mp_chunk_attention's, partial results are fp32. */
+MP_API int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefix_cfg, const void* q,
+                               const int32_t* cu_q, const int32_t* kv_len, int32_t total_q, int32_t max_q,
+                               int32_t max_kv, const void* keys, const void* values, const int32_t* page_table,
+                               const int32_t* cu_group, const int32_t* prefix_len, int32_t max_group_q,
+                               int32_t max_prefix, const void* prefix_keys, const void* prefix_values,
+                               const int32_t* prefix_table, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* Turn cached keys, in place, from the rotation that they have to another: after an eviction that
+ * moved them to other slots, after the frequencies were scaled for a longer context, or where a text's
+ * cache is used at another place. For the slots [0, kv_len[b]) of every KV head and the pairs i of
+ * mp_rotary's layout:
+ *   t = to * to_freq[i] - from * from_freq[i]
+ *   (a, b) -> scale (a cos t - b sin t, b cos t + a sin t)
+ * in fp32, rounded once; elements from rot_dim on are left as they are. Angles are exact fractions of a
+ * turn as in mp_cache_append; their sine and cosine are off by at most 2^-20 in bf16 and 2^-23 in fp32.
+ *   rotary     : rot_dim and interleaved, with mp_cache_append's limits; eps is not used.
+ *   from_freq  : device double [rot_dim/2], radians per position.
+ *   to_freq    : the same of the new rotation; NULL: from_freq.
+ *   from_positions, to_positions : device int32 [batch][position_heads][position_cols], or NULL: a
+ *                key's slot. position_heads is 1 or kv_heads, position_cols >= max_kv (both are
+ *                not looked at where both arrays are NULL). mp_cache_evict's `kept` fits as
+ *                from_positions, with to_positions NULL: the kept keys then stand at 0, 1, ...
+ *   scale      : finite.
+ * No page may hold slots of two sequences (it would be turned twice). Slots in a bad page are left. */
+MP_API int mp_cache_rotate(const mp_cache_config* cfg, const mp_rotary* rotary, void* keys, const int32_t* page_table,
+                           const int32_t* kv_len, int32_t max_kv, const double* from_freq, const double* to_freq,
+                           const int32_t* from_positions, const int32_t* to_positions, int32_t position_heads,
+                           int32_t position_cols, float scale, uint32_t* status, void* stream);
 
 /* Copy the device status word to *status (synchronises `stream`). */
 MP_API int mp_get_status(const void* tables, uint32_t* status, void* stream);

@@ -34,6 +34,7 @@ MP_STATUS_NOT_BUILT = 0x8
 MP_STATUS_BAD_INDEX = 0x10
 MP_STATUS_BAD_PAGE = 0x20
 MP_STATUS_BAD_LENGTH = 0x40
+MP_STATUS_NO_ROOM = 0x80
 
 MP_DTYPE_F32 = 0
 MP_DTYPE_BF16 = 1
@@ -113,6 +114,12 @@ _SIGS = {
     "mp_evict_workspace_bytes": (ctypes.c_int, [_CCFG, _I, _I, _U64]),
     "mp_cache_evict": (ctypes.c_int, [_CCFG, _CCFG, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _Z,
                                       _P, _P]),
+    "mp_cache_plan": (ctypes.c_int, [_CCFG, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "mp_prefix_workspace_bytes": (ctypes.c_int, [_CCFG, _CCFG, _I, _I, _I, _I, _I, _U64]),
+    "mp_prefix_attention": (ctypes.c_int, [_CCFG, _CCFG, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P,
+                                           _P, _Z, _P, _P]),
+    "mp_cache_rotate": (ctypes.c_int, [_CCFG, ctypes.POINTER(mp_rotary), _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, ctypes.c_float,
+                                       _P, _P]),
     "mp_get_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
     "mp_profile_enable": (ctypes.c_int, [ctypes.c_int]),
     "mp_profile_read": (ctypes.c_int, [ctypes.POINTER(mp_kernel_time), ctypes.c_int32,
@@ -271,7 +278,8 @@ def _cache_calls():
     mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mp_calls", loader))
     loader.exec_module(mod)
     mod.bind(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
-        "mp_cache_append", "mp_chunk_attention", "mp_cache_weights", "mp_cache_evict")))
+        "mp_cache_append", "mp_chunk_attention", "mp_cache_weights", "mp_cache_evict", "mp_cache_plan", "mp_prefix_attention",
+        "mp_cache_rotate")))
     _calls = mod
     return mod
 
@@ -323,6 +331,44 @@ def mp_cache_evict(cfg: mp_cache_config, dst_cfg: mp_cache_config, keys, values,
     return _check("mp_cache_evict", (_calls or _cache_calls()).evict(
         cfg, dst_cfg, keys, values, page_table, kv_len, max_kv, scores, n_sink, window, budget, dst_keys, dst_values,
         dst_page_table, dst_scores, dst_len, kept, workspace, status, stream if stream is None else _stream(stream)))
+
+
+MP_PLAN_SEQUENCES = 8192
+
+
+def mp_cache_plan(cfg: mp_cache_config, change, base, kv_len, n_free, max_rows: int, page_table, free_pages, new_len, new_free, cu_q,
+                  positions=None, slots=None, row_seq=None, status=None, stream=None) -> int:
+    """A step's lengths, pages and packed rows from how each sequence changes: change[b] > 0 tokens more, < 0 slots fewer.
+    new_len may be kv_len and new_free n_free; page_table and free_pages are updated in place."""
+    return _check("mp_cache_plan", (_calls or _cache_calls()).plan(
+        cfg, change, base, kv_len, n_free, max_rows, page_table, free_pages, new_len, new_free, cu_q, positions, slots, row_seq,
+        status, stream if stream is None else _stream(stream)))
+
+
+def mp_prefix_workspace_bytes(cfg: mp_cache_config, prefix_cfg: mp_cache_config, total_q: int, max_q: int, max_kv: int,
+                              max_group_q: int, max_prefix: int) -> int:
+    n = ctypes.c_uint64(0)
+    _check("mp_prefix_workspace_bytes", _lib.mp_prefix_workspace_bytes(
+        cfg, prefix_cfg, total_q, max_q, max_kv, max_group_q, max_prefix, ctypes.byref(n)))
+    return n.value
+
+
+def mp_prefix_attention(cfg: mp_cache_config, prefix_cfg: mp_cache_config, q, cu_q, kv_len, max_q: int, max_kv: int, keys, values,
+                        page_table, cu_group, prefix_len, max_group_q: int, max_prefix: int, prefix_keys, prefix_values,
+                        prefix_table, out, lse=None, workspace=None, status=None, stream=None) -> int:
+    """Exact attention of the new tokens q [total_q, q_heads, head_dim] over the prefix that their group of sequences
+    shares (read once for all of them) and their sequences' own slots."""
+    return _check("mp_prefix_attention", (_calls or _cache_calls()).prefix(
+        cfg, prefix_cfg, q, cu_q, kv_len, max_q, max_kv, keys, values, page_table, cu_group, prefix_len, max_group_q, max_prefix,
+        prefix_keys, prefix_values, prefix_table, out, lse, workspace, status, stream if stream is None else _stream(stream)))
+
+
+def mp_cache_rotate(cfg: mp_cache_config, rotary: mp_rotary, keys, page_table, kv_len, max_kv: int, from_freq, to_freq=None,
+                    from_positions=None, to_positions=None, scale: float = 1.0, status=None, stream=None) -> int:
+    """Turn cached keys in place from one rotation to another. Positions: [batch, 1 or kv_heads, slots] or None for a key's slot."""
+    return _check("mp_cache_rotate", (_calls or _cache_calls()).rotate(
+        cfg, rotary, keys, page_table, kv_len, max_kv, from_freq, to_freq, from_positions, to_positions, scale, status,
+        stream if stream is None else _stream(stream)))
 
 
 def mp_get_status(tables, stream=None) -> int:

@@ -268,7 +268,8 @@ static const char* kKernelNames[K_COUNT] = {"prepare_w", "center", "hash_keys_si
                                             "match_csr", "attend", "planes_build", "planes_append",
                                             "scan", "compact", "hash_step", "logu_lut", "cache_append",
                                             "chunk_attend", "chunk_join", "cache_weights", "evict_select",
-                                            "evict_gather"};
+                                            "evict_gather", "cache_plan", "cache_rotate",
+                                            "prefix_attend", "prefix_join"};
 struct ProfRec {
   int id;
   cudaEvent_t a, b;

@@ -20,6 +20,9 @@ decltype(&mp_cache_append) g_append = nullptr;
 decltype(&mp_chunk_attention) g_attend = nullptr;
 decltype(&mp_cache_weights) g_weights = nullptr;
 decltype(&mp_cache_evict) g_evict = nullptr;
+decltype(&mp_cache_plan) g_plan = nullptr;
+decltype(&mp_prefix_attention) g_prefix = nullptr;
+decltype(&mp_cache_rotate) g_rotate = nullptr;
 
 struct Refused {};  // a Python exception is set
 
@@ -115,6 +118,29 @@ class Args {
     }
     *stride = rows > 1 ? t.stride(0) : heads * d;  // one row has no stride of its own
     return t.data_ptr();
+  }
+  // address of a dense [batch, heads, columns] tensor (None: nullptr), whose last two sizes come out
+  void* per_slot(const char* name, at::ScalarType type, int64_t batch, int32_t* heads, int32_t* columns) {
+    PyObject* o = a_[i_++];
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = checked(o, name, type);
+    const bool fits = t.dim() == 3 && t.size(0) == batch && t.size(1) <= INT_MAX && t.size(2) <= INT_MAX;
+    if (!fits || !t.is_contiguous()) {
+      PyErr_Format(PyExc_ValueError, "%s must be a contiguous (%lld, heads, slots)", name, (long long)batch);
+      throw Refused();
+    }
+    if (*columns >= 0 && (t.size(1) != *heads || t.size(2) != *columns)) {
+      PyErr_Format(PyExc_ValueError, "%s has another shape than the other positions", name);
+      throw Refused();
+    }
+    *heads = int32_t(t.size(1));
+    *columns = int32_t(t.size(2));
+    return t.data_ptr();
+  }
+  float real() {
+    const double v = PyFloat_AsDouble(a_[i_++]);
+    if (v == -1.0 && PyErr_Occurred()) throw Refused();
+    return float(v);
   }
   size_t bytes_of_last() const { return a_[i_ - 1] == Py_None ? 0 : size_t(THPVariable_Unpack(a_[i_ - 1]).numel()); }
   // None: PyTorch's current stream; else a cudaStream_t as a number
@@ -275,6 +301,90 @@ int evict(Args a) {
   });
 }
 
+int plan(Args a) {
+  const auto cfg = a.structure<mp_cache_config>("config");
+  a.first("change");
+  const int64_t batch = cfg.batch;
+  const void* change = a.dense("change", at::kInt, batch);
+  const void* base = a.dense("base", at::kInt, batch, true);
+  const void* kv_len = a.dense("kv_len", at::kInt, batch);
+  const void* n_free = a.dense("n_free", at::kInt, 1, true);
+  const int32_t max_rows = a.number("max_rows");
+  void* table = a.dense("page_table", at::kInt, batch * cfg.max_pages, true);
+  void* free_pages = a.dense("free_pages", at::kInt, cfg.n_pages, true);
+  void* new_len = a.dense("new_len", at::kInt, batch);
+  void* new_free = a.dense("new_free", at::kInt, 1, true);
+  void* cu_q = a.dense("cu_q", at::kInt, batch + 1);
+  void* positions = a.dense("positions", at::kInt, max_rows, true);
+  void* slots = a.dense("slots", at::kInt, max_rows, true);
+  void* row_seq = a.dense("row_seq", at::kInt, max_rows, true);
+  void* status = a.dense("status", at::kInt, 1, true);
+  void* stream = a.stream();
+  return unlocked([&] {
+    return g_plan(&cfg, static_cast<const int32_t*>(change), static_cast<const int32_t*>(base), static_cast<const int32_t*>(kv_len),
+                  static_cast<const int32_t*>(n_free), max_rows, static_cast<int32_t*>(table), static_cast<int32_t*>(free_pages),
+                  static_cast<int32_t*>(new_len), static_cast<int32_t*>(new_free), static_cast<int32_t*>(cu_q),
+                  static_cast<int32_t*>(positions), static_cast<int32_t*>(slots), static_cast<int32_t*>(row_seq),
+                  static_cast<uint32_t*>(status), stream);
+  });
+}
+
+int prefix(Args a) {
+  const auto cfg = a.structure<mp_cache_config>("config"), pre = a.structure<mp_cache_config>("prefix config");
+  const auto t = type_of(cfg);
+  const int64_t rows = a.first("q").dim() ? a.first("q").size(0) : 0, width = int64_t(cfg.q_heads) * cfg.head_dim;
+  const void* q = a.rows_of("q", t, rows, width);
+  const void* cu_q = a.dense("cu_q", at::kInt, int64_t(cfg.batch) + 1);
+  const void* kv_len = a.dense("kv_len", at::kInt, cfg.batch);
+  const int32_t max_q = a.number("max_q"), max_kv = a.number("max_kv");
+  const void* keys = a.dense("keys", t, pool_of(cfg));
+  const void* values = a.dense("values", t, pool_of(cfg));
+  const void* table = a.dense("page_table", at::kInt, int64_t(cfg.batch) * cfg.max_pages, true);
+  const void* cu_group = a.dense("cu_group", at::kInt, int64_t(pre.batch) + 1);
+  const void* prefix_len = a.dense("prefix_len", at::kInt, pre.batch);
+  const int32_t max_group_q = a.number("max_group_q"), max_prefix = a.number("max_prefix");
+  const void* prefix_keys = a.dense("prefix_keys", t, pool_of(pre));
+  const void* prefix_values = a.dense("prefix_values", t, pool_of(pre));
+  const void* prefix_table = a.dense("prefix_table", at::kInt, int64_t(pre.batch) * pre.max_pages, true);
+  void* out = a.rows_of("out", t, rows, width);
+  void* lse = a.dense("lse", at::kFloat, rows * cfg.q_heads, true);
+  void* workspace = a.dense("workspace", at::kByte, 0, true);
+  const size_t bytes = a.bytes_of_last();
+  void* status = a.dense("status", at::kInt, 1, true);
+  void* stream = a.stream();
+  return unlocked([&] {
+    return g_prefix(&cfg, &pre, q, static_cast<const int32_t*>(cu_q), static_cast<const int32_t*>(kv_len), int32_t(rows), max_q,
+                    max_kv, keys, values, static_cast<const int32_t*>(table), static_cast<const int32_t*>(cu_group),
+                    static_cast<const int32_t*>(prefix_len), max_group_q, max_prefix, prefix_keys, prefix_values,
+                    static_cast<const int32_t*>(prefix_table), out, static_cast<float*>(lse), workspace, bytes,
+                    static_cast<uint32_t*>(status), stream);
+  });
+}
+
+int rotate(Args a) {
+  const auto cfg = a.structure<mp_cache_config>("config");
+  const auto rotary = a.structure<mp_rotary>("rotary");
+  const auto t = type_of(cfg);
+  a.first("keys");
+  void* keys = a.dense("keys", t, pool_of(cfg));
+  const void* table = a.dense("page_table", at::kInt, int64_t(cfg.batch) * cfg.max_pages, true);
+  const void* kv_len = a.dense("kv_len", at::kInt, cfg.batch);
+  const int32_t max_kv = a.number("max_kv");
+  const void* from_freq = a.dense("from_freq", at::kDouble, rotary.rot_dim / 2, true);
+  const void* to_freq = a.dense("to_freq", at::kDouble, rotary.rot_dim / 2, true);
+  int32_t heads = 1, columns = -1;
+  const void* from = a.per_slot("from_positions", at::kInt, cfg.batch, &heads, &columns);
+  const void* to = a.per_slot("to_positions", at::kInt, cfg.batch, &heads, &columns);
+  const float scale = a.real();
+  void* status = a.dense("status", at::kInt, 1, true);
+  void* stream = a.stream();
+  return unlocked([&] {
+    return g_rotate(&cfg, &rotary, keys, static_cast<const int32_t*>(table), static_cast<const int32_t*>(kv_len), max_kv,
+                    static_cast<const double*>(from_freq), static_cast<const double*>(to_freq), static_cast<const int32_t*>(from),
+                    static_cast<const int32_t*>(to), heads, columns < 0 ? 0 : columns, scale, static_cast<uint32_t*>(status), stream);
+  });
+}
+
 // METH_FASTCALL entry: the library's return code, or a Python exception
 template <int (*F)(Args), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -287,11 +397,12 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
-// bind(append, attend, weights, evict): addresses of the entry points
+// bind(append, attend, weights, evict, plan, prefix, rotate): addresses of the entry points
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  void* p[4];
-  if (n != 4) return PyErr_Format(PyExc_TypeError, "four addresses are needed");
-  for (int i = 0; i < 4; ++i) {
+  constexpr int kEntries = 7;
+  void* p[kEntries];
+  if (n != kEntries) return PyErr_Format(PyExc_TypeError, "%d addresses are needed", kEntries);
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(args[i]);
     if (!p[i]) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "a null address");
   }
@@ -299,6 +410,9 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   g_attend = reinterpret_cast<decltype(g_attend)>(p[1]);
   g_weights = reinterpret_cast<decltype(g_weights)>(p[2]);
   g_evict = reinterpret_cast<decltype(g_evict)>(p[3]);
+  g_plan = reinterpret_cast<decltype(g_plan)>(p[4]);
+  g_prefix = reinterpret_cast<decltype(g_prefix)>(p[5]);
+  g_rotate = reinterpret_cast<decltype(g_rotate)>(p[6]);
   Py_RETURN_NONE;
 }
 
@@ -308,6 +422,9 @@ PyMethodDef methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                          {"attend", FAST((call<attend, 14>)), METH_FASTCALL, nullptr},
                          {"weights", FAST((call<weights, 12>)), METH_FASTCALL, nullptr},
                          {"evict", FAST((call<evict, 20>)), METH_FASTCALL, nullptr},
+                         {"plan", FAST((call<plan, 16>)), METH_FASTCALL, nullptr},
+                         {"prefix", FAST((call<prefix, 22>)), METH_FASTCALL, nullptr},
+                         {"rotate", FAST((call<rotate, 13>)), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mp_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -16,6 +16,10 @@ struct CacheArgs {
   const int32_t* kv_len;
   int total_q, max_q, max_kv;
   uint32_t* status;              // may be nullptr
+  // set for the pass over shared prefixes: `batch` counts groups then, and kv_len, table and the sizes
+  // are the prefixes'; group g are the sequences [cu_group[g], cu_group[g + 1]) of `sequences`
+  const int32_t* cu_group = nullptr;
+  int sequences = 0;
 };
 
 struct ChunkArgs {
@@ -30,6 +34,9 @@ struct ChunkArgs {
   float* part;  // [..][d]: unnormalised sums
   float* ml;    // [..][2]: their reference (log2) and sum
   void* cuts;   // shared tiles (tensor cores)
+  // tensor cores: where set, a row's unnormalised sum [total_q][q_heads][d] and its reference and sum
+  // go here in the place of out and lse
+  float *state = nullptr, *state_ml = nullptr;
 #if MP_CHECK
   bool stall;  // one CTA stops half way, so that the others' waits run out
 #endif
@@ -81,6 +88,7 @@ struct StepPlan {
   bool joined;  // the slices join themselves
 };
 StepPlan chunk_step_plan(const mp_cache_config* c, int max_q, int max_kv);
+int chunk_step_separate(const mp_cache_config* c, int max_q, int max_kv);  // slices that do not join themselves
 int chunk_step_most(const mp_cache_config* c, int max_q, int max_kv);  // separate slices of any cache of up to max_kv slots
 int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv);
 uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv);
@@ -99,6 +107,8 @@ cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st);
+// The joined slices of rows of which the first `prefix_slices` are of the prefix of the row's group.
+cudaError_t launch_prefix_join(const ChunkArgs& a, const CacheArgs& prefix, int prefix_slices, int dtype, cudaStream_t st);
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_weights_bf16(const WeightsArgs& a, cudaStream_t st);
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
@@ -148,6 +158,26 @@ __host__ __device__ __forceinline__ Seq seq_of(const CacheArgs& c, int b) {
     flag(c.status, MP_STATUS_BAD_LENGTH);
   }
   return s;
+}
+
+// The rows of group g and the slots of its prefix, cut the same way. Every row sees every slot.
+__host__ __device__ __forceinline__ Seq group_of(const CacheArgs& c, int g) {
+  Seq s;
+  const int n = c.kv_len[g], i0 = c.cu_group[g], i1 = c.cu_group[g + 1];
+  s.n = max(0, min(n, int(min(int64_t(c.max_kv), int64_t(c.cols) * c.page_size))));
+  const int b0 = max(0, min(i0, c.sequences)), b1 = max(b0, min(i1, c.sequences));
+  const int r0 = c.cu_q[b0], r1 = c.cu_q[b1];
+  s.row0 = max(0, min(r0, c.total_q));
+  const int e = max(s.row0, min(r1, c.total_q));
+  s.m = min(e - s.row0, c.max_q);
+  s.first = s.n;
+  if (s.n != n || b0 != i0 || b1 != i1 || s.row0 != r0 || s.row0 + s.m != r1) flag(c.status, MP_STATUS_BAD_LENGTH);
+  return s;
+}
+template <bool GROUP>
+__host__ __device__ __forceinline__ Seq rows_of(const CacheArgs& c, int b) {
+  if constexpr (GROUP) return group_of(c, b);
+  else return seq_of(c, b);
 }
 
 // Of numbers that are not negative; nearly always of 32 bits, where it costs a fraction.

@@ -124,7 +124,9 @@ struct Cut {
   int r0, rows;    // the tile's first row and its rows
 };
 
-template <int D>
+// GROUP: the rows of a group over the prefix that its sequences share. STATE: a row's sum goes to
+// a.state as it is, to be joined with the other slots' (of the row's own sequence, or of its prefix).
+template <int D, bool GROUP, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkArgs a,
                const int box, const int b_begin, const int b_end, const int slot_rows) {
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(kGroup * sizeof(Seq) <= kKeys * 128, "one tile of the ring");
   int longest = 0;  // steps of a tile
   for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
-    const Seq s = seq_of(c, b);
+    const Seq s = rows_of<GROUP>(c, b);
     const int tiles = tiles_of(s, c.group);
     int64_t u = 0;
     for (int t = lane; t < tiles; t += 32) {
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               left = 0;
               break;
             }
-            s = seq_of(c, b);
+            s = rows_of<GROUP>(c, b);
             tiles = tiles_of(s, c.group);
           } while (tiles == 0);
         }
@@ -731,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = int64_t(pc.slot) * slot_rows + (r - pc.r0);
         if (real) {
           if (!whole) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m, sum);
+          else if (STATE) *reinterpret_cast<float2*>(a.state_ml + row * 2) = make_float2(m, sum);
           else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
         }
         uint32_t all[D / 32][32];
@@ -750,6 +753,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 8; ++i)
                 dst[i * slot_rows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                  __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            }
+          } else if (STATE) {
+            if (real && sum > 0.f) {
+              float4* dst = reinterpret_cast<float4*>(a.state + row * D + g * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                     __uint_as_float(o[4 * i + 3]));
             }
           } else {
             // Four lanes swap their rows' 16-byte parts, so that each store writes 64 bytes of a row.
@@ -800,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows, a lane each, and 8 columns. Partial sums lie [slot][column / 4][row][4], so that
 // the threads that own rows (in the kernel above and here) write and read whole lines. Set up
 // while k_chunk_tc still runs; it waits for it first.
-template <int D>
+template <int D, bool STATE>
 __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const int slot_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
@@ -859,6 +870,13 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
   }
   const int group = a.c.group, r = cut.r0 + i;
   const int64_t row = cut.row + int64_t(r / group) * (a.c.kvh * group) + r % group;
+  if (STATE) {
+    if (columns == 0) *reinterpret_cast<float2*>(a.state_ml + row * 2) = make_float2(m, l);
+    float4* out = reinterpret_cast<float4*>(a.state + row * D + columns * 8);
+    out[0] = o[0];
+    out[1] = o[1];
+    return;
+  }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   if (a.lse && columns == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
   uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + columns * 8);
@@ -868,7 +886,7 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
 
 int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
 
-template <int D>
+template <int D, bool GROUP, bool STATE>
 cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
   const CacheArgs& c = a.c;
   CUtensorMap mk, mv;
@@ -878,7 +896,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
       !make_map(&mv, a.values, D, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<D>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, GROUP, STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   const int ctas = chunk_tc_ctas(c.batch, c.kvh, c.group, c.max_q, c.max_kv);
   const int slot_rows = slot_rows_of(c.group, c.max_q);
@@ -889,7 +907,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
   ws += align256(uint64_t(2 * ctas) * slot_rows * 8);
   a.part = reinterpret_cast<float*>(ws);
   for (int b = 0; b < c.batch; b += kGroup) {
-    k_chunk_tc<D><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
+    k_chunk_tc<D, GROUP, STATE><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 8) + 7) / 8);
     cfg.blockDim = dim3(256);
@@ -899,7 +917,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D, STATE>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
@@ -920,7 +938,9 @@ uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv) {
 }
 
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st) {
-  return a.c.d == 128 ? launch<128>(a, workspace, st) : launch<64>(a, workspace, st);
+  if (a.c.cu_group) return a.c.d == 128 ? launch<128, true, true>(a, workspace, st) : launch<64, true, true>(a, workspace, st);
+  if (a.state) return a.c.d == 128 ? launch<128, false, true>(a, workspace, st) : launch<64, false, true>(a, workspace, st);
+  return a.c.d == 128 ? launch<128, false, false>(a, workspace, st) : launch<64, false, false>(a, workspace, st);
 }
 
 }  // namespace mp

@@ -1,0 +1,252 @@
+// One step's lengths, pages and packed rows from how each sequence changes.
+//
+// Per sequence three running sums say everything: rows, pages taken and pages given back before it.
+// The free pages with those given back behind them are one list e = 0, 1, ..., free + back - 1, of
+// which the a-th page taken is entry free + back - 1 - a: where an entry lies (in the list as it was,
+// or in the table of a sequence that shrinks) follows from the sums, so that no page has to be moved
+// before another can be taken. What is read (entries below n_free, pages of sequences that shrink, old
+// pages of those that grow) is written by no one, except lengths and n_free where they are updated in
+// place: those are written behind a barrier.
+//
+// Bound by latency: the sums are formed by every CTA for itself (a few reads a sequence) and rows and
+// pages are shared out to one CTA, or a cluster of eight where there are many.
+#include <algorithm>
+
+#include "mp_cache_host.h"
+#include "mp_tc.cuh"
+
+namespace mp {
+namespace {
+
+struct PlanArgs {
+  int batch, page_size, cols, n_pages, max_rows;
+  const int32_t *change, *base, *kv_len, *n_free;
+  int32_t *table, *free, *new_len, *new_free, *cu_q, *positions, *slots, *row_seq;
+  uint32_t* status;
+};
+
+constexpr int kMostThreads = 1024;
+constexpr int kCluster = 8;
+
+// the last i in [0, n) with at[i] <= x, where at[0] = 0 <= x < at[n]
+__device__ __forceinline__ int owner(const uint32_t* at, int n, uint32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
+  extern __shared__ uint32_t sm[];
+  __shared__ int64_t sums[3][32];
+  const int batch = a.batch, threads = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* rows = sm;                    // [batch + 1], before each sequence
+  uint32_t* taken = rows + batch + 1;     // [batch + 1] pages
+  uint32_t* back = taken + batch + 1;     // [batch + 1] pages
+  int* old_len = reinterpret_cast<int*>(back + batch + 1);  // [batch]
+  int* left = old_len + batch;            // [batch]: of the old slots
+  const int rank = CLUSTER ? int(blockIdx.x) : 0, ctas = CLUSTER ? int(gridDim.x) : 1;
+  auto pages = [&](int n) { return int((uint32_t(n) + uint32_t(a.page_size) - 1u) / uint32_t(a.page_size)); };
+  const int64_t cap = int64_t(a.cols) * a.page_size;
+  uint32_t wrong = 0;
+
+  int n_free = 0;
+  if (a.table) {
+    const int given = *a.n_free;
+    n_free = max(0, min(given, a.n_pages));
+    if (n_free != given) wrong |= MP_STATUS_BAD_LENGTH;
+  }
+  // Sums are 64-bit; kept are 32 bits of them, cut where no comparison below tells the difference.
+  int64_t carry[3] = {0, 0, 0};
+  if (tid == 0) rows[0] = taken[0] = back[0] = 0;
+  for (int b0 = 0; b0 < batch; b0 += threads) {
+    const int b = b0 + tid;
+    int64_t v[3] = {0, 0, 0};
+    if (b < batch) {
+      const int given = a.kv_len[b], x = a.change[b];
+      const int n = int(max(int64_t(0), min(int64_t(given), cap)));
+      int grow = max(x, 0);
+      if (n != given || int64_t(n) + grow > cap) wrong |= MP_STATUS_BAD_LENGTH;
+      if (int64_t(n) + grow > cap) grow = 0;
+      const int keep = int(max(int64_t(0), int64_t(n) + min(x, 0)));
+      old_len[b] = n;
+      left[b] = keep;
+      v[0] = grow;
+      if (a.table) {
+        v[1] = pages(n + grow) - pages(n);
+        v[2] = pages(n) - pages(keep);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, v[k], o);
+        if (lane >= o) v[k] += up;
+      }
+    if (lane == 31)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) sums[k][warp] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int64_t mine = lane < threads / 32 ? sums[k][lane] : 0;
+      int64_t pre = lane < warp ? mine : 0, all = mine;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        pre += __shfl_xor_sync(0xffffffffu, pre, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+      }
+      v[k] += carry[k] + pre;
+      carry[k] += all;
+    }
+    if (b < batch) {
+      rows[b + 1] = uint32_t(min(v[0], int64_t(a.max_rows) + 1));
+      taken[b + 1] = uint32_t(min(v[1], int64_t(a.n_pages) + 1));
+      back[b + 1] = uint32_t(min(v[2], int64_t(a.n_pages) - n_free));
+    }
+    __syncthreads();
+  }
+  if (CLUSTER) cluster_arrive();  // this CTA has read the lengths and n_free
+  if (carry[2] > a.n_pages - n_free) wrong |= MP_STATUS_BAD_LENGTH;
+  const uint32_t list = uint32_t(n_free) + back[batch];  // free pages and those given back
+  int served = 0;                                        // sequences before the first that has to wait
+  for (int b0 = 0; b0 < batch; b0 += threads) {
+    const int b = b0 + tid;
+    served += __syncthreads_count(b < batch && rows[b + 1] <= uint32_t(a.max_rows) && taken[b + 1] <= list);
+  }
+  if (served < batch) wrong |= MP_STATUS_NO_ROOM;
+  const uint32_t all_rows = rows[served], all_taken = taken[served];
+
+  // entry e of the list
+  auto entry = [&](uint32_t e) {
+    int p;
+    if (e < uint32_t(n_free)) {
+      p = a.free[e];
+    } else {
+      const int b = owner(back, batch, e - n_free);
+      p = a.table[int64_t(b) * a.cols + pages(left[b]) + int(e - n_free - back[b])];
+    }
+    if (p < 0 || p >= a.n_pages) wrong |= MP_STATUS_BAD_PAGE;
+    return p;
+  };
+  const uint32_t first = uint32_t(rank * threads + tid), step = uint32_t(ctas * threads);
+  if (a.positions || a.slots || a.row_seq) {
+    for (uint32_t r = first; r < all_rows; r += step) {
+      const int b = owner(rows, served, r), slot = old_len[b] + int(r - rows[b]);
+      if (a.positions) a.positions[r] = int(uint32_t(a.base ? a.base[b] : 0) + uint32_t(slot));
+      if (a.row_seq) a.row_seq[r] = b;
+      if (a.slots) {
+        const int col = int(uint32_t(slot) / uint32_t(a.page_size)), had = pages(old_len[b]);
+        int p = b;
+        if (a.table) p = col < had ? a.table[int64_t(b) * a.cols + col] : entry(list - 1 - (taken[b] + uint32_t(col - had)));
+        const bool good = p >= 0 && p < a.n_pages;
+        if (!good) wrong |= MP_STATUS_BAD_PAGE;
+        a.slots[r] = good ? p * a.page_size + (slot - col * a.page_size) : -1;
+      }
+    }
+  }
+  for (uint32_t i = first; i < all_taken; i += step) {
+    const int b = owner(taken, served, i);
+    a.table[int64_t(b) * a.cols + pages(old_len[b]) + int(i - taken[b])] = entry(list - 1 - i);
+  }
+  // pages given back and not taken again
+  for (uint32_t e = uint32_t(n_free) + first; e + all_taken < list; e += step) a.free[e] = entry(e);
+  if (CLUSTER) cluster_wait();
+  for (int b = int(first); b < batch; b += int(step)) {
+    a.new_len[b] = left[b] + (b < served ? int(rows[b + 1] - rows[b]) : 0);
+    a.cu_q[b] = int(min(rows[b], all_rows));
+  }
+  if (first == 0) {
+    a.cu_q[batch] = int(all_rows);
+    if (a.table) *a.new_free = int(list - all_taken);
+  }
+  if (wrong) flag(a.status, wrong);
+}
+
+size_t plan_smem(int batch) { return (size_t(batch) * 5 + 3) * 4; }
+
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
+  const bool many = std::max(a.batch, a.max_rows) > kMostThreads;
+  const size_t smem = plan_smem(a.batch);
+  cudaError_t e = cudaFuncSetAttribute(many ? k_cache_plan<true> : k_cache_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(many ? kCluster : 1);
+  cfg.blockDim = dim3(std::min(kMostThreads, (std::max(a.batch, std::min(a.max_rows, kMostThreads)) + 31) / 32 * 32));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kCluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = many ? 1 : 0;
+  return many ? cudaLaunchKernelEx(&cfg, k_cache_plan<true>, a) : cudaLaunchKernelEx(&cfg, k_cache_plan<false>, a);
+}
+
+}  // namespace
+}  // namespace mp
+
+using namespace mp;
+
+extern "C" int mp_cache_plan(const mp_cache_config* cfg, const int32_t* change, const int32_t* base, const int32_t* kv_len,
+                             const int32_t* n_free, int32_t max_rows, int32_t* page_table, int32_t* free_pages,
+                             int32_t* new_len, int32_t* new_free, int32_t* cu_q, int32_t* positions, int32_t* slots,
+                             int32_t* row_seq, uint32_t* status, void* stream) {
+  int rc = check_cache(cfg);
+  if (rc != MP_OK) return rc;
+  if ((rc = check_pages(cfg, page_table)) != MP_OK) return rc;
+  if (max_rows < 0 || !change || !kv_len || !new_len || !cu_q) return MP_ERR_INVALID_ARG;
+  if (page_table && (!n_free || !free_pages || !new_free)) return MP_ERR_INVALID_ARG;
+  if (cfg->batch > MP_PLAN_SEQUENCES || max_rows > (1 << 30)) return MP_ERR_UNSUPPORTED;
+  const uint64_t b = uint64_t(cfg->batch);
+  const Range used[] = {{change, b * 4},
+                        {base, b * 4},
+                        {kv_len, b * 4},
+                        {page_table ? n_free : nullptr, 4},
+                        {page_table, b * cfg->max_pages * 4},
+                        {page_table ? free_pages : nullptr, uint64_t(cfg->n_pages) * 4},
+                        {new_len, b * 4},
+                        {page_table ? new_free : nullptr, 4},
+                        {cu_q, b * 4 + 4},
+                        {positions, uint64_t(max_rows) * 4},
+                        {slots, uint64_t(max_rows) * 4},
+                        {row_seq, uint64_t(max_rows) * 4},
+                        {status, 4}};
+  constexpr int kUsed = sizeof(used) / sizeof(used[0]), kInputs = 4;  // inputs may overlap each other
+  for (const Range& r : used)
+    if (!aligned4(r.p)) return MP_ERR_INVALID_ARG;
+  if (injected("plan")) return MP_ERR_INJECTED;
+  for (int i = 0; i < kUsed; ++i)
+    for (int j = std::max(i + 1, kInputs); j < kUsed; ++j)
+      if (overlap(used[i], used[j]) && !(used[i].p == used[j].p && ((i == 2 && j == 6) || (i == 3 && j == 7))))  // updated in place
+        return MP_ERR_INVALID_ARG;
+  PlanArgs a;
+  a.batch = cfg->batch;
+  a.page_size = cfg->page_size;
+  a.cols = cfg->max_pages;
+  a.n_pages = cfg->n_pages;
+  a.max_rows = max_rows;
+  a.change = change;
+  a.base = base;
+  a.kv_len = kv_len;
+  a.n_free = n_free;
+  a.table = page_table;
+  a.free = free_pages;
+  a.new_len = new_len;
+  a.new_free = new_free;
+  a.cu_q = cu_q;
+  a.positions = positions;
+  a.slots = slots;
+  a.row_seq = row_seq;
+  a.status = status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  ProfScope ps(st, K_CACHE_PLAN);
+  return launch_plan(a, st) == cudaSuccess ? MP_OK : MP_ERR_CUDA;
+}
