@@ -269,7 +269,7 @@ static const char* kKernelNames[K_COUNT] = {"prepare_w", "center", "hash_keys_si
                                             "scan", "compact", "hash_step", "logu_lut", "cache_append",
                                             "chunk_attend", "chunk_join", "cache_weights", "evict_select",
                                             "evict_gather", "cache_plan", "cache_rotate",
-                                            "prefix_attend", "prefix_join"};
+                                            "prefix_few", "prefix_attend", "prefix_join"};
 struct ProfRec {
   int id;
   cudaEvent_t a, b;

@@ -37,6 +37,8 @@ struct ChunkArgs {
   // tensor cores: where set, a row's unnormalised sum [total_q][q_heads][d] and its reference and sum
   // go here in the place of out and lse
   float *state = nullptr, *state_ml = nullptr;
+  // prefixes in slices (tensor cores): `splits` are the most; a group's number goes here, for each KV head
+  int32_t* pieces = nullptr;
 #if MP_CHECK
   bool stall;  // one CTA stops half way, so that the others' waits run out
 #endif
@@ -88,7 +90,6 @@ struct StepPlan {
   bool joined;  // the slices join themselves
 };
 StepPlan chunk_step_plan(const mp_cache_config* c, int max_q, int max_kv);
-int chunk_step_separate(const mp_cache_config* c, int max_q, int max_kv);  // slices that do not join themselves
 int chunk_step_most(const mp_cache_config* c, int max_q, int max_kv);  // separate slices of any cache of up to max_kv slots
 int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv);
 uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv);
@@ -107,8 +108,9 @@ cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st);
-// The joined slices of rows of which the first `prefix_slices` are of the prefix of the row's group.
-cudaError_t launch_prefix_join(const ChunkArgs& a, const CacheArgs& prefix, int prefix_slices, int dtype, cudaStream_t st);
+// Whether a pass over prefixes on the tensor cores goes in slices, and how many (without: one, after a join of its own).
+bool prefix_in_slices(const mp_cache_config* c, int total_q, int max_q);
+int prefix_slices(const mp_cache_config* c, int max_q, int max_kv);
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_weights_bf16(const WeightsArgs& a, cudaStream_t st);
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);

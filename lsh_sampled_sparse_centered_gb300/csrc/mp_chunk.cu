@@ -244,25 +244,12 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
   }
 }
 
-// Whether packed row t of sequence b takes part in a group's pass over its prefix.
-__device__ __forceinline__ bool in_group(const CacheArgs& c, int b, int t) {
-  int lo = 0, hi = c.batch;  // cu_group[lo] <= b is kept where it holds for 0
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (c.cu_group[mid] <= b) lo = mid;
-    else hi = mid;
-  }
-  const Seq s = group_of(c, lo);
-  return s.row0 <= t && t < s.row0 + s.m;
-}
-
 // Joins the splits' (m, l, sum) of a query row, in an order that is fixed by their number:
 // WARPS warps per row (8 where there are many splits, so that their loads overlap) take
 // eight splits at a time each. Started while the slices still run (its launch costs as much
 // as its work); it waits for them first.
-// GROUP: the first `prefix_slices` are of the prefix of the row's group, and not written where it has none.
-template <typename T, int D, int WARPS, bool GROUP>
-__global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a, const CacheArgs prefix, const int prefix_slices) {
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   constexpr int PER = D / 32;
   __shared__ float so[8][D], sl[8];
   const CacheArgs& c = a.c;
@@ -278,16 +265,15 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a, const Cac
   const Seq s = seq_of(c, b);
   if (t < s.row0 || t >= s.row0 + s.m) return;
   const float2* ml = reinterpret_cast<const float2*>(a.ml) + row;
-  const int begin = GROUP && !in_group(prefix, b, t) ? prefix_slices : 0;
   float m = -INFINITY;
-  for (int i = begin + lane; i < a.splits; i += 32) m = fmaxf(m, ml[i * rows].x);
+  for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, ml[i * rows].x);
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
   const float ref = m == -INFINITY ? 0.f : m;
   float l = 0.f, o[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) o[j] = 0.f;
-  for (int i = begin + part * 8; i < a.splits; i += WARPS * 8) {
+  for (int i = part * 8; i < a.splits; i += WARPS * 8) {
     float x[8][PER], f[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -386,8 +372,8 @@ cudaError_t chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   k_chunk_simt<D, GROUP><<<dim3(unsigned(tiles * a.splits), a.c.kvh, a.c.batch), kThr, smem, st>>>(a);
   return cudaGetLastError();
 }
-template <typename T, int D, bool GROUP>
-cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, int prefix_slices, cudaStream_t st) {
+template <typename T, int D>
+cudaError_t join(const ChunkArgs& a, cudaStream_t st) {
   const int64_t rows = int64_t(a.c.total_q) * a.c.kvh * a.c.group;
   cudaLaunchConfig_t cfg = {};
   const bool wide = a.splits > 8;
@@ -399,8 +385,7 @@ cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, int prefix_slices,
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, k_chunk_join<T, D, 8, GROUP>, a, prefix, prefix_slices)
-              : cudaLaunchKernelEx(&cfg, k_chunk_join<T, D, 1, GROUP>, a, prefix, prefix_slices);
+  return wide ? cudaLaunchKernelEx(&cfg, k_chunk_join<T, D, 8>, a) : cudaLaunchKernelEx(&cfg, k_chunk_join<T, D, 1>, a);
 }
 template <int D>
 cudaError_t weights_simt(const WeightsArgs& a, cudaStream_t st) {
@@ -427,15 +412,8 @@ cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   return a.c.d == 128 ? chunk_simt<128, false>(a, st) : chunk_simt<64, false>(a, st);
 }
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == MP_DTYPE_BF16)
-    return a.c.d == 128 ? join<__nv_bfloat16, 128, false>(a, a.c, 0, st) : join<__nv_bfloat16, 64, false>(a, a.c, 0, st);
-  return a.c.d == 128 ? join<float, 128, false>(a, a.c, 0, st) : join<float, 64, false>(a, a.c, 0, st);
-}
-cudaError_t launch_prefix_join(const ChunkArgs& a, const CacheArgs& prefix, int prefix_slices, int dtype, cudaStream_t st) {
-  if (dtype == MP_DTYPE_BF16)
-    return a.c.d == 128 ? join<__nv_bfloat16, 128, true>(a, prefix, prefix_slices, st)
-                        : join<__nv_bfloat16, 64, true>(a, prefix, prefix_slices, st);
-  return a.c.d == 128 ? join<float, 128, true>(a, prefix, prefix_slices, st) : join<float, 64, true>(a, prefix, prefix_slices, st);
+  if (dtype == MP_DTYPE_BF16) return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, st) : join<__nv_bfloat16, 64>(a, st);
+  return a.c.d == 128 ? join<float, 128>(a, st) : join<float, 64>(a, st);
 }
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t st) {
   if (dtype == MP_DTYPE_BF16) return launch_weights_bf16(a, st);

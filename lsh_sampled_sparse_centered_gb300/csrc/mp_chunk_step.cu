@@ -41,8 +41,7 @@ __device__ __forceinline__ uint32_t pair(const uint4& a, const uint4& b, int e) 
 
 // NT: query rows in eights. JOINED: the slices of a KV head are a cluster and join through
 // distributed shared memory (no second kernel, no workspace).
-// GROUP: the rows of a group over the prefix that its sequences share.
-template <int D, int NT, bool JOINED, bool GROUP>
+template <int D, int NT, bool JOINED>
 __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const ChunkArgs a) {
   constexpr int kWarps = warps_of(JOINED);
   constexpr int KC = D / 32;      // chunks of a K row per lane
@@ -53,7 +52,7 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
   const CacheArgs& c = a.c;
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const Seq s = rows_of<GROUP>(c, b);
+  const Seq s = seq_of(c, b);
   const int rows = s.m * c.group, first = s.first, qh = c.kvh * c.group;
   // A cluster goes through its barriers without new tokens too: were the length written meanwhile
   // (a caller that does not wait for its own copy), a CTA that had left would be read by the
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
     const int64_t at = int64_t(split) * c.total_q * qh + row;
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
     if (lane == 0 && !JOINED) {
-      if (a.part) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(top, sum);
+      if (a.splits > 1) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(top, sum);
       else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
     }
     for (int d = lane * 4; d < D; d += 128) {
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
       }
       if (JOINED)
         *reinterpret_cast<float4*>(&so[0][r][d]) = y;  // this row's own place, read above
-      else if (a.part)
+      else if (a.splits > 1)
         *reinterpret_cast<float4*>(a.part + at * D + d) = y;
       else
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d) =
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
   cluster.sync();  // no CTA leaves while others read its sums
 }
 
-template <int D, bool GROUP>
+template <int D>
 cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.splits, a.c.kvh, a.c.batch);
@@ -311,9 +310,9 @@ cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
   const bool one = int64_t(a.c.max_q) * a.c.group <= 8;
   if (a.joined) {
     cfg.numAttrs = 1;
-    return one ? cudaLaunchKernelEx(&cfg, k_chunk_step<D, 1, true, false>, a) : cudaLaunchKernelEx(&cfg, k_chunk_step<D, 2, true, false>, a);
+    return one ? cudaLaunchKernelEx(&cfg, k_chunk_step<D, 1, true>, a) : cudaLaunchKernelEx(&cfg, k_chunk_step<D, 2, true>, a);
   }
-  return one ? cudaLaunchKernelEx(&cfg, k_chunk_step<D, 1, false, GROUP>, a) : cudaLaunchKernelEx(&cfg, k_chunk_step<D, 2, false, GROUP>, a);
+  return one ? cudaLaunchKernelEx(&cfg, k_chunk_step<D, 1, false>, a) : cudaLaunchKernelEx(&cfg, k_chunk_step<D, 2, false>, a);
 }
 
 }  // namespace
@@ -342,8 +341,8 @@ static int clusters_at_once(int d, bool one, int size) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     auto ask = [&](auto kernel) { return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg); };
-    const cudaError_t e = d == 128 ? (one ? ask(k_chunk_step<128, 1, true, false>) : ask(k_chunk_step<128, 2, true, false>))
-                                   : (one ? ask(k_chunk_step<64, 1, true, false>) : ask(k_chunk_step<64, 2, true, false>));
+    const cudaError_t e = d == 128 ? (one ? ask(k_chunk_step<128, 1, true>) : ask(k_chunk_step<128, 2, true>))
+                                   : (one ? ask(k_chunk_step<64, 1, true>) : ask(k_chunk_step<64, 2, true>));
     if (e != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = 76 / size;
@@ -365,8 +364,8 @@ static int ctas_per_sm(int d, bool one) {
   int n = kept.load(std::memory_order_relaxed);
   if (n == 0) {
     auto ask = [&](auto kernel) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, warps_of(false) * 32, 0); };
-    const cudaError_t e = d == 128 ? (one ? ask(k_chunk_step<128, 1, false, false>) : ask(k_chunk_step<128, 2, false, false>))
-                                   : (one ? ask(k_chunk_step<64, 1, false, false>) : ask(k_chunk_step<64, 2, false, false>));
+    const cudaError_t e = d == 128 ? (one ? ask(k_chunk_step<128, 1, false>) : ask(k_chunk_step<128, 2, false>))
+                                   : (one ? ask(k_chunk_step<64, 1, false>) : ask(k_chunk_step<64, 2, false>));
     if (e != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = one ? 3 : 2;
@@ -406,9 +405,6 @@ StepPlan chunk_step_plan(const mp_cache_config* c, int max_q, int max_kv) {
     if (size < 2 * most && max_kv <= size * kSlice && units <= clusters_at_once(c->head_dim, rows <= 8, size)) return {size, true};
   return {separate_slices(c, rows <= 8, max_kv), false};
 }
-int chunk_step_separate(const mp_cache_config* c, int max_q, int max_kv) {
-  return separate_slices(c, int64_t(max_q) * (c->q_heads / c->kv_heads) <= 8, max_kv);
-}
 // (separate_slices only grows with max_kv; caches of up to max_kv slots all join themselves where
 // the longest of them do in fours, or up to two slices' slots in twos)
 int chunk_step_most(const mp_cache_config* c, int max_q, int max_kv) {
@@ -421,8 +417,7 @@ int chunk_step_most(const mp_cache_config* c, int max_q, int max_kv) {
 }
 
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st) {
-  if (a.c.cu_group) return a.c.d == 128 ? launch<128, true>(a, st) : launch<64, true>(a, st);
-  return a.c.d == 128 ? launch<128, false>(a, st) : launch<64, false>(a, st);
+  return a.c.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
 
 }  // namespace mp

@@ -48,6 +48,9 @@ constexpr int kGroup = 1024;  // sequences of a launch
 // CTA, d = 128 counts more (8192 tokens over as many slots: 429 us with 3, 404 with 4, 398 with
 // 5, 394 with 6); where tiles are cut in many pieces, less (300 over 2000: 27.3 and 29.5 us).
 constexpr int kLead = 3, kLeadWhole = 5;
+// The same for a piece of a cut, whose sums are written and joined besides: its start is Q behind the first
+// copies of K and V (1 and 2 pieces a CTA, 512 rows over 98304 slots: 139 and 150 us).
+constexpr int kLeadPiece = 7;
 constexpr int kMinRun = 2;    // units of a CTA at least
 constexpr int kCut = 10;      // units that cutting the tiles costs: a second piece for most CTAs, and the join
 
@@ -56,10 +59,19 @@ struct Piece {
   int b, h, row0, n, lead;  // sequence, KV head, first packed row, slots, slot of that row
   int r0, rows;             // the tile's first row, and the rows of the whole chunk
   int u0, u1;               // u0 == u1: the run has ended
-  int whole, slot;          // all of its tile's units; else where its partial result goes
+  int whole, slot;          // all of its tile's units; else where its partial result goes (in slices: the slice)
 };
 
 static_assert(kKeys / 16 <= 8, "boxes of 16 rows at least");
+
+// What a launch works on, and where its sums go.
+enum Mode {
+  kChunk,  // chunks over their sequences' slots: out and lse
+  kOwn,    // the same, a row's sum to a.state, to be joined with that over its prefix
+  kRuns,   // the rows of groups over the prefixes that their sequences share, a row's sum to a.state
+  kCuts,   // the same in slices: every tile of a group is cut into as many pieces of its keys
+  kPairs,  // the same with at most 128 rows a group: the halves share them and take every other step
+};
 
 template <int D>
 struct Smem {
@@ -77,6 +89,7 @@ struct Smem {
   int start[4];  // sequence, KV head, tile, unit
   Seq first;     // that sequence
   int longest[12];  // steps of a tile, of each warp's sequences
+  uint64_t pair_full, pair_done;
   uint8_t filled[kStages];  // phase in which each tile of the ring was last filled (1: never)
   uint32_t tmem_base;
   uint32_t abort;
@@ -124,12 +137,61 @@ struct Cut {
   int r0, rows;    // the tile's first row and its rows
 };
 
-// GROUP: the rows of a group over the prefix that its sequences share. STATE: a row's sum goes to
-// a.state as it is, to be joined with the other slots' (of the row's own sequence, or of its prefix).
-template <int D, bool GROUP, bool STATE>
+// Pieces of a tile of `steps` steps, so that none is longer than `longest`; piece i of n starts at its
+// step i steps / n.
+__device__ __forceinline__ int pieces_of(int steps, int longest) { return (steps + longest - 1) / longest; }
+// Steps of a prefix (0: none).
+__device__ __forceinline__ int prefix_steps(const Seq& s) { return (s.n + kKeys - 1) / kKeys; }
+
+// The cut of kCuts and kPairs. Tiles that share a prefix are cut at the same keys and worked on side by
+// side, so that K and V come from HBM once whatever the number of tiles (512 rows over 98304 slots of
+// eight KV heads in equal runs of units, whose tiles meet a key 400 MB apart: twice). Pieces are at most
+// L steps long: short enough that there are no more than r for every CTA, for the r that ends first. With
+// U steps and T tiles in all, L steps give U / L to U / L + T pieces: for each r that leaves L between two
+// limits, of which the upper one is short enough; up to 32 groups are counted for four values, one a lane.
+// Called by a warp; steps and tiles (of a KV head) of the groups lie in shared memory.
+__device__ int longest_piece(const int* steps, const int* tiles, int groups, int kvh, int ctas, int most_pieces) {
+  const int lane = threadIdx.x & 31;
+  int top = 1;
+  int64_t all = 0, all_tiles = 0;
+  for (int g = lane; g < groups; g += 32) {
+    if (tiles[g]) top = max(top, steps[g]);
+    all += int64_t(tiles[g]) * steps[g];
+    all_tiles += steps[g] ? tiles[g] : 0;
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    all_tiles += __shfl_xor_sync(0xffffffffu, all_tiles, o);
+  }
+  all *= kvh;
+  all_tiles *= kvh;
+  const int64_t r = 1 + lane / 4, room = r * ctas - all_tiles;
+  uint32_t cost = UINT32_MAX;
+  int length = top;
+  if (room > 0) {
+    const int low = int(quotient(all + r * ctas - 1, r * ctas)), high = int(min(int64_t(top), quotient(all + room - 1, room)));
+    length = max(max(1, (top + most_pieces - 1) / most_pieces), min(top, groups <= 32 ? low + (high - low) * (lane & 3) / 3 : high));
+    bool fits = length >= high;
+    if (!fits) {
+      int64_t n = 0;
+      for (int g = 0; g < groups; ++g) n += int64_t(tiles[g]) * pieces_of(steps[g], length);
+      fits = n * kvh <= r * ctas;
+    }
+    if (fits) cost = uint32_t(min(r * (length + kLeadPiece), int64_t(INT32_MAX)));
+  }
+  const uint32_t best = __reduce_min_sync(0xffffffffu, cost);
+  if (best == UINT32_MAX) return top;
+  return __shfl_sync(0xffffffffu, length, __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1);
+}
+
+template <int D, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkArgs a,
                const int box, const int b_begin, const int b_end, const int slot_rows) {
+  constexpr bool GROUP = MODE == kRuns || MODE == kCuts || MODE == kPairs, STATE = MODE == kOwn || MODE == kRuns;
+  constexpr bool PAIR = MODE == kPairs, CUT = MODE == kCuts || PAIR;
   extern __shared__ __align__(1024) unsigned char smraw[];
   const uint32_t base = saddr(smraw);
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(smraw + ((1024 - (base & 1023)) & 1023));
@@ -163,8 +225,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.drain[i], 1);
       mbar_init(&S.turn[i], 4);
     }
+    mbar_init(&S.pair_full, 8);
+    mbar_init(&S.pair_done, 8);
     S.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (CUT && threadIdx.x == 256) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV)) : "memory");
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem_base)),
@@ -176,11 +244,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* units = reinterpret_cast<int64_t*>(&S.kv[0][0][0]);  // of each sequence and KV head; the ring is not yet in use
   int* counts = reinterpret_cast<int*>(&S.kv[1][0][0]);                  // tiles of each sequence and KV head
   Seq* seqs = reinterpret_cast<Seq*>(&S.kv[2][0][0]);
+  int* steps = reinterpret_cast<int*>(seqs);  // of each prefix (kCuts, kPairs)
   static_assert(kGroup * sizeof(Seq) <= kKeys * 128, "one tile of the ring");
   int longest = 0;  // steps of a tile
   for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
     const Seq s = rows_of<GROUP>(c, b);
     const int tiles = tiles_of(s, c.group);
+    if (CUT) {
+      if (lane == 0) {
+        steps[b - b_begin] = prefix_steps(s);
+        counts[b - b_begin] = tiles;
+      }
+      continue;
+    }
     int64_t u = 0;
     for (int t = lane; t < tiles; t += 32) {
       const int mine = steps_of(s, c.group, t);
@@ -198,7 +274,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 0) S.longest[warp] = longest;
   __syncthreads();
-  if (warp == 0) {
+  Seq early = {0, 0, 0, 0};  // the first groups, a lane each, for the warp that walks the pieces
+  if (CUT) {
+    if (warp == 10 && b_begin + lane < b_end) early = group_of(c, b_begin + lane);
+    if (warp == 0) {
+      const int groups = b_end - b_begin, length = longest_piece(steps, counts, groups, c.kvh, gridDim.x, a.splits);
+      if (lane == 0) S.lead = length;
+      if (blockIdx.x == 0)
+        for (int i = lane; i < groups * c.kvh; i += 32) a.pieces[b_begin * c.kvh + i] = pieces_of(steps[i / c.kvh], length);
+      fence_async();
+    }
+  } else if (warp == 0) {
     int64_t all = 0, all_tiles = 0;
     for (int b = lane; b < b_end - b_begin; b += 32) {
       all += units[b] * c.kvh;
@@ -299,7 +385,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   // registers: 8 x 208 + 4 x 80 a lane, within the 12 x 168 of the launch
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 10) {
+    if (warp == 10 && CUT) {
+      // ---------------- the CTA's pieces: numbers cta, cta + ctas, ... of (group, KV head, piece, tile) ----------------
+      const int length = S.lead;
+      int64_t item = blockIdx.x, base = 0;  // base: pieces of the groups before these 32
+      int g0 = b_begin;
+      Seq s = early;
+      int tiles = 0, pieces = 0;
+      int64_t mine = 0, pre = 0;
+      auto look = [&]() {  // a group per lane
+        if (g0 != b_begin) s = g0 + lane < b_end ? group_of(c, g0 + lane) : Seq{0, 0, 0, 0};
+        tiles = tiles_of(s, c.group);
+        pieces = pieces_of(prefix_steps(s), length);
+        pre = mine = int64_t(tiles) * pieces * c.kvh;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += v;
+        }
+      };
+      look();
+      bool ok = true;
+      for (uint32_t i = 0; ok; ++i, item += gridDim.x) {
+        uint32_t past = 0;
+        while (g0 < b_end) {
+          past = __ballot_sync(0xffffffffu, base + pre > item);
+          if (past) break;
+          base += __shfl_sync(0xffffffffu, pre, 31);
+          g0 += 32;
+          look();
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.piece_empty[i & 1], ((i >> 1) & 1) ^ 1, abort));
+        if (!ok) break;
+        Piece& p = S.piece[i & 1];
+        if (!past) {
+          if (lane == 0) {
+            p.u0 = p.u1 = 0;
+            mbar_arrive(&S.piece_full[i & 1]);
+          }
+          break;
+        }
+        if (lane == __ffs(past) - 1) {
+          int64_t at = item - base - (pre - mine);
+          const int64_t per = int64_t(tiles) * pieces;
+          p.b = g0 + lane;
+          p.h = int(quotient(at, per));
+          at -= p.h * per;
+          p.slot = int(at / tiles);
+          p.r0 = int(at % tiles) * kRows;
+          p.row0 = s.row0;
+          p.n = s.n;
+          p.lead = s.first;
+          p.rows = s.m * c.group;
+          p.whole = 0;
+          const int64_t steps = prefix_steps(s);
+          p.u0 = int(p.slot * steps / pieces);
+          p.u1 = int((p.slot + 1) * steps / pieces);
+          mbar_arrive(&S.piece_full[i & 1]);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 10) {
       // ---------------- the run's pieces, two of them ahead ----------------
       if (lane == 0) {
         Cut cut;
@@ -400,6 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int live = max(0, min(kKeys, pc.n - n0));  // rows that hold slots of the sequence
           const int boxes = (live + box - 1) / box;
           for (int kv = 0; kv < 2; ++kv) {
+            // Q behind five tiles in the memory's queue came 7 us late, so the first K waits for it alone
+            if (CUT && i == 0 && u == pc.u0 && kv == 1) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&S.q_full[0], 0, abort));
+              if (!ok) break;
+            }
             ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[st], ph ^ 1, abort));
             if (!ok) break;
             // rows of V behind the last slot are zeroed before the products see the tile: they may
@@ -498,6 +649,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) mbar_arrive(&S.piece_empty[i & 1]);
         __syncwarp();
         if (steps == 0) break;
+        if (PAIR) {
+          // Steps half, half + 2, ... of the piece. The ring's tiles in between are the other half's, but are
+          // waited for and given back here too: a half that passed one unseen could take a barrier's phase for
+          // the one before it (copies do not land in order), and one that did not give it back could miss a phase.
+          int k_at = 0, v_at = 0;  // steps whose tiles the cursors have come to (one cursor: v_at)
+          auto pass = [&](int stage, uint32_t phase) {
+            ok = ok && mbar_wait_warp(&S.full[stage], phase, abort);
+            if (ok && elect_one()) mbar_arrive(&S.empty[stage]);
+            __syncwarp();
+          };
+          auto to_k = [&](int u) {
+            for (int& at = kOwnP ? k_at : v_at; ok && at < u; ++at) {
+              pass(st, ph);
+              advance();
+              if (!kOwnP) {
+                pass(st, ph);
+                advance();
+              }
+            }
+          };
+          auto to_v = [&](int u) {
+            if (kOwnP)
+              for (; ok && v_at < u; ++v_at) {
+                pass(v_st, v_ph);
+                advance_v();
+              }
+          };
+          auto form_s = [&](int u) {
+            to_k(u);
+            ok = ok && mbar_wait_warp(&S.full[st], ph, abort);
+            if (ok) product_s();
+            ++k_at;
+          };
+          if (half < steps) {
+            ok = mbar_wait_warp(&S.q_full[half], ph_q, abort);
+            ph_q ^= 1;
+            if (ok) form_s(half);
+          }
+          for (int u = half; ok && u < steps; u += 2) {
+            if (kOwnP) {
+              ok = mbar_wait_warp(&S.s_free[half], ph_f, abort);
+              if (!ok) break;
+              ph_f ^= 1;
+              if (u + 2 < steps) form_s(u + 2);
+              to_v(u);
+              if (!ok) break;
+            }
+            const int at = kOwnP ? v_st : st;
+            ok = mbar_wait_warp(&S.full[at], kOwnP ? v_ph : ph, abort);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              ok = ok && mbar_wait_warp(&S.p_full[half][part], ph_p, abort);
+              if (!ok) break;
+              fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = part * 4; kk < part * 4 + 4; ++kk)
+                  mma_bf16_ta(t_o, t_p + uint32_t(kk * 8), dv + at * kTile + kk * 128, id_o, (u > half || kk > 0) ? 1u : 0u);
+                if (part == 1) {
+                  mma_commit(&S.o_full[half]);
+                  mma_commit(&S.empty[at]);
+                }
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            ph_p ^= 1;
+            advance_v();
+            ++v_at;
+            if (!kOwnP && u + 2 < steps) form_s(u + 2);
+          }
+          to_k(steps);
+          to_v(steps);
+          continue;
+        }
         if (!active) {  // the ring's tiles pass this half by
           for (int j = 0; j < steps && ok; ++j) {
             ok = mbar_wait_warp(&S.full[st], ph, abort);
@@ -578,15 +804,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&S.piece_full[i & 1], (i >> 1) & 1, abort));
       if (!ok) break;
       const Piece& pc = S.piece[i & 1];
-      const int r0 = pc.r0 + half * 128, rows = pc.rows;
+      const int r0 = pc.r0 + (PAIR ? 0 : half * 128), rows = pc.rows;
       if (pc.u0 == pc.u1) break;
+      if (PAIR && i > 0) {  // the other half has read this half's sums of the piece before
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.pair_done, (i & 1) ^ 1, abort));
+        if (!ok) break;
+      }
       if (r0 < rows) {
         const int64_t head = int64_t(pc.row0) * qh + pc.h * c.group;  // row of token 0's first head
         const int r = r0 + quarter * 32 + lane;
         const int64_t row = head + int64_t(r / c.group) * qh + r % c.group;
+        const int steps = PAIR ? (pc.u1 - pc.u0 - half + 1) / 2 : pc.u1 - pc.u0;
         // the warp's rows of Q into their swizzled places (16-byte chunk i of row k at i ^ (k % 8)),
-        // 512 contiguous bytes a load
-        {
+        // 512 contiguous bytes a load (none for a half without a step: its sums take that place at once)
+        if (!PAIR || steps > 0) {
           constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;
           const int i = lane % kChunks, own = lane / kChunks;
           uint4 v[kChunks];
@@ -608,13 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&S.q_full[half]);
         }
         // slots below this, counted from the piece's first, are seen
-        int see = r < rows ? min(pc.n, pc.lead + r / c.group + 1) - pc.u0 * kKeys : 0;
+        constexpr int kStride = PAIR ? 2 * kKeys : kKeys;  // from one of this half's steps to the next
+        int see = r < rows ? min(pc.n, pc.lead + r / c.group + 1) - (pc.u0 + (PAIR ? half : 0)) * kKeys : 0;
         // the lowest limit of this warp's rows decides whether a step needs the mask at all
         int see_low = __reduce_min_sync(0xffffffffu, r < rows ? see : INT32_MAX);
         float m = -INFINITY;  // the row's reference, in log2
         uint64_t l0 = 0, l1 = 0;
-        const int steps = pc.u1 - pc.u0;
-        const bool turns = !kOwnP && rows - pc.r0 > 128;  // both halves have rows
+        const bool turns = !PAIR && !kOwnP && rows - pc.r0 > 128;  // both halves have rows
         for (int j = 0; j < steps; ++j) {
           ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[half], ph_s, abort));
           ph_s ^= 1;
@@ -648,8 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (i + 96 >= see) x3[i] = 0xff800000u;
             }
           }
-          see -= kKeys;
-          see_low -= kKeys;
+          see -= kStride;
+          see_low -= kStride;
           float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
@@ -724,10 +955,90 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph_o ^= 1;  // past this step's second product
         }
         if (!ok) break;
-        ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[half], ph_o ^ 1, abort));
+        if (!PAIR || steps > 0) ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[half], ph_o ^ 1, abort));
         if (!ok) break;
         fence_after();
         const float sum = lo2(l0) + hi2(l0) + lo2(l1) + hi2(l1);
+        if (CUT) {
+          // the sums of this piece: a slice of its rows
+          const int64_t slice = int64_t(pc.slot) * c.total_q * qh;
+          const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + 256;
+          float by0 = 1.f, by1 = 0.f, top = m, all_sum = sum;
+          if (PAIR) {
+            // both halves' sums over these rows: each half takes half of the columns of both
+            const int own = quarter * 32 + lane;
+            float2* const ml = reinterpret_cast<float2*>(&S.q[0][0][0]);  // in the place of Q, which has been read
+            float2* const ml1 = reinterpret_cast<float2*>(&S.q[1][0][0]);
+            (half ? ml1 : ml)[own] = make_float2(m, sum);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.pair_full);
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.pair_full, i & 1, abort));
+            if (!ok) break;
+            fence_after();
+            const float2 a0 = ml[own], a1 = ml1[own];
+            top = fmaxf(a0.x, a1.x);
+            by0 = a0.y == 0.f ? 0.f : exp2f(a0.x - top);
+            by1 = a1.y == 0.f ? 0.f : exp2f(a1.x - top);
+            all_sum = fmaf(a0.y, by0, a1.y * by1);
+          }
+          if (r < rows && (!PAIR || half == 0)) *reinterpret_cast<float2*>(a.ml + (slice + row) * 2) = make_float2(top, all_sum);
+          constexpr int kBlocks = PAIR ? D / 64 : D / 32;  // of 32 columns
+          const int g0 = PAIR ? half * kBlocks : 0;
+          uint32_t mine[kBlocks][32], others[PAIR ? kBlocks : 1][32];
+#pragma unroll
+          for (int g = 0; g < kBlocks; ++g) {
+            tmem_ld32(lanes + (PAIR ? 0 : half * D) + (g0 + g) * 32, mine[g]);
+            if (PAIR) tmem_ld32(lanes + D + (g0 + g) * 32, others[g]);
+          }
+          tmem_wait_ld(mine[0]);
+#pragma unroll
+          for (int g = 0; g < kBlocks; ++g) {
+            if (g > 0) tmem_tie(mine[g]);
+            if (PAIR) tmem_tie(others[g]);
+          }
+          if (PAIR) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.pair_done);
+          }
+#pragma unroll
+          for (int g = 0; g < kBlocks; ++g) {
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              v[k] = __uint_as_float(mine[g][k]);
+              if (PAIR) {  // a half without a step has written nothing
+                v[k] = by0 == 0.f ? 0.f : v[k] * by0;
+                v[k] = by1 == 0.f ? v[k] : fmaf(__uint_as_float(others[g][k]), by1, v[k]);
+              }
+            }
+            // four lanes swap their rows' 32-byte parts, so that they write 128 bytes of a row together
+#pragma unroll
+            for (int bit = 1; bit <= 2; bit *= 2) {
+              const bool high = lane & bit;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                if (k & (8 * bit)) continue;
+                const float got = __shfl_xor_sync(0xffffffffu, high ? v[k] : v[k + 8 * bit], bit);
+                if (high) v[k] = got;
+                else v[k + 8 * bit] = got;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int64_t to_row = __shfl_sync(0xffffffffu, row, (lane & ~3) + k);
+              if (r - (lane & 3) + k < rows) {
+                float4* dst = reinterpret_cast<float4*>(a.part + (slice + to_row) * D + (g0 + g) * 32 + (lane & 3) * 8);
+                dst[0] = make_float4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]);
+                dst[1] = make_float4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]);
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.piece_empty[i & 1]);
+          continue;
+        }
         const float inv = sum > 0.f ? 1.0f / sum : sum;
         const bool real = r < rows, whole = pc.whole;
         const int64_t at = int64_t(pc.slot) * slot_rows + (r - pc.r0);
@@ -794,6 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (CUT) asm volatile("griddepcontrol.wait;" ::: "memory");  // the join waits for this kernel, and so for the one before it too
   fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -886,8 +1198,9 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
 
 int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
 
-template <int D, bool GROUP, bool STATE>
+template <int D, Mode MODE>
 cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
+  constexpr bool STATE = MODE == kOwn || MODE == kRuns, CUT = MODE == kCuts || MODE == kPairs;
   const CacheArgs& c = a.c;
   CUtensorMap mk, mv;
   const int box = box_rows(c.table, c.page_size);
@@ -896,33 +1209,60 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
       !make_map(&mv, a.values, D, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<D>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, GROUP, STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   const int ctas = chunk_tc_ctas(c.batch, c.kvh, c.group, c.max_q, c.max_kv);
   const int slot_rows = slot_rows_of(c.group, c.max_q);
-  char* ws = static_cast<char*>(workspace);
-  a.cuts = ws;
-  ws += align256(uint64_t(ctas) * sizeof(Cut));
-  a.ml = reinterpret_cast<float*>(ws);
-  ws += align256(uint64_t(2 * ctas) * slot_rows * 8);
-  a.part = reinterpret_cast<float*>(ws);
+  if (!CUT) {
+    char* ws = static_cast<char*>(workspace);
+    a.cuts = ws;
+    ws += align256(uint64_t(ctas) * sizeof(Cut));
+    a.ml = reinterpret_cast<float*>(ws);
+    ws += align256(uint64_t(2 * ctas) * slot_rows * 8);
+    a.part = reinterpret_cast<float*>(ws);
+  }
   for (int b = 0; b < c.batch; b += kGroup) {
-    k_chunk_tc<D, GROUP, STATE><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 8) + 7) / 8);
-    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    if (CUT) {  // needs nothing of the kernel before it, and starts as that one's CTAs leave their SMs
+      cfg.gridDim = dim3(ctas);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = smem;
+      if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc<D, MODE>, mk, mv, ChunkArgs(a), box, b, std::min(c.batch, b + kGroup), slot_rows)) != cudaSuccess)
+        return e;
+      continue;
+    }
+    k_chunk_tc<D, MODE><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
+    cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 8) + 7) / 8);
+    cfg.blockDim = dim3(256);
     if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D, STATE>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
 
 }  // namespace
+
+// Tiles of groups of at most max_q rows in all their KV heads, of total_q rows altogether.
+static int64_t prefix_tiles(const mp_cache_config* c, int total_q, int max_q) {
+  const int64_t group = c->q_heads / c->kv_heads, each = (max_q * group + kRows - 1) / kRows;
+  return c->kv_heads * std::min(c->batch * each, c->batch + total_q * group / kRows);
+}
+// Slices are taken where a group's rows fit one half, and otherwise where there are at most half as many
+// tiles as SMs: more keep each other's keys in L2 as they are, and equal runs leave no CTA idle.
+bool prefix_in_slices(const mp_cache_config* c, int total_q, int max_q) {
+  return int64_t(max_q) * (c->q_heads / c->kv_heads) <= 128 || 2 * prefix_tiles(c, total_q, max_q) <= device_sm_count();
+}
+// Two pieces a CTA where all groups have as many tiles as the largest, one a CTA at most.
+int prefix_slices(const mp_cache_config* c, int max_q, int max_kv) {
+  const int sms = device_sm_count(), tiles = int((int64_t(max_q) * (c->q_heads / c->kv_heads) + kRows - 1) / kRows);
+  const int most = std::min((max_kv + kKeys - 1) / kKeys, (sms + c->kv_heads - 1) / c->kv_heads);
+  return std::max(1, std::min(most, int((2 * int64_t(sms) + int64_t(c->kv_heads) * tiles - 1) / (int64_t(c->kv_heads) * tiles))));
+}
 
 // One CTA per SM, or fewer when the limits leave fewer runs of units than that.
 int chunk_tc_ctas(int batch, int kvh, int group, int max_q, int max_kv) {
@@ -938,9 +1278,14 @@ uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv) {
 }
 
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st) {
-  if (a.c.cu_group) return a.c.d == 128 ? launch<128, true, true>(a, workspace, st) : launch<64, true, true>(a, workspace, st);
-  if (a.state) return a.c.d == 128 ? launch<128, false, true>(a, workspace, st) : launch<64, false, true>(a, workspace, st);
-  return a.c.d == 128 ? launch<128, false, false>(a, workspace, st) : launch<64, false, false>(a, workspace, st);
+  const bool d128 = a.c.d == 128;
+  if (a.c.cu_group && a.pieces) {
+    if (int64_t(a.c.max_q) * a.c.group <= 128) return d128 ? launch<128, kPairs>(a, nullptr, st) : launch<64, kPairs>(a, nullptr, st);
+    return d128 ? launch<128, kCuts>(a, nullptr, st) : launch<64, kCuts>(a, nullptr, st);
+  }
+  if (a.c.cu_group) return d128 ? launch<128, kRuns>(a, workspace, st) : launch<64, kRuns>(a, workspace, st);
+  if (a.state) return d128 ? launch<128, kOwn>(a, workspace, st) : launch<64, kOwn>(a, workspace, st);
+  return d128 ? launch<128, kChunk>(a, workspace, st) : launch<64, kChunk>(a, workspace, st);
 }
 
 }  // namespace mp

@@ -162,7 +162,7 @@ enum KernelId {
   K_PREPARE_W, K_CENTER, K_HASH_KEYS_SIMT, K_HASH_KEYS_TC, K_CSR_BUILD, K_HASH_APPEND, K_MARK_APPENDED,
   K_HASH_QUERY, K_MATCH_CSR, K_ATTEND, K_PLANES_BUILD, K_PLANES_APPEND, K_SCAN, K_COMPACT, K_HASH_STEP, K_LOGU_LUT,
   K_CACHE_APPEND, K_CHUNK_ATTEND, K_CHUNK_JOIN, K_CACHE_WEIGHTS, K_EVICT_SELECT, K_EVICT_GATHER,
-  K_CACHE_PLAN, K_CACHE_ROTATE, K_PREFIX_ATTEND, K_PREFIX_JOIN,
+  K_CACHE_PLAN, K_CACHE_ROTATE, K_PREFIX_FEW, K_PREFIX_ATTEND, K_PREFIX_JOIN,
   K_COUNT
 };
 // Brackets one launcher call with events when profiling is on.

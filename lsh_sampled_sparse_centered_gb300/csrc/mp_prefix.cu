@@ -1,29 +1,179 @@
-// Attention of a batch whose sequences share prefixes (host side).
+// Attention of a batch whose sequences share prefixes: the join of its two passes, and the host side.
 //
 // The softmax over a row's prefix and its own slots is the join of two: every partial result is an
 // unnormalised sum with its reference and its weights' sum (fp32), whatever slots it covers. So one pass
 // goes over the prefixes, whose rows are those of all the sequences of a group: each prefix is read once,
 // and the products have as many rows as the group has. The other goes over the sequences' own slots, as
-// the attention of a chunk does. The last kernel joins both passes' slices.
+// the attention of a chunk does. The last kernel joins both passes' slices: memory bound where there are
+// many rows, and otherwise a chain of lookups (sequence, group, pieces) and loads, which it keeps short by
+// having the loads of all a row's slices in flight.
 #include "mp_cache_host.h"
+#include "mp_prefix.h"
+#include "mp_tc.cuh"
 
 namespace mp {
 namespace {
 
-// Slices of one pass over a cache, as (slice, packed row) pairs are kept for them.
-int slices_of(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
-  if (chunk_on_tensor_cores(c, max_q)) return 1;
-  const int s = c->dtype == MP_DTYPE_BF16 ? chunk_step_separate(c, max_q, max_kv) : chunk_splits(c, max_q, max_kv);
-  // as many fewer where most packed rows belong to no sequence
-  return std::max(1, int(s * part_rows(c, total_q, max_q) / total_q));
+// Slices of the two passes, and their numbers per (group or sequence, KV head) where these differ.
+struct Slices {
+  int shared, own;
+  int32_t *pre_pieces, *own_pieces;
+};
+
+// Joins the slices' (m, l, sum) of a sequence's query rows, in their order. A warp takes ROWS rows (of
+// D / 4 lanes each, 16 bytes a lane) and has the loads of kAtOnce slices of each in flight. The first
+// `shared` slices are of the prefix, the `own` behind them of the own slots; where their numbers are kept
+// per (group or sequence, KV head), as many of them are there. Rows without a prefix have none of it.
+// Grid: rows of a sequence x sequences, so that what has to be looked up does not hang on a row.
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const CacheArgs prefix, const Slices sl) {
+  constexpr int kLanes = D / 4, kTurns = ROWS * kLanes / 32, kAtOnce = ROWS == 32 / kLanes ? 8 : 2;
+  const CacheArgs& c = a.c;
+  const int qh = c.kvh * c.group, b = blockIdx.y;
+  const int64_t rows = int64_t(c.total_q) * qh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kLanes, e = lane % kLanes * 4;
+  const Seq s = seq_of(c, b);
+  int lo = 0, hi = prefix.batch;  // cu_group[lo] <= b is kept where it holds for 0
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix.cu_group[mid] <= b) lo = mid;
+    else hi = mid;
+  }
+  const Seq g = group_of(prefix, lo);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t first = (int64_t(blockIdx.x) * 8 + warp) * ROWS, mine = int64_t(s.m) * qh;
+  if (first >= mine) return;
+  float m[kTurns], l[kTurns];
+  float4 o[kTurns];
+  int64_t row[kTurns];
+  int there[kTurns], all[kTurns];  // slices of the row's prefix, and with those of its own slots
+  int most = 0;
+#pragma unroll
+  for (int j = 0; j < kTurns; ++j) {
+    const int64_t i = first + j * (32 / kLanes) + sub;
+    row[j] = i < mine ? int64_t(s.row0) * qh + i : -1;
+    const int t = s.row0 + int(i / qh);
+    const int h = int(i % qh) / c.group;
+    there[j] = g.row0 <= t && t < g.row0 + g.m ? sl.shared : 0;
+    all[j] = sl.own;
+    if (row[j] >= 0) {
+      if (sl.pre_pieces && there[j]) there[j] = min(there[j], sl.pre_pieces[int64_t(lo) * c.kvh + h]);
+      if (sl.own_pieces) all[j] = min(all[j], sl.own_pieces[int64_t(b) * c.kvh + h]);
+    }
+    all[j] += there[j];
+    most = max(most, all[j]);
+    m[j] = -INFINITY;
+    l[j] = 0.f;
+    o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  for (int i0 = 0; i0 < most; i0 += kAtOnce) {
+    float2 v[kTurns][kAtOnce];
+    float4 x[kTurns][kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kTurns; ++j) {
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = i0 + k;
+        const bool live = row[j] >= 0 && i < all[j];
+        const int64_t at = live ? (i < there[j] ? i : i - there[j] + sl.shared) * rows + row[j] : 0;
+        v[j][k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
+        x[j][k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kTurns; ++j) {
+      float top = m[j];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, v[j][k].x);
+      const float ref = top == -INFINITY ? 0.f : top, before = exp2f(m[j] - ref);  // 0 while nothing was seen
+      m[j] = top;
+      l[j] *= before;
+      o[j].x *= before;
+      o[j].y *= before;
+      o[j].z *= before;
+      o[j].w *= before;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const bool any = v[j][k].y != 0.f;  // a slice that saw nothing has written no sum
+        const float by = any ? exp2f(v[j][k].x - ref) : 0.f;
+        l[j] = fmaf(v[j][k].y, by, l[j]);
+        o[j].x = any ? fmaf(x[j][k].x, by, o[j].x) : o[j].x;
+        o[j].y = any ? fmaf(x[j][k].y, by, o[j].y) : o[j].y;
+        o[j].z = any ? fmaf(x[j][k].z, by, o[j].z) : o[j].z;
+        o[j].w = any ? fmaf(x[j][k].w, by, o[j].w) : o[j].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kTurns; ++j) {
+    if (row[j] < 0) continue;
+    const float inv = l[j] == 0.f ? 0.f : 1.0f / l[j];
+    if (a.lse && e == 0) a.lse[row[j]] = l[j] == 0.f ? -INFINITY : m[j] * 0.6931471805599453f + logf(l[j]);
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row[j] * D + e) = make_uint2(bf2(o[j].x * inv, o[j].y * inv), bf2(o[j].z * inv, o[j].w * inv));
+    else
+      *reinterpret_cast<float4*>(static_cast<T*>(a.out) + row[j] * D + e) = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
+  }
 }
-// The most that slices_of() * total_q comes to for limits that are at most these.
-uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int max_kv) {
+
+template <typename T, int D>
+cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, cudaStream_t st) {
+  const int each = 32 / (D / 4), qh = a.c.kvh * a.c.group;
+  // four rows a lane where that still leaves the SMs 16 warps each
+  const bool many = int64_t(a.c.total_q) * qh >= int64_t(device_sm_count()) * 16 * 4 * each;
+  const int rows = 8 * each * (many ? 4 : 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((int64_t(a.c.max_q) * qh + rows - 1) / rows), a.c.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return many ? cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 4 * (128 / D)>, a, prefix, sl)
+              : cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D>, a, prefix, sl);
+}
+
+cudaError_t launch_join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, int dtype, cudaStream_t st) {
+  if (dtype == MP_DTYPE_BF16)
+    return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, prefix, sl, st) : join<__nv_bfloat16, 64>(a, prefix, sl, st);
+  return a.c.d == 128 ? join<float, 128>(a, prefix, sl, st) : join<float, 64>(a, prefix, sl, st);
+}
+
+// How a pass goes, by its rows per KV head: up to 32 through k_prefix_few, more on the tensor cores, fp32
+// on the CUDA cores. kTiles leaves one slice, kSlices as many as prefix_slices() says.
+enum Kind { kFew, kTiles, kSlices, kSimt };
+struct Pass {
+  Kind kind;
+  int slices;  // the most
+};
+Kind kind_of(const mp_cache_config* c, int total_q, int max_q, bool prefix) {
+  if (c->dtype != MP_DTYPE_BF16) return kSimt;
+  if (int64_t(max_q) * (c->q_heads / c->kv_heads) <= kFewRows) return kFew;
+  return prefix && prefix_in_slices(c, total_q, max_q) ? kSlices : kTiles;
+}
+Pass pass_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool prefix) {
+  const Kind kind = kind_of(c, total_q, max_q, prefix);
+  if (kind == kFew) return {kind, prefix_few_pieces(c, total_q, max_kv)};
+  if (kind == kTiles) return {kind, 1};
+  const int s = kind == kSlices ? prefix_slices(c, max_q, max_kv) : chunk_splits(c, max_q, max_kv);
+  // as many fewer where most packed rows belong to no sequence
+  return {kind, std::max(1, int(s * part_rows(c, total_q, max_q) / total_q))};
+}
+// The most that pass_of().slices * total_q comes to for limits that are at most these.
+uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool prefix) {
   const int group = c->q_heads / c->kv_heads;
   uint64_t most = uint64_t(total_q);
   if (c->dtype == MP_DTYPE_BF16) {
-    for (int q = 1; q <= max_q && chunk_is_step(group, q); ++q)
-      most = std::max(most, uint64_t(chunk_step_separate(c, q, max_kv)) * part_rows(c, total_q, q));
+    if (group <= kFewRows) most = std::max(most, uint64_t(prefix_few_rows_most(c, total_q, max_kv)));
+    // large tiles: the slices go by the tiles of a group, one where they are many
+    for (int64_t tiles = 1; prefix; ++tiles) {
+      const int q = int(std::min<int64_t>(max_q, std::max<int64_t>(1, tiles * 256 / group))), s = prefix_slices(c, q, max_kv);
+      most = std::max(most, uint64_t(s) * part_rows(c, total_q, q));
+      if (s == 1 || q == max_q) break;
+    }
     return most;
   }
   // the slices go by the number of row tiles: the largest max_q of each, until one slice is left
@@ -33,11 +183,12 @@ uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int m
     if (s == 1 || q == max_q) return most;
   }
 }
-uint64_t tc_bytes(const mp_cache_config* c, int max_q, int max_kv) {
+uint64_t tiles_bytes(const mp_cache_config* c, int max_q, int max_kv) {
   return chunk_on_tensor_cores(c, max_q) ? chunk_tc_workspace(c, max_q, max_kv) : 0;
 }
 uint64_t sums_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * c->head_dim * 4); }
 uint64_t ml_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * 2 * 4); }
+uint64_t pieces_bytes(const mp_cache_config* c) { return align256(uint64_t(c->batch) * c->kv_heads * 4); }
 
 int check(const mp_cache_config* c, const mp_cache_config* p, int total_q, int max_q, int max_kv, int max_group_q, int max_prefix) {
   int rc = check_cache(c);
@@ -48,21 +199,17 @@ int check(const mp_cache_config* c, const mp_cache_config* p, int total_q, int m
   return check_limits(p, total_q, max_group_q, max_prefix);
 }
 
-// One pass: its slices go to `part` and `ml`.
-cudaError_t pass(ChunkArgs a, int dtype, bool tensor_cores, int slices, float* part, float* ml, void* pieces, cudaStream_t st) {
-  a.out = nullptr;
-  a.lse = nullptr;
-  a.splits = slices;
-  a.joined = false;
-  a.cuts = nullptr;
-  if (tensor_cores) {
-    a.state = part;
-    a.state_ml = ml;
-    return launch_chunk_tc(a, pieces, st);
+// A pass of its own kernel; its slices lie at a.part and a.ml.
+cudaError_t launch_pass(ChunkArgs a, const Pass& pass, void* tiles, cudaStream_t st) {
+  a.splits = pass.slices;
+  if (pass.kind == kSimt) return launch_chunk_simt(a, st);
+  if (pass.kind == kTiles) {
+    a.state = a.part;
+    a.state_ml = a.ml;
+    a.part = a.ml = nullptr;
+    a.pieces = nullptr;
   }
-  a.part = part;
-  a.ml = ml;
-  return dtype == MP_DTYPE_BF16 ? launch_chunk_step(a, st) : launch_chunk_simt(a, st);
+  return launch_chunk_tc(a, tiles, st);
 }
 
 }  // namespace
@@ -81,9 +228,9 @@ int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_config*
   if (total_q == 0) return MP_OK;
   max_q = std::min(max_q, total_q);
   max_group_q = std::min(max_group_q, total_q);
-  const uint64_t rows = slice_rows_most(cfg, total_q, max_q, max_kv) + slice_rows_most(prefix_cfg, total_q, max_group_q, max_prefix);
-  *bytes = sums_bytes(cfg, rows) + ml_bytes(cfg, rows) +
-           std::max(tc_bytes(cfg, max_q, max_kv), tc_bytes(prefix_cfg, max_group_q, max_prefix));
+  const uint64_t rows = slice_rows_most(cfg, total_q, max_q, max_kv, false) + slice_rows_most(prefix_cfg, total_q, max_group_q, max_prefix, true);
+  *bytes = pieces_bytes(cfg) + pieces_bytes(prefix_cfg) + sums_bytes(cfg, rows) + ml_bytes(cfg, rows) +
+           std::max(tiles_bytes(cfg, max_q, max_kv), tiles_bytes(prefix_cfg, max_group_q, max_prefix));
   return MP_OK;
 }
 
@@ -108,51 +255,77 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     if (!aligned4(p)) return MP_ERR_INVALID_ARG;
   max_q = std::min(max_q, total_q);
   max_group_q = std::min(max_group_q, total_q);
-  const bool tc = chunk_on_tensor_cores(cfg, max_q), prefix_tc = chunk_on_tensor_cores(prefix_cfg, max_group_q);
-  const int own = slices_of(cfg, total_q, max_q, max_kv), shared = slices_of(prefix_cfg, total_q, max_group_q, max_prefix);
-  const uint64_t sums = sums_bytes(cfg, uint64_t(own + shared) * total_q), ml = ml_bytes(cfg, uint64_t(own + shared) * total_q);
-  const uint64_t need = sums + ml + std::max(tc_bytes(cfg, max_q, max_kv), tc_bytes(prefix_cfg, max_group_q, max_prefix));
+  const Pass own = pass_of(cfg, total_q, max_q, max_kv, false), shared = pass_of(prefix_cfg, total_q, max_group_q, max_prefix, true);
+  const uint64_t rows = uint64_t(own.slices + shared.slices) * total_q;
+  const uint64_t sums = sums_bytes(cfg, rows), ml = ml_bytes(cfg, rows), own_pieces = pieces_bytes(cfg), pre_pieces = pieces_bytes(prefix_cfg);
+  const uint64_t need = own_pieces + pre_pieces + sums + ml + std::max(own.kind == kTiles ? tiles_bytes(cfg, max_q, max_kv) : 0,
+                                                                       shared.kind == kTiles ? tiles_bytes(prefix_cfg, max_group_q, max_prefix) : 0);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MP_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MP_ERR_SCRATCH;
   if (injected("prefix")) return MP_ERR_INJECTED;
 
-  ChunkArgs a;
+  char* ws = static_cast<char*>(workspace);
+  Slices sl = {shared.slices, own.slices, nullptr, nullptr};
+  if (own.kind == kFew) sl.own_pieces = reinterpret_cast<int32_t*>(ws);
+  if (shared.kind == kFew || shared.kind == kSlices) sl.pre_pieces = reinterpret_cast<int32_t*>(ws + own_pieces);
+  ws += own_pieces + pre_pieces;
+  void* tiles = ws + sums + ml;
+  ChunkArgs p, a;
   a.c = cache_args(cfg, page_table, cu_q, kv_len, total_q, max_q, max_kv, status);
   a.q = q;
   a.keys = keys;
   a.values = values;
+  a.out = nullptr;
+  a.lse = nullptr;
+  a.splits = 1;
+  a.joined = false;
+  a.cuts = nullptr;
 #if MP_CHECK
   a.stall = injected("prefix_wait");
 #endif
-  ChunkArgs p = a;
+  p = a;
   p.c = cache_args(prefix_cfg, prefix_table, cu_q, prefix_len, total_q, max_group_q, max_prefix, status);
   p.c.cu_group = cu_group;
   p.c.sequences = cfg->batch;
   p.keys = prefix_keys;
   p.values = prefix_values;
-  char* ws = static_cast<char*>(workspace);
-  float *part0 = reinterpret_cast<float*>(ws), *ml0 = reinterpret_cast<float*>(ws + sums);
-  void* pieces = ws + sums + ml;
+  p.pieces = sl.pre_pieces;
   const int64_t slice = int64_t(total_q) * cfg->q_heads;
+  p.part = reinterpret_cast<float*>(ws);
+  p.ml = reinterpret_cast<float*>(ws + sums);
+  a.part = p.part + shared.slices * slice * cfg->head_dim;
+  a.ml = p.ml + shared.slices * slice * 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  {
-    ProfScope ps(st, K_PREFIX_ATTEND);
-    if (pass(p, cfg->dtype, prefix_tc, shared, part0, ml0, pieces, st) != cudaSuccess) return MP_ERR_CUDA;
-  }
-  {
+  if (own.kind != kFew) {
     ProfScope ps(st, K_CHUNK_ATTEND);
-    if (pass(a, cfg->dtype, tc, own, part0 + shared * slice * cfg->head_dim, ml0 + shared * slice * 2, pieces, st) != cudaSuccess)
-      return MP_ERR_CUDA;
+    if (launch_pass(a, own, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
+  }
+  // few rows: both passes in one launch where both have them
+  if (own.kind == kFew || shared.kind == kFew) {
+    PrefixFew few;
+    few.pre = p;
+    few.own = a;
+    few.groups = shared.kind == kFew ? prefix_cfg->batch : 0;
+    few.own_units = own.kind == kFew;
+    few.most_shared = shared.slices;
+    few.most_own = own.slices;
+    few.pre_pieces = sl.pre_pieces;
+    few.own_pieces = sl.own_pieces;
+    const int most_q = std::max(own.kind == kFew ? max_q : 1, shared.kind == kFew ? max_group_q : 1);
+    ProfScope ps(st, K_PREFIX_FEW);
+    if (launch_prefix_few(few, most_q * (cfg->q_heads / cfg->kv_heads), st) != cudaSuccess) return MP_ERR_CUDA;
+  }
+  if (shared.kind != kFew) {
+    ProfScope ps(st, K_PREFIX_ATTEND);
+    if (launch_pass(p, shared, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   a.out = out;
   a.lse = lse;
-  a.splits = shared + own;
-  a.joined = false;
-  a.part = part0;
-  a.ml = ml0;
+  a.part = p.part;
+  a.ml = p.ml;
   ProfScope ps(st, K_PREFIX_JOIN);
-  return launch_prefix_join(a, p.c, shared, cfg->dtype, st) == cudaSuccess ? MP_OK : MP_ERR_CUDA;
+  return launch_join(a, p.c, sl, cfg->dtype, st) == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
 
 }  // extern "C"

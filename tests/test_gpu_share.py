@@ -325,6 +325,28 @@ def test_prefix_attention(mp, dtype, hq, hk, d, page, q_lens, kv, groups, prefix
     assert c.status.item() == 0
 
 
+@pytest.mark.parametrize("hq,hk,d,page,q_lens,groups,prefixes", [
+    (32, 8, 128, 64, [1] * 20, [20], [9000]),          # 80 rows: several steps of each half
+    (40, 40, 64, 16, [1] * 20, [20], [12000]),         # many steps of each half
+    (16, 16, 128, 0, [1] * 24, [24], [7777]),
+    (32, 8, 64, 48, [1] * 11, [5, 6], [5000, 900]),    # pieces of two prefixes in one CTA
+    (16, 2, 128, 16, [1] * 40, [40], [6000]),          # 320 rows: two tiles side by side
+    (16, 2, 64, 0, [3] * 30, [30], [6001]),
+    (40, 40, 128, 32, [1] * 300, [300], [700]),        # more tiles than half of the SMs: equal runs
+])
+def test_prefix_attention_of_long_prefixes(mp, hq, hk, d, page, q_lens, groups, prefixes):
+    c = Shared(mp, "bf16", hq, hk, d, page, [m + 2 for m in q_lens], groups, prefixes)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1], hq, d, by=1.5)
+    first = None
+    for _ in range(20):  # many at once, so that they load the memory
+        out, lse = attend_prefix(mp, c, q, cu, cu_t, max(q_lens))
+        first = first if first is not None else out
+        assert torch.equal(out, first)
+    check_prefix(c, "bf16", q, cu, out, lse)
+    assert c.status.item() == 0
+
+
 def test_prefix_attention_over_pages_of_another_size(mp):
     """The prefixes' cache is another one: short pages here, a dense one there."""
     for page, ppage in ((16, 128), (64, 0), (0, 48)):
