@@ -470,7 +470,8 @@ MP_API int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_
  * prefix alone.
  *   cfg, q, cu_q, kv_len, total_q, max_q, max_kv, keys, values, page_table, out, lse : as
  *              mp_chunk_attention takes them, of the sequences' own slots.
- *   prefix_cfg : the prefixes' cache: batch = groups; heads, head_dim and dtype as in cfg.
+ *   prefix_cfg : the prefixes' cache: batch = groups; heads, head_dim and dtype as in cfg. Sequences and
+ *              groups together are at most 65535 (MP_ERR_UNSUPPORTED).
  *   cu_group   : device int32 [groups + 1], not decreasing, from 0 to at most cfg.batch.
  *   prefix_len : device int32 [groups], the slots of each prefix (0 is allowed).
  *   max_group_q, max_prefix : limits as max_q and max_kv: packed rows of any group, slots of any

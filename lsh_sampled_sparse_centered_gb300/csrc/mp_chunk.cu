@@ -7,6 +7,8 @@
 // and the unnormalised sum of 2^(x - m) v; keys past a row's own slot enter as -infinity.
 // The slots can be split over several CTAs; each then stores (m, l, sum) and k_chunk_join
 // combines them.
+#include <algorithm>
+
 #include "mp_cache.cuh"
 
 namespace mp {
@@ -74,9 +76,9 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // row / 8 % 2 for Q, key % 16 for P, 0 for V (with d = 64 3 % slower than padding).
 // Products run as packed pairs, over pairs of d for S and of rows for O. V arrives under S and
 // the softmax, the next K under the product with V.
-// GROUP: the rows of a group over the prefix that its sequences share.
+// GROUP: b may be a group, whose rows go over the prefix that its sequences share (c.cu_group is set).
 template <int D, bool GROUP>
-__global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const ChunkArgs a) {
+__device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b) {
   constexpr bool kPad = D == 64;
   constexpr int kRow = D + kPad * 4, kPt = kBM + kPad * 4;
   auto place = [](int at, int x) { return kPad ? at : at ^ (x * 4); };  // of a chunk's first float
@@ -86,9 +88,9 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
   float* vs = ks + kBN * kRow;   // [64][kRow]
   float* pt = vs + kBN * kRow;   // [64 keys][kPt]
   const CacheArgs& c = a.c;
-  const int b = blockIdx.z, h = blockIdx.y;
+  const int h = blockIdx.y;
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
-  const Seq s = rows_of<GROUP>(c, b);
+  const Seq s = GROUP && c.cu_group ? group_of(c, b) : seq_of(c, b);
   const int rows = s.m * c.group, r0 = tile * kBM;
   if (r0 >= rows) return;
   const int qh = c.kvh * c.group;
@@ -244,6 +246,17 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
   }
 }
 
+template <int D>
+__global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const ChunkArgs a) {
+  chunk_simt_tile<D, false>(a, blockIdx.z);
+}
+// Groups over their prefixes and sequences over their own slots in one launch.
+template <int D>
+__global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_prefix_simt(const __grid_constant__ ChunkArgs pre, const __grid_constant__ ChunkArgs own) {
+  const int groups = pre.c.batch, b = blockIdx.z;
+  chunk_simt_tile<D, true>(b < groups ? pre : own, b < groups ? b : b - groups);
+}
+
 // Joins the splits' (m, l, sum) of a query row, in an order that is fixed by their number:
 // WARPS warps per row (8 where there are many splits, so that their loads overlap) take
 // eight splits at a time each. Started while the slices still run (its launch costs as much
@@ -363,13 +376,24 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
   }
 }
 
-template <int D, bool GROUP>
+constexpr int simt_smem(int d) { return (3 * 64 * (d + (d == 64 ? 4 : 0)) + 64 * (64 + (d == 64 ? 4 : 0))) * 4; }
+template <int D>
 cudaError_t chunk_simt(const ChunkArgs& a, cudaStream_t st) {
-  constexpr int pad = D == 64 ? 4 : 0, smem = (3 * 64 * (D + pad) + 64 * (64 + pad)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_chunk_simt<D, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = simt_smem(D);
+  cudaError_t e = cudaFuncSetAttribute(k_chunk_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t(a.c.max_q) * a.c.group + kBM - 1) / kBM;
-  k_chunk_simt<D, GROUP><<<dim3(unsigned(tiles * a.splits), a.c.kvh, a.c.batch), kThr, smem, st>>>(a);
+  k_chunk_simt<D><<<dim3(unsigned(tiles * a.splits), a.c.kvh, a.c.batch), kThr, smem, st>>>(a);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t prefix_simt(const ChunkArgs& pre, const ChunkArgs& own, cudaStream_t st) {
+  constexpr int smem = simt_smem(D);
+  cudaError_t e = cudaFuncSetAttribute(k_prefix_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  int64_t x = 1;
+  for (const ChunkArgs* a : {&pre, &own}) x = std::max(x, (int64_t(a->c.max_q) * a->c.group + kBM - 1) / kBM * a->splits);
+  k_prefix_simt<D><<<dim3(unsigned(x), own.c.kvh, pre.c.batch + own.c.batch), kThr, smem, st>>>(pre, own);
   return cudaGetLastError();
 }
 template <typename T, int D>
@@ -408,8 +432,10 @@ int chunk_splits(const mp_cache_config* c, int max_q, int max_kv) {
 }
 
 cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st) {
-  if (a.c.cu_group) return a.c.d == 128 ? chunk_simt<128, true>(a, st) : chunk_simt<64, true>(a, st);
-  return a.c.d == 128 ? chunk_simt<128, false>(a, st) : chunk_simt<64, false>(a, st);
+  return a.c.d == 128 ? chunk_simt<128>(a, st) : chunk_simt<64>(a, st);
+}
+cudaError_t launch_prefix_simt(const ChunkArgs& pre, const ChunkArgs& own, cudaStream_t st) {
+  return own.c.d == 128 ? prefix_simt<128>(pre, own, st) : prefix_simt<64>(pre, own, st);
 }
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st) {
   if (dtype == MP_DTYPE_BF16) return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, st) : join<__nv_bfloat16, 64>(a, st);

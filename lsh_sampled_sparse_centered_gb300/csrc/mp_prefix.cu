@@ -21,13 +21,17 @@ struct Slices {
 };
 
 // Joins the slices' (m, l, sum) of a sequence's query rows, in their order. A warp takes ROWS rows (of
-// D / 4 lanes each, 16 bytes a lane) and has the loads of kAtOnce slices of each in flight. The first
+// D / 4 lanes each, 16 bytes a lane) and has the loads of kAtOnce slices of each in flight; with WARPS > 1
+// as many warps share the slices of their rows, so that all of them are in flight together. The first
 // `shared` slices are of the prefix, the `own` behind them of the own slots; where their numbers are kept
 // per (group or sequence, KV head), as many of them are there. Rows without a prefix have none of it.
 // Grid: rows of a sequence x sequences, so that what has to be looked up does not hang on a row.
-template <typename T, int D, int ROWS>
+template <typename T, int D, int ROWS, int WARPS>
 __global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const CacheArgs prefix, const Slices sl) {
-  constexpr int kLanes = D / 4, kTurns = ROWS * kLanes / 32, kAtOnce = ROWS == 32 / kLanes ? 8 : 2;
+  constexpr int kLanes = D / 4, kTurns = ROWS * kLanes / 32, kAtOnce = kTurns == 1 ? 8 : 2;
+  static_assert(WARPS == 1 || kTurns == 1);
+  __shared__ float4 so[WARPS > 1 ? 8 : 1][32];
+  __shared__ float2 sml[WARPS > 1 ? 8 : 1][32];
   const CacheArgs& c = a.c;
   const int qh = c.kvh * c.group, b = blockIdx.y;
   const int64_t rows = int64_t(c.total_q) * qh;
@@ -41,8 +45,8 @@ __global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const Ca
   }
   const Seq g = group_of(prefix, lo);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t first = (int64_t(blockIdx.x) * 8 + warp) * ROWS, mine = int64_t(s.m) * qh;
-  if (first >= mine) return;
+  const int64_t first = (int64_t(blockIdx.x) * (8 / WARPS) + warp / WARPS) * ROWS, mine = int64_t(s.m) * qh;
+  if (WARPS == 1 && first >= mine) return;
   float m[kTurns], l[kTurns];
   float4 o[kTurns];
   int64_t row[kTurns];
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const Ca
     o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  for (int i0 = 0; i0 < most; i0 += kAtOnce) {
+  for (int i0 = warp % WARPS * kAtOnce; i0 < most; i0 += WARPS * kAtOnce) {
     float2 v[kTurns][kAtOnce];
     float4 x[kTurns][kAtOnce];
 #pragma unroll
@@ -105,6 +109,34 @@ __global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const Ca
       }
     }
   }
+  if (WARPS > 1) {  // the warps' parts, in their order
+    so[warp][lane] = o[0];
+    sml[warp][lane] = make_float2(m[0], l[0]);
+    __syncthreads();
+    if (warp % WARPS != 0) return;
+    float2 v[WARPS];
+    float4 x[WARPS];
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      v[w] = sml[warp + w][lane];
+      x[w] = so[warp + w][lane];
+      top = fmaxf(top, v[w].x);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    m[0] = top;
+    l[0] = 0.f;
+    o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float by = v[w].y == 0.f ? 0.f : exp2f(v[w].x - ref);
+      l[0] = fmaf(v[w].y, by, l[0]);
+      o[0].x = fmaf(x[w].x, by, o[0].x);
+      o[0].y = fmaf(x[w].y, by, o[0].y);
+      o[0].z = fmaf(x[w].z, by, o[0].z);
+      o[0].w = fmaf(x[w].w, by, o[0].w);
+    }
+  }
 #pragma unroll
   for (int j = 0; j < kTurns; ++j) {
     if (row[j] < 0) continue;
@@ -120,9 +152,11 @@ __global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const Ca
 template <typename T, int D>
 cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, cudaStream_t st) {
   const int each = 32 / (D / 4), qh = a.c.kvh * a.c.group;
-  // four rows a lane where that still leaves the SMs 16 warps each
-  const bool many = int64_t(a.c.total_q) * qh >= int64_t(device_sm_count()) * 16 * 4 * each;
-  const int rows = 8 * each * (many ? 4 : 1);
+  // four rows a lane where that still leaves the SMs 16 warps each, four warps a row where there are at
+  // most 8 rows an SM (32 tokens of 32 heads: 76 and 73 us a call with one and four, 128: 232 and 239)
+  const int64_t all = int64_t(a.c.total_q) * qh / each, sms = device_sm_count();
+  const bool many = all >= sms * 16 * 4, few = all <= sms * 8;
+  const int rows = each * (many ? 32 : (few ? 2 : 8));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((int64_t(a.c.max_q) * qh + rows - 1) / rows), a.c.batch);
   cfg.blockDim = dim3(256);
@@ -132,14 +166,29 @@ cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 4 * (128 / D)>, a, prefix, sl)
-              : cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D>, a, prefix, sl);
+  if (many) return cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 4 * (128 / D), 1>, a, prefix, sl);
+  return few ? cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D, 4>, a, prefix, sl)
+             : cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D, 1>, a, prefix, sl);
 }
 
 cudaError_t launch_join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, int dtype, cudaStream_t st) {
   if (dtype == MP_DTYPE_BF16)
     return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, prefix, sl, st) : join<__nv_bfloat16, 64>(a, prefix, sl, st);
   return a.c.d == 128 ? join<float, 128>(a, prefix, sl, st) : join<float, 64>(a, prefix, sl, st);
+}
+
+// fp32: slices of as few 64-slot tiles as leave all CTAs of both passes room on the SMs at once: a tile
+// is 7 us (101 rows over 2000 shared slots of eight KV heads, d = 64: 57 us with slices of four tiles in
+// two launches).
+int simt_fit(const mp_cache_config* c) { return (c->head_dim == 64 ? 3 : 2) * device_sm_count(); }
+int64_t simt_ctas(const mp_cache_config* c, int max_q, int slices) {
+  const int64_t group = c->q_heads / c->kv_heads;
+  return (max_q * group + kChunkRows - 1) / kChunkRows * c->kv_heads * c->batch * slices;
+}
+int simt_slices(int max_kv, int tiles) { return std::min(64, (max_kv + 64 * tiles - 1) / (64 * tiles)); }
+// of one pass alone, which are not fewer
+int simt_slices_most(const mp_cache_config* c, int max_q, int max_kv) {
+  return int(std::max<int64_t>(1, std::min<int64_t>({simt_fit(c) / simt_ctas(c, max_q, 1), (int64_t(max_kv) + 63) / 64, 64})));
 }
 
 // How a pass goes, by its rows per KV head: up to 32 through k_prefix_few, more on the tensor cores, fp32
@@ -158,7 +207,7 @@ Pass pass_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool 
   const Kind kind = kind_of(c, total_q, max_q, prefix);
   if (kind == kFew) return {kind, prefix_few_pieces(c, total_q, max_kv)};
   if (kind == kTiles) return {kind, 1};
-  const int s = kind == kSlices ? prefix_slices(c, max_q, max_kv) : chunk_splits(c, max_q, max_kv);
+  const int s = kind == kSlices ? prefix_slices(c, max_q, max_kv) : simt_slices_most(c, max_q, max_kv);
   // as many fewer where most packed rows belong to no sequence
   return {kind, std::max(1, int(s * part_rows(c, total_q, max_q) / total_q))};
 }
@@ -178,7 +227,7 @@ uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int m
   }
   // the slices go by the number of row tiles: the largest max_q of each, until one slice is left
   for (int64_t rows = (int64_t(group) + kChunkRows - 1) / kChunkRows * kChunkRows;; rows += kChunkRows) {
-    const int q = int(std::min<int64_t>(max_q, rows / group)), s = chunk_splits(c, q, max_kv);
+    const int q = int(std::min<int64_t>(max_q, rows / group)), s = simt_slices_most(c, q, max_kv);
     most = std::max(most, uint64_t(s) * part_rows(c, total_q, q));
     if (s == 1 || q == max_q) return most;
   }
@@ -195,6 +244,7 @@ int check(const mp_cache_config* c, const mp_cache_config* p, int total_q, int m
   if (rc != MP_OK) return rc;
   if ((rc = check_cache(p)) != MP_OK) return rc;
   if (p->kv_heads != c->kv_heads || p->q_heads != c->q_heads || p->head_dim != c->head_dim || p->dtype != c->dtype) return MP_ERR_INVALID_ARG;
+  if (c->batch + p->batch > 65535) return MP_ERR_UNSUPPORTED;  // one grid's z
   if ((rc = check_limits(c, total_q, max_q, max_kv)) != MP_OK) return rc;
   return check_limits(p, total_q, max_group_q, max_prefix);
 }
@@ -202,7 +252,6 @@ int check(const mp_cache_config* c, const mp_cache_config* p, int total_q, int m
 // A pass of its own kernel; its slices lie at a.part and a.ml.
 cudaError_t launch_pass(ChunkArgs a, const Pass& pass, void* tiles, cudaStream_t st) {
   a.splits = pass.slices;
-  if (pass.kind == kSimt) return launch_chunk_simt(a, st);
   if (pass.kind == kTiles) {
     a.state = a.part;
     a.state_ml = a.ml;
@@ -255,7 +304,15 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     if (!aligned4(p)) return MP_ERR_INVALID_ARG;
   max_q = std::min(max_q, total_q);
   max_group_q = std::min(max_group_q, total_q);
-  const Pass own = pass_of(cfg, total_q, max_q, max_kv, false), shared = pass_of(prefix_cfg, total_q, max_group_q, max_prefix, true);
+  Pass own = pass_of(cfg, total_q, max_q, max_kv, false), shared = pass_of(prefix_cfg, total_q, max_group_q, max_prefix, true);
+  if (own.kind == kSimt) {
+    int tiles = 1;
+    while (tiles * 64 < std::max(max_kv, max_prefix) && simt_ctas(cfg, max_q, simt_slices(max_kv, tiles)) +
+               simt_ctas(prefix_cfg, max_group_q, simt_slices(max_prefix, tiles)) > simt_fit(cfg))
+      ++tiles;
+    own.slices = std::min(own.slices, simt_slices(max_kv, tiles));
+    shared.slices = std::min(shared.slices, simt_slices(max_prefix, tiles));
+  }
   const uint64_t rows = uint64_t(own.slices + shared.slices) * total_q;
   const uint64_t sums = sums_bytes(cfg, rows), ml = ml_bytes(cfg, rows), own_pieces = pieces_bytes(cfg), pre_pieces = pieces_bytes(prefix_cfg);
   const uint64_t need = own_pieces + pre_pieces + sums + ml + std::max(own.kind == kTiles ? tiles_bytes(cfg, max_q, max_kv) : 0,
@@ -297,7 +354,14 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   a.ml = p.ml + shared.slices * slice * 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  if (own.kind != kFew) {
+  const bool simt = own.kind == kSimt;
+  if (simt) {
+    a.splits = own.slices;
+    p.splits = shared.slices;
+    ProfScope ps(st, K_CHUNK_ATTEND);
+    if (launch_prefix_simt(p, a, st) != cudaSuccess) return MP_ERR_CUDA;
+  }
+  if (own.kind != kFew && !simt) {
     ProfScope ps(st, K_CHUNK_ATTEND);
     if (launch_pass(a, own, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
   }
@@ -316,7 +380,7 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     ProfScope ps(st, K_PREFIX_FEW);
     if (launch_prefix_few(few, most_q * (cfg->q_heads / cfg->kv_heads), st) != cudaSuccess) return MP_ERR_CUDA;
   }
-  if (shared.kind != kFew) {
+  if (shared.kind != kFew && !simt) {
     ProfScope ps(st, K_PREFIX_ATTEND);
     if (launch_pass(p, shared, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
   }

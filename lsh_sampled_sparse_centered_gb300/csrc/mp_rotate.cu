@@ -18,7 +18,9 @@ namespace mp {
 namespace {
 
 constexpr int kThr = 256;
-constexpr int kAtOnce = 4;  // keys of a lane whose loads are in flight together
+constexpr int kOneAtOnce = 2, kOwnAtOnce = 1;  // keys of a lane that are worked on, as many more are on their way
+constexpr int kResident = 3;  // CTAs of an SM
+constexpr int kRounds = 2;
 
 struct RotateArgs {
   CacheArgs c;
@@ -44,6 +46,7 @@ struct Vec<float> {
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
+  static constexpr float kSign = 1.f;
   // The quarter of the turn is taken off first, so that the rest is small and its float exact enough.
   static __device__ __forceinline__ void turn(uint32_t phase, float* s, float* c) {
     const uint32_t quarter = (phase + 0x20000000u) >> 30;
@@ -75,9 +78,12 @@ struct Vec<__nv_bfloat16> {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // off by 2^-21 in [-pi, pi], a 2^12th of what the result's rounding takes
+  // The fraction's upper 23 bits as a mantissa, which takes no conversion (those go through the unit of
+  // the sines): half a turn less than the angle, so that both come out with the other sign. They are off by
+  // 2^-21 in [-pi, pi] and the angle by 2^-22, a 2^11th of what the result's rounding takes.
+  static constexpr float kSign = -1.f;
   static __device__ __forceinline__ void turn(uint32_t phase, float* s, float* c) {
-    const float x = float(int32_t(phase)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float x = (__uint_as_float(0x3f800000u | (phase >> 9)) - 1.5f) * 6.283185307179586f;
     *s = __sinf(x);
     *c = __cosf(x);
   }
@@ -85,49 +91,51 @@ struct Vec<__nv_bfloat16> {
 
 // ONE: a slot's heads stand at one position. TWO: the new frequencies are others.
 template <typename T, bool ONE, bool TWO>
-__global__ void __launch_bounds__(kThr) k_cache_rotate(const RotateArgs a) {
-  constexpr int V = Vec<T>::N;
-  __shared__ uint64_t turns[2][64];  // a position's fraction of a turn
+__global__ void __launch_bounds__(kThr, kResident) k_cache_rotate(const RotateArgs a) {
+  constexpr int V = Vec<T>::N, kAtOnce = ONE ? kOneAtOnce : kOwnAtOnce;
+  __shared__ uint2 turns[TWO ? 2 : 1][64];  // a position's fraction of a turn (lower, upper half): pair j of lane i at j lanes + i
   const CacheArgs& c = a.c;
   const int half = a.rot / 2, b = blockIdx.z;
   for (int i = threadIdx.x; i < (TWO ? 2 : 1) * 64; i += kThr) {
     const int k = i >> 6, p = i & 63;
-    if (p >= half) continue;
-    const double t = (k ? a.to_freq : a.from_freq)[p] * 0.15915494309189533577;  // 1 / 2 pi
-    turns[k][p] = static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
+    if (p >= a.lanes * V) continue;
+    const double t = p < half ? (k ? a.to_freq : a.from_freq)[p] * 0.15915494309189533577 : 0.0;  // 1 / 2 pi
+    const uint64_t per = static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
+    turns[k][p % V * a.lanes + p / V] = make_uint2(uint32_t(per), uint32_t(per >> 32));
   }
   __syncthreads();
   const Seq s = seq_of(c, b);
   const int lane = threadIdx.x & (a.lanes - 1), own = threadIdx.x / a.lanes, per = kThr / a.lanes;
   const int p0 = lane * V;  // the lane's first pair
   if (p0 >= half) return;
-  uint64_t from_turn[V], to_turn[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int p = min(p0 + j, half - 1);
-    from_turn[j] = turns[0][p];
-    to_turn[j] = turns[TWO ? 1 : 0][p];
-  }
   const int e0 = a.interleaved ? 2 * p0 : p0, e1 = a.interleaved ? 2 * p0 + V : half + p0;  // its two vectors
   const bool whole = p0 + V <= half;
   const int64_t head_stride = int64_t(c.page_size) * c.d;
   T* keys = static_cast<T*>(a.keys);
 
-  auto angles = [&](int slot, int h, float (&cs)[V], float (&sn)[V]) {
-    const int64_t at = (int64_t(b) * a.position_heads + (ONE ? 0 : h)) * a.position_cols + slot;
-    const int64_t from = a.from ? a.from[at] : slot, to = a.to ? a.to[at] : slot;
+  const float scale = a.scale * Vec<T>::kSign;
+  // upper half of position * turn modulo 2^64
+  auto phase = [](int32_t position, uint2 turn) {
+    return __umulhi(uint32_t(position), turn.x) + uint32_t(position) * turn.y - (position < 0 ? turn.x : 0u);
+  };
+  auto angles = [&](int32_t from, int32_t to, float (&cs)[V], float (&sn)[V]) {
+    const int32_t by = int32_t(uint32_t(to) - uint32_t(from));
+    const bool near = int64_t(to) - from == by;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const uint64_t phase = TWO ? uint64_t(to) * to_turn[j] - uint64_t(from) * from_turn[j] : uint64_t(to - from) * from_turn[j];
-      Vec<T>::turn(uint32_t((phase + 0x80000000ull) >> 32), &sn[j], &cs[j]);
-      sn[j] *= a.scale;
-      cs[j] *= a.scale;
+      const uint2 turn = turns[0][j * a.lanes + lane];
+      uint32_t x;
+      if (TWO) x = phase(to, turns[TWO ? 1 : 0][j * a.lanes + lane]) - phase(from, turn);
+      else x = near ? phase(by, turn) : phase(to, turn) - phase(from, turn);
+      Vec<T>::turn(x, &sn[j], &cs[j]);
+      sn[j] *= scale;
+      cs[j] *= scale;
     }
   };
-  auto apply = [&](T* row, const uint4& u0, const uint4& u1, const float (&cs)[V], const float (&sn)[V]) {
+  auto apply = [&](T* row, const uint4 (&u)[2], const float (&cs)[V], const float (&sn)[V]) {
     float x[V], y[V], x2[V], y2[V];
-    Vec<T>::unpack(u0, x);
-    Vec<T>::unpack(u1, y);
+    Vec<T>::unpack(u[0], x);
+    Vec<T>::unpack(u[1], y);
     if (a.interleaved) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -149,55 +157,91 @@ __global__ void __launch_bounds__(kThr) k_cache_rotate(const RotateArgs a) {
         y2[j] = y[j] * cs[j] + x[j] * sn[j];
       }
     }
-    *reinterpret_cast<uint4*>(row + e0) = Vec<T>::pack(x2);
-    *reinterpret_cast<uint4*>(row + e1) = Vec<T>::pack(y2);
+    __stcs(reinterpret_cast<uint4*>(row + e0), Vec<T>::pack(x2));
+    __stcs(reinterpret_cast<uint4*>(row + e1), Vec<T>::pack(y2));
   };
-  // element offset of a slot's key of head h, or -1
-  auto row_of = [&](int slot, int h) -> int64_t {
+  // the key of a slot and head 0 (ONE) or blockIdx.y, and where it stands; at < 0: none
+  struct Key {
+    int64_t at;
+    int32_t from, to;
+  };
+  const int h = ONE ? 0 : blockIdx.y;
+  auto find = [&](int64_t slot64) {
+    Key k = {-1, 0, 0};
+    if (slot64 >= s.n) return k;
+    const int slot = int(slot64);
+    const int64_t where = (int64_t(b) * a.position_heads + h) * a.position_cols + slot;
+    k.from = a.from ? a.from[where] : slot;
+    k.to = a.to ? a.to[where] : slot;
     const int col = c.page_shift >= 0 ? slot >> c.page_shift : slot / c.page_size;
     const int p = page_at(c.table, c.cols, c.n_pages, b, col, c.status);
-    return p < 0 ? -1 : ((int64_t(p) * c.kvh + h) * c.page_size + (slot - col * c.page_size)) * c.d;
+    if (p >= 0) k.at = ((int64_t(p) * c.kvh + h) * c.page_size + (slot - col * c.page_size)) * c.d;
+    return k;
+  };
+  auto load = [&](int64_t at, uint4 (&u)[2]) {
+    if (at < 0) return;
+    u[0] = __ldcs(reinterpret_cast<const uint4*>(keys + at + e0));
+    u[1] = __ldcs(reinterpret_cast<const uint4*>(keys + at + e1));
   };
 
-  const int step = gridDim.x * per;
+  // A batch of keys is worked on while the next one's loads are in flight, and the one after that is looked up.
+  const int64_t step = int64_t(gridDim.x) * per;
+  int64_t slot = int64_t(blockIdx.x) * per + own;
+  uint4 u[kAtOnce][2], ahead[kAtOnce][2];
   if (ONE) {
-    for (int slot = blockIdx.x * per + own; slot < s.n; slot += step) {
-      const int64_t at = row_of(slot, 0);
-      if (at < 0) continue;
+    Key now = find(slot), next = find(slot + step);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (k < c.kvh) load(now.at < 0 ? -1 : now.at + k * head_stride, ahead[k]);
+    for (; slot < s.n; slot += step) {
+      const Key later = find(slot + 2 * step);
       float cs[V], sn[V];
-      angles(slot, 0, cs, sn);
+      angles(now.from, now.to, cs, sn);
       for (int h0 = 0; h0 < c.kvh; h0 += kAtOnce) {
-        uint4 u[kAtOnce][2];
+        const bool last = h0 + kAtOnce >= c.kvh;
+        const Key& k2 = last ? next : now;
+        const int h2 = last ? 0 : h0 + kAtOnce;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          u[k][0] = ahead[k][0];
+          u[k][1] = ahead[k][1];
+        }
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k)
-          if (h0 + k < c.kvh) {
-            const T* row = keys + at + (h0 + k) * head_stride;
-            u[k][0] = *reinterpret_cast<const uint4*>(row + e0);
-            u[k][1] = *reinterpret_cast<const uint4*>(row + e1);
-          }
+          if (h2 + k < c.kvh) load(k2.at < 0 ? -1 : k2.at + (h2 + k) * head_stride, ahead[k]);
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k)
-          if (h0 + k < c.kvh) apply(keys + at + (h0 + k) * head_stride, u[k][0], u[k][1], cs, sn);
+          if (h0 + k < c.kvh && now.at >= 0) apply(keys + now.at + (h0 + k) * head_stride, u[k], cs, sn);
       }
+      now = next;
+      next = later;
     }
   } else {
-    const int h = blockIdx.y;
-    for (int slot = blockIdx.x * per + own; slot < s.n; slot += kAtOnce * step) {
-      uint4 u[kAtOnce][2];
-      int64_t at[kAtOnce];
+    Key now[kAtOnce], next[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) now[k] = find(slot + k * step);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) load(now[k].at, ahead[k]);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) next[k] = find(slot + (kAtOnce + k) * step);
+    for (; slot < s.n; slot += kAtOnce * step) {
+      Key later[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        at[k] = slot + int64_t(k) * step < s.n ? row_of(slot + k * step, h) : -1;
-        if (at[k] < 0) continue;
-        u[k][0] = *reinterpret_cast<const uint4*>(keys + at[k] + e0);
-        u[k][1] = *reinterpret_cast<const uint4*>(keys + at[k] + e1);
+        u[k][0] = ahead[k][0];
+        u[k][1] = ahead[k][1];
+        load(next[k].at, ahead[k]);
+        later[k] = find(slot + (2 * kAtOnce + k) * step);
       }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        if (at[k] < 0) continue;
-        float cs[V], sn[V];
-        angles(slot + k * step, h, cs, sn);
-        apply(keys + at[k], u[k][0], u[k][1], cs, sn);
+        if (now[k].at >= 0) {
+          float cs[V], sn[V];
+          angles(now[k].from, now[k].to, cs, sn);
+          apply(keys + now[k].at, u[k], cs, sn);
+        }
+        now[k] = next[k];
+        next[k] = later[k];
       }
     }
   }
@@ -206,10 +250,10 @@ __global__ void __launch_bounds__(kThr) k_cache_rotate(const RotateArgs a) {
 template <typename T>
 cudaError_t launch(const RotateArgs& a, cudaStream_t st) {
   const bool one = a.position_heads == 1 || (!a.from && !a.to), two = a.to_freq != nullptr;
-  const int heads = one ? 1 : a.c.kvh, per = kThr / a.lanes * (one ? 1 : kAtOnce);
+  const int heads = one ? 1 : a.c.kvh, per = kThr / a.lanes * (one ? 1 : kOwnAtOnce);
   // CTAs that fit, and one more round of them: what a CTA sets up is paid once for all its slots
   const int64_t units = int64_t(a.c.batch) * heads, most = (int64_t(a.c.max_kv) + per - 1) / per;
-  const int64_t fill = std::max<int64_t>(1, 8 * int64_t(device_sm_count()) / units);
+  const int64_t fill = std::max<int64_t>(1, kRounds * kResident * int64_t(device_sm_count()) / units);
   const dim3 grid(unsigned(std::min(most, fill)), unsigned(heads), unsigned(a.c.batch));
   if (one) {
     if (two) k_cache_rotate<T, true, true><<<grid, kThr, 0, st>>>(a);
