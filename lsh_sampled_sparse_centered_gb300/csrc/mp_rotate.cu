@@ -119,17 +119,24 @@ __global__ void __launch_bounds__(kThr, kResident) k_cache_rotate(const RotateAr
     return __umulhi(uint32_t(position), turn.x) + uint32_t(position) * turn.y - (position < 0 ? turn.x : 0u);
   };
   auto angles = [&](int32_t from, int32_t to, float (&cs)[V], float (&sn)[V]) {
-    const int32_t by = int32_t(uint32_t(to) - uint32_t(from));
-    const bool near = int64_t(to) - from == by;
+    if (!TWO) {
+      // by |to - from|, which fits 32 bits without a sign, and the other way round where it is less than 0
+      const uint32_t by = to < from ? uint32_t(from) - uint32_t(to) : uint32_t(to) - uint32_t(from);
+      const float back = to < from ? -scale : scale;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint2 turn = turns[0][j * a.lanes + lane];
-      uint32_t x;
-      if (TWO) x = phase(to, turns[TWO ? 1 : 0][j * a.lanes + lane]) - phase(from, turn);
-      else x = near ? phase(by, turn) : phase(to, turn) - phase(from, turn);
-      Vec<T>::turn(x, &sn[j], &cs[j]);
-      sn[j] *= scale;
-      cs[j] *= scale;
+      for (int j = 0; j < V; ++j) {
+        const uint2 turn = turns[0][j * a.lanes + lane];
+        Vec<T>::turn(__umulhi(by, turn.x) + by * turn.y, &sn[j], &cs[j]);
+        sn[j] *= back;
+        cs[j] *= scale;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        Vec<T>::turn(phase(to, turns[TWO ? 1 : 0][j * a.lanes + lane]) - phase(from, turns[0][j * a.lanes + lane]), &sn[j], &cs[j]);
+        sn[j] *= scale;
+        cs[j] *= scale;
+      }
     }
   };
   auto apply = [&](T* row, const uint4 (&u)[2], const float (&cs)[V], const float (&sn)[V]) {
