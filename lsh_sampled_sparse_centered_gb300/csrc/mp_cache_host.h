@@ -52,6 +52,13 @@ inline int check_rotary(const mp_rotary* r, const mp_cache_config* c) {
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// log2 of a power of two, else -1
+inline int shift_of(int n) {
+  for (int i = 0; i < 31; ++i)
+    if (n == 1 << i) return i;
+  return -1;
+}
+
 inline CacheArgs cache_args(const mp_cache_config* c, const int32_t* table, const int32_t* cu_q, const int32_t* kv_len,
                             int total_q, int max_q, int max_kv, uint32_t* status) {
   CacheArgs a;
@@ -62,9 +69,7 @@ inline CacheArgs cache_args(const mp_cache_config* c, const int32_t* table, cons
   a.page_size = c->page_size;
   a.n_pages = c->n_pages;
   a.cols = c->max_pages;
-  a.page_shift = -1;
-  for (int i = 0; i < 31; ++i)
-    if (c->page_size == 1 << i) a.page_shift = i;
+  a.page_shift = shift_of(c->page_size);
   a.table = table;
   a.cu_q = cu_q;
   a.kv_len = kv_len;

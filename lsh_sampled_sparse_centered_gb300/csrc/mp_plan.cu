@@ -19,7 +19,7 @@ namespace mp {
 namespace {
 
 struct PlanArgs {
-  int batch, page_size, cols, n_pages, max_rows;
+  int batch, page_size, page_shift, cols, n_pages, max_rows;
   const int32_t *change, *base, *kv_len, *n_free;
   int32_t *table, *free, *new_len, *new_free, *cu_q, *positions, *slots, *row_seq;
   uint32_t* status;
@@ -42,32 +42,36 @@ __device__ __forceinline__ int owner(const uint32_t* at, int n, uint32_t x) {
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
   extern __shared__ uint32_t sm[];
-  __shared__ int64_t sums[3][32];
+  __shared__ uint32_t sums[3][32];
   const int batch = a.batch, threads = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* rows = sm;                    // [batch + 1], before each sequence
   uint32_t* taken = rows + batch + 1;     // [batch + 1] pages
   uint32_t* back = taken + batch + 1;     // [batch + 1] pages
   int* old_len = reinterpret_cast<int*>(back + batch + 1);  // [batch]
   int* left = old_len + batch;            // [batch]: of the old slots
+  int* base = left + batch;               // [batch]
   const int rank = CLUSTER ? int(blockIdx.x) : 0, ctas = CLUSTER ? int(gridDim.x) : 1;
-  auto pages = [&](int n) { return int((uint32_t(n) + uint32_t(a.page_size) - 1u) / uint32_t(a.page_size)); };
+  auto pages = [&](int n) {
+    const uint32_t up = uint32_t(n) + uint32_t(a.page_size) - 1u;
+    return int(a.page_shift >= 0 ? up >> a.page_shift : up / uint32_t(a.page_size));
+  };
   const int64_t cap = int64_t(a.cols) * a.page_size;
   uint32_t wrong = 0;
 
-  int n_free = 0;
-  if (a.table) {
-    const int given = *a.n_free;
-    n_free = max(0, min(given, a.n_pages));
-    if (n_free != given) wrong |= MP_STATUS_BAD_LENGTH;
-  }
-  // Sums are 64-bit; kept are 32 bits of them, cut where no comparison below tells the difference.
-  int64_t carry[3] = {0, 0, 0};
+  const int given_free = a.table ? *a.n_free : 0;
+  const int n_free = max(0, min(given_free, a.n_pages));
+  if (a.table && n_free != given_free) wrong |= MP_STATUS_BAD_LENGTH;
+  // Sums stop at a value that no comparison below tells from a larger one, so 32 bits hold them (rows and
+  // pages are at most 2^30 each: a table's pages have 16 slots or more): min(a + b, top) is associative.
+  const uint32_t top[3] = {uint32_t(a.max_rows) + 1, uint32_t(a.table ? a.n_pages : 0) + 1, uint32_t(a.table ? a.n_pages : 0) + 1};
+  uint32_t carry[3] = {0, 0, 0};
   if (tid == 0) rows[0] = taken[0] = back[0] = 0;
   for (int b0 = 0; b0 < batch; b0 += threads) {
     const int b = b0 + tid;
-    int64_t v[3] = {0, 0, 0};
+    uint32_t v[3] = {0, 0, 0};
     if (b < batch) {
       const int given = a.kv_len[b], x = a.change[b];
+      base[b] = a.base ? a.base[b] : 0;
       const int n = int(max(int64_t(0), min(int64_t(given), cap)));
       int grow = max(x, 0);
       if (n != given || int64_t(n) + grow > cap) wrong |= MP_STATUS_BAD_LENGTH;
@@ -75,18 +79,18 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
       const int keep = int(max(int64_t(0), int64_t(n) + min(x, 0)));
       old_len[b] = n;
       left[b] = keep;
-      v[0] = grow;
+      v[0] = min(uint32_t(grow), top[0]);
       if (a.table) {
-        v[1] = pages(n + grow) - pages(n);
-        v[2] = pages(n) - pages(keep);
+        v[1] = min(uint32_t(pages(n + grow) - pages(n)), top[1]);
+        v[2] = min(uint32_t(pages(n) - pages(keep)), top[2]);
       }
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, v[k], o);
-        if (lane >= o) v[k] += up;
+        const uint32_t up = __shfl_up_sync(0xffffffffu, v[k], o);
+        if (lane >= o) v[k] = min(v[k] + up, top[k]);
       }
     if (lane == 31)
 #pragma unroll
@@ -94,25 +98,25 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const int64_t mine = lane < threads / 32 ? sums[k][lane] : 0;
-      int64_t pre = lane < warp ? mine : 0, all = mine;
+      uint32_t all = lane < threads / 32 ? sums[k][lane] : 0;  // of the warps up to this lane's
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        pre += __shfl_xor_sync(0xffffffffu, pre, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all = min(all + up, top[k]);
       }
-      v[k] += carry[k] + pre;
-      carry[k] += all;
+      const uint32_t pre = __shfl_sync(0xffffffffu, all, max(0, warp - 1));
+      v[k] = min(carry[k] + min(v[k] + (warp ? pre : 0), top[k]), top[k]);
+      carry[k] = min(carry[k] + __shfl_sync(0xffffffffu, all, 31), top[k]);
     }
     if (b < batch) {
-      rows[b + 1] = uint32_t(min(v[0], int64_t(a.max_rows) + 1));
-      taken[b + 1] = uint32_t(min(v[1], int64_t(a.n_pages) + 1));
-      back[b + 1] = uint32_t(min(v[2], int64_t(a.n_pages) - n_free));
+      rows[b + 1] = v[0];
+      taken[b + 1] = v[1];
+      back[b + 1] = min(v[2], uint32_t(a.n_pages - n_free));
     }
     __syncthreads();
   }
   if (CLUSTER) cluster_arrive();  // this CTA has read the lengths and n_free
-  if (carry[2] > a.n_pages - n_free) wrong |= MP_STATUS_BAD_LENGTH;
+  if (carry[2] > uint32_t(a.n_pages - n_free)) wrong |= MP_STATUS_BAD_LENGTH;
   const uint32_t list = uint32_t(n_free) + back[batch];  // free pages and those given back
   int served = 0;                                        // sequences before the first that has to wait
   for (int b0 = 0; b0 < batch; b0 += threads) {
@@ -122,40 +126,66 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
   if (served < batch) wrong |= MP_STATUS_NO_ROOM;
   const uint32_t all_rows = rows[served], all_taken = taken[served];
 
-  // entry e of the list
-  auto entry = [&](uint32_t e) {
-    int p;
-    if (e < uint32_t(n_free)) {
-      p = a.free[e];
-    } else {
-      const int b = owner(back, batch, e - n_free);
-      p = a.table[int64_t(b) * a.cols + pages(left[b]) + int(e - n_free - back[b])];
-    }
+  // where entry e of the list lies
+  auto entry = [&](uint32_t e) -> const int32_t* {
+    if (e < uint32_t(n_free)) return a.free + e;
+    const int b = owner(back, batch, e - n_free);
+    return a.table + int64_t(b) * a.cols + pages(left[b]) + int(e - n_free - back[b]);
+  };
+  auto checked = [&](int p) {
     if (p < 0 || p >= a.n_pages) wrong |= MP_STATUS_BAD_PAGE;
     return p;
   };
+  // What each of the three loops below waits for is a load per element, at a place that the searches in
+  // shared memory give: kAtOnce of them are in flight.
+  constexpr int kAtOnce = 4;
   const uint32_t first = uint32_t(rank * threads + tid), step = uint32_t(ctas * threads);
   if (a.positions || a.slots || a.row_seq) {
-    for (uint32_t r = first; r < all_rows; r += step) {
-      const int b = owner(rows, served, r), slot = old_len[b] + int(r - rows[b]);
-      if (a.positions) a.positions[r] = int(uint32_t(a.base ? a.base[b] : 0) + uint32_t(slot));
-      if (a.row_seq) a.row_seq[r] = b;
-      if (a.slots) {
-        const int col = int(uint32_t(slot) / uint32_t(a.page_size)), had = pages(old_len[b]);
-        int p = b;
-        if (a.table) p = col < had ? a.table[int64_t(b) * a.cols + col] : entry(list - 1 - (taken[b] + uint32_t(col - had)));
-        const bool good = p >= 0 && p < a.n_pages;
-        if (!good) wrong |= MP_STATUS_BAD_PAGE;
-        a.slots[r] = good ? p * a.page_size + (slot - col * a.page_size) : -1;
+    for (uint32_t r0 = first; r0 < all_rows; r0 += kAtOnce * step) {
+      int b[kAtOnce], slot[kAtOnce], page[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const uint32_t r = r0 + k * step;
+        if (r >= all_rows) continue;
+        b[k] = owner(rows, served, r);
+        slot[k] = old_len[b[k]] + int(r - rows[b[k]]);
+        page[k] = b[k];
+        if (a.slots && a.table) {
+          const int col = pages(slot[k] + 1) - 1, had = pages(old_len[b[k]]);
+          page[k] = *(col < had ? a.table + int64_t(b[k]) * a.cols + col : entry(list - 1 - (taken[b[k]] + uint32_t(col - had))));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const uint32_t r = r0 + k * step;
+        if (r >= all_rows) continue;
+        if (a.positions) a.positions[r] = int(uint32_t(base[b[k]]) + uint32_t(slot[k]));
+        if (a.row_seq) a.row_seq[r] = b[k];
+        if (a.slots) {
+          const int p = checked(page[k]), at = slot[k] - (pages(slot[k] + 1) - 1) * a.page_size;
+          a.slots[r] = p >= 0 && p < a.n_pages ? p * a.page_size + at : -1;
+        }
       }
     }
   }
   for (uint32_t i = first; i < all_taken; i += step) {
     const int b = owner(taken, served, i);
-    a.table[int64_t(b) * a.cols + pages(old_len[b]) + int(i - taken[b])] = entry(list - 1 - i);
+    a.table[int64_t(b) * a.cols + pages(old_len[b]) + int(i - taken[b])] = checked(*entry(list - 1 - i));
   }
   // pages given back and not taken again
-  for (uint32_t e = uint32_t(n_free) + first; e + all_taken < list; e += step) a.free[e] = entry(e);
+  for (uint32_t e0 = uint32_t(n_free) + first; e0 + all_taken < list; e0 += kAtOnce * step) {
+    int page[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t e = e0 + k * step;
+      page[k] = e + all_taken < list ? *entry(e) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t e = e0 + k * step;
+      if (e + all_taken < list) a.free[e] = checked(page[k]);
+    }
+  }
   if (CLUSTER) cluster_wait();
   for (int b = int(first); b < batch; b += int(step)) {
     a.new_len[b] = left[b] + (b < served ? int(rows[b + 1] - rows[b]) : 0);
@@ -168,13 +198,15 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
   if (wrong) flag(a.status, wrong);
 }
 
-size_t plan_smem(int batch) { return (size_t(batch) * 5 + 3) * 4; }
+size_t plan_smem(int batch) { return (size_t(batch) * 6 + 3) * 4; }
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
   const bool many = std::max(a.batch, a.max_rows) > kMostThreads;
   const size_t smem = plan_smem(a.batch);
-  cudaError_t e = cudaFuncSetAttribute(many ? k_cache_plan<true> : k_cache_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
+  if (smem > 40 * 1024) {  // 48 KB with the static part need no asking
+    const cudaError_t e = cudaFuncSetAttribute(many ? k_cache_plan<true> : k_cache_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(many ? kCluster : 1);
   cfg.blockDim = dim3(std::min(kMostThreads, (std::max(a.batch, std::min(a.max_rows, kMostThreads)) + 31) / 32 * 32));
@@ -229,6 +261,7 @@ extern "C" int mp_cache_plan(const mp_cache_config* cfg, const int32_t* change, 
   PlanArgs a;
   a.batch = cfg->batch;
   a.page_size = cfg->page_size;
+  a.page_shift = shift_of(cfg->page_size);
   a.cols = cfg->max_pages;
   a.n_pages = cfg->n_pages;
   a.max_rows = max_rows;
