@@ -4,9 +4,9 @@
 // The free pages with those given back behind them are one list e = 0, 1, ..., free + back - 1, of
 // which the a-th page taken is entry free + back - 1 - a: where an entry lies (in the list as it was,
 // or in the table of a sequence that shrinks) follows from the sums, so that no page has to be moved
-// before another can be taken. What is read (entries below n_free, pages of sequences that shrink, old
-// pages of those that grow) is written by no one, except lengths and n_free where they are updated in
-// place: those are written behind a barrier.
+// before another can be taken. What this reads (entries below n_free, pages of sequences that shrink) is
+// written by no one, except lengths and n_free where they are updated in place: those are written behind
+// a barrier, and so are the rows, which read their pages from the tables.
 //
 // Bound by latency: the sums are formed by every CTA for itself (a few reads a sequence) and rows and
 // pages are shared out to one CTA, or a cluster of eight where there are many.
@@ -115,7 +115,6 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
     }
     __syncthreads();
   }
-  if (CLUSTER) cluster_arrive();  // this CTA has read the lengths and n_free
   if (carry[2] > uint32_t(a.n_pages - n_free)) wrong |= MP_STATUS_BAD_LENGTH;
   const uint32_t list = uint32_t(n_free) + back[batch];  // free pages and those given back
   int served = 0;                                        // sequences before the first that has to wait
@@ -136,38 +135,10 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
     if (p < 0 || p >= a.n_pages) wrong |= MP_STATUS_BAD_PAGE;
     return p;
   };
-  // What each of the three loops below waits for is a load per element, at a place that the searches in
-  // shared memory give: kAtOnce of them are in flight.
+  // What the loops over rows and pages given back wait for is a load per element, at a place that shared
+  // memory gives: kAtOnce of them are in flight.
   constexpr int kAtOnce = 4;
   const uint32_t first = uint32_t(rank * threads + tid), step = uint32_t(ctas * threads);
-  if (a.positions || a.slots || a.row_seq) {
-    for (uint32_t r0 = first; r0 < all_rows; r0 += kAtOnce * step) {
-      int b[kAtOnce], slot[kAtOnce], page[kAtOnce];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const uint32_t r = r0 + k * step;
-        if (r >= all_rows) continue;
-        b[k] = owner(rows, served, r);
-        slot[k] = old_len[b[k]] + int(r - rows[b[k]]);
-        page[k] = b[k];
-        if (a.slots && a.table) {
-          const int col = pages(slot[k] + 1) - 1, had = pages(old_len[b[k]]);
-          page[k] = *(col < had ? a.table + int64_t(b[k]) * a.cols + col : entry(list - 1 - (taken[b[k]] + uint32_t(col - had))));
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const uint32_t r = r0 + k * step;
-        if (r >= all_rows) continue;
-        if (a.positions) a.positions[r] = int(uint32_t(base[b[k]]) + uint32_t(slot[k]));
-        if (a.row_seq) a.row_seq[r] = b[k];
-        if (a.slots) {
-          const int p = checked(page[k]), at = slot[k] - (pages(slot[k] + 1) - 1) * a.page_size;
-          a.slots[r] = p >= 0 && p < a.n_pages ? p * a.page_size + at : -1;
-        }
-      }
-    }
-  }
   for (uint32_t i = first; i < all_taken; i += step) {
     const int b = owner(taken, served, i);
     a.table[int64_t(b) * a.cols + pages(old_len[b]) + int(i - taken[b])] = checked(*entry(list - 1 - i));
@@ -186,7 +157,74 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
       if (e + all_taken < list) a.free[e] = checked(page[k]);
     }
   }
-  if (CLUSTER) cluster_wait();
+  // The pages taken are in the tables, and every CTA has read the lengths and n_free.
+  if (CLUSTER) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  // kAtOnce rows from r0 on, `by` apart and before `end`; b_of says whose a row is
+  auto write_rows = [&](uint32_t r0, uint32_t by, uint32_t end, auto b_of) {
+    int b[kAtOnce], slot[kAtOnce], page[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t r = r0 + k * by;
+      if (r >= end) continue;
+      b[k] = b_of(r);
+      slot[k] = old_len[b[k]] + int(r - rows[b[k]]);
+      page[k] = b[k];
+      if (a.slots && a.table) page[k] = __ldcg(a.table + int64_t(b[k]) * a.cols + (pages(slot[k] + 1) - 1));
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t r = r0 + k * by;
+      if (r >= end) continue;
+      if (a.positions) a.positions[r] = int(uint32_t(base[b[k]]) + uint32_t(slot[k]));
+      if (a.row_seq) a.row_seq[r] = b[k];
+      if (a.slots) {
+        const int p = checked(page[k]), at = slot[k] - (pages(slot[k] + 1) - 1) * a.page_size;
+        a.slots[r] = p >= 0 && p < a.n_pages ? p * a.page_size + at : -1;
+      }
+    }
+  };
+  const bool any_rows = a.positions || a.slots || a.row_seq;
+  if (any_rows && !CLUSTER) {
+    for (uint32_t r = first; r < all_rows; r += kAtOnce * step) write_rows(r, step, all_rows, [&](uint32_t at) { return owner(rows, served, at); });
+  }
+  if (any_rows && CLUSTER) {
+    // Many rows: a search each is more than all the rest, so a tile's owners are marked where their rows
+    // begin and carried on by a running maximum (31000 rows of 1000 sequences: 6 us of searches).
+    uint32_t* own = reinterpret_cast<uint32_t*>(base + batch);  // [kAtOnce * threads]
+    const uint32_t most = uint32_t(kAtOnce * threads), share = (all_rows + ctas - 1) / ctas, tile = min(most, max(1u, share));
+    for (uint32_t begin = rank * tile; begin < all_rows; begin += ctas * tile) {
+      const uint32_t end = min(all_rows, begin + tile);
+      for (uint32_t i = tid; i < most; i += threads) own[i] = 0;
+      __syncthreads();
+      const int b0 = owner(rows, served, begin), b1 = owner(rows, served, end - 1);
+      for (int b = b0 + tid; b <= b1; b += threads)
+        if (rows[b + 1] > rows[b]) own[max(rows[b], begin) - begin] = uint32_t(b);
+      __syncthreads();
+      uint32_t v[kAtOnce], high = 0;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) v[k] = high = max(high, own[tid * kAtOnce + k]);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, high, o);
+        if (lane >= o) high = max(high, up);
+      }
+      if (lane == 31) sums[0][warp] = high;
+      __syncthreads();
+      uint32_t before = __reduce_max_sync(0xffffffffu, lane < warp ? sums[0][lane] : 0u);
+      const uint32_t up = __shfl_up_sync(0xffffffffu, high, 1);
+      if (lane > 0) before = max(before, up);
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) own[tid * kAtOnce + k] = max(v[k], before);
+      __syncthreads();
+      write_rows(begin + tid, threads, end, [&](uint32_t at) { return int(own[at - begin]); });
+      __syncthreads();  // own and sums are written again
+    }
+  }
   for (int b = int(first); b < batch; b += int(step)) {
     a.new_len[b] = left[b] + (b < served ? int(rows[b + 1] - rows[b]) : 0);
     a.cu_q[b] = int(min(rows[b], all_rows));
@@ -198,18 +236,19 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
   if (wrong) flag(a.status, wrong);
 }
 
-size_t plan_smem(int batch) { return (size_t(batch) * 6 + 3) * 4; }
+size_t plan_smem(int batch, int threads) { return (size_t(batch) * 6 + 3 + 4 * threads) * 4; }
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
   const bool many = std::max(a.batch, a.max_rows) > kMostThreads;
-  const size_t smem = plan_smem(a.batch);
+  const int threads = std::min(kMostThreads, (std::max(a.batch, std::min(a.max_rows, kMostThreads)) + 31) / 32 * 32);
+  const size_t smem = plan_smem(a.batch, threads);
   if (smem > 40 * 1024) {  // 48 KB with the static part need no asking
     const cudaError_t e = cudaFuncSetAttribute(many ? k_cache_plan<true> : k_cache_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(many ? kCluster : 1);
-  cfg.blockDim = dim3(std::min(kMostThreads, (std::max(a.batch, std::min(a.max_rows, kMostThreads)) + 31) / 32 * 32));
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
