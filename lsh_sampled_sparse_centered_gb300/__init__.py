@@ -277,9 +277,9 @@ def _cache_calls():
     loader = importlib.machinery.ExtensionFileLoader("_mp_calls", path)
     mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mp_calls", loader))
     loader.exec_module(mod)
-    mod.bind(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
-        "mp_cache_append", "mp_chunk_attention", "mp_cache_weights", "mp_cache_evict", "mp_cache_plan", "mp_prefix_attention",
-        "mp_cache_rotate")))
+    address = lambda f: ctypes.cast(getattr(_lib, f), _P).value
+    mod.bind(*map(address, ("mp_cache_append", "mp_chunk_attention", "mp_cache_weights", "mp_cache_evict")))
+    mod.bind_shared(*map(address, ("mp_cache_plan", "mp_prefix_attention", "mp_cache_rotate")))
     _calls = mod
     return mod
 

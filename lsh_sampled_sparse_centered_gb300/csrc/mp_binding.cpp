@@ -397,27 +397,34 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
-// bind(append, attend, weights, evict, plan, prefix, rotate): addresses of the entry points
-PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  constexpr int kEntries = 7;
-  void* p[kEntries];
-  if (n != kEntries) return PyErr_Format(PyExc_TypeError, "%d addresses are needed", kEntries);
-  for (int i = 0; i < kEntries; ++i) {
+// The entry points' addresses, in the order of `to`.
+template <int N>
+PyObject* take(PyObject* const* args, Py_ssize_t n, void** const (&to)[N]) {
+  void* p[N];
+  if (n != N) return PyErr_Format(PyExc_TypeError, "%d addresses are needed", N);
+  for (int i = 0; i < N; ++i) {
     p[i] = PyLong_AsVoidPtr(args[i]);
     if (!p[i]) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "a null address");
   }
-  g_append = reinterpret_cast<decltype(g_append)>(p[0]);
-  g_attend = reinterpret_cast<decltype(g_attend)>(p[1]);
-  g_weights = reinterpret_cast<decltype(g_weights)>(p[2]);
-  g_evict = reinterpret_cast<decltype(g_evict)>(p[3]);
-  g_plan = reinterpret_cast<decltype(g_plan)>(p[4]);
-  g_prefix = reinterpret_cast<decltype(g_prefix)>(p[5]);
-  g_rotate = reinterpret_cast<decltype(g_rotate)>(p[6]);
+  for (int i = 0; i < N; ++i) *to[i] = p[i];
   Py_RETURN_NONE;
+}
+template <typename F>
+void** place(F& f) {
+  return reinterpret_cast<void**>(&f);
+}
+// bind(append, attend, weights, evict)
+PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return take<4>(args, n, {place(g_append), place(g_attend), place(g_weights), place(g_evict)});
+}
+// bind_shared(plan, prefix, rotate)
+PyObject* bind_shared(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return take<3>(args, n, {place(g_plan), place(g_prefix), place(g_rotate)});
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f))
 PyMethodDef methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
+                         {"bind_shared", FAST(bind_shared), METH_FASTCALL, nullptr},
                          {"append", FAST((call<append, 17>)), METH_FASTCALL, nullptr},
                          {"attend", FAST((call<attend, 14>)), METH_FASTCALL, nullptr},
                          {"weights", FAST((call<weights, 12>)), METH_FASTCALL, nullptr},

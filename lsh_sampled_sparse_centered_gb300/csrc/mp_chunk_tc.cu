@@ -67,10 +67,16 @@ static_assert(kKeys / 16 <= 8, "boxes of 16 rows at least");
 // What a launch works on, and where its sums go.
 enum Mode {
   kChunk,  // chunks over their sequences' slots: out and lse
-  kOwn,    // the same, a row's sum to a.state, to be joined with that over its prefix
-  kRuns,   // the rows of groups over the prefixes that their sequences share, a row's sum to a.state
-  kCuts,   // the same in slices: every tile of a group is cut into as many pieces of its keys
+  kBoth,   // groups' rows over the prefixes that their sequences share, and chunks over their own slots: sums to a.state
+  kCuts,   // groups over their prefixes in slices: every tile of a group is cut into as many pieces of its keys
   kPairs,  // the same with at most 128 rows a group: the halves share them and take every other step
+};
+
+// The prefixes of kBoth: its units are the groups, and behind them the sequences of `a`.
+struct Prefixes {
+  CacheArgs c;
+  int box, groups;
+  int64_t own_slice;  // where the own slots' sums begin, in rows of a.state
 };
 
 template <int D>
@@ -189,8 +195,9 @@ __device__ int longest_piece(const int* steps, const int* tiles, int groups, int
 template <int D, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkArgs a,
-               const int box, const int b_begin, const int b_end, const int slot_rows) {
-  constexpr bool GROUP = MODE == kRuns || MODE == kCuts || MODE == kPairs, STATE = MODE == kOwn || MODE == kRuns;
+               const int box, const int b_begin, const int b_end, const int slot_rows, const __grid_constant__ CUtensorMap tmK0,
+               const __grid_constant__ CUtensorMap tmV0, const __grid_constant__ Prefixes pre) {
+  constexpr bool BOTH = MODE == kBoth;
   constexpr bool PAIR = MODE == kPairs, CUT = MODE == kCuts || PAIR;
   extern __shared__ __align__(1024) unsigned char smraw[];
   const uint32_t base = saddr(smraw);
@@ -205,6 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile uint32_t* abort = &S.abort;
   const int qh = c.kvh * c.group;
+  auto rows_at = [&](int b) {
+    if constexpr (BOTH) return b < pre.groups ? group_of(pre.c, b) : seq_of(c, b - pre.groups);
+    else return rows_of<CUT>(c, b);
+  };
 
   if (threadIdx.x == 320) {
     for (int i = 0; i < kStages; ++i) {
@@ -248,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(kGroup * sizeof(Seq) <= kKeys * 128, "one tile of the ring");
   int longest = 0;  // steps of a tile
   for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
-    const Seq s = rows_of<GROUP>(c, b);
+    const Seq s = rows_at(b);
     const int tiles = tiles_of(s, c.group);
     if (CUT) {
       if (lane == 0) {
@@ -490,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u0 == 0 && !whole) {
               // this CTA begins the tile; the CTAs of the units up to the tile's last go on with it
               cut.row = int64_t(s.row0) * qh + h * c.group;
+              if (BOTH && b >= pre.groups) cut.row += pre.own_slice;
               cut.slot = slot;
               cut.r0 = t * kRows;
               cut.rows = min(kRows, s.m * c.group - t * kRows);
@@ -508,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               left = 0;
               break;
             }
-            s = rows_of<GROUP>(c, b);
+            s = rows_at(b);
             tiles = tiles_of(s, c.group);
           } while (tiles == 0);
         }
@@ -530,10 +542,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Where the boxes of a tile lie (eight at most), for four steps at a time and one such round
         // ahead: a page looked up when its box is due cost every tile that wait (a ragged batch over
         // pages of 16: 2 us a step).
+        const bool shared = BOTH && pc.b < pre.groups;
+        const CacheArgs& cache = shared ? pre.c : c;
+        const int cb = BOTH && !shared ? pc.b - pre.groups : pc.b, rows_of_box = shared ? pre.box : box;
         auto look = [&](int u) {
-          const int n = u * kKeys + (lane >> 3) * kKeys + (lane & 7) * box;
-          const bool any = u + (lane >> 3) < pc.u1 && (lane & 7) * box < kKeys && n < pc.n;
-          return any ? slot_row(c, pc.b, pc.h, n) : 0;
+          const int n = u * kKeys + (lane >> 3) * kKeys + (lane & 7) * rows_of_box;
+          const bool any = u + (lane >> 3) < pc.u1 && (lane & 7) * rows_of_box < kKeys && n < pc.n;
+          return any ? slot_row(cache, cb, pc.h, n) : 0;
         };
         int rows = 0, ahead = look(pc.u0);
         for (int u = pc.u0; u < pc.u1 && ok; ++u) {
@@ -544,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = __shfl_sync(0xffffffffu, rows, ((u - pc.u0) & 3) * 8 + (lane & 7));
           const int n0 = u * kKeys;
           const int live = max(0, min(kKeys, pc.n - n0));  // rows that hold slots of the sequence
-          const int boxes = (live + box - 1) / box;
+          const int boxes = (live + rows_of_box - 1) / rows_of_box;
           for (int kv = 0; kv < 2; ++kv) {
             // Q behind five tiles in the memory's queue came 7 us late, so the first K waits for it alone
             if (CUT && i == 0 && u == pc.u0 && kv == 1) {
@@ -558,14 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool patch = kv == 1 && live < kKeys;
             uint64_t* bar = patch ? &S.tail : &S.full[st];
             if (lane == 0) {
-              mbar_expect_tx(bar, uint32_t(boxes) * box * kRowBytes * kSub);
+              mbar_expect_tx(bar, uint32_t(boxes) * rows_of_box * kRowBytes * kSub);
               S.filled[st] = uint8_t(ph);
             }
             __syncwarp();
             if (lane < boxes) {
 #pragma unroll
               for (int s = 0; s < kSub; ++s)
-                tma_load_2d(&S.kv[st][s][lane * box * 64], kv ? &tmV : &tmK, s * 64, row, bar);
+                tma_load_2d(&S.kv[st][s][lane * rows_of_box * 64], shared ? (kv ? &tmV0 : &tmK0) : (kv ? &tmV : &tmK), s * 64, row, bar);
             }
             if (patch) {
               ok = __all_sync(0xffffffffu, mbar_wait(&S.tail, tails & 1, abort));
@@ -959,9 +974,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after();
         const float sum = lo2(l0) + hi2(l0) + lo2(l1) + hi2(l1);
-        if (CUT) {
+        if (CUT || (BOTH && pc.whole)) {
           // the sums of this piece: a slice of its rows
-          const int64_t slice = int64_t(pc.slot) * c.total_q * qh;
+          const int64_t slice = BOTH ? (pc.b < pre.groups ? 0 : pre.own_slice) : int64_t(pc.slot) * c.total_q * qh;
+          float *const to_ml = BOTH ? a.state_ml : a.ml, *const to_part = BOTH ? a.state : a.part;
           const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + 256;
           float by0 = 1.f, by1 = 0.f, top = m, all_sum = sum;
           if (PAIR) {
@@ -982,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             by1 = a1.y == 0.f ? 0.f : exp2f(a1.x - top);
             all_sum = fmaf(a0.y, by0, a1.y * by1);
           }
-          if (r < rows && (!PAIR || half == 0)) *reinterpret_cast<float2*>(a.ml + (slice + row) * 2) = make_float2(top, all_sum);
+          if (r < rows && (!PAIR || half == 0)) *reinterpret_cast<float2*>(to_ml + (slice + row) * 2) = make_float2(top, all_sum);
           constexpr int kBlocks = PAIR ? D / 64 : D / 32;  // of 32 columns
           const int g0 = PAIR ? half * kBlocks : 0;
           uint32_t mine[kBlocks][32], others[PAIR ? kBlocks : 1][32];
@@ -1029,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               const int64_t to_row = __shfl_sync(0xffffffffu, row, (lane & ~3) + k);
               if (r - (lane & 3) + k < rows) {
-                float4* dst = reinterpret_cast<float4*>(a.part + (slice + to_row) * D + (g0 + g) * 32 + (lane & 3) * 8);
+                float4* dst = reinterpret_cast<float4*>(to_part + (slice + to_row) * D + (g0 + g) * 32 + (lane & 3) * 8);
                 dst[0] = make_float4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]);
                 dst[1] = make_float4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]);
               }
@@ -1044,7 +1060,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = int64_t(pc.slot) * slot_rows + (r - pc.r0);
         if (real) {
           if (!whole) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m, sum);
-          else if (STATE) *reinterpret_cast<float2*>(a.state_ml + row * 2) = make_float2(m, sum);
           else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
         }
         uint32_t all[D / 32][32];
@@ -1064,14 +1079,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 8; ++i)
                 dst[i * slot_rows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                  __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-            }
-          } else if (STATE) {
-            if (real && sum > 0.f) {
-              float4* dst = reinterpret_cast<float4*>(a.state + row * D + g * 32);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                     __uint_as_float(o[4 * i + 3]));
             }
           } else {
             // Four lanes swap their rows' 16-byte parts, so that each store writes 64 bytes of a row.
@@ -1123,6 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows, a lane each, and 8 columns. Partial sums lie [slot][column / 4][row][4], so that
 // the threads that own rows (in the kernel above and here) write and read whole lines. Set up
 // while k_chunk_tc still runs; it waits for it first.
+// STATE: to a.state and a.state_ml, unnormalised.
 template <int D, bool STATE>
 __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const int slot_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1196,11 +1204,18 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
                         bf2(o[1].x * inv, o[1].y * inv), bf2(o[1].z * inv, o[1].w * inv));
 }
 
+// CTAs of kBoth for the prefixes and the own slots of these limits (either may be missing).
+int both_ctas(const CacheArgs* own, const CacheArgs* pre) {
+  int n = 0;
+  for (const CacheArgs* c : {own, pre})
+    if (c) n += chunk_tc_ctas(c->batch, c->kvh, c->group, c->max_q, c->max_kv);
+  return std::min(n, device_sm_count());
+}
 int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
 
 template <int D, Mode MODE>
-cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
-  constexpr bool STATE = MODE == kOwn || MODE == kRuns, CUT = MODE == kCuts || MODE == kPairs;
+cudaError_t launch(ChunkArgs a, const ChunkArgs* shared, bool own, void* workspace, cudaStream_t st) {
+  constexpr bool BOTH = MODE == kBoth, CUT = MODE == kCuts || MODE == kPairs;
   const CacheArgs& c = a.c;
   CUtensorMap mk, mv;
   const int box = box_rows(c.table, c.page_size);
@@ -1208,11 +1223,30 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
   if (!make_map(&mk, a.keys, D, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&mv, a.values, D, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  CUtensorMap mk0 = mk, mv0 = mv;
+  Prefixes pre = {};
+  int units = c.batch, max_q = c.max_q;
+  if (BOTH) {
+    units = own ? c.batch : 0;
+    if (!own) max_q = 1;
+    if (shared) {
+      pre.c = shared->c;
+      pre.groups = pre.c.batch;
+      pre.box = box_rows(pre.c.table, pre.c.page_size);
+      const uint64_t pre_rows = uint64_t(pre.c.n_pages) * c.kvh * pre.c.page_size;
+      if (!make_map(&mk0, shared->keys, D, pre_rows, 64, pre.box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+          !make_map(&mv0, shared->values, D, pre_rows, 64, pre.box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+      units += pre.groups;
+      max_q = std::max(max_q, pre.c.max_q);
+    }
+    pre.own_slice = a.own_slice;
+  }
   const size_t smem = sizeof(Smem<D>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  const int ctas = chunk_tc_ctas(c.batch, c.kvh, c.group, c.max_q, c.max_kv);
-  const int slot_rows = slot_rows_of(c.group, c.max_q);
+  const int ctas = BOTH ? both_ctas(own ? &c : nullptr, shared ? &shared->c : nullptr) : chunk_tc_ctas(c.batch, c.kvh, c.group, c.max_q, c.max_kv);
+  const int slot_rows = slot_rows_of(c.group, max_q);
   if (!CUT) {
     char* ws = static_cast<char*>(workspace);
     a.cuts = ws;
@@ -1221,7 +1255,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
     ws += align256(uint64_t(2 * ctas) * slot_rows * 8);
     a.part = reinterpret_cast<float*>(ws);
   }
-  for (int b = 0; b < c.batch; b += kGroup) {
+  for (int b = 0; b < units; b += kGroup) {
     cudaLaunchConfig_t cfg = {};
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -1233,14 +1267,15 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t st) {
       cfg.gridDim = dim3(ctas);
       cfg.blockDim = dim3(kThreads);
       cfg.dynamicSmemBytes = smem;
-      if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc<D, MODE>, mk, mv, ChunkArgs(a), box, b, std::min(c.batch, b + kGroup), slot_rows)) != cudaSuccess)
+      if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc<D, MODE>, mk, mv, ChunkArgs(a), box, b, std::min(units, b + kGroup), slot_rows, mk0, mv0,
+                                  Prefixes(pre))) != cudaSuccess)
         return e;
       continue;
     }
-    k_chunk_tc<D, MODE><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(c.batch, b + kGroup), slot_rows);
+    k_chunk_tc<D, MODE><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(units, b + kGroup), slot_rows, mk0, mv0, pre);
     cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 8) + 7) / 8);
     cfg.blockDim = dim3(256);
-    if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D, STATE>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D, BOTH>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
@@ -1277,15 +1312,28 @@ uint64_t chunk_tc_workspace(const mp_cache_config* c, int max_q, int max_kv) {
   return align256(uint64_t(ctas) * sizeof(Cut)) + align256(rows * 8) + align256(rows * c->head_dim * 4);
 }
 
+uint64_t both_tc_workspace(const mp_cache_config* own, int max_q, int max_kv, const mp_cache_config* pre, int max_group_q, int max_prefix) {
+  const mp_cache_config* any = own ? own : pre;
+  const int group = any->q_heads / any->kv_heads;
+  int ctas = 0;
+  if (own) ctas += chunk_tc_ctas(own->batch, own->kv_heads, group, max_q, max_kv);
+  if (pre) ctas += chunk_tc_ctas(pre->batch, pre->kv_heads, group, max_group_q, max_prefix);
+  ctas = std::min(ctas, device_sm_count());
+  const uint64_t rows = uint64_t(2 * ctas) * slot_rows_of(group, std::max(own ? max_q : 1, pre ? max_group_q : 1));
+  return align256(uint64_t(ctas) * sizeof(Cut)) + align256(rows * 8) + align256(rows * any->head_dim * 4);
+}
+
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st) {
+  return a.c.d == 128 ? launch<128, kChunk>(a, nullptr, true, workspace, st) : launch<64, kChunk>(a, nullptr, true, workspace, st);
+}
+cudaError_t launch_prefix_slices(const ChunkArgs& a, cudaStream_t st) {
   const bool d128 = a.c.d == 128;
-  if (a.c.cu_group && a.pieces) {
-    if (int64_t(a.c.max_q) * a.c.group <= 128) return d128 ? launch<128, kPairs>(a, nullptr, st) : launch<64, kPairs>(a, nullptr, st);
-    return d128 ? launch<128, kCuts>(a, nullptr, st) : launch<64, kCuts>(a, nullptr, st);
-  }
-  if (a.c.cu_group) return d128 ? launch<128, kRuns>(a, workspace, st) : launch<64, kRuns>(a, workspace, st);
-  if (a.state) return d128 ? launch<128, kOwn>(a, workspace, st) : launch<64, kOwn>(a, workspace, st);
-  return d128 ? launch<128, kChunk>(a, workspace, st) : launch<64, kChunk>(a, workspace, st);
+  if (int64_t(a.c.max_q) * a.c.group <= 128)
+    return d128 ? launch<128, kPairs>(a, nullptr, true, nullptr, st) : launch<64, kPairs>(a, nullptr, true, nullptr, st);
+  return d128 ? launch<128, kCuts>(a, nullptr, true, nullptr, st) : launch<64, kCuts>(a, nullptr, true, nullptr, st);
+}
+cudaError_t launch_both_tc(const ChunkArgs& own, bool own_units, const ChunkArgs* pre, void* workspace, cudaStream_t st) {
+  return own.c.d == 128 ? launch<128, kBoth>(own, pre, own_units, workspace, st) : launch<64, kBoth>(own, pre, own_units, workspace, st);
 }
 
 }  // namespace mp

@@ -232,9 +232,6 @@ uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int m
     if (s == 1 || q == max_q) return most;
   }
 }
-uint64_t tiles_bytes(const mp_cache_config* c, int max_q, int max_kv) {
-  return chunk_on_tensor_cores(c, max_q) ? chunk_tc_workspace(c, max_q, max_kv) : 0;
-}
 uint64_t sums_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * c->head_dim * 4); }
 uint64_t ml_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * 2 * 4); }
 uint64_t pieces_bytes(const mp_cache_config* c) { return align256(uint64_t(c->batch) * c->kv_heads * 4); }
@@ -247,18 +244,6 @@ int check(const mp_cache_config* c, const mp_cache_config* p, int total_q, int m
   if (c->batch + p->batch > 65535) return MP_ERR_UNSUPPORTED;  // one grid's z
   if ((rc = check_limits(c, total_q, max_q, max_kv)) != MP_OK) return rc;
   return check_limits(p, total_q, max_group_q, max_prefix);
-}
-
-// A pass of its own kernel; its slices lie at a.part and a.ml.
-cudaError_t launch_pass(ChunkArgs a, const Pass& pass, void* tiles, cudaStream_t st) {
-  a.splits = pass.slices;
-  if (pass.kind == kTiles) {
-    a.state = a.part;
-    a.state_ml = a.ml;
-    a.part = a.ml = nullptr;
-    a.pieces = nullptr;
-  }
-  return launch_chunk_tc(a, tiles, st);
 }
 
 }  // namespace
@@ -279,7 +264,7 @@ int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_config*
   max_group_q = std::min(max_group_q, total_q);
   const uint64_t rows = slice_rows_most(cfg, total_q, max_q, max_kv, false) + slice_rows_most(prefix_cfg, total_q, max_group_q, max_prefix, true);
   *bytes = pieces_bytes(cfg) + pieces_bytes(prefix_cfg) + sums_bytes(cfg, rows) + ml_bytes(cfg, rows) +
-           std::max(tiles_bytes(cfg, max_q, max_kv), tiles_bytes(prefix_cfg, max_group_q, max_prefix));
+           (cfg->dtype == MP_DTYPE_BF16 ? both_tc_workspace(cfg, max_q, max_kv, prefix_cfg, max_group_q, max_prefix) : 0);
   return MP_OK;
 }
 
@@ -315,8 +300,10 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   }
   const uint64_t rows = uint64_t(own.slices + shared.slices) * total_q;
   const uint64_t sums = sums_bytes(cfg, rows), ml = ml_bytes(cfg, rows), own_pieces = pieces_bytes(cfg), pre_pieces = pieces_bytes(prefix_cfg);
-  const uint64_t need = own_pieces + pre_pieces + sums + ml + std::max(own.kind == kTiles ? tiles_bytes(cfg, max_q, max_kv) : 0,
-                                                                       shared.kind == kTiles ? tiles_bytes(prefix_cfg, max_group_q, max_prefix) : 0);
+  const bool own_tiles = own.kind == kTiles, shared_tiles = shared.kind == kTiles;
+  uint64_t need = own_pieces + pre_pieces + sums + ml;
+  if (own_tiles || shared_tiles)
+    need += both_tc_workspace(own_tiles ? cfg : nullptr, max_q, max_kv, shared_tiles ? prefix_cfg : nullptr, max_group_q, max_prefix);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MP_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MP_ERR_SCRATCH;
   if (injected("prefix")) return MP_ERR_INJECTED;
@@ -354,16 +341,11 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   a.ml = p.ml + shared.slices * slice * 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  const bool simt = own.kind == kSimt;
-  if (simt) {
-    a.splits = own.slices;
-    p.splits = shared.slices;
+  a.splits = own.slices;
+  p.splits = shared.slices;
+  if (own.kind == kSimt) {
     ProfScope ps(st, K_CHUNK_ATTEND);
     if (launch_prefix_simt(p, a, st) != cudaSuccess) return MP_ERR_CUDA;
-  }
-  if (own.kind != kFew && !simt) {
-    ProfScope ps(st, K_CHUNK_ATTEND);
-    if (launch_pass(a, own, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   // few rows: both passes in one launch where both have them
   if (own.kind == kFew || shared.kind == kFew) {
@@ -380,9 +362,18 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     ProfScope ps(st, K_PREFIX_FEW);
     if (launch_prefix_few(few, most_q * (cfg->q_heads / cfg->kv_heads), st) != cudaSuccess) return MP_ERR_CUDA;
   }
-  if (shared.kind != kFew && !simt) {
+  // large tiles: likewise, in equal runs of all of them
+  if (own_tiles || shared_tiles) {
+    ChunkArgs both = a;
+    both.state = p.part;
+    both.state_ml = p.ml;
+    both.own_slice = shared.slices * slice;
     ProfScope ps(st, K_PREFIX_ATTEND);
-    if (launch_pass(p, shared, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
+    if (launch_both_tc(both, own_tiles, shared_tiles ? &p : nullptr, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
+  }
+  if (shared.kind == kSlices) {
+    ProfScope ps(st, K_PREFIX_ATTEND);
+    if (launch_prefix_slices(p, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   a.out = out;
   a.lse = lse;
