@@ -51,6 +51,7 @@ constexpr int kLead = 3, kLeadWhole = 5;
 // The same for a piece of a cut, whose sums are written and joined besides: its start is Q behind the first
 // copies of K and V (1 and 2 pieces a CTA, 512 rows over 98304 slots: 139 and 150 us).
 constexpr int kLeadPiece = 7;
+constexpr int kLeadBoth = 8;
 constexpr int kMinRun = 2;    // units of a CTA at least
 constexpr int kCut = 10;      // units that cutting the tiles costs: a second piece for most CTAs, and the join
 
@@ -95,7 +96,7 @@ struct Smem {
   int start[4];  // sequence, KV head, tile, unit
   Seq first;     // that sequence
   int longest[12];  // steps of a tile, of each warp's sequences
-  uint64_t pair_full, pair_done;
+  uint64_t pair_full, pair_done, q_asked;
   uint8_t filled[kStages];  // phase in which each tile of the ring was last filled (1: never)
   uint32_t tmem_base;
   uint32_t abort;
@@ -155,15 +156,19 @@ __device__ __forceinline__ int prefix_steps(const Seq& s) { return (s.n + kKeys 
 // L steps long: short enough that there are no more than r for every CTA, for the r that ends first. With
 // U steps and T tiles in all, L steps give U / L to U / L + T pieces: for each r that leaves L between two
 // limits, of which the upper one is short enough; up to 32 groups are counted for four values, one a lane.
-// Called by a warp; steps and tiles (of a KV head) of the groups lie in shared memory.
-__device__ int longest_piece(const int* steps, const int* tiles, int groups, int kvh, int ctas, int most_pieces) {
+// Called by a warp. get(g, &steps, &tiles) says a group's steps and tiles (of a KV head); it is called by
+// all lanes at once, with one group each in `own` and with the same one otherwise.
+template <typename Own, typename Get>
+__device__ __forceinline__ int longest_piece(Own own, Get get, int groups, int kvh, int ctas, int most_pieces) {
   const int lane = threadIdx.x & 31;
   int top = 1;
   int64_t all = 0, all_tiles = 0;
   for (int g = lane; g < groups; g += 32) {
-    if (tiles[g]) top = max(top, steps[g]);
-    all += int64_t(tiles[g]) * steps[g];
-    all_tiles += steps[g] ? tiles[g] : 0;
+    int steps, tiles;
+    own(g, &steps, &tiles);
+    if (tiles) top = max(top, steps);
+    all += int64_t(tiles) * steps;
+    all_tiles += steps ? tiles : 0;
   }
   top = __reduce_max_sync(0xffffffffu, top);
 #pragma unroll
@@ -174,19 +179,21 @@ __device__ int longest_piece(const int* steps, const int* tiles, int groups, int
   all *= kvh;
   all_tiles *= kvh;
   const int64_t r = 1 + lane / 4, room = r * ctas - all_tiles;
+  const bool counted = groups <= 32;
   uint32_t cost = UINT32_MAX;
-  int length = top;
+  int length = top, high = top;
   if (room > 0) {
-    const int low = int(quotient(all + r * ctas - 1, r * ctas)), high = int(min(int64_t(top), quotient(all + room - 1, room)));
-    length = max(max(1, (top + most_pieces - 1) / most_pieces), min(top, groups <= 32 ? low + (high - low) * (lane & 3) / 3 : high));
-    bool fits = length >= high;
-    if (!fits) {
-      int64_t n = 0;
-      for (int g = 0; g < groups; ++g) n += int64_t(tiles[g]) * pieces_of(steps[g], length);
-      fits = n * kvh <= r * ctas;
-    }
-    if (fits) cost = uint32_t(min(r * (length + kLeadPiece), int64_t(INT32_MAX)));
+    const int low = int(quotient(all + r * ctas - 1, r * ctas));
+    high = int(min(int64_t(top), quotient(all + room - 1, room)));
+    length = max(max(1, (top + most_pieces - 1) / most_pieces), min(top, counted ? low + (high - low) * (lane & 3) / 3 : high));
   }
+  int64_t n = 0;
+  for (int g = 0; counted && g < groups; ++g) {
+    int steps, tiles;
+    get(g, &steps, &tiles);
+    n += int64_t(tiles) * pieces_of(steps, length);
+  }
+  if (room > 0 && (length >= high || (counted && n * kvh <= r * ctas))) cost = uint32_t(min(r * (length + kLeadPiece), int64_t(INT32_MAX)));
   const uint32_t best = __reduce_min_sync(0xffffffffu, cost);
   if (best == UINT32_MAX) return top;
   return __shfl_sync(0xffffffffu, length, __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1);
@@ -238,12 +245,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&S.pair_full, 8);
     mbar_init(&S.pair_done, 8);
+    mbar_init(&S.q_asked, 4);
     S.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (CUT && threadIdx.x == 256) {
+  if (MODE != kChunk && threadIdx.x == 256) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV)) : "memory");
+    if (BOTH) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK0)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV0)) : "memory");
+    }
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem_base)),
@@ -258,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* steps = reinterpret_cast<int*>(seqs);  // of each prefix (kCuts, kPairs)
   static_assert(kGroup * sizeof(Seq) <= kKeys * 128, "one tile of the ring");
   int longest = 0;  // steps of a tile
-  for (int b = b_begin + warp; b < b_end; b += kThreads / 32) {
+  const bool by_warp = CUT && b_end - b_begin <= 32;  // then the warp that walks the pieces plans alone
+  for (int b = by_warp ? b_end : b_begin + warp; b < b_end; b += kThreads / 32) {
     const Seq s = rows_at(b);
     const int tiles = tiles_of(s, c.group);
     if (CUT) {
@@ -284,17 +297,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 0) S.longest[warp] = longest;
-  __syncthreads();
+  if (!by_warp) __syncthreads();
   Seq early = {0, 0, 0, 0};  // the first groups, a lane each, for the warp that walks the pieces
   if (CUT) {
     if (warp == 10 && b_begin + lane < b_end) early = group_of(c, b_begin + lane);
-    if (warp == 0) {
-      const int groups = b_end - b_begin, length = longest_piece(steps, counts, groups, c.kvh, gridDim.x, a.splits);
-      if (lane == 0) S.lead = length;
+    const int groups = b_end - b_begin;
+    int length = 0;
+    if (by_warp && warp == 10) {
+      const int steps1 = prefix_steps(early), tiles1 = tiles_of(early, c.group);
+      length = longest_piece(
+          [&](int, int* st, int* ti) {
+            *st = steps1;
+            *ti = tiles1;
+          },
+          [&](int g, int* st, int* ti) {
+            *st = __shfl_sync(0xffffffffu, steps1, g);
+            *ti = __shfl_sync(0xffffffffu, tiles1, g);
+          },
+          groups, c.kvh, gridDim.x, a.splits);
+      if (blockIdx.x == 0)
+        for (int g = 0; g < groups; ++g) {
+          const int n = pieces_of(__shfl_sync(0xffffffffu, steps1, g), length);
+          for (int h = lane; h < c.kvh; h += 32) a.pieces[(b_begin + g) * c.kvh + h] = n;
+        }
+    }
+    if (!by_warp && warp == 0) {
+      auto at = [&](int g, int* st, int* ti) {
+        *st = steps[g];
+        *ti = counts[g];
+      };
+      length = longest_piece(at, at, groups, c.kvh, gridDim.x, a.splits);
       if (blockIdx.x == 0)
         for (int i = lane; i < groups * c.kvh; i += 32) a.pieces[b_begin * c.kvh + i] = pieces_of(steps[i / c.kvh], length);
       fence_async();
     }
+    if (length > 0 && lane == 0) S.lead = length;
   } else if (warp == 0) {
     int64_t all = 0, all_tiles = 0;
     for (int b = lane; b < b_end - b_begin; b += 32) {
@@ -307,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       all_tiles += __shfl_xor_sync(0xffffffffu, all_tiles, o);
     }
     longest = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? S.longest[lane] : 0);
-    const int lead = D == 128 && all_tiles >= gridDim.x ? kLeadWhole : kLead;
+    const int lead = BOTH ? kLeadBoth : D == 128 && all_tiles >= gridDim.x ? kLeadWhole : kLead;
     all += lead * all_tiles;
     longest += lead;
     auto units_of = [&](int b) { return units[b - b_begin] + int64_t(lead) * counts[b - b_begin]; };
@@ -561,9 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int live = max(0, min(kKeys, pc.n - n0));  // rows that hold slots of the sequence
           const int boxes = (live + rows_of_box - 1) / rows_of_box;
           for (int kv = 0; kv < 2; ++kv) {
-            // Q behind five tiles in the memory's queue came 7 us late, so the first K waits for it alone
-            if (CUT && i == 0 && u == pc.u0 && kv == 1) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&S.q_full[0], 0, abort));
+            // Q behind five tiles in the memory's queue came 7 us late, so its loads go before all but the first
+            if (MODE != kChunk && i == 0 && u == pc.u0 && kv == 1) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&S.q_asked, 0, abort));
               if (!ok) break;
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[st], ph ^ 1, abort));
@@ -814,6 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = kLog2e * rsqrtf(float(D));
     uint32_t ph_s = 0, ph_o = 0;  // phases of s_full, and of o_full's next completion
     uint32_t ph_t = half == 0;    // of turn; the first turn is half 0's
+    bool first_piece = true;
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
       ok = __all_sync(0xffffffffu, mbar_wait(&S.piece_full[i & 1], (i >> 1) & 1, abort));
@@ -843,6 +881,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[j] = make_uint4(0, 0, 0, 0);
             if (r - lane + k < rows)
               v[j] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + from * D)[i];
+          }
+          if (MODE != kChunk && half == 0 && first_piece) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.q_asked);
+            first_piece = false;
           }
 #pragma unroll
           for (int j = 0; j < kChunks; ++j) {

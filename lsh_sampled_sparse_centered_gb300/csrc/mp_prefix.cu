@@ -18,17 +18,25 @@ namespace {
 struct Slices {
   int shared, own;
   int32_t *pre_pieces, *own_pieces;
+  int pre_blocks, own_blocks, block_rows;  // numbers of a KV head: one for every block_rows rows
 };
+
+// A join of many rows (1264 tokens of 32 heads in two slices: 22 us with four rows and two CTAs, 16 so):
+constexpr int kRowsALane = 2;
+constexpr int kResident = 4;  // CTAs of an SM
+// One of few rows: several warps a row, with four slices each in flight.
+constexpr int kFewAtOnce = 4;
 
 // Joins the slices' (m, l, sum) of a sequence's query rows, in their order. A warp takes ROWS rows (of
 // D / 4 lanes each, 16 bytes a lane) and has the loads of kAtOnce slices of each in flight; with WARPS > 1
 // as many warps share the slices of their rows, so that all of them are in flight together. The first
 // `shared` slices are of the prefix, the `own` behind them of the own slots; where their numbers are kept
-// per (group or sequence, KV head), as many of them are there. Rows without a prefix have none of it.
+// per (group or sequence, KV head, block of rows), as many of them are there. Rows without a prefix have
+// none of it.
 // Grid: rows of a sequence x sequences, so that what has to be looked up does not hang on a row.
 template <typename T, int D, int ROWS, int WARPS>
-__global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const CacheArgs prefix, const Slices sl) {
-  constexpr int kLanes = D / 4, kTurns = ROWS * kLanes / 32, kAtOnce = kTurns == 1 ? 8 : 2;
+__global__ void __launch_bounds__(256, WARPS == 4 || ROWS > 128 / D ? kResident : 2) k_prefix_join(const ChunkArgs a, const CacheArgs prefix, const Slices sl) {
+  constexpr int kLanes = D / 4, kTurns = ROWS * kLanes / 32, kAtOnce = WARPS > 1 ? kFewAtOnce : (kTurns == 1 ? 8 : 2);
   static_assert(WARPS == 1 || kTurns == 1);
   __shared__ float4 so[WARPS > 1 ? 8 : 1][32];
   __shared__ float2 sml[WARPS > 1 ? 8 : 1][32];
@@ -61,8 +69,12 @@ __global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const Ca
     there[j] = g.row0 <= t && t < g.row0 + g.m ? sl.shared : 0;
     all[j] = sl.own;
     if (row[j] >= 0) {
-      if (sl.pre_pieces && there[j]) there[j] = min(there[j], sl.pre_pieces[int64_t(lo) * c.kvh + h]);
-      if (sl.own_pieces) all[j] = min(all[j], sl.own_pieces[int64_t(b) * c.kvh + h]);
+      const int in_head = int(i % qh) - h * c.group;  // row of the KV head's in its token
+      auto number = [&](const int32_t* pieces, int unit, int token, int blocks) {
+        return pieces[(int64_t(unit) * c.kvh + h) * blocks + (blocks > 1 ? (token * c.group + in_head) / sl.block_rows : 0)];
+      };
+      if (sl.pre_pieces && there[j]) there[j] = min(there[j], number(sl.pre_pieces, lo, t - g.row0, sl.pre_blocks));
+      if (sl.own_pieces) all[j] = min(all[j], number(sl.own_pieces, b, t - s.row0, sl.own_blocks));
     }
     all[j] += there[j];
     most = max(most, all[j]);
@@ -152,11 +164,12 @@ __global__ void __launch_bounds__(256) k_prefix_join(const ChunkArgs a, const Ca
 template <typename T, int D>
 cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, cudaStream_t st) {
   const int each = 32 / (D / 4), qh = a.c.kvh * a.c.group;
-  // four rows a lane where that still leaves the SMs 16 warps each, four warps a row where there are at
-  // most 8 rows an SM (32 tokens of 32 heads: 76 and 73 us a call with one and four, 128: 232 and 239)
+  // Two rows a lane where that still leaves the SMs 16 warps each, four warps a row where there are at most
+  // 8 rows an SM, eight where there are at most two (32 tokens of 32 heads: 76, 69 and 71 us a call with
+  // one, four and eight, four tokens: 18.7, 16.6 and 15.0).
   const int64_t all = int64_t(a.c.total_q) * qh / each, sms = device_sm_count();
-  const bool many = all >= sms * 16 * 4, few = all <= sms * 8;
-  const int rows = each * (many ? 32 : (few ? 2 : 8));
+  const bool many = all >= sms * 16 * kRowsALane, few = all <= sms * 8, least = all <= sms * 2;
+  const int rows = each * (many ? 8 * kRowsALane : (least ? 1 : (few ? 2 : 8)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((int64_t(a.c.max_q) * qh + rows - 1) / rows), a.c.batch);
   cfg.blockDim = dim3(256);
@@ -166,7 +179,8 @@ cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (many) return cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 4 * (128 / D), 1>, a, prefix, sl);
+  if (many) return cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, kRowsALane * (128 / D), 1>, a, prefix, sl);
+  if (least) return cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D, 8>, a, prefix, sl);
   return few ? cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D, 4>, a, prefix, sl)
              : cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D, 1>, a, prefix, sl);
 }
@@ -191,20 +205,20 @@ int simt_slices_most(const mp_cache_config* c, int max_q, int max_kv) {
   return int(std::max<int64_t>(1, std::min<int64_t>({simt_fit(c) / simt_ctas(c, max_q, 1), (int64_t(max_kv) + 63) / 64, 64})));
 }
 
-// How a pass goes, by its rows per KV head: up to 32 through k_prefix_few, more on the tensor cores, fp32
-// on the CUDA cores. kTiles leaves one slice, kSlices as many as prefix_slices() says.
+// How a pass goes: few rows per KV head through k_prefix_few, more on the tensor cores, fp32 on the CUDA
+// cores. kTiles leaves one slice, kSlices as many as prefix_slices() says.
 enum Kind { kFew, kTiles, kSlices, kSimt };
 struct Pass {
   Kind kind;
   int slices;  // the most
 };
-Kind kind_of(const mp_cache_config* c, int total_q, int max_q, bool prefix) {
+Kind kind_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool prefix) {
   if (c->dtype != MP_DTYPE_BF16) return kSimt;
-  if (int64_t(max_q) * (c->q_heads / c->kv_heads) <= kFewRows) return kFew;
+  if (prefix_is_few(c, max_q, max_kv)) return kFew;
   return prefix && prefix_in_slices(c, total_q, max_q) ? kSlices : kTiles;
 }
 Pass pass_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool prefix) {
-  const Kind kind = kind_of(c, total_q, max_q, prefix);
+  const Kind kind = kind_of(c, total_q, max_q, max_kv, prefix);
   if (kind == kFew) return {kind, prefix_few_pieces(c, total_q, max_kv)};
   if (kind == kTiles) return {kind, 1};
   const int s = kind == kSlices ? prefix_slices(c, max_q, max_kv) : simt_slices_most(c, max_q, max_kv);
@@ -216,7 +230,7 @@ uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int m
   const int group = c->q_heads / c->kv_heads;
   uint64_t most = uint64_t(total_q);
   if (c->dtype == MP_DTYPE_BF16) {
-    if (group <= kFewRows) most = std::max(most, uint64_t(prefix_few_rows_most(c, total_q, max_kv)));
+    most = std::max(most, uint64_t(prefix_few_rows_most(c, total_q, max_kv)));
     // large tiles: the slices go by the tiles of a group, one where they are many
     for (int64_t tiles = 1; prefix; ++tiles) {
       const int q = int(std::min<int64_t>(max_q, std::max<int64_t>(1, tiles * 256 / group))), s = prefix_slices(c, q, max_kv);
@@ -234,7 +248,13 @@ uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int m
 }
 uint64_t sums_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * c->head_dim * 4); }
 uint64_t ml_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * 2 * 4); }
-uint64_t pieces_bytes(const mp_cache_config* c) { return align256(uint64_t(c->batch) * c->kv_heads * 4); }
+// Blocks of k_prefix_few that numbers of pieces are kept for (one where all of a KV head's rows have the same).
+int blocks_of(const mp_cache_config* c, const Pass& pass, int max_q) { return pass.kind == kFew ? few_blocks(c->q_heads / c->kv_heads, max_q) : 1; }
+uint64_t pieces_bytes(const mp_cache_config* c, int blocks) { return align256(uint64_t(c->batch) * c->kv_heads * blocks * 4); }
+// for limits that are at most these
+uint64_t pieces_bytes_most(const mp_cache_config* c, int max_q) {
+  return pieces_bytes(c, std::min(8, few_blocks(c->q_heads / c->kv_heads, max_q)));
+}
 
 int check(const mp_cache_config* c, const mp_cache_config* p, int total_q, int max_q, int max_kv, int max_group_q, int max_prefix) {
   int rc = check_cache(c);
@@ -263,7 +283,7 @@ int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_config*
   max_q = std::min(max_q, total_q);
   max_group_q = std::min(max_group_q, total_q);
   const uint64_t rows = slice_rows_most(cfg, total_q, max_q, max_kv, false) + slice_rows_most(prefix_cfg, total_q, max_group_q, max_prefix, true);
-  *bytes = pieces_bytes(cfg) + pieces_bytes(prefix_cfg) + sums_bytes(cfg, rows) + ml_bytes(cfg, rows) +
+  *bytes = pieces_bytes_most(cfg, max_q) + pieces_bytes_most(prefix_cfg, max_group_q) + sums_bytes(cfg, rows) + ml_bytes(cfg, rows) +
            (cfg->dtype == MP_DTYPE_BF16 ? both_tc_workspace(cfg, max_q, max_kv, prefix_cfg, max_group_q, max_prefix) : 0);
   return MP_OK;
 }
@@ -299,7 +319,9 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     shared.slices = std::min(shared.slices, simt_slices(max_prefix, tiles));
   }
   const uint64_t rows = uint64_t(own.slices + shared.slices) * total_q;
-  const uint64_t sums = sums_bytes(cfg, rows), ml = ml_bytes(cfg, rows), own_pieces = pieces_bytes(cfg), pre_pieces = pieces_bytes(prefix_cfg);
+  const int own_blocks = blocks_of(cfg, own, max_q), pre_blocks = blocks_of(prefix_cfg, shared, max_group_q);
+  const uint64_t sums = sums_bytes(cfg, rows), ml = ml_bytes(cfg, rows), own_pieces = pieces_bytes(cfg, own_blocks),
+                 pre_pieces = pieces_bytes(prefix_cfg, pre_blocks);
   const bool own_tiles = own.kind == kTiles, shared_tiles = shared.kind == kTiles;
   uint64_t need = own_pieces + pre_pieces + sums + ml;
   if (own_tiles || shared_tiles)
@@ -309,7 +331,9 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   if (injected("prefix")) return MP_ERR_INJECTED;
 
   char* ws = static_cast<char*>(workspace);
-  Slices sl = {shared.slices, own.slices, nullptr, nullptr};
+  const int most_q = std::max(own.kind == kFew ? max_q : 1, shared.kind == kFew ? max_group_q : 1);
+  const int few_rows = int(std::min<int64_t>(kFewRows, int64_t(most_q) * (cfg->q_heads / cfg->kv_heads)));
+  Slices sl = {shared.slices, own.slices, nullptr, nullptr, pre_blocks, own_blocks, kFewRows};
   if (own.kind == kFew) sl.own_pieces = reinterpret_cast<int32_t*>(ws);
   if (shared.kind == kFew || shared.kind == kSlices) sl.pre_pieces = reinterpret_cast<int32_t*>(ws + own_pieces);
   ws += own_pieces + pre_pieces;
@@ -356,11 +380,12 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     few.own_units = own.kind == kFew;
     few.most_shared = shared.slices;
     few.most_own = own.slices;
+    few.pre_blocks = pre_blocks;
+    few.own_blocks = own_blocks;
     few.pre_pieces = sl.pre_pieces;
     few.own_pieces = sl.own_pieces;
-    const int most_q = std::max(own.kind == kFew ? max_q : 1, shared.kind == kFew ? max_group_q : 1);
     ProfScope ps(st, K_PREFIX_FEW);
-    if (launch_prefix_few(few, most_q * (cfg->q_heads / cfg->kv_heads), st) != cudaSuccess) return MP_ERR_CUDA;
+    if (launch_prefix_few(few, few_rows, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   // large tiles: likewise, in equal runs of all of them
   if (own_tiles || shared_tiles) {

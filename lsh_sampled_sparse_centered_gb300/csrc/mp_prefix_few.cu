@@ -1,6 +1,6 @@
-// Attention with shared prefixes, the units with few query rows: the own slots of sequences with at most
-// 32 rows per KV head (tokens x heads of the group), and the prefixes of groups with as few. bf16, bound
-// by one pass over K and V.
+// Attention with shared prefixes, with few query rows per KV head (tokens x heads of the group): the own
+// slots of sequences, and the prefixes of groups with up to 32 rows, or with more over short prefixes, 32
+// of them at a time. bf16, bound by one pass over K and V.
 //
 // Many sequences with a few hundred slots each are many short streams, and what a stream costs besides
 // its bytes (lengths, pages, Q, the sums' way out) is as much as they are. So every warp works for itself,
@@ -33,8 +33,8 @@ struct Maps {
   CUtensorMap k[2], v[2];  // of the prefixes, of the own slots
 };
 struct Piece {
-  int own;               // 0: of a prefix
-  int row0, rows, first, n, h, u0, u1, slice;
+  int own;  // 0: of a prefix
+  int row0, r0, rows, first, n, h, u0, u1, slice;  // rows [r0, rows) of those that start in packed row row0
 };
 
 template <int D>
@@ -47,7 +47,6 @@ struct Smem {
   int least[kWarps];
   uint32_t abort[kWarps];
 };
-static_assert(sizeof(Piece) == 36);
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_constant__ Maps maps, const __grid_constant__ PrefixFew a) {
@@ -71,21 +70,26 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
 
   // ---- where this warp's run starts ----
   auto seq = [&](int v) { return v < a.groups ? group_of(a.pre.c, v) : seq_of(co, v - a.groups); };
-  auto pieces_at = [&](int v) { return v < a.groups ? a.pre_pieces + int64_t(v) * kvh : a.own_pieces + int64_t(v - a.groups) * kvh; };
+  auto pieces_at = [&](int v, int h, int block) -> int32_t& {
+    return v < a.groups ? a.pre_pieces[(int64_t(v) * kvh + h) * a.pre_blocks + block]
+                        : a.own_pieces[(int64_t(v - a.groups) * kvh + h) * a.own_blocks + block];
+  };
   auto steps_in = [&](const Seq& s) { return s.m > 0 ? (s.n + kStep - 1) / kStep : 0; };
-  int* kept = reinterpret_cast<int*>(&S.ring[0][0][0][0][0]);
-  static_assert(kKept * 4 <= sizeof(S.ring));
+  auto blocks_in = [&](const Seq& s) { return (s.m * group + NT * 8 - 1) / (NT * 8); };
+  int2* kept = reinterpret_cast<int2*>(&S.ring[0][0][0][0][0]);  // steps and blocks
+  static_assert(kKept * 8 <= sizeof(S.ring));
   int64_t total = 0;
   int64_t least = kMinRun;  // steps of a run, so that no unit is cut into more pieces than it may: as long as its steps by one less
   for (int v = threadIdx.x; v < units; v += kWarps * 32) {
     const Seq s = seq(v);
-    const int n = steps_in(s);
-    if (v < kKept) kept[v] = n;
-    total += n ? n + kLead : 0;
+    const int n = steps_in(s), blocks = blocks_in(s);
+    if (v < kKept) kept[v] = make_int2(n, blocks);
+    total += n ? int64_t(n + kLead) * blocks : 0;
     const int most = v < a.groups ? a.most_shared : a.most_own;
     least = max(least, int64_t((n + most - 2) / (most - 1)));
     if (n == 0 && v % gridDim.x == blockIdx.x)
-      for (int h = 0; h < kvh; ++h) pieces_at(v)[h] = 0;
+      for (int h = 0; h < kvh; ++h)
+        for (int i = 0; i < blocks; ++i) pieces_at(v, h, i) = 0;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -105,14 +109,24 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
   const int64_t run = max(least, quotient(total + workers - 1, workers));
   const int64_t r0 = (int64_t(blockIdx.x) * kWarps + warp) * run, r1 = min(total, r0 + run);
   // the unit being fetched: its first step (kLead of them before its slots) among all, its sequence
-  int fv = 0, fh = 0, f_steps = 0;
+  int fv = 0, fi = 0, f_steps = 0, f_blocks = 1;  // fi: KV head and block of rows, the blocks next to each other
   int64_t f_at = 0;
   Seq fs = {0, 0, 0, 0};
   if (r0 < total) {
     int64_t at = r0;  // into what is left
     for (int v0 = 0; v0 < units; v0 += 32) {
-      const int v = v0 + lane, n = v < units ? (v < kKept ? kept[v] : steps_in(seq(v))) : 0;
-      const int64_t mine = n ? int64_t(n + kLead) * kvh : 0;
+      const int v = v0 + lane;
+      int2 k = make_int2(0, 1);
+      if (v < units) {
+        if (v < kKept) {
+          k = kept[v];
+        } else {
+          const Seq s = seq(v);
+          k = make_int2(steps_in(s), blocks_in(s));
+        }
+      }
+      const int n = k.x;
+      const int64_t mine = n ? int64_t(n + kLead) * kvh * k.y : 0;
       int64_t pre = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -125,12 +139,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
         at -= __shfl_sync(0xffffffffu, pre - mine, i);
         fv = v0 + i;
         f_steps = __shfl_sync(0xffffffffu, n, i);
+        f_blocks = __shfl_sync(0xffffffffu, k.y, i);
         break;
       }
       at -= __shfl_sync(0xffffffffu, pre, 31);
     }
-    fh = int(quotient(at, int64_t(f_steps + kLead)));
-    f_at = r0 - (at - int64_t(fh) * (f_steps + kLead));
+    fi = int(quotient(at, int64_t(f_steps + kLead)));
+    f_at = r0 - (at - int64_t(fi) * (f_steps + kLead));
     fs = seq(fv);
   }
   fence_async();
@@ -142,16 +157,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
   auto look = [&]() {  // the next 32 steps' rows of the pool, one a lane
     f_base = fu;
     const CacheArgs& c = fv < a.groups ? a.pre.c : co;
-    f_row = fu + lane < fu1 ? slot_row(c, fv < a.groups ? fv : fv - a.groups, fh, (fu + lane) * kStep) : 0;
+    f_row = fu + lane < fu1 ? slot_row(c, fv < a.groups ? fv : fv - a.groups, fi / f_blocks, (fu + lane) * kStep) : 0;
   };
   auto advance = [&]() {  // to the next unit
     f_at += f_steps + kLead;
-    if (++fh < kvh) return;
-    fh = 0;
+    if (++fi < kvh * f_blocks) return;
+    fi = 0;
     f_steps = 0;
     while (f_at < r1 && ++fv < units) {
       fs = seq(fv);
       f_steps = steps_in(fs);
+      f_blocks = blocks_in(fs);
       if (f_steps) break;
     }
     if (f_steps == 0) f_at = r1;
@@ -166,15 +182,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
       if (lane == 0) {
         Piece& p = S.piece[warp][pushed & 7];
         p.own = fv >= a.groups;
+        const int h = fi / f_blocks, block = fi - h * f_blocks;
         p.row0 = fs.row0;
+        p.r0 = block * NT * 8;
         p.rows = fs.m * group;
         p.first = fs.first;
         p.n = fs.n;
-        p.h = fh;
+        p.h = h;
         p.u0 = u0;
         p.u1 = u1;
         p.slice = int(quotient(r0, run) - first);
-        if (u0 == 0) pieces_at(fv)[fh] = int(quotient(lead + f_steps - 1, run) - first) + 1;
+        if (u0 == 0) pieces_at(fv, h, block) = int(quotient(lead + f_steps - 1, run) - first) + 1;
       }
       ++pushed;
       fu = u0;
@@ -215,7 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
     int see[NT];  // the lane's row (8 u + g) sees the slots below this
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      const int r = u * 8 + g;
+      const int r = p.r0 + u * 8 + g;
       see[u] = r < p.rows ? min(p.n, p.first + r / group + 1) : 0;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.own.q) +
                                  (int64_t(p.row0 + r / group) * qh + p.h * group + r % group) * D + t * 8;
@@ -338,10 +356,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
     for (int u = 0; u < NT; ++u) {
       l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
       l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-      if (t == 0 && u * 8 + g < p.rows) *reinterpret_cast<float2*>(to.ml + row_at(u * 8 + g) * 2) = make_float2(m[u], l[u]);
+      if (t == 0 && p.r0 + u * 8 + g < p.rows) *reinterpret_cast<float2*>(to.ml + row_at(p.r0 + u * 8 + g) * 2) = make_float2(m[u], l[u]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int r = u * 8 + 2 * t + k;
+        const int r = p.r0 + u * 8 + 2 * t + k;
         if (r >= p.rows) continue;
         float4* dst = reinterpret_cast<float4*>(to.part + row_at(r) * D + 8 * g);
         dst[0] = make_float4(o[u][0][k], o[u][1][k], o[u][2][k], o[u][3][k]);
@@ -390,10 +408,20 @@ cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st) {
         !make_map(&maps.v[i], both[i]->values, d, pool, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
     const int units = i ? (a.own_units ? c.batch : 0) : a.groups;
-    steps += int64_t(units) * c.kvh * ((c.max_kv + kStep - 1) / kStep + kLead);
+    steps += int64_t(units) * c.kvh * few_blocks(c.group, c.max_q) * ((c.max_kv + kStep - 1) / kStep + kLead);
   }
   const int ctas = int(std::min<int64_t>(kCtas * int64_t(device_sm_count()), steps / (kMinRun * kWarps) + 1));
   return d == 128 ? launch_rows<128>(maps, a, rows, ctas, st) : launch_rows<64>(maps, a, rows, ctas, st);
+}
+
+// Up to 32 rows; with more, K and V are read once for every 32 of them, from L2 then, and a step of them is
+// 1 us of a warp. The large tiles do better, but a kernel of them starts 10 us later. (Groups of 56, 68 and
+// 20 rows over 3001, 777 and 5000 slots of four KV heads, d = 64: 28.8 us a call with large tiles for the
+// prefixes, .)
+bool prefix_is_few(const mp_cache_config* c, int max_q, int max_kv) {
+  const int64_t blocks = few_blocks(c->q_heads / c->kv_heads, max_q);
+  const int64_t steps = int64_t(c->batch) * c->kv_heads * ((max_kv + kStep - 1) / kStep);
+  return blocks <= 1 || (blocks <= 8 && steps * blocks <= 16384);
 }
 
 // The most pieces that a unit is cut into: as many warps as there are for it, 32 at least, so that one long
