@@ -52,35 +52,41 @@ __global__ void __launch_bounds__(256, WARPS == 4 || ROWS > 128 / D ? kResident 
     else hi = mid;
   }
   const Seq g = group_of(prefix, lo);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t first = (int64_t(blockIdx.x) * (8 / WARPS) + warp / WARPS) * ROWS, mine = int64_t(s.m) * qh;
-  if (WARPS == 1 && first >= mine) return;
+  // all rows together are 32-bit
+  const int first = int(blockIdx.x * (8 / WARPS) + warp / WARPS) * ROWS, mine = s.m * qh;
   float m[kTurns], l[kTurns];
   float4 o[kTurns];
   int64_t row[kTurns];
   int there[kTurns], all[kTurns];  // slices of the row's prefix, and with those of its own slots
-  int most = 0;
+  const int32_t *there_at[kTurns], *all_at[kTurns];  // or where their numbers are
 #pragma unroll
   for (int j = 0; j < kTurns; ++j) {
-    const int64_t i = first + j * (32 / kLanes) + sub;
-    row[j] = i < mine ? int64_t(s.row0) * qh + i : -1;
-    const int t = s.row0 + int(i / qh);
-    const int h = int(i % qh) / c.group;
-    there[j] = g.row0 <= t && t < g.row0 + g.m ? sl.shared : 0;
-    all[j] = sl.own;
-    if (row[j] >= 0) {
-      const int in_head = int(i % qh) - h * c.group;  // row of the KV head's in its token
-      auto number = [&](const int32_t* pieces, int unit, int token, int blocks) {
-        return pieces[(int64_t(unit) * c.kvh + h) * blocks + (blocks > 1 ? (token * c.group + in_head) / sl.block_rows : 0)];
-      };
-      if (sl.pre_pieces && there[j]) there[j] = min(there[j], number(sl.pre_pieces, lo, t - g.row0, sl.pre_blocks));
-      if (sl.own_pieces) all[j] = min(all[j], number(sl.own_pieces, b, t - s.row0, sl.own_blocks));
-    }
-    all[j] += there[j];
-    most = max(most, all[j]);
+    const int i = first + j * (32 / kLanes) + sub;
+    const bool live = i < mine;
+    row[j] = live ? int64_t(s.row0) * qh + i : -1;
+    const int token = i / qh, in = i - token * qh, h = in / c.group, in_head = in - h * c.group, t = s.row0 + token;
+    const bool shared = live && g.row0 <= t && t < g.row0 + g.m;
+    there[j] = shared ? sl.shared : 0;
+    all[j] = live ? sl.own : 0;
+    there_at[j] = !shared || !sl.pre_pieces ? nullptr
+                  : sl.pre_pieces + (int64_t(lo) * c.kvh + h) * sl.pre_blocks +
+                        (sl.pre_blocks > 1 ? ((t - g.row0) * c.group + in_head) / sl.block_rows : 0);
+    all_at[j] = !live || !sl.own_pieces ? nullptr
+                : sl.own_pieces + (int64_t(b) * c.kvh + h) * sl.own_blocks +
+                      (sl.own_blocks > 1 ? (token * c.group + in_head) / sl.block_rows : 0);
     m[j] = -INFINITY;
     l[j] = 0.f;
     o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (WARPS == 1 && first >= mine) return;
+  int most = 0;
+#pragma unroll
+  for (int j = 0; j < kTurns; ++j) {
+    if (there_at[j]) there[j] = min(there[j], *there_at[j]);
+    if (all_at[j]) all[j] = min(all[j], *all_at[j]);
+    all[j] += there[j];
+    most = max(most, all[j]);
   }
   most = __reduce_max_sync(0xffffffffu, most);
   for (int i0 = warp % WARPS * kAtOnce; i0 < most; i0 += WARPS * kAtOnce) {
@@ -91,7 +97,7 @@ __global__ void __launch_bounds__(256, WARPS == 4 || ROWS > 128 / D ? kResident 
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
         const int i = i0 + k;
-        const bool live = row[j] >= 0 && i < all[j];
+        const bool live = i < all[j];
         const int64_t at = live ? (i < there[j] ? i : i - there[j] + sl.shared) * rows + row[j] : 0;
         v[j][k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
         x[j][k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
