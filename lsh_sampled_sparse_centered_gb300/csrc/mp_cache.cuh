@@ -110,7 +110,6 @@ cudaError_t launch_prefix_simt(const ChunkArgs& pre, const ChunkArgs& own, cudaS
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st);
-cudaError_t launch_prefix_slices(const ChunkArgs& a, cudaStream_t st);
 // Groups over their prefixes (pre) and chunks over their own slots (own_units), either of which may be missing.
 cudaError_t launch_both_tc(const ChunkArgs& own, bool own_units, const ChunkArgs* pre, void* workspace, cudaStream_t st);
 uint64_t both_tc_workspace(const mp_cache_config* own, int max_q, int max_kv, const mp_cache_config* pre, int max_group_q, int max_prefix);

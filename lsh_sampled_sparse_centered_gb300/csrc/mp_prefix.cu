@@ -218,13 +218,13 @@ struct Pass {
   Kind kind;
   int slices;  // the most
 };
-Kind kind_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool prefix) {
+Kind kind_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool slices) {
   if (c->dtype != MP_DTYPE_BF16) return kSimt;
   if (prefix_is_few(c, max_q, max_kv)) return kFew;
-  return prefix && prefix_in_slices(c, total_q, max_q) ? kSlices : kTiles;
+  return slices && prefix_in_slices(c, total_q, max_q) ? kSlices : kTiles;
 }
-Pass pass_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool prefix) {
-  const Kind kind = kind_of(c, total_q, max_q, max_kv, prefix);
+Pass pass_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool slices) {
+  const Kind kind = kind_of(c, total_q, max_q, max_kv, slices);
   if (kind == kFew) return {kind, prefix_few_pieces(c, total_q, max_kv)};
   if (kind == kTiles) return {kind, 1};
   const int s = kind == kSlices ? prefix_slices(c, max_q, max_kv) : simt_slices_most(c, max_q, max_kv);
@@ -315,7 +315,8 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     if (!aligned4(p)) return MP_ERR_INVALID_ARG;
   max_q = std::min(max_q, total_q);
   max_group_q = std::min(max_group_q, total_q);
-  Pass own = pass_of(cfg, total_q, max_q, max_kv, false), shared = pass_of(prefix_cfg, total_q, max_group_q, max_prefix, true);
+  Pass own = pass_of(cfg, total_q, max_q, max_kv, false);
+  Pass shared = pass_of(prefix_cfg, total_q, max_group_q, max_prefix, own.kind == kFew);
   if (own.kind == kSimt) {
     int tiles = 1;
     while (tiles * 64 < std::max(max_kv, max_prefix) && simt_ctas(cfg, max_q, simt_slices(max_kv, tiles)) +
@@ -379,6 +380,7 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   }
   // few rows: both passes in one launch where both have them
   if (own.kind == kFew || shared.kind == kFew) {
+    const bool beside = shared.kind == kSlices;
     PrefixFew few;
     few.pre = p;
     few.own = a;
@@ -390,8 +392,8 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     few.own_blocks = own_blocks;
     few.pre_pieces = sl.pre_pieces;
     few.own_pieces = sl.own_pieces;
-    ProfScope ps(st, K_PREFIX_FEW);
-    if (launch_prefix_few(few, few_rows, st) != cudaSuccess) return MP_ERR_CUDA;
+    ProfScope ps(st, beside ? K_PREFIX_ATTEND : K_PREFIX_FEW);
+    if ((beside ? launch_prefix_slices(p, few, few_rows, st) : launch_prefix_few(few, few_rows, st)) != cudaSuccess) return MP_ERR_CUDA;
   }
   // large tiles: likewise, in equal runs of all of them
   if (own_tiles || shared_tiles) {
@@ -401,10 +403,6 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     both.own_slice = shared.slices * slice;
     ProfScope ps(st, K_PREFIX_ATTEND);
     if (launch_both_tc(both, own_tiles, shared_tiles ? &p : nullptr, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
-  }
-  if (shared.kind == kSlices) {
-    ProfScope ps(st, K_PREFIX_ATTEND);
-    if (launch_prefix_slices(p, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   a.out = out;
   a.lse = lse;

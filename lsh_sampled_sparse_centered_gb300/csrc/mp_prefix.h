@@ -17,6 +17,8 @@ struct PrefixFew {
   int32_t *pre_pieces, *own_pieces;   // [groups or batch][kv_heads][blocks]
 };
 cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st);
+// The prefixes of `a` in slices on large tiles, and beside them the own slots of `few` (no groups).
+cudaError_t launch_prefix_slices(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st);
 // Whether a pass with these limits goes through it.
 bool prefix_is_few(const mp_cache_config* c, int max_q, int max_kv);
 inline int few_blocks(int group, int max_q) { return int((int64_t(max_q) * group + kFewRows - 1) / kFewRows); }

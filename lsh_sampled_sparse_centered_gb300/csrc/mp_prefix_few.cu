@@ -1,382 +1,52 @@
-// Attention with shared prefixes, with few query rows per KV head (tokens x heads of the group): the own
-// slots of sequences, and the prefixes of groups with up to 32 rows, or with more over short prefixes, 32
-// of them at a time. bf16, bound by one pass over K and V.
-//
-// Many sequences with a few hundred slots each are many short streams, and what a stream costs besides
-// its bytes (lengths, pages, Q, the sums' way out) is as much as they are. So every warp works for itself,
-// without a barrier of its CTA: the steps of all (sequence, KV head) units, 16 slots each, are laid end to
-// end and cut into equal runs, one a warp. A warp's TMA copies run ahead of its products by a ring of
-// three steps (d = 64: six), across the ends of units. A unit that is cut lies in several slices: warp w
-// writes slice w - (first warp of the unit), k_prefix_join joins them.
-//
-// S and O^T are warp-level products, with the fragments of the few-row attention (mp_chunk_step.cu):
-// lane (g, t) takes the 16-byte chunks t, t + 4, ... of the keys g and g + 8, and chunk g of V of the
-// keys 2t, 2t + 1, 2t + 8 and 2t + 9. P enters the second product as the sum of two bf16 terms.
+// The kernel of mp_prefix_few.cuh alone, and its host side.
 #include <algorithm>
 
 #include "mp_cache_host.h"
-#include "mp_prefix.h"
-#include "mp_tc.cuh"
+#include "mp_prefix_few.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int kWarps = 4, kCtas = 2;  // of a CTA; CTAs of an SM
-constexpr int kStep = 16;             // slots
-constexpr int kLead = 3;              // steps that starting and ending a unit counts as
-constexpr int kMinRun = 4;            // steps of a warp at least
-constexpr int kKept = 8192;           // units' lengths that the planning keeps
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaise = 8.0f;
+using namespace few;
 
-struct Maps {
-  CUtensorMap k[2], v[2];  // of the prefixes, of the own slots
-};
-struct Piece {
-  int own;  // 0: of a prefix
-  int row0, r0, rows, first, n, h, u0, u1, slice;  // rows [r0, rows) of those that start in packed row row0
-};
+constexpr int kWarps = 4, kCtas = 2;  // of a CTA; CTAs of an SM
 
 template <int D>
 struct Smem {
-  static constexpr int kSub = D / 64, kStages = 3 * (128 / D);
-  __nv_bfloat16 ring[kWarps][kStages][2][kSub][kStep * 64];
-  uint64_t full[kWarps][kStages];
-  Piece piece[kWarps][8];  // a warp's, from the one it works on to the one it fetches
+  static constexpr int kStages = 3 * (128 / D);
+  Ring<D, kStages> ring[kWarps];
+  State<kStages> state[kWarps];
   int64_t total[kWarps];
   int least[kWarps];
-  uint32_t abort[kWarps];
 };
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_constant__ Maps maps, const __grid_constant__ PrefixFew a) {
   extern __shared__ __align__(1024) unsigned char smraw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(smraw + ((1024 - (saddr(smraw) & 1023)) & 1023));
-  constexpr int kStages = Smem<D>::kStages, kSub = Smem<D>::kSub;
-  static_assert(sizeof(S.ring[0][0][0][0]) % 1024 == 0);  // swizzled copies take their tiles from there
-  constexpr int KC = D / 32, VC = D / 64, TILES = D / 16;
-  constexpr int kSets = (NT + 1) / 2;  // 16-row sets of Q
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const CacheArgs& co = a.own.c;
-  const int kvh = co.kvh, group = co.group, qh = kvh * group;
-  const int units = a.groups + (a.own_units ? co.batch : 0);
   // the kernel behind this one needs nothing of it before its end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&S.full[warp][i], 1);
-    S.abort[warp] = 0u;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-
-  // ---- where this warp's run starts ----
-  auto seq = [&](int v) { return v < a.groups ? group_of(a.pre.c, v) : seq_of(co, v - a.groups); };
-  auto pieces_at = [&](int v, int h, int block) -> int32_t& {
-    return v < a.groups ? a.pre_pieces[(int64_t(v) * kvh + h) * a.pre_blocks + block]
-                        : a.own_pieces[(int64_t(v - a.groups) * kvh + h) * a.own_blocks + block];
-  };
-  auto steps_in = [&](const Seq& s) { return s.m > 0 ? (s.n + kStep - 1) / kStep : 0; };
-  auto blocks_in = [&](const Seq& s) { return (s.m * group + NT * 8 - 1) / (NT * 8); };
-  int2* kept = reinterpret_cast<int2*>(&S.ring[0][0][0][0][0]);  // steps and blocks
-  static_assert(kKept * 8 <= sizeof(S.ring));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int2* kept = reinterpret_cast<int2*>(&S.ring[0]);
+  static_assert(kKept * sizeof(int2) <= sizeof(S.ring));
   int64_t total = 0;
-  int64_t least = kMinRun;  // steps of a run, so that no unit is cut into more pieces than it may: as long as its steps by one less
-  for (int v = threadIdx.x; v < units; v += kWarps * 32) {
-    const Seq s = seq(v);
-    const int n = steps_in(s), blocks = blocks_in(s);
-    if (v < kKept) kept[v] = make_int2(n, blocks);
-    total += n ? int64_t(n + kLead) * blocks : 0;
-    const int most = v < a.groups ? a.most_shared : a.most_own;
-    least = max(least, int64_t((n + most - 2) / (most - 1)));
-    if (n == 0 && v % gridDim.x == blockIdx.x)
-      for (int h = 0; h < kvh; ++h)
-        for (int i = 0; i < blocks; ++i) pieces_at(v, h, i) = 0;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  least = __reduce_max_sync(0xffffffffu, int(least));
+  int least = 0;
+  survey<NT>(a, kept, threadIdx.x, kWarps * 32, &total, &least);
   if (lane == 0) {
     S.total[warp] = total;
-    S.least[warp] = int(least);
+    S.least[warp] = least;
   }
   __syncthreads();
   total = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
-    total += S.total[i] * kvh;
-    least = max(least, int64_t(S.least[i]));
+    total += S.total[i] * a.own.c.kvh;
+    least = max(least, S.least[i]);
   }
-  const int64_t workers = int64_t(gridDim.x) * kWarps;
-  const int64_t run = max(least, quotient(total + workers - 1, workers));
-  const int64_t r0 = (int64_t(blockIdx.x) * kWarps + warp) * run, r1 = min(total, r0 + run);
-  // the unit being fetched: its first step (kLead of them before its slots) among all, its sequence
-  int fv = 0, fi = 0, f_steps = 0, f_blocks = 1;  // fi: KV head and block of rows, the blocks next to each other
-  int64_t f_at = 0;
-  Seq fs = {0, 0, 0, 0};
-  if (r0 < total) {
-    int64_t at = r0;  // into what is left
-    for (int v0 = 0; v0 < units; v0 += 32) {
-      const int v = v0 + lane;
-      int2 k = make_int2(0, 1);
-      if (v < units) {
-        if (v < kKept) {
-          k = kept[v];
-        } else {
-          const Seq s = seq(v);
-          k = make_int2(steps_in(s), blocks_in(s));
-        }
-      }
-      const int n = k.x;
-      const int64_t mine = n ? int64_t(n + kLead) * kvh * k.y : 0;
-      int64_t pre = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += up;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, pre > at);
-      if (past) {
-        const int i = __ffs(past) - 1;
-        at -= __shfl_sync(0xffffffffu, pre - mine, i);
-        fv = v0 + i;
-        f_steps = __shfl_sync(0xffffffffu, n, i);
-        f_blocks = __shfl_sync(0xffffffffu, k.y, i);
-        break;
-      }
-      at -= __shfl_sync(0xffffffffu, pre, 31);
-    }
-    fi = int(quotient(at, int64_t(f_steps + kLead)));
-    f_at = r0 - (at - int64_t(fi) * (f_steps + kLead));
-    fs = seq(fv);
-  }
-  fence_async();
-  __syncthreads();  // the ring may be written
-
-  // ---- fetching: pieces in order, a step a call ----
-  uint32_t fetched = 0, pushed = 0;
-  int fu = 0, fu1 = 0, f_base = 0, f_row = 0;
-  auto look = [&]() {  // the next 32 steps' rows of the pool, one a lane
-    f_base = fu;
-    const CacheArgs& c = fv < a.groups ? a.pre.c : co;
-    f_row = fu + lane < fu1 ? slot_row(c, fv < a.groups ? fv : fv - a.groups, fi / f_blocks, (fu + lane) * kStep) : 0;
-  };
-  auto advance = [&]() {  // to the next unit
-    f_at += f_steps + kLead;
-    if (++fi < kvh * f_blocks) return;
-    fi = 0;
-    f_steps = 0;
-    while (f_at < r1 && ++fv < units) {
-      fs = seq(fv);
-      f_steps = steps_in(fs);
-      f_blocks = blocks_in(fs);
-      if (f_steps) break;
-    }
-    if (f_steps == 0) f_at = r1;
-  };
-  // the piece of the unit that the cursor is at; false when the run has ended
-  auto open = [&]() {
-    for (; f_at + kLead < r1; advance()) {
-      const int64_t lead = f_at + kLead;
-      const int u0 = int(max(int64_t(0), r0 - lead)), u1 = int(min(int64_t(f_steps), r1 - lead));
-      if (u1 <= u0) continue;
-      const int64_t first = quotient(lead, run);  // the warp that has the unit's first step
-      if (lane == 0) {
-        Piece& p = S.piece[warp][pushed & 7];
-        p.own = fv >= a.groups;
-        const int h = fi / f_blocks, block = fi - h * f_blocks;
-        p.row0 = fs.row0;
-        p.r0 = block * NT * 8;
-        p.rows = fs.m * group;
-        p.first = fs.first;
-        p.n = fs.n;
-        p.h = h;
-        p.u0 = u0;
-        p.u1 = u1;
-        p.slice = int(quotient(r0, run) - first);
-        if (u0 == 0) pieces_at(fv, h, block) = int(quotient(lead + f_steps - 1, run) - first) + 1;
-      }
-      ++pushed;
-      fu = u0;
-      fu1 = u1;
-      look();
-      return true;
-    }
-    return false;
-  };
-  bool more = r0 < total && open();
-  auto fetch = [&]() {
-    if (!more) return;
-    const int st = int(fetched % kStages);
-    if (fu - f_base == 32) look();
-    const int row = __shfl_sync(0xffffffffu, f_row, fu - f_base);
-    if (lane == 0) mbar_expect_tx(&S.full[warp][st], kStep * D * 2 * 2);
-    __syncwarp();
-    if (lane < 2 * kSub) {
-      const int kv = lane / kSub, sub = lane % kSub, which = fv >= a.groups;
-      tma_load_2d(&S.ring[warp][st][kv][sub][0], kv ? &maps.v[which] : &maps.k[which], sub * 64, row, &S.full[warp][st]);
-    }
-    ++fetched;
-    if (++fu == fu1) {
-      advance();
-      more = open();
-    }
-  };
-  for (int i = 0; i < kStages; ++i) fetch();
-
-  // ---- the pieces ----
-  uint32_t used = 0;
-  bool ok = true;
-  const float scale = kLog2e * rsqrtf(float(D));
-  for (uint32_t i = 0; i < pushed && ok; ++i) {
-    __syncwarp();
-    const Piece p = S.piece[warp][i & 7];
-    uint4 q[NT][KC];
-    int see[NT];  // the lane's row (8 u + g) sees the slots below this
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      const int r = p.r0 + u * 8 + g;
-      see[u] = r < p.rows ? min(p.n, p.first + r / group + 1) : 0;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.own.q) +
-                                 (int64_t(p.row0 + r / group) * qh + p.h * group + r % group) * D + t * 8;
-#pragma unroll
-      for (int j = 0; j < KC; ++j) q[u][j] = r < p.rows ? *reinterpret_cast<const uint4*>(src + j * 32) : make_uint4(0, 0, 0, 0);
-    }
-    float o[NT][TILES][4], m[NT], l[NT];
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      m[u] = -INFINITY;
-      l[u] = 0.f;
-#pragma unroll
-      for (int j = 0; j < TILES; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[u][j][k] = 0.f;
-    }
-    for (int u16 = p.u0; u16 < p.u1; ++u16) {
-      const int st = int(used % kStages), n0 = u16 * kStep;
-      ok = mbar_wait_warp(&S.full[warp][st], (used / kStages) & 1, &S.abort[warp]);
-      if (!ok) break;
-      const char* const ks = reinterpret_cast<const char*>(&S.ring[warp][st][0][0][0]);
-      char* const vs = reinterpret_cast<char*>(&S.ring[warp][st][1][0][0]);
-      if (n0 + kStep > p.n) {
-        // rows of V behind the last slot may hold anything, and 0 * NaN is NaN (in S they are masked)
-        const int live = p.n - n0;
-#pragma unroll
-        for (int j = 0; j < kSub; ++j)
-          for (int k = live * 8 + lane; k < kStep * 8; k += 32) *reinterpret_cast<uint4*>(vs + j * (kStep * 128) + k * 16) = make_uint4(0, 0, 0, 0);
-        fence_async();  // before the next copy into this place
-        __syncwarp();
-      }
-      // 16-byte chunk c of row r of a tile lies at c ^ (r % 8)
-      float x[NT][2][2];
-#pragma unroll
-      for (int i2 = 0; i2 < 2; ++i2) {
-        float d[kSets][4];
-#pragma unroll
-        for (int s = 0; s < kSets; ++s) d[s][0] = d[s][1] = d[s][2] = d[s][3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < KC; ++j) {
-          const int c = t + 4 * j, r = g + 8 * i2;
-          const uint4 k = *reinterpret_cast<const uint4*>(ks + (c >> 3) * (kStep * 128) + r * 128 + (((c & 7) ^ g) << 4));
-#pragma unroll
-          for (int s = 0; s < kSets; ++s) {
-            const uint4 lo = q[2 * s][j], hi = 2 * s + 1 < NT ? q[2 * s + 1 < NT ? 2 * s + 1 : 0][j] : make_uint4(0, 0, 0, 0);
-            mma_16816(d[s], lo.x, hi.x, lo.y, hi.y, k.x, k.y);
-            mma_16816(d[s], lo.z, hi.z, lo.w, hi.w, k.z, k.w);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            x[u][i2][j] = n0 + 8 * i2 + 2 * t + j < see[u] ? d[u / 2][2 * (u & 1) + j] * scale : -INFINITY;
-      }
-      uint4 v[4][VC];
-      auto load_v = [&]() {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 2 * t + (k & 1) + 8 * (k >> 1);
-#pragma unroll
-          for (int j = 0; j < VC; ++j) v[k][j] = *reinterpret_cast<const uint4*>(vs + j * (kStep * 128) + r * 128 + ((g ^ (r & 7)) << 4));
-        }
-        __syncwarp();  // K and V have been read
-        ++used;
-        fetch();
-      };
-      if (NT < 4) load_v();  // else when the softmax needs its registers no more
-      uint32_t w[NT][2], rest[NT][2];  // P and what its rounding leaves
-#pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        float top = fmaxf(fmaxf(x[u][0][0], x[u][0][1]), fmaxf(x[u][1][0], x[u][1][1]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const bool raise = top > m[u] + kRaise || (m[u] == -INFINITY && top > m[u]);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float by = raise ? exp2f(m[u] - top) : 1.f;  // 0 for the first reference
-          if (raise) m[u] = top;
-          l[u] *= by;
-          const float b0 = __shfl_sync(0xffffffffu, by, 8 * t), b1 = __shfl_sync(0xffffffffu, by, 8 * t + 4);
-#pragma unroll
-          for (int j = 0; j < TILES; ++j) {
-            o[u][j][0] *= b0;
-            o[u][j][1] *= b1;
-            o[u][j][2] *= b0;
-            o[u][j][3] *= b1;
-          }
-        }
-        const float ref = m[u] == -INFINITY ? 0.f : m[u];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float e0 = ex2(x[u][j][0] - ref), e1 = ex2(x[u][j][1] - ref);
-          l[u] += e0 + e1;
-          w[u][j] = bf2(e0, e1);
-          rest[u][j] = bf2(e0 - __uint_as_float(w[u][j] << 16), e1 - __uint_as_float(w[u][j] & 0xffff0000u));
-        }
-      }
-      if (NT == 4) load_v();
-      auto word = [](const uint4& y, int k) { return k == 0 ? y.x : (k == 1 ? y.y : (k == 2 ? y.z : y.w)); };
-      auto pair = [&](const uint4& y, const uint4& z, int e) { return __byte_perm(word(y, e >> 1), word(z, e >> 1), (e & 1) ? 0x7632 : 0x5410); };
-#pragma unroll
-      for (int j = 0; j < TILES; ++j) {
-        const int e1 = D == 128 ? j : j + 4, c1 = D == 128 ? VC - 1 : 0;
-        const uint32_t a0 = pair(v[0][0], v[1][0], j), a1 = pair(v[0][c1], v[1][c1], e1);
-        const uint32_t a2 = pair(v[2][0], v[3][0], j), a3 = pair(v[2][c1], v[3][c1], e1);
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
-          mma_16816(o[u][j], a0, a1, a2, a3, w[u][0], w[u][1]);
-          mma_16816(o[u][j], a0, a1, a2, a3, rest[u][0], rest[u][1]);
-        }
-      }
-    }
-    if (!ok) break;
-    // The piece's sums to its slice. Lane (g, t) has the rows 2t and 2t + 1 of every eight, of them the
-    // elements 8 g .. 8 g + 7 (d = 128: and those 64 further on).
-    const ChunkArgs& to = p.own ? a.own : a.pre;
-    const int64_t slice = int64_t(p.slice) * co.total_q * qh;
-    auto row_at = [&](int r) { return slice + int64_t(p.row0 + r / group) * qh + p.h * group + r % group; };
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-      if (t == 0 && p.r0 + u * 8 + g < p.rows) *reinterpret_cast<float2*>(to.ml + row_at(p.r0 + u * 8 + g) * 2) = make_float2(m[u], l[u]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = p.r0 + u * 8 + 2 * t + k;
-        if (r >= p.rows) continue;
-        float4* dst = reinterpret_cast<float4*>(to.part + row_at(r) * D + 8 * g);
-        dst[0] = make_float4(o[u][0][k], o[u][1][k], o[u][2][k], o[u][3][k]);
-        if constexpr (D == 128) {
-          dst[1] = make_float4(o[u][4][k], o[u][5][k], o[u][6][k], o[u][7][k]);
-          dst[16] = make_float4(o[u][0][2 + k], o[u][1][2 + k], o[u][2][2 + k], o[u][3][2 + k]);
-          dst[17] = make_float4(o[u][4][2 + k], o[u][5][2 + k], o[u][6][2 + k], o[u][7][2 + k]);
-        } else {
-          dst[1] = make_float4(o[u][0][2 + k], o[u][1][2 + k], o[u][2][2 + k], o[u][3][2 + k]);
-        }
-      }
-    }
-  }
-  if (!ok && lane == 0) {
-    for (; used != fetched; ++used) mbar_drain(&S.full[warp][used % kStages], (used / kStages) & 1);
-    flag(co.status, MP_STATUS_WAIT_TIMEOUT);
-  }
+  work<D, NT, Smem<D>::kStages>(maps, a, S.ring[warp], S.state[warp], kept, total, least, int64_t(blockIdx.x) * kWarps + warp, int64_t(gridDim.x) * kWarps, [] {
+    fence_async();
+    __syncthreads();
+  });
 }
 
 template <int D, int NT>
@@ -396,17 +66,26 @@ cudaError_t launch_rows(const Maps& maps, const PrefixFew& a, int rows, int ctas
 
 }  // namespace
 
+bool few::few_maps(const PrefixFew& a, Maps* maps) {
+  const ChunkArgs* both[2] = {&a.pre, &a.own};
+  for (int i = 0; i < 2; ++i) {
+    const CacheArgs& c = both[i]->c;
+    const uint64_t pool = uint64_t(c.n_pages) * c.kvh * c.page_size;
+    if (!make_map(&maps->k[i], both[i]->keys, c.d, pool, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&maps->v[i], both[i]->values, c.d, pool, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B))
+      return false;
+  }
+  return true;
+}
+
 cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st) {
   Maps maps;
+  if (!few_maps(a, &maps)) return cudaErrorInvalidValue;
   const ChunkArgs* both[2] = {&a.pre, &a.own};
   const int d = a.own.c.d;
   int64_t steps = 0;
   for (int i = 0; i < 2; ++i) {
     const CacheArgs& c = both[i]->c;
-    const uint64_t pool = uint64_t(c.n_pages) * c.kvh * c.page_size;
-    if (!make_map(&maps.k[i], both[i]->keys, d, pool, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&maps.v[i], both[i]->values, d, pool, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
     const int units = i ? (a.own_units ? c.batch : 0) : a.groups;
     steps += int64_t(units) * c.kvh * few_blocks(c.group, c.max_q) * ((c.max_kv + kStep - 1) / kStep + kLead);
   }

@@ -1,0 +1,44 @@
+// Host side of prefixes in slices on large tiles, beside which some CTAs go over the own slots.
+#include "mp_chunk_tc.cuh"
+
+namespace mp {
+
+// Tiles of groups of at most max_q rows in all their KV heads, of total_q rows altogether.
+static int64_t prefix_tiles(const mp_cache_config* c, int total_q, int max_q) {
+  const int64_t group = c->q_heads / c->kv_heads, each = (max_q * group + kRows - 1) / kRows;
+  return c->kv_heads * std::min(c->batch * each, c->batch + total_q * group / kRows);
+}
+// Slices are taken where a group's rows fit one half, and otherwise where there are at most half as many
+// tiles as SMs: more keep each other's keys in L2 as they are, and equal runs leave no CTA idle.
+bool prefix_in_slices(const mp_cache_config* c, int total_q, int max_q) {
+  return int64_t(max_q) * (c->q_heads / c->kv_heads) <= 128 || 2 * prefix_tiles(c, total_q, max_q) <= device_sm_count();
+}
+// Two pieces a CTA where all groups have as many tiles as the largest, one a CTA at most.
+int prefix_slices(const mp_cache_config* c, int max_q, int max_kv) {
+  const int sms = device_sm_count(), tiles = int((int64_t(max_q) * (c->q_heads / c->kv_heads) + kRows - 1) / kRows);
+  const int most = std::min((max_kv + kKeys - 1) / kKeys, (sms + c->kv_heads - 1) / c->kv_heads);
+  return std::max(1, std::min(most, int((2 * int64_t(sms) + int64_t(c->kv_heads) * tiles - 1) / (int64_t(c->kv_heads) * tiles))));
+}
+
+template <int D, Mode MODE>
+static cudaError_t launch_rows(const ChunkArgs& a, const Extra<MODE>& x, int rows, int ctas, cudaStream_t st) {
+  if (rows <= 8) return launch<D, MODE, 1>(a, x, a.c.batch, ctas, kRows, nullptr, st);
+  if (rows <= 16) return launch<D, MODE, 2>(a, x, a.c.batch, ctas, kRows, nullptr, st);
+  return launch<D, MODE, 4>(a, x, a.c.batch, ctas, kRows, nullptr, st);
+}
+template <Mode MODE>
+static cudaError_t launch_mode(const ChunkArgs& a, const OwnSide& own, int rows, cudaStream_t st) {
+  Extra<MODE> x;
+  static_cast<OwnSide&>(x) = own;
+  const int ctas = device_sm_count();
+  return a.c.d == 128 ? launch_rows<128, MODE>(a, x, rows, ctas, st) : launch_rows<64, MODE>(a, x, rows, ctas, st);
+}
+
+cudaError_t launch_prefix_slices(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st) {
+  OwnSide own;
+  own.few = few;
+  if (!few::few_maps(few, &own.maps)) return cudaErrorInvalidValue;
+  return int64_t(a.c.max_q) * a.c.group <= 128 ? launch_mode<kPairs>(a, own, rows, st) : launch_mode<kCuts>(a, own, rows, st);
+}
+
+}  // namespace mp
