@@ -1,5 +1,5 @@
-// Host side of prefixes in slices on large tiles, beside which some CTAs go over the own slots.
-#include "mp_chunk_tc.cuh"
+// Prefixes in slices on large tiles, and beside them the own slots: the rules, and heads of 128.
+#include "mp_prefix_tc.cuh"
 
 namespace mp {
 
@@ -20,25 +20,9 @@ int prefix_slices(const mp_cache_config* c, int max_q, int max_kv) {
   return std::max(1, std::min(most, int((2 * int64_t(sms) + int64_t(c->kv_heads) * tiles - 1) / (int64_t(c->kv_heads) * tiles))));
 }
 
-template <int D, Mode MODE>
-static cudaError_t launch_rows(const ChunkArgs& a, const Extra<MODE>& x, int rows, int ctas, cudaStream_t st) {
-  if (rows <= 8) return launch<D, MODE, 1>(a, x, a.c.batch, ctas, kRows, nullptr, st);
-  if (rows <= 16) return launch<D, MODE, 2>(a, x, a.c.batch, ctas, kRows, nullptr, st);
-  return launch<D, MODE, 4>(a, x, a.c.batch, ctas, kRows, nullptr, st);
-}
-template <Mode MODE>
-static cudaError_t launch_mode(const ChunkArgs& a, const OwnSide& own, int rows, cudaStream_t st) {
-  Extra<MODE> x;
-  static_cast<OwnSide&>(x) = own;
-  const int ctas = device_sm_count();
-  return a.c.d == 128 ? launch_rows<128, MODE>(a, x, rows, ctas, st) : launch_rows<64, MODE>(a, x, rows, ctas, st);
-}
-
+cudaError_t launch_prefix_slices_64(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st);
 cudaError_t launch_prefix_slices(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st) {
-  OwnSide own;
-  own.few = few;
-  if (!few::few_maps(few, &own.maps)) return cudaErrorInvalidValue;
-  return int64_t(a.c.max_q) * a.c.group <= 128 ? launch_mode<kPairs>(a, own, rows, st) : launch_mode<kCuts>(a, own, rows, st);
+  return a.c.d == 128 ? launch_slices_of<128>(a, few, rows, st) : launch_prefix_slices_64(a, few, rows, st);
 }
 
 }  // namespace mp

@@ -333,9 +333,20 @@ def test_prefix_attention(mp, dtype, hq, hk, d, page, q_lens, kv, groups, prefix
     (16, 2, 128, 16, [1] * 40, [40], [6000]),          # 320 rows: two tiles side by side
     (16, 2, 64, 0, [3] * 30, [30], [6001]),
     (40, 40, 128, 32, [1] * 300, [300], [700]),        # more tiles than half of the SMs: equal runs
+    # own rows in eights, sixteens and more beside one half's rows and beside whole tiles
+    (32, 8, 128, 64, [4, 1, 3, 4, 2, 4, 4, 4], [8], [12001]),
+    (32, 8, 64, 16, [4, 1, 3, 4, 2, 4, 4, 4], [8], [12001]),
+    (32, 8, 128, 48, [8, 1, 3, 4, 2, 6, 4, 4], [8], [9999]),
+    (32, 8, 64, 0, [8, 1, 3, 4, 2, 6, 4, 4], [8], [20000]),
+    (16, 2, 128, 0, [4, 3, 2, 1] * 10, [40], [9000]),
+    (16, 2, 128, 16, [2, 1] * 20, [40], [8001]),
+    (16, 2, 64, 64, [2, 1] * 20, [38], [8001]),
+    (16, 2, 128, 64, [1] * 40, [33], [6000]),           # a long cache among the own ones
 ])
 def test_prefix_attention_of_long_prefixes(mp, hq, hk, d, page, q_lens, groups, prefixes):
-    c = Shared(mp, "bf16", hq, hk, d, page, [m + 2 for m in q_lens], groups, prefixes)
+    own = [m + (37 * i) % 400 for i, m in enumerate(q_lens)]
+    own[1] += 5000 if groups == [33] else 0
+    c = Shared(mp, "bf16", hq, hk, d, page, own, groups, prefixes)
     cu, cu_t = offsets(q_lens)
     q = c.randn(cu[-1], hq, d, by=1.5)
     first = None
@@ -396,6 +407,19 @@ def test_prefix_attention_of_more_groups_than_one_launch_takes(mp):
     cu, cu_t = offsets([1] * batch)
     q = c.randn(batch, 8, 64)
     out, lse = attend_prefix(mp, c, q, cu, cu_t, 1, group_q=3)
+    check_prefix(c, "bf16", q, cu, out, lse)
+    assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("seqs", [5, 20])
+def test_prefix_attention_of_many_groups_in_slices(mp, seqs):
+    """1030 groups, planned 1024 at a time and most of them without a sequence, next to own slots."""
+    groups = [seqs if g % 103 == 1 or g == 1027 else 0 for g in range(1030)]
+    batch = sum(groups) + 1
+    c = Shared(mp, "bf16", 8, 1, 64, 16, [(7 * b) % 90 + 1 for b in range(batch)], groups, [(11 * g) % 300 for g in range(1030)], cap=100, pcap=4800)
+    cu, cu_t = offsets([1] * batch)
+    q = c.randn(batch, 8, 64)
+    out, lse = attend_prefix(mp, c, q, cu, cu_t, 1, max_prefix=300 * 16)
     check_prefix(c, "bf16", q, cu, out, lse)
     assert c.status.item() == 0
 
