@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
 }
 // Groups over their prefixes and sequences over their own slots in one launch.
 template <int D>
-__global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_prefix_simt(const __grid_constant__ ChunkArgs pre, const __grid_constant__ ChunkArgs own) {
-  const int groups = pre.c.batch, b = blockIdx.z;
+__global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_prefix_simt(const __grid_constant__ ChunkArgs pre, const __grid_constant__ ChunkArgs own, const int groups) {
+  const int b = blockIdx.z;
   chunk_simt_tile<D, true>(b < groups ? pre : own, b < groups ? b : b - groups);
 }
 
@@ -387,13 +387,19 @@ cudaError_t chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 template <int D>
-cudaError_t prefix_simt(const ChunkArgs& pre, const ChunkArgs& own, cudaStream_t st) {
+cudaError_t prefix_simt(const ChunkArgs* pre, const ChunkArgs* own, cudaStream_t st) {
   constexpr int smem = simt_smem(D);
   cudaError_t e = cudaFuncSetAttribute(k_prefix_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   int64_t x = 1;
-  for (const ChunkArgs* a : {&pre, &own}) x = std::max(x, (int64_t(a->c.max_q) * a->c.group + kBM - 1) / kBM * a->splits);
-  k_prefix_simt<D><<<dim3(unsigned(x), own.c.kvh, pre.c.batch + own.c.batch), kThr, smem, st>>>(pre, own);
+  int units = 0;
+  for (const ChunkArgs* a : {pre, own}) {
+    if (!a) continue;
+    x = std::max(x, (int64_t(a->c.max_q) * a->c.group + kBM - 1) / kBM * a->splits);
+    units += a->c.batch;
+  }
+  const ChunkArgs& any = own ? *own : *pre;
+  k_prefix_simt<D><<<dim3(unsigned(x), any.c.kvh, units), kThr, smem, st>>>(pre ? *pre : any, any, pre ? pre->c.batch : 0);
   return cudaGetLastError();
 }
 template <typename T, int D>
@@ -434,8 +440,8 @@ int chunk_splits(const mp_cache_config* c, int max_q, int max_kv) {
 cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   return a.c.d == 128 ? chunk_simt<128>(a, st) : chunk_simt<64>(a, st);
 }
-cudaError_t launch_prefix_simt(const ChunkArgs& pre, const ChunkArgs& own, cudaStream_t st) {
-  return own.c.d == 128 ? prefix_simt<128>(pre, own, st) : prefix_simt<64>(pre, own, st);
+cudaError_t launch_prefix_simt(const ChunkArgs* pre, const ChunkArgs* own, cudaStream_t st) {
+  return (own ? own : pre)->c.d == 128 ? prefix_simt<128>(pre, own, st) : prefix_simt<64>(pre, own, st);
 }
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st) {
   if (dtype == MP_DTYPE_BF16) return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, st) : join<__nv_bfloat16, 64>(a, st);

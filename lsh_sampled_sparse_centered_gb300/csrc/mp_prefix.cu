@@ -211,15 +211,15 @@ int simt_slices_most(const mp_cache_config* c, int max_q, int max_kv) {
   return int(std::max<int64_t>(1, std::min<int64_t>({simt_fit(c) / simt_ctas(c, max_q, 1), (int64_t(max_kv) + 63) / 64, 64})));
 }
 
-// How a pass goes: few rows per KV head through k_prefix_few, more on the tensor cores, fp32 on the CUDA
-// cores. kTiles leaves one slice, kSlices as many as prefix_slices() says.
+// How a pass goes: few rows per KV head through k_prefix_few (fp32: k_prefix_few32), more on the tensor
+// cores (fp32: in tiles on the CUDA cores). kTiles leaves one slice, kSlices as many as prefix_slices() says.
 enum Kind { kFew, kTiles, kSlices, kSimt };
 struct Pass {
   Kind kind;
   int slices;  // the most
 };
 Kind kind_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool slices) {
-  if (c->dtype != MP_DTYPE_BF16) return kSimt;
+  if (c->dtype != MP_DTYPE_BF16) return int64_t(max_q) * (c->q_heads / c->kv_heads) <= kFewRows32 ? kFew : kSimt;
   if (prefix_is_few(c, max_q, max_kv)) return kFew;
   return slices && prefix_in_slices(c, total_q, max_q) ? kSlices : kTiles;
 }
@@ -245,6 +245,7 @@ uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int m
     }
     return most;
   }
+  if (group <= kFewRows32) most = std::max(most, uint64_t(prefix_few_rows_most(c, total_q, max_kv)));
   // the slices go by the number of row tiles: the largest max_q of each, until one slice is left
   for (int64_t rows = (int64_t(group) + kChunkRows - 1) / kChunkRows * kChunkRows;; rows += kChunkRows) {
     const int q = int(std::min<int64_t>(max_q, rows / group)), s = simt_slices_most(c, q, max_kv);
@@ -317,7 +318,7 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   max_group_q = std::min(max_group_q, total_q);
   Pass own = pass_of(cfg, total_q, max_q, max_kv, false);
   Pass shared = pass_of(prefix_cfg, total_q, max_group_q, max_prefix, own.kind == kFew);
-  if (own.kind == kSimt) {
+  if (own.kind == kSimt && shared.kind == kSimt) {
     int tiles = 1;
     while (tiles * 64 < std::max(max_kv, max_prefix) && simt_ctas(cfg, max_q, simt_slices(max_kv, tiles)) +
                simt_ctas(prefix_cfg, max_group_q, simt_slices(max_prefix, tiles)) > simt_fit(cfg))
@@ -374,9 +375,9 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   cudaGetLastError();
   a.splits = own.slices;
   p.splits = shared.slices;
-  if (own.kind == kSimt) {
+  if (own.kind == kSimt || shared.kind == kSimt) {
     ProfScope ps(st, K_CHUNK_ATTEND);
-    if (launch_prefix_simt(p, a, st) != cudaSuccess) return MP_ERR_CUDA;
+    if (launch_prefix_simt(shared.kind == kSimt ? &p : nullptr, own.kind == kSimt ? &a : nullptr, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   // few rows: both passes in one launch where both have them
   if (own.kind == kFew || shared.kind == kFew) {
@@ -393,7 +394,9 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     few.pre_pieces = sl.pre_pieces;
     few.own_pieces = sl.own_pieces;
     ProfScope ps(st, beside ? K_PREFIX_ATTEND : K_PREFIX_FEW);
-    if ((beside ? launch_prefix_slices(p, few, few_rows, st) : launch_prefix_few(few, few_rows, st)) != cudaSuccess) return MP_ERR_CUDA;
+    const cudaError_t e = beside ? launch_prefix_slices(p, few, few_rows, st)
+                                 : (cfg->dtype == MP_DTYPE_BF16 ? launch_prefix_few(few, few_rows, st) : launch_prefix_few32(few, few_rows, st));
+    if (e != cudaSuccess) return MP_ERR_CUDA;
   }
   // large tiles: likewise, in equal runs of all of them
   if (own_tiles || shared_tiles) {

@@ -5,7 +5,8 @@
 
 namespace mp {
 
-constexpr int kFewRows = 32;  // query rows of a unit of k_prefix_few
+constexpr int kFewRows = 32;    // query rows of a unit of k_prefix_few
+constexpr int kFewRows32 = 16;  // and of k_prefix_few32
 
 // Units: up to 32 rows each of groups over their prefixes (none: groups = 0) and of sequences over their own slots.
 struct PrefixFew {
@@ -19,6 +20,7 @@ struct PrefixFew {
 cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st);
 // The prefixes of `a` in slices on large tiles, and beside them the own slots of `few` (no groups).
 cudaError_t launch_prefix_slices(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st);
+cudaError_t launch_prefix_few32(const PrefixFew& a, int rows, cudaStream_t st);  // fp32, up to kFewRows32 rows
 // Whether a pass with these limits goes through it.
 bool prefix_is_few(const mp_cache_config* c, int max_q, int max_kv);
 inline int few_blocks(int group, int max_q) { return int((int64_t(max_q) * group + kFewRows - 1) / kFewRows); }

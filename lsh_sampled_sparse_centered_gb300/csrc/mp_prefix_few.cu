@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
   static_assert(kKept * sizeof(int2) <= sizeof(S.ring));
   int64_t total = 0;
   int least = 0;
-  survey<NT>(a, kept, threadIdx.x, kWarps * 32, &total, &least);
+  survey<NT * 8>(a, kept, threadIdx.x, kWarps * 32, &total, &least);
   if (lane == 0) {
     S.total[warp] = total;
     S.least[warp] = least;
@@ -96,7 +96,7 @@ cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st) {
 // Up to 32 rows; with more, K and V are read once for every 32 of them, from L2 then, and a step of them is
 // 1 us of a warp. The large tiles do better, but a kernel of them starts 10 us later. (Groups of 56, 68 and
 // 20 rows over 3001, 777 and 5000 slots of four KV heads, d = 64: 28.8 us a call with large tiles for the
-// prefixes, .)
+// prefixes, 20.8 with blocks.)
 bool prefix_is_few(const mp_cache_config* c, int max_q, int max_kv) {
   const int64_t blocks = few_blocks(c->q_heads / c->kv_heads, max_q);
   const int64_t steps = int64_t(c->batch) * c->kv_heads * ((max_kv + kStep - 1) / kStep);

@@ -32,7 +32,7 @@ struct Maps {
   CUtensorMap k[2], v[2];  // of the prefixes, of the own slots
 };
 struct Piece {
-  int own;  // 0: of a prefix
+  int own, b;  // 0: of a prefix; group or sequence
   int row0, r0, rows, first, n, h, u0, u1, slice;  // rows [r0, rows) of those that start in packed row row0
 };
 // A warp's tiles (from a 1024-byte boundary: copies are swizzled) and the rest of its shared memory.
@@ -52,39 +52,135 @@ struct State {
 bool few_maps(const PrefixFew& a, Maps* maps);  // false when the driver refuses
 
 #ifdef __CUDACC__
+__device__ __forceinline__ Seq unit_of(const PrefixFew& a, int v) {
+  return v < a.groups ? group_of(a.pre.c, v) : seq_of(a.own.c, v - a.groups);
+}
+__device__ __forceinline__ int32_t& pieces_at(const PrefixFew& a, int v, int h, int block) {
+  const int kvh = a.own.c.kvh;
+  return v < a.groups ? a.pre_pieces[(int64_t(v) * kvh + h) * a.pre_blocks + block]
+                      : a.own_pieces[(int64_t(v - a.groups) * kvh + h) * a.own_blocks + block];
+}
+__device__ __forceinline__ int steps_in(const Seq& s) { return s.m > 0 ? (s.n + kStep - 1) / kStep : 0; }
+template <int ROWS>
+__device__ __forceinline__ int blocks_in(const Seq& s, int group) { return (s.m * group + ROWS - 1) / ROWS; }
+
 // Lengths and blocks of the units of this thread, of `threads`: their steps, summed and with kLead each (of
 // one KV head), and the least steps of a run for which no unit is cut into more pieces than it may. Units
 // without a slot have no piece.
-template <int NT>
+template <int ROWS, int KEPT = kKept>
 __device__ __forceinline__ void survey(const PrefixFew& a, int2* kept, int thread, int threads, int64_t* sum, int* at_least) {
   const CacheArgs& co = a.own.c;
   const int kvh = co.kvh, group = co.group;
   const int units = a.groups + (a.own_units ? co.batch : 0);
-  auto seq = [&](int v) { return v < a.groups ? group_of(a.pre.c, v) : seq_of(co, v - a.groups); };
-  auto pieces_at = [&](int v, int h, int block) -> int32_t& {
-    return v < a.groups ? a.pre_pieces[(int64_t(v) * kvh + h) * a.pre_blocks + block]
-                        : a.own_pieces[(int64_t(v - a.groups) * kvh + h) * a.own_blocks + block];
-  };
-  auto steps_in = [&](const Seq& s) { return s.m > 0 ? (s.n + kStep - 1) / kStep : 0; };
-  auto blocks_in = [&](const Seq& s) { return (s.m * group + NT * 8 - 1) / (NT * 8); };
   int64_t total = 0;
   int64_t least = kMinRun;  // as long as a unit's steps by one less than its most pieces
   for (int v = thread; v < units; v += threads) {
-    const Seq s = seq(v);
-    const int n = steps_in(s), blocks = blocks_in(s);
-    if (v < kKept) kept[v] = make_int2(n, blocks);
+    const Seq s = unit_of(a, v);
+    const int n = steps_in(s), blocks = blocks_in<ROWS>(s, group);
+    if (v < KEPT) kept[v] = make_int2(n, blocks);
     total += n ? int64_t(n + kLead) * blocks : 0;
     const int most = v < a.groups ? a.most_shared : a.most_own;
     least = max(least, int64_t((n + most - 2) / (most - 1)));
     if (n == 0 && v % gridDim.x == blockIdx.x)
       for (int h = 0; h < kvh; ++h)
-        for (int i = 0; i < blocks; ++i) pieces_at(v, h, i) = 0;
+        for (int i = 0; i < blocks; ++i) pieces_at(a, v, h, i) = 0;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   *sum = total;
   *at_least = __reduce_max_sync(0xffffffffu, int(least));
 }
+
+// A warp's run, `worker` of `workers`, of `total` steps in all: its pieces in order. All lanes hold the same.
+template <int ROWS, int KEPT = kKept>
+struct Walk {
+  const PrefixFew& a;
+  int64_t run, r0, r1, at = 0;  // at: the first step of the unit (kLead of them before its slots) among all
+  int units, v = 0, i = 0, steps = 0, blocks = 1;  // i: KV head and block of rows, the blocks next to each other
+  Seq s = {0, 0, 0, 0};
+
+  __device__ __forceinline__ Walk(const PrefixFew& few, const int2* kept, int64_t total, int64_t least, int64_t worker, int64_t workers) : a(few) {
+    const int lane = threadIdx.x & 31, kvh = a.own.c.kvh, group = a.own.c.group;
+    units = a.groups + (a.own_units ? a.own.c.batch : 0);
+    run = max(least, quotient(total + workers - 1, workers));
+    r0 = worker * run;
+    r1 = min(total, r0 + run);
+    if (r0 >= total) {
+      at = r1;  // nothing is left
+      return;
+    }
+    int64_t in = r0;  // into what is left
+    for (int v0 = 0; v0 < units; v0 += 32) {
+      int2 k = make_int2(0, 1);
+      if (v0 + lane < units) {
+        if (v0 + lane < KEPT) {
+          k = kept[v0 + lane];
+        } else {
+          const Seq u = unit_of(a, v0 + lane);
+          k = make_int2(steps_in(u), blocks_in<ROWS>(u, group));
+        }
+      }
+      const int64_t mine = k.x ? int64_t(k.x + kLead) * kvh * k.y : 0;
+      int64_t pre = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, pre > in);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        in -= __shfl_sync(0xffffffffu, pre - mine, l);
+        v = v0 + l;
+        steps = __shfl_sync(0xffffffffu, k.x, l);
+        blocks = __shfl_sync(0xffffffffu, k.y, l);
+        break;
+      }
+      in -= __shfl_sync(0xffffffffu, pre, 31);
+    }
+    i = int(quotient(in, int64_t(steps + kLead)));
+    at = r0 - (in - int64_t(i) * (steps + kLead));
+    s = unit_of(a, v);
+  }
+  __device__ __forceinline__ void advance() {  // to the next unit
+    at += steps + kLead;
+    if (++i < a.own.c.kvh * blocks) return;
+    i = 0;
+    steps = 0;
+    while (at < r1 && ++v < units) {
+      s = unit_of(a, v);
+      steps = steps_in(s);
+      blocks = blocks_in<ROWS>(s, a.own.c.group);
+      if (steps) break;
+    }
+    if (steps == 0) at = r1;
+  }
+  // The piece of the unit that the walk is at, or of the first behind it that has one; false where the run
+  // has ended. The warp that starts a unit notes its number of pieces.
+  __device__ __forceinline__ bool open(Piece* p) {
+    for (; at + kLead < r1; advance()) {
+      const int64_t lead = at + kLead;
+      const int u0 = int(max(int64_t(0), r0 - lead)), u1 = int(min(int64_t(steps), r1 - lead));
+      if (u1 <= u0) continue;
+      const int64_t first = quotient(lead, run);  // the warp that has the unit's first step
+      const int h = i / blocks, block = i - h * blocks;
+      p->own = v >= a.groups;
+      p->b = v >= a.groups ? v - a.groups : v;
+      p->row0 = s.row0;
+      p->r0 = block * ROWS;
+      p->rows = s.m * a.own.c.group;
+      p->first = s.first;
+      p->n = s.n;
+      p->h = h;
+      p->u0 = u0;
+      p->u1 = u1;
+      p->slice = int(quotient(r0, run) - first);
+      if (u0 == 0 && (threadIdx.x & 31) == 0) pieces_at(a, v, h, block) = int(quotient(lead + steps - 1, run) - first) + 1;
+      return true;
+    }
+    return false;
+  }
+};
 
 // One warp's run: `worker` of `workers`, of `total` steps in all. `found` is called by all warps of the CTA
 // between the last look at `kept` and the first copy into the rings.
@@ -98,56 +194,7 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const CacheArgs& co = a.own.c;
   const int kvh = co.kvh, group = co.group, qh = kvh * group;
-  const int units = a.groups + (a.own_units ? co.batch : 0);
-  auto seq = [&](int v) { return v < a.groups ? group_of(a.pre.c, v) : seq_of(co, v - a.groups); };
-  auto pieces_at = [&](int v, int h, int block) -> int32_t& {
-    return v < a.groups ? a.pre_pieces[(int64_t(v) * kvh + h) * a.pre_blocks + block]
-                        : a.own_pieces[(int64_t(v - a.groups) * kvh + h) * a.own_blocks + block];
-  };
-  auto steps_in = [&](const Seq& s) { return s.m > 0 ? (s.n + kStep - 1) / kStep : 0; };
-  auto blocks_in = [&](const Seq& s) { return (s.m * group + NT * 8 - 1) / (NT * 8); };
-  const int64_t run = max(least, quotient(total + workers - 1, workers));
-  const int64_t r0 = worker * run, r1 = min(total, r0 + run);
-  // the unit being fetched: its first step (kLead of them before its slots) among all, its sequence
-  int fv = 0, fi = 0, f_steps = 0, f_blocks = 1;  // fi: KV head and block of rows, the blocks next to each other
-  int64_t f_at = 0;
-  Seq fs = {0, 0, 0, 0};
-  if (r0 < total) {
-    int64_t at = r0;  // into what is left
-    for (int v0 = 0; v0 < units; v0 += 32) {
-      const int v = v0 + lane;
-      int2 k = make_int2(0, 1);
-      if (v < units) {
-        if (v < kKept) {
-          k = kept[v];
-        } else {
-          const Seq s = seq(v);
-          k = make_int2(steps_in(s), blocks_in(s));
-        }
-      }
-      const int n = k.x;
-      const int64_t mine = n ? int64_t(n + kLead) * kvh * k.y : 0;
-      int64_t pre = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += up;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, pre > at);
-      if (past) {
-        const int i = __ffs(past) - 1;
-        at -= __shfl_sync(0xffffffffu, pre - mine, i);
-        fv = v0 + i;
-        f_steps = __shfl_sync(0xffffffffu, n, i);
-        f_blocks = __shfl_sync(0xffffffffu, k.y, i);
-        break;
-      }
-      at -= __shfl_sync(0xffffffffu, pre, 31);
-    }
-    fi = int(quotient(at, int64_t(f_steps + kLead)));
-    f_at = r0 - (at - int64_t(fi) * (f_steps + kLead));
-    fs = seq(fv);
-  }
+  Walk<NT * 8> walk(a, kept, total, least, worker, workers);
   found();
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&S.full[i], 1);
@@ -159,56 +206,22 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
 
   // ---- fetching: pieces in order, a step a call ----
   uint32_t fetched = 0, pushed = 0;
-  int fu = 0, fu1 = 0, f_base = 0, f_row = 0;
+  int fu = 0, f_base = 0, f_row = 0;
+  Piece next = {};  // the piece that is fetched
   auto look = [&]() {  // the next 32 steps' rows of the pool, one a lane
     f_base = fu;
-    const CacheArgs& c = fv < a.groups ? a.pre.c : co;
-    f_row = fu + lane < fu1 ? slot_row(c, fv < a.groups ? fv : fv - a.groups, fi / f_blocks, (fu + lane) * kStep) : 0;
+    const CacheArgs& c = next.own ? co : a.pre.c;
+    f_row = fu + lane < next.u1 ? slot_row(c, next.b, next.h, (fu + lane) * kStep) : 0;
   };
-  auto advance = [&]() {  // to the next unit
-    f_at += f_steps + kLead;
-    if (++fi < kvh * f_blocks) return;
-    fi = 0;
-    f_steps = 0;
-    while (f_at < r1 && ++fv < units) {
-      fs = seq(fv);
-      f_steps = steps_in(fs);
-      f_blocks = blocks_in(fs);
-      if (f_steps) break;
-    }
-    if (f_steps == 0) f_at = r1;
-  };
-  // the piece of the unit that the cursor is at; false when the run has ended
   auto open = [&]() {
-    for (; f_at + kLead < r1; advance()) {
-      const int64_t lead = f_at + kLead;
-      const int u0 = int(max(int64_t(0), r0 - lead)), u1 = int(min(int64_t(f_steps), r1 - lead));
-      if (u1 <= u0) continue;
-      const int64_t first = quotient(lead, run);  // the warp that has the unit's first step
-      if (lane == 0) {
-        Piece& p = S.piece[pushed & 7];
-        p.own = fv >= a.groups;
-        const int h = fi / f_blocks, block = fi - h * f_blocks;
-        p.row0 = fs.row0;
-        p.r0 = block * NT * 8;
-        p.rows = fs.m * group;
-        p.first = fs.first;
-        p.n = fs.n;
-        p.h = h;
-        p.u0 = u0;
-        p.u1 = u1;
-        p.slice = int(quotient(r0, run) - first);
-        if (u0 == 0) pieces_at(fv, h, block) = int(quotient(lead + f_steps - 1, run) - first) + 1;
-      }
-      ++pushed;
-      fu = u0;
-      fu1 = u1;
-      look();
-      return true;
-    }
-    return false;
+    if (!walk.open(&next)) return false;
+    if (lane == 0) S.piece[pushed & 7] = next;
+    ++pushed;
+    fu = next.u0;
+    look();
+    return true;
   };
-  bool more = r0 < total && open();
+  bool more = open();
   auto fetch = [&]() {
     if (!more) return;
     const int st = int(fetched % kStages);
@@ -217,12 +230,12 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
     if (lane == 0) mbar_expect_tx(&S.full[st], kStep * D * 2 * 2);
     __syncwarp();
     if (lane < 2 * kSub) {
-      const int kv = lane / kSub, sub = lane % kSub, which = fv >= a.groups;
+      const int kv = lane / kSub, sub = lane % kSub, which = next.own;
       tma_load_2d(&ring.tile[st][kv][sub][0], kv ? &maps.v[which] : &maps.k[which], sub * 64, row, &S.full[st]);
     }
     ++fetched;
-    if (++fu == fu1) {
-      advance();
+    if (++fu == next.u1) {
+      walk.advance();
       more = open();
     }
   };

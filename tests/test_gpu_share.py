@@ -358,6 +358,33 @@ def test_prefix_attention_of_long_prefixes(mp, hq, hk, d, page, q_lens, groups, 
     assert c.status.item() == 0
 
 
+@pytest.mark.parametrize("hq,hk,d,page,q_lens,groups,prefixes", [
+    (40, 40, 128, 0, [1] * 30, [], []),                       # a row per KV head, no prefix at all
+    (8, 8, 64, 16, [1, 2, 3, 4, 1, 1], [4, 1], [333, 0]),     # up to four rows, both passes
+    (8, 2, 64, 48, [1, 2, 1, 0, 2], [1, 1, 1], [5000, 17, 3]),  # up to eight
+    (8, 2, 128, 16, [2, 1, 2, 1], [1, 0, 2], [2999, 5, 16]),
+    (7, 1, 128, 32, [1, 2, 1], [2], [9000]),                  # up to sixteen
+    (16, 1, 64, 0, [1, 1, 1], [1, 1], [31, 4097]),
+    (5, 5, 128, 0, [1, 3, 7, 2], [1, 2], [64, 1500]),        # own slots by warps, a group's prefix in tiles
+    (4, 1, 64, 64, [1, 1, 30], [2], [700]),                   # and the other way round
+    (12, 1, 128, 256, [1] * 9, [9], [777]),
+])
+def test_prefix_attention_of_few_rows_in_fp32(mp, hq, hk, d, page, q_lens, groups, prefixes):
+    own = [m + (173 * i) % 900 for i, m in enumerate(q_lens)]
+    own[-1] = q_lens[-1]
+    c = Shared(mp, "f32", hq, hk, d, page, own, groups or [0], prefixes or [0])
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1] + 2, hq, d, by=1.5)
+    group_q = max(c.limits(cu)[0], 1)
+    out, lse = attend_prefix(mp, c, q, cu, cu_t, max(q_lens), group_q=group_q)
+    check_prefix(c, "f32", q, cu, out, lse)
+    wide, z = attend_prefix(mp, c, q, cu, cu_t, max(q_lens), max_kv=c.ps * c.cols, group_q=group_q + 2, max_prefix=c.pre.ps * c.pre.cols)
+    check_prefix(c, "f32", q, cu, wide, z)
+    assert c.status.item() == 0
+    again, _ = attend_prefix(mp, c, q, cu, cu_t, max(q_lens), group_q=group_q)
+    assert torch.equal(again[:cu[-1]], out[:cu[-1]])
+
+
 def test_prefix_attention_over_pages_of_another_size(mp):
     """The prefixes' cache is another one: short pages here, a dense one there."""
     for page, ppage in ((16, 128), (64, 0), (0, 48)):
