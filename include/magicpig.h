@@ -504,7 +504,8 @@ MP_API int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config
  *                not looked at where both arrays are NULL). mp_cache_evict's `kept` fits as
  *                from_positions, with to_positions NULL: the kept keys then stand at 0, 1, ...
  *   scale      : finite.
- * No page may hold slots of two sequences (it would be turned twice). Slots in a bad page are left. */
+ * No page stands twice in the tables (its keys would be turned twice, and by two at once). Slots in a bad
+ * page are left. */
 MP_API int mp_cache_rotate(const mp_cache_config* cfg, const mp_rotary* rotary, void* keys, const int32_t* page_table,
                            const int32_t* kv_len, int32_t max_kv, const double* from_freq, const double* to_freq,
                            const int32_t* from_positions, const int32_t* to_positions, int32_t position_heads,

@@ -1,4 +1,5 @@
-// Exact attention of a chunk of new tokens on the 5th-generation tensor cores (bf16).
+// Exact attention of a chunk of new tokens on the 5th-generation tensor cores (bf16), and of the rows of
+// groups over the prefixes that their sequences share (see Mode).
 //
 // A CTA works on 256 query rows of one KV head (row = token * group + head of the group),
 // as two halves of 128 rows, against 128 keys at a time:
@@ -54,6 +55,8 @@ constexpr int kLead = 3, kLeadWhole = 5;
 // The same for a piece of a cut, whose sums are written and joined besides: its start is Q behind the first
 // copies of K and V (1 and 2 pieces a CTA, 512 rows over 98304 slots: 139 and 150 us).
 constexpr int kLeadPiece = 7;
+// And where every tile's sums are written and joined (six chunks of 33 to 517 tokens over 16384 shared
+// slots, 32/8 heads: 302 us with 5, 277 with 8, 280 with 11, 286 with 14).
 constexpr int kLeadBoth = 8;
 constexpr int kMinRun = 2;    // units of a CTA at least
 constexpr int kCut = 10;      // units that cutting the tiles costs: a second piece for most CTAs, and the join
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (blockIdx.x == 0)
         for (int g = 0; g < groups; ++g) {
           const int n = pieces_of(__shfl_sync(0xffffffffu, steps1, g), length);
-          for (int h = lane; h < c.kvh; h += 32) a.pieces[(b_begin + g) * c.kvh + h] = n;
+          for (int h = lane; h < c.kvh; h += 32) a.pieces[int64_t(b_begin + g) * c.kvh + h] = n;
         }
     }
     if (!by_warp && warp == 0) {
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       length = longest_piece(at, at, groups, c.kvh, max(1, tile_ctas), a.splits);
       if (blockIdx.x == 0)
-        for (int i = lane; i < groups * c.kvh; i += 32) a.pieces[b_begin * c.kvh + i] = pieces_of(steps[i / c.kvh], length);
+        for (int i = lane; i < groups * c.kvh; i += 32) a.pieces[int64_t(b_begin) * c.kvh + i] = pieces_of(steps[i / c.kvh], length);
       fence_async();
     }
     if (length > 0 && lane == 0) S.lead = length;
@@ -1400,18 +1403,18 @@ cudaError_t launch(ChunkArgs a, Extra<MODE> extra, int units, int ctas, int slot
     k_chunk_tc<D, MODE, NT><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(units, b + kGroup), slot_rows, extra);
     if constexpr (CUT) {
       extra.few.own_units = false;  // the first launch has done them
-      continue;
+    } else {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 8) + 7) / 8);
+      cfg.blockDim = dim3(256);
+      cfg.stream = st;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D, MODE == kBoth>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, ((slot_rows + 31) / 32 * (D / 8) + 7) / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D, MODE == kBoth>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }

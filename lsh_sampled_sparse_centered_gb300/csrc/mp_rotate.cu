@@ -20,7 +20,7 @@ namespace {
 constexpr int kThr = 256;
 constexpr int kOneAtOnce = 2, kOwnAtOnce = 1;  // keys of a lane that are worked on, as many more are on their way
 constexpr int kResident = 3;  // CTAs of an SM
-constexpr int kRounds = 2;
+constexpr int kRounds = 2;    // of them (ROUNDS)
 
 struct RotateArgs {
   CacheArgs c;
@@ -164,8 +164,14 @@ __global__ void __launch_bounds__(kThr, kResident) k_cache_rotate(const RotateAr
         y2[j] = y[j] * cs[j] + x[j] * sn[j];
       }
     }
-    __stcs(reinterpret_cast<uint4*>(row + e0), Vec<T>::pack(x2));
-    __stcs(reinterpret_cast<uint4*>(row + e1), Vec<T>::pack(y2));
+    uint4 w0 = Vec<T>::pack(x2), w1 = Vec<T>::pack(y2);
+    if (V == 8 && !whole) {  // elements that do not turn keep their bits, whatever NaN they are
+      const int live = half - p0;  // pairs, a 32-bit word each (only interleaved ones end inside a lane's vectors)
+      w0 = make_uint4(w0.x, live > 1 ? w0.y : u[0].y, live > 2 ? w0.z : u[0].z, live > 3 ? w0.w : u[0].w);
+      w1 = make_uint4(live > 4 ? w1.x : u[1].x, live > 5 ? w1.y : u[1].y, live > 6 ? w1.z : u[1].z, live > 7 ? w1.w : u[1].w);
+    }
+    __stcs(reinterpret_cast<uint4*>(row + e0), w0);
+    __stcs(reinterpret_cast<uint4*>(row + e1), w1);
   };
   // the key of a slot and head 0 (ONE) or blockIdx.y, and where it stands; at < 0: none
   struct Key {

@@ -11,7 +11,10 @@ Tolerances, with h = half a step of a type relative to the value (fp32 2^-24, bf
   of up to 2^31 positions and is off by 2^-53 of it: 2^-22 of a turn at most, for positions below 2^20 2^-33.
 """
 import math
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -427,14 +430,15 @@ def test_prefix_attention_is_the_chunk_attention_over_both(mp):
         check_prefix(c, "bf16", q, cu, both, z)
 
 
-def test_prefix_attention_of_more_groups_than_one_launch_takes(mp):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefix_attention_of_more_groups_than_one_launch_takes(mp, dtype):
     groups = [(i * 3) % 4 for i in range(1100)]
     batch = sum(groups) + 2
-    c = Shared(mp, "bf16", 8, 1, 64, 16, [(7 * b) % 20 + 1 for b in range(batch)], groups, [(11 * g) % 50 for g in range(1100)])
+    c = Shared(mp, dtype, 8, 1, 64, 16, [(7 * b) % 20 + 1 for b in range(batch)], groups, [(11 * g) % 50 for g in range(1100)])
     cu, cu_t = offsets([1] * batch)
     q = c.randn(batch, 8, 64)
     out, lse = attend_prefix(mp, c, q, cu, cu_t, 1, group_q=3)
-    check_prefix(c, "bf16", q, cu, out, lse)
+    check_prefix(c, dtype, q, cu, out, lse)
     assert c.status.item() == 0
 
 
@@ -711,6 +715,20 @@ def test_rotate_keeps_infinities_in_their_pairs(mp):
         assert hit <= odd <= hit | {40} and torch.isfinite(k[0, 0, [0, 2]]).all()
 
 
+def test_rotate_leaves_the_bits_of_what_does_not_turn(mp):
+    """NaN of any bits behind rot_dim, interleaved pairs that end inside a lane's vectors among them."""
+    for dtype, word, bits in (("bf16", torch.int16, -3), ("f32", torch.int32, -5)):
+        for rot in (2, 6, 8, 14, 18, 32, 54, 64):
+            c = Cache(mp, dtype, 2, 2, 64, 16, [20, 3])
+            c.keys[:] = torch.randn(c.keys.shape, device=DEV).to(DT[dtype])
+            c.keys.view(word)[..., rot:] = bits
+            start = torch.full((2, 1, 20), 11, dtype=torch.int32, device=DEV)
+            before = c.keys.clone()
+            mp.mp_cache_rotate(c.cfg, mp.make_rotary(rot_dim=rot, interleaved=True), c.keys, c.table, c.kv_len, 20, freq(rot), None, start, None, 1.0, c.status)
+            assert (c.keys.view(word)[..., rot:] == bits).all() and torch.isfinite(c.keys[..., :rot]).all()
+            assert not torch.equal(c.keys.view(word), before.view(word))
+
+
 def test_rotate_captured_follows_lengths_and_positions(mp):
     c = Cache(mp, "bf16", 2, 2, 128, 64, [500, 90])
     start = torch.zeros(2, 2, 500, dtype=torch.int32, device=DEV)
@@ -802,3 +820,56 @@ def test_a_serving_loop_plans_shares_cuts_and_moves(mp):
     for change in ([1, 1, 1, 1, 1], [5, -2, 1, 3, 1]):
         step(change, dense, dk, dv, None, None, None, kv_len, ds, 64)
     assert status.item() == 0 and kv_len.tolist() == lengths
+
+
+FIRST = '''
+import sys
+import torch
+sys.path.insert(0, {root!r})
+import lsh_sampled_sparse_centered_gb300 as mp
+dev, d, hk, hq, n, prefix, m = "cuda:0", {d}, 2, 8, 700, {prefix}, {m}
+dt = {{"bf16": torch.bfloat16, "f32": torch.float32}}[{dtype!r}]
+g = torch.Generator(device=dev).manual_seed(1)
+rnd = lambda *s: torch.randn(*s, generator=g, device=dev).to(dt)
+ints = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+cfg = mp.make_cache_config(batch=2, kv_heads=hk, q_heads=hq, head_dim=d, page_size=16, n_pages=96, max_pages=44, dtype={dtype!r})
+pre = mp.make_cache_config(batch=1, kv_heads=hk, q_heads=hq, head_dim=d, page_size=prefix, n_pages=1, dtype={dtype!r})
+keys, values, pk, pv = rnd(96, hk, 16, d), rnd(96, hk, 16, d), rnd(1, hk, prefix, d), rnd(1, hk, prefix, d)
+table, free = ints([list(range(44)), list(range(44, 88))]), ints(list(range(88, 96)) + [0] * 88)
+q, out, lse = rnd(2 * m, hq, d), torch.empty(2 * m, hq, d, dtype=dt, device=dev), torch.empty(2 * m, hq, device=dev)
+kv, change, n_free, new_len, new_free, cu, group, pl = ints([640, 600]), ints([m, m]), ints([8]), ints([0, 0]), ints([0]), ints([0, 0, 0]), ints([0, 2]), ints([prefix])
+f, at = torch.ones(d // 2, dtype=torch.float64, device=dev), ints([[[i + 1 for i in range(700)]]] * 2)
+ws = torch.empty(mp.mp_prefix_workspace_bytes(cfg, pre, 2 * m, m, 700, 2 * m, prefix), dtype=torch.uint8, device=dev)
+status = ints([0])
+first = keys.clone()
+def step():
+    mp.mp_cache_plan(cfg, change, None, kv, n_free, 2 * m, table, free, new_len, new_free, cu, None, None, None, status)
+    mp.mp_prefix_attention(cfg, pre, q, cu, new_len, m, 700, keys, values, table, group, pl, 2 * m, prefix, pk, pv, None, out, lse, ws, status)
+    mp.mp_cache_rotate(cfg, mp.make_rotary(rot_dim=d), keys, table, new_len, 700, f, None, at, None, 1.0, status)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (out, lse, new_len, new_free, cu, keys)]
+keys.copy_(first)
+step()
+torch.cuda.synchronize()
+assert status.item() == 0 and new_len.tolist() == [640 + m, 600 + m]
+assert all(torch.equal(a, b) for a, b in zip(got, (out, lse, new_len, new_free, cu, keys)))
+print("same")
+'''
+
+
+@pytest.mark.parametrize("dtype,d,m,prefix", [("bf16", 128, 1, 500), ("bf16", 64, 12, 40000), ("bf16", 128, 12, 40000), ("bf16", 128, 40, 1000),
+                                              ("f32", 64, 1, 700), ("f32", 128, 30, 300)])
+def test_a_first_call_may_be_captured(dtype, d, m, prefix):
+    """Kernels are loaded and their shared memory set under the capture; equal bits afterwards."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, dtype=dtype, d=d, m=m, prefix=prefix)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), (r.stdout[-500:], r.stderr[-2000:])
