@@ -106,8 +106,6 @@ inline int box_rows(const int32_t* table, int page_size) {
 
 cudaError_t launch_cache_append(const AppendArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st);
-// Groups over their prefixes and sequences over their own slots, either of which may be missing (fp32).
-cudaError_t launch_prefix_simt(const ChunkArgs* pre, const ChunkArgs* own, cudaStream_t st);
 cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st);

@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "mp_cache.cuh"
+#include "mp_prefix_few.cuh"
 
 namespace mp {
 namespace {
@@ -76,9 +77,11 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // row / 8 % 2 for Q, key % 16 for P, 0 for V (with d = 64 3 % slower than padding).
 // Products run as packed pairs, over pairs of d for S and of rows for O. V arrives under S and
 // the softmax, the next K under the product with V.
-// GROUP: b may be a group, whose rows go over the prefix that its sequences share (c.cu_group is set).
-template <int D, bool GROUP>
-__device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b) {
+// The tile: rows [r0, r0 + 64) of those of `s` (sequence b, or a group where c.cu_group is set), over the
+// slots [k0, k1) that any of them sees; `split` is the slice for its sums.
+template <int D>
+__device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b, const int h, const Seq& s, const int r0, const int k0, const int k1,
+                                                const int split) {
   constexpr bool kPad = D == 64;
   constexpr int kRow = D + kPad * 4, kPt = kBM + kPad * 4;
   auto place = [](int at, int x) { return kPad ? at : at ^ (x * 4); };  // of a chunk's first float
@@ -88,18 +91,8 @@ __device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b)
   float* vs = ks + kBN * kRow;   // [64][kRow]
   float* pt = vs + kBN * kRow;   // [64 keys][kPt]
   const CacheArgs& c = a.c;
-  const int h = blockIdx.y;
-  const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
-  const Seq s = GROUP && c.cu_group ? group_of(c, b) : seq_of(c, b);
-  const int rows = s.m * c.group, r0 = tile * kBM;
-  if (r0 >= rows) return;
-  const int qh = c.kvh * c.group;
-  const int first = s.first;                                         // slot of token 0
-  const int last = first + min(r0 + kBM - 1, rows - 1) / c.group;     // slot of the tile's last token
+  const int rows = s.m * c.group, qh = c.kvh * c.group, first = s.first;  // first: slot of token 0
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  // this split's keys: a run of 64-key tiles of the sequence
-  const int tiles = (s.n + kBN - 1) / kBN, per = (tiles + a.splits - 1) / a.splits;
-  const int k0 = min(s.n, split * per * kBN), k1 = min(min(s.n, last + 1), (split + 1) * per * kBN);
   constexpr int kVec = D / 4, kStep = kThr / kVec;  // vectors of a row, rows that the CTA copies at a time
   const int cr = threadIdx.x / kVec, ce = threadIdx.x % kVec * 4;
   auto copy_tile = [&](float* dst, const void* base, int n0, int swizzle) {
@@ -220,7 +213,7 @@ __device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b)
     if (more) copy_tile(vs, a.values, n0 + kBN, 0);
   }
   copy_wait<0>();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_chunk_join may be set up
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float sum = l[i];
@@ -246,15 +239,52 @@ __device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b)
   }
 }
 
+// The last slot that a row of the tile sees, and one.
+__device__ __forceinline__ int seen_by(const Seq& s, int group, int r0) { return min(s.n, s.first + min(r0 + kBM - 1, s.m * group - 1) / group + 1); }
+
 template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const ChunkArgs a) {
-  chunk_simt_tile<D, false>(a, blockIdx.z);
+  const int split = blockIdx.x % a.splits, r0 = blockIdx.x / a.splits * kBM;
+  const Seq s = seq_of(a.c, blockIdx.z);
+  if (r0 >= s.m * a.c.group) return;
+  // this split's keys: a run of 64-key tiles of the sequence
+  const int tiles = (s.n + kBN - 1) / kBN, per = (tiles + a.splits - 1) / a.splits;
+  chunk_simt_tile<D>(a, blockIdx.z, blockIdx.y, s, r0, min(s.n, split * per * kBN), min(seen_by(s, a.c.group, r0), (split + 1) * per * kBN), split);
 }
-// Groups over their prefixes and sequences over their own slots in one launch.
+
+// Groups over their prefixes and sequences over their own slots: the tiles of all, a step for every 64
+// slots, laid end to end and cut into equal runs, one a CTA, as the warps of the kernels of few rows have them
+// (mp_prefix_few.cuh). Slices of one length for all took longer where lengths differ, us a call:
+//   drafts of 1 to 9 tokens of 33 sequences, 6/2 heads, prefixes of 614, 20978 and 47562 slots, d = 64   836   140
+//   of 29 sequences, 12/1 heads, five prefixes of 1 to 14768, d = 128                                   1190   160
+//   of 14 sequences, 28/4 heads, prefixes of 26434 and 11304, d = 64                                     552   408
+// and less where they do not (five chunks, 101 rows over 2000 slots, eight heads: 37 and 43).
 template <int D>
-__global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_prefix_simt(const __grid_constant__ ChunkArgs pre, const __grid_constant__ ChunkArgs own, const int groups) {
-  const int b = blockIdx.z;
-  chunk_simt_tile<D, true>(b < groups ? pre : own, b < groups ? b : b - groups);
+__global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_prefix_simt(const __grid_constant__ PrefixFew a) {
+  using Cut = few::Cutting<kBM, kBN, 1, 1, 2048>;
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int64_t totals[kThr / 32];
+  __shared__ int leasts[kThr / 32];
+  int2* kept = reinterpret_cast<int2*>(sm);
+  int64_t total = 0;
+  int least = 0;
+  few::survey<Cut>(a, kept, threadIdx.x, kThr, &total, &least);
+  if ((threadIdx.x & 31) == 0) {
+    totals[threadIdx.x >> 5] = total;
+    leasts[threadIdx.x >> 5] = least;
+  }
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kThr / 32; ++i) {
+    total += totals[i] * a.own.c.kvh;
+    least = max(least, leasts[i]);
+  }
+  few::Walk<Cut> walk(a, kept, total, least, blockIdx.x, gridDim.x);
+  __syncthreads();  // `kept` lies where the tiles go
+  few::Piece p = {};
+  for (; walk.open(&p); walk.advance())
+    chunk_simt_tile<D>(p.own ? a.own : a.pre, p.b, p.h, walk.s, p.r0, min(p.n, p.u0 * kBN), min(seen_by(walk.s, a.own.c.group, p.r0), p.u1 * kBN), p.slice);
 }
 
 // Joins the splits' (m, l, sum) of a query row, in an order that is fixed by their number:
@@ -387,19 +417,18 @@ cudaError_t chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 template <int D>
-cudaError_t prefix_simt(const ChunkArgs* pre, const ChunkArgs* own, cudaStream_t st) {
+cudaError_t prefix_simt(const PrefixFew& a, cudaStream_t st) {
   constexpr int smem = simt_smem(D);
+  static_assert(2048 * sizeof(int2) <= smem);
   cudaError_t e = cudaFuncSetAttribute(k_prefix_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  int64_t x = 1;
-  int units = 0;
-  for (const ChunkArgs* a : {pre, own}) {
-    if (!a) continue;
-    x = std::max(x, (int64_t(a->c.max_q) * a->c.group + kBM - 1) / kBM * a->splits);
-    units += a->c.batch;
+  int64_t steps = 0;
+  for (const ChunkArgs* x : {&a.pre, &a.own}) {
+    const int units = x == &a.pre ? a.groups : (a.own_units ? x->c.batch : 0);
+    steps += int64_t(units) * x->c.kvh * ((int64_t(x->c.max_q) * x->c.group + kBM - 1) / kBM) * ((int64_t(x->c.max_kv) + kBN - 1) / kBN + 1);
   }
-  const ChunkArgs& any = own ? *own : *pre;
-  k_prefix_simt<D><<<dim3(unsigned(x), any.c.kvh, units), kThr, smem, st>>>(pre ? *pre : any, any, pre ? pre->c.batch : 0);
+  const int ctas = int(std::max<int64_t>(1, std::min<int64_t>((D == 64 ? 3 : 2) * int64_t(device_sm_count()), steps)));
+  k_prefix_simt<D><<<ctas, kThr, smem, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T, int D>
@@ -440,9 +469,7 @@ int chunk_splits(const mp_cache_config* c, int max_q, int max_kv) {
 cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t st) {
   return a.c.d == 128 ? chunk_simt<128>(a, st) : chunk_simt<64>(a, st);
 }
-cudaError_t launch_prefix_simt(const ChunkArgs* pre, const ChunkArgs* own, cudaStream_t st) {
-  return (own ? own : pre)->c.d == 128 ? prefix_simt<128>(pre, own, st) : prefix_simt<64>(pre, own, st);
-}
+cudaError_t launch_prefix_simt(const PrefixFew& a, cudaStream_t st) { return a.own.c.d == 128 ? prefix_simt<128>(a, st) : prefix_simt<64>(a, st); }
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st) {
   if (dtype == MP_DTYPE_BF16) return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, st) : join<__nv_bfloat16, 64>(a, st);
   return a.c.d == 128 ? join<float, 128>(a, st) : join<float, 64>(a, st);

@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t sum;
     int least;
     if (warp == 10 && by_warp) early = b_begin + lane < b_end ? group_of(c, b_begin + lane) : early;
-    few::survey<NT * 8>(extra.few, own_kept, threadIdx.x, kThreads, &sum, &least);
+    few::survey<few::Cutting<NT * 8>>(extra.few, own_kept, threadIdx.x, kThreads, &sum, &least);
     if (lane == 0) {
       S.own_total[warp] = sum;
       S.own_least[warp] = least;

@@ -18,7 +18,7 @@ namespace {
 struct Slices {
   int shared, own;
   int32_t *pre_pieces, *own_pieces;
-  int pre_blocks, own_blocks, block_rows;  // numbers of a KV head: one for every block_rows rows
+  int pre_keys, own_keys, pre_rows, own_rows;  // at piece_key() of blocks of so many rows (pre_keys = 0: one for [group][KV head])
 };
 
 // A join of many rows (1264 tokens of 32 heads in two slices: 22 us with four rows and two CTAs, 16 so):
@@ -69,11 +69,11 @@ __global__ void __launch_bounds__(256, WARPS == 4 || ROWS > 128 / D ? kResident 
     there[j] = shared ? sl.shared : 0;
     all[j] = live ? sl.own : 0;
     there_at[j] = !shared || !sl.pre_pieces ? nullptr
-                  : sl.pre_pieces + (int64_t(lo) * c.kvh + h) * sl.pre_blocks +
-                        (sl.pre_blocks > 1 ? ((t - g.row0) * c.group + in_head) / sl.block_rows : 0);
+                  : sl.pre_pieces + (sl.pre_keys ? int64_t(h) * sl.pre_keys + piece_key(g.row0, c.group, sl.pre_rows,
+                                                                                         ((t - g.row0) * c.group + in_head) / sl.pre_rows, lo)
+                                                 : int64_t(lo) * c.kvh + h);
     all_at[j] = !live || !sl.own_pieces ? nullptr
-                : sl.own_pieces + (int64_t(b) * c.kvh + h) * sl.own_blocks +
-                      (sl.own_blocks > 1 ? (token * c.group + in_head) / sl.block_rows : 0);
+                : sl.own_pieces + int64_t(h) * sl.own_keys + piece_key(s.row0, c.group, sl.own_rows, (token * c.group + in_head) / sl.own_rows, b);
     m[j] = -INFINITY;
     l[j] = 0.f;
     o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -197,71 +197,66 @@ cudaError_t launch_join(const ChunkArgs& a, const CacheArgs& prefix, const Slice
   return a.c.d == 128 ? join<float, 128>(a, prefix, sl, st) : join<float, 64>(a, prefix, sl, st);
 }
 
-// fp32: slices of as few 64-slot tiles as leave all CTAs of both passes room on the SMs at once: a tile
-// is 7 us (101 rows over 2000 shared slots of eight KV heads, d = 64: 57 us with slices of four tiles in
-// two launches).
-int simt_fit(const mp_cache_config* c) { return (c->head_dim == 64 ? 3 : 2) * device_sm_count(); }
-int64_t simt_ctas(const mp_cache_config* c, int max_q, int slices) {
-  const int64_t group = c->q_heads / c->kv_heads;
-  return (max_q * group + kChunkRows - 1) / kChunkRows * c->kv_heads * c->batch * slices;
-}
-int simt_slices(int max_kv, int tiles) { return std::min(64, (max_kv + 64 * tiles - 1) / (64 * tiles)); }
-// of one pass alone, which are not fewer
-int simt_slices_most(const mp_cache_config* c, int max_q, int max_kv) {
-  return int(std::max<int64_t>(1, std::min<int64_t>({simt_fit(c) / simt_ctas(c, max_q, 1), (int64_t(max_kv) + 63) / 64, 64})));
-}
-
-// How a pass goes: few rows per KV head through k_prefix_few (fp32: k_prefix_few32), more on the tensor
-// cores (fp32: in tiles on the CUDA cores). kTiles leaves one slice, kSlices as many as prefix_slices() says.
-enum Kind { kFew, kTiles, kSlices, kSimt };
-struct Pass {
-  Kind kind;
-  int slices;  // the most
+// How the passes go, and the rows of a block where they are cut into runs (kFew, kSimt).
+enum Kind {
+  kFew,    // few rows per KV head: launch_prefix_few, fp32 launch_prefix_few32
+  kSimt,   // fp32 with more: launch_prefix_simt
+  kTiles,  // bf16 with more: large tiles, joined to one slice
+  kSlices  // prefixes on large tiles in slices, and the own slots (kFew) beside them
 };
-Kind kind_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool slices) {
-  if (c->dtype != MP_DTYPE_BF16) return int64_t(max_q) * (c->q_heads / c->kv_heads) <= kFewRows32 ? kFew : kSimt;
-  if (prefix_is_few(c, max_q, max_kv)) return kFew;
-  return slices && prefix_in_slices(c, total_q, max_q) ? kSlices : kTiles;
+struct Plan {
+  Kind own, shared;
+  int own_rows, pre_rows;
+};
+int few_rows(int64_t rows, int least) { return rows <= least ? least : (rows <= 2 * least ? 2 * least : 4 * least); }
+
+// bf16: a block of 32 rows takes more registers than a warp has with d = 128, and beside large tiles, whose
+// warps have 208, with d = 64 too. us a call, 32/8 heads, with up to 32 rows in blocks beside slices, and with
+// large tiles for both from 17 rows on:
+//   32 sequences of 32 rows, 300 own slots, 4000 shared, d = 128     129    68       d = 64   47    53
+//   the same over 1500 own slots                                     212    95                74    68
+//   64 sequences of 20 rows, 1500 own slots, 60000 shared            975   333               440   250
+// and up to 16 rows in blocks, with large tiles from 9 on:
+//   32 sequences of 12 rows, 300 own slots, 4000 shared, d = 128      39    58                37    45
+// Where all rows are as few as a block's, both passes take it whatever the lengths (d = 64: up to 32 rows).
+// Own slots in blocks and prefixes on large tiles without slices, or the other way round, are two launches.
+Plan plan_of(const mp_cache_config* c, const mp_cache_config* p, int total_q, int max_q, int max_group_q, int max_prefix) {
+  const int64_t group = c->q_heads / c->kv_heads, own = max_q * group, pre = max_group_q * group, both = std::max(own, pre);
+  if (c->dtype != MP_DTYPE_BF16) {
+    constexpr int kMost = 16;
+    const int rows = few_rows(pre <= kMost ? (own <= kMost ? both : pre) : own, 4);
+    return {own <= kMost ? kFew : kSimt, pre <= kMost ? kFew : kSimt, own <= kMost ? rows : kChunkRows, pre <= kMost ? rows : kChunkRows};
+  }
+  const int most = c->head_dim == 128 ? 16 : 32;
+  if (both <= most) return {kFew, kFew, few_rows(both, 8), few_rows(both, 8)};
+  const int rows = few_rows(own, 8);
+  const bool few = own <= most && prefix_is_few(p, max_group_q, max_prefix, rows);
+  if (few || own <= 16) return {kFew, few ? kFew : (prefix_in_slices(p, total_q, max_group_q) ? kSlices : kTiles), rows, rows};
+  return {kTiles, kTiles, 0, 0};
 }
-Pass pass_of(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool slices) {
-  const Kind kind = kind_of(c, total_q, max_q, max_kv, slices);
-  if (kind == kFew) return {kind, prefix_few_pieces(c, total_q, max_kv)};
-  if (kind == kTiles) return {kind, 1};
-  const int s = kind == kSlices ? prefix_slices(c, max_q, max_kv) : simt_slices_most(c, max_q, max_kv);
+// The most slices of a pass.
+int slices_of(Kind kind, const mp_cache_config* c, int total_q, int max_q, int max_kv) {
+  if (kind == kTiles) return 1;
+  if (kind != kSlices) return prefix_few_pieces(c, total_q, max_kv);
   // as many fewer where most packed rows belong to no sequence
-  return {kind, std::max(1, int(s * part_rows(c, total_q, max_q) / total_q))};
+  return std::max(1, int(prefix_slices(c, max_q, max_kv) * part_rows(c, total_q, max_q) / total_q));
 }
-// The most that pass_of().slices * total_q comes to for limits that are at most these.
+// The most that slices_of() * total_q comes to for limits that are at most these.
 uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int max_kv, bool prefix) {
   const int group = c->q_heads / c->kv_heads;
-  uint64_t most = uint64_t(total_q);
-  if (c->dtype == MP_DTYPE_BF16) {
-    most = std::max(most, uint64_t(prefix_few_rows_most(c, total_q, max_kv)));
-    // large tiles: the slices go by the tiles of a group, one where they are many
-    for (int64_t tiles = 1; prefix; ++tiles) {
-      const int q = int(std::min<int64_t>(max_q, std::max<int64_t>(1, tiles * 256 / group))), s = prefix_slices(c, q, max_kv);
-      most = std::max(most, uint64_t(s) * part_rows(c, total_q, q));
-      if (s == 1 || q == max_q) break;
-    }
-    return most;
-  }
-  if (group <= kFewRows32) most = std::max(most, uint64_t(prefix_few_rows_most(c, total_q, max_kv)));
-  // the slices go by the number of row tiles: the largest max_q of each, until one slice is left
-  for (int64_t rows = (int64_t(group) + kChunkRows - 1) / kChunkRows * kChunkRows;; rows += kChunkRows) {
-    const int q = int(std::min<int64_t>(max_q, rows / group)), s = simt_slices_most(c, q, max_kv);
+  uint64_t most = prefix_few_rows_most(c, total_q, max_kv);
+  // large tiles: the slices go by the tiles of a group, one where they are many
+  for (int64_t tiles = 1; prefix && c->dtype == MP_DTYPE_BF16; ++tiles) {
+    const int q = int(std::min<int64_t>(max_q, std::max<int64_t>(1, tiles * 256 / group))), s = prefix_slices(c, q, max_kv);
     most = std::max(most, uint64_t(s) * part_rows(c, total_q, q));
-    if (s == 1 || q == max_q) return most;
+    if (s == 1 || q == max_q) break;
   }
+  return most;
 }
 uint64_t sums_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * c->head_dim * 4); }
 uint64_t ml_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * 2 * 4); }
-// Blocks of k_prefix_few that numbers of pieces are kept for (one where all of a KV head's rows have the same).
-int blocks_of(const mp_cache_config* c, const Pass& pass, int max_q) { return pass.kind == kFew ? few_blocks(c->q_heads / c->kv_heads, max_q) : 1; }
-uint64_t pieces_bytes(const mp_cache_config* c, int blocks) { return align256(uint64_t(c->batch) * c->kv_heads * blocks * 4); }
-// for limits that are at most these
-uint64_t pieces_bytes_most(const mp_cache_config* c, int max_q) {
-  return pieces_bytes(c, std::min(8, few_blocks(c->q_heads / c->kv_heads, max_q)));
-}
+uint64_t pieces_bytes(const mp_cache_config* c, int total_q, int rows) { return align256(uint64_t(piece_keys(c, total_q, rows)) * c->kv_heads * 4); }
+constexpr int kLeastRows = 4;  // of a block
 
 int check(const mp_cache_config* c, const mp_cache_config* p, int total_q, int max_q, int max_kv, int max_group_q, int max_prefix) {
   int rc = check_cache(c);
@@ -290,7 +285,7 @@ int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_config*
   max_q = std::min(max_q, total_q);
   max_group_q = std::min(max_group_q, total_q);
   const uint64_t rows = slice_rows_most(cfg, total_q, max_q, max_kv, false) + slice_rows_most(prefix_cfg, total_q, max_group_q, max_prefix, true);
-  *bytes = pieces_bytes_most(cfg, max_q) + pieces_bytes_most(prefix_cfg, max_group_q) + sums_bytes(cfg, rows) + ml_bytes(cfg, rows) +
+  *bytes = pieces_bytes(cfg, total_q, kLeastRows) + pieces_bytes(prefix_cfg, total_q, kLeastRows) + sums_bytes(cfg, rows) + ml_bytes(cfg, rows) +
            (cfg->dtype == MP_DTYPE_BF16 ? both_tc_workspace(cfg, max_q, max_kv, prefix_cfg, max_group_q, max_prefix) : 0);
   return MP_OK;
 }
@@ -316,21 +311,12 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     if (!aligned4(p)) return MP_ERR_INVALID_ARG;
   max_q = std::min(max_q, total_q);
   max_group_q = std::min(max_group_q, total_q);
-  Pass own = pass_of(cfg, total_q, max_q, max_kv, false);
-  Pass shared = pass_of(prefix_cfg, total_q, max_group_q, max_prefix, own.kind == kFew);
-  if (own.kind == kSimt && shared.kind == kSimt) {
-    int tiles = 1;
-    while (tiles * 64 < std::max(max_kv, max_prefix) && simt_ctas(cfg, max_q, simt_slices(max_kv, tiles)) +
-               simt_ctas(prefix_cfg, max_group_q, simt_slices(max_prefix, tiles)) > simt_fit(cfg))
-      ++tiles;
-    own.slices = std::min(own.slices, simt_slices(max_kv, tiles));
-    shared.slices = std::min(shared.slices, simt_slices(max_prefix, tiles));
-  }
-  const uint64_t rows = uint64_t(own.slices + shared.slices) * total_q;
-  const int own_blocks = blocks_of(cfg, own, max_q), pre_blocks = blocks_of(prefix_cfg, shared, max_group_q);
-  const uint64_t sums = sums_bytes(cfg, rows), ml = ml_bytes(cfg, rows), own_pieces = pieces_bytes(cfg, own_blocks),
-                 pre_pieces = pieces_bytes(prefix_cfg, pre_blocks);
-  const bool own_tiles = own.kind == kTiles, shared_tiles = shared.kind == kTiles;
+  const Plan plan = plan_of(cfg, prefix_cfg, total_q, max_q, max_group_q, max_prefix);
+  const int own_slices = slices_of(plan.own, cfg, total_q, max_q, max_kv), slices = slices_of(plan.shared, prefix_cfg, total_q, max_group_q, max_prefix);
+  const uint64_t rows = uint64_t(own_slices + slices) * total_q, sums = sums_bytes(cfg, rows), ml = ml_bytes(cfg, rows),
+                 own_pieces = plan.own_rows ? pieces_bytes(cfg, total_q, plan.own_rows) : 0,
+                 pre_pieces = plan.pre_rows ? pieces_bytes(prefix_cfg, total_q, plan.pre_rows) : 0;
+  const bool own_tiles = plan.own == kTiles, shared_tiles = plan.shared == kTiles;
   uint64_t need = own_pieces + pre_pieces + sums + ml;
   if (own_tiles || shared_tiles)
     need += both_tc_workspace(own_tiles ? cfg : nullptr, max_q, max_kv, shared_tiles ? prefix_cfg : nullptr, max_group_q, max_prefix);
@@ -339,11 +325,15 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   if (injected("prefix")) return MP_ERR_INJECTED;
 
   char* ws = static_cast<char*>(workspace);
-  const int most_q = std::max(own.kind == kFew ? max_q : 1, shared.kind == kFew ? max_group_q : 1);
-  const int few_rows = int(std::min<int64_t>(kFewRows, int64_t(most_q) * (cfg->q_heads / cfg->kv_heads)));
-  Slices sl = {shared.slices, own.slices, nullptr, nullptr, pre_blocks, own_blocks, kFewRows};
-  if (own.kind == kFew) sl.own_pieces = reinterpret_cast<int32_t*>(ws);
-  if (shared.kind == kFew || shared.kind == kSlices) sl.pre_pieces = reinterpret_cast<int32_t*>(ws + own_pieces);
+  Slices sl = {slices, own_slices, nullptr, nullptr, 0, 0, plan.pre_rows, plan.own_rows};
+  if (!own_tiles) {
+    sl.own_pieces = reinterpret_cast<int32_t*>(ws);
+    sl.own_keys = int(piece_keys(cfg, total_q, plan.own_rows));
+  }
+  if (!shared_tiles) {
+    sl.pre_pieces = reinterpret_cast<int32_t*>(ws + own_pieces);
+    if (plan.shared != kSlices) sl.pre_keys = int(piece_keys(prefix_cfg, total_q, plan.pre_rows));
+  }
   ws += own_pieces + pre_pieces;
   void* tiles = ws + sums + ml;
   ChunkArgs p, a;
@@ -369,33 +359,33 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   const int64_t slice = int64_t(total_q) * cfg->q_heads;
   p.part = reinterpret_cast<float*>(ws);
   p.ml = reinterpret_cast<float*>(ws + sums);
-  a.part = p.part + shared.slices * slice * cfg->head_dim;
-  a.ml = p.ml + shared.slices * slice * 2;
+  a.part = p.part + slices * slice * cfg->head_dim;
+  a.ml = p.ml + slices * slice * 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  a.splits = own.slices;
-  p.splits = shared.slices;
-  if (own.kind == kSimt || shared.kind == kSimt) {
-    ProfScope ps(st, K_CHUNK_ATTEND);
-    if (launch_prefix_simt(shared.kind == kSimt ? &p : nullptr, own.kind == kSimt ? &a : nullptr, st) != cudaSuccess) return MP_ERR_CUDA;
-  }
-  // few rows: both passes in one launch where both have them
-  if (own.kind == kFew || shared.kind == kFew) {
-    const bool beside = shared.kind == kSlices;
+  a.splits = own_slices;
+  p.splits = slices;
+  // the passes that are cut into runs, both in one launch where both are of a kind
+  for (Kind kind : {kSimt, kFew}) {
+    if (plan.own != kind && plan.shared != kind) continue;
+    const bool beside = kind == kFew && plan.shared == kSlices, bf16 = cfg->dtype == MP_DTYPE_BF16;
     PrefixFew few;
     few.pre = p;
     few.own = a;
-    few.groups = shared.kind == kFew ? prefix_cfg->batch : 0;
-    few.own_units = own.kind == kFew;
-    few.most_shared = shared.slices;
-    few.most_own = own.slices;
-    few.pre_blocks = pre_blocks;
-    few.own_blocks = own_blocks;
+    few.groups = plan.shared == kind ? prefix_cfg->batch : 0;
+    few.own_units = plan.own == kind;
+    few.most_shared = slices;
+    few.most_own = own_slices;
+    few.pre_keys = sl.pre_keys;
+    few.own_keys = sl.own_keys;
     few.pre_pieces = sl.pre_pieces;
     few.own_pieces = sl.own_pieces;
-    ProfScope ps(st, beside ? K_PREFIX_ATTEND : K_PREFIX_FEW);
-    const cudaError_t e = beside ? launch_prefix_slices(p, few, few_rows, st)
-                                 : (cfg->dtype == MP_DTYPE_BF16 ? launch_prefix_few(few, few_rows, st) : launch_prefix_few32(few, few_rows, st));
+    const int block = plan.own == kFew ? plan.own_rows : plan.pre_rows;
+    ProfScope ps(st, beside ? K_PREFIX_ATTEND : (kind == kFew ? K_PREFIX_FEW : K_CHUNK_ATTEND));
+    const cudaError_t e = beside          ? launch_prefix_slices(p, few, block, st)
+                          : kind == kSimt ? launch_prefix_simt(few, st)
+                          : bf16          ? launch_prefix_few(few, block, st)
+                                          : launch_prefix_few32(few, block, st);
     if (e != cudaSuccess) return MP_ERR_CUDA;
   }
   // large tiles: likewise, in equal runs of all of them
@@ -403,7 +393,7 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     ChunkArgs both = a;
     both.state = p.part;
     both.state_ml = p.ml;
-    both.own_slice = shared.slices * slice;
+    both.own_slice = slices * slice;
     ProfScope ps(st, K_PREFIX_ATTEND);
     if (launch_both_tc(both, own_tiles, shared_tiles ? &p : nullptr, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
   }

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_prefix_few(const __grid_
   static_assert(kKept * sizeof(int2) <= sizeof(S.ring));
   int64_t total = 0;
   int least = 0;
-  survey<NT * 8>(a, kept, threadIdx.x, kWarps * 32, &total, &least);
+  survey<Cutting<NT * 8>>(a, kept, threadIdx.x, kWarps * 32, &total, &least);
   if (lane == 0) {
     S.total[warp] = total;
     S.least[warp] = least;
@@ -60,8 +60,10 @@ cudaError_t launch(const Maps& maps, const PrefixFew& a, int ctas, cudaStream_t 
 template <int D>
 cudaError_t launch_rows(const Maps& maps, const PrefixFew& a, int rows, int ctas, cudaStream_t st) {
   if (rows <= 8) return launch<D, 1>(maps, a, ctas, st);
-  if (rows <= 16) return launch<D, 2>(maps, a, ctas, st);
-  return launch<D, 4>(maps, a, ctas, st);
+  if constexpr (D == 64) {
+    if (rows > 16) return launch<D, 4>(maps, a, ctas, st);
+  }
+  return launch<D, 2>(maps, a, ctas, st);
 }
 
 }  // namespace
@@ -87,20 +89,20 @@ cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st) {
   for (int i = 0; i < 2; ++i) {
     const CacheArgs& c = both[i]->c;
     const int units = i ? (a.own_units ? c.batch : 0) : a.groups;
-    steps += int64_t(units) * c.kvh * few_blocks(c.group, c.max_q) * ((c.max_kv + kStep - 1) / kStep + kLead);
+    steps += int64_t(units) * c.kvh * ((int64_t(c.max_q) * c.group + rows - 1) / rows) * ((c.max_kv + kStep - 1) / kStep + kLead);
   }
   const int ctas = int(std::min<int64_t>(kCtas * int64_t(device_sm_count()), steps / (kMinRun * kWarps) + 1));
   return d == 128 ? launch_rows<128>(maps, a, rows, ctas, st) : launch_rows<64>(maps, a, rows, ctas, st);
 }
 
-// Up to 32 rows; with more, K and V are read once for every 32 of them, from L2 then, and a step of them is
-// 1 us of a warp. The large tiles do better, but a kernel of them starts 10 us later. (Groups of 56, 68 and
-// 20 rows over 3001, 777 and 5000 slots of four KV heads, d = 64: 28.8 us a call with large tiles for the
-// prefixes, 20.8 with blocks.)
-bool prefix_is_few(const mp_cache_config* c, int max_q, int max_kv) {
-  const int64_t blocks = few_blocks(c->q_heads / c->kv_heads, max_q);
+// K and V are read once for every `rows` rows, from L2 but for the first, and a step of 32 rows is 1 us of a
+// warp. The large tiles do better, but a kernel of them starts 10 us later. (Groups of 56, 68 and 20 rows
+// over 3001, 777 and 5000 slots of four KV heads, d = 64, own rows up to 24: 28.8 us a call with large tiles
+// for the prefixes, 20.8 with blocks.)
+bool prefix_is_few(const mp_cache_config* c, int max_q, int max_kv, int rows) {
+  const int64_t all = int64_t(max_q) * (c->q_heads / c->kv_heads), blocks = (all + rows - 1) / rows;
   const int64_t steps = int64_t(c->batch) * c->kv_heads * ((max_kv + kStep - 1) / kStep);
-  return blocks <= 1 || (blocks <= 8 && steps * blocks <= 16384);
+  return all <= 256 && steps * blocks <= 16384;
 }
 
 // The most pieces that a unit is cut into: as many warps as there are for it, 32 at least, so that one long

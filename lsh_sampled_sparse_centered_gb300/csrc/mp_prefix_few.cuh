@@ -1,6 +1,6 @@
 // Attention with shared prefixes, with few query rows per KV head (tokens x heads of the group): the own
-// slots of sequences, and the prefixes of groups with up to 32 rows, or with more over short prefixes, 32
-// of them at a time. bf16, bound by one pass over K and V.
+// slots of sequences with up to 16 rows (d = 64: 32), and the prefixes of groups with as few, or with more
+// over short prefixes, as many of them at a time. bf16, bound by one pass over K and V.
 //
 // Many sequences with a few hundred slots each are many short streams, and what a stream costs besides
 // its bytes (lengths, pages, Q, the sums' way out) is as much as they are. So every warp works for itself,
@@ -25,6 +25,11 @@ constexpr int kStep = 16;     // slots
 constexpr int kLead = 3;      // steps that starting and ending a unit counts as
 constexpr int kMinRun = 4;    // steps of a warp at least
 constexpr int kKept = 8192;   // units' lengths that the planning keeps
+// How work is cut: blocks of so many query rows, and the four above.
+template <int ROWS, int STEP = kStep, int LEAD = kLead, int MIN_RUN = kMinRun, int KEPT = kKept>
+struct Cutting {
+  static constexpr int kRows = ROWS, kStep = STEP, kLead = LEAD, kMinRun = MIN_RUN, kKept = KEPT;
+};
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRaise = 8.0f;
 
@@ -55,35 +60,37 @@ bool few_maps(const PrefixFew& a, Maps* maps);  // false when the driver refuses
 __device__ __forceinline__ Seq unit_of(const PrefixFew& a, int v) {
   return v < a.groups ? group_of(a.pre.c, v) : seq_of(a.own.c, v - a.groups);
 }
-__device__ __forceinline__ int32_t& pieces_at(const PrefixFew& a, int v, int h, int block) {
-  const int kvh = a.own.c.kvh;
-  return v < a.groups ? a.pre_pieces[(int64_t(v) * kvh + h) * a.pre_blocks + block]
-                      : a.own_pieces[(int64_t(v - a.groups) * kvh + h) * a.own_blocks + block];
+template <typename C>
+__device__ __forceinline__ int32_t& pieces_at(const PrefixFew& a, int v, const Seq& s, int h, int block) {
+  const bool own = v >= a.groups;
+  const int key = piece_key(s.row0, a.own.c.group, C::kRows, block, own ? v - a.groups : v);
+  return own ? a.own_pieces[int64_t(h) * a.own_keys + key] : a.pre_pieces[int64_t(h) * a.pre_keys + key];
 }
-__device__ __forceinline__ int steps_in(const Seq& s) { return s.m > 0 ? (s.n + kStep - 1) / kStep : 0; }
-template <int ROWS>
-__device__ __forceinline__ int blocks_in(const Seq& s, int group) { return (s.m * group + ROWS - 1) / ROWS; }
+template <typename C>
+__device__ __forceinline__ int steps_in(const Seq& s) { return s.m > 0 ? (s.n + C::kStep - 1) / C::kStep : 0; }
+template <typename C>
+__device__ __forceinline__ int blocks_in(const Seq& s, int group) { return (s.m * group + C::kRows - 1) / C::kRows; }
 
 // Lengths and blocks of the units of this thread, of `threads`: their steps, summed and with kLead each (of
 // one KV head), and the least steps of a run for which no unit is cut into more pieces than it may. Units
 // without a slot have no piece.
-template <int ROWS, int KEPT = kKept>
+template <typename C>
 __device__ __forceinline__ void survey(const PrefixFew& a, int2* kept, int thread, int threads, int64_t* sum, int* at_least) {
   const CacheArgs& co = a.own.c;
   const int kvh = co.kvh, group = co.group;
   const int units = a.groups + (a.own_units ? co.batch : 0);
   int64_t total = 0;
-  int64_t least = kMinRun;  // as long as a unit's steps by one less than its most pieces
+  int64_t least = C::kMinRun;  // as long as a unit's steps by one less than its most pieces
   for (int v = thread; v < units; v += threads) {
     const Seq s = unit_of(a, v);
-    const int n = steps_in(s), blocks = blocks_in<ROWS>(s, group);
-    if (v < KEPT) kept[v] = make_int2(n, blocks);
-    total += n ? int64_t(n + kLead) * blocks : 0;
+    const int n = steps_in<C>(s), blocks = blocks_in<C>(s, group);
+    if (v < C::kKept) kept[v] = make_int2(n, blocks);
+    total += n ? int64_t(n + C::kLead) * blocks : 0;
     const int most = v < a.groups ? a.most_shared : a.most_own;
     least = max(least, int64_t((n + most - 2) / (most - 1)));
     if (n == 0 && v % gridDim.x == blockIdx.x)
       for (int h = 0; h < kvh; ++h)
-        for (int i = 0; i < blocks; ++i) pieces_at(a, v, h, i) = 0;
+        for (int i = 0; i < blocks; ++i) pieces_at<C>(a, v, s, h, i) = 0;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -91,9 +98,10 @@ __device__ __forceinline__ void survey(const PrefixFew& a, int2* kept, int threa
   *at_least = __reduce_max_sync(0xffffffffu, int(least));
 }
 
-// A warp's run, `worker` of `workers`, of `total` steps in all: its pieces in order. All lanes hold the same.
-template <int ROWS, int KEPT = kKept>
+// A worker's run, `worker` of `workers`, of `total` steps in all: its pieces in order. All lanes hold the same.
+template <typename C>
 struct Walk {
+  static constexpr int kLead = C::kLead;
   const PrefixFew& a;
   int64_t run, r0, r1, at = 0;  // at: the first step of the unit (kLead of them before its slots) among all
   int units, v = 0, i = 0, steps = 0, blocks = 1;  // i: KV head and block of rows, the blocks next to each other
@@ -113,11 +121,11 @@ struct Walk {
     for (int v0 = 0; v0 < units; v0 += 32) {
       int2 k = make_int2(0, 1);
       if (v0 + lane < units) {
-        if (v0 + lane < KEPT) {
+        if (v0 + lane < C::kKept) {
           k = kept[v0 + lane];
         } else {
           const Seq u = unit_of(a, v0 + lane);
-          k = make_int2(steps_in(u), blocks_in<ROWS>(u, group));
+          k = make_int2(steps_in<C>(u), blocks_in<C>(u, group));
         }
       }
       const int64_t mine = k.x ? int64_t(k.x + kLead) * kvh * k.y : 0;
@@ -149,8 +157,8 @@ struct Walk {
     steps = 0;
     while (at < r1 && ++v < units) {
       s = unit_of(a, v);
-      steps = steps_in(s);
-      blocks = blocks_in<ROWS>(s, a.own.c.group);
+      steps = steps_in<C>(s);
+      blocks = blocks_in<C>(s, a.own.c.group);
       if (steps) break;
     }
     if (steps == 0) at = r1;
@@ -167,7 +175,7 @@ struct Walk {
       p->own = v >= a.groups;
       p->b = v >= a.groups ? v - a.groups : v;
       p->row0 = s.row0;
-      p->r0 = block * ROWS;
+      p->r0 = block * C::kRows;
       p->rows = s.m * a.own.c.group;
       p->first = s.first;
       p->n = s.n;
@@ -175,7 +183,7 @@ struct Walk {
       p->u0 = u0;
       p->u1 = u1;
       p->slice = int(quotient(r0, run) - first);
-      if (u0 == 0 && (threadIdx.x & 31) == 0) pieces_at(a, v, h, block) = int(quotient(lead + steps - 1, run) - first) + 1;
+      if (u0 == 0 && (threadIdx.x & 31) == 0) pieces_at<C>(a, v, s, h, block) = int(quotient(lead + steps - 1, run) - first) + 1;
       return true;
     }
     return false;
@@ -194,7 +202,7 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const CacheArgs& co = a.own.c;
   const int kvh = co.kvh, group = co.group, qh = kvh * group;
-  Walk<NT * 8> walk(a, kept, total, least, worker, workers);
+  Walk<Cutting<NT * 8>> walk(a, kept, total, least, worker, workers);
   found();
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&S.full[i], 1);

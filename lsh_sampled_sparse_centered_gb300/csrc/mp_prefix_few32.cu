@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(kWarps * 32, resident(R)) k_prefix_few32(const
   constexpr int L = D / 4, HALVES = 32 / L;  // lanes of a row of K; rows of a load
   constexpr int SL = L / R;                  // slots of a round of each half
   constexpr int SR = SL * HALVES, kRounds = kStep / SR;
-  __shared__ int2 kept[kKept / 4];
+  using Cut = Cutting<R, kStep, kLead, kMinRun, 2048>;
+  __shared__ int2 kept[Cut::kKept];
   __shared__ int64_t totals[kWarps];
   __shared__ int leasts[kWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident(R)) k_prefix_few32(const
   const int group = co.group, qh = co.kvh * group;
   int64_t total = 0;
   int least = 0;
-  survey<R, kKept / 4>(a, kept, threadIdx.x, kWarps * 32, &total, &least);
+  survey<Cut>(a, kept, threadIdx.x, kWarps * 32, &total, &least);
   if (lane == 0) {
     totals[warp] = total;
     leasts[warp] = least;
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident(R)) k_prefix_few32(const
     total += totals[i] * co.kvh;
     least = max(least, leasts[i]);
   }
-  Walk<R, kKept / 4> walk(a, kept, total, least, int64_t(blockIdx.x) * kWarps + warp, int64_t(gridDim.x) * kWarps);
+  Walk<Cut> walk(a, kept, total, least, int64_t(blockIdx.x) * kWarps + warp, int64_t(gridDim.x) * kWarps);
   const float scale = kLog2e * rsqrtf(float(D));
   Piece p = {};
   for (; walk.open(&p); walk.advance()) {

@@ -11,9 +11,8 @@ cudaError_t launch_slices(const ChunkArgs& a, const OwnSide& own, int rows, cuda
   Extra<MODE> x;
   static_cast<OwnSide&>(x) = own;
   const int ctas = device_sm_count();
-  if (rows <= 8) return launch<D, MODE, 1>(a, x, a.c.batch, ctas, kRows, nullptr, st);
-  if (rows <= 16) return launch<D, MODE, 2>(a, x, a.c.batch, ctas, kRows, nullptr, st);
-  return launch<D, MODE, 4>(a, x, a.c.batch, ctas, kRows, nullptr, st);
+  return rows <= 8 ? launch<D, MODE, 1>(a, x, a.c.batch, ctas, kRows, nullptr, st)
+                   : launch<D, MODE, 2>(a, x, a.c.batch, ctas, kRows, nullptr, st);
 }
 template <int D>
 cudaError_t launch_slices_of(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st) {
