@@ -24,6 +24,9 @@ struct Slices {
 // A join of many rows (1264 tokens of 32 heads in two slices: 22 us with four rows and two CTAs, 16 so):
 constexpr int kRowsALane = 2;
 constexpr int kResident = 4;  // CTAs of an SM
+// and CTAs that fit go this many times into the grid: each looks up its sequence once for several rows (six chunks
+// of 33 to 517 tokens, the whole call with 1, 2 and 4: 280, 272 and 274 us; a CTA for every 16 rows: 278).
+constexpr int kRounds = 2;
 // One of few rows: several warps a row, with four slices each in flight.
 constexpr int kFewAtOnce = 4;
 
@@ -52,119 +55,122 @@ __global__ void __launch_bounds__(256, WARPS == 4 || ROWS > 128 / D ? kResident 
     else hi = mid;
   }
   const Seq g = group_of(prefix, lo);
-  // all rows together are 32-bit
-  const int first = int(blockIdx.x * (8 / WARPS) + warp / WARPS) * ROWS, mine = s.m * qh;
-  float m[kTurns], l[kTurns];
-  float4 o[kTurns];
-  int64_t row[kTurns];
-  int there[kTurns], all[kTurns];  // slices of the row's prefix, and with those of its own slots
-  const int32_t *there_at[kTurns], *all_at[kTurns];  // or where their numbers are
-#pragma unroll
-  for (int j = 0; j < kTurns; ++j) {
-    const int i = first + j * (32 / kLanes) + sub;
-    const bool live = i < mine;
-    row[j] = live ? int64_t(s.row0) * qh + i : -1;
-    const int token = i / qh, in = i - token * qh, h = in / c.group, in_head = in - h * c.group, t = s.row0 + token;
-    const bool shared = live && g.row0 <= t && t < g.row0 + g.m;
-    there[j] = shared ? sl.shared : 0;
-    all[j] = live ? sl.own : 0;
-    there_at[j] = !shared || !sl.pre_pieces ? nullptr
-                  : sl.pre_pieces + (sl.pre_keys ? int64_t(h) * sl.pre_keys + piece_key(g.row0, c.group, sl.pre_rows,
-                                                                                         ((t - g.row0) * c.group + in_head) / sl.pre_rows, lo)
-                                                 : int64_t(lo) * c.kvh + h);
-    all_at[j] = !live || !sl.own_pieces ? nullptr
-                : sl.own_pieces + int64_t(h) * sl.own_keys + piece_key(s.row0, c.group, sl.own_rows, (token * c.group + in_head) / sl.own_rows, b);
-    m[j] = -INFINITY;
-    l[j] = 0.f;
-    o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (WARPS == 1 && first >= mine) return;
-  int most = 0;
-#pragma unroll
-  for (int j = 0; j < kTurns; ++j) {
-    if (there_at[j]) there[j] = min(there[j], *there_at[j]);
-    if (all_at[j]) all[j] = min(all[j], *all_at[j]);
-    all[j] += there[j];
-    most = max(most, all[j]);
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  for (int i0 = warp % WARPS * kAtOnce; i0 < most; i0 += WARPS * kAtOnce) {
-    float2 v[kTurns][kAtOnce];
-    float4 x[kTurns][kAtOnce];
+  const int mine = s.m * qh, step = int(gridDim.x) * (8 / WARPS) * ROWS;  // all rows together are 32-bit
+  int first = int(blockIdx.x * (8 / WARPS) + warp / WARPS) * ROWS;
+  do {
+    float m[kTurns], l[kTurns];
+    float4 o[kTurns];
+    int64_t row[kTurns];
+    int there[kTurns], all[kTurns];  // slices of the row's prefix, and with those of its own slots
+    const int32_t *there_at[kTurns], *all_at[kTurns];  // or where their numbers are
 #pragma unroll
     for (int j = 0; j < kTurns; ++j) {
+      const int i = first + j * (32 / kLanes) + sub;
+      const bool live = i < mine;
+      row[j] = live ? int64_t(s.row0) * qh + i : -1;
+      const int token = i / qh, in = i - token * qh, h = in / c.group, in_head = in - h * c.group, t = s.row0 + token;
+      const bool shared = live && g.row0 <= t && t < g.row0 + g.m;
+      there[j] = shared ? sl.shared : 0;
+      all[j] = live ? sl.own : 0;
+      there_at[j] = !shared || !sl.pre_pieces ? nullptr
+                    : sl.pre_pieces + (sl.pre_keys ? int64_t(h) * sl.pre_keys + piece_key(g.row0, c.group, sl.pre_rows,
+                                                                                           ((t - g.row0) * c.group + in_head) / sl.pre_rows, lo)
+                                                   : int64_t(lo) * c.kvh + h);
+      all_at[j] = !live || !sl.own_pieces ? nullptr
+                  : sl.own_pieces + int64_t(h) * sl.own_keys + piece_key(s.row0, c.group, sl.own_rows, (token * c.group + in_head) / sl.own_rows, b);
+      m[j] = -INFINITY;
+      l[j] = 0.f;
+      o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (WARPS == 1 && first >= mine) return;
+    int most = 0;
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int i = i0 + k;
-        const bool live = i < all[j];
-        const int64_t at = live ? (i < there[j] ? i : i - there[j] + sl.shared) * rows + row[j] : 0;
-        v[j][k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
-        x[j][k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < kTurns; ++j) {
+      if (there_at[j]) there[j] = min(there[j], *there_at[j]);
+      if (all_at[j]) all[j] = min(all[j], *all_at[j]);
+      all[j] += there[j];
+      most = max(most, all[j]);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    for (int i0 = warp % WARPS * kAtOnce; i0 < most; i0 += WARPS * kAtOnce) {
+      float2 v[kTurns][kAtOnce];
+      float4 x[kTurns][kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kTurns; ++j) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int i = i0 + k;
+          const bool live = i < all[j];
+          const int64_t at = live ? (i < there[j] ? i : i - there[j] + sl.shared) * rows + row[j] : 0;
+          v[j][k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
+          x[j][k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kTurns; ++j) {
+        float top = m[j];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, v[j][k].x);
+        const float ref = top == -INFINITY ? 0.f : top, before = exp2f(m[j] - ref);  // 0 while nothing was seen
+        m[j] = top;
+        l[j] *= before;
+        o[j].x *= before;
+        o[j].y *= before;
+        o[j].z *= before;
+        o[j].w *= before;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const bool any = v[j][k].y != 0.f;  // a slice that saw nothing has written no sum
+          const float by = any ? exp2f(v[j][k].x - ref) : 0.f;
+          l[j] = fmaf(v[j][k].y, by, l[j]);
+          o[j].x = any ? fmaf(x[j][k].x, by, o[j].x) : o[j].x;
+          o[j].y = any ? fmaf(x[j][k].y, by, o[j].y) : o[j].y;
+          o[j].z = any ? fmaf(x[j][k].z, by, o[j].z) : o[j].z;
+          o[j].w = any ? fmaf(x[j][k].w, by, o[j].w) : o[j].w;
+        }
+      }
+    }
+    if (WARPS > 1) {  // the warps' parts, in their order
+      so[warp][lane] = o[0];
+      sml[warp][lane] = make_float2(m[0], l[0]);
+      __syncthreads();
+      if (warp % WARPS != 0) return;
+      float2 v[WARPS];
+      float4 x[WARPS];
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        v[w] = sml[warp + w][lane];
+        x[w] = so[warp + w][lane];
+        top = fmaxf(top, v[w].x);
+      }
+      const float ref = top == -INFINITY ? 0.f : top;
+      m[0] = top;
+      l[0] = 0.f;
+      o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float by = v[w].y == 0.f ? 0.f : exp2f(v[w].x - ref);
+        l[0] = fmaf(v[w].y, by, l[0]);
+        o[0].x = fmaf(x[w].x, by, o[0].x);
+        o[0].y = fmaf(x[w].y, by, o[0].y);
+        o[0].z = fmaf(x[w].z, by, o[0].z);
+        o[0].w = fmaf(x[w].w, by, o[0].w);
       }
     }
 #pragma unroll
     for (int j = 0; j < kTurns; ++j) {
-      float top = m[j];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, v[j][k].x);
-      const float ref = top == -INFINITY ? 0.f : top, before = exp2f(m[j] - ref);  // 0 while nothing was seen
-      m[j] = top;
-      l[j] *= before;
-      o[j].x *= before;
-      o[j].y *= before;
-      o[j].z *= before;
-      o[j].w *= before;
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const bool any = v[j][k].y != 0.f;  // a slice that saw nothing has written no sum
-        const float by = any ? exp2f(v[j][k].x - ref) : 0.f;
-        l[j] = fmaf(v[j][k].y, by, l[j]);
-        o[j].x = any ? fmaf(x[j][k].x, by, o[j].x) : o[j].x;
-        o[j].y = any ? fmaf(x[j][k].y, by, o[j].y) : o[j].y;
-        o[j].z = any ? fmaf(x[j][k].z, by, o[j].z) : o[j].z;
-        o[j].w = any ? fmaf(x[j][k].w, by, o[j].w) : o[j].w;
-      }
+      if (row[j] < 0) continue;
+      const float inv = l[j] == 0.f ? 0.f : 1.0f / l[j];
+      if (a.lse && e == 0) a.lse[row[j]] = l[j] == 0.f ? -INFINITY : m[j] * 0.6931471805599453f + logf(l[j]);
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row[j] * D + e) = make_uint2(bf2(o[j].x * inv, o[j].y * inv), bf2(o[j].z * inv, o[j].w * inv));
+      else
+        *reinterpret_cast<float4*>(static_cast<T*>(a.out) + row[j] * D + e) = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
     }
-  }
-  if (WARPS > 1) {  // the warps' parts, in their order
-    so[warp][lane] = o[0];
-    sml[warp][lane] = make_float2(m[0], l[0]);
-    __syncthreads();
-    if (warp % WARPS != 0) return;
-    float2 v[WARPS];
-    float4 x[WARPS];
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      v[w] = sml[warp + w][lane];
-      x[w] = so[warp + w][lane];
-      top = fmaxf(top, v[w].x);
-    }
-    const float ref = top == -INFINITY ? 0.f : top;
-    m[0] = top;
-    l[0] = 0.f;
-    o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float by = v[w].y == 0.f ? 0.f : exp2f(v[w].x - ref);
-      l[0] = fmaf(v[w].y, by, l[0]);
-      o[0].x = fmaf(x[w].x, by, o[0].x);
-      o[0].y = fmaf(x[w].y, by, o[0].y);
-      o[0].z = fmaf(x[w].z, by, o[0].z);
-      o[0].w = fmaf(x[w].w, by, o[0].w);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kTurns; ++j) {
-    if (row[j] < 0) continue;
-    const float inv = l[j] == 0.f ? 0.f : 1.0f / l[j];
-    if (a.lse && e == 0) a.lse[row[j]] = l[j] == 0.f ? -INFINITY : m[j] * 0.6931471805599453f + logf(l[j]);
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row[j] * D + e) = make_uint2(bf2(o[j].x * inv, o[j].y * inv), bf2(o[j].z * inv, o[j].w * inv));
-    else
-      *reinterpret_cast<float4*>(static_cast<T*>(a.out) + row[j] * D + e) = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
-  }
+    first += step;
+  } while (WARPS == 1 && first < mine);
 }
 
 template <typename T, int D>
@@ -177,7 +183,9 @@ cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, 
   const bool many = all >= sms * 16 * kRowsALane, few = all <= sms * 8, least = all <= sms * 2;
   const int rows = each * (many ? 8 * kRowsALane : (least ? 1 : (few ? 2 : 8)));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((int64_t(a.c.max_q) * qh + rows - 1) / rows), a.c.batch);
+  // many rows: as many CTAs as fit, which take several rows one after the other
+  const int64_t most = (int64_t(a.c.max_q) * qh + rows - 1) / rows;
+  cfg.gridDim = dim3(unsigned(many ? std::min(most, std::max<int64_t>(1, kRounds * kResident * sms / a.c.batch)) : most), a.c.batch);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
