@@ -78,8 +78,8 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // Products run as packed pairs, over pairs of d for S and of rows for O. V arrives under S and
 // the softmax, the next K under the product with V.
 // The tile: rows [r0, r0 + 64) of those of `s` (sequence b, or a group where c.cu_group is set), over the
-// slots [k0, k1) that any of them sees; `split` is the slice for its sums.
-template <int D>
+// slots [k0, k1) that any of them sees; `split` is the slice for its sums, where there are slices.
+template <int D, bool SLICES>
 __device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b, const int h, const Seq& s, const int r0, const int k0, const int k1,
                                                 const int split) {
   constexpr bool kPad = D == 64;
@@ -92,6 +92,7 @@ __device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b,
   float* pt = vs + kBN * kRow;   // [64 keys][kPt]
   const CacheArgs& c = a.c;
   const int rows = s.m * c.group, qh = c.kvh * c.group, first = s.first;  // first: slot of token 0
+  const bool slices = SLICES || a.splits > 1;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   constexpr int kVec = D / 4, kStep = kThr / kVec;  // vectors of a row, rows that the CTA copies at a time
   const int cr = threadIdx.x / kVec, ce = threadIdx.x % kVec * 4;
@@ -223,12 +224,12 @@ __device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b,
     if (r >= rows) continue;
     const int64_t row = int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group;
     const int64_t at = int64_t(split) * c.total_q * qh + row;
-    const float inv = a.part ? 1.f : (sum > 0.f ? 1.0f / sum : sum);
+    const float inv = slices ? 1.f : (sum > 0.f ? 1.0f / sum : sum);
     if (tx == 0) {
-      if (a.part) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m[i], sum);
+      if (slices) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m[i], sum);
       else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m[i] * kLn2 + logf(sum);
     }
-    float* out = a.part ? a.part + at * D : static_cast<float*>(a.out) + row * D;
+    float* out = slices ? a.part + at * D : static_cast<float*>(a.out) + row * D;
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
       float y[4];
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
   if (r0 >= s.m * a.c.group) return;
   // this split's keys: a run of 64-key tiles of the sequence
   const int tiles = (s.n + kBN - 1) / kBN, per = (tiles + a.splits - 1) / a.splits;
-  chunk_simt_tile<D>(a, blockIdx.z, blockIdx.y, s, r0, min(s.n, split * per * kBN), min(seen_by(s, a.c.group, r0), (split + 1) * per * kBN), split);
+  chunk_simt_tile<D, false>(a, blockIdx.z, blockIdx.y, s, r0, min(s.n, split * per * kBN), min(seen_by(s, a.c.group, r0), (split + 1) * per * kBN), split);
 }
 
 // Groups over their prefixes and sequences over their own slots: the tiles of all, a step for every 64
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_chunk_simt(const Chun
 //   drafts of 1 to 9 tokens of 33 sequences, 6/2 heads, prefixes of 614, 20978 and 47562 slots, d = 64   836   140
 //   of 29 sequences, 12/1 heads, five prefixes of 1 to 14768, d = 128                                   1190   160
 //   of 14 sequences, 28/4 heads, prefixes of 26434 and 11304, d = 64                                     552   408
-// and less where they do not (five chunks, 101 rows over 2000 slots, eight heads: 37 and 43).
+// and less where they do not (five chunks, 101 rows over 2000 slots, eight heads: 37 and 41).
 template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_prefix_simt(const __grid_constant__ PrefixFew a) {
   using Cut = few::Cutting<kBM, kBN, 1, 1, 2048>;
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 3 : 2) k_prefix_simt(const __g
   __syncthreads();  // `kept` lies where the tiles go
   few::Piece p = {};
   for (; walk.open(&p); walk.advance())
-    chunk_simt_tile<D>(p.own ? a.own : a.pre, p.b, p.h, walk.s, p.r0, min(p.n, p.u0 * kBN), min(seen_by(walk.s, a.own.c.group, p.r0), p.u1 * kBN), p.slice);
+    chunk_simt_tile<D, true>(p.own ? a.own : a.pre, p.b, p.h, walk.s, p.r0, min(p.n, p.u0 * kBN), min(seen_by(walk.s, a.own.c.group, p.r0), p.u1 * kBN), p.slice);
 }
 
 // Joins the splits' (m, l, sum) of a query row, in an order that is fixed by their number:
@@ -422,12 +423,12 @@ cudaError_t prefix_simt(const PrefixFew& a, cudaStream_t st) {
   static_assert(2048 * sizeof(int2) <= smem);
   cudaError_t e = cudaFuncSetAttribute(k_prefix_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  int64_t steps = 0;
+  double steps = 0;
   for (const ChunkArgs* x : {&a.pre, &a.own}) {
     const int units = x == &a.pre ? a.groups : (a.own_units ? x->c.batch : 0);
-    steps += int64_t(units) * x->c.kvh * ((int64_t(x->c.max_q) * x->c.group + kBM - 1) / kBM) * ((int64_t(x->c.max_kv) + kBN - 1) / kBN + 1);
+    steps += double(units) * x->c.kvh * ((int64_t(x->c.max_q) * x->c.group + kBM - 1) / kBM) * ((x->c.max_kv + kBN - 1) / kBN + 1);
   }
-  const int ctas = int(std::max<int64_t>(1, std::min<int64_t>((D == 64 ? 3 : 2) * int64_t(device_sm_count()), steps)));
+  const int ctas = int(std::max(1.0, std::min((D == 64 ? 3.0 : 2.0) * device_sm_count(), steps)));
   k_prefix_simt<D><<<ctas, kThr, smem, st>>>(a);
   return cudaGetLastError();
 }

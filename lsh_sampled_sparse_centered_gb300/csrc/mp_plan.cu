@@ -9,7 +9,8 @@
 // a barrier, and so are the rows, which read their pages from the tables.
 //
 // Bound by latency: the sums are formed by every CTA for itself (a few reads a sequence) and rows and
-// pages are shared out to one CTA, or a cluster of eight where there are many.
+// pages are shared out to one CTA, or a cluster of eight where there are many (64 single tokens 5.5 us a call,
+// 1000 sequences with 29000 rows 12.4; an empty launch is 4).
 #include <algorithm>
 
 #include "mp_cache_host.h"

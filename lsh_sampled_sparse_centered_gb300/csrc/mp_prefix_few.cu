@@ -85,13 +85,13 @@ cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st) {
   if (!few_maps(a, &maps)) return cudaErrorInvalidValue;
   const ChunkArgs* both[2] = {&a.pre, &a.own};
   const int d = a.own.c.d;
-  int64_t steps = 0;
+  double steps = 0;
   for (int i = 0; i < 2; ++i) {
     const CacheArgs& c = both[i]->c;
     const int units = i ? (a.own_units ? c.batch : 0) : a.groups;
-    steps += int64_t(units) * c.kvh * ((int64_t(c.max_q) * c.group + rows - 1) / rows) * ((c.max_kv + kStep - 1) / kStep + kLead);
+    steps += double(units) * c.kvh * ((int64_t(c.max_q) * c.group + rows - 1) / rows) * ((c.max_kv + kStep - 1) / kStep + kLead);
   }
-  const int ctas = int(std::min<int64_t>(kCtas * int64_t(device_sm_count()), steps / (kMinRun * kWarps) + 1));
+  const int ctas = int(std::min(double(kCtas) * device_sm_count(), steps / (kMinRun * kWarps) + 1));
   return d == 128 ? launch_rows<128>(maps, a, rows, ctas, st) : launch_rows<64>(maps, a, rows, ctas, st);
 }
 

