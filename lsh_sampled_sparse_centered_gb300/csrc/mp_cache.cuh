@@ -34,8 +34,8 @@ struct ChunkArgs {
   float* part;  // [..][d]: unnormalised sums
   float* ml;    // [..][2]: their reference (log2) and sum
   void* cuts;   // shared tiles (tensor cores)
-  // attention with prefixes, tensor cores: a row's unnormalised sum [total_q][q_heads][d] and its reference
-  // and sum go here in the place of out and lse, those of the own slots own_slice rows further on
+  // attention with prefixes, large tiles: a row's unnormalised sum [total_q][q_heads][d] and its reference
+  // and sum go here where its tile is whole, those of the own slots own_slice rows further on
   float *state = nullptr, *state_ml = nullptr;
   int64_t own_slice = 0;
   // prefixes in slices (tensor cores): `splits` are the most; a group's number goes here, for each KV head
@@ -110,8 +110,14 @@ cudaError_t launch_chunk_step(const ChunkArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st);
 // Groups over their prefixes (pre) and chunks over their own slots (own_units), either of which may be missing.
-cudaError_t launch_both_tc(const ChunkArgs& own, bool own_units, const ChunkArgs* pre, void* workspace, cudaStream_t st);
-uint64_t both_tc_workspace(const mp_cache_config* own, int max_q, int max_kv, const mp_cache_config* pre, int max_group_q, int max_prefix);
+// Whole tiles' sums go to state; of cut ones the pieces' go to part and ml, both_tc_rows() rows at most.
+constexpr int kTileRows = 256;
+struct TilePieces {
+  int pre_keys, own_keys;
+  int2 *pre_pieces, *own_pieces;  // pieces of each tile, and the slot (of as many rows as a tile has at most) of the first
+};
+cudaError_t launch_both_tc(const ChunkArgs& own, bool own_units, const ChunkArgs* pre, const TilePieces& at, cudaStream_t st);
+uint64_t both_tc_rows(const mp_cache_config* own, int max_q, int max_kv, const mp_cache_config* pre, int max_group_q, int max_prefix);
 // Whether a pass over prefixes on the tensor cores goes in slices, and how many (without: one, after a join of its own).
 bool prefix_in_slices(const mp_cache_config* c, int total_q, int max_q);
 int prefix_slices(const mp_cache_config* c, int max_q, int max_kv);

@@ -40,7 +40,7 @@
 namespace mp {
 namespace {
 
-constexpr int kRows = 256;   // query rows of a CTA
+constexpr int kRows = kTileRows;  // query rows of a CTA
 constexpr int kKeys = 128;   // keys of a step
 constexpr int kThreads = 384;  // 12 warps: two of softmax for each lane quarter, TMA, work, two of products
 constexpr float kLog2e = 1.4426950408889634f;
@@ -84,6 +84,9 @@ struct Prefixes {
   CacheArgs c;
   int box, groups;
   int64_t own_slice;  // where the own slots' sums begin, in rows of a.state
+  int first_slot;     // of this launch's cut tiles
+  int pre_keys, own_keys;
+  int2 *pre_pieces, *own_pieces;  // [KV head][keys], at piece_key() of kRows: pieces of a tile, and the slot of the first if it is cut
 };
 
 template <int D>
@@ -133,7 +136,9 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr) {
 // tile, whole tiles, and the start of another.
 // Whole tiles are written out; of a tile that is cut every piece stores its unnormalised
 // sum, and k_chunk_tc_join puts the pieces together. A CTA has two such pieces at most: the
-// one that starts its run (slot 2 cta) and the one that ends it (slot 2 cta + 1).
+// one that starts its run (slot 2 cta) and the one that ends it (slot 2 cta + 1). With prefixes (kBoth) whole
+// tiles are sums too, pieces lie [slot][row][d] and k_prefix_join finds them; the first is in an odd slot and
+// the others in the even ones of the CTAs behind.
 __device__ __forceinline__ int tiles_of(const Seq& s, int group) {
   return int((int64_t(s.m) * group + kRows - 1) / kRows);
 }
@@ -636,18 +641,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.u0 = u0;
             p.u1 = u1;
             const bool whole = u0 == 0 && u1 == steps;
-            const int slot = 2 * int(blockIdx.x) + (i == 0 ? 0 : 1);
+            int slot = 2 * int(blockIdx.x) + (i == 0 ? 0 : 1);
+            if constexpr (BOTH) slot = extra.pre.first_slot + 2 * int(blockIdx.x) + (u0 == 0 ? 1 : 0);
             p.whole = whole;
             p.slot = slot;
             mbar_arrive(&S.piece_full[k]);
-            if (u0 == 0 && !whole) {
+            if (u0 == 0 && (BOTH || !whole)) {
               // this CTA begins the tile; the CTAs of the units up to the tile's last go on with it
-              cut.row = int64_t(s.row0) * qh + h * c.group;
-              if constexpr (BOTH) cut.row += b >= extra.pre.groups ? extra.pre.own_slice : 0;
-              cut.slot = slot;
-              cut.r0 = t * kRows;
-              cut.rows = min(kRows, s.m * c.group - t * kRows);
-              cut.pieces = int(quotient(end - left - at + lead + steps - 1, run)) - int(blockIdx.x) + 1;
+              const int pieces = whole ? 1 : int(quotient(end - left - at + lead + steps - 1, run)) - int(blockIdx.x) + 1;
+              if constexpr (BOTH) {
+                const Prefixes& pre = extra.pre;
+                const bool own = b >= pre.groups;
+                (own ? pre.own_pieces : pre.pre_pieces)[int64_t(h) * (own ? pre.own_keys : pre.pre_keys) +
+                                                       piece_key(s.row0, c.group, kRows, t, own ? b - pre.groups : b)] = make_int2(pieces, slot);
+              } else {
+                cut.row = int64_t(s.row0) * qh + h * c.group;
+                cut.slot = slot;
+                cut.r0 = t * kRows;
+                cut.rows = min(kRows, s.m * c.group - t * kRows);
+                cut.pieces = pieces;
+              }
             }
             ++i;
           }
@@ -666,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tiles = tiles_of(s, c.group);
           } while (tiles == 0);
         }
-        static_cast<Cut*>(a.cuts)[blockIdx.x] = cut;
+        if (!BOTH) static_cast<Cut*>(a.cuts)[blockIdx.x] = cut;
       }
       __syncwarp();
     } else if (warp == 8) {
@@ -1145,11 +1158,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after();
         const float sum = lo2(l0) + hi2(l0) + lo2(l1) + hi2(l1);
-        if (CUT || (BOTH && pc.whole)) {
-          // the sums of this piece: a slice of its rows
-          int64_t slice = int64_t(pc.slot) * c.total_q * qh;
-          if constexpr (BOTH) slice = pc.b < extra.pre.groups ? 0 : extra.pre.own_slice;
-          float *const to_ml = BOTH ? a.state_ml : a.ml, *const to_part = BOTH ? a.state : a.part;
+        if constexpr (CUT || BOTH) {
+          // the sums of this piece: a slice of its rows, or (kBoth, cut) its slot's
+          int64_t place = int64_t(pc.slot) * c.total_q * qh + row;
+          float *to_ml = a.ml, *to_part = a.part;
+          if constexpr (BOTH) {
+            place = int64_t(pc.slot) * slot_rows + (r - pc.r0);
+            if (pc.whole) {
+              place = (pc.b < extra.pre.groups ? 0 : extra.pre.own_slice) + row;
+              to_ml = a.state_ml;
+              to_part = a.state;
+            }
+          }
           const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + 256;
           float by0 = 1.f, by1 = 0.f, top = m, all_sum = sum;
           if (PAIR) {
@@ -1170,7 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             by1 = a1.y == 0.f ? 0.f : exp2f(a1.x - top);
             all_sum = fmaf(a0.y, by0, a1.y * by1);
           }
-          if (r < rows && (!PAIR || half == 0)) *reinterpret_cast<float2*>(to_ml + (slice + row) * 2) = make_float2(top, all_sum);
+          if (r < rows && (!PAIR || half == 0)) *reinterpret_cast<float2*>(to_ml + place * 2) = make_float2(top, all_sum);
           constexpr int kBlocks = PAIR ? D / 64 : D / 32;  // of 32 columns
           const int g0 = PAIR ? half * kBlocks : 0;
           uint32_t mine[kBlocks][32], others[PAIR ? kBlocks : 1][32];
@@ -1215,66 +1235,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int64_t to_row = __shfl_sync(0xffffffffu, row, (lane & ~3) + k);
+              const int64_t to_row = __shfl_sync(0xffffffffu, place, (lane & ~3) + k);
               if (r - (lane & 3) + k < rows) {
-                float4* dst = reinterpret_cast<float4*>(to_part + (slice + to_row) * D + (g0 + g) * 32 + (lane & 3) * 8);
+                float4* dst = reinterpret_cast<float4*>(to_part + to_row * D + (g0 + g) * 32 + (lane & 3) * 8);
                 dst[0] = make_float4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]);
                 dst[1] = make_float4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]);
               }
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.piece_empty[i & 1]);
-          continue;
-        }
-        const float inv = sum > 0.f ? 1.0f / sum : sum;
-        const bool real = r < rows, whole = pc.whole;
-        const int64_t at = int64_t(pc.slot) * slot_rows + (r - pc.r0);
-        if (real) {
-          if (!whole) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m, sum);
-          else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
-        }
-        uint32_t all[D / 32][32];
+        } else {
+          const float inv = sum > 0.f ? 1.0f / sum : sum;
+          const bool real = r < rows, whole = pc.whole;
+          const int64_t at = int64_t(pc.slot) * slot_rows + (r - pc.r0);
+          if (real) {
+            if (!whole) *reinterpret_cast<float2*>(a.ml + at * 2) = make_float2(m, sum);
+            else if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
+          }
+          uint32_t all[D / 32][32];
 #pragma unroll
-        for (int g = 0; g < D / 32; ++g) tmem_ld32(to + g * 32, all[g]);
-        tmem_wait_ld(all[0]);
+          for (int g = 0; g < D / 32; ++g) tmem_ld32(to + g * 32, all[g]);
+          tmem_wait_ld(all[0]);
 #pragma unroll
-        for (int g = 1; g < D / 32; ++g) tmem_tie(all[g]);
+          for (int g = 1; g < D / 32; ++g) tmem_tie(all[g]);
 #pragma unroll
-        for (int g = 0; g < D / 32; ++g) {
-          uint32_t (&o)[32] = all[g];
-          if (!whole) {
-            if (real && sum > 0.f) {
-              float4* dst = reinterpret_cast<float4*>(a.part) +
-                            (int64_t(pc.slot) * (D / 4) + g * 8) * slot_rows + (r - pc.r0);
+          for (int g = 0; g < D / 32; ++g) {
+            uint32_t (&o)[32] = all[g];
+            if (!whole) {
+              if (real && sum > 0.f) {
+                float4* dst = reinterpret_cast<float4*>(a.part) +
+                              (int64_t(pc.slot) * (D / 4) + g * 8) * slot_rows + (r - pc.r0);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i * slot_rows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-            }
-          } else {
-            // Four lanes swap their rows' 16-byte parts, so that each store writes 64 bytes of a row.
-            uint32_t v[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              v[k] = bf2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-#pragma unroll
-            for (int bit = 1; bit <= 2; bit *= 2) {
-              const bool high = lane & bit;
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                if (k & (4 * bit)) continue;
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? v[k] : v[k + 4 * bit], bit);
-                if (high) v[k] = got;
-                else v[k + 4 * bit] = got;
+                for (int i = 0; i < 8; ++i)
+                  dst[i * slot_rows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                   __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
               }
-            }
+            } else {
+              // Four lanes swap their rows' 16-byte parts, so that each store writes 64 bytes of a row.
+              uint32_t v[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int64_t to_row = __shfl_sync(0xffffffffu, row, (lane & ~3) + i);
-              if (r - (lane & 3) + i < rows)
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to_row * D + g * 32 + (lane & 3) * 8) =
-                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              for (int k = 0; k < 16; ++k)
+                v[k] = bf2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+#pragma unroll
+              for (int bit = 1; bit <= 2; bit *= 2) {
+                const bool high = lane & bit;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  if (k & (4 * bit)) continue;
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? v[k] : v[k + 4 * bit], bit);
+                  if (high) v[k] = got;
+                  else v[k + 4 * bit] = got;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int64_t to_row = __shfl_sync(0xffffffffu, row, (lane & ~3) + i);
+                if (r - (lane & 3) + i < rows)
+                  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to_row * D + g * 32 + (lane & 3) * 8) =
+                      make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              }
             }
           }
         }
@@ -1301,8 +1319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows, a lane each, and 8 columns. Partial sums lie [slot][column / 4][row][4], so that
 // the threads that own rows (in the kernel above and here) write and read whole lines. Set up
 // while k_chunk_tc still runs; it waits for it first.
-// STATE: to a.state and a.state_ml, unnormalised.
-template <int D, bool STATE>
+template <int D>
 __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const int slot_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
@@ -1361,13 +1378,6 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
   }
   const int group = a.c.group, r = cut.r0 + i;
   const int64_t row = cut.row + int64_t(r / group) * (a.c.kvh * group) + r % group;
-  if (STATE) {
-    if (columns == 0) *reinterpret_cast<float2*>(a.state_ml + row * 2) = make_float2(m, l);
-    float4* out = reinterpret_cast<float4*>(a.state + row * D + columns * 8);
-    out[0] = o[0];
-    out[1] = o[1];
-    return;
-  }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   if (a.lse && columns == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
   uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + columns * 8);
@@ -1379,7 +1389,6 @@ int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int
 
 template <int D, Mode MODE, int NT>
 cudaError_t launch(ChunkArgs a, Extra<MODE> extra, int units, int ctas, int slot_rows, void* workspace, cudaStream_t st) {
-  constexpr bool CUT = MODE == kCuts || MODE == kPairs;
   const CacheArgs& c = a.c;
   CUtensorMap mk, mv;
   const int box = box_rows(c.table, c.page_size);
@@ -1391,7 +1400,7 @@ cudaError_t launch(ChunkArgs a, Extra<MODE> extra, int units, int ctas, int slot
   static_assert(sizeof(Smem<D>) + 1024 <= 227 * 1024);
   cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  if (!CUT) {
+  if (MODE == kChunk) {
     char* ws = static_cast<char*>(workspace);
     a.cuts = ws;
     ws += align256(uint64_t(ctas) * sizeof(Cut));
@@ -1401,7 +1410,9 @@ cudaError_t launch(ChunkArgs a, Extra<MODE> extra, int units, int ctas, int slot
   }
   for (int b = 0; b < units; b += kGroup) {
     k_chunk_tc<D, MODE, NT><<<ctas, kThreads, smem, st>>>(mk, mv, a, box, b, std::min(units, b + kGroup), slot_rows, extra);
-    if constexpr (CUT) {
+    if constexpr (MODE == kBoth) {
+      extra.pre.first_slot += 2 * ctas;
+    } else if constexpr (MODE != kChunk) {
       extra.few.own_units = false;  // the first launch has done them
     } else {
       cudaLaunchConfig_t cfg = {};
@@ -1413,7 +1424,7 @@ cudaError_t launch(ChunkArgs a, Extra<MODE> extra, int units, int ctas, int slot
       at[0].val.programmaticStreamSerializationAllowed = 1;
       cfg.attrs = at;
       cfg.numAttrs = 1;
-      if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D, MODE == kBoth>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
+      if ((e = cudaLaunchKernelEx(&cfg, k_chunk_tc_join<D>, ChunkArgs(a), int(slot_rows))) != cudaSuccess) return e;
     }
   }
   return cudaGetLastError();

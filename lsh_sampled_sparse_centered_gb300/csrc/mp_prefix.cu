@@ -19,173 +19,242 @@ struct Slices {
   int shared, own;
   int32_t *pre_pieces, *own_pieces;
   int pre_keys, own_keys, pre_rows, own_rows;  // at piece_key() of blocks of so many rows (pre_keys = 0: one for [group][KV head])
+  // Large tiles: their pieces instead, two numbers each (TilePieces). A cut tile's are slots of `slot_rows` rows
+  // each, `slots` in all, from row `cut` of the sums on: the first piece's slot s, then s + 1, s + 3, ...
+  bool pre_tiles, own_tiles;
+  int slot_rows, slots;
+  int64_t cut;
 };
 
-// A join of many rows (1264 tokens of 32 heads in two slices: 22 us with four rows and two CTAs, 16 so):
-constexpr int kRowsALane = 2;
-constexpr int kResident = 4;  // CTAs of an SM
-// and CTAs that fit go this many times into the grid: each looks up its sequence once for several rows (six chunks
-// of 33 to 517 tokens, the whole call with 1, 2 and 4: 280, 272 and 274 us; a CTA for every 16 rows: 278).
-constexpr int kRounds = 2;
-// One of few rows: several warps a row, with four slices each in flight.
-constexpr int kFewAtOnce = 4;
+// Where the sums of a query row are: slices [0, there) of the prefix, [there, all) of the own slots.
+// TILES: some passes are large tiles'.
+template <bool TILES>
+struct RowSums {
+  int row;  // among all rows, which are 32-bit together; -1: none
+  int there, all;
+  const int32_t *there_at, *all_at;  // where their numbers are, if they differ
+  int tile[2];                       // the row's place in its tile of the prefix, of the own slots
+  int64_t from[2];                   // the first slice's row of the sums, where its tile is cut
+  bool cut[2];
 
-// Joins the slices' (m, l, sum) of a sequence's query rows, in their order. A warp takes ROWS rows (of
-// D / 4 lanes each, 16 bytes a lane) and has the loads of kAtOnce slices of each in flight; with WARPS > 1
-// as many warps share the slices of their rows, so that all of them are in flight together. The first
-// `shared` slices are of the prefix, the `own` behind them of the own slots; where their numbers are kept
-// per (group or sequence, KV head, block of rows), as many of them are there. Rows without a prefix have
-// none of it.
-// Grid: rows of a sequence x sequences, so that what has to be looked up does not hang on a row.
-template <typename T, int D, int ROWS, int WARPS>
-__global__ void __launch_bounds__(256, WARPS == 4 || ROWS > 128 / D ? kResident : 2) k_prefix_join(const ChunkArgs a, const CacheArgs prefix, const Slices sl) {
-  constexpr int kLanes = D / 4, kTurns = ROWS * kLanes / 32, kAtOnce = WARPS > 1 ? kFewAtOnce : (kTurns == 1 ? 8 : 2);
-  static_assert(WARPS == 1 || kTurns == 1);
-  __shared__ float4 so[WARPS > 1 ? 8 : 1][32];
-  __shared__ float2 sml[WARPS > 1 ? 8 : 1][32];
-  const CacheArgs& c = a.c;
-  const int qh = c.kvh * c.group, b = blockIdx.y;
-  const int64_t rows = int64_t(c.total_q) * qh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kLanes, e = lane % kLanes * 4;
-  const Seq s = seq_of(c, b);
+  // Row i of the `mine` rows of sequence b, `s`, whose group is `g`.
+  __device__ __forceinline__ void place(const CacheArgs& c, const Slices& sl, const Seq& s, int b, const Seq& g, int group, int i, int mine) {
+    const int qh = c.kvh * c.group;
+    const bool live = i < mine;
+    row = live ? s.row0 * qh + i : -1;
+    const int token = i / qh, in = i - token * qh, h = in / c.group, in_head = in - h * c.group, t = s.row0 + token;
+    const bool shared = live && g.row0 <= t && t < g.row0 + g.m;
+    const int at0 = (t - g.row0) * c.group + in_head, at1 = token * c.group + in_head;  // among the group's and the sequence's
+    there = shared ? sl.shared : 0;
+    all = live ? sl.own : 0;
+    there_at = !shared || !sl.pre_pieces ? nullptr
+               : sl.pre_pieces + (sl.pre_keys ? int64_t(h) * sl.pre_keys + piece_key(g.row0, c.group, sl.pre_rows, at0 / sl.pre_rows, group)
+                                              : int64_t(group) * c.kvh + h);
+    all_at = !live || !sl.own_pieces ? nullptr
+             : sl.own_pieces + int64_t(h) * sl.own_keys + piece_key(s.row0, c.group, sl.own_rows, at1 / sl.own_rows, b);
+    if (TILES) {
+      tile[0] = at0 % kTileRows;
+      tile[1] = at1 % kTileRows;
+      // numbers of tiles are twice as long
+      if (there_at && sl.pre_tiles) there_at += there_at - sl.pre_pieces;
+      if (all_at && sl.own_tiles) all_at += all_at - sl.own_pieces;
+    }
+  }
+  // Behind the kernels that wrote the numbers.
+  __device__ __forceinline__ void find(const Slices& sl) {
+    cut[0] = cut[1] = false;
+    auto look = [&](const int32_t* at, bool tiles, int& n, int64_t& begin, bool& is_cut, int in_tile) {
+      if (!at) return;
+      if (!TILES || !tiles) {
+        n = min(n, *at);
+        return;
+      }
+      const int2 v = *reinterpret_cast<const int2*>(at);
+      // (numbers that a kernel whose waits ran out did not write lead nowhere)
+      n = v.x < 0 || v.x > sl.slots || (v.x > 1 && (v.y < 1 || v.y >= sl.slots || v.y + 2 * v.x - 3 >= sl.slots)) ? 0 : v.x;
+      is_cut = n > 1;
+      begin = sl.cut + int64_t(v.y - 1) * sl.slot_rows + in_tile;
+    };
+    look(there_at, sl.pre_tiles, there, from[0], cut[0], tile[0]);
+    look(all_at, sl.own_tiles, all, from[1], cut[1], tile[1]);
+    all += there;
+  }
+  // The row of the sums that slice i is; `rows` are all query rows.
+  __device__ __forceinline__ int64_t at(const Slices& sl, int64_t rows, int i) const {
+    const bool own = i >= there;
+    const int n = own ? i - there : i;
+    if (TILES && (own ? cut[1] : cut[0])) return (own ? from[1] : from[0]) + int64_t(n > 0 ? 2 * n : 1) * sl.slot_rows;
+    return (own ? n + sl.shared : n) * rows + row;
+  }
+};
+
+// The running join of a row: four of its columns.
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&v)[N], const float4 (&x)[N]) {
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < N; ++k) top = fmaxf(top, v[k].x);
+    const float ref = top == -INFINITY ? 0.f : top, before = exp2f(m - ref);  // 0 while nothing was seen
+    m = top;
+    l *= before;
+    o.x *= before;
+    o.y *= before;
+    o.z *= before;
+    o.w *= before;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const bool any = v[k].y != 0.f;  // a slice that saw nothing has written no sum
+      const float by = any ? exp2f(v[k].x - ref) : 0.f;
+      l = fmaf(v[k].y, by, l);
+      o.x = any ? fmaf(x[k].x, by, o.x) : o.x;
+      o.y = any ? fmaf(x[k].y, by, o.y) : o.y;
+      o.z = any ? fmaf(x[k].z, by, o.z) : o.z;
+      o.w = any ? fmaf(x[k].w, by, o.w) : o.w;
+    }
+  }
+  template <typename T, int D>
+  __device__ __forceinline__ void write(const ChunkArgs& a, int64_t row, int e) const {
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    if (a.lse && e == 0) a.lse[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + e) = make_uint2(bf2(o.x * inv, o.y * inv), bf2(o.z * inv, o.w * inv));
+    else
+      *reinterpret_cast<float4*>(static_cast<T*>(a.out) + row * D + e) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+};
+
+// The group that sequence b is in, if it is in one.
+__device__ __forceinline__ int group_at(const CacheArgs& prefix, int b) {
   int lo = 0, hi = prefix.batch;  // cu_group[lo] <= b is kept where it holds for 0
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (prefix.cu_group[mid] <= b) lo = mid;
     else hi = mid;
   }
-  const Seq g = group_of(prefix, lo);
-  const int mine = s.m * qh, step = int(gridDim.x) * (8 / WARPS) * ROWS;  // all rows together are 32-bit
-  int first = int(blockIdx.x * (8 / WARPS) + warp / WARPS) * ROWS;
-  do {
-    float m[kTurns], l[kTurns];
-    float4 o[kTurns];
-    int64_t row[kTurns];
-    int there[kTurns], all[kTurns];  // slices of the row's prefix, and with those of its own slots
-    const int32_t *there_at[kTurns], *all_at[kTurns];  // or where their numbers are
-#pragma unroll
-    for (int j = 0; j < kTurns; ++j) {
-      const int i = first + j * (32 / kLanes) + sub;
-      const bool live = i < mine;
-      row[j] = live ? int64_t(s.row0) * qh + i : -1;
-      const int token = i / qh, in = i - token * qh, h = in / c.group, in_head = in - h * c.group, t = s.row0 + token;
-      const bool shared = live && g.row0 <= t && t < g.row0 + g.m;
-      there[j] = shared ? sl.shared : 0;
-      all[j] = live ? sl.own : 0;
-      there_at[j] = !shared || !sl.pre_pieces ? nullptr
-                    : sl.pre_pieces + (sl.pre_keys ? int64_t(h) * sl.pre_keys + piece_key(g.row0, c.group, sl.pre_rows,
-                                                                                           ((t - g.row0) * c.group + in_head) / sl.pre_rows, lo)
-                                                   : int64_t(lo) * c.kvh + h);
-      all_at[j] = !live || !sl.own_pieces ? nullptr
-                  : sl.own_pieces + int64_t(h) * sl.own_keys + piece_key(s.row0, c.group, sl.own_rows, (token * c.group + in_head) / sl.own_rows, b);
-      m[j] = -INFINITY;
-      l[j] = 0.f;
-      o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (WARPS == 1 && first >= mine) return;
-    int most = 0;
-#pragma unroll
-    for (int j = 0; j < kTurns; ++j) {
-      if (there_at[j]) there[j] = min(there[j], *there_at[j]);
-      if (all_at[j]) all[j] = min(all[j], *all_at[j]);
-      all[j] += there[j];
-      most = max(most, all[j]);
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    for (int i0 = warp % WARPS * kAtOnce; i0 < most; i0 += WARPS * kAtOnce) {
-      float2 v[kTurns][kAtOnce];
-      float4 x[kTurns][kAtOnce];
-#pragma unroll
-      for (int j = 0; j < kTurns; ++j) {
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const int i = i0 + k;
-          const bool live = i < all[j];
-          const int64_t at = live ? (i < there[j] ? i : i - there[j] + sl.shared) * rows + row[j] : 0;
-          v[j][k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
-          x[j][k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kTurns; ++j) {
-        float top = m[j];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, v[j][k].x);
-        const float ref = top == -INFINITY ? 0.f : top, before = exp2f(m[j] - ref);  // 0 while nothing was seen
-        m[j] = top;
-        l[j] *= before;
-        o[j].x *= before;
-        o[j].y *= before;
-        o[j].z *= before;
-        o[j].w *= before;
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const bool any = v[j][k].y != 0.f;  // a slice that saw nothing has written no sum
-          const float by = any ? exp2f(v[j][k].x - ref) : 0.f;
-          l[j] = fmaf(v[j][k].y, by, l[j]);
-          o[j].x = any ? fmaf(x[j][k].x, by, o[j].x) : o[j].x;
-          o[j].y = any ? fmaf(x[j][k].y, by, o[j].y) : o[j].y;
-          o[j].z = any ? fmaf(x[j][k].z, by, o[j].z) : o[j].z;
-          o[j].w = any ? fmaf(x[j][k].w, by, o[j].w) : o[j].w;
-        }
-      }
-    }
-    if (WARPS > 1) {  // the warps' parts, in their order
-      so[warp][lane] = o[0];
-      sml[warp][lane] = make_float2(m[0], l[0]);
-      __syncthreads();
-      if (warp % WARPS != 0) return;
-      float2 v[WARPS];
-      float4 x[WARPS];
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        v[w] = sml[warp + w][lane];
-        x[w] = so[warp + w][lane];
-        top = fmaxf(top, v[w].x);
-      }
-      const float ref = top == -INFINITY ? 0.f : top;
-      m[0] = top;
-      l[0] = 0.f;
-      o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float by = v[w].y == 0.f ? 0.f : exp2f(v[w].x - ref);
-        l[0] = fmaf(v[w].y, by, l[0]);
-        o[0].x = fmaf(x[w].x, by, o[0].x);
-        o[0].y = fmaf(x[w].y, by, o[0].y);
-        o[0].z = fmaf(x[w].z, by, o[0].z);
-        o[0].w = fmaf(x[w].w, by, o[0].w);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kTurns; ++j) {
-      if (row[j] < 0) continue;
-      const float inv = l[j] == 0.f ? 0.f : 1.0f / l[j];
-      if (a.lse && e == 0) a.lse[row[j]] = l[j] == 0.f ? -INFINITY : m[j] * 0.6931471805599453f + logf(l[j]);
-      if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row[j] * D + e) = make_uint2(bf2(o[j].x * inv, o[j].y * inv), bf2(o[j].z * inv, o[j].w * inv));
-      else
-        *reinterpret_cast<float4*>(static_cast<T*>(a.out) + row[j] * D + e) = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
-    }
-    first += step;
-  } while (WARPS == 1 && first < mine);
+  return lo;
 }
 
-template <typename T, int D>
+// Joins the slices' (m, l, sum) of a sequence's query rows, in their order, where they are few: WARPS warps share
+// the slices of 128 / D rows (D / 4 lanes a row, 16 bytes a lane), so that all their loads are in flight together.
+// Grid: rows of a sequence x sequences, so that what has to be looked up does not hang on a row.
+template <typename T, int D, int WARPS, bool TILES>
+__global__ void __launch_bounds__(256, 4) k_prefix_join(const ChunkArgs a, const CacheArgs prefix, const Slices sl) {
+  constexpr int kLanes = D / 4, kAtOnce = 4;
+  __shared__ float4 so[8][32];
+  __shared__ float2 sml[8][32];
+  const CacheArgs& c = a.c;
+  const int qh = c.kvh * c.group, b = blockIdx.y;
+  const int64_t rows = int64_t(c.total_q) * qh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = lane % kLanes * 4;
+  const Seq s = seq_of(c, b);
+  const int group = group_at(prefix, b);
+  const Seq g = group_of(prefix, group);
+  RowSums<TILES> r;
+  r.place(c, sl, s, b, g, group, int(blockIdx.x * (8 / WARPS) + warp / WARPS) * (32 / kLanes) + lane / kLanes, s.m * qh);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  r.find(sl);
+  Joined j;
+  const int most = __reduce_max_sync(0xffffffffu, r.all);
+  for (int i0 = warp % WARPS * kAtOnce; i0 < most; i0 += WARPS * kAtOnce) {
+    float2 v[kAtOnce];
+    float4 x[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const bool live = i0 + k < r.all;
+      const int64_t at = live ? r.at(sl, rows, i0 + k) : 0;
+      v[k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
+      x[k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    j.add(v, x);
+  }
+  // the warps' parts, in their order
+  so[warp][lane] = j.o;
+  sml[warp][lane] = make_float2(j.m, j.l);
+  __syncthreads();
+  if (warp % WARPS != 0 || r.row < 0) return;
+  float2 v[WARPS];
+  float4 x[WARPS];
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    v[w] = sml[warp + w][lane];
+    x[w] = so[warp + w][lane];
+  }
+  Joined all;
+  all.add(v, x);
+  all.template write<T, D>(a, r.row, e);
+}
+
+// The same where they are many: a warp looks up `each` rows at once, one a lane (what a row has to look up is
+// more instructions than its join: 1264 tokens of 32 heads 37 and 31 us), and then joins them one after the other.
+template <typename T, int D, bool TILES>
+__global__ void __launch_bounds__(256, 4) k_prefix_join_many(const ChunkArgs a, const CacheArgs prefix, const Slices sl, const int each) {
+  constexpr int kLanes = D / 4, kAtOnce = 4, kTogether = 32 / kLanes;
+  const CacheArgs& c = a.c;
+  const int qh = c.kvh * c.group, b = blockIdx.y;
+  const int64_t rows = int64_t(c.total_q) * qh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = lane % kLanes * 4;
+  const Seq s = seq_of(c, b);
+  const int group = group_at(prefix, b), mine = s.m * qh;
+  const Seq g = group_of(prefix, group);
+  int first = int(blockIdx.x * 8 + warp) * each;
+  RowSums<TILES> own;
+  own.place(c, sl, s, b, g, group, first + lane, lane < each ? mine : 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  while (first < mine) {
+    own.find(sl);
+    for (int i = 0; i < each && first + i < mine; i += kTogether) {
+      const int src = i + lane / kLanes;
+      RowSums<TILES> r;
+      r.row = __shfl_sync(0xffffffffu, own.row, src);
+      r.there = __shfl_sync(0xffffffffu, own.there, src);
+      r.all = __shfl_sync(0xffffffffu, own.all, src);
+      if (TILES) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          r.from[k] = __shfl_sync(0xffffffffu, own.from[k], src);
+          r.cut[k] = __shfl_sync(0xffffffffu, int(own.cut[k]), src);
+        }
+      }
+      Joined j;
+      const int most = __reduce_max_sync(0xffffffffu, r.all);
+      for (int i0 = 0; i0 < most; i0 += kAtOnce) {
+        float2 v[kAtOnce];
+        float4 x[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const bool live = i0 + k < r.all;
+          const int64_t at = live ? r.at(sl, rows, i0 + k) : 0;
+          v[k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
+          x[k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        j.add(v, x);
+      }
+      if (r.row >= 0) j.template write<T, D>(a, r.row, e);
+    }
+    first += int(gridDim.x) * 8 * each;
+    own.place(c, sl, s, b, g, group, first + lane, lane < each ? mine : 0);
+  }
+}
+
+template <typename T, int D, bool TILES>
 cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, cudaStream_t st) {
-  const int each = 32 / (D / 4), qh = a.c.kvh * a.c.group;
-  // Two rows a lane where that still leaves the SMs 16 warps each, four warps a row where there are at most
-  // 8 rows an SM, eight where there are at most two (32 tokens of 32 heads: 76, 69 and 71 us a call with
-  // one, four and eight, four tokens: 18.7, 16.6 and 15.0).
-  const int64_t all = int64_t(a.c.total_q) * qh / each, sms = device_sm_count();
-  const bool many = all >= sms * 16 * kRowsALane, few = all <= sms * 8, least = all <= sms * 2;
-  const int rows = each * (many ? 8 * kRowsALane : (least ? 1 : (few ? 2 : 8)));
+  const int together = 32 / (D / 4), qh = a.c.kvh * a.c.group;
+  // Four warps a row where there are at most 16 rows an SM, eight where there are at most two (32 tokens of 32
+  // heads: 76, 69 and 71 us a call with one, four and eight, four tokens: 18.7, 16.6 and 15.0; 1500 rows: 53 and 49
+  // with one and four, 4000 rows: 43 and 50); otherwise as many rows a warp as leave each SM 64 of these batches.
+  const int64_t sms = device_sm_count(), warps = int64_t(a.c.total_q) * qh / together;
+  const bool few = warps <= sms * 16, least = warps <= sms * 2;
+  int each = together;
+  while (each < 32 && warps * together > sms * 32 * 2 * each) each *= 2;
   cudaLaunchConfig_t cfg = {};
-  // many rows: as many CTAs as fit, which take several rows one after the other
-  const int64_t most = (int64_t(a.c.max_q) * qh + rows - 1) / rows;
-  cfg.gridDim = dim3(unsigned(many ? std::min(most, std::max<int64_t>(1, kRounds * kResident * sms / a.c.batch)) : most), a.c.batch);
+  const int cta_rows = few ? together * (least ? 1 : 2) : 8 * each;
+  cfg.gridDim = dim3(unsigned((int64_t(a.c.max_q) * qh + cta_rows - 1) / cta_rows), a.c.batch);
+  // and as many CTAs as fit, twice, which take several such batches
+  if (!few) cfg.gridDim.x = unsigned(std::min<int64_t>(cfg.gridDim.x, std::max<int64_t>(1, 8 * sms / a.c.batch)));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -193,16 +262,15 @@ cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (many) return cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, kRowsALane * (128 / D), 1>, a, prefix, sl);
-  if (least) return cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D, 8>, a, prefix, sl);
-  return few ? cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D, 4>, a, prefix, sl)
-             : cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 128 / D, 1>, a, prefix, sl);
+  if (!few) return cudaLaunchKernelEx(&cfg, k_prefix_join_many<T, D, TILES>, a, prefix, sl, int(each));
+  return least ? cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 8, TILES>, a, prefix, sl) : cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 4, TILES>, a, prefix, sl);
 }
 
 cudaError_t launch_join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, int dtype, cudaStream_t st) {
-  if (dtype == MP_DTYPE_BF16)
-    return a.c.d == 128 ? join<__nv_bfloat16, 128>(a, prefix, sl, st) : join<__nv_bfloat16, 64>(a, prefix, sl, st);
-  return a.c.d == 128 ? join<float, 128>(a, prefix, sl, st) : join<float, 64>(a, prefix, sl, st);
+  using B = __nv_bfloat16;
+  if (sl.pre_tiles || sl.own_tiles) return a.c.d == 128 ? join<B, 128, true>(a, prefix, sl, st) : join<B, 64, true>(a, prefix, sl, st);
+  if (dtype == MP_DTYPE_BF16) return a.c.d == 128 ? join<B, 128, false>(a, prefix, sl, st) : join<B, 64, false>(a, prefix, sl, st);
+  return a.c.d == 128 ? join<float, 128, false>(a, prefix, sl, st) : join<float, 64, false>(a, prefix, sl, st);
 }
 
 // How the passes go, and the rows of a block where they are cut into runs (kFew, kSimt).
@@ -239,8 +307,9 @@ Plan plan_of(const mp_cache_config* c, const mp_cache_config* p, int total_q, in
   if (both <= most) return {kFew, kFew, few_rows(both, 8), few_rows(both, 8)};
   const int rows = few_rows(own, 8);
   const bool few = own <= most && prefix_is_few(p, max_group_q, max_prefix, rows);
-  if (few || own <= 16) return {kFew, few ? kFew : (prefix_in_slices(p, total_q, max_group_q) ? kSlices : kTiles), rows, rows};
-  return {kTiles, kTiles, 0, 0};
+  if (few || (own <= 16 && prefix_in_slices(p, total_q, max_group_q))) return {kFew, few ? kFew : kSlices, rows, rows};
+  if (own <= 16) return {kFew, kTiles, rows, kTileRows};
+  return {kTiles, kTiles, kTileRows, kTileRows};
 }
 // The most slices of a pass.
 int slices_of(Kind kind, const mp_cache_config* c, int total_q, int max_q, int max_kv) {
@@ -263,8 +332,14 @@ uint64_t slice_rows_most(const mp_cache_config* c, int total_q, int max_q, int m
 }
 uint64_t sums_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * c->head_dim * 4); }
 uint64_t ml_bytes(const mp_cache_config* c, uint64_t slice_rows) { return align256(slice_rows * c->q_heads * 2 * 4); }
-uint64_t pieces_bytes(const mp_cache_config* c, int total_q, int rows) { return align256(uint64_t(piece_keys(c, total_q, rows)) * c->kv_heads * 4); }
-constexpr int kLeastRows = 4;  // of a block
+// Numbers of pieces (two for large tiles), and for any plan.
+uint64_t pieces_bytes(const mp_cache_config* c, int total_q, int rows) {
+  return align256(uint64_t(piece_keys(c, total_q, rows)) * c->kv_heads * (rows == kTileRows ? 8 : 4));
+}
+uint64_t pieces_bytes_most(const mp_cache_config* c, int total_q) { return align256(uint64_t(piece_keys(c, total_q, 4)) * c->kv_heads * 8); }
+
+// Rows of cut tiles as packed rows, which have a sum for each query head.
+uint64_t cut_rows(const mp_cache_config* c, uint64_t rows) { return (rows + c->q_heads - 1) / c->q_heads; }
 
 int check(const mp_cache_config* c, const mp_cache_config* p, int total_q, int max_q, int max_kv, int max_group_q, int max_prefix) {
   int rc = check_cache(c);
@@ -292,9 +367,9 @@ int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_config*
   if (total_q == 0) return MP_OK;
   max_q = std::min(max_q, total_q);
   max_group_q = std::min(max_group_q, total_q);
-  const uint64_t rows = slice_rows_most(cfg, total_q, max_q, max_kv, false) + slice_rows_most(prefix_cfg, total_q, max_group_q, max_prefix, true);
-  *bytes = pieces_bytes(cfg, total_q, kLeastRows) + pieces_bytes(prefix_cfg, total_q, kLeastRows) + sums_bytes(cfg, rows) + ml_bytes(cfg, rows) +
-           (cfg->dtype == MP_DTYPE_BF16 ? both_tc_workspace(cfg, max_q, max_kv, prefix_cfg, max_group_q, max_prefix) : 0);
+  uint64_t rows = slice_rows_most(cfg, total_q, max_q, max_kv, false) + slice_rows_most(prefix_cfg, total_q, max_group_q, max_prefix, true);
+  if (cfg->dtype == MP_DTYPE_BF16) rows += cut_rows(cfg, both_tc_rows(cfg, max_q, max_kv, prefix_cfg, max_group_q, max_prefix));
+  *bytes = pieces_bytes_most(cfg, total_q) + pieces_bytes_most(prefix_cfg, total_q) + sums_bytes(cfg, rows) + ml_bytes(cfg, rows);
   return MP_OK;
 }
 
@@ -321,29 +396,34 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   max_group_q = std::min(max_group_q, total_q);
   const Plan plan = plan_of(cfg, prefix_cfg, total_q, max_q, max_group_q, max_prefix);
   const int own_slices = slices_of(plan.own, cfg, total_q, max_q, max_kv), slices = slices_of(plan.shared, prefix_cfg, total_q, max_group_q, max_prefix);
-  const uint64_t rows = uint64_t(own_slices + slices) * total_q, sums = sums_bytes(cfg, rows), ml = ml_bytes(cfg, rows),
-                 own_pieces = plan.own_rows ? pieces_bytes(cfg, total_q, plan.own_rows) : 0,
-                 pre_pieces = plan.pre_rows ? pieces_bytes(prefix_cfg, total_q, plan.pre_rows) : 0;
   const bool own_tiles = plan.own == kTiles, shared_tiles = plan.shared == kTiles;
-  uint64_t need = own_pieces + pre_pieces + sums + ml;
-  if (own_tiles || shared_tiles)
-    need += both_tc_workspace(own_tiles ? cfg : nullptr, max_q, max_kv, shared_tiles ? prefix_cfg : nullptr, max_group_q, max_prefix);
+  const uint64_t tile_rows = own_tiles || shared_tiles ? both_tc_rows(own_tiles ? cfg : nullptr, max_q, max_kv, shared_tiles ? prefix_cfg : nullptr,
+                                                                      max_group_q, max_prefix)
+                                                       : 0;
+  const uint64_t whole = uint64_t(own_slices + slices) * total_q, rows = whole + cut_rows(cfg, tile_rows), sums = sums_bytes(cfg, rows),
+                 own_pieces = pieces_bytes(cfg, total_q, plan.own_rows), pre_pieces = pieces_bytes(prefix_cfg, total_q, plan.pre_rows);
+  const uint64_t need = own_pieces + pre_pieces + sums + ml_bytes(cfg, rows);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MP_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MP_ERR_SCRATCH;
   if (injected("prefix")) return MP_ERR_INJECTED;
 
   char* ws = static_cast<char*>(workspace);
-  Slices sl = {slices, own_slices, nullptr, nullptr, 0, 0, plan.pre_rows, plan.own_rows};
-  if (!own_tiles) {
-    sl.own_pieces = reinterpret_cast<int32_t*>(ws);
-    sl.own_keys = int(piece_keys(cfg, total_q, plan.own_rows));
-  }
-  if (!shared_tiles) {
-    sl.pre_pieces = reinterpret_cast<int32_t*>(ws + own_pieces);
-    if (plan.shared != kSlices) sl.pre_keys = int(piece_keys(prefix_cfg, total_q, plan.pre_rows));
-  }
+  Slices sl;
+  sl.shared = slices;
+  sl.own = own_slices;
+  sl.own_pieces = reinterpret_cast<int32_t*>(ws);
+  sl.pre_pieces = reinterpret_cast<int32_t*>(ws + own_pieces);
+  sl.own_keys = int(piece_keys(cfg, total_q, plan.own_rows));
+  sl.pre_keys = plan.shared == kSlices ? 0 : int(piece_keys(prefix_cfg, total_q, plan.pre_rows));
+  sl.own_rows = plan.own_rows;
+  sl.pre_rows = plan.pre_rows;
+  sl.own_tiles = own_tiles;
+  sl.pre_tiles = shared_tiles;
+  sl.slot_rows = int(std::min<int64_t>(kTileRows, int64_t(std::max(own_tiles ? max_q : 1, shared_tiles ? max_group_q : 1)) *
+                                                      (cfg->q_heads / cfg->kv_heads)));
+  sl.slots = int(tile_rows / sl.slot_rows);
+  sl.cut = int64_t(whole) * cfg->q_heads;
   ws += own_pieces + pre_pieces;
-  void* tiles = ws + sums + ml;
   ChunkArgs p, a;
   a.c = cache_args(cfg, page_table, cu_q, kv_len, total_q, max_q, max_kv, status);
   a.q = q;
@@ -402,8 +482,11 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     both.state = p.part;
     both.state_ml = p.ml;
     both.own_slice = slices * slice;
+    both.part = p.part + sl.cut * cfg->head_dim;
+    both.ml = p.ml + sl.cut * 2;
+    const TilePieces at = {sl.pre_keys, sl.own_keys, reinterpret_cast<int2*>(sl.pre_pieces), reinterpret_cast<int2*>(sl.own_pieces)};
     ProfScope ps(st, K_PREFIX_ATTEND);
-    if (launch_both_tc(both, own_tiles, shared_tiles ? &p : nullptr, tiles, st) != cudaSuccess) return MP_ERR_CUDA;
+    if (launch_both_tc(both, own_tiles, shared_tiles ? &p : nullptr, at, st) != cudaSuccess) return MP_ERR_CUDA;
   }
   a.out = out;
   a.lse = lse;
