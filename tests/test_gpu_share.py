@@ -442,6 +442,26 @@ def test_prefix_attention_of_more_groups_than_one_launch_takes(mp, dtype):
     assert c.status.item() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefix_attention_of_more_tiles_than_one_launch_takes(mp, dtype):
+    """Chunks of 1350 sequences and 1000 groups on tiles: three launches, whose cut tiles are joined at once. Two
+    long caches and a long prefix among short ones."""
+    groups = [1 + g % 2 if g % 3 else 0 for g in range(1000)]
+    batch = sum(groups) + 351
+    q_lens = [(5 * b) % 7 for b in range(batch)]
+    q_lens[1200] = 300
+    own = [max(1, m) + (7 * b) % 20 for b, m in enumerate(q_lens)]
+    own[3], own[1201] = 3000, 900
+    prefixes = [(11 * g) % 50 for g in range(1000)]
+    prefixes[700] = 2000
+    c = Shared(mp, dtype, 8, 1, 64, 16, own, groups, prefixes)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1], 8, 64)
+    out, lse = attend_prefix(mp, c, q, cu, cu_t, 300)
+    check_prefix(c, dtype, q, cu, out, lse)
+    assert c.status.item() == 0
+
+
 @pytest.mark.parametrize("seqs", [5, 20])
 def test_prefix_attention_of_many_groups_in_slices(mp, seqs):
     """1030 groups, planned 1024 at a time and most of them without a sequence, next to own slots."""
