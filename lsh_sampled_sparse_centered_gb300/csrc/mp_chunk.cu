@@ -105,14 +105,16 @@ __device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b,
     }
     copy_commit();
   };
-  for (int i = cr; i < kBM; i += kStep) {
-    const int r = r0 + i;
-    const bool live = r < rows;
-    const float* src = static_cast<const float*>(a.q);
-    if (live) src += (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D + ce;
-    copy16(qs + i * kRow + place(ce, (i >> 3) & 1), src, live);
-  }
+  // Q's copies are of K's group, so that there are none where no slot is seen: nothing would wait for them, and
+  // they could land on the rows of the CTA's next tile.
   if (k0 < k1) {
+    for (int i = cr; i < kBM; i += kStep) {
+      const int r = r0 + i;
+      const bool live = r < rows;
+      const float* src = static_cast<const float*>(a.q);
+      if (live) src += (int64_t(s.row0 + r / c.group) * qh + h * c.group + r % c.group) * D + ce;
+      copy16(qs + i * kRow + place(ce, (i >> 3) & 1), src, live);
+    }
     copy_tile(ks, a.keys, k0, 7);
     copy_tile(vs, a.values, k0, 0);
   }
