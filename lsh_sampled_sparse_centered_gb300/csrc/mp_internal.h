@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "magicpig.h"
 
 namespace mp {
@@ -150,6 +152,23 @@ cudaError_t launch_attend(const Geometry& g, int n, int splits, const TablesPtrs
                           cudaStream_t st);
 
 int device_sm_count();
+
+// Lets kernel F ask for as much dynamic shared memory as a CTA can have. The limit belongs to the function, on all
+// threads: one that followed the call's own size would be lowered by another thread's smaller call before the launch.
+#ifdef __CUDACC__
+template <auto F>
+cudaError_t allow_smem() {
+  static std::atomic<int> most{0};  // beside F's own static part
+  int bytes = most.load(std::memory_order_relaxed);
+  if (bytes == 0) {
+    cudaFuncAttributes own;
+    const cudaError_t e = cudaFuncGetAttributes(&own, F);
+    if (e != cudaSuccess) return e;
+    most.store(bytes = 227 * 1024 - int(own.sharedSizeBytes), std::memory_order_relaxed);
+  }
+  return cudaFuncSetAttribute(F, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+#endif
 
 // ---- host helpers shared by the entry points (mp_api.cu) ----
 uint64_t align256(uint64_t x);

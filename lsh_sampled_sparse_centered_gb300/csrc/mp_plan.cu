@@ -244,7 +244,7 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
   const int threads = std::min(kMostThreads, (std::max(a.batch, std::min(a.max_rows, kMostThreads)) + 31) / 32 * 32);
   const size_t smem = plan_smem(a.batch, threads);
   if (smem > 40 * 1024) {  // 48 KB with the static part need no asking
-    const cudaError_t e = cudaFuncSetAttribute(many ? k_cache_plan<true> : k_cache_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = many ? allow_smem<k_cache_plan<true>>() : allow_smem<k_cache_plan<false>>();
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -1,10 +1,16 @@
 """Planning, attention over shared prefixes and rotation on the GPU where one call meets another: tiles of one CTA,
 threads that call at once, a cache that goes on after it was turned. Tolerances as in test_gpu_share.py."""
+import os
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
+import share_reference as S
 from test_gpu_cache import DEV, offsets
-from test_gpu_share import Shared, attend_prefix, check_prefix, mp  # noqa: F401
+from test_gpu_share import Plan, Shared, attend_prefix, check_prefix, ints, mp  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +36,84 @@ def test_fp32_tiles_behind_tiles_that_see_nothing(mp, hk, d, m, n, prefix):  # n
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     check_prefix(c, "f32", q, cu, *first)
     assert c.status.item() == 0
+
+
+def together(*loops):
+    """Runs the functions in a thread each, at once; the first exception of any is raised."""
+    failed = []
+    start = threading.Barrier(len(loops))
+
+    def run(f):
+        try:
+            start.wait()
+            f()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(f,)) for f in loops]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if failed:
+        raise failed[0]
+
+
+def test_plans_of_two_sizes_from_two_threads(mp):  # noqa: F811
+    """A batch of 8192 sequences needs more shared memory than one of 1500: neither thread's calls take it from the
+    other's, and both pools are planned as if they were alone."""
+    sizes, steps = (8192, 1500, 700), 2000
+    pools = [Plan(mp, [10 + i] * n, 16, 8, spare=2 * n, seed=i) for i, n in enumerate(sizes)]
+    cu = [torch.zeros(n + 1, dtype=torch.int32, device=DEV) for n in sizes]
+    change = [(ints([1] * n), ints([-1] * n)) for n in sizes]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+
+    def loop(i):
+        p, st = pools[i], streams[i]
+
+        def run():
+            for k in range(steps):
+                mp.mp_cache_plan(p.cfg, change[i][k % 2], None, p.d_kv, p.d_n, 3 * p.batch, p.d_table, p.d_free, p.d_kv, p.d_n, cu[i], None, None, None,
+                                 p.status, stream=st)
+        return run
+
+    together(*(loop(i) for i in range(len(sizes))))
+    torch.cuda.synchronize()
+    for p, c in zip(pools, cu):
+        kv, n_free, table, free = p.kv, p.n_free, p.table, p.free
+        for x in (1, -1):  # every two steps end where they began, the pages given back in another order once
+            kv, n_free, cu_want, table, free, _ = S.plan([x] * p.batch, kv, [0] * p.batch, table, free, n_free, 16, 8, 3 * p.batch)
+        assert p.d_kv.tolist() == kv == p.kv and p.d_n.tolist() == [n_free] and c.tolist() == cu_want and p.status.item() == 0
+
+
+FIRST_PLAN = '''
+import sys
+import torch
+sys.path.insert(0, {root!r})
+import lsh_sampled_sparse_centered_gb300 as mp
+ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda:0")
+n = 3000
+cfg = mp.make_cache_config(batch=n, kv_heads=1, q_heads=1, head_dim=64, page_size=16, n_pages=2 * n, max_pages=4)
+table, free, n_free = torch.zeros(n, 4, dtype=torch.int32, device="cuda:0"), torch.arange(2 * n, dtype=torch.int32, device="cuda:0"), ints(2 * n)
+change, kv, cu = torch.ones(n, dtype=torch.int32, device="cuda:0"), torch.zeros(n, dtype=torch.int32, device="cuda:0"), torch.zeros(n + 1, dtype=torch.int32, device="cuda:0")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    mp.mp_cache_plan(cfg, change, None, kv, n_free, n, table, free, kv, n_free, cu)
+graph.replay()
+torch.cuda.synchronize()
+assert (kv == 1).all() and n_free.item() == n and cu[-1].item() == n and table[:, 0].tolist() == list(range(2 * n - 1, n - 1, -1))
+print("same")
+'''
+
+
+def test_a_first_plan_of_many_sequences_may_be_captured():
+    """What it asks about its kernel, it may ask under a capture."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_PLAN.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), (r.stdout[-500:], r.stderr[-2000:])
