@@ -132,7 +132,8 @@ cudaError_t launch_csr_build(const Geometry& g, int n_prefill, const TablesPtrs&
   if (hi <= lo) return cudaSuccess;
   const int segs = (hi - lo + kCsrSeg - 1) / kCsrSeg;
   const size_t smem = ((size_t(g.nb) * 4 + 15) & ~size_t(15)) + size_t(kCsrSeg + 16) * 2;
-  cudaFuncSetAttribute(k_csr_build, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  const cudaError_t e = allow_smem<k_csr_build>();
+  if (e != cudaSuccess) return e;
   dim3 grid(g.units * g.L, segs);
   k_csr_build<<<grid, kCsrThreads, smem, st>>>(t.codes, t.off, t.ids, g.cap, g.nb, g.nseg, lo, hi, &t.hdr->status);
   return cudaGetLastError();

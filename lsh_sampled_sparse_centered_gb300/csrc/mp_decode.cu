@@ -270,7 +270,8 @@ cudaError_t launch_match_csr(const Geometry& g, int n, const TablesPtrs& t, cons
   const int nwords = (n - lo + 31) >> 5;
   const int body = g.threshold >= 3 ? nwords * 9 : nwords * 2;
   const size_t smem = size_t(body + 1) * 4 + size_t(g.L) * g.nseg * 12 + 4 + size_t(g.L) * 2 + 16;
-  cudaFuncSetAttribute(k_match_csr, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  const cudaError_t e = allow_smem<k_match_csr>();
+  if (e != cudaSuccess) return e;
   k_match_csr<<<g.queries, kMatchWarps * 32, smem, st>>>(t.hdr, dp.qcodes, t.codes, t.off, t.ids, dp.lists,
                                                          dp.list_len, dp.sample_count, dp.counters, n, g.s, g.w, g.L,
                                                          g.nb, g.cap, g.nseg, g.group, g.threshold);

@@ -662,7 +662,7 @@ cudaError_t launch_rows_tc(const Geometry& g, const RowsHashTc& h0, const RowsHa
     mx1 = mx0;
   }
   const size_t smem = RowsLayout<D>::bytes(a.nr) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(k_hash_rows_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  const cudaError_t e = allow_smem<k_hash_rows_tc<D>>();
   if (e != cudaSuccess) return e;
   dim3 grid((a.vrows + a.nr - 1) / a.nr, g.nt, h0.groups);
   k_hash_rows_tc<D><<<grid, kRowsWarps * 32, smem, st>>>(mw, mx0, mx1, a, g.L, g.K, g.tpt);

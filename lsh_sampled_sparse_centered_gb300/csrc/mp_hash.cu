@@ -327,7 +327,7 @@ static void launch_rows_tw(const Geometry& g, const HashRowsArgs& a, cudaStream_
   dim3 grid((a.rows + R - 1) / R, g.nt, a.groups);
   const int wstride = g.d * int(sizeof(WT)) / 4 + 1;
   const size_t smem = size_t(R) * g.d * sizeof(float) + size_t(kHashCols) * wstride * 4;
-  cudaFuncSetAttribute(k_hash_rows<T, WT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (allow_smem<k_hash_rows<T, WT, R>>() != cudaSuccess) return;  // the caller asks for the error
   k_hash_rows<T, WT, R><<<grid, kHashCols, smem, st>>>(a, g.d, g.K, g.L, g.tpt, g.kltc);
 }
 

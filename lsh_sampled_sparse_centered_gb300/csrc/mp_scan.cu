@@ -146,11 +146,13 @@ cudaError_t launch_scan(const Geometry& g, int n, const TablesPtrs& t, const Dec
   dim3 grid((nwords + 4 * kScanThreads - 1) / (4 * kScanThreads), g.units);
   const size_t smem = size_t(g.group) * g.L * sizeof(uint16_t);
   if (g.threshold >= 3) {
-    cudaFuncSetAttribute(k_scan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = allow_smem<k_scan<true>>();
+    if (e != cudaSuccess) return e;
     k_scan<true><<<grid, kScanThreads, smem, st>>>(t.planes, dp.qcodes, dp.sbits, g.L, g.K, g.cw, nwords,
                                                    g.group, g.threshold);
   } else {
-    cudaFuncSetAttribute(k_scan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = allow_smem<k_scan<false>>();
+    if (e != cudaSuccess) return e;
     k_scan<false><<<grid, kScanThreads, smem, st>>>(t.planes, dp.qcodes, dp.sbits, g.L, g.K, g.cw, nwords,
                                                     g.group, g.threshold);
   }
