@@ -7,7 +7,7 @@
 namespace mp {
 
 // One layer's paged cache and the packed batch of a call (host-checked limits).
-struct CacheArgs {
+struct CacheCall {
   int batch, kvh, group, d;      // group = q_heads / kv_heads
   int page_size, n_pages, cols;  // cols: columns of the page table
   int page_shift;                // log2(page_size) where it is a power of two, else -1
@@ -16,14 +16,17 @@ struct CacheArgs {
   const int32_t* kv_len;
   int total_q, max_q, max_kv;
   uint32_t* status;              // may be nullptr
-  // set for the pass over shared prefixes: `batch` counts groups then, and kv_len, table and the sizes
-  // are the prefixes'; group g are the sequences [cu_group[g], cu_group[g + 1]) of `sequences`
+};
+// The same, or a pass over shared prefixes: `batch` counts groups there, and kv_len, table and the sizes
+// are the prefixes'; group g are the sequences [cu_group[g], cu_group[g + 1]) of `sequences`.
+struct CacheArgs : CacheCall {
   const int32_t* cu_group = nullptr;
   int sequences = 0;
 };
 
-struct ChunkArgs {
-  CacheArgs c;
+template <typename Cache>
+struct ChunkArgsOf {
+  Cache c;
   const void *q, *keys, *values;
   void* out;
   float* lse;   // may be nullptr
@@ -34,19 +37,24 @@ struct ChunkArgs {
   float* part;  // [..][d]: unnormalised sums
   float* ml;    // [..][2]: their reference (log2) and sum
   void* cuts;   // shared tiles (tensor cores)
-  // attention with prefixes, large tiles: a row's unnormalised sum [total_q][q_heads][d] and its reference
-  // and sum go here where its tile is whole, those of the own slots own_slice rows further on
-  float *state = nullptr, *state_ml = nullptr;
-  int64_t own_slice = 0;
-  // prefixes in slices (tensor cores): `splits` are the most; a group's number goes here, for each KV head
-  int32_t* pieces = nullptr;
 #if MP_CHECK
   bool stall;  // one CTA stops half way, so that the others' waits run out
 #endif
 };
+// What the prefixes take besides is no part of it: a launch of few tokens is so short that 48 bytes more of
+// arguments show in it (one token over 2000 slots, d = 64: 6.99 and 7.24 us).
+using ChunkArgs = ChunkArgsOf<CacheCall>;
+struct PrefixArgs : ChunkArgsOf<CacheArgs> {
+  // large tiles: a row's unnormalised sum [total_q][q_heads][d] and its reference and sum go here where its
+  // tile is whole, those of the own slots own_slice rows further on
+  float *state = nullptr, *state_ml = nullptr;
+  int64_t own_slice = 0;
+  // prefixes in slices (tensor cores): `splits` are the most; a group's number goes here, for each KV head
+  int32_t* pieces = nullptr;
+};
 
 struct WeightsArgs {
-  CacheArgs c;
+  CacheCall c;
   const void *q, *keys;
   const float* lse;
   float* scores;
@@ -56,7 +64,7 @@ struct WeightsArgs {
 };
 
 struct AppendArgs {
-  CacheArgs c;
+  CacheCall c;
   const void *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;
   const void *q_norm, *k_norm;
@@ -68,7 +76,7 @@ struct AppendArgs {
 };
 
 struct EvictArgs {
-  CacheArgs c;
+  CacheCall c;
   const void *keys, *values;
   const float* scores;
   int n_sink, window, budget;
@@ -116,7 +124,7 @@ struct TilePieces {
   int pre_keys, own_keys;
   int2 *pre_pieces, *own_pieces;  // pieces of each tile, and the slot (of as many rows as a tile has at most) of the first
 };
-cudaError_t launch_both_tc(const ChunkArgs& own, bool own_units, const ChunkArgs* pre, const TilePieces& at, cudaStream_t st);
+cudaError_t launch_both_tc(const PrefixArgs& own, bool own_units, const PrefixArgs* pre, const TilePieces& at, cudaStream_t st);
 uint64_t both_tc_rows(const mp_cache_config* own, int max_q, int max_kv, const mp_cache_config* pre, int max_group_q, int max_prefix);
 // Whether a pass over prefixes on the tensor cores goes in slices, and how many (without: one, after a join of its own).
 bool prefix_in_slices(const mp_cache_config* c, int total_q, int max_q);
@@ -146,7 +154,7 @@ struct Seq {
   int row0, m, n, first;
   __host__ __device__ int seen() const { return max(0, min(n, first + m)); }  // slots that any row sees
 };
-__host__ __device__ __forceinline__ Seq seq_of(const CacheArgs& c, int b) {
+__host__ __device__ __forceinline__ Seq seq_of(const CacheCall& c, int b) {
   Seq s;
   const int64_t slots = int64_t(c.cols) * c.page_size;
   const int n = c.kv_len[b];
@@ -186,8 +194,8 @@ __host__ __device__ __forceinline__ Seq group_of(const CacheArgs& c, int g) {
   if (s.n != n || b0 != i0 || b1 != i1 || s.row0 != r0 || s.row0 + s.m != r1) flag(c.status, MP_STATUS_BAD_LENGTH);
   return s;
 }
-template <bool GROUP>
-__host__ __device__ __forceinline__ Seq rows_of(const CacheArgs& c, int b) {
+template <bool GROUP, typename Cache>
+__host__ __device__ __forceinline__ Seq rows_of(const Cache& c, int b) {
   if constexpr (GROUP) return group_of(c, b);
   else return seq_of(c, b);
 }
@@ -200,7 +208,7 @@ __host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // Sequence that packed row r belongs to, or -1: the last b with cu_q[b] <= r, if r is
 // one of its rows. A table that decreases somewhere gives some sequence or none, never
 // an index outside it.
-__host__ __device__ __forceinline__ int seq_at(const CacheArgs& c, int r) {
+__host__ __device__ __forceinline__ int seq_at(const CacheCall& c, int r) {
   int lo = 0, hi = c.batch;  // cu_q[lo] <= r is kept where it holds for 0
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -213,7 +221,7 @@ __host__ __device__ __forceinline__ int seq_at(const CacheArgs& c, int r) {
 #ifdef __CUDACC__
 // The same for a whole warp that asks for one row: 32 boundaries are looked at at a time, so
 // that up to 33 sequences take one round of loads and not five that wait for each other.
-__device__ __forceinline__ int seq_at_warp(const CacheArgs& c, int r) {
+__device__ __forceinline__ int seq_at_warp(const CacheCall& c, int r) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = c.batch;  // cu_q[lo] <= r is kept where it holds for 0
   while (hi - lo > 1) {
@@ -240,14 +248,14 @@ __host__ __device__ __forceinline__ int page_at(const int32_t* table, int cols, 
 
 // Row of the pool that holds slot s of KV head h, for reading: a bad page reads page 0
 // instead. The pool's rows are 32-bit (checked by the host).
-__host__ __device__ __forceinline__ int slot_row(const CacheArgs& c, int b, int h, int s) {
+__host__ __device__ __forceinline__ int slot_row(const CacheCall& c, int b, int h, int s) {
   if (!c.table) return (b * c.kvh + h) * c.page_size + s;
   const int col = c.page_shift >= 0 ? s >> c.page_shift : s / c.page_size;
   const int p = max(0, page_at(c.table, c.cols, c.n_pages, b, col, c.status));
   return (p * c.kvh + h) * c.page_size + (s - col * c.page_size);
 }
 // Its element offset.
-__host__ __device__ __forceinline__ int64_t slot_read(const CacheArgs& c, int b, int h, int s) {
+__host__ __device__ __forceinline__ int64_t slot_read(const CacheCall& c, int b, int h, int s) {
   return int64_t(slot_row(c, b, h, s)) * c.d;
 }
 #endif

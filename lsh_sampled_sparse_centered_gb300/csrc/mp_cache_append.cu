@@ -57,7 +57,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32, kResident) k_cache_append(const AppendArgs a, const int parts) {
   constexpr int V = Vec<T>::N, TPH = D / V, HPW = 32 / TPH;  // heads of a warp at a time
   __shared__ alignas(16) float cosine[kWarps][D / 2], sine[kWarps][D / 2];  // of each pair's angle
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int warp = threadIdx.x >> 5, l32 = threadIdx.x & 31, lane = l32 % TPH, e0 = lane * V;
   const int64_t w = int64_t(blockIdx.x) * kWarps + warp;
   const int64_t r = w / parts;

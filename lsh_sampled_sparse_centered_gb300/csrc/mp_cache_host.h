@@ -59,9 +59,9 @@ inline int shift_of(int n) {
   return -1;
 }
 
-inline CacheArgs cache_args(const mp_cache_config* c, const int32_t* table, const int32_t* cu_q, const int32_t* kv_len,
+inline CacheCall cache_args(const mp_cache_config* c, const int32_t* table, const int32_t* cu_q, const int32_t* kv_len,
                             int total_q, int max_q, int max_kv, uint32_t* status) {
-  CacheArgs a;
+  CacheCall a;
   a.batch = c->batch;
   a.kvh = c->kv_heads;
   a.group = c->q_heads / c->kv_heads;

@@ -79,8 +79,8 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // the softmax, the next K under the product with V.
 // The tile: rows [r0, r0 + 64) of those of `s` (sequence b, or a group where c.cu_group is set), over the
 // slots [k0, k1) that any of them sees; `split` is the slice for its sums, where there are slices.
-template <int D, bool SLICES>
-__device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b, const int h, const Seq& s, const int r0, const int k0, const int k1,
+template <int D, bool SLICES, typename A>
+__device__ __forceinline__ void chunk_simt_tile(const A& a, const int b, const int h, const Seq& s, const int r0, const int k0, const int k1,
                                                 const int split) {
   constexpr bool kPad = D == 64;
   constexpr int kRow = D + kPad * 4, kPt = kBM + kPad * 4;
@@ -90,7 +90,7 @@ __device__ __forceinline__ void chunk_simt_tile(const ChunkArgs& a, const int b,
   float* ks = qs + kBM * kRow;   // [64][kRow]
   float* vs = ks + kBN * kRow;   // [64][kRow]
   float* pt = vs + kBN * kRow;   // [64 keys][kPt]
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int rows = s.m * c.group, qh = c.kvh * c.group, first = s.first;  // first: slot of token 0
   const bool slices = SLICES || a.splits > 1;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -298,7 +298,7 @@ template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(256) k_chunk_join(const ChunkArgs a) {
   constexpr int PER = D / 32;
   __shared__ float so[8][D], sl[8];
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int qh = c.kvh * c.group;
   const int64_t rows = int64_t(c.total_q) * qh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThr) k_weights_simt(const WeightsArgs a) {
   float* qt = sm;            // [D][64]
   float* kt = qt + D * kBM;  // [D][64]
   float* col = kt + D * kBN; // [8][64] partial column sums
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int b = blockIdx.z, h = blockIdx.y, n0 = blockIdx.x * kBN;
   const Seq s = seq_of(c, b);
   if (n0 >= s.seen() || s.m == 0) return;
@@ -426,7 +426,7 @@ cudaError_t prefix_simt(const PrefixFew& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(k_prefix_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   double steps = 0;
-  for (const ChunkArgs* x : {&a.pre, &a.own}) {
+  for (const PrefixArgs* x : {&a.pre, &a.own}) {
     const int units = x == &a.pre ? a.groups : (a.own_units ? x->c.batch : 0);
     steps += double(units) * x->c.kvh * ((int64_t(x->c.max_q) * x->c.group + kBM - 1) / kBM) * ((x->c.max_kv + kBN - 1) / kBN + 1);
   }

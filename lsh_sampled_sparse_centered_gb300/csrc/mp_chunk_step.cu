@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(warps_of(JOINED) * 32) k_chunk_step(const Chun
   constexpr int TILES = D / 16;   // 16-row tiles of O^T
   __shared__ float so[kWarps][NT * 8][D + 4];
   __shared__ float sm[kWarps][NT * 8], sl[kWarps][NT * 8];
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Seq s = seq_of(c, b);

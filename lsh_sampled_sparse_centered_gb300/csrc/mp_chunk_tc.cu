@@ -27,13 +27,13 @@ uint64_t both_tc_rows(const mp_cache_config* own, int max_q, int max_kv, const m
 }
 
 cudaError_t launch_chunk_tc(const ChunkArgs& a, void* workspace, cudaStream_t st) {
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int ctas = chunk_tc_ctas(c.batch, c.kvh, c.group, c.max_q, c.max_kv), slot_rows = slot_rows_of(c.group, c.max_q);
   return c.d == 128 ? launch<128, kChunk, 0>(a, {}, c.batch, ctas, slot_rows, workspace, st)
                     : launch<64, kChunk, 0>(a, {}, c.batch, ctas, slot_rows, workspace, st);
 }
 
-cudaError_t launch_both_tc(const ChunkArgs& a, bool own, const ChunkArgs* shared, const TilePieces& at, cudaStream_t st) {
+cudaError_t launch_both_tc(const PrefixArgs& a, bool own, const PrefixArgs* shared, const TilePieces& at, cudaStream_t st) {
   const CacheArgs& c = a.c;
   Extra<kBoth> x = {};
   int own_ctas = 0, pre_ctas = 0, units = 0, max_q = 1;

@@ -32,6 +32,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mp_cache.cuh"
 #include "mp_prefix_few.cuh"
@@ -233,6 +234,8 @@ template <>
 struct Extra<kCuts> : OwnSide {};
 template <>
 struct Extra<kPairs> : OwnSide {};
+template <Mode MODE>
+using ArgsOf = std::conditional_t<MODE == kChunk, ChunkArgs, PrefixArgs>;
 
 // CTAs of `ctas` that take the own slots (the last of the grid), so that both kinds end together. Times in
 // 0.1 us: a step of large tiles takes an SM 1.5 us with two halves (d = 64: 1.1) and about 1.0 for 128 rows
@@ -265,7 +268,7 @@ __device__ __forceinline__ int own_ctas(int64_t tile_steps, int64_t tiles, int64
 // NT: rows in eights of the own side's units (slices).
 template <int D, Mode MODE, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_chunk_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkArgs a,
+    k_chunk_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ArgsOf<MODE> a,
                const int box, const int b_begin, const int b_end, const int slot_rows,
                const __grid_constant__ Extra<MODE> extra) {
   constexpr bool BOTH = MODE == kBoth;
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(offsetof(Smem<D>, q) % 1024 == 0 && offsetof(Smem<D>, kv) % 1024 == 0 && sizeof(S.q[0][0]) % 1024 == 0 &&
                 sizeof(S.kv[0][0]) % 1024 == 0);
   constexpr uint32_t kRowBytes = 128;
-  const CacheArgs& c = a.c;
+  const auto& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile uint32_t* abort = &S.abort;
   const int qh = c.kvh * c.group;
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tiles = 0, pieces = 0;
       int64_t mine = 0, pre = 0;
       auto look = [&]() {  // a group per lane
-        if (g0 != b_begin) s = g0 + lane < b_end ? group_of(c, g0 + lane) : Seq{0, 0, 0, 0};
+        if (g0 != b_begin) s = g0 + lane < b_end ? rows_of<CUT>(c, g0 + lane) : Seq{0, 0, 0, 0};
         tiles = tiles_of(s, c.group);
         pieces = pieces_of(prefix_steps(s), length);
         pre = mine = int64_t(tiles) * pieces * c.kvh;
@@ -697,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Where the boxes of a tile lie (eight at most), for four steps at a time and one such round
         // ahead: a page looked up when its box is due cost every tile that wait (a ragged batch over
         // pages of 16: 2 us a step).
-        const CacheArgs* cache = &c;
+        const CacheCall* cache = &c;
         const CUtensorMap *map_k = &tmK, *map_v = &tmV;
         int cb = pc.b, rows_of_box = box;
         if constexpr (BOTH) {
@@ -1388,8 +1391,8 @@ __global__ void __launch_bounds__(256) k_chunk_tc_join(const ChunkArgs a, const 
 int slot_rows_of(int group, int max_q) { return int(std::min<int64_t>(kRows, int64_t(max_q) * group)); }
 
 template <int D, Mode MODE, int NT>
-cudaError_t launch(ChunkArgs a, Extra<MODE> extra, int units, int ctas, int slot_rows, void* workspace, cudaStream_t st) {
-  const CacheArgs& c = a.c;
+cudaError_t launch(ArgsOf<MODE> a, Extra<MODE> extra, int units, int ctas, int slot_rows, void* workspace, cudaStream_t st) {
+  const CacheCall& c = a.c;
   CUtensorMap mk, mv;
   const int box = box_rows(c.table, c.page_size);
   const uint64_t rows = uint64_t(c.n_pages) * c.kvh * c.page_size;

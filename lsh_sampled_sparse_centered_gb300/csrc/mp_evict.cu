@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kSel, 1) k_evict_select(const EvictArgs a) {
   __shared__ SelectSmem S;
   extern __shared__ uint32_t stage[];
   cg::cluster_group cluster = cg::this_cluster();
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int h = blockIdx.x / ranks, b = blockIdx.y;
   const int n = seq_of(c, b).n;
@@ -200,7 +200,7 @@ constexpr int kRowsEach = 2, kResident = 8;  // CTAs of an SM: 32 registers
 template <int ROW>
 __global__ void __launch_bounds__(256, kResident) k_evict_gather(const EvictArgs a) {
   constexpr int GROUPS = 256 / ROW;
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int h = blockIdx.y, b = blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // k_evict_select has written the kept slots
   const int m = min(seq_of(c, b).n, a.budget);

@@ -43,7 +43,7 @@ struct Joined {
     }
   }
   template <typename T, int D>
-  __device__ __forceinline__ void write(const ChunkArgs& a, int64_t row, int e) const {
+  __device__ __forceinline__ void write(const PrefixArgs& a, int64_t row, int e) const {
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     if (a.lse && e == 0) a.lse[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
     if constexpr (sizeof(T) == 2)
@@ -68,11 +68,11 @@ __device__ __forceinline__ int group_at(const CacheArgs& prefix, int b) {
 // the slices of 128 / D rows (D / 4 lanes a row, 16 bytes a lane), so that all their loads are in flight together.
 // Grid: rows of a sequence x sequences, so that what has to be looked up does not hang on a row.
 template <typename T, int D, int WARPS, bool TILES>
-__global__ void __launch_bounds__(256, 4) k_prefix_join(const ChunkArgs a, const CacheArgs prefix, const Slices sl) {
+__global__ void __launch_bounds__(256, 4) k_prefix_join(const PrefixArgs a, const CacheArgs prefix, const Slices sl) {
   constexpr int kLanes = D / 4, kAtOnce = 4;
   __shared__ float4 so[8][32];
   __shared__ float2 sml[8][32];
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int qh = c.kvh * c.group, b = blockIdx.y;
   const int64_t rows = int64_t(c.total_q) * qh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = lane % kLanes * 4;
@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(256, 4) k_prefix_join(const ChunkArgs a, const
 // The same where they are many: a warp looks up `each` rows at once, one a lane (what a row has to look up is
 // more instructions than its join: 1264 tokens of 32 heads 37 and 31 us), and then joins them one after the other.
 template <typename T, int D, bool TILES>
-__global__ void __launch_bounds__(256, 4) k_prefix_join_many(const ChunkArgs a, const CacheArgs prefix, const Slices sl, const int each) {
+__global__ void __launch_bounds__(256, 4) k_prefix_join_many(const PrefixArgs a, const CacheArgs prefix, const Slices sl, const int each) {
   constexpr int kLanes = D / 4, kAtOnce = 4, kTogether = 32 / kLanes;
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int qh = c.kvh * c.group, b = blockIdx.y;
   const int64_t rows = int64_t(c.total_q) * qh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = lane % kLanes * 4;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(256, 4) k_prefix_join_many(const ChunkArgs a, 
 }
 
 template <typename T, int D, bool TILES>
-cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, cudaStream_t st) {
+cudaError_t join(const PrefixArgs& a, const CacheArgs& prefix, const Slices& sl, cudaStream_t st) {
   const int together = 32 / (D / 4), qh = a.c.kvh * a.c.group;
   // Four warps a row where there are at most 16 rows an SM, eight where there are at most two (32 tokens of 32
   // heads: 76, 69 and 71 us a call with one, four and eight, four tokens: 18.7, 16.6 and 15.0; 1500 rows: 53 and 49
@@ -192,7 +192,7 @@ cudaError_t join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, 
   return least ? cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 8, TILES>, a, prefix, sl) : cudaLaunchKernelEx(&cfg, k_prefix_join<T, D, 4, TILES>, a, prefix, sl);
 }
 
-cudaError_t launch_join(const ChunkArgs& a, const CacheArgs& prefix, const Slices& sl, int dtype, cudaStream_t st) {
+cudaError_t launch_join(const PrefixArgs& a, const CacheArgs& prefix, const Slices& sl, int dtype, cudaStream_t st) {
   using B = __nv_bfloat16;
   if (sl.pre_tiles || sl.own_tiles) return a.c.d == 128 ? join<B, 128, true>(a, prefix, sl, st) : join<B, 64, true>(a, prefix, sl, st);
   if (dtype == MP_DTYPE_BF16) return a.c.d == 128 ? join<B, 128, false>(a, prefix, sl, st) : join<B, 64, false>(a, prefix, sl, st);
@@ -350,8 +350,8 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   sl.slots = int(tile_rows / sl.slot_rows);
   sl.cut = int64_t(whole) * cfg->q_heads;
   ws += own_pieces + pre_pieces;
-  ChunkArgs p, a;
-  a.c = cache_args(cfg, page_table, cu_q, kv_len, total_q, max_q, max_kv, status);
+  PrefixArgs p, a;
+  static_cast<CacheCall&>(a.c) = cache_args(cfg, page_table, cu_q, kv_len, total_q, max_q, max_kv, status);
   a.q = q;
   a.keys = keys;
   a.values = values;
@@ -364,7 +364,7 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   a.stall = injected("prefix_wait");
 #endif
   p = a;
-  p.c = cache_args(prefix_cfg, prefix_table, cu_q, prefix_len, total_q, max_group_q, max_prefix, status);
+  static_cast<CacheCall&>(p.c) = cache_args(prefix_cfg, prefix_table, cu_q, prefix_len, total_q, max_group_q, max_prefix, status);
   p.c.cu_group = cu_group;
   p.c.sequences = cfg->batch;
   p.keys = prefix_keys;
@@ -404,7 +404,7 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
   }
   // large tiles: likewise, in equal runs of all of them
   if (own_tiles || shared_tiles) {
-    ChunkArgs both = a;
+    PrefixArgs both = a;
     both.state = p.part;
     both.state_ml = p.ml;
     both.own_slice = slices * slice;

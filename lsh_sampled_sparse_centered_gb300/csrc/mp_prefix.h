@@ -7,7 +7,7 @@ namespace mp {
 
 // Units: blocks of rows of groups over their prefixes (none: groups = 0) and of sequences over their own slots.
 struct PrefixFew {
-  ChunkArgs pre, own;  // part and ml: slices [..][total_q][q_heads]
+  PrefixArgs pre, own;  // part and ml: slices [..][total_q][q_heads]
   int groups;
   bool own_units;
   int most_shared, most_own;          // pieces of a unit
@@ -23,7 +23,7 @@ inline int64_t piece_keys(const mp_cache_config* c, int total_q, int rows) { ret
 
 cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st);  // bf16, in blocks of 8, 16 or (d = 64) 32 rows
 // The prefixes of `a` in slices on large tiles, and beside them the own slots of `few` (no groups).
-cudaError_t launch_prefix_slices(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st);
+cudaError_t launch_prefix_slices(const PrefixArgs& a, const PrefixFew& few, int rows, cudaStream_t st);
 cudaError_t launch_prefix_few32(const PrefixFew& a, int rows, cudaStream_t st);  // fp32, up to 4, 8 or 16 rows
 cudaError_t launch_prefix_simt(const PrefixFew& a, cudaStream_t st);             // fp32, in blocks of kChunkRows
 // Whether prefixes with these limits go through launch_prefix_few, in blocks of `rows`.
@@ -57,7 +57,7 @@ struct RowSums {
   bool cut[2];
 
   // Row i of the `mine` rows of sequence b, `s`, whose group is `g`.
-  __host__ __device__ __forceinline__ void place(const CacheArgs& c, const Slices& sl, const Seq& s, int b, const Seq& g, int group, int i, int mine) {
+  __host__ __device__ __forceinline__ void place(const CacheCall& c, const Slices& sl, const Seq& s, int b, const Seq& g, int group, int i, int mine) {
     const int qh = c.kvh * c.group;
     const bool live = i < mine;
     row = live ? s.row0 * qh + i : -1;

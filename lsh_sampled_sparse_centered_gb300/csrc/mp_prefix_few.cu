@@ -69,9 +69,9 @@ cudaError_t launch_rows(const Maps& maps, const PrefixFew& a, int rows, int ctas
 }  // namespace
 
 bool few::few_maps(const PrefixFew& a, Maps* maps) {
-  const ChunkArgs* both[2] = {&a.pre, &a.own};
+  const PrefixArgs* both[2] = {&a.pre, &a.own};
   for (int i = 0; i < 2; ++i) {
-    const CacheArgs& c = both[i]->c;
+    const CacheCall& c = both[i]->c;
     const uint64_t pool = uint64_t(c.n_pages) * c.kvh * c.page_size;
     if (!make_map(&maps->k[i], both[i]->keys, c.d, pool, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map(&maps->v[i], both[i]->values, c.d, pool, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -83,11 +83,11 @@ bool few::few_maps(const PrefixFew& a, Maps* maps) {
 cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st) {
   Maps maps;
   if (!few_maps(a, &maps)) return cudaErrorInvalidValue;
-  const ChunkArgs* both[2] = {&a.pre, &a.own};
+  const PrefixArgs* both[2] = {&a.pre, &a.own};
   const int d = a.own.c.d;
   double steps = 0;
   for (int i = 0; i < 2; ++i) {
-    const CacheArgs& c = both[i]->c;
+    const CacheCall& c = both[i]->c;
     const int units = i ? (a.own_units ? c.batch : 0) : a.groups;
     steps += double(units) * c.kvh * ((int64_t(c.max_q) * c.group + rows - 1) / rows) * ((c.max_kv + kStep - 1) / kStep + kLead);
   }

@@ -77,7 +77,7 @@ __device__ __forceinline__ int blocks_in(const Seq& s, int group) { return (s.m 
 // without a slot have no piece.
 template <typename C>
 __device__ __forceinline__ void survey(const PrefixFew& a, int2* kept, int thread, int threads, int64_t* sum, int* at_least) {
-  const CacheArgs& co = a.own.c;
+  const CacheCall& co = a.own.c;
   const int kvh = co.kvh, group = co.group;
   const int units = a.groups + (a.own_units ? co.batch : 0);
   int64_t total = 0;
@@ -201,7 +201,7 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
   constexpr int KC = D / 32, VC = D / 64, TILES = D / 16;
   constexpr int kSets = (NT + 1) / 2;  // 16-row sets of Q
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const CacheArgs& co = a.own.c;
+  const CacheCall& co = a.own.c;
   const int kvh = co.kvh, group = co.group, qh = kvh * group;
   Walk<Cutting<NT * 8>> walk(a, kept, total, least, worker, workers);
   found();
@@ -219,7 +219,7 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
   Piece next = {};  // the piece that is fetched
   auto look = [&]() {  // the next 32 steps' rows of the pool, one a lane
     f_base = fu;
-    const CacheArgs& c = next.own ? co : a.pre.c;
+    const CacheCall& c = next.own ? co : a.pre.c;
     f_row = fu + lane < next.u1 ? slot_row(c, next.b, next.h, (fu + lane) * kStep) : 0;
   };
   auto open = [&]() {
@@ -377,7 +377,7 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
     if (!ok) break;
     // The piece's sums to its slice. Lane (g, t) has the rows 2t and 2t + 1 of every eight, of them the
     // elements 8 g .. 8 g + 7 (d = 128: and those 64 further on).
-    const ChunkArgs& to = p.own ? a.own : a.pre;
+    const PrefixArgs& to = p.own ? a.own : a.pre;
     const int64_t slice = int64_t(p.slice) * co.total_q * qh;
     auto row_at = [&](int r) { return slice + int64_t(p.row0 + r / group) * qh + p.h * group + r % group; };
 #pragma unroll

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident(R)) k_prefix_few32(const
   __shared__ int leasts[kWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane % L, half = lane / L, own_row = lane % R;
-  const CacheArgs& co = a.own.c;
+  const CacheCall& co = a.own.c;
   const int group = co.group, qh = co.kvh * group;
   int64_t total = 0;
   int least = 0;
@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kWarps * 32, resident(R)) k_prefix_few32(const
   const float scale = kLog2e * rsqrtf(float(D));
   Piece p = {};
   for (; walk.open(&p); walk.advance()) {
-    const CacheArgs& c = p.own ? co : a.pre.c;
-    const ChunkArgs& side = p.own ? a.own : a.pre;
+    const CacheCall& c = p.own ? co : a.pre.c;
+    const PrefixArgs& side = p.own ? a.own : a.pre;
     const float *keys = static_cast<const float*>(side.keys) + part * 4, *values = static_cast<const float*>(side.values) + part * 4;
     auto row_of = [&](int r) { return int64_t(p.row0 + r / group) * qh + p.h * group + r % group; };
     float4 q[R];

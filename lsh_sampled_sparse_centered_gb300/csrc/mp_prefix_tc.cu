@@ -20,8 +20,8 @@ int prefix_slices(const mp_cache_config* c, int max_q, int max_kv) {
   return std::max(1, std::min(most, int((2 * int64_t(sms) + int64_t(c->kv_heads) * tiles - 1) / (int64_t(c->kv_heads) * tiles))));
 }
 
-cudaError_t launch_prefix_slices_64(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st);
-cudaError_t launch_prefix_slices(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st) {
+cudaError_t launch_prefix_slices_64(const PrefixArgs& a, const PrefixFew& few, int rows, cudaStream_t st);
+cudaError_t launch_prefix_slices(const PrefixArgs& a, const PrefixFew& few, int rows, cudaStream_t st) {
   return a.c.d == 128 ? launch_slices_of<128>(a, few, rows, st) : launch_prefix_slices_64(a, few, rows, st);
 }
 

@@ -7,7 +7,7 @@ namespace mp {
 namespace {
 
 template <int D, Mode MODE>
-cudaError_t launch_slices(const ChunkArgs& a, const OwnSide& own, int rows, cudaStream_t st) {
+cudaError_t launch_slices(const PrefixArgs& a, const OwnSide& own, int rows, cudaStream_t st) {
   Extra<MODE> x;
   static_cast<OwnSide&>(x) = own;
   const int ctas = device_sm_count();
@@ -15,7 +15,7 @@ cudaError_t launch_slices(const ChunkArgs& a, const OwnSide& own, int rows, cuda
                    : launch<D, MODE, 2>(a, x, a.c.batch, ctas, kRows, nullptr, st);
 }
 template <int D>
-cudaError_t launch_slices_of(const ChunkArgs& a, const PrefixFew& few, int rows, cudaStream_t st) {
+cudaError_t launch_slices_of(const PrefixArgs& a, const PrefixFew& few, int rows, cudaStream_t st) {
   OwnSide own;
   own.few = few;
   if (!few::few_maps(few, &own.maps)) return cudaErrorInvalidValue;

@@ -24,7 +24,7 @@ constexpr int kOneAtOnce = 2, kOwnAtOnce = 1;  // keys of a lane that are worked
 constexpr int kResident = 3;
 
 struct RotateArgs {
-  CacheArgs c;
+  CacheCall c;
   void* keys;
   const double *from_freq, *to_freq;
   const int32_t *from, *to;  // [batch][position_heads][position_cols]; nullptr: the slot
@@ -95,7 +95,7 @@ template <typename T, bool ONE, bool TWO>
 __global__ void __launch_bounds__(kThr, kResident) k_cache_rotate(const RotateArgs a) {
   constexpr int V = Vec<T>::N, kAtOnce = ONE ? kOneAtOnce : kOwnAtOnce;
   __shared__ uint2 turns[TWO ? 2 : 1][64];  // a position's fraction of a turn (lower, upper half): pair j of lane i at j lanes + i
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int half = a.rot / 2, b = blockIdx.z;
   for (int i = threadIdx.x; i < (TWO ? 2 : 1) * 64; i += kThr) {
     const int k = i >> 6, p = i & 63;

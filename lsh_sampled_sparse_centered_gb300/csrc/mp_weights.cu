@@ -116,7 +116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   static_assert(offsetof(WSmem<D>, k) % 1024 == 0 && offsetof(WSmem<D>, q) % 1024 == 0 && sizeof(S.k[0][0]) % 1024 == 0 &&
                 sizeof(S.q[0][0]) % 1024 == 0 && offsetof(WSmem<D>, z) % 256 == 0 && offsetof(WSmem<D>, ones) % 256 == 0 &&
                 sizeof(S.z[0]) % 256 == 0);
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
   volatile uint32_t* abort = &S.abort;
   const int qh = c.kvh * c.group;
@@ -574,7 +574,7 @@ constexpr int kStepWarps = 4, kRound = 16;  // keys of a warp and round
 template <int D, int NT>
 __global__ void __launch_bounds__(kStepWarps * 32) k_weights_step(const WeightsArgs a) {
   constexpr int KC = D / 32;  // 16-byte chunks of a row per lane
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int b = blockIdx.z, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Seq s = seq_of(c, b);
@@ -680,7 +680,7 @@ int step_ctas_per_sm(int kind) {
 
 template <int D>
 cudaError_t launch(const WeightsArgs& a, cudaStream_t st) {
-  const CacheArgs& c = a.c;
+  const CacheCall& c = a.c;
   const int64_t rows = int64_t(c.max_q) * c.group;
   if (rows <= 32) {
     // Slices of at least four rounds, one wave of the CTAs that fit (one more per SM than fit: 16

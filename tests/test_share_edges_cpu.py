@@ -1,4 +1,5 @@
-"""Index arithmetic of the attention over shared prefixes run on the host, over numbers that no kernel wrote."""
+"""Host side of the attention over shared prefixes: index arithmetic over numbers that no kernel wrote, arguments of the
+older calls."""
 import os
 import shutil
 import subprocess
@@ -23,4 +24,9 @@ def run_host(name, tmp_path):
 def test_the_join_stays_inside_the_sums_whatever_its_numbers_are(tmp_path):
     """A wait that ran out leaves numbers of pieces unwritten; the join runs behind it."""
     r = run_host("row_sums_host", tmp_path)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
+def test_the_older_calls_take_no_arguments_of_the_prefixes(tmp_path):
+    r = run_host("call_sizes_host", tmp_path)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
