@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import share_reference as S
-from test_gpu_cache import DEV, offsets
+from test_gpu_cache import DEV, HALF, offsets
 from test_gpu_share import Plan, Shared, attend_prefix, check_prefix, ints, mp  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -37,6 +37,24 @@ def test_fp32_tiles_behind_tiles_that_see_nothing(mp, hk, d, m, n, prefix):  # n
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     check_prefix(c, "f32", q, cu, *first)
     assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("hq,hk,d,page,q_lens,own,groups,prefixes", [
+    (8, 2, 128, 16, [1, 1, 1], [1, 17, 300], [3], [333]),                            # all rows few
+    (16, 16, 64, 0, [3, 1, 2], [30, 700, 5], [2], [4000]),
+    (8, 1, 128, 64, [1] * 20, [5 + 30 * i for i in range(20)], [20], [500]),         # 160 rows of a group over a short prefix
+    (4, 1, 64, 16, [4] * 15, [20 + 9 * i for i in range(15)], [10, 5], [300, 900]),
+])
+def test_few_rows_have_weights_of_two_terms(mp, hq, hk, d, page, q_lens, own, groups, prefixes):  # noqa: F811
+    """Where the header says so, in both passes: a weight is off by what two roundings to bf16 leave of it, 2^-16, where
+    one leaves 2^-8."""
+    c = Shared(mp, "bf16", hq, hk, d, page, own, groups, prefixes)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1], hq, d, by=1.5)
+    out, _ = attend_prefix(mp, c, q, cu, cu_t, max(q_lens))
+    want, _, spread, slack = S.prefix_attention(q, cu, c.kv, c.keys, c.values, c.table, c.groups, c.prefixes, c.pre.keys, c.pre.values, c.pre.table, hk)
+    rel = 2 * (d + 8) * 2.0 ** -24 * slack + (max(own) + max(prefixes)) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -16
+    assert ((out.double() - want).abs() <= HALF["bf16"] * want.abs() + (1 + HALF["bf16"]) * rel[..., None] * spread).all()
 
 
 def together(*loops):
