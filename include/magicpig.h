@@ -508,7 +508,8 @@ MP_API int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config
  *                key's slot. position_heads is 1 or kv_heads, position_cols >= max_kv (both are
  *                not looked at where both arrays are NULL). mp_cache_evict's `kept` fits as
  *                from_positions, with to_positions NULL: the kept keys then stand at 0, 1, ...
- *   scale      : finite.
+ *   scale      : finite. mp_cache_append has no such factor: keys that are appended behind scaled ones are brought
+ *                to it by the first rot_dim elements of k_norm, or of k where there is no norm, multiplied by it.
  * No page stands twice in the tables (its keys would be turned twice, and by two at once). Slots in a bad
  * page are left. */
 MP_API int mp_cache_rotate(const mp_cache_config* cfg, const mp_rotary* rotary, void* keys, const int32_t* page_table,

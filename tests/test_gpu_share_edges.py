@@ -9,9 +9,10 @@ import threading
 import pytest
 import torch
 
+import cache_reference as R
 import share_reference as S
-from test_gpu_cache import DEV, HALF, offsets
-from test_gpu_share import Plan, Shared, attend_prefix, check_prefix, ints, mp  # noqa: F401
+from test_gpu_cache import DEV, HALF, Cache, offsets
+from test_gpu_share import Plan, Shared, attend_prefix, check_prefix, freq, ints, mp  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -171,3 +172,36 @@ def test_bf16_sines_and_cosines_within_their_bound(mp, two):  # noqa: F811
             assert over.max() <= 2.0 ** -20 + 2.0 ** -28, (name, over.max().item())
             if want.abs().max() < 2.0 ** -10:
                 assert (got - want).mean().abs() <= 2.0 ** -22, (name, units[0].item(), (got - want).mean().item())
+
+
+@pytest.mark.parametrize("rot,norm", [(128, True), (128, False), (64, True), (64, False)])
+def test_a_scaled_cache_goes_on(mp, rot, norm):  # noqa: F811
+    """Keys appended behind scaled ones, their k (or k_norm) multiplied in its first rot_dim elements, are the keys that
+    the append and then the rotation would have given: each of the two is within 2^-20 of the size of an element's pair
+    of it (the rotation's tolerance), and the factor's own rounding is a part of that."""
+    n, m, hk, d, scale = 70, 23, 2, 128, 1.375 * math.sqrt(0.7)
+    g = torch.Generator().manual_seed(rot)
+    q, k, v = (torch.randn(n, hk, d, generator=g).to(DEV) for _ in range(3))
+    w = 1 + 0.3 * torch.randn(d, generator=g).to(DEV)
+    by = torch.ones(d, device=DEV)
+    by[:rot] = scale
+    rotary, f = mp.make_rotary(rot_dim=rot, eps=1e-6), freq(rot)
+
+    def append(c, kv, rows, k, w):
+        cu, cu_t = offsets([len(rows)])
+        mp.mp_cache_append(c.cfg, rotary, q[rows], k[rows].contiguous(), v[rows], None, w, f, None, cu_t, ints([kv]), c.keys, c.values, c.table,
+                           torch.empty_like(q[rows]), c.status)
+
+    whole, on = (Cache(mp, "f32", hk, hk, d, 16, [n]) for _ in range(2))
+    append(whole, n, list(range(n)), k, w if norm else None)
+    mp.mp_cache_rotate(whole.cfg, rotary, whole.keys, whole.table, ints([n]), n, f, None, None, None, scale, whole.status)
+    append(on, n - m, list(range(n - m)), k, w if norm else None)
+    mp.mp_cache_rotate(on.cfg, rotary, on.keys, on.table, ints([n - m]), n, f, None, None, None, scale, on.status)
+    append(on, n, list(range(n - m, n)), k if norm else k * by, w * by if norm else None)
+    for h in range(hk):
+        a, b = R.gather(whole.keys, whole.table, 0, h, n), R.gather(on.keys, on.table, 0, h, n)
+        size = a.abs()
+        size[:, :rot] = torch.hypot(a[:, :rot // 2], a[:, rot // 2:rot]).repeat(1, 2)
+        assert torch.equal(a[:n - m], b[:n - m])
+        assert ((a - b).abs() <= 2 * 2.0 ** -20 * size).all()
+    assert whole.status.item() == 0 and on.status.item() == 0
