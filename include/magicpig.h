@@ -480,6 +480,10 @@ MP_API int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_
  *   prefix_keys, prefix_values, prefix_table : the prefixes' pages, which may be pages of the same pool.
  * A row that sees nothing gets out = 0 and lse = -infinity. mp_cache_weights takes q and this lse for
  * the sequences' own slots. Partial results are fp32.
+ * Where prefixes fill whole pages of the sequences' pool, mp_chunk_attention over tables that begin with the same pages
+ * gives the same, reads a prefix for each sequence, and is the faster one where that is little: in bf16, with single
+ * tokens or a few drafts, up to about 25 MB of keys and values read again ((sequences - 1) x prefix), and with
+ * tens of tokens a sequence, whose products are what counts, up to some 16000 shared slots.
  * bf16: as in mp_chunk_attention the softmax weights enter the second product as bf16, or as the sum of two bf16
  * where there are few rows (tokens x heads of a KV head's group), and for a prefix those are the rows of a whole group.
  * The limits decide: the own slots have two where max_q tokens are at most 16 rows; the prefixes have two where
