@@ -487,7 +487,7 @@ MP_API int mp_prefix_workspace_bytes(const mp_cache_config* cfg, const mp_cache_
  * bf16: as in mp_chunk_attention the softmax weights enter the second product as bf16, or as the sum of two bf16
  * where there are few rows (tokens x heads of a KV head's group), and for a prefix those are the rows of a whole group.
  * The limits decide: the own slots have two where max_q tokens are at most 16 rows; the prefixes have two where
- * besides max_group_q tokens are as few, or at most 256 rows over prefixes that are short for their number. So
+ * besides max_group_q tokens are as few, or max_prefix is short for the number of a group's rows. So
  * many single tokens over a long prefix, to which mp_chunk_attention gives two, have one there. */
 MP_API int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefix_cfg, const void* q,
                                const int32_t* cu_q, const int32_t* kv_len, int32_t total_q, int32_t max_q,

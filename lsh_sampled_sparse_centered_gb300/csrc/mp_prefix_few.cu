@@ -96,13 +96,22 @@ cudaError_t launch_prefix_few(const PrefixFew& a, int rows, cudaStream_t st) {
 }
 
 // K and V are read once for every `rows` rows, from L2 but for the first, and a step of 32 rows is 1 us of a
-// warp. The large tiles do better, but a kernel of them starts 10 us later. (Groups of 56, 68 and 20 rows
-// over 3001, 777 and 5000 slots of four KV heads, d = 64, own rows up to 24: 28.8 us a call with large tiles
-// for the prefixes, 20.8 with blocks.)
+// warp. The large tiles do better, but a kernel of them starts 10 us later, and the more so the more own slots
+// there are beside them. So it goes by the steps. us a call in a graph with blocks and with large tiles for the prefix,
+// single tokens with 256 own slots, one group:
+//                                      4096 steps     8192          16384         32768
+//   d = 128, 32/8 heads,   64 rows     15.0  20.2     18.9  20.4    25.9  21.9    38.1  24.4
+//                         128 rows     16.7  21.7     20.1  22.8    25.7  22.6    38.7  25.3
+//                         512 rows                    35.5  62.7    39.7  70.0    50.7  52.1
+//                        1024 rows                                  61.9  90.5    69.8  99.3
+//            16/2 heads,  128 rows     13.8  18.1     17.5  19.7    23.7  21.7    35.5  22.7
+//   d = 64,  16/4 heads,   64 rows     11.6  16.6     14.5  17.6    18.5  17.7    27.1  18.5
+//                         128 rows     11.9  22.1     14.0  22.4    18.4  23.1    26.1  23.6
+//                         512 rows     17.9  23.3     19.5  23.7    23.4  24.0    30.6  23.7
 bool prefix_is_few(const mp_cache_config* c, int max_q, int max_kv, int rows) {
   const int64_t all = int64_t(max_q) * (c->q_heads / c->kv_heads), blocks = (all + rows - 1) / rows;
   const int64_t steps = int64_t(c->batch) * c->kv_heads * ((max_kv + kStep - 1) / kStep);
-  return all <= 256 && steps * blocks <= 16384;
+  return double(steps) * double(blocks) <= 16384;
 }
 
 // The most pieces that a unit is cut into: as many warps as there are for it, 32 at least, so that one long

@@ -45,6 +45,9 @@ def test_fp32_tiles_behind_tiles_that_see_nothing(mp, hk, d, m, n, prefix):  # n
     (16, 16, 64, 0, [3, 1, 2], [30, 700, 5], [2], [4000]),
     (8, 1, 128, 64, [1] * 20, [5 + 30 * i for i in range(20)], [20], [500]),         # 160 rows of a group over a short prefix
     (4, 1, 64, 16, [4] * 15, [20 + 9 * i for i in range(15)], [10, 5], [300, 900]),
+    (8, 1, 128, 16, [1] * 90, [1 + 7 * i for i in range(90)], [80], [333]),          # 640 rows
+    (16, 2, 64, 48, [2, 1, 3] * 20, [9 + 11 * i for i in range(60)], [50, 9], [200, 77]),  # 800 rows in blocks of 32
+    (24, 6, 128, 0, [1] * 150, [1 + i % 50 for i in range(150)], [1, 149], [40, 64]),
 ])
 def test_few_rows_have_weights_of_two_terms(mp, hq, hk, d, page, q_lens, own, groups, prefixes):  # noqa: F811
     """Where the header says so, in both passes: a weight is off by what two roundings to bf16 leave of it, 2^-16, where
