@@ -200,7 +200,7 @@ static DecodePtrs decode_ptrs(const Geometry& g, void* base) {
 // MP_FAULT_INJECT=build|append|decode|chunk|weights|evict|plan|prefix|rotate|all makes the named calls
 // fail before any launch (host-side fault injection for error-path tests). In the bounds-checking build
 // chunk_wait|weights_wait|prefix_wait stop one CTA of the tensor-core kernels, so that the others' bounded
-// waits run out.
+// waits run out, and with prefix_few_wait a warp of the few-row kernel waits for bytes that never come.
 bool injected(const char* what) {
   const char* e = std::getenv("MP_FAULT_INJECT");
   if (!e || !*e) return false;

@@ -146,6 +146,18 @@ __host__ __device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
 #endif
 }
 
+// in_range() of a call whose status may be missing.
+__host__ __device__ __forceinline__ bool inside(bool ok, uint32_t* status) {
+#if MP_CHECK
+  if (!ok) flag(status, MP_STATUS_BAD_INDEX);
+  return ok;
+#else
+  (void)ok;
+  (void)status;
+  return true;
+#endif
+}
+
 // Sequence b's packed rows [row0, row0 + m) and its n slots, cut to the call's limits, and the
 // slot that row row0 stands in. That slot goes by the lengths as they are, so that a cut moves
 // no token: row r is in slot kv_len - cu_q[b + 1] + r. Where every slot is behind (before) the

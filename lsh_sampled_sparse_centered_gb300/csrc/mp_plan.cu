@@ -129,8 +129,9 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
   // where entry e of the list lies
   auto entry = [&](uint32_t e) -> const int32_t* {
     if (e < uint32_t(n_free)) return a.free + e;
-    const int b = owner(back, batch, e - n_free);
-    return a.table + int64_t(b) * a.cols + pages(left[b]) + int(e - n_free - back[b]);
+    const int b = owner(back, batch, e - n_free), col = pages(left[b]) + int(e - n_free - back[b]);
+    if (!inside(b >= 0 && b < batch && col >= 0 && col < a.cols && e < uint32_t(a.n_pages), a.status)) return a.table;
+    return a.table + int64_t(b) * a.cols + col;
   };
   auto checked = [&](int p) {
     if (p < 0 || p >= a.n_pages) wrong |= MP_STATUS_BAD_PAGE;
@@ -141,8 +142,8 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
   constexpr int kAtOnce = 4;
   const uint32_t first = uint32_t(rank * threads + tid), step = uint32_t(ctas * threads);
   for (uint32_t i = first; i < all_taken; i += step) {
-    const int b = owner(taken, served, i);
-    a.table[int64_t(b) * a.cols + pages(old_len[b]) + int(i - taken[b])] = checked(*entry(list - 1 - i));
+    const int b = owner(taken, served, i), col = pages(old_len[b]) + int(i - taken[b]);
+    if (inside(b >= 0 && b < batch && col >= 0 && col < a.cols, a.status)) a.table[int64_t(b) * a.cols + col] = checked(*entry(list - 1 - i));
   }
   // pages given back and not taken again
   for (uint32_t e0 = uint32_t(n_free) + first; e0 + all_taken < list; e0 += kAtOnce * step) {
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const uint32_t e = e0 + k * step;
-      if (e + all_taken < list) a.free[e] = checked(page[k]);
+      if (e + all_taken < list && inside(e < uint32_t(a.n_pages), a.status)) a.free[e] = checked(page[k]);
     }
   }
   // The pages taken are in the tables, and every CTA has read the lengths and n_free.
@@ -173,14 +174,15 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
       const uint32_t r = r0 + k * by;
       if (r >= end) continue;
       b[k] = b_of(r);
+      if (!inside(b[k] >= 0 && b[k] < batch && r < uint32_t(a.max_rows), a.status)) b[k] = 0;
       slot[k] = old_len[b[k]] + int(r - rows[b[k]]);
       page[k] = b[k];
-      if (a.slots && a.table) page[k] = __ldcg(a.table + int64_t(b[k]) * a.cols + (pages(slot[k] + 1) - 1));
+      if (a.slots && a.table && inside(slot[k] >= 0 && slot[k] < cap, a.status)) page[k] = __ldcg(a.table + int64_t(b[k]) * a.cols + (pages(slot[k] + 1) - 1));
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const uint32_t r = r0 + k * by;
-      if (r >= end) continue;
+      if (r >= end || !inside(r < uint32_t(a.max_rows), a.status)) continue;
       if (a.positions) a.positions[r] = int(uint32_t(base[b[k]]) + uint32_t(slot[k]));
       if (a.row_seq) a.row_seq[r] = b[k];
       if (a.slots) {
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kMostThreads) k_cache_plan(const PlanArgs a) {
       __syncthreads();
       const int b0 = owner(rows, served, begin), b1 = owner(rows, served, end - 1);
       for (int b = b0 + tid; b <= b1; b += threads)
-        if (rows[b + 1] > rows[b]) own[max(rows[b], begin) - begin] = uint32_t(b);
+        if (rows[b + 1] > rows[b] && inside(max(rows[b], begin) - begin < most, a.status)) own[max(rows[b], begin) - begin] = uint32_t(b);
       __syncthreads();
       uint32_t v[kAtOnce], high = 0;
 #pragma unroll

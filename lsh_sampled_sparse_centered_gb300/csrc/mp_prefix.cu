@@ -90,8 +90,9 @@ __global__ void __launch_bounds__(256, 4) k_prefix_join(const PrefixArgs a, cons
     float4 x[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const bool live = i0 + k < r.all;
+      bool live = i0 + k < r.all;
       const int64_t at = live ? r.at(sl, rows, i0 + k) : 0;
+      live = live && inside(at >= 0 && at < r.total(sl), c.status);
       v[k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
       x[k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -152,8 +153,9 @@ __global__ void __launch_bounds__(256, 4) k_prefix_join_many(const PrefixArgs a,
         float4 x[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-          const bool live = i0 + k < r.all;
+          bool live = i0 + k < r.all;
           const int64_t at = live ? r.at(sl, rows, i0 + k) : 0;
+          live = live && inside(at >= 0 && at < r.total(sl), c.status);
           v[k] = live ? *reinterpret_cast<const float2*>(a.ml + at * 2) : make_float2(-INFINITY, 0.f);
           x[k] = live ? *reinterpret_cast<const float4*>(a.part + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -384,6 +386,9 @@ int mp_prefix_attention(const mp_cache_config* cfg, const mp_cache_config* prefi
     if (plan.own != kind && plan.shared != kind) continue;
     const bool beside = kind == kFew && plan.shared == kSlices, bf16 = cfg->dtype == MP_DTYPE_BF16;
     PrefixFew few;
+#if MP_CHECK
+    few.stall = injected("prefix_few_wait");
+#endif
     few.pre = p;
     few.own = a;
     few.groups = plan.shared == kind ? prefix_cfg->batch : 0;

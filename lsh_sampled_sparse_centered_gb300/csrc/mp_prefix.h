@@ -13,6 +13,9 @@ struct PrefixFew {
   int most_shared, most_own;          // pieces of a unit
   int pre_keys, own_keys;             // numbers of pieces that a KV head has place for
   int32_t *pre_pieces, *own_pieces;   // [kv_heads][keys]: at piece_key()
+#if MP_CHECK
+  bool stall;  // a warp waits for bytes that never come (bf16)
+#endif
 };
 // Where the number of pieces of a block of rows is kept: block `block` (of `rows` rows each) of the group or
 // sequence `unit` whose first packed row is `row0`. No two of them meet where no packed row is in two.
@@ -99,7 +102,9 @@ struct RowSums {
     look(all_at, sl.own_tiles, all, from[1], cut[1], tile[1]);
     all += there;
   }
-  // The row of the sums that slice i is; `rows` are all query rows.
+  // The rows of the sums; `rows` are all query rows.
+  __host__ __device__ static __forceinline__ int64_t total(const Slices& sl) { return sl.cut + int64_t(sl.slots) * sl.slot_rows; }
+  // The row of them that slice i is.
   __host__ __device__ __forceinline__ int64_t at(const Slices& sl, int64_t rows, int i) const {
     const bool own = i >= there;
     const int n = own ? i - there : i;

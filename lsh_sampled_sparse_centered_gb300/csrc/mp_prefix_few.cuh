@@ -62,10 +62,11 @@ __device__ __forceinline__ Seq unit_of(const PrefixFew& a, int v) {
   return v < a.groups ? group_of(a.pre.c, v) : seq_of(a.own.c, v - a.groups);
 }
 template <typename C>
-__device__ __forceinline__ int32_t& pieces_at(const PrefixFew& a, int v, const Seq& s, int h, int block) {
+__device__ __forceinline__ void note_pieces(const PrefixFew& a, int v, const Seq& s, int h, int block, int pieces) {
   const bool own = v >= a.groups;
-  const int key = piece_key(s.row0, a.own.c.group, C::kRows, block, own ? v - a.groups : v);
-  return own ? a.own_pieces[int64_t(h) * a.own_keys + key] : a.pre_pieces[int64_t(h) * a.pre_keys + key];
+  const int key = piece_key(s.row0, a.own.c.group, C::kRows, block, own ? v - a.groups : v), keys = own ? a.own_keys : a.pre_keys;
+  if (!inside(key >= 0 && key < keys && pieces >= 0 && pieces <= (own ? a.most_own : a.most_shared), a.own.c.status)) return;
+  (own ? a.own_pieces : a.pre_pieces)[int64_t(h) * keys + key] = pieces;
 }
 template <typename C>
 __device__ __forceinline__ int steps_in(const Seq& s) { return s.m > 0 ? (s.n + C::kStep - 1) / C::kStep : 0; }
@@ -91,7 +92,7 @@ __device__ __forceinline__ void survey(const PrefixFew& a, int2* kept, int threa
     least = max(least, int64_t((n + most - 2) / (most - 1)));
     if (n == 0 && v % gridDim.x == blockIdx.x)
       for (int h = 0; h < kvh; ++h)
-        for (int i = 0; i < blocks; ++i) pieces_at<C>(a, v, s, h, i) = 0;
+        for (int i = 0; i < blocks; ++i) note_pieces<C>(a, v, s, h, i, 0);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -184,7 +185,7 @@ struct Walk {
       p->u0 = u0;
       p->u1 = u1;
       p->slice = int(quotient(r0, run) - first);
-      if (u0 == 0 && (threadIdx.x & 31) == 0) pieces_at<C>(a, v, s, h, block) = int(quotient(lead + steps - 1, run) - first) + 1;
+      if (u0 == 0 && (threadIdx.x & 31) == 0) note_pieces<C>(a, v, s, h, block, int(quotient(lead + steps - 1, run) - first) + 1);
       return true;
     }
     return false;
@@ -236,7 +237,11 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
     const int st = int(fetched % kStages);
     if (fu - f_base == 32) look();
     const int row = __shfl_sync(0xffffffffu, f_row, fu - f_base);
-    if (lane == 0) mbar_expect_tx(&S.full[st], kStep * D * 2 * 2);
+    uint32_t bytes = kStep * D * 2 * 2;
+#if MP_CHECK
+    if (a.stall && worker == 0 && fetched == 0) bytes += 16;  // that never come: the wait for them runs out
+#endif
+    if (lane == 0) mbar_expect_tx(&S.full[st], bytes);
     __syncwarp();
     if (lane < 2 * kSub) {
       const int kv = lane / kSub, sub = lane % kSub, which = next.own;
@@ -378,6 +383,7 @@ __device__ __forceinline__ void work(const Maps& maps, const PrefixFew& a, Ring<
     // The piece's sums to its slice. Lane (g, t) has the rows 2t and 2t + 1 of every eight, of them the
     // elements 8 g .. 8 g + 7 (d = 128: and those 64 further on).
     const PrefixArgs& to = p.own ? a.own : a.pre;
+    if (!inside(p.slice >= 0 && p.slice < (p.own ? a.most_own : a.most_shared) && p.row0 + (p.rows - 1) / group < co.total_q, co.status)) continue;
     const int64_t slice = int64_t(p.slice) * co.total_q * qh;
     auto row_at = [&](int r) { return slice + int64_t(p.row0 + r / group) * qh + p.h * group + r % group; };
 #pragma unroll

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident(R)) k_prefix_few32(const
     // the piece's sums to its slice
 #pragma unroll
     for (int w = R; w < 32; w *= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
+    if (!inside(p.slice >= 0 && p.slice < (p.own ? a.most_own : a.most_shared) && p.row0 + (p.rows - 1) / group < co.total_q, co.status)) continue;
     const int64_t slice = int64_t(p.slice) * co.total_q * qh;
     if (lane < R && lane < p.rows) *reinterpret_cast<float2*>(side.ml + (slice + row_of(lane)) * 2) = make_float2(m, l);
 #pragma unroll

@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kThr, kResident) k_cache_rotate(const RotateAr
     if (slot64 >= s.n) return k;
     const int slot = int(slot64);
     const int64_t where = (int64_t(b) * a.position_heads + h) * a.position_cols + slot;
+    if (!inside(!(a.from || a.to) || (slot < a.position_cols && h < a.position_heads), c.status)) return k;
     k.from = a.from ? a.from[where] : slot;
     k.to = a.to ? a.to[where] : slot;
     const int col = c.page_shift >= 0 ? slot >> c.page_shift : slot / c.page_size;
