@@ -116,7 +116,7 @@ struct OneTile {
 //   drafts of 1 to 9 tokens of 33 sequences, 6/2 heads, prefixes of 614, 20978 and 47562 slots, d = 64   836   140
 //   of 29 sequences, 12/1 heads, five prefixes of 1 to 14768, d = 128                                   1190   160
 //   of 14 sequences, 28/4 heads, prefixes of 26434 and 11304, d = 64                                     552   408
-// and less where they do not (five chunks, 101 rows over 2000 slots, eight heads: 37 and 41).
+// and less where they do not (five chunks, 101 rows over 2000 slots, eight heads: 37 and 38).
 // One function for both: with the tile in a function of its own, which the compiler inlined, the kernel without runs
 // took ten registers more and 2 % of its time (512 tokens over 8192 slots, 32/8 heads: 1937 us, in one function 1907,
 // alone 1896), and the one with runs with d = 64 9 % (five chunks, 101 rows over 2000 slots, eight heads, in a graph:

@@ -72,7 +72,10 @@ struct Piece {
 
 static_assert(kKeys / 16 <= 8, "boxes of 16 rows at least");
 
-// What a launch works on, and where its sums go.
+// What a launch works on, and where its sums go. P is one bf16 term in all of them, for single tokens over prefixes
+// too, which mp_chunk_step gives two: a second is a second product and its conversions in the softmax warps, whose
+// chain a step waits for, and with d = 64 tensor memory has no place for it. (Error of the output against 64 bits
+// 0.0023, of rounding it alone 0.0017.)
 enum Mode {
   kChunk,  // chunks over their sequences' slots: out and lse
   kBoth,   // groups' rows over the prefixes that their sequences share, and chunks over their own slots: sums to a.state
