@@ -82,6 +82,126 @@ def together(*loops):
         raise failed[0]
 
 
+KINDS = [  # one batch for each way the attention goes: dtype, q heads, kv heads, d, page, tokens, own lengths, groups, prefixes, limit of the prefixes
+    ("bf16", 8, 2, 128, 16, [1] * 3, [40, 300, 7], [3], [500], 600),            # few rows for both
+    ("bf16", 32, 8, 64, 64, [1] * 20, [30 + 9 * i for i in range(20)], [20], [9000], 12000),   # slices, a half each step
+    ("bf16", 16, 2, 128, 0, [1] * 40, [30 + 9 * i for i in range(40)], [40], [9000], 12000),   # slices of two tiles
+    ("bf16", 40, 40, 64, 32, [1] * 200, [9 + i % 70 for i in range(200)], [200], [900], 20000),  # few own rows, tiles for the prefix
+    ("bf16", 8, 2, 128, 64, [100, 33], [100, 400], [2], [700], 5000),           # tiles for both
+    ("f32", 8, 2, 128, 16, [1] * 3, [40, 300, 7], [3], [500], 600),             # few rows
+    ("f32", 8, 2, 64, 16, [1] * 9, [40 + i for i in range(9)], [9], [500], 600),  # few own rows, tiles for the prefix
+    ("f32", 8, 8, 64, 0, [50, 33], [100, 400], [2], [700], 5000),               # tiles for both
+]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefix_attention_of_rows_that_see_nothing_at_all(mp, kind):  # noqa: F811
+    """Every prefix and every cache is empty, whatever the limits let expect; then some of them are not."""
+    dtype, hq, hk, d, page, q_lens, own, groups, prefixes, most = kind
+    c = Shared(mp, dtype, hq, hk, d, page, own, groups, prefixes, cap=max(own) + 50, pcap=most)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1] + 2, hq, d, by=1.5)
+    for kv, pl in (([0] * len(own), [0] * len(groups)), ([0] * len(own), prefixes), ([0] * (len(own) - 1) + own[-1:], [0] * len(groups)), (own, prefixes)):
+        c.kv, c.prefixes = kv, pl
+        c.kv_len.copy_(ints(kv))
+        c.pre.kv_len.copy_(ints(pl))
+        out, lse = attend_prefix(mp, c, q, cu, cu_t, max(q_lens), max_kv=max(own) + 50, max_prefix=most)
+        if not any(kv) and not any(pl):
+            assert (out[:cu[-1]] == 0).all() and (lse[:cu[-1]] == -math.inf).all() and (out[cu[-1]:] == 77).all()
+        else:
+            check_prefix(c, dtype, q, cu, out, lse)
+    assert c.status.item() == 0
+
+
+def test_prefix_attentions_from_several_threads(mp):  # noqa: F811
+    """A thread, a stream and a workspace for each of the ways: the bits that each gives alone."""
+    runs = []
+    for dtype, hq, hk, d, page, q_lens, own, groups, prefixes, most in KINDS:
+        c = Shared(mp, dtype, hq, hk, d, page, own, groups, prefixes)
+        cu, cu_t = offsets(q_lens)
+        q = c.randn(cu[-1], hq, d, by=1.5)
+        want = attend_prefix(mp, c, q, cu, cu_t, max(q_lens))
+        out, lse = torch.empty_like(q), torch.empty_like(want[1])
+        g, l = c.limits(cu)
+        ws = torch.empty(mp.mp_prefix_workspace_bytes(c.cfg, c.pre.cfg, cu[-1], max(q_lens), max(own), g, l), dtype=torch.uint8, device=DEV)
+        runs.append((c, q, cu_t, max(q_lens), max(own), g, l, out, lse, ws, torch.cuda.Stream(), want))
+    torch.cuda.synchronize()
+
+    def loop(c, q, cu_t, m, n, g, l, out, lse, ws, st, want):
+        def run():
+            for _ in range(200):
+                mp.mp_prefix_attention(c.cfg, c.pre.cfg, q, cu_t, c.kv_len, m, n, c.keys, c.values, c.table, c.cu_group, c.pre.kv_len, g, l,
+                                       c.pre.keys, c.pre.values, c.pre.table, out, lse, ws, c.status, stream=st)
+        return run
+
+    together(*(loop(*r) for r in runs))
+    torch.cuda.synchronize()
+    for c, *_, out, lse, ws, st, want in runs:
+        assert c.status.item() == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def in_a_new_thread(call):
+    """What `call` gives in a thread that has asked nothing of CUDA before."""
+    got = []
+    together(lambda: got.append(call()))
+    torch.cuda.synchronize()
+    return got[0]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_threads_first_call_is_a_prefix_attention(mp, kind):  # noqa: F811
+    dtype, hq, hk, d, page, q_lens, own, groups, prefixes, most = kind
+    c = Shared(mp, dtype, hq, hk, d, page, own, groups, prefixes)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1], hq, d, by=1.5)
+    out, lse = attend_prefix(mp, c, q, cu, cu_t, max(q_lens))
+    g, l = c.limits(cu)
+    ws = torch.empty(mp.mp_prefix_workspace_bytes(c.cfg, c.pre.cfg, cu[-1], max(q_lens), max(own), g, l), dtype=torch.uint8, device=DEV)
+    o, z = torch.empty_like(out), torch.empty_like(lse)
+    torch.cuda.synchronize()
+    in_a_new_thread(lambda: mp.mp_prefix_attention(c.cfg, c.pre.cfg, q, cu_t, c.kv_len, max(q_lens), max(own), c.keys, c.values, c.table, c.cu_group,
+                                                   c.pre.kv_len, g, l, c.pre.keys, c.pre.values, c.pre.table, o, z, ws, c.status))
+    assert torch.equal(o, out) and torch.equal(z, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 100])
+def test_a_threads_first_call_is_one_of_the_cache(mp, dtype, m):  # noqa: F811
+    """Attention and weights of a token and of a chunk, append, plan, rotation and eviction, each in a thread of its own."""
+    c = Cache(mp, dtype, 8, 2, 128, 16, [300, m + 5])
+    cu, cu_t = offsets([m, m])
+    q, k = c.randn(2 * m, 8, 128), c.randn(2 * m, 2, 128)
+    rotary, f = mp.make_rotary(rot_dim=128), freq(128)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    dst = mp.make_cache_config(batch=2, kv_heads=2, q_heads=8, head_dim=128, page_size=64, n_pages=2, dtype=dtype)
+    shape = (2, 2, 64, 128)
+
+    def calls():
+        """[(call, what it writes)], each call with outputs of its own."""
+        keys, values = c.keys.clone(), c.values.clone()
+        out, lse, rotated = torch.zeros_like(q), torch.zeros(2 * m, 8, device=DEV), torch.zeros_like(q)
+        scores = torch.zeros(2, 2, c.ps * c.cols, device=DEV)
+        spread = torch.rand(scores.shape, generator=torch.Generator().manual_seed(1)).to(DEV)
+        dk, dv, kept, length = torch.zeros(shape, dtype=c.dtype, device=DEV), torch.zeros(shape, dtype=c.dtype, device=DEV), ints([0] * 2 * 2 * 50), ints([0, 0])
+        z = torch.full((2 * m, 8), 3.0, device=DEV)
+        plan = [ints([0, 0, 0]), ints([0, 0])]
+        return [
+            (lambda: mp.mp_chunk_attention(c.cfg, q, cu_t, c.kv_len, m, 300, c.keys, c.values, c.table, out, lse, ws), (out, lse)),
+            (lambda: mp.mp_cache_weights(c.cfg, q, z, cu_t, c.kv_len, m, 300, c.keys, c.table, scores), (scores[:, :, :m + 5],)),
+            (lambda: mp.mp_cache_append(c.cfg, rotary, q, k, k, None, None, f, None, cu_t, c.kv_len, keys, values, c.table, rotated), (rotated,)),
+            (lambda: mp.mp_cache_rotate(c.cfg, rotary, keys, c.table, c.kv_len, 300, f, f * 0.5), (keys.nan_to_num(0.0),)),
+            (lambda: mp.mp_cache_evict(c.cfg, dst, c.keys, c.values, c.table, c.kv_len, 300, spread, 4, 8, 50, dk, dv, None, None, length, kept, ws), (dk, dv, length, kept)),
+            (lambda: mp.mp_cache_plan(c.cfg, ints([0, -3]), None, c.kv_len, ints([0]), 8, c.table.clone(), torch.zeros(c.pages, dtype=torch.int32, device=DEV), plan[1],
+                                      ints([0]), plan[0]), plan),
+        ]
+
+    for i, ((here, want), (there, got)) in enumerate(zip(calls(), calls())):
+        here()
+        torch.cuda.synchronize()
+        in_a_new_thread(there)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+
+
 def test_plans_of_two_sizes_from_two_threads(mp):  # noqa: F811
     """A batch of 8192 sequences needs more shared memory than one of 1500: neither thread's calls take it from the
     other's, and both pools are planned as if they were alone."""

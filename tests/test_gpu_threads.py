@@ -1,5 +1,5 @@
-"""Two threads that build tables and decode over tables of their own, of other sizes: kernels whose shared memory goes by
-the call's sizes. Each thread's results are those of the same calls alone."""
+"""Building tables and decoding from several threads: over tables of other sizes at once (kernels whose shared memory goes by
+the call's sizes), and as a thread's first call. The results are those of the same calls alone."""
 import pytest
 import torch
 
@@ -56,3 +56,20 @@ def test_two_threads_of_other_sizes(mp, mode, threshold, small, large):
     torch.cuda.synchronize()
     for (r, _, _), want in zip(runs, alone):
         assert r.status() == 0 and torch.equal(r.out, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_threads_first_call_builds_appends_or_decodes(mp, dtype):
+    """Each call in a thread that has asked nothing of CUDA before gives what it gives in this one."""
+    wl = WL.Workload("first", layers=1, batch=1, kv_heads=2, q_heads=8, head_dim=128, n_prefill=2000, steps=4, append=True, K=8, L=30, dtype=dtype, seed=9)
+    t = WL.generate(wl)
+    here, there = (DeviceRun(mp, wl, t, "cuda:0") for _ in range(2))
+    torch.cuda.synchronize()
+    calls = lambda r: [r.build, lambda: r.decode(0, 2000), lambda: r.append(2000), lambda: r.decode(1, 2001), lambda: r.step(2, 2002)]
+    for i, (a, b) in enumerate(zip(calls(here), calls(there))):
+        a()
+        torch.cuda.synchronize()
+        together(b)
+        torch.cuda.synchronize()
+        assert here.status() == there.status() == 0
+        assert i in (0, 2) or torch.equal(here.out, there.out), i
