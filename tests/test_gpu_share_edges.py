@@ -113,6 +113,42 @@ def test_prefix_attention_of_rows_that_see_nothing_at_all(mp, kind):  # noqa: F8
     assert c.status.item() == 0
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_weights_behind_a_prefix(mp, kind):  # noqa: F811
+    """The own slots' weights by the lse over prefix and own slots: what the formula gives for that lse, with the weights'
+    own tolerance (test_gpu_cache.py), tokens in front of their cache's first slot among them."""
+    dtype, hq, hk, d, page, q_lens, own, groups, prefixes, most = kind
+    own = [max(1, own[0] // 3)] + own[1:]
+    c = Shared(mp, dtype, hq, hk, d, page, own, groups, prefixes)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1], hq, d, by=1.5)
+    _, lse = attend_prefix(mp, c, q, cu, cu_t, max(q_lens))
+    scores = torch.zeros(len(own), hk, c.ps * c.cols, device=DEV)
+    want, slack = R.weights(q, lse, cu, own, c.keys, c.table, scores)
+    mp.mp_cache_weights(c.cfg, q, lse, cu_t, c.kv_len, max(q_lens), max(own), c.keys, c.table, scores, c.status)
+    for b, n in enumerate(own):
+        rel = (d + 8) * 2.0 ** -24 * slack[b, :, :n] + 2.0 ** -21 * (1 + lse.abs().max().item()) + (hq // hk * max(q_lens) + 2) * 2.0 ** -24
+        assert ((scores[b, :, :n].double() - want[b, :, :n]).abs() <= rel * want[b, :, :n] + 1e-30).all(), b
+    assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("dtype,hq,hk,d,page,q_lens,own,groups,prefixes", [
+    ("bf16", 300, 1, 64, 16, [1, 2], [40, 300], [2], [500]),        # more heads of a group than a tile has rows
+    ("bf16", 600, 2, 128, 0, [1, 1, 1], [40, 1, 9], [1, 2], [5000, 33]),
+    ("f32", 300, 1, 128, 32, [1, 2], [40, 300], [2], [500]),
+    ("bf16", 1, 1, 128, 16, [1, 3, 40], [40, 300, 41], [3], [500]),  # a single head
+    ("f32", 1, 1, 64, 0, [1, 3, 40], [40, 300, 41], [3], [500]),
+    ("bf16", 65, 13, 64, 16, [1] * 7, [5, 16, 17, 31, 32, 33, 1], [3, 3], [15, 17]),
+])
+def test_prefix_attention_of_odd_heads(mp, dtype, hq, hk, d, page, q_lens, own, groups, prefixes):  # noqa: F811
+    c = Shared(mp, dtype, hq, hk, d, page, own, groups, prefixes)
+    cu, cu_t = offsets(q_lens)
+    q = c.randn(cu[-1] + 1, hq, d, by=1.5)
+    out, lse = attend_prefix(mp, c, q, cu, cu_t, max(q_lens))
+    check_prefix(c, dtype, q, cu, out, lse)
+    assert c.status.item() == 0
+
+
 def test_prefix_attentions_from_several_threads(mp):  # noqa: F811
     """A thread, a stream and a workspace for each of the ways: the bits that each gives alone."""
     runs = []
